@@ -36,6 +36,8 @@ STATIC_WEIGHTS = 0x100  # W4A16_STATIC_WEIGHTS
 SILU_MUL = 0x200        # W4A16_SILU_MUL
 BF16 = 0x400            # W4A16_BF16
 ACT_A8 = 0x800          # W4A16_ACT_A8
+CACHE_E4M3 = 0x1000        # W4A16_CACHE_E4M3
+ROPE_INTERLEAVED = 0x2000  # W4A16_ROPE_INTERLEAVED
 
 ERRORS = {
     -1: "INVALID_ARG", -2: "UNSUPPORTED_SHAPE", -3: "MISALIGNED",
@@ -48,6 +50,8 @@ _I = ctypes.c_int
 _SZ = ctypes.c_size_t
 _PSZ = ctypes.POINTER(ctypes.c_size_t)
 _PI = ctypes.POINTER(ctypes.c_int)
+_L = ctypes.c_int64
+_F = ctypes.c_float
 SIGNATURES = {
     "w4a16_last_error": (ctypes.c_char_p, []),
     "w4a16_version": (_I, []),
@@ -65,6 +69,15 @@ SIGNATURES = {
     "w4a16_plan": (_I, [_I, _I, _I, _I, _PI, _PI]),
     "w4a16_tc_config": (_I, [_I, _I, _I, _PI, _I]),
     "w4a16_gemm_noalloc": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _P, _P]),
+    "w4a16_gemm_scaled": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _SZ, _I, _I, _P]),
+    "w4a16_rms_norm": (_I, [_P, _L, _P, _L, _P, _I, _I, _F, _I, _P, _P, _P, _P, _P, _L, _P]),
+    "w4a16_rope_append": (_I, [_P, _L, _P, _I, _I, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _I,
+                               _I, _I, _P]),
+    "w4a16_attn_workspace_size": (_I, [_I, _I, _I, _I, _I, _PSZ]),
+    "w4a16_attn_decode": (_I, [_P, _L, _P, _P, _P, _P, _I, _I, _P, _L, _I, _P, _I, _I, _I, _I, _F,
+                               _P, _P, _P, _SZ, _I, _P]),
+    "w4a16_attn_prompt": (_I, [_P, _L, _P, _P, _P, _P, _I, _I, _P, _L, _I, _P, _P, _I, _I, _I, _I,
+                               _I, _F, _P, _P, _P, _SZ, _I, _P]),
     "w4a16_device_status": (_I, [_P]),
     "w4a16_selftest_wait": (_I, [_I, _P]),
 }
@@ -334,6 +347,10 @@ def gemm_noalloc(A: torch.Tensor, pw: PackedWeight, out: Optional[torch.Tensor] 
                                     _dev(out, torch.float16, "out"), _stream(stream)),
            "w4a16_gemm_noalloc")
     return out
+
+
+from .layer import (KVCache, attn_decode, attn_prompt, attn_workspace_size,  # noqa: E402,F401
+                    gemm_scaled, new_kv_cache, rms_norm, rope_append)
 
 
 def selftest_wait(which: int, stream=None) -> None:

@@ -208,7 +208,7 @@ size_t workspace_for(int M, int N, int K, int group, int path, int parts, bool s
 int gemm_impl(const uint16_t* A, const uint32_t* Wq, const uint16_t* scales,
               const uint32_t* zeros, int M, int N, int K, int group, uint16_t* Y,
               void* workspace, size_t workspace_bytes, int path, int parts,
-              cudaStream_t stream) {
+              cudaStream_t stream, const float* row_scale = nullptr) {
   if (M < 0) return fail(W4A16_ERR_INVALID_ARG, "M=%d is negative", M);
   if (M > kMaxDim) return fail(W4A16_ERR_UNSUPPORTED_SHAPE, "M=%d above %d", M, kMaxDim);
   if (int rc = check_kn(K, N, group)) return rc;
@@ -234,7 +234,9 @@ int gemm_impl(const uint16_t* A, const uint32_t* Wq, const uint16_t* scales,
   // W4A8: quantize the activations into the workspace, then multiply the
   // codes and scale each row of the result (launched once the workspace is
   // checked, below)
-  const float* row_scale = nullptr;
+  if (a8 && row_scale)
+    return fail(W4A16_ERR_INVALID_ARG, "W4A16_ACT_A8 quantizes A itself: no row_scale with it");
+  if (!aligned(row_scale, 4)) return fail(W4A16_ERR_MISALIGNED, "alignment: row_scale needs 4 bytes");
   auto quantize_activations = [&](const WsLayout& l) -> cudaError_t {
     uint16_t* codes = reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + l.codes);
     float* sc = reinterpret_cast<float*>(static_cast<char*>(workspace) + l.scales);
@@ -464,6 +466,14 @@ int w4a16_gemm_ex(const uint16_t* A, const uint32_t* Wq, const uint16_t* scales,
                    parts, (cudaStream_t)stream);
 }
 
+int w4a16_gemm_scaled(const uint16_t* A, const float* row_scale, const uint32_t* Wq, const uint16_t* scales,
+                      const uint32_t* zeros, int M, int N, int K, int group, uint16_t* Y, void* workspace,
+                      size_t workspace_bytes, int path, int parts, void* stream) {
+  if (M > 0 && !row_scale) return fail(W4A16_ERR_INVALID_ARG, "null pointer (row_scale)");
+  return gemm_impl(A, Wq, scales, zeros, M, N, K, group, Y, workspace, workspace_bytes, path, parts,
+                   (cudaStream_t)stream, row_scale);
+}
+
 int w4a16_plan(int M, int N, int K, int group, int* path, int* parts) {
   if (M < 0) return fail(W4A16_ERR_INVALID_ARG, "M=%d is negative", M);
   if (int rc = check_kn(K, N, group)) return rc;
@@ -514,7 +524,7 @@ int w4a16_device_status(void* stream) {
     return fail(W4A16_ERR_DEVICE_CHECK,
                 "device error word = 0x%x (bits: 1 producer, 2 MMA, 4 dequant, 8 epilogue waits "
                 "timed out; 16 drain timed out; 32 decode fix-up wait timed out; 64 access out of "
-                "bounds, bounds-checked build)",
+                "bounds, bounds-checked build; 128 slot, position, page or length outside its range)",
                 flag);
   return ok();
 }

@@ -122,6 +122,24 @@ bool tc_config(int M, int K, int group, int out[8]);
 cudaError_t launch_selftest_flag_wait(cudaStream_t stream);
 cudaError_t launch_selftest_mbar_wait(cudaStream_t stream);
 
+// The other operators of a decoder layer (validated by layer_api.cu).
+// Root-mean-square norm of x (+ residual) with row strides; y, codes (16-bit
+// integer values), aq (int8) and h may be null, s_a goes with codes or aq.
+cudaError_t launch_rms_norm(const uint16_t* x, long long ldx, const uint16_t* residual, long long ldr,
+                            const uint16_t* weight, int M, int K, float eps, bool bf16, uint16_t* y,
+                            uint16_t* codes, int8_t* aq, float* s_a, uint16_t* h, long long ldh,
+                            cudaStream_t stream);
+// Rotation of the query and key heads of T qkv rows, q written out and keys
+// and values stored at their slots of the paged cache.
+cudaError_t launch_rope_append(const uint16_t* qkv, long long ld, const float* table, int table_len, int R,
+                               const int32_t* positions, const int64_t* slots, int T, int heads, int kv_heads,
+                               int head_dim, uint16_t* q, void* k, void* v, const float* k_scale,
+                               const float* v_scale, int pages, int page_shift, bool bf16, bool e4m3,
+                               bool interleaved, cudaStream_t stream);
+// Attention over the paged cache, one warp per row and head.
+struct AttnArgs;
+cudaError_t launch_attn_rows(const AttnArgs& args, int head_dim, bool bf16, bool e4m3, cudaStream_t stream);
+
 // Reads the device error word (bounded waits that gave up, self-checks) and
 // clears it if set.
 cudaError_t read_and_clear_device_error(int* flag);

@@ -327,6 +327,122 @@ int w4a16_gemm_noalloc(const uint16_t* A, const uint32_t* Wq, const uint16_t* sc
                        const uint32_t* zeros, int M, int N, int K, int group,
                        uint16_t* Y, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The other operators of a decoder layer: what stands between its linears.
+ * The pages' serving systems run these layers whole (vLLM PR #1032: LLaMA;
+ * lmdeploy issue #2274: online activation quantization fused with the norm).
+ * 16-bit arrays are fp16, or bfloat16 with W4A16_BF16. Sums, softmax
+ * statistics and rotations are fp32 and each result is rounded once.
+ * Outputs must not overlap inputs except where an entry says so. Data read
+ * on the device (slots, positions, page numbers, lengths) that names
+ * something outside its buffer touches nothing there: bit 128 of the error
+ * word records it (w4a16_device_status) and the entry says what happens
+ * instead. Every launch uses programmatic stream serialization, as the GEMMs
+ * do.
+ * ------------------------------------------------------------------------ */
+
+/* The GEMM of activations that are integer codes already: as w4a16_gemm_ex
+ * with A [M][K] holding codes as 16-bit integer values (what w4a16_rms_norm
+ * writes to `codes`) and row m of the fp32 result multiplied by
+ * row_scale[m] before its rounding. The product and accuracy of
+ * W4A16_ACT_A8, without its quantization pass; W4A16_ACT_A8 itself is
+ * W4A16_ERR_INVALID_ARG here. The workspace is that of the same path
+ * without W4A16_ACT_A8. */
+int w4a16_gemm_scaled(const uint16_t* A, const float* row_scale, const uint32_t* Wq,
+                      const uint16_t* scales, const uint32_t* zeros, int M, int N, int K, int group,
+                      uint16_t* Y, void* workspace, size_t workspace_bytes, int path, int parts,
+                      void* stream);
+
+/* Root-mean-square norm with the residual's addition. Per row, in fp32:
+ *   h = x + residual,  y = h * (mean_k h^2 + eps)^(-1/2) * weight.
+ * x and residual (or null) are [M][K] with row strides in elements, weight
+ * [K]. Outputs, each null where it is not wanted:
+ *   y      [M][K]  the 16-bit result
+ *   h      row stride h_stride: the 16-bit residual stream; may be the
+ *          residual array itself
+ *   codes  [M][K]  8 bits: s_a = max_k |y| / 127 (1 for a row of zeros) and
+ *          clamp(round(y / s_a), -127, 127), ties to even, from the fp32 y,
+ *          as 16-bit integer values (w4a16_gemm_scaled's A)
+ *   aq     [M][K]  the same codes as int8
+ *   s_a    [M]     fp32, with codes or aq
+ * 1 <= K <= 65536, any 2-byte alignment (16-byte aligned rows run faster);
+ * 8-bit results need finite rows. */
+int w4a16_rms_norm(const uint16_t* x, int64_t x_stride, const uint16_t* residual,
+                   int64_t residual_stride, const uint16_t* weight, int M, int K, float eps,
+                   int flags, uint16_t* y, uint16_t* codes, int8_t* aq, float* s_a, uint16_t* h,
+                   int64_t h_stride, void* stream);
+
+/* The paged key-value cache of the three entry points below. k_cache and
+ * v_cache are [pages][kv_heads][page_size][head_dim], 16-bit, or with
+ * W4A16_CACHE_E4M3 8-bit floats (e4m3) whose value is code * k_scale[head]
+ * (v_scale[head]), fp32 [kv_heads], not null then and null otherwise.
+ * page_size 16, 32, 64, 128 or 256; head_dim 64 or 128; heads a multiple of
+ * kv_heads, at most 1024; query head h reads the keys and values of head
+ * h / (heads / kv_heads). Token i of a sequence lies at place i % page_size
+ * of the page that entry i / page_size of its page table names. */
+#define W4A16_CACHE_E4M3 0x1000
+#define W4A16_ROPE_INTERLEAVED 0x2000
+
+/* Rotates queries and keys by their positions and appends keys and values to
+ * the cache. qkv [tokens][(heads + 2 kv_heads) * head_dim] (row stride in
+ * elements) holds each token's query heads, key heads, value heads (a fused
+ * qkv GEMM's row). cos_sin [table_len][rotary] fp32: row p holds rotary/2
+ * cosines, then the sines, of position p. The pair of dimensions
+ * (i, i + rotary/2) (with W4A16_ROPE_INTERLEAVED (2i, 2i + 1)), i < rotary/2,
+ * turns from (a, b) to (a cos - b sin, b cos + a sin); dimensions from
+ * `rotary` on (even, at most head_dim) pass through. q [tokens][heads]
+ * [head_dim] receives the queries; keys and values go to slot
+ * slots[t] = page * page_size + place of the cache, rounded to its type
+ * (e4m3: x / scale, nearest even, saturating). A negative slot stores
+ * nothing. A slot beyond the cache stores nothing and a position outside the
+ * table turns as position 0, both recorded (bit 128). Two tokens must not
+ * have the same slot. */
+int w4a16_rope_append(const uint16_t* qkv, int64_t qkv_stride, const float* cos_sin, int table_len,
+                      int rotary, const int32_t* positions, const int64_t* slots, int tokens,
+                      int heads, int kv_heads, int head_dim, uint16_t* q, void* k_cache,
+                      void* v_cache, const float* k_scale, const float* v_scale, int pages,
+                      int page_size, int flags, void* stream);
+
+/* Scratch bytes of w4a16_attn_decode (tokens = batch) and w4a16_attn_prompt
+ * on the current device; 0 when none. The buffer is of w4a16_gemm's kind: a
+ * flag area that must be zero before the first use and that every call
+ * leaves zero, so one buffer serves the GEMMs and these calls in turn.
+ * Host-only. */
+int w4a16_attn_workspace_size(int tokens, int batch, int heads, int kv_heads, int head_dim,
+                              size_t* bytes);
+
+/* Attention of one new token per sequence over the cache:
+ *   out[b][h] = sum_j softmax_j(scale q[b][h].k_j) v_j, j < lens[b],
+ * q [batch] rows (stride in elements, heads adjacent, 16-byte aligned rows),
+ * out [batch][heads][head_dim]; lse [batch][heads] fp32 (or null) receives
+ * the logarithm of the softmax's sum. table [batch] rows (stride in
+ * elements) of max_pages page numbers, of which the first
+ * ceil(lens[b] / page_size) are read. A length of 0 gives zeros and -inf.
+ * What the cache holds beyond a sequence's length is never used. A length
+ * below 0 or beyond the table's row is clamped and a page number outside the
+ * cache reads page 0, both recorded (bit 128). */
+int w4a16_attn_decode(const uint16_t* q, int64_t q_stride, const void* k_cache, const void* v_cache,
+                      const float* k_scale, const float* v_scale, int pages, int page_size,
+                      const int32_t* table, int64_t table_stride, int max_pages, const int32_t* lens,
+                      int batch, int heads, int kv_heads, int head_dim, float scale, uint16_t* out,
+                      float* lse, void* workspace, size_t workspace_bytes, int flags, void* stream);
+
+/* Causal attention of prompts, or of pieces of prompts behind what is cached
+ * of them, over the cache (which holds the new tokens' keys and values
+ * already). Sequence b has the rows starts[b] .. starts[b + 1) of q
+ * ([tokens] rows, as above) and lens[b] cached tokens, the new ones last:
+ * its row starts[b] + i sees the keys 0 .. lens[b] - n_b + i with
+ * n_b = starts[b + 1] - starts[b]; a row that sees none gives zeros and
+ * -inf. starts [batch + 1] must not decrease; rows outside
+ * [starts[0], starts[batch]) of out and lse are left as they are. The rest as
+ * w4a16_attn_decode. */
+int w4a16_attn_prompt(const uint16_t* q, int64_t q_stride, const void* k_cache, const void* v_cache,
+                      const float* k_scale, const float* v_scale, int pages, int page_size,
+                      const int32_t* table, int64_t table_stride, int max_pages,
+                      const int32_t* starts, const int32_t* lens, int tokens, int batch, int heads,
+                      int kv_heads, int head_dim, float scale, uint16_t* out, float* lse,
+                      void* workspace, size_t workspace_bytes, int flags, void* stream);
+
 /* Synchronizes `stream`, then reads and clears the library's device error
  * word (set by a kernel that gave up a bounded wait or failed a self-check;
  * in the bounds-checked build of the library, compiled with -DW4A16_CHECKED,
