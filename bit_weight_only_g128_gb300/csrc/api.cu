@@ -346,6 +346,7 @@ cudaError_t set_max_smem_once(const void* kernel, int bytes) {
 // units of the library.
 int report_error(int code, const char* message) { return fail(code, "%s", message); }
 int report_ok() { return ok(); }
+int device_sms() { return sm_count(); }
 
 }  // namespace w4a16
 

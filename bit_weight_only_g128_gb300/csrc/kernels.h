@@ -138,6 +138,11 @@ cudaError_t launch_rope_append(const uint16_t* qkv, long long ld, const float* t
                                bool interleaved, cudaStream_t stream);
 // Attention over the paged cache, one warp per row and head.
 struct AttnArgs;
+// Decode attention, split over the cache's length: the workspace holds the
+// arrival counters (zero between calls) in its flag area, then the parts.
+size_t attn_decode_workspace_bytes(int head_dim, int sms);
+cudaError_t launch_attn_decode(const AttnArgs& args, int head_dim, bool bf16, bool e4m3, void* workspace, int sms,
+                               cudaStream_t stream);
 cudaError_t launch_attn_rows(const AttnArgs& args, int head_dim, bool bf16, bool e4m3, cudaStream_t stream);
 
 // Reads the device error word (bounded waits that gave up, self-checks) and
@@ -148,6 +153,9 @@ cudaError_t read_and_clear_device_error(int* flag);
 // device, once per (kernel, device): the attribute is per device, and setting
 // it on every launch costs a driver call.
 cudaError_t set_max_smem_once(const void* kernel, int bytes);
+
+// SM count of the current device.
+int device_sms();
 
 // Set (or clear) the calling thread's w4a16_last_error message; returns code.
 int report_error(int code, const char* message);

@@ -92,6 +92,14 @@ int check_attn(AttnArgs* a, const uint16_t* q, int64_t q_stride, const void* k, 
   return W4A16_OK;
 }
 
+int check_workspace(const void* workspace, size_t bytes, size_t need) {
+  if (need > 0 && (!workspace || bytes < need))
+    return fail(W4A16_ERR_WORKSPACE_TOO_SMALL, "attention needs a workspace of %zu bytes (got %zu)", need,
+                workspace ? bytes : (size_t)0);
+  if (need > 0 && !aligned(workspace, 256)) return fail(W4A16_ERR_MISALIGNED, "workspace needs 256-byte alignment");
+  return W4A16_OK;
+}
+
 }  // namespace
 }  // namespace w4a16
 
@@ -150,7 +158,7 @@ int w4a16_attn_workspace_size(int tokens, int batch, int heads, int kv_heads, in
   if (tokens < 0 || batch < 0 || heads <= 0 || kv_heads <= 0 || head_dim <= 0)
     return fail(W4A16_ERR_INVALID_ARG, "negative or zero size");
   if (!bytes) return fail(W4A16_ERR_INVALID_ARG, "null output pointer");
-  *bytes = 0;
+  *bytes = tokens == 0 || batch == 0 ? 0 : attn_decode_workspace_bytes(head_dim, device_sms());
   return report_ok();
 }
 
@@ -164,8 +172,10 @@ int w4a16_attn_decode(const uint16_t* q, int64_t q_stride, const void* k_cache, 
                           max_pages, lens, batch, batch, heads, kv_heads, head_dim, scale, out, lse, flags))
     return rc;
   if (batch == 0) return report_ok();
-  return finish(launch_attn_rows(a, head_dim, (flags & W4A16_BF16) != 0, (flags & W4A16_CACHE_E4M3) != 0,
-                                 (cudaStream_t)stream),
+  const int sms = device_sms();
+  if (int rc = check_workspace(workspace, workspace_bytes, attn_decode_workspace_bytes(head_dim, sms))) return rc;
+  return finish(launch_attn_decode(a, head_dim, (flags & W4A16_BF16) != 0, (flags & W4A16_CACHE_E4M3) != 0, workspace,
+                                   sms, (cudaStream_t)stream),
                 "decode attention launch");
 }
 
