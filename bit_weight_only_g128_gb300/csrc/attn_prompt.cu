@@ -1,0 +1,542 @@
+// Causal attention of prompts over the paged cache on the tensor cores.
+//
+// For the rows of a sequence (a row is a query token and one of the G =
+// heads / kv_heads query heads of a key/value head; rows of one token are
+// adjacent, so that they share the keys' tiles) and tiles of 128 keys:
+//   S = Q K^T, x = S scale log2 e (-inf where the row may not see the key),
+//   P = 2^(x - m), l += row sums of P, O += P V; at the end O / l.
+// m is a running maximum that follows the row's true maximum only when that
+// is more than 2^8 above it: P stays within 2^8 (fp16 holds it, the sums are
+// fp32) and O is rarely rescaled.
+//
+// Bound: the tensor cores, 4 D operations per row and key. One block per SM
+// takes 256 rows, two tiles of 128 whose softmax and products alternate: while
+// one tile's 128 threads (a row each) form P, the tensor cores work on the
+// other tile.
+//   warps 0-3, 4-7   softmax of tile 0, 1 (a thread owns a row: a lane of
+//                    tensor memory), the rare rescaling of O, the results
+//   warps 8-11       copies: queries, then the tiles K0 V0 K1 V1 .. into a
+//                    ring of five slots, from their pages, 16 bytes at a time
+//                    (rows beyond the sequence as zeros, so that what the
+//                    cache holds there meets P = 0 as 0); e4m3 codes become
+//                    16-bit values on the way
+//   warp 12          tcgen05.mma: S from shared memory, O += P V with P read
+//                    from tensor memory, where it takes the place of S
+// Tensor memory: S0, S1 (128 columns each), O0, O1 (D each). Registers: 128 a
+// thread at launch, 192 for the softmax warps and 64 for the rest (256 x 192
+// + 256 x 64 = 512 x 128).
+#include "common.cuh"
+#include "kernels.h"
+#include "layer.cuh"
+#include "tc_ptx.cuh"
+
+namespace w4a16 {
+namespace {
+
+using namespace tc;
+
+constexpr int kThreads = 512;
+constexpr int kTile = 128;  // rows of a tile, and keys of a tile
+constexpr int kSlots = 5;
+constexpr int kPanel = kTile * 128;  // bytes of 64 dimensions of 128 rows
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kSlack = 8.f;  // log2 of how far a row's maximum may run ahead
+
+// barriers: full[kSlots], empty[kSlots], queries[2], scores[2], probs[2], out[2],
+// drain
+enum { kFull = 0, kEmpty = kSlots, kQueries = 2 * kSlots, kScores = kQueries + 2, kProbs = kScores + 2,
+       kOut = kProbs + 2, kDrain = kOut + 2, kBars };
+
+struct Control {
+  uint64_t bars[kBars];
+  uint32_t tmem;
+  int abort;
+  int scan[kThreads / 32];
+  int unit[2];  // sequence, unit of it
+  float power[2 * kTile];  // what a row's queries were divided by (bf16 over e4m3)
+};
+
+template <int D>
+constexpr int kTileBytes = D / 64 * kPanel;
+template <int D>
+constexpr int kSmem = (2 + kSlots) * kTileBytes<D> + (int)sizeof(Control) + 1024;
+
+struct PromptArgs {
+  AttnArgs a;
+  int group;
+  float mult;      // |scale| log2 e
+  uint32_t negate;  // scale < 0
+};
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Byte offset of 16-byte chunk c of row r in a tile: panels of 64 dimensions
+// with the 128-byte swizzle.
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+  return (uint32_t)((c >> 3) * kPanel + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+// Descriptor of the values' tile as the MMA's B operand with the dimensions
+// innermost (MN-major, 128-byte swizzle): 8-key groups 1024 bytes apart
+// (stride byte offset), panels of 64 dimensions kPanel bytes apart (leading
+// byte offset).
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(kPanel >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+// Eight e4m3 codes to fp16 (exact).
+__device__ __forceinline__ uint4 widen(uint32_t lo, uint32_t hi) {
+  return make_uint4(e4m3x2_to_half2(lo & 0xffffu), e4m3x2_to_half2(lo >> 16), e4m3x2_to_half2(hi & 0xffffu),
+                    e4m3x2_to_half2(hi >> 16));
+}
+
+// kB: 16-bit values are bf16, else fp16; k8: e4m3 cache. Its products are in
+// fp16, which holds every code; bf16 queries are then divided by a power of
+// two per row that brings them into fp16's range.
+template <bool kB, bool k8, int D>
+__global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptArgs p) {
+  constexpr int kBytes = kTileBytes<D>;
+  constexpr bool kP = kB && !k8;  // products in bf16
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = (uint32_t)__cvta_generic_to_shared(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  Control& ctl = *reinterpret_cast<Control*>(smem_raw + (base - raw) + (2 + kSlots) * kBytes);
+  const uint32_t bars = (uint32_t)__cvta_generic_to_shared(&ctl.bars[0]);
+  auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
+  const AttnArgs& a = p.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  volatile int* abort_flag = &ctl.abort;
+
+  allow_dependent_launch();
+  grid_dependency_wait();
+
+  // which unit of 256 rows: the last ones of a sequence (the most keys) first
+  const int hk = blockIdx.x % a.cache.kv_heads;
+  int total = 0;
+  auto units = [&](int b) {
+    return b < a.batch ? (int)(((long long)row_count(a, b) * p.group + 2 * kTile - 1) / (2 * kTile)) : 0;
+  };
+  auto scan = [&](int v) {  // inclusive over the block, and the total
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
+    }
+    if (lane == 31) ctl.scan[warp] = v;
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += ctl.scan[w];
+      all += ctl.scan[w];
+    }
+    __syncthreads();
+    return make_int2(v + before, all);
+  };
+  for (int b0 = 0; b0 < a.batch; b0 += kThreads) total += scan(units(b0 + tid)).y;
+  const int want = total - 1 - (int)(blockIdx.x / a.cache.kv_heads);
+  if (want < 0) return;
+  for (int b0 = 0, carry = 0; b0 < a.batch; b0 += kThreads) {
+    const int v = units(b0 + tid);
+    const int2 s = scan(v);
+    const int lo = carry + s.x - v;
+    if (lo <= want && want < lo + v) {
+      ctl.unit[0] = b0 + tid;
+      ctl.unit[1] = want - lo;
+    }
+    carry += s.y;
+  }
+  if (tid == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(bar(kFull + i), 128);
+      mbar_init(bar(kEmpty + i), 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(bar(kQueries + t), 128);
+      mbar_init(bar(kScores + t), 1);
+      mbar_init(bar(kProbs + t), 128);
+      mbar_init(bar(kOut + t), 1);
+    }
+    mbar_init(bar(kDrain), 1);
+    ctl.abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 12) {
+    tmem_alloc((uint32_t)__cvta_generic_to_shared(&ctl.tmem), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl.tmem;
+  const int b = ctl.unit[0];
+  const int first = row_start(a, b), fresh = row_count(a, b);
+  const int len = seq_length(a, b), past = len - fresh;  // may be negative: rows that see nothing
+  const long long rows = (long long)fresh * p.group;
+  const long long row0 = (long long)ctl.unit[1] * (2 * kTile);
+  // key tiles of the two row tiles: up to the last row's position
+  int n[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const long long lo = row0 + t * kTile, hi = min(lo + kTile, rows);
+    const int last = lo < hi ? past + (int)((hi - 1) / p.group) : -1;
+    n[t] = last < 0 ? 0 : last / kTile + 1;
+  }
+  const int most = max(n[0], n[1]);
+
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    const int t = warp >> 2;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // the warp's quarter of the lanes
+    const uint32_t scores = tmem + lanes + (uint32_t)(t * kTile), out = tmem + lanes + 256u + (uint32_t)(t * D);
+    const long long row = row0 + t * kTile + (tid & 127);
+    const bool live = row < rows;
+    const int token = live ? (int)(row / p.group) : 0, head = hk * p.group + (live ? (int)(row % p.group) : 0);
+    const int limit = live ? past + token + 1 : 0;  // keys this row sees
+    float mult = p.mult * (k8 ? a.cache.k_scale[hk] : 1.f);
+    const int nt = t ? n[1] : n[0];
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    if (kB && k8 && nt > 0) {
+      ok = mbar_wait(bar(kQueries + t), 0u, abort_flag, kErrEpilogue, a.err);
+      mult *= ctl.power[t * kTile + (tid & 127)];
+    }
+    for (int j = 0; j < nt && ok; ++j) {
+      if (!(ok = mbar_wait(bar(kScores + t), (uint32_t)j & 1u, abort_flag, kErrEpilogue, a.err))) break;
+      tc_fence_after();
+      uint32_t s[4][32];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) tmem_ld32(scores + 32 * q, s[q]);
+      tmem_wait_ld();
+      const int seen = limit - j * kTile;
+      if (!__all_sync(0xffffffffu, seen >= kTile)) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (32 * q + i >= seen) s[q][i] = 0xff800000u;
+      }
+      float top4[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float u = fmaxf(__uint_as_float(s[q][0]), __uint_as_float(s[q][1]));
+#pragma unroll
+        for (int i = 2; i < 32; i += 2) u = fmaxf(fmaxf(u, __uint_as_float(s[q][i])), __uint_as_float(s[q][i + 1]));
+        top4[q] = u;
+      }
+      const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * mult;
+      const bool moves = top > m + kSlack;
+      if (__any_sync(0xffffffffu, moves)) {
+        const float f = moves ? ex2(m - top) : 1.f;
+        if (moves) m = top;
+        l *= f;
+        if (j > 0) {
+          // the scores' arrival says that the product with the last P is done
+#pragma unroll
+          for (int c = 0; c < D; c += 16) {
+            uint32_t o[16];
+            tmem_ld16(out + c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st16(out + c, o);
+          }
+        }
+      }
+      const float shift = m == -INFINITY ? 0.f : -m;
+      float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float x = ex2(fmaf(__uint_as_float(s[q][2 * i]), mult, shift));
+          const float y = ex2(fmaf(__uint_as_float(s[q][2 * i + 1]), mult, shift));
+          l4[i & 3] += x + y;
+          w[i] = pack16<kP>(x, y);
+        }
+        tmem_st16(scores + 16 * q, w);
+      }
+      l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(bar(kProbs + t));
+    }
+    if (ok && nt > 0) ok = mbar_wait(bar(kOut + t), 0u, abort_flag, kErrEpilogue, a.err);
+    tc_fence_after();
+    if (ok) {
+      const float inv = l > 0.f ? (k8 ? a.cache.v_scale[hk] : 1.f) / l : 0.f;
+      uint16_t* dst = a.out + ((size_t)(first + token) * a.heads + head) * D;
+#pragma unroll
+      for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        if (nt > 0) {
+          tmem_ld32(out + c, o);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0;
+        }
+        if (live) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) {
+            float f[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) f[k] = l > 0.f ? __uint_as_float(o[i + k]) * inv : 0.f;
+            *reinterpret_cast<uint4*>(dst + c + i) = make_uint4(pack16<kB>(f[0], f[1]), pack16<kB>(f[2], f[3]),
+                                                                pack16<kB>(f[4], f[5]), pack16<kB>(f[6], f[7]));
+          }
+        }
+      }
+      if (live && a.lse) a.lse[(size_t)(first + token) * a.heads + head] = l > 0.f ? m * kLn2 + logf(l) : -INFINITY;
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp < 12) {
+      const int u = tid - 256;
+      constexpr int kChunks = D / 8;  // 16-byte chunks of a row
+      bool ok = true;
+      // the queries
+      for (int t = 0; t < 2; ++t) {
+        if (t ? n[1] > 0 : n[0] > 0) {
+#pragma unroll 4
+          for (int i = u; i < kTile * kChunks; i += 128) {
+            const int r = i / kChunks, c = i % kChunks;
+            const long long row = row0 + t * kTile + r;
+            const bool valid = row < rows;
+            const uint16_t* src = a.q + (valid ? (size_t)(first + (int)(row / p.group)) * a.ldq +
+                                                     (size_t)(hk * p.group + (int)(row % p.group)) * D + c * 8
+                                               : 0);
+            const uint32_t dst = base + t * kBytes + chunk_at(r, c);
+            if (kB && k8) {
+              uint4 v = make_uint4(0, 0, 0, 0);
+              if (valid) v = *reinterpret_cast<const uint4*>(src);
+              const float2 f[4] = {unpack16<true>(v.x), unpack16<true>(v.y), unpack16<true>(v.z), unpack16<true>(v.w)};
+              float top = 0.f;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) top = fmaxf(top, fmaxf(fabsf(f[k].x), fabsf(f[k].y)));
+#pragma unroll
+              for (int o = kChunks / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+              const int e = top > 0.f ? ilogbf(top) : 0;  // |q| 2^-e < 2
+              uint32_t w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) w[k] = pack16<false>(scalbnf(f[k].x, -e), scalbnf(f[k].y, -e));
+              sts128(dst, w[0], w[1], w[2], w[3]);
+              if (c == 0) ctl.power[t * kTile + r] = scalbnf(1.f, e);
+            } else {
+              cp16(dst, src, valid);
+            }
+          }
+        }
+        cp_commit();
+      }
+      const int shift = a.cache.page_shift, mask = (1 << shift) - 1;
+      // byte offset of row 16 * (lane & 7) of key tile j in the caches
+      auto place = [&](int j) -> unsigned long long {
+        const int key = j * kTile + 16 * (lane & 7);
+        if (key >= len) return 0;
+        return ((((unsigned long long)page_of(a, b, key >> shift) * a.cache.kv_heads + hk) << shift) + (key & mask)) *
+               (D * (k8 ? 1 : 2));
+      };
+      unsigned long long at = most > 0 ? place(0) : 0;
+      int waiting = 0;  // tiles copied, not yet announced
+      for (int i = 0; i < 2 * most && ok; ++i) {
+        const int j = i >> 1, slot = i % kSlots;
+        const uint8_t* src = static_cast<const uint8_t*>(i & 1 ? a.cache.v : a.cache.k);
+        const uint32_t dst = base + (2 + slot) * kBytes;
+        auto wait_slot = [&]() {
+          return i < kSlots || mbar_wait(bar(kEmpty + slot), (uint32_t)(i / kSlots - 1) & 1u, abort_flag, kErrProducer, a.err);
+        };
+        if (k8) {
+          constexpr int kPieces = D / 16;                   // 16-code pieces of a row
+          constexpr int kLoads = kTile * kPieces / 128;     // per thread
+          uint4 v[kLoads];
+#pragma unroll
+          for (int x = 0; x < kLoads; ++x) {
+            const int e = x * 128 + u, r = e / kPieces, c = e % kPieces;
+            const unsigned long long row = __shfl_sync(0xffffffffu, at, r >> 4) + (unsigned long long)((r & 15) * D + c * 16);
+            v[x] = make_uint4(0, 0, 0, 0);
+            if (j * kTile + r < len) v[x] = ldg_stream(reinterpret_cast<const uint4*>(src + row));
+          }
+          if (!(ok = wait_slot())) break;
+#pragma unroll
+          for (int x = 0; x < kLoads; ++x) {
+            const int e = x * 128 + u, r = e / kPieces, c = e % kPieces;
+            const uint4 lo = widen(v[x].x, v[x].y), hi = widen(v[x].z, v[x].w);
+            sts128(dst + chunk_at(r, 2 * c), lo.x, lo.y, lo.z, lo.w);
+            sts128(dst + chunk_at(r, 2 * c + 1), hi.x, hi.y, hi.z, hi.w);
+          }
+          if (i == 0) cp_wait<0>();
+          fence_async_shared();
+          if (i == 0) {
+            mbar_arrive(bar(kQueries));
+            mbar_arrive(bar(kQueries + 1));
+          }
+          mbar_arrive(bar(kFull + slot));
+        } else {
+          if (!(ok = wait_slot())) break;
+#pragma unroll 4
+          for (int x = 0; x < kTile * kChunks / 128; ++x) {
+            const int e = x * 128 + u, r = e / kChunks, c = e % kChunks;
+            const unsigned long long row = __shfl_sync(0xffffffffu, at, r >> 4) + (unsigned long long)((r & 15) * (2 * D) + c * 16);
+            const bool valid = j * kTile + r < len;
+            cp16(dst + chunk_at(r, c), valid ? src + row : src, valid);
+          }
+          cp_commit();
+          // announce the tile before this one (and with the first the queries)
+          if (i > 0) {
+            cp_wait<1>();
+            fence_async_shared();
+            if (i == 1) {
+              mbar_arrive(bar(kQueries));
+              mbar_arrive(bar(kQueries + 1));
+            }
+            mbar_arrive(bar(kFull + (i - 1) % kSlots));
+          }
+          waiting = 1;
+        }
+        if ((i & 1) && j + 1 < most) at = place(j + 1);
+      }
+      cp_wait<0>();
+      if (!k8 && ok && waiting) {
+        fence_async_shared();
+        mbar_arrive(bar(kFull + (2 * most - 1) % kSlots));
+      }
+    } else if (warp == 12 && lane == 0) {
+      const uint32_t idesc_s = f16_idesc(kTile, kTile, kP) | (p.negate << 13);
+      const uint32_t idesc_o = f16_idesc(kTile, D, kP) | (1u << 16);  // B with the dimensions innermost
+      bool ok = true;
+      auto score = [&](int t, int slot) {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = (uint32_t)((k >> 2) * kPanel + (k & 3) * 32);
+          tc_mma_f16(tmem + t * kTile, sw128_kmajor_desc(base + t * kBytes + off),
+                     sw128_kmajor_desc(base + (2 + slot) * kBytes + off), idesc_s, k > 0);
+        }
+        tc_commit(bar(kScores + t));
+      };
+      auto full = [&](int i) {
+        return mbar_wait(bar(kFull + i % kSlots), (uint32_t)(i / kSlots) & 1u, abort_flag, kErrMma, a.err);
+      };
+      if (most > 0) {
+        ok = mbar_wait(bar(kQueries), 0u, abort_flag, kErrMma, a.err) &&
+             mbar_wait(bar(kQueries + 1), 0u, abort_flag, kErrMma, a.err) && full(0);
+        if (ok) {
+          tc_fence_after();
+          for (int t = 0; t < 2; ++t)
+            if (n[t] > 0) score(t, 0);
+          tc_commit(bar(kEmpty));
+        }
+      }
+      for (int j = 0; j < most && ok; ++j) {
+        const int iv = 2 * j + 1, ik = 2 * j + 2;
+        if (!(ok = full(iv))) break;
+        bool have_k = false;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (j >= n[t]) continue;
+          if (!(ok = mbar_wait(bar(kProbs + t), (uint32_t)j & 1u, abort_flag, kErrMma, a.err))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < kTile / 16; ++k)
+            tc_mma_f16_ts(tmem + 256 + t * D, tmem + t * kTile + 8 * k,
+                          sw128_mnmajor_desc(base + (2 + iv % kSlots) * kBytes + k * 2048), idesc_o, j > 0 || k > 0);
+          if (j + 1 < n[t]) {
+            if (!have_k) {
+              if (!(ok = full(ik))) break;
+              tc_fence_after();
+              have_k = true;
+            }
+            score(t, ik % kSlots);
+          } else {
+            tc_commit(bar(kOut + t));
+          }
+        }
+        if (!ok) break;
+        tc_commit(bar(kEmpty + iv % kSlots));
+        if (have_k) tc_commit(bar(kEmpty + ik % kSlots));
+      }
+      if (!ok) {
+        // no product may run past the release of the tensor memory
+        tc_commit(bar(kDrain));
+        mbar_drain(bar(kDrain), 0u, a.err);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <bool kB, bool k8, int D>
+cudaError_t launch(const PromptArgs& p, unsigned blocks, cudaStream_t stream) {
+  auto kern = attn_prompt_kernel<kB, k8, D>;
+  cudaError_t e = set_max_smem_once(reinterpret_cast<const void*>(kern), kSmem<D>);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3(blocks), dim3(kThreads), kSmem<D>, stream, p);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_prompt(const AttnArgs& args, int head_dim, bool bf16, bool e4m3, cudaStream_t stream) {
+  if (args.rows == 0 || args.batch == 0) return cudaSuccess;
+  PromptArgs p;
+  p.a = args;
+  cudaError_t e = device_error_word(&p.a.err);
+  if (e != cudaSuccess) return e;
+  p.group = args.heads / args.cache.kv_heads;
+  // the scores' maximum is taken before the scale, so it has to be positive:
+  // a negative scale negates the product, and a scale of zero becomes one too
+  // small to tell from it
+  p.mult = fmaxf(fabsf(args.scale) * kLog2e, 1e-37f);
+  p.negate = args.scale < 0.f;
+  // at most: whole units of all rows, and a ragged one per sequence
+  const long long units = (long long)args.rows * p.group / (2 * kTile) + args.batch;
+  const long long blocks = units * args.cache.kv_heads;
+  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+  switch ((bf16 ? 4 : 0) | (e4m3 ? 2 : 0) | (head_dim == 128 ? 1 : 0)) {
+    case 0: return launch<false, false, 64>(p, (unsigned)blocks, stream);
+    case 1: return launch<false, false, 128>(p, (unsigned)blocks, stream);
+    case 2: return launch<false, true, 64>(p, (unsigned)blocks, stream);
+    case 3: return launch<false, true, 128>(p, (unsigned)blocks, stream);
+    case 4: return launch<true, false, 64>(p, (unsigned)blocks, stream);
+    case 5: return launch<true, false, 128>(p, (unsigned)blocks, stream);
+    case 6: return launch<true, true, 64>(p, (unsigned)blocks, stream);
+    default: return launch<true, true, 128>(p, (unsigned)blocks, stream);
+  }
+}
+
+}  // namespace w4a16

@@ -136,14 +136,15 @@ cudaError_t launch_rope_append(const uint16_t* qkv, long long ld, const float* t
                                int head_dim, uint16_t* q, void* k, void* v, const float* k_scale,
                                const float* v_scale, int pages, int page_shift, bool bf16, bool e4m3,
                                bool interleaved, cudaStream_t stream);
-// Attention over the paged cache, one warp per row and head.
+// Attention over the paged cache (AttnArgs: layer.cuh).
 struct AttnArgs;
+// Causal attention of prompts on the tensor cores.
+cudaError_t launch_attn_prompt(const AttnArgs& args, int head_dim, bool bf16, bool e4m3, cudaStream_t stream);
 // Decode attention, split over the cache's length: the workspace holds the
 // arrival counters (zero between calls) in its flag area, then the parts.
 size_t attn_decode_workspace_bytes(int head_dim, int sms);
 cudaError_t launch_attn_decode(const AttnArgs& args, int head_dim, bool bf16, bool e4m3, void* workspace, int sms,
                                cudaStream_t stream);
-cudaError_t launch_attn_rows(const AttnArgs& args, int head_dim, bool bf16, bool e4m3, cudaStream_t stream);
 
 // Reads the device error word (bounded waits that gave up, self-checks) and
 // clears it if set.

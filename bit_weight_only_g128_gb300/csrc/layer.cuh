@@ -7,16 +7,12 @@
 #include <cuda_fp8.h>
 
 #include "common.cuh"
+#include "tc_ptx.cuh"
 
 namespace w4a16 {
 
-// Programmatic dependent launch: let the next grid on the stream be
-// scheduled, and wait until the previous grid has completed and its writes
-// are visible.
-__device__ __forceinline__ void allow_dependent_launch() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+using tc::allow_dependent_launch;
+using tc::grid_dependency_wait;
 
 // Launch with programmatic stream serialization: the grid may be scheduled
 // while the previous one drains and waits for it (grid_dependency_wait)
@@ -112,6 +108,21 @@ __device__ __forceinline__ int seq_length(const AttnArgs& a, int b) {
   if (n >= 0 && n <= most) return n;
   atomicOr(a.err, kErrRange);
   return n < 0 ? 0 : (int)most;
+}
+
+// First row of sequence b, and its number of rows; entries outside [0, rows]
+// or in falling order are recorded and clamped.
+__device__ __forceinline__ int row_start(const AttnArgs& a, int b) {
+  const int v = a.starts[b];
+  if (v >= 0 && v <= a.rows) return v;
+  atomicOr(a.err, kErrRange);
+  return v < 0 ? 0 : a.rows;
+}
+__device__ __forceinline__ int row_count(const AttnArgs& a, int b) {
+  const int n = row_start(a, b + 1) - row_start(a, b);
+  if (n >= 0) return n;
+  atomicOr(a.err, kErrRange);
+  return 0;
 }
 
 // Page number i of sequence b; one outside the cache is recorded and page 0

@@ -375,7 +375,7 @@ int w4a16_rms_norm(const uint16_t* x, int64_t x_stride, const uint16_t* residual
 /* The paged key-value cache of the three entry points below. k_cache and
  * v_cache are [pages][kv_heads][page_size][head_dim], 16-bit, or with
  * W4A16_CACHE_E4M3 8-bit floats (e4m3) whose value is code * k_scale[head]
- * (v_scale[head]), fp32 [kv_heads], not null then and null otherwise.
+ * (v_scale[head]), fp32 [kv_heads], positive; not null then and null otherwise.
  * page_size 16, 32, 64, 128 or 256; head_dim 64 or 128; heads a multiple of
  * kv_heads, at most 1024; query head h reads the keys and values of head
  * h / (heads / kv_heads). Token i of a sequence lies at place i % page_size
@@ -433,7 +433,8 @@ int w4a16_attn_decode(const uint16_t* q, int64_t q_stride, const void* k_cache, 
  * ([tokens] rows, as above) and lens[b] cached tokens, the new ones last:
  * its row starts[b] + i sees the keys 0 .. lens[b] - n_b + i with
  * n_b = starts[b + 1] - starts[b]; a row that sees none gives zeros and
- * -inf. starts [batch + 1] must not decrease; rows outside
+ * -inf. starts [batch + 1] must not decrease nor leave
+ * [0, tokens] (clamped and recorded, bit 128); rows outside
  * [starts[0], starts[batch]) of out and lse are left as they are. The rest as
  * w4a16_attn_decode. */
 int w4a16_attn_prompt(const uint16_t* q, int64_t q_stride, const void* k_cache, const void* v_cache,
