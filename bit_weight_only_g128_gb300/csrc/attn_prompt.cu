@@ -105,13 +105,36 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
   return (uint32_t)((c >> 3) * kPanel + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
-// Descriptor of the values' tile as the MMA's B operand with the dimensions
-// innermost (MN-major, 128-byte swizzle): 8-key groups 1024 bytes apart
-// (stride byte offset), panels of 64 dimensions kPanel bytes apart (leading
-// byte offset).
-__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(kPanel >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+  return ok != 0;
+}
+
+// tcgen05.mma kind::f16 with A and B (ss), or B alone (ts: A in tensor
+// memory), given by the lower halves of their shared-memory descriptors. Both
+// kinds of tiles have the same upper half: 8-row groups 1024 bytes apart
+// (stride byte offset), 128-byte swizzle. The queries and keys are K-major;
+// the values are read with the dimensions innermost (MN-major: 8-key groups at
+// the stride byte offset, panels of 64 dimensions at the leading one).
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t hi, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+      "mov.b64 db, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(hi), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
 }
 
 // Eight e4m3 codes to fp16 (exact).
@@ -432,65 +455,86 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
         fence_async_shared();
         mbar_arrive(bar(kFull + (2 * most - 1) % kSlots));
       }
-    } else if (warp == 12 && lane == 0) {
+    } else if (warp == 12) {
+      // the whole warp waits; one elected lane issues (operands that are known
+      // to be uniform over the warp)
+      constexpr uint32_t kDescHi = (uint32_t)(1024 >> 4) | (1u << 14) | (2u << 29);  // the upper half of both descriptors
       const uint32_t idesc_s = f16_idesc(kTile, kTile, kP) | (p.negate << 13);
       const uint32_t idesc_o = f16_idesc(kTile, D, kP) | (1u << 16);  // B with the dimensions innermost
+      const uint32_t q_lo = ((base & 0x3FFFFu) >> 4) | (1u << 16);                        // K-major
+      const uint32_t k_lo = (((base + 2 * kBytes) & 0x3FFFFu) >> 4) | (1u << 16);
+      const uint32_t v_lo = (((base + 2 * kBytes) & 0x3FFFFu) >> 4) | ((uint32_t)(kPanel >> 4) << 16);  // MN-major
       bool ok = true;
       auto score = [&](int t, int slot) {
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (uint32_t)((k >> 2) * kPanel + (k & 3) * 32);
-          tc_mma_f16(tmem + t * kTile, sw128_kmajor_desc(base + t * kBytes + off),
-                     sw128_kmajor_desc(base + (2 + slot) * kBytes + off), idesc_s, k > 0);
+          const uint32_t off = (uint32_t)((k >> 2) * kPanel + (k & 3) * 32) >> 4;
+          mma_ss(tmem + t * kTile, q_lo + t * (kBytes >> 4) + off, k_lo + slot * (kBytes >> 4) + off, kDescHi, idesc_s, k > 0);
         }
         tc_commit(bar(kScores + t));
       };
-      auto full = [&](int i) {
-        return mbar_wait(bar(kFull + i % kSlots), (uint32_t)(i / kSlots) & 1u, abort_flag, kErrMma, a.err);
-      };
+      auto full = [&](int slot, uint32_t phase) { return mbar_wait(bar(kFull + slot), phase, abort_flag, kErrMma, a.err); };
+      RingPos pos;  // of the next tile
+      pos.init(0, kSlots);
       if (most > 0) {
         ok = mbar_wait(bar(kQueries), 0u, abort_flag, kErrMma, a.err) &&
-             mbar_wait(bar(kQueries + 1), 0u, abort_flag, kErrMma, a.err) && full(0);
+             mbar_wait(bar(kQueries + 1), 0u, abort_flag, kErrMma, a.err) && full(0, 0);
+        ok = __all_sync(0xffffffffu, ok);
         if (ok) {
           tc_fence_after();
-          for (int t = 0; t < 2; ++t)
-            if (n[t] > 0) score(t, 0);
-          tc_commit(bar(kEmpty));
+          if (elect_one()) {
+            for (int t = 0; t < 2; ++t)
+              if (n[t] > 0) score(t, 0);
+            tc_commit(bar(kEmpty));
+          }
+          __syncwarp();
         }
+        pos.step(1, kSlots);
       }
       for (int j = 0; j < most && ok; ++j) {
-        const int iv = 2 * j + 1, ik = 2 * j + 2;
-        if (!(ok = full(iv))) break;
+        const int sv = pos.slot;
+        ok = full(sv, pos.phase);
+        pos.step(1, kSlots);
+        const int sk = pos.slot;
+        const uint32_t pk = pos.phase;
+        pos.step(1, kSlots);
         bool have_k = false;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           if (j >= n[t]) continue;
-          if (!(ok = mbar_wait(bar(kProbs + t), (uint32_t)j & 1u, abort_flag, kErrMma, a.err))) break;
+          ok = ok && mbar_wait(bar(kProbs + t), (uint32_t)j & 1u, abort_flag, kErrMma, a.err);
+          const bool more = j + 1 < n[t];
+          if (!__all_sync(0xffffffffu, ok)) break;
           tc_fence_after();
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < kTile / 16; ++k)
-            tc_mma_f16_ts(tmem + 256 + t * D, tmem + t * kTile + 8 * k,
-                          sw128_mnmajor_desc(base + (2 + iv % kSlots) * kBytes + k * 2048), idesc_o, j > 0 || k > 0);
-          if (j + 1 < n[t]) {
-            if (!have_k) {
-              if (!(ok = full(ik))) break;
-              tc_fence_after();
-              have_k = true;
-            }
-            score(t, ik % kSlots);
-          } else {
-            tc_commit(bar(kOut + t));
+            for (int k = 0; k < kTile / 16; ++k)
+              mma_ts(tmem + 256 + t * D, tmem + t * kTile + 8 * k, v_lo + sv * (kBytes >> 4) + k * (2048 >> 4), kDescHi, idesc_o,
+                     j > 0 || k > 0);
+            if (!more) tc_commit(bar(kOut + t));
           }
+          __syncwarp();
+          if (!more) continue;
+          if (!have_k) ok = full(sk, pk);
+          have_k = true;
+          if (!__all_sync(0xffffffffu, ok)) break;
+          tc_fence_after();
+          if (elect_one()) score(t, sk);
+          __syncwarp();
         }
-        if (!ok) break;
-        tc_commit(bar(kEmpty + iv % kSlots));
-        if (have_k) tc_commit(bar(kEmpty + ik % kSlots));
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok && elect_one()) {
+          tc_commit(bar(kEmpty + sv));
+          if (have_k) tc_commit(bar(kEmpty + sk));
+        }
+        __syncwarp();
       }
-      if (!ok) {
+      if (!ok && elect_one()) {
         // no product may run past the release of the tensor memory
         tc_commit(bar(kDrain));
         mbar_drain(bar(kDrain), 0u, a.err);
       }
+      __syncwarp();
     }
   }
   tc_fence_before();
