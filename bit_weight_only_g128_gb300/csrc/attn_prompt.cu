@@ -20,7 +20,7 @@
 //                    (rows beyond the sequence as zeros, so that what the
 //                    cache holds there meets P = 0 as 0); e4m3 codes become
 //                    16-bit values on the way
-//   warp 12          tcgen05.mma: S from shared memory, O += P V with P read
+//   warps 12, 13     tcgen05.mma of tile 0, 1: S from shared memory, O += P V with P read
 //                    from tensor memory, where it takes the place of S
 // Tensor memory: S0, S1 (128 columns each), O0, O1 (D each). Registers: 128 a
 // thread at launch, 192 for the softmax warps and 64 for the rest (256 x 192
@@ -38,14 +38,16 @@ using namespace tc;
 constexpr int kThreads = 512;
 constexpr int kTile = 128;  // rows of a tile, and keys of a tile
 constexpr int kSlots = 5;
+constexpr int kLag = 2;  // tiles whose copies are in flight behind the one being issued
 constexpr int kPanel = kTile * 128;  // bytes of 64 dimensions of 128 rows
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.f;  // log2 of how far a row's maximum may run ahead
 
-// barriers: full[kSlots], empty[kSlots], queries[2], scores[2], probs[2], out[2],
-// drain
+// barriers: full[kSlots], empty[kSlots], queries[2], scores[2], probs[2 halves][2],
+// out[2], drain[2], turn[2]
 enum { kFull = 0, kEmpty = kSlots, kQueries = 2 * kSlots, kScores = kQueries + 2, kProbs = kScores + 2,
-       kOut = kProbs + 2, kDrain = kOut + 2, kBars };
+       kOut = kProbs + 4, kDrain = kOut + 2, kTurn = kDrain + 2,
+       kBars = kTurn + 2 };
 
 struct Control {
   uint64_t bars[kBars];
@@ -91,6 +93,33 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// Two fp32 lanes of one 64-bit register.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  return v;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// Keeps the uses of loaded tensor-memory registers behind the wait for them.
+__device__ __forceinline__ void tie(uint32_t (&r)[32]) {
+  asm volatile(""
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
 }
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool valid) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
@@ -202,15 +231,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
   if (tid == 0) {
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(bar(kFull + i), 128);
-      mbar_init(bar(kEmpty + i), 1);
+      mbar_init(bar(kEmpty + i), 2);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar(kQueries + t), 128);
       mbar_init(bar(kScores + t), 1);
       mbar_init(bar(kProbs + t), 128);
+      mbar_init(bar(kProbs + 2 + t), 128);
       mbar_init(bar(kOut + t), 1);
+      mbar_init(bar(kDrain + t), 1);
+      mbar_init(bar(kTurn + t), 1);
     }
-    mbar_init(bar(kDrain), 1);
     ctl.abort = 0;
     fence_barrier_init();
   }
@@ -261,6 +292,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
 #pragma unroll
       for (int q = 0; q < 4; ++q) tmem_ld32(scores + 32 * q, s[q]);
       tmem_wait_ld();
+#pragma unroll
+      for (int q = 0; q < 4; ++q) tie(s[q]);
       const int seen = limit - j * kTile;
       if (!__all_sync(0xffffffffu, seen >= kTile)) {
 #pragma unroll
@@ -271,12 +304,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
       }
       float top4[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float u = fmaxf(__uint_as_float(s[q][0]), __uint_as_float(s[q][1]));
+      for (int q = 0; q < 4; ++q) top4[q] = fmaxf(__uint_as_float(s[q][0]), __uint_as_float(s[q][1]));
 #pragma unroll
-        for (int i = 2; i < 32; i += 2) u = fmaxf(fmaxf(u, __uint_as_float(s[q][i])), __uint_as_float(s[q][i + 1]));
-        top4[q] = u;
-      }
+      for (int i = 2; i < 32; i += 2)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          top4[q] = fmaxf(fmaxf(top4[q], __uint_as_float(s[q][i])), __uint_as_float(s[q][i + 1]));
       const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * mult;
       const bool moves = top > m + kSlack;
       if (__any_sync(0xffffffffu, moves)) {
@@ -297,23 +330,36 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
         }
       }
       const float shift = m == -INFINITY ? 0.f : -m;
-      float l4[4] = {0.f, 0.f, 0.f, 0.f};
+      // P in two halves of 64 keys: the product with the first runs while the
+      // second is formed; the sums wait until both are on their way
+      const uint64_t mult2 = pack2(mult, mult), shift2 = pack2(shift, shift);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t w[16];
+      for (int half = 0; half < 2; ++half) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float x = ex2(fmaf(__uint_as_float(s[q][2 * i]), mult, shift));
-          const float y = ex2(fmaf(__uint_as_float(s[q][2 * i + 1]), mult, shift));
-          l4[i & 3] += x + y;
-          w[i] = pack16<kP>(x, y);
+        for (int q = 2 * half; q < 2 * half + 2; ++q) {
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float x, y;
+            unpack2(fma2(pack2(__uint_as_float(s[q][2 * i]), __uint_as_float(s[q][2 * i + 1])), mult2, shift2), x, y);
+            x = ex2(x), y = ex2(y);
+            s[q][2 * i] = __float_as_uint(x), s[q][2 * i + 1] = __float_as_uint(y);
+            w[i] = pack16<kP>(x, y);
+          }
+          tmem_st16(scores + 16 * q, w);
         }
-        tmem_st16(scores + 16 * q, w);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(kProbs + 2 * half + t));
       }
-      l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(bar(kProbs + t));
+      uint64_t l4[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < 32; i += 2)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) l4[q] = add2(l4[q], pack2(__uint_as_float(s[q][i]), __uint_as_float(s[q][i + 1])));
+      float lo, hi;
+      unpack2(add2(add2(l4[0], l4[1]), add2(l4[2], l4[3])), lo, hi);
+      l += lo + hi;
     }
     if (ok && nt > 0) ok = mbar_wait(bar(kOut + t), 0u, abort_flag, kErrEpilogue, a.err);
     tc_fence_after();
@@ -326,6 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
         if (nt > 0) {
           tmem_ld32(out + c, o);
           tmem_wait_ld();
+          tie(o);
         } else {
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = 0;
@@ -391,150 +438,154 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
         return ((((unsigned long long)page_of(a, b, key >> shift) * a.cache.kv_heads + hk) << shift) + (key & mask)) *
                (D * (k8 ? 1 : 2));
       };
+      // A thread copies one chunk c of the rows r0 + x * kStride, of a tile's
+      // eight groups of 16 rows (a group lies in one page): with these strides
+      // the group is a constant of x (and of the warp), and so is the place in
+      // the swizzled tile but for the thread's own offset.
+      constexpr int kPieces = k8 ? D / 16 : kChunks;  // 16-byte pieces of a row in the cache
+      constexpr int kStride = 128 / kPieces, kLoads = kTile / kStride;
+      constexpr int kRowBytes = D * (k8 ? 1 : 2);
+      const int r0 = u / kPieces, c = u % kPieces;
+      const unsigned long long own = (unsigned long long)((r0 & 15) * kRowBytes + c * 16);
+      auto announce = [&](int i) {  // tile i is in shared memory (and with the first the queries)
+        fence_async_shared();
+        if (i == 0) {
+          mbar_arrive(bar(kQueries));
+          mbar_arrive(bar(kQueries + 1));
+        }
+        mbar_arrive(bar(kFull + i % kSlots));
+      };
       unsigned long long at = most > 0 ? place(0) : 0;
-      int waiting = 0;  // tiles copied, not yet announced
-      for (int i = 0; i < 2 * most && ok; ++i) {
-        const int j = i >> 1, slot = i % kSlots;
-        const uint8_t* src = static_cast<const uint8_t*>(i & 1 ? a.cache.v : a.cache.k);
+      RingPos pos;
+      pos.init(0, kSlots);
+      int i = 0;
+      for (; i < 2 * most && ok; ++i) {
+        const int j = i >> 1, slot = pos.slot;
+        const uint8_t* src = static_cast<const uint8_t*>(i & 1 ? a.cache.v : a.cache.k) + own;
         const uint32_t dst = base + (2 + slot) * kBytes;
+        const bool inside = (j + 1) * kTile <= len;
+        const uint32_t freed = pos.phase ^ 1u;
+        pos.step(1, kSlots);
         auto wait_slot = [&]() {
-          return i < kSlots || mbar_wait(bar(kEmpty + slot), (uint32_t)(i / kSlots - 1) & 1u, abort_flag, kErrProducer, a.err);
+          return i < kSlots || mbar_wait(bar(kEmpty + slot), freed, abort_flag, kErrProducer, a.err);
+        };
+        auto row = [&](int x) {  // the bytes of row r0 + x * kStride
+          const int group = kStride >= 16 ? x * (kStride / 16) + (r0 >> 4) : x / (16 / kStride);
+          const unsigned long long g = __shfl_sync(0xffffffffu, at, group);
+          return src + g + (kStride < 16 ? x % (16 / kStride) * kStride * kRowBytes : 0);
         };
         if (k8) {
-          constexpr int kPieces = D / 16;                   // 16-code pieces of a row
-          constexpr int kLoads = kTile * kPieces / 128;     // per thread
           uint4 v[kLoads];
 #pragma unroll
           for (int x = 0; x < kLoads; ++x) {
-            const int e = x * 128 + u, r = e / kPieces, c = e % kPieces;
-            const unsigned long long row = __shfl_sync(0xffffffffu, at, r >> 4) + (unsigned long long)((r & 15) * D + c * 16);
+            const uint8_t* p8 = row(x);
             v[x] = make_uint4(0, 0, 0, 0);
-            if (j * kTile + r < len) v[x] = ldg_stream(reinterpret_cast<const uint4*>(src + row));
+            if (inside || j * kTile + r0 + x * kStride < len) v[x] = ldg_stream(reinterpret_cast<const uint4*>(p8));
           }
           if (!(ok = wait_slot())) break;
+          const uint32_t lo_at = dst + chunk_at(r0, 2 * c), hi_at = dst + chunk_at(r0, 2 * c + 1);
 #pragma unroll
-          for (int x = 0; x < kLoads; ++x) {
-            const int e = x * 128 + u, r = e / kPieces, c = e % kPieces;
+          for (int x = 0; x < kLoads; ++x) {  // kStride is a multiple of 8: the swizzle stays
             const uint4 lo = widen(v[x].x, v[x].y), hi = widen(v[x].z, v[x].w);
-            sts128(dst + chunk_at(r, 2 * c), lo.x, lo.y, lo.z, lo.w);
-            sts128(dst + chunk_at(r, 2 * c + 1), hi.x, hi.y, hi.z, hi.w);
+            sts128(lo_at + x * kStride * 128, lo.x, lo.y, lo.z, lo.w);
+            sts128(hi_at + x * kStride * 128, hi.x, hi.y, hi.z, hi.w);
           }
           if (i == 0) cp_wait<0>();
-          fence_async_shared();
-          if (i == 0) {
-            mbar_arrive(bar(kQueries));
-            mbar_arrive(bar(kQueries + 1));
-          }
-          mbar_arrive(bar(kFull + slot));
+          announce(i);
         } else {
           if (!(ok = wait_slot())) break;
-#pragma unroll 4
-          for (int x = 0; x < kTile * kChunks / 128; ++x) {
-            const int e = x * 128 + u, r = e / kChunks, c = e % kChunks;
-            const unsigned long long row = __shfl_sync(0xffffffffu, at, r >> 4) + (unsigned long long)((r & 15) * (2 * D) + c * 16);
-            const bool valid = j * kTile + r < len;
-            cp16(dst + chunk_at(r, c), valid ? src + row : src, valid);
+          const uint32_t at0 = dst + chunk_at(r0, c);
+          if (inside) {
+#pragma unroll
+            for (int x = 0; x < kLoads; ++x) cp16(at0 + x * kStride * 128, row(x), true);
+          } else {
+#pragma unroll
+            for (int x = 0; x < kLoads; ++x) {
+              const bool valid = j * kTile + r0 + x * kStride < len;
+              const uint8_t* from = row(x);
+              cp16(at0 + x * kStride * 128, valid ? from : src, valid);
+            }
           }
           cp_commit();
-          // announce the tile before this one (and with the first the queries)
-          if (i > 0) {
-            cp_wait<1>();
-            fence_async_shared();
-            if (i == 1) {
-              mbar_arrive(bar(kQueries));
-              mbar_arrive(bar(kQueries + 1));
-            }
-            mbar_arrive(bar(kFull + (i - 1) % kSlots));
+          if (i >= kLag) {  // the copies of kLag tiles stay in flight
+            cp_wait<kLag>();
+            announce(i - kLag);
           }
-          waiting = 1;
         }
         if ((i & 1) && j + 1 < most) at = place(j + 1);
       }
       cp_wait<0>();
-      if (!k8 && ok && waiting) {
-        fence_async_shared();
-        mbar_arrive(bar(kFull + (2 * most - 1) % kSlots));
-      }
-    } else if (warp == 12) {
-      // the whole warp waits; one elected lane issues (operands that are known
-      // to be uniform over the warp)
+      if (!k8 && ok)
+        for (int x = i < kLag ? 0 : i - kLag; x < i; ++x) announce(x);
+    } else if (warp < 14 && elect_one()) {
+      // one warp per row tile, one thread of it
       constexpr uint32_t kDescHi = (uint32_t)(1024 >> 4) | (1u << 14) | (2u << 29);  // the upper half of both descriptors
+      const int t = warp - 12, nt = t ? n[1] : n[0];
+      const uint32_t scores = tmem + t * kTile, out = tmem + 256 + t * D;
       const uint32_t idesc_s = f16_idesc(kTile, kTile, kP) | (p.negate << 13);
       const uint32_t idesc_o = f16_idesc(kTile, D, kP) | (1u << 16);  // B with the dimensions innermost
-      const uint32_t q_lo = ((base & 0x3FFFFu) >> 4) | (1u << 16);                        // K-major
+      const uint32_t q_lo = (((base + t * kBytes) & 0x3FFFFu) >> 4) | (1u << 16);  // K-major
       const uint32_t k_lo = (((base + 2 * kBytes) & 0x3FFFFu) >> 4) | (1u << 16);
       const uint32_t v_lo = (((base + 2 * kBytes) & 0x3FFFFu) >> 4) | ((uint32_t)(kPanel >> 4) << 16);  // MN-major
       bool ok = true;
-      auto score = [&](int t, int slot) {
+      auto wait = [&](int i, uint32_t phase) {
+        ok = mbar_wait(bar(i), phase, abort_flag, kErrMma, a.err);
+        return ok;
+      };
+      auto score = [&](int slot) {
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t off = (uint32_t)((k >> 2) * kPanel + (k & 3) * 32) >> 4;
-          mma_ss(tmem + t * kTile, q_lo + t * (kBytes >> 4) + off, k_lo + slot * (kBytes >> 4) + off, kDescHi, idesc_s, k > 0);
+          mma_ss(scores, q_lo + off, k_lo + slot * (kBytes >> 4) + off, kDescHi, idesc_s, k > 0);
         }
         tc_commit(bar(kScores + t));
+        tc_commit(bar(kEmpty + slot));
       };
-      auto full = [&](int slot, uint32_t phase) { return mbar_wait(bar(kFull + slot), phase, abort_flag, kErrMma, a.err); };
+      auto value = [&](int slot, int half, bool add) {  // 64 keys
+#pragma unroll
+        for (int k = 4 * half; k < 4 * half + 4; ++k)
+          mma_ts(out, scores + 8 * k, v_lo + slot * (kBytes >> 4) + k * (2048 >> 4), kDescHi, idesc_o, add || k > 0);
+      };
       RingPos pos;  // of the next tile
       pos.init(0, kSlots);
-      if (most > 0) {
-        ok = mbar_wait(bar(kQueries), 0u, abort_flag, kErrMma, a.err) &&
-             mbar_wait(bar(kQueries + 1), 0u, abort_flag, kErrMma, a.err) && full(0, 0);
-        ok = __all_sync(0xffffffffu, ok);
-        if (ok) {
-          tc_fence_after();
-          if (elect_one()) {
-            for (int t = 0; t < 2; ++t)
-              if (n[t] > 0) score(t, 0);
-            tc_commit(bar(kEmpty));
-          }
-          __syncwarp();
-        }
+      if (most > 0 && (nt == 0 || wait(kQueries + t, 0)) && wait(kFull, 0)) {
+        tc_fence_after();
+        if (nt > 0) score(0); else mbar_arrive(bar(kEmpty));
         pos.step(1, kSlots);
       }
       for (int j = 0; j < most && ok; ++j) {
         const int sv = pos.slot;
-        ok = full(sv, pos.phase);
+        const uint32_t pv = pos.phase;
         pos.step(1, kSlots);
         const int sk = pos.slot;
         const uint32_t pk = pos.phase;
         pos.step(1, kSlots);
-        bool have_k = false;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (j >= n[t]) continue;
-          ok = ok && mbar_wait(bar(kProbs + t), (uint32_t)j & 1u, abort_flag, kErrMma, a.err);
-          const bool more = j + 1 < n[t];
-          if (!__all_sync(0xffffffffu, ok)) break;
+        const bool more = j + 1 < nt;
+        // the tiles take turns, so that one's products run while the other's
+        // softmax does: in step they would wait for the tensor cores together
+        if (!wait(kFull + sv, pv)) break;
+        if (j + 1 < most && !wait(kFull + sk, pk)) break;
+        if (j < nt && !wait(kProbs + t, (uint32_t)j & 1u)) break;
+        if ((t || j) && !wait(kTurn + t, (uint32_t)(t ? j : j - 1) & 1u)) break;
+        if (j < nt) {
           tc_fence_after();
-          if (elect_one()) {
-#pragma unroll
-            for (int k = 0; k < kTile / 16; ++k)
-              mma_ts(tmem + 256 + t * D, tmem + t * kTile + 8 * k, v_lo + sv * (kBytes >> 4) + k * (2048 >> 4), kDescHi, idesc_o,
-                     j > 0 || k > 0);
-            if (!more) tc_commit(bar(kOut + t));
-          }
-          __syncwarp();
-          if (!more) continue;
-          if (!have_k) ok = full(sk, pk);
-          have_k = true;
-          if (!__all_sync(0xffffffffu, ok)) break;
+          value(sv, 0, j > 0);
+          if (!wait(kProbs + 2 + t, (uint32_t)j & 1u)) break;
           tc_fence_after();
-          if (elect_one()) score(t, sk);
-          __syncwarp();
-        }
-        ok = __all_sync(0xffffffffu, ok);
-        if (ok && elect_one()) {
+          value(sv, 1, true);
           tc_commit(bar(kEmpty + sv));
-          if (have_k) tc_commit(bar(kEmpty + sk));
+          if (more) score(sk); else tc_commit(bar(kOut + t));
+        } else {
+          mbar_arrive(bar(kEmpty + sv));  // a tile that only the other rows need
         }
-        __syncwarp();
+        mbar_arrive(bar(kTurn + 1 - t));
+        if (!more && j + 1 < most) mbar_arrive(bar(kEmpty + sk));
       }
-      if (!ok && elect_one()) {
+      if (!ok) {
         // no product may run past the release of the tensor memory
-        tc_commit(bar(kDrain));
-        mbar_drain(bar(kDrain), 0u, a.err);
+        tc_commit(bar(kDrain + t));
+        mbar_drain(bar(kDrain + t), 0u, a.err);
       }
-      __syncwarp();
     }
   }
   tc_fence_before();
