@@ -16,10 +16,11 @@
 //   warps 0-3, 4-7   softmax of tile 0, 1 (a thread owns a row: a lane of
 //                    tensor memory), the rare rescaling of O, the results
 //   warps 8-11       copies: queries, then the tiles K0 V0 K1 V1 .. into a
-//                    ring of five slots, from their pages, 16 bytes at a time
-//                    (rows beyond the sequence as zeros, so that what the
-//                    cache holds there meets P = 0 as 0); e4m3 codes become
-//                    16-bit values on the way
+//                    ring of five slots: tile copies (TMA) of the pages' rows;
+//                    16 bytes at a time where a tile ends beyond the sequence
+//                    (those rows as zeros, so that what the cache holds there
+//                    meets P = 0 as 0) and for e4m3 codes, which become fp16
+//                    on the way
 //   warps 12, 13     tcgen05.mma of tile 0, 1: S from shared memory, O += P V with P read
 //                    from tensor memory, where it takes the place of S
 // Tensor memory: S0, S1 (128 columns each), O0, O1 (D each). Registers: 128 a
@@ -38,7 +39,6 @@ using namespace tc;
 constexpr int kThreads = 512;
 constexpr int kTile = 128;  // rows of a tile, and keys of a tile
 constexpr int kSlots = 5;
-constexpr int kLag = 2;  // tiles whose copies are in flight behind the one being issued
 constexpr int kPanel = kTile * 128;  // bytes of 64 dimensions of 128 rows
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.f;  // log2 of how far a row's maximum may run ahead
@@ -68,6 +68,7 @@ struct PromptArgs {
   int group;
   float mult;      // |scale| log2 e
   uint32_t negate;  // scale < 0
+  int tiled;        // the maps are there
 };
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
@@ -134,6 +135,15 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
   return (uint32_t)((c >> 3) * kPanel + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
+// Among the 128 copying threads.
+__device__ __forceinline__ void loaders_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+// The row of a key, or 0 for one beyond the sequence (whose page is not looked up).
+template <class F>
+__device__ __forceinline__ unsigned long long row_of_or_0(const F& row_of, int key, int len) {
+  return key < len ? row_of(key) : 0ull;
+}
+
 // True in one lane of the (converged) warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t ok;
@@ -176,7 +186,8 @@ __device__ __forceinline__ uint4 widen(uint32_t lo, uint32_t hi) {
 // fp16, which holds every code; bf16 queries are then divided by a power of
 // two per row that brings them into fp16's range.
 template <bool kB, bool k8, int D>
-__global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptArgs p) {
+__global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptArgs p, const __grid_constant__ CUtensorMap map_k,
+                                                                 const __grid_constant__ CUtensorMap map_v) {
   constexpr int kBytes = kTileBytes<D>;
   constexpr bool kP = kB && !k8;  // products in bf16
   extern __shared__ uint8_t smem_raw[];
@@ -230,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
   }
   if (tid == 0) {
     for (int i = 0; i < kSlots; ++i) {
-      mbar_init(bar(kFull + i), 128);
+      mbar_init(bar(kFull + i), k8 ? 128 : 1);
       mbar_init(bar(kEmpty + i), 2);
     }
     for (int t = 0; t < 2; ++t) {
@@ -428,61 +439,96 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
             }
           }
         }
-        cp_commit();
       }
+      cp_commit();
+      cp_wait<0>();
+      fence_async_shared();
+      mbar_arrive(bar(kQueries));
+      mbar_arrive(bar(kQueries + 1));
       const int shift = a.cache.page_shift, mask = (1 << shift) - 1;
-      // byte offset of row 16 * (lane & 7) of key tile j in the caches
-      auto place = [&](int j) -> unsigned long long {
-        const int key = j * kTile + 16 * (lane & 7);
-        if (key >= len) return 0;
-        return ((((unsigned long long)page_of(a, b, key >> shift) * a.cache.kv_heads + hk) << shift) + (key & mask)) *
-               (D * (k8 ? 1 : 2));
-      };
-      // A thread copies one chunk c of the rows r0 + x * kStride, of a tile's
-      // eight groups of 16 rows (a group lies in one page): with these strides
-      // the group is a constant of x (and of the warp), and so is the place in
-      // the swizzled tile but for the thread's own offset.
-      constexpr int kPieces = k8 ? D / 16 : kChunks;  // 16-byte pieces of a row in the cache
-      constexpr int kStride = 128 / kPieces, kLoads = kTile / kStride;
-      constexpr int kRowBytes = D * (k8 ? 1 : 2);
-      const int r0 = u / kPieces, c = u % kPieces;
-      const unsigned long long own = (unsigned long long)((r0 & 15) * kRowBytes + c * 16);
-      auto announce = [&](int i) {  // tile i is in shared memory (and with the first the queries)
-        fence_async_shared();
-        if (i == 0) {
-          mbar_arrive(bar(kQueries));
-          mbar_arrive(bar(kQueries + 1));
-        }
-        mbar_arrive(bar(kFull + i % kSlots));
-      };
-      unsigned long long at = most > 0 ? place(0) : 0;
       RingPos pos;
       pos.init(0, kSlots);
       int i = 0;
-      for (; i < 2 * most && ok; ++i) {
-        const int j = i >> 1, slot = pos.slot;
-        const uint8_t* src = static_cast<const uint8_t*>(i & 1 ? a.cache.v : a.cache.k) + own;
-        const uint32_t dst = base + (2 + slot) * kBytes;
-        const bool inside = (j + 1) * kTile <= len;
-        const uint32_t freed = pos.phase ^ 1u;
-        pos.step(1, kSlots);
-        auto wait_slot = [&]() {
-          return i < kSlots || mbar_wait(bar(kEmpty + slot), freed, abort_flag, kErrProducer, a.err);
-        };
-        auto row = [&](int x) {  // the bytes of row r0 + x * kStride
-          const int group = kStride >= 16 ? x * (kStride / 16) + (r0 >> 4) : x / (16 / kStride);
-          const unsigned long long g = __shfl_sync(0xffffffffu, at, group);
-          return src + g + (kStride < 16 ? x % (16 / kStride) * kStride * kRowBytes : 0);
-        };
-        if (k8) {
+      auto wait_slot = [&]() {
+        return i < kSlots || mbar_wait(bar(kEmpty + pos.slot), pos.phase ^ 1u, abort_flag, kErrProducer, a.err);
+      };
+      // the first row, in the cache seen as rows of D values, of this head's
+      // place of key `key` of the sequence
+      auto row_of = [&](int key) {
+        return (((unsigned long long)page_of(a, b, key >> shift) * a.cache.kv_heads + hk) << shift) + (key & mask);
+      };
+      if (!k8) {
+        // tiles that lie inside the sequence: tile copies of the pages' rows,
+        // a lane of the first warp for each page and panel
+        const int whole = p.tiled ? min(most, len / kTile) : 0;
+        if (warp == 8) {
+          const int box = min(1 << shift, kTile), boxes = kTile / box;
+          const int panel = lane / boxes, part = lane % boxes;
+          unsigned long long row = 0;
+          for (; i < 2 * whole && ok; ++i) {
+            const int j = i >> 1;
+            if (!(i & 1)) row = row_of(j * kTile + part * box);
+            if (!(ok = wait_slot())) break;
+            const uint32_t full = bar(kFull + pos.slot);
+            if (lane == 0) mbar_expect_tx(full, kBytes);
+            __syncwarp();
+            if (lane < D / 64 * boxes)
+              tma_load_2d(base + (2 + pos.slot) * kBytes + panel * kPanel + part * box * 128, i & 1 ? &map_v : &map_k, panel * 64,
+                          (int)row, full);
+            pos.step(1, kSlots);
+          }
+          ok = __all_sync(0xffffffffu, ok);
+        } else {
+          i = 2 * whole;
+          pos.init(i, kSlots);
+        }
+        // the ragged last tile: 16 bytes at a time, rows beyond the sequence
+        // as zeros
+        if (whole < most) {
+          loaders_sync();  // the ring's slots are within one round of `pos`
+          const int r0 = u / kChunks, c = u % kChunks;
+          constexpr int kStride = 128 / kChunks;
+          for (; i < 2 * most && ok; ++i) {
+            const uint8_t* src = static_cast<const uint8_t*>(i & 1 ? a.cache.v : a.cache.k);
+            const unsigned long long group = row_of_or_0(row_of, (i >> 1) * kTile + 16 * (lane & 7), len);
+            ok = wait_slot();
+            const uint32_t dst = base + (2 + pos.slot) * kBytes + chunk_at(r0, c);
+#pragma unroll 4
+            for (int x = 0; x < kTile / kStride; ++x) {
+              const int r = r0 + x * kStride;
+              const unsigned long long row = __shfl_sync(0xffffffffu, group, r >> 4) + (r & 15);
+              const bool valid = ok && (i >> 1) * kTile + r < len;
+              cp16(dst + x * kStride * 128, valid ? src + row * (2 * D) + c * 16 : src, valid);
+            }
+            cp_commit();
+            cp_wait<0>();
+            fence_async_shared();
+            loaders_sync();
+            if (u == 0 && ok) mbar_arrive(bar(kFull + pos.slot));
+            pos.step(1, kSlots);
+          }
+        }
+      } else {
+        // A thread copies one 16-code piece c of the rows r0 + x * kStride of
+        // a tile's eight groups of 16 rows (a group lies in one page): the
+        // group is a constant of x and of the warp.
+        constexpr int kPieces = D / 16, kStride = 128 / kPieces, kLoads = kTile / kStride;
+        const int r0 = u / kPieces, c = u % kPieces;
+        unsigned long long group = 0;
+        for (; i < 2 * most; ++i) {
+          const int j = i >> 1;
+          if (!(i & 1)) group = row_of_or_0(row_of, j * kTile + 16 * (lane & 7), len) * D;
+          const uint8_t* src = static_cast<const uint8_t*>(i & 1 ? a.cache.v : a.cache.k) + (r0 & 15) * D + c * 16;
+          const bool inside = (j + 1) * kTile <= len;
           uint4 v[kLoads];
 #pragma unroll
           for (int x = 0; x < kLoads; ++x) {
-            const uint8_t* p8 = row(x);
+            const uint8_t* from = src + __shfl_sync(0xffffffffu, group, x * (kStride / 16) + (r0 >> 4));
             v[x] = make_uint4(0, 0, 0, 0);
-            if (inside || j * kTile + r0 + x * kStride < len) v[x] = ldg_stream(reinterpret_cast<const uint4*>(p8));
+            if (inside || j * kTile + r0 + x * kStride < len) v[x] = ldg_stream(reinterpret_cast<const uint4*>(from));
           }
           if (!(ok = wait_slot())) break;
+          const uint32_t dst = base + (2 + pos.slot) * kBytes;
           const uint32_t lo_at = dst + chunk_at(r0, 2 * c), hi_at = dst + chunk_at(r0, 2 * c + 1);
 #pragma unroll
           for (int x = 0; x < kLoads; ++x) {  // kStride is a multiple of 8: the swizzle stays
@@ -490,33 +536,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
             sts128(lo_at + x * kStride * 128, lo.x, lo.y, lo.z, lo.w);
             sts128(hi_at + x * kStride * 128, hi.x, hi.y, hi.z, hi.w);
           }
-          if (i == 0) cp_wait<0>();
-          announce(i);
-        } else {
-          if (!(ok = wait_slot())) break;
-          const uint32_t at0 = dst + chunk_at(r0, c);
-          if (inside) {
-#pragma unroll
-            for (int x = 0; x < kLoads; ++x) cp16(at0 + x * kStride * 128, row(x), true);
-          } else {
-#pragma unroll
-            for (int x = 0; x < kLoads; ++x) {
-              const bool valid = j * kTile + r0 + x * kStride < len;
-              const uint8_t* from = row(x);
-              cp16(at0 + x * kStride * 128, valid ? from : src, valid);
-            }
-          }
-          cp_commit();
-          if (i >= kLag) {  // the copies of kLag tiles stay in flight
-            cp_wait<kLag>();
-            announce(i - kLag);
-          }
+          fence_async_shared();
+          mbar_arrive(bar(kFull + pos.slot));
+          pos.step(1, kSlots);
         }
-        if ((i & 1) && j + 1 < most) at = place(j + 1);
       }
       cp_wait<0>();
-      if (!k8 && ok)
-        for (int x = i < kLag ? 0 : i - kLag; x < i; ++x) announce(x);
     } else if (warp < 14 && elect_one()) {
       // one warp per row tile, one thread of it
       constexpr uint32_t kDescHi = (uint32_t)(1024 >> 4) | (1u << 14) | (2u << 29);  // the upper half of both descriptors
@@ -597,11 +622,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
 }
 
 template <bool kB, bool k8, int D>
-cudaError_t launch(const PromptArgs& p, unsigned blocks, cudaStream_t stream) {
+cudaError_t launch(PromptArgs p, unsigned blocks, cudaStream_t stream) {
+  // the caches as rows of D values, copied in panels of 64 dimensions by up to
+  // 128 rows of a page (row numbers are 32-bit coordinates)
+  CUtensorMap map_k = {}, map_v = {};
+  const long long rows = ((long long)p.a.cache.pages * p.a.cache.kv_heads) << p.a.cache.page_shift;
+  p.tiled = !k8 && rows <= 0x7fffffff;
+  if (p.tiled) {
+    const auto dt = kB ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const uint32_t box = 1u << (p.a.cache.page_shift < 7 ? p.a.cache.page_shift : 7);
+    if (!encode_tensor_map(&map_k, p.a.cache.k, dt, 2, D, (uint64_t)rows, 64, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_tensor_map(&map_v, p.a.cache.v, dt, 2, D, (uint64_t)rows, 64, box, CU_TENSOR_MAP_SWIZZLE_128B))
+      return cudaErrorInvalidValue;
+  }
   auto kern = attn_prompt_kernel<kB, k8, D>;
   cudaError_t e = set_max_smem_once(reinterpret_cast<const void*>(kern), kSmem<D>);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(blocks), dim3(kThreads), kSmem<D>, stream, p);
+  return launch_pdl(kern, dim3(blocks), dim3(kThreads), kSmem<D>, stream, p, map_k, map_v);
 }
 
 }  // namespace
