@@ -21,7 +21,7 @@
 //                    (those rows as zeros, so that what the cache holds there
 //                    meets P = 0 as 0) and for e4m3 codes, which become fp16
 //                    on the way
-//   warps 12, 13     tcgen05.mma of tile 0, 1: S from shared memory, O += P V with P read
+//   warps 14, 15     tcgen05.mma of tile 0, 1: S from shared memory, O += P V with P read
 //                    from tensor memory, where it takes the place of S
 // Tensor memory: S0, S1 (128 columns each), O0, O1 (D each). Registers: 128 a
 // thread at launch, 192 for the softmax warps and 64 for the rest (256 x 192
@@ -43,7 +43,7 @@ constexpr int kPanel = kTile * 128;  // bytes of 64 dimensions of 128 rows
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.f;  // log2 of how far a row's maximum may run ahead
 
-// barriers: full[kSlots], empty[kSlots], queries[2], scores[2], probs[2 halves][2],
+// barriers: full[kSlots], empty[kSlots], queries[2], scores[2], probs[2 parts][2],
 // out[2], drain[2], turn[2]
 enum { kFull = 0, kEmpty = kSlots, kQueries = 2 * kSlots, kScores = kQueries + 2, kProbs = kScores + 2,
        kOut = kProbs + 4, kDrain = kOut + 2, kTurn = kDrain + 2,
@@ -341,13 +341,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
         }
       }
       const float shift = m == -INFINITY ? 0.f : -m;
-      // P in two halves of 64 keys: the product with the first runs while the
-      // second is formed; the sums wait until both are on their way
+      // P in two parts, of 96 and 32 keys: the product with the first runs
+      // while the second is formed; the sums wait until both are on their way
       const uint64_t mult2 = pack2(mult, mult), shift2 = pack2(shift, shift);
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
+      for (int part = 0; part < 2; ++part) {
 #pragma unroll
-        for (int q = 2 * half; q < 2 * half + 2; ++q) {
+        for (int q = part ? 3 : 0; q < (part ? 4 : 3); ++q) {
           uint32_t w[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
         }
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(bar(kProbs + 2 * half + t));
+        mbar_arrive(bar(kProbs + 2 * part + t));
       }
       uint64_t l4[4] = {0, 0, 0, 0};
 #pragma unroll
@@ -542,10 +542,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
         }
       }
       cp_wait<0>();
-    } else if (warp < 14 && elect_one()) {
+    } else if (warp >= 14 && elect_one()) {
       // one warp per row tile, one thread of it
       constexpr uint32_t kDescHi = (uint32_t)(1024 >> 4) | (1u << 14) | (2u << 29);  // the upper half of both descriptors
-      const int t = warp - 12, nt = t ? n[1] : n[0];
+      const int t = warp - 14, nt = t ? n[1] : n[0];
       const uint32_t scores = tmem + t * kTile, out = tmem + 256 + t * D;
       const uint32_t idesc_s = f16_idesc(kTile, kTile, kP) | (p.negate << 13);
       const uint32_t idesc_o = f16_idesc(kTile, D, kP) | (1u << 16);  // B with the dimensions innermost
@@ -566,9 +566,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
         tc_commit(bar(kScores + t));
         tc_commit(bar(kEmpty + slot));
       };
-      auto value = [&](int slot, int half, bool add) {  // 64 keys
+      auto value = [&](int slot, int part, bool add) {  // 96 or 32 keys
 #pragma unroll
-        for (int k = 4 * half; k < 4 * half + 4; ++k)
+        for (int k = part ? 6 : 0; k < (part ? 8 : 6); ++k)
           mma_ts(out, scores + 8 * k, v_lo + slot * (kBytes >> 4) + k * (2048 >> 4), kDescHi, idesc_o, add || k > 0);
       };
       RingPos pos;  // of the next tile
