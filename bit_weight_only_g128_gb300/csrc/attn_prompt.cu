@@ -54,7 +54,7 @@ struct Control {
   uint32_t tmem;
   int abort;
   int scan[kThreads / 32];
-  int unit[2];  // sequence, unit of it
+  int unit[5];  // sequence, unit of it, its first row, rows and length
   float power[2 * kTile];  // what a row's queries were divided by (bf16 over e4m3)
 };
 
@@ -200,45 +200,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   volatile int* abort_flag = &ctl.abort;
 
-  allow_dependent_launch();
-  grid_dependency_wait();
-
-  // which unit of 256 rows: the last ones of a sequence (the most keys) first
-  const int hk = blockIdx.x % a.cache.kv_heads;
-  int total = 0;
-  auto units = [&](int b) {
-    return b < a.batch ? (int)(((long long)row_count(a, b) * p.group + 2 * kTile - 1) / (2 * kTile)) : 0;
-  };
-  auto scan = [&](int v) {  // inclusive over the block, and the total
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += u;
-    }
-    if (lane == 31) ctl.scan[warp] = v;
-    __syncthreads();
-    int before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) before += ctl.scan[w];
-      all += ctl.scan[w];
-    }
-    __syncthreads();
-    return make_int2(v + before, all);
-  };
-  for (int b0 = 0; b0 < a.batch; b0 += kThreads) total += scan(units(b0 + tid)).y;
-  const int want = total - 1 - (int)(blockIdx.x / a.cache.kv_heads);
-  if (want < 0) return;
-  for (int b0 = 0, carry = 0; b0 < a.batch; b0 += kThreads) {
-    const int v = units(b0 + tid);
-    const int2 s = scan(v);
-    const int lo = carry + s.x - v;
-    if (lo <= want && want < lo + v) {
-      ctl.unit[0] = b0 + tid;
-      ctl.unit[1] = want - lo;
-    }
-    carry += s.y;
-  }
   if (tid == 0) {
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(bar(kFull + i), k8 ? 128 : 1);
@@ -261,20 +222,90 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
     tmem_relinquish();
   }
   tc_fence_before();
+  allow_dependent_launch();
+  grid_dependency_wait();
+
+  // which unit of 256 rows: the last ones of a sequence (the most keys) first
+  const int hk = blockIdx.x % a.cache.kv_heads;
+  const int turn = (int)(blockIdx.x / a.cache.kv_heads);
+  // units of the sequence b0 + tid, and what is known of it
+  int first = 0, fresh = 0, len = 0;
+  auto units = [&](int b) {
+    fresh = 0;
+    if (b >= a.batch) return 0;
+    const int s0 = a.starts[b], s1 = a.starts[b + 1], n = a.lens[b];
+    first = checked(a, s0, a.rows);
+    fresh = checked(a, s1, a.rows) - first;
+    if (fresh < 0) {
+      atomicOr(a.err, kErrRange);
+      fresh = 0;
+    }
+    len = checked(a, n, (int)min((long long)a.max_pages << a.cache.page_shift, 0x7fffffffll));
+    return (int)(((long long)fresh * p.group + 2 * kTile - 1) / (2 * kTile));
+  };
+  auto scan = [&](int v) {  // inclusive over the block, and the total
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
+    }
+    if (lane == 31) ctl.scan[warp] = v;
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += ctl.scan[w];
+      all += ctl.scan[w];
+    }
+    __syncthreads();
+    return make_int2(v + before, all);
+  };
+  int want = -1;
+  auto find = [&](int b, int v, int lo) {
+    if (lo <= want && want < lo + v) {
+      ctl.unit[0] = b;
+      ctl.unit[1] = want - lo;
+      ctl.unit[2] = first;
+      ctl.unit[3] = fresh;
+      ctl.unit[4] = len;
+    }
+  };
+  if (a.batch <= kThreads) {
+    const int v = units(tid);
+    const int2 s = scan(v);
+    want = s.y - 1 - turn;
+    find(tid, v, s.x - v);
+  } else {
+    int total = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += kThreads) total += scan(units(b0 + tid)).y;
+    want = total - 1 - turn;
+    for (int b0 = 0, carry = 0; b0 < a.batch; b0 += kThreads) {
+      const int v = units(b0 + tid);
+      const int2 s = scan(v);
+      find(b0 + tid, v, carry + s.x - v);
+      carry += s.y;
+    }
+  }
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl.tmem;
+  if (want < 0) {  // fewer units than blocks
+    if (warp == 12) tmem_dealloc(tmem, 512);
+    return;
+  }
   const int b = ctl.unit[0];
-  const int first = row_start(a, b), fresh = row_count(a, b);
-  const int len = seq_length(a, b), past = len - fresh;  // may be negative: rows that see nothing
-  const long long rows = (long long)fresh * p.group;
-  const long long row0 = (long long)ctl.unit[1] * (2 * kTile);
+  first = ctl.unit[2];
+  fresh = ctl.unit[3];
+  len = ctl.unit[4];
+  const int past = len - fresh;  // may be negative: rows that see nothing
+  const int rows = fresh * p.group;  // at most 2^30
+  const int row0 = ctl.unit[1] * (2 * kTile);
   // key tiles of the two row tiles: up to the last row's position
   int n[2];
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    const long long lo = row0 + t * kTile, hi = min(lo + kTile, rows);
-    const int last = lo < hi ? past + (int)((hi - 1) / p.group) : -1;
+    const int lo = row0 + t * kTile, hi = min(lo + kTile, rows);
+    const int last = lo < hi ? past + (hi - 1) / p.group : -1;
     n[t] = last < 0 ? 0 : last / kTile + 1;
   }
   const int most = max(n[0], n[1]);
@@ -284,9 +315,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
     const int t = warp >> 2;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // the warp's quarter of the lanes
     const uint32_t scores = tmem + lanes + (uint32_t)(t * kTile), out = tmem + lanes + 256u + (uint32_t)(t * D);
-    const long long row = row0 + t * kTile + (tid & 127);
+    const int row = row0 + t * kTile + (tid & 127);
     const bool live = row < rows;
-    const int token = live ? (int)(row / p.group) : 0, head = hk * p.group + (live ? (int)(row % p.group) : 0);
+    const int token = live ? row / p.group : 0, head = hk * p.group + (live ? row % p.group : 0);
     const int limit = live ? past + token + 1 : 0;  // keys this row sees
     float mult = p.mult * (k8 ? a.cache.k_scale[hk] : 1.f);
     const int nt = t ? n[1] : n[0];
@@ -372,11 +403,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
       unpack2(add2(add2(l4[0], l4[1]), add2(l4[2], l4[3])), lo, hi);
       l += lo + hi;
     }
-    if (ok && nt > 0) ok = mbar_wait(bar(kOut + t), 0u, abort_flag, kErrEpilogue, a.err);
+    // (rows without a key wait for their queries only, whose place is used below)
+    if (ok) ok = mbar_wait(bar(nt > 0 ? kOut + t : kQueries + t), 0u, abort_flag, kErrEpilogue, a.err);
     tc_fence_after();
     if (ok) {
       const float inv = l > 0.f ? (k8 ? a.cache.v_scale[hk] : 1.f) / l : 0.f;
-      uint16_t* dst = a.out + ((size_t)(first + token) * a.heads + head) * D;
+      // through the warp's rows of the queries' tile, which no product reads
+      // any more, so that whole rows are written
 #pragma unroll
       for (int c = 0; c < D; c += 32) {
         uint32_t o[32];
@@ -384,67 +417,82 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
           tmem_ld32(out + c, o);
           tmem_wait_ld();
           tie(o);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = 0;
         }
-        if (live) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            float f[8];
+        for (int i = 0; i < 32; i += 8) {
+          float f[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) f[k] = l > 0.f ? __uint_as_float(o[i + k]) * inv : 0.f;
-            *reinterpret_cast<uint4*>(dst + c + i) = make_uint4(pack16<kB>(f[0], f[1]), pack16<kB>(f[2], f[3]),
-                                                                pack16<kB>(f[4], f[5]), pack16<kB>(f[6], f[7]));
-          }
+          for (int k = 0; k < 8; ++k) f[k] = l > 0.f ? __uint_as_float(o[i + k]) * inv : 0.f;
+          sts128(base + t * kBytes + chunk_at(tid & 127, (c + i) / 8), pack16<kB>(f[0], f[1]), pack16<kB>(f[2], f[3]),
+                 pack16<kB>(f[4], f[5]), pack16<kB>(f[6], f[7]));
         }
+      }
+      __syncwarp();
+      constexpr int kChunks = D / 8, kAtOnce = 32 / kChunks;  // rows per store of the warp
+      const int c = lane % kChunks, r1 = lane / kChunks;
+#pragma unroll 4
+      for (int r = r1; r < 32; r += kAtOnce) {
+        const int to = __shfl_sync(0xffffffffu, live ? (first + token) * a.heads + head : -1, r);
+        const uint4 v = lds128(base + t * kBytes + chunk_at((tid & 96) + r, c));
+        if (to >= 0) *reinterpret_cast<uint4*>(a.out + (size_t)to * D + c * 8) = v;
       }
       if (live && a.lse) a.lse[(size_t)(first + token) * a.heads + head] = l > 0.f ? m * kLn2 + logf(l) : -INFINITY;
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp >= 10 && warp < 14) {
+      // the queries: a thread copies chunk c of every kStride-th row
+      constexpr int kChunks = D / 8, kStride = 128 / kChunks;
+      const int u = tid - 320, c = u % kChunks;
+      const int step_token = kStride / p.group, step_head = kStride % p.group;
+      int row = row0 + u / kChunks;
+      int token = row / p.group, head = row % p.group;
+#pragma unroll 1
+      for (int t = 0; t < 2; ++t) {
+#pragma unroll 4
+        for (int r = u / kChunks; r < kTile; r += kStride) {
+          const bool valid = row < rows;
+          const uint16_t* src = a.q + (valid ? (size_t)(first + token) * a.ldq + (size_t)(hk * p.group + head) * D + c * 8 : 0);
+          const uint32_t dst = base + t * kBytes + chunk_at(r, c);
+          if (kB && k8) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (valid) v = *reinterpret_cast<const uint4*>(src);
+            const float2 f[4] = {unpack16<true>(v.x), unpack16<true>(v.y), unpack16<true>(v.z), unpack16<true>(v.w)};
+            float top = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) top = fmaxf(top, fmaxf(fabsf(f[k].x), fabsf(f[k].y)));
+#pragma unroll
+            for (int o = kChunks / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const int e = top > 0.f ? ilogbf(top) : 0;  // |q| 2^-e < 2
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = pack16<false>(scalbnf(f[k].x, -e), scalbnf(f[k].y, -e));
+            sts128(dst, w[0], w[1], w[2], w[3]);
+            if (c == 0) ctl.power[t * kTile + r] = scalbnf(1.f, e);
+          } else {
+            cp16(dst, src, valid);
+          }
+          row += kStride;
+          token += step_token;
+          head += step_head;
+          if (head >= p.group) {
+            head -= p.group;
+            ++token;
+          }
+        }
+        cp_commit();
+      }
+      cp_wait<1>();
+      fence_async_shared();
+      mbar_arrive(bar(kQueries));
+      cp_wait<0>();
+      fence_async_shared();
+      mbar_arrive(bar(kQueries + 1));
+    }
     if (warp < 12) {
       const int u = tid - 256;
       constexpr int kChunks = D / 8;  // 16-byte chunks of a row
       bool ok = true;
-      // the queries
-      for (int t = 0; t < 2; ++t) {
-        if (t ? n[1] > 0 : n[0] > 0) {
-#pragma unroll 4
-          for (int i = u; i < kTile * kChunks; i += 128) {
-            const int r = i / kChunks, c = i % kChunks;
-            const long long row = row0 + t * kTile + r;
-            const bool valid = row < rows;
-            const uint16_t* src = a.q + (valid ? (size_t)(first + (int)(row / p.group)) * a.ldq +
-                                                     (size_t)(hk * p.group + (int)(row % p.group)) * D + c * 8
-                                               : 0);
-            const uint32_t dst = base + t * kBytes + chunk_at(r, c);
-            if (kB && k8) {
-              uint4 v = make_uint4(0, 0, 0, 0);
-              if (valid) v = *reinterpret_cast<const uint4*>(src);
-              const float2 f[4] = {unpack16<true>(v.x), unpack16<true>(v.y), unpack16<true>(v.z), unpack16<true>(v.w)};
-              float top = 0.f;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) top = fmaxf(top, fmaxf(fabsf(f[k].x), fabsf(f[k].y)));
-#pragma unroll
-              for (int o = kChunks / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-              const int e = top > 0.f ? ilogbf(top) : 0;  // |q| 2^-e < 2
-              uint32_t w[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) w[k] = pack16<false>(scalbnf(f[k].x, -e), scalbnf(f[k].y, -e));
-              sts128(dst, w[0], w[1], w[2], w[3]);
-              if (c == 0) ctl.power[t * kTile + r] = scalbnf(1.f, e);
-            } else {
-              cp16(dst, src, valid);
-            }
-          }
-        }
-      }
-      cp_commit();
-      cp_wait<0>();
-      fence_async_shared();
-      mbar_arrive(bar(kQueries));
-      mbar_arrive(bar(kQueries + 1));
       const int shift = a.cache.page_shift, mask = (1 << shift) - 1;
       RingPos pos;
       pos.init(0, kSlots);

@@ -100,29 +100,17 @@ struct AttnArgs {
   int* err;
 };
 
-// Cached tokens of sequence b; a length outside [0, capacity of its table
-// row] is recorded and clamped.
-__device__ __forceinline__ int seq_length(const AttnArgs& a, int b) {
-  const int n = a.lens[b];
-  const long long most = (long long)a.max_pages << a.cache.page_shift;
-  if (n >= 0 && n <= most) return n;
+// A value read on the device that has to lie in [0, most]; one that does not
+// is recorded and clamped.
+__device__ __forceinline__ int checked(const AttnArgs& a, int v, int most) {
+  if (v >= 0 && v <= most) return v;
   atomicOr(a.err, kErrRange);
-  return n < 0 ? 0 : (int)most;
+  return v < 0 ? 0 : most;
 }
 
-// First row of sequence b, and its number of rows; entries outside [0, rows]
-// or in falling order are recorded and clamped.
-__device__ __forceinline__ int row_start(const AttnArgs& a, int b) {
-  const int v = a.starts[b];
-  if (v >= 0 && v <= a.rows) return v;
-  atomicOr(a.err, kErrRange);
-  return v < 0 ? 0 : a.rows;
-}
-__device__ __forceinline__ int row_count(const AttnArgs& a, int b) {
-  const int n = row_start(a, b + 1) - row_start(a, b);
-  if (n >= 0) return n;
-  atomicOr(a.err, kErrRange);
-  return 0;
+// Cached tokens of sequence b, within the capacity of its table row.
+__device__ __forceinline__ int seq_length(const AttnArgs& a, int b) {
+  return checked(a, a.lens[b], (int)min((long long)a.max_pages << a.cache.page_shift, 0x7fffffffll));
 }
 
 // Page number i of sequence b; one outside the cache is recorded and page 0
