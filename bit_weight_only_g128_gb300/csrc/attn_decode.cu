@@ -40,10 +40,16 @@ constexpr int kRows = 16;                // query rows of an item
 constexpr int kJoinRows = 8;             // rows joined at a time
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
+// Column of value d of row r in the joining rows: rows that are stored
+// together fall on different banks (two rows of 16 floats at a time with k8,
+// four of 8 without). No padding: two blocks' shared memory just fits an SM.
+template <bool k8>
+__device__ __forceinline__ int join_at(int r, int d) { return d ^ (k8 ? (r & 1) * 16 : (r & 3) * 8); }
+
 template <int D>
 struct Smem {
   uint8_t ring[kWarps][kStages][2][kTileBytes];
-  float o[kWarps][kJoinRows][D + 8];  // padded: rows land on other banks
+  float o[kWarps][kJoinRows][D];  // columns permuted by join_at
   float ml[2][kWarps][kRows];         // maxima, sums
   float top[kRows], sum[kRows];       // of the item
   int scan[kWarps];
@@ -57,6 +63,8 @@ struct DecodeArgs {
   float* parts;     // [blocks][2] of kPartFloats
   int group, tiles;  // query heads per key/value head, 16-row tiles of them
 };
+
+static_assert(sizeof(Smem<128>) <= (227 * 1024 + 1024) / 2 - 1024, "two blocks per SM");
 
 template <int D>
 constexpr int kPartFloats = kRows * (D + 2);
@@ -419,25 +427,26 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(const DecodeAr
       __syncthreads();  // the maxima are there, and the rows before these are read
       const float base = sm.top[g + 8 * half] == -INFINITY ? 0.f : sm.top[g + 8 * half];
       const float f = ex2(m[half] - base);
+      float* row = &sm.o[warp][g][0];
+      if (k8) {
+        // (even, odd) pairs of blocks hold four dimensions in a row
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        if (k8) {
-          // (even, odd) pairs of blocks: dimensions 16 (i / 2) + 4t + (i & 1), and 2 further
-          float* d = &sm.o[warp][g][16 * (i >> 1) + 4 * t + (i & 1)];
-          d[0] = o[i][2 * half] * f;
-          d[2] = o[i][2 * half + 1] * f;
-        } else {
-          *reinterpret_cast<float2*>(&sm.o[warp][g][8 * i + 2 * t]) = make_float2(o[i][2 * half] * f, o[i][2 * half + 1] * f);
-        }
+        for (int i = 0; i < D / 8; i += 2)
+          *reinterpret_cast<float4*>(row + join_at<k8>(g, 8 * i + 4 * t)) =
+              make_float4(o[i][2 * half] * f, o[i + 1][2 * half] * f, o[i][2 * half + 1] * f, o[i + 1][2 * half + 1] * f);
+      } else {
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+          *reinterpret_cast<float2*>(row + join_at<k8>(g, 8 * i + 2 * t)) = make_float2(o[i][2 * half] * f, o[i][2 * half + 1] * f);
       }
       __syncthreads();
       const int some = min(kJoinRows, rows - half * kJoinRows);
       for (int u = tid; u < some * (D / 4); u += kThreads) {
         const int r = u / (D / 4), d = u % (D / 4) * 4, row = half * kJoinRows + r;
-        float4 v = *reinterpret_cast<const float4*>(&sm.o[0][r][d]);
+        float4 v = *reinterpret_cast<const float4*>(&sm.o[0][r][join_at<k8>(r, d)]);
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) {
-          const float4 x = *reinterpret_cast<const float4*>(&sm.o[w][r][d]);
+          const float4 x = *reinterpret_cast<const float4*>(&sm.o[w][r][join_at<k8>(r, d)]);
           v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
         }
         if (whole) {
