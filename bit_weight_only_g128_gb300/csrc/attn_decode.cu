@@ -2,7 +2,7 @@
 // the cache's length and joined.
 //
 // For the query rows of one key/value head (the group of G = heads / kv_heads
-// query heads that share it, at most 16 at a time) and the cached keys and
+// query heads that share it, 8 or 16 at a time) and the cached keys and
 // values j < n:
 //   s_j = scale q.k_j,  o = sum_j 2^(x_j - m) v_j / l,  x_j = s_j log2 e,
 // with the running maximum m of x and the sum l of 2^(x_j - m). Two parts of
@@ -12,12 +12,14 @@
 // Bound: HBM bytes, every cached key and value read once (2 n D values per
 // key/value head; the queries and results are small). So the kernel is built
 // around bytes in flight: each warp streams its own tiles (4 KiB of keys, 4
-// KiB of values) through a private ring of kStages slots with 16-byte
-// asynchronous copies, without any barrier between warps; two blocks of four
-// warps per SM hold 128 KiB in flight. Both products run on mma.sync m16n8k16
-// (the group's rows are its 16 rows): at 24 B per clock and SM they need a
-// tenth of its rate, and a tcgen05 tile of 128 rows would be filled with at
-// most 16.
+// KiB of values) through a private ring with 16-byte asynchronous copies,
+// without any barrier between warps. Both products run on mma.sync m16n8k16
+// with the tokens (keys) and the dimensions (values) as its 16 rows and the
+// group's heads as its 8 columns:
+//   S^T = K Q^T (16 tokens x 8 heads),  O^T += V^T P^T (16 dims x 8 heads),
+// P^T being S^T's accumulators through one 8 x 8 transpose per 8 tokens. At 24
+// B per clock and SM they need a twentieth of its rate; a tcgen05 tile of 128
+// rows would be filled with at most 16.
 //
 // Work: all (sequence, head, step of four tiles) triples in one line, cut into
 // equal runs, one per block, from the lengths on the device. A run may begin
@@ -34,40 +36,46 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 3;
-constexpr int kTileBytes = 4096;         // of keys, and as many of values
-constexpr int kRows = 16;                // query rows of an item
-constexpr int kJoinRows = 8;             // rows joined at a time
+constexpr int kTileBytes = 4096;  // of keys, and as many of values
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// Column of value d of row r in the joining rows: rows that are stored
-// together fall on different banks (two rows of 16 floats at a time with k8,
-// four of 8 without). No padding: two blocks' shared memory just fits an SM.
-template <bool k8>
-__device__ __forceinline__ int join_at(int r, int d) { return d ^ (k8 ? (r & 1) * 16 : (r & 3) * 8); }
+// Blocks per SM and ring slots of a warp by the heads of an item: 8 heads'
+// accumulators leave registers for three blocks, whose warps cover each
+// other's item changes; the rings fill what shared memory is left.
+template <int kHeads>
+constexpr int kBlocks = kHeads == 8 ? 3 : 2;
+template <int kHeads>
+constexpr int kStages = kHeads == 8 ? 2 : 3;
+constexpr int kJoinHeads = 4;  // heads joined at a time
 
-template <int D>
+// Column of dimension d of head h in the joining rows: heads that are stored
+// together fall on different banks.
+__device__ __forceinline__ int join_at(int h, int d) { return d ^ (((h >> 1) & 3) * 8); }
+
+template <int D, int kHeads>
 struct Smem {
-  uint8_t ring[kWarps][kStages][2][kTileBytes];
-  float o[kWarps][kJoinRows][D];  // columns permuted by join_at
-  float ml[2][kWarps][kRows];         // maxima, sums
-  float top[kRows], sum[kRows];       // of the item
+  uint8_t ring[kWarps][kStages<kHeads>][2][kTileBytes];
+  float o[kWarps][kJoinHeads][D];
+  float ml[2][kWarps][kHeads];  // maxima, sums
+  float top[kHeads], sum[kHeads];  // of the item
   int scan[kWarps];
-  int start[3];  // sequence, steps before it, total
+  int start[3];  // sequence, item and step where the run begins
   int last;
 };
+static_assert(sizeof(Smem<128, 8>) + 1024 <= 228 * 1024 / kBlocks<8>, "blocks per SM");
+static_assert(sizeof(Smem<128, 16>) + 1024 <= 228 * 1024 / kBlocks<16>, "blocks per SM");
 
 struct DecodeArgs {
   AttnArgs a;
-  int* arrived;     // one counter per block: parts of the split item that it begins
-  float* parts;     // [blocks][2] of kPartFloats
-  int group, tiles;  // query heads per key/value head, 16-row tiles of them
+  int* arrived;  // one counter per block: parts of the split item that it begins
+  float* parts;  // [blocks][2] of kPartFloats
+  int group, tiles;  // query heads per key/value head, items of kHeads of them
+  float mult;        // |scale| log2 e
+  uint32_t negate;   // sign bits of a pair of queries, where scale < 0
 };
 
-static_assert(sizeof(Smem<128>) <= (227 * 1024 + 1024) / 2 - 1024, "two blocks per SM");
-
-template <int D>
-constexpr int kPartFloats = kRows * (D + 2);
+template <int D, int kHeads>
+constexpr int kPartFloats = kHeads * (D + 2);
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool valid) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
@@ -93,6 +101,12 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   else
     mma_16816(c, a[0], a[1], a[2], a[3], b0, b1);
+}
+// An 8 x 8 matrix of 16-bit values, two of a row per lane, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
 }
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -123,18 +137,19 @@ __device__ __forceinline__ int steps_of(int len) {
 
 // kB: 16-bit values are bf16, else fp16; k8: e4m3 cache (its products in
 // fp16, which holds every e4m3 code).
-template <bool kB, bool k8, int D>
-__global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(const DecodeArgs p) {
+template <bool kB, bool k8, int D, int kHeads>
+__global__ void __launch_bounds__(kThreads, kBlocks<kHeads>) attn_decode_kernel(const DecodeArgs p) {
   constexpr int kRowBytes = D * (k8 ? 1 : 2);
   constexpr int kTok = kTileBytes / kRowBytes;  // tokens per tile
   constexpr int kStep = kWarps * kTok;
   constexpr int kChunks = kRowBytes / 16;
-  constexpr int kPages = kTok / 16;  // most pages of a tile
-  constexpr bool kP = kB && !k8;     // products in bf16
-  constexpr int kSteps16 = D / 16;   // k-steps of the score product
+  constexpr int kPages = kTok / 16;   // most pages of a tile
+  constexpr bool kP = kB && !k8;      // products in bf16
+  constexpr int kNb = kHeads / 8;     // column blocks of heads
+  constexpr int kSlots = kStages<kHeads>;
 
   extern __shared__ __align__(128) uint8_t smem_raw[];
-  Smem<D>& sm = *reinterpret_cast<Smem<D>*>(smem_raw);
+  Smem<D, kHeads>& sm = *reinterpret_cast<Smem<D, kHeads>*>(smem_raw);
   const AttnArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const int items = a.cache.kv_heads * p.tiles;  // per sequence
@@ -143,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(const DecodeAr
   grid_dependency_wait();
 
   // the line's length, and where this block's run begins in it
-  auto scan = [&](int v) {  // inclusive over the block; the total in `total`
+  auto scan = [&](int v) {  // inclusive over the block, and the total
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int u = __shfl_up_sync(0xffffffffu, v, o);
@@ -160,27 +175,42 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(const DecodeAr
     __syncthreads();
     return make_int2(v + before, all);
   };
-  long long total = 0;
-  for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
-    const int v = b0 + tid < a.batch ? steps_of<kStep>(seq_length(a, b0 + tid)) : 0;
-    total += (long long)scan(v).y * items;
-  }
+  auto steps_at = [&](int b) { return b < a.batch ? steps_of<kStep>(seq_length(a, b)) : 0; };
+  const long long me = blockIdx.x;
+  long long total = 0, blocks = 0, begin = 0, end = 0;
   // at least a step per block, so that every block from an item's first to
   // its last has a part of it
-  const long long blocks = min((long long)gridDim.x, total), me = blockIdx.x;
-  if (me >= blocks) return;
-  const long long begin = me * total / blocks, end = (me + 1) * total / blocks;
-  long long carry = 0;
-  for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
-    const int v = b0 + tid < a.batch ? steps_of<kStep>(seq_length(a, b0 + tid)) : 0;
-    const int2 s = scan(v);
-    const long long hi = carry + (long long)s.x * items, lo = hi - (long long)v * items;
+  auto cut = [&]() {
+    blocks = min((long long)gridDim.x, total);
+    begin = me * total / blocks;
+    end = (me + 1) * total / blocks;
+  };
+  auto find = [&](int b, int v, long long hi) {
+    const long long lo = hi - (long long)v * items;
     if (lo <= begin && begin < hi) {
-      sm.start[0] = b0 + tid;
+      sm.start[0] = b;
       sm.start[1] = (int)((begin - lo) / v);
       sm.start[2] = (int)((begin - lo) % v);
     }
-    carry += (long long)s.y * items;
+  };
+  if (a.batch <= kThreads) {
+    const int v = steps_at(tid);
+    const int2 s = scan(v);
+    total = (long long)s.y * items;
+    cut();
+    if (me >= blocks) return;
+    find(tid, v, (long long)s.x * items);
+  } else {
+    for (int b0 = 0; b0 < a.batch; b0 += kThreads) total += (long long)scan(steps_at(b0 + tid)).y * items;
+    cut();
+    if (me >= blocks) return;
+    long long carry = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
+      const int v = steps_at(b0 + tid);
+      const int2 s = scan(v);
+      find(b0 + tid, v, carry + (long long)s.x * items);
+      carry += (long long)s.y * items;
+    }
   }
   __syncthreads();
 
@@ -192,8 +222,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(const DecodeAr
   load.steps = steps_of<kStep>(load.len);
   Place cur = load;  // what the products take next
   long long load_left = end - begin, left = end - begin;
-  auto advance = [&](Place& q) {  // by one step
-    if (++q.step < q.steps) return;
+  auto next_item = [&](Place& q) {
     q.step = 0;
     if (++q.item < items) return;
     q.item = 0;
@@ -205,208 +234,266 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(const DecodeAr
 
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(&sm.ring[warp][0][0][0]);
   const int shift = a.cache.page_shift, mask = (1 << shift) - 1;
+  // A lane copies chunk c of every kLaneRows-th row. The swizzled places of
+  // its rows repeat after 8 rows (kPeriod copies), 1 KiB or less apart.
+  constexpr int kLaneRows = 32 / kChunks;
+  constexpr int kPeriod = kLaneRows >= 8 ? 1 : 8 / kLaneRows;
+  const int r0 = lane / kChunks, c0 = lane % kChunks;
+  uint32_t place[kPeriod];
+#pragma unroll
+  for (int i = 0; i < kPeriod; ++i) place[i] = tile_at<kRowBytes>(r0 + i * kLaneRows, c0);
+  const uint8_t* const k_lane = static_cast<const uint8_t*>(a.cache.k) + r0 * kRowBytes + c0 * 16;
+  const uint8_t* const v_lane = static_cast<const uint8_t*>(a.cache.v) + r0 * kRowBytes + c0 * 16;
   auto issue = [&](int slot) {  // the next step's tile of this warp into a ring slot
     if (load_left > 0) {
       --load_left;
       const int tok0 = (load.step * kWarps + warp) * kTok;
       if (tok0 < load.len) {
         const int head = load.item / p.tiles;
-        size_t page[kPages];
-#pragma unroll
-        for (int i = 0; i < kPages; ++i) {
-          const int tok = tok0 + 16 * i;
-          // a place of the page's rows of this head, in bytes
-          page[i] = tok < load.len
-                        ? ((((size_t)page_of(a, load.b, tok >> shift) * a.cache.kv_heads + head) << shift) + (tok & mask)) *
-                              kRowBytes
-                        : 0;
-        }
         const uint32_t dst = ring + slot * (2 * kTileBytes);
-        const uint8_t* k = static_cast<const uint8_t*>(a.cache.k);
-        const uint8_t* v = static_cast<const uint8_t*>(a.cache.v);
+        const bool whole = tok0 + kTok <= load.len;
 #pragma unroll
-        for (int i = 0; i < kTileBytes / 512; ++i) {
-          const int u = i * 32 + lane, r = u / kChunks, c = u % kChunks;
-          const bool valid = tok0 + r < load.len;
-          const size_t at = valid ? page[(i * 32 / kChunks) / 16] + (size_t)(r & 15) * kRowBytes + c * 16 : 0;
-          cp16(dst + tile_at<kRowBytes>(r, c), k + at, valid);
-          cp16(dst + kTileBytes + tile_at<kRowBytes>(r, c), v + at, valid);
+        for (int i = 0; i < kPages; ++i) {  // 16 rows in one page
+          const int tok = tok0 + 16 * i;
+          if (tok < load.len || whole) {
+            const size_t at =
+                ((((size_t)page_of(a, load.b, tok >> shift) * a.cache.kv_heads + head) << shift) + (tok & mask)) * kRowBytes;
+            const uint8_t* k = k_lane + at;
+            const uint8_t* v = v_lane + at;
+#pragma unroll
+            for (int x = 0; x < 16 / kLaneRows; ++x) {
+              const int n = i * (16 / kLaneRows) + x;
+              const uint32_t to = dst + place[n % kPeriod] + n / kPeriod * kPeriod * kLaneRows * kRowBytes;
+              if (whole) {
+                cp16(to, k + x * kLaneRows * kRowBytes, true);
+                cp16(to + kTileBytes, v + x * kLaneRows * kRowBytes, true);
+              } else {
+                const bool valid = tok + r0 + x * kLaneRows < load.len;
+                cp16(to, valid ? k + x * kLaneRows * kRowBytes : k_lane, valid);
+                cp16(to + kTileBytes, valid ? v + x * kLaneRows * kRowBytes : v_lane, valid);
+              }
+            }
+          } else {  // rows beyond the sequence, as zeros
+#pragma unroll
+            for (int x = 0; x < 16 / kLaneRows; ++x) {
+              const int n = i * (16 / kLaneRows) + x;
+              const uint32_t to = dst + place[n % kPeriod] + n / kPeriod * kPeriod * kLaneRows * kRowBytes;
+              cp16(to, k_lane, false);
+              cp16(to + kTileBytes, v_lane, false);
+            }
+          }
         }
       }
-      advance(load);
+      if (++load.step == load.steps) next_item(load);
     }
     cp_commit();
   };
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) issue(i);
+  for (int i = 0; i < kSlots - 1; ++i) issue(i);
   int slot = 0;
 
   while (left > 0) {
     // one item's steps of this run
-    const int head = cur.item / p.tiles, row0 = (cur.item % p.tiles) * kRows;
-    const int rows = min(kRows, p.group - row0);
+    const int head = cur.item / p.tiles, head0 = (cur.item % p.tiles) * kHeads;
+    const int heads = min(kHeads, p.group - head0);
     const bool starts = cur.step == 0;
     const int n = (int)min((long long)(cur.steps - cur.step), left);
     const bool ends = cur.step + n == cur.steps;
 
-    // the queries as A fragments: rows g and g + 8; for the e4m3 cache in
-    // fp16 with the dimensions of a k-step in the order its codes come in
-    // (4t, 4t + 1 | 4t + 2, 4t + 3), each row divided by a power of two
-    uint32_t qf[kSteps16][4];
-    float mult[2];
+    // the queries as B fragments, head g of each column block; for the e4m3
+    // cache in fp16 with the dimensions of a k-step in the order its codes
+    // come in (4t, 4t + 1 | 4t + 2, 4t + 3), each head divided by a power of
+    // two. mult: of this lane's accumulator columns, heads 2t and 2t + 1.
+    uint32_t qf[kNb][D / 16][2];
+    float mult[kNb][2];
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int r = g + 8 * half;
-      const uint16_t* q = a.q + (size_t)cur.b * a.ldq + (size_t)(head * p.group + row0 + (r < rows ? r : 0)) * D;
+    for (int nb = 0; nb < kNb; ++nb) {
+      const int h = 8 * nb + g;
+      const uint16_t* q = a.q + (size_t)cur.b * a.ldq + (size_t)(head * p.group + head0 + (h < heads ? h : 0)) * D;
       float top = 0.f;
 #pragma unroll
-      for (int i = 0; i < kSteps16; ++i) {
+      for (int i = 0; i < D / 16; ++i) {
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           const int d = k8 ? 16 * i + 4 * t + 2 * w : 16 * i + 2 * t + 8 * w;
-          const uint32_t v = r < rows ? *reinterpret_cast<const uint32_t*>(q + d) : 0;
-          qf[i][half + 2 * w] = v;
+          const uint32_t v = h < heads ? *reinterpret_cast<const uint32_t*>(q + d) ^ p.negate : 0;
+          qf[nb][i][w] = v;
           if (k8 && kB) {
             const float2 f = unpack16<true>(v);
             top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
           }
         }
       }
-      mult[half] = a.scale * kLog2e * (k8 ? a.cache.k_scale[head] : 1.f);
+      const float m0 = p.mult * (k8 ? a.cache.k_scale[head] : 1.f);
       if (k8 && kB) {
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const int e = top > 0.f ? ilogbf(top) : 0;  // |q| 2^-e < 2
 #pragma unroll
-        for (int i = 0; i < kSteps16; ++i)
+        for (int i = 0; i < D / 16; ++i)
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
-            const float2 f = unpack16<true>(qf[i][half + 2 * w]);
-            qf[i][half + 2 * w] = pack16<false>(scalbnf(f.x, -e), scalbnf(f.y, -e));
+            const float2 f = unpack16<true>(qf[nb][i][w]);
+            qf[nb][i][w] = pack16<false>(scalbnf(f.x, -e), scalbnf(f.y, -e));
           }
-        mult[half] = scalbnf(mult[half], e);
+        const float own = scalbnf(m0, e);
+        mult[nb][0] = __shfl_sync(0xffffffffu, own, 8 * t);
+        mult[nb][1] = __shfl_sync(0xffffffffu, own, 8 * t + 4);
+      } else {
+        mult[nb][0] = mult[nb][1] = m0;
       }
     }
 
-    float o[D / 8][4];
+    float o[kNb][D / 16][4];  // dimensions g, g + 8 (k8: 2g, 2g + 1) x heads 2t, 2t + 1
+    float m[kNb][2], l[kNb][2];
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i)
+    for (int nb = 0; nb < kNb; ++nb) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[nb][i][j] = 0.f;
+      m[nb][0] = m[nb][1] = -INFINITY;
+      l[nb][0] = l[nb][1] = 0.f;
+    }
 
     for (int k = 0; k < n; ++k) {
-      cp_wait<kStages - 2>();
+      cp_wait<kSlots - 2>();
       __syncwarp();
-      issue(slot == 0 ? kStages - 1 : slot - 1);  // into the slot read one step ago
+      issue(slot == 0 ? kSlots - 1 : slot - 1);  // into the slot read one step ago
       const int tok0 = (cur.step * kWarps + warp) * kTok;
       const uint32_t kt = ring + slot * (2 * kTileBytes), vt = kt + kTileBytes;
       if (tok0 < cur.len) {
-        // scores: kTok tokens in blocks of 8
-        float s[kTok / 8][4];
+        // scores: 16 tokens (g, g + 8) x 8 heads (2t, 2t + 1) at a time
+        float s[kTok / 16][kNb][4];
 #pragma unroll
-        for (int nb = 0; nb < kTok / 8; ++nb) {
-          s[nb][0] = s[nb][1] = s[nb][2] = s[nb][3] = 0.f;
-          const int r = nb * 8 + (lane & 7);
+        for (int i = 0; i < kTok / 16; ++i)
 #pragma unroll
-          for (int c = 0; c < kChunks; c += 4) {
-            uint32_t b[4];
-            ldsm4(b, kt + tile_at<kRowBytes>(r, c + (lane >> 3)));
+          for (int nb = 0; nb < kNb; ++nb)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[i][nb][j] = 0.f;
+#pragma unroll
+        for (int c = 0; c < kChunks; c += 2)
+#pragma unroll
+          for (int i = 0; i < kTok / 16; ++i) {
+            // tokens 0-7 and 8-15 of chunk c, then of chunk c + 1
+            uint32_t r[4];
+            ldsm4(r, kt + tile_at<kRowBytes>(16 * i + (lane & 15), c + (lane >> 4)));
             if (k8) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                mma<kP>(s[nb], qf[c + i], e4m3x2_to_half2(b[i] & 0xffffu), e4m3x2_to_half2(b[i] >> 16));
-            } else {
-              mma<kP>(s[nb], qf[c / 2], b[0], b[1]);
-              mma<kP>(s[nb], qf[c / 2 + 1], b[2], b[3]);
-            }
-          }
-        }
-        float top[2] = {-INFINITY, -INFINITY};
+              for (int x = 0; x < 2; ++x) {
+                const uint32_t f[4] = {e4m3x2_to_half2(r[2 * x] & 0xffffu), e4m3x2_to_half2(r[2 * x + 1] & 0xffffu),
+                                       e4m3x2_to_half2(r[2 * x] >> 16), e4m3x2_to_half2(r[2 * x + 1] >> 16)};
 #pragma unroll
-        for (int nb = 0; nb < kTok / 8; ++nb)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int tok = tok0 + nb * 8 + 2 * t + (j & 1);
-            s[nb][j] = tok < cur.len ? s[nb][j] * mult[j >> 1] : -INFINITY;
-            top[j >> 1] = fmaxf(top[j >> 1], s[nb][j]);
-          }
-        bool grew = false;
-        float base[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
-          top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
-          grew |= top[h] > m[h];
-          top[h] = fmaxf(m[h], top[h]);
-          base[h] = top[h] == -INFINITY ? 0.f : top[h];
-        }
-        if (__any_sync(0xffffffffu, grew)) {
-          float f[2];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            f[h] = ex2(m[h] - base[h]);
-            l[h] *= f[h];
-            m[h] = top[h];
-          }
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) o[i][j] *= f[j >> 1];
-        }
-#pragma unroll
-        for (int nb = 0; nb < kTok / 8; ++nb)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            s[nb][j] = ex2(s[nb][j] - base[j >> 1]);
-            l[j >> 1] += s[nb][j];
-          }
-        // values: 16 tokens per k-step, the probabilities rounded to 16 bits
-        // for the product (relative 2^-11 or 2^-8 of each term)
-#pragma unroll
-        for (int ks = 0; ks < kTok / 16; ++ks) {
-          uint32_t pa[4];
-          pa[0] = pack16<kP>(s[2 * ks][0], s[2 * ks][1]);
-          pa[1] = pack16<kP>(s[2 * ks][2], s[2 * ks][3]);
-          pa[2] = pack16<kP>(s[2 * ks + 1][0], s[2 * ks + 1][1]);
-          pa[3] = pack16<kP>(s[2 * ks + 1][2], s[2 * ks + 1][3]);
-          const int r = ks * 16 + (lane & 15);
-#pragma unroll
-          for (int c = 0; c < kChunks; c += 2) {
-            uint32_t b[4];
-            ldsm4t(b, vt + tile_at<kRowBytes>(r, c + (lane >> 4)));
-            if (k8) {
-              // a register holds dimensions (2g, 2g + 1) of two tokens: the
-              // even ones of both first, then the odd ones
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const uint32_t x = __byte_perm(b[2 * i], 0, 0x3120), y = __byte_perm(b[2 * i + 1], 0, 0x3120);
-                mma<kP>(o[2 * (c + i)], pa, e4m3x2_to_half2(x & 0xffffu), e4m3x2_to_half2(y & 0xffffu));
-                mma<kP>(o[2 * (c + i) + 1], pa, e4m3x2_to_half2(x >> 16), e4m3x2_to_half2(y >> 16));
+                for (int nb = 0; nb < kNb; ++nb) mma<kP>(s[i][nb], f, qf[nb][c + x][0], qf[nb][c + x][1]);
               }
             } else {
-              mma<kP>(o[c], pa, b[0], b[1]);
-              mma<kP>(o[c + 1], pa, b[2], b[3]);
+#pragma unroll
+              for (int nb = 0; nb < kNb; ++nb) mma<kP>(s[i][nb], r, qf[nb][c / 2][0], qf[nb][c / 2][1]);
             }
           }
+        if (tok0 + kTok > cur.len) {
+#pragma unroll
+          for (int i = 0; i < kTok / 16; ++i)
+#pragma unroll
+            for (int nb = 0; nb < kNb; ++nb)
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (tok0 + 16 * i + g + 8 * (j >> 1) >= cur.len) s[i][nb][j] = -INFINITY;
         }
+        bool grew = false;
+        float shift2[kNb][2];
+#pragma unroll
+        for (int nb = 0; nb < kNb; ++nb)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float top = fmaxf(s[0][nb][h], s[0][nb][2 + h]);
+#pragma unroll
+            for (int i = 1; i < kTok / 16; ++i) top = fmaxf(top, fmaxf(s[i][nb][h], s[i][nb][2 + h]));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16)) * mult[nb][h];
+            grew |= top > m[nb][h];
+            shift2[nb][h] = fmaxf(m[nb][h], top);
+          }
+        if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+          for (int nb = 0; nb < kNb; ++nb) {
+            float f[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              f[h] = ex2(m[nb][h] - shift2[nb][h]);
+              l[nb][h] *= f[h];
+              m[nb][h] = shift2[nb][h];
+            }
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) o[nb][i][j] *= f[j & 1];
+          }
+        }
+        // probabilities, rounded to 16 bits for the product (relative 2^-11
+        // or 2^-8 of each term), as B fragments: 16 tokens x 8 heads. (The
+        // tile has a token, so the maxima are finite.)
+        uint32_t pf[kTok / 16][kNb][2];
+#pragma unroll
+        for (int i = 0; i < kTok / 16; ++i)
+#pragma unroll
+          for (int nb = 0; nb < kNb; ++nb) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              s[i][nb][j] = ex2(fmaf(s[i][nb][j], mult[nb][j & 1], -m[nb][j & 1]));
+              l[nb][j & 1] += s[i][nb][j];
+            }
+            pf[i][nb][0] = transpose8(pack16<kP>(s[i][nb][0], s[i][nb][1]));
+            pf[i][nb][1] = transpose8(pack16<kP>(s[i][nb][2], s[i][nb][3]));
+          }
+#pragma unroll
+        for (int i = 0; i < kTok / 16; ++i)
+#pragma unroll
+          for (int c = 0; c < kChunks; c += 2) {
+            if (k8) {
+              // transposed 16-bit units: tokens 0-7 and 8-15 of chunk c, then
+              // of chunk c + 1. A register holds dimensions (2g, 2g + 1) of
+              // two tokens: the even ones of both are row g, the odd ones row
+              // g + 8
+              uint32_t r[4];
+              ldsm4t(r, vt + tile_at<kRowBytes>(16 * i + (lane & 15), c + (lane >> 4)));
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const uint32_t u = __byte_perm(r[2 * x], 0, 0x3120), w = __byte_perm(r[2 * x + 1], 0, 0x3120);
+                const uint32_t f[4] = {e4m3x2_to_half2(u & 0xffffu), e4m3x2_to_half2(u >> 16), e4m3x2_to_half2(w & 0xffffu),
+                                       e4m3x2_to_half2(w >> 16)};
+#pragma unroll
+                for (int nb = 0; nb < kNb; ++nb) mma<kP>(o[nb][c + x], f, pf[i][nb][0], pf[i][nb][1]);
+              }
+            } else {
+              // transposed: dimensions 0-7 and 8-15 of the pair of chunks for
+              // tokens 0-7, then for tokens 8-15
+              uint32_t r[4];
+              ldsm4t(r, vt + tile_at<kRowBytes>(16 * i + (lane & 7) + 8 * (lane >> 4), c + ((lane >> 3) & 1)));
+#pragma unroll
+              for (int nb = 0; nb < kNb; ++nb) mma<kP>(o[nb][c / 2], r, pf[i][nb][0], pf[i][nb][1]);
+            }
+          }
       }
-      slot = slot == kStages - 1 ? 0 : slot + 1;
+      slot = slot == kSlots - 1 ? 0 : slot + 1;
       ++cur.step;
     }
 
     // join the warps
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-      if (t == 0) {
-        sm.ml[0][warp][g + 8 * h] = m[h];
-        sm.ml[1][warp][g + 8 * h] = l[h];
+    for (int nb = 0; nb < kNb; ++nb)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int w = 4; w < 32; w <<= 1) l[nb][h] += __shfl_xor_sync(0xffffffffu, l[nb][h], w);
+        if (g == 0) {
+          sm.ml[0][warp][8 * nb + 2 * t + h] = m[nb][h];
+          sm.ml[1][warp][8 * nb + 2 * t + h] = l[nb][h];
+        }
       }
-    }
     __syncthreads();
-    if (tid < kRows) {
+    if (tid < kHeads) {
       float top = sm.ml[0][0][tid];
 #pragma unroll
       for (int w = 1; w < kWarps; ++w) top = fmaxf(top, sm.ml[0][w][tid]);
@@ -417,53 +504,66 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(const DecodeAr
       sm.top[tid] = top;
       sm.sum[tid] = sum;
     }
+    __syncthreads();
     const bool whole = starts && ends;
-    float* part = p.parts + (size_t)(2 * me + (starts ? 1 : 0)) * kPartFloats<D>;
+    float* part = p.parts + (size_t)(2 * me + (starts ? 1 : 0)) * kPartFloats<D, kHeads>;
     const float v_scale = k8 ? a.cache.v_scale[head] : 1.f;
-    const size_t out0 = (size_t)cur.b * a.heads + head * p.group + row0;
+    const size_t out0 = (size_t)cur.b * a.heads + head * p.group + head0;
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      if (half * kJoinRows >= rows) break;
-      __syncthreads();  // the maxima are there, and the rows before these are read
-      const float base = sm.top[g + 8 * half] == -INFINITY ? 0.f : sm.top[g + 8 * half];
-      const float f = ex2(m[half] - base);
-      float* row = &sm.o[warp][g][0];
-      if (k8) {
-        // (even, odd) pairs of blocks hold four dimensions in a row
+    for (int nb = 0; nb < kNb; ++nb)
 #pragma unroll
-        for (int i = 0; i < D / 8; i += 2)
-          *reinterpret_cast<float4*>(row + join_at<k8>(g, 8 * i + 4 * t)) =
-              make_float4(o[i][2 * half] * f, o[i + 1][2 * half] * f, o[i][2 * half + 1] * f, o[i + 1][2 * half + 1] * f);
-      } else {
+      for (int h = 0; h < 2; ++h) {
+        const float top = sm.top[8 * nb + 2 * t + h];
+        const float f = ex2(m[nb][h] - (top == -INFINITY ? 0.f : top));
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i)
-          *reinterpret_cast<float2*>(row + join_at<k8>(g, 8 * i + 2 * t)) = make_float2(o[i][2 * half] * f, o[i][2 * half + 1] * f);
+        for (int i = 0; i < D / 16; ++i) o[nb][i][h] *= f, o[nb][i][2 + h] *= f;
+      }
+#pragma unroll
+    for (int round = 0; round < kHeads / kJoinHeads; ++round) {
+      if (round * kJoinHeads >= heads) break;
+      if (round) __syncthreads();  // the heads before these are read
+      if ((t >> 1) == (round & 1)) {
+        const int nb = round >> 1;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = 2 * (t & 1) + h;  // of the round's heads
+          float* row = &sm.o[warp][r][0];
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            if (k8) {
+              *reinterpret_cast<float2*>(row + join_at(r, 16 * i + 2 * g)) = make_float2(o[nb][i][h], o[nb][i][2 + h]);
+            } else {
+              row[join_at(r, 16 * i + g)] = o[nb][i][h];
+              row[join_at(r, 16 * i + 8 + g)] = o[nb][i][2 + h];
+            }
+          }
+        }
       }
       __syncthreads();
-      const int some = min(kJoinRows, rows - half * kJoinRows);
+      const int some = min(kJoinHeads, heads - round * kJoinHeads);
       for (int u = tid; u < some * (D / 4); u += kThreads) {
-        const int r = u / (D / 4), d = u % (D / 4) * 4, row = half * kJoinRows + r;
-        float4 v = *reinterpret_cast<const float4*>(&sm.o[0][r][join_at<k8>(r, d)]);
+        const int r = u / (D / 4), d = u % (D / 4) * 4, h = round * kJoinHeads + r;
+        float4 v = *reinterpret_cast<const float4*>(&sm.o[0][r][join_at(r, d)]);
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) {
-          const float4 x = *reinterpret_cast<const float4*>(&sm.o[w][r][join_at<k8>(r, d)]);
+          const float4 x = *reinterpret_cast<const float4*>(&sm.o[w][r][join_at(r, d)]);
           v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
         }
         if (whole) {
-          const float l1 = sm.sum[row], inv = l1 > 0.f ? v_scale / l1 : 0.f;
-          *reinterpret_cast<uint2*>(a.out + (out0 + row) * D + d) =
+          const float l1 = sm.sum[h], inv = l1 > 0.f ? v_scale / l1 : 0.f;
+          *reinterpret_cast<uint2*>(a.out + (out0 + h) * D + d) =
               make_uint2(pack16<kB>(v.x * inv, v.y * inv), pack16<kB>(v.z * inv, v.w * inv));
         } else {
-          *reinterpret_cast<float4*>(part + row * D + d) = v;
+          *reinterpret_cast<float4*>(part + h * D + d) = v;
         }
       }
     }
-    if (tid < rows) {
+    if (tid < heads) {
       if (whole) {
         if (a.lse) a.lse[out0 + tid] = sm.sum[tid] > 0.f ? sm.top[tid] * kLn2 + logf(sm.sum[tid]) : -INFINITY;
       } else {
-        part[kRows * D + tid] = sm.top[tid];
-        part[kRows * D + kRows + tid] = sm.sum[tid];
+        part[kHeads * D + tid] = sm.top[tid];
+        part[kHeads * D + kHeads + tid] = sm.sum[tid];
       }
     }
 
@@ -478,68 +578,70 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(const DecodeAr
       if (sm.last) {
         __threadfence();
         const int count = (int)(final - first) + 1;
-        auto part_of = [&](int i) { return p.parts + (size_t)(2 * (first + i) + (i == 0 ? 1 : 0)) * kPartFloats<D>; };
-        // maxima and sums: 8 threads per row over the parts
+        auto part_of = [&](int i) {
+          return p.parts + (size_t)(2 * (first + i) + (i == 0 ? 1 : 0)) * kPartFloats<D, kHeads>;
+        };
         {
-          const int r = tid >> 3, j = tid & 7;
+          // maxima and sums: kEach threads per head over the parts
+          constexpr int kEach = kThreads / kHeads;
+          const int h = tid / kEach, j = tid % kEach;
           float top = -INFINITY, sum = 0.f;
-          if (r < rows)
-            for (int i = j; i < count; i += 8) top = fmaxf(top, __ldcg(part_of(i) + kRows * D + r));
+          if (h < heads)
+            for (int i = j; i < count; i += kEach) top = fmaxf(top, __ldcg(part_of(i) + kHeads * D + h));
 #pragma unroll
-          for (int w = 1; w < 8; w <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+          for (int w = 1; w < kEach; w <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
           const float base = top == -INFINITY ? 0.f : top;
-          if (r < rows)
-            for (int i = j; i < count; i += 8)
-              sum += __ldcg(part_of(i) + kRows * D + kRows + r) * ex2(__ldcg(part_of(i) + kRows * D + r) - base);
+          if (h < heads)
+            for (int i = j; i < count; i += kEach)
+              sum += __ldcg(part_of(i) + kHeads * D + kHeads + h) * ex2(__ldcg(part_of(i) + kHeads * D + h) - base);
 #pragma unroll
-          for (int w = 1; w < 8; w <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+          for (int w = 1; w < kEach; w <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
           if (j == 0) {
-            sm.top[r] = top;
-            sm.sum[r] = sum;
+            sm.top[h] = top;
+            sm.sum[h] = sum;
           }
         }
         __syncthreads();
-        for (int u = tid; u < rows * (D / 4); u += kThreads) {
-          const int r = u / (D / 4), d = u % (D / 4) * 4;
-          const float base = sm.top[r] == -INFINITY ? 0.f : sm.top[r];
+        for (int u = tid; u < heads * (D / 4); u += kThreads) {
+          const int h = u / (D / 4), d = u % (D / 4) * 4;
+          const float base = sm.top[h] == -INFINITY ? 0.f : sm.top[h];
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
           for (int i = 0; i < count; ++i) {
             const float* q = part_of(i);
-            const float f = ex2(__ldcg(q + kRows * D + r) - base);
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(q + r * D + d));
+            const float f = ex2(__ldcg(q + kHeads * D + h) - base);
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(q + h * D + d));
             v.x = fmaf(x.x, f, v.x), v.y = fmaf(x.y, f, v.y), v.z = fmaf(x.z, f, v.z), v.w = fmaf(x.w, f, v.w);
           }
-          const float l1 = sm.sum[r], inv = l1 > 0.f ? v_scale / l1 : 0.f;
-          *reinterpret_cast<uint2*>(a.out + (out0 + r) * D + d) =
+          const float l1 = sm.sum[h], inv = l1 > 0.f ? v_scale / l1 : 0.f;
+          *reinterpret_cast<uint2*>(a.out + (out0 + h) * D + d) =
               make_uint2(pack16<kB>(v.x * inv, v.y * inv), pack16<kB>(v.z * inv, v.w * inv));
         }
-        if (a.lse && tid < rows)
+        if (a.lse && tid < heads)
           a.lse[out0 + tid] = sm.sum[tid] > 0.f ? sm.top[tid] * kLn2 + logf(sm.sum[tid]) : -INFINITY;
         if (tid == 0) p.arrived[first] = 0;  // left zero for the next call
       }
     }
     left -= n;
-    // to the next item
-    cur.step = 0;
-    if (++cur.item == items) {
-      cur.item = 0;
-      if (++cur.b < a.batch) {
-        cur.len = seq_length(a, cur.b);
-        cur.steps = steps_of<kStep>(cur.len);
-      }
-    }
+    next_item(cur);
     __syncthreads();  // the shared maxima and rows are free again
   }
   cp_wait<0>();
 }
 
-template <bool kB, bool k8, int D>
-cudaError_t launch(const DecodeArgs& p, int blocks, cudaStream_t stream) {
-  auto kern = attn_decode_kernel<kB, k8, D>;
-  cudaError_t e = set_max_smem_once(reinterpret_cast<const void*>(kern), (int)sizeof(Smem<D>));
+template <bool kB, bool k8, int D, int kHeads>
+cudaError_t launch(const DecodeArgs& p, int sms, cudaStream_t stream) {
+  auto kern = attn_decode_kernel<kB, k8, D, kHeads>;
+  cudaError_t e = set_max_smem_once(reinterpret_cast<const void*>(kern), (int)sizeof(Smem<D, kHeads>));
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3((unsigned)blocks), dim3(kThreads), sizeof(Smem<D>), stream, p);
+  return launch_pdl(kern, dim3((unsigned)(kBlocks<kHeads> * sms)), dim3(kThreads), sizeof(Smem<D, kHeads>), stream, p);
+}
+
+template <bool kB, bool k8, int D>
+cudaError_t launch_heads(DecodeArgs& p, int sms, cudaStream_t stream) {
+  const int heads = p.group <= 8 ? 8 : 16;
+  p.tiles = (p.group + heads - 1) / heads;
+  return heads == 8 ? launch<kB, k8, D, 8>(p, sms, stream) : launch<kB, k8, D, 16>(p, sms, stream);
 }
 
 constexpr size_t kFlagBytes = 32768;
@@ -547,7 +649,8 @@ constexpr size_t kFlagBytes = 32768;
 }  // namespace
 
 size_t attn_decode_workspace_bytes(int head_dim, int sms) {
-  return kFlagBytes + (size_t)(2 * sms) * 2 * kRows * (head_dim + 2) * sizeof(float);
+  const size_t few = (size_t)kBlocks<8> * 8, many = (size_t)kBlocks<16> * 16;  // heads of an SM's parts
+  return kFlagBytes + (size_t)sms * 2 * (few > many ? few : many) * (head_dim + 2) * sizeof(float);
 }
 
 cudaError_t launch_attn_decode(const AttnArgs& args, int head_dim, bool bf16, bool e4m3, void* workspace, int sms,
@@ -560,17 +663,20 @@ cudaError_t launch_attn_decode(const AttnArgs& args, int head_dim, bool bf16, bo
   p.arrived = static_cast<int*>(workspace);
   p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kFlagBytes);
   p.group = args.heads / args.cache.kv_heads;
-  p.tiles = (p.group + kRows - 1) / kRows;
-  const int blocks = 2 * sms;
+  // the scores' maximum is taken before the scale, so it has to be positive:
+  // a negative scale negates the queries, and a scale of zero becomes one too
+  // small to tell from it
+  p.mult = fmaxf(fabsf(args.scale) * kLog2e, 1e-37f);
+  p.negate = args.scale < 0.f ? 0x80008000u : 0u;
   switch ((bf16 ? 4 : 0) | (e4m3 ? 2 : 0) | (head_dim == 128 ? 1 : 0)) {
-    case 0: return launch<false, false, 64>(p, blocks, stream);
-    case 1: return launch<false, false, 128>(p, blocks, stream);
-    case 2: return launch<false, true, 64>(p, blocks, stream);
-    case 3: return launch<false, true, 128>(p, blocks, stream);
-    case 4: return launch<true, false, 64>(p, blocks, stream);
-    case 5: return launch<true, false, 128>(p, blocks, stream);
-    case 6: return launch<true, true, 64>(p, blocks, stream);
-    default: return launch<true, true, 128>(p, blocks, stream);
+    case 0: return launch_heads<false, false, 64>(p, sms, stream);
+    case 1: return launch_heads<false, false, 128>(p, sms, stream);
+    case 2: return launch_heads<false, true, 64>(p, sms, stream);
+    case 3: return launch_heads<false, true, 128>(p, sms, stream);
+    case 4: return launch_heads<true, false, 64>(p, sms, stream);
+    case 5: return launch_heads<true, false, 128>(p, sms, stream);
+    case 6: return launch_heads<true, true, 64>(p, sms, stream);
+    default: return launch_heads<true, true, 128>(p, sms, stream);
   }
 }
 
