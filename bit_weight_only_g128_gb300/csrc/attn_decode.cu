@@ -381,8 +381,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks<kHeads>) attn_decode_kernel(
             if (k8) {
 #pragma unroll
               for (int x = 0; x < 2; ++x) {
-                const uint32_t f[4] = {e4m3x2_to_half2(r[2 * x] & 0xffffu), e4m3x2_to_half2(r[2 * x + 1] & 0xffffu),
-                                       e4m3x2_to_half2(r[2 * x] >> 16), e4m3x2_to_half2(r[2 * x + 1] >> 16)};
+                uint32_t f[4];
+                e4m3x4_to_half2x2(r[2 * x], f[0], f[2]);
+                e4m3x4_to_half2x2(r[2 * x + 1], f[1], f[3]);
 #pragma unroll
                 for (int nb = 0; nb < kNb; ++nb) mma<kP>(s[i][nb], f, qf[nb][c + x][0], qf[nb][c + x][1]);
               }
@@ -460,9 +461,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks<kHeads>) attn_decode_kernel(
               ldsm4t(r, vt + tile_at<kRowBytes>(16 * i + (lane & 15), c + (lane >> 4)));
 #pragma unroll
               for (int x = 0; x < 2; ++x) {
-                const uint32_t u = __byte_perm(r[2 * x], 0, 0x3120), w = __byte_perm(r[2 * x + 1], 0, 0x3120);
-                const uint32_t f[4] = {e4m3x2_to_half2(u & 0xffffu), e4m3x2_to_half2(u >> 16), e4m3x2_to_half2(w & 0xffffu),
-                                       e4m3x2_to_half2(w >> 16)};
+                uint32_t f[4];
+                e4m3x4_to_half2x2(__byte_perm(r[2 * x], 0, 0x3120), f[0], f[1]);
+                e4m3x4_to_half2x2(__byte_perm(r[2 * x + 1], 0, 0x3120), f[2], f[3]);
 #pragma unroll
                 for (int nb = 0; nb < kNb; ++nb) mma<kP>(o[nb][c + x], f, pf[i][nb][0], pf[i][nb][1]);
               }

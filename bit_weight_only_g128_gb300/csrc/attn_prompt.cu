@@ -178,8 +178,10 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, ui
 
 // Eight e4m3 codes to fp16 (exact).
 __device__ __forceinline__ uint4 widen(uint32_t lo, uint32_t hi) {
-  return make_uint4(e4m3x2_to_half2(lo & 0xffffu), e4m3x2_to_half2(lo >> 16), e4m3x2_to_half2(hi & 0xffffu),
-                    e4m3x2_to_half2(hi >> 16));
+  uint4 v;
+  e4m3x4_to_half2x2(lo, v.x, v.y);
+  e4m3x4_to_half2x2(hi, v.z, v.w);
+  return v;
 }
 
 // kB: 16-bit values are bf16, else fp16; k8: e4m3 cache. Its products are in
