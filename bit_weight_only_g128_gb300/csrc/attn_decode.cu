@@ -59,7 +59,7 @@ struct Smem {
   float ml[2][kWarps][kHeads];  // maxima, sums
   float top[kHeads], sum[kHeads];  // of the item
   int scan[kWarps];
-  int start[3];  // sequence, item and step where the run begins
+  int start[4];  // sequence, item and step where the run begins, the sequence's length
   int last;
 };
 static_assert(sizeof(Smem<128, 8>) + 1024 <= 228 * 1024 / kBlocks<8>, "blocks per SM");
@@ -175,7 +175,12 @@ __global__ void __launch_bounds__(kThreads, kBlocks<kHeads>) attn_decode_kernel(
     __syncthreads();
     return make_int2(v + before, all);
   };
-  auto steps_at = [&](int b) { return b < a.batch ? steps_of<kStep>(seq_length(a, b)) : 0; };
+  int own_len = 0;  // of the sequence of steps_at
+  auto steps_at = [&](int b) {
+    if (b >= a.batch) return 0;
+    own_len = seq_length(a, b);
+    return steps_of<kStep>(own_len);
+  };
   const long long me = blockIdx.x;
   long long total = 0, blocks = 0, begin = 0, end = 0;
   // at least a step per block, so that every block from an item's first to
@@ -191,6 +196,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks<kHeads>) attn_decode_kernel(
       sm.start[0] = b;
       sm.start[1] = (int)((begin - lo) / v);
       sm.start[2] = (int)((begin - lo) % v);
+      sm.start[3] = own_len;
     }
   };
   if (a.batch <= kThreads) {
@@ -218,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks<kHeads>) attn_decode_kernel(
   load.b = sm.start[0];
   load.item = sm.start[1];
   load.step = sm.start[2];
-  load.len = seq_length(a, load.b);
+  load.len = sm.start[3];
   load.steps = steps_of<kStep>(load.len);
   Place cur = load;  // what the products take next
   long long load_left = end - begin, left = end - begin;
@@ -572,54 +578,55 @@ __global__ void __launch_bounds__(kThreads, kBlocks<kHeads>) attn_decode_kernel(
       // this item's steps in the line, and the blocks that have a part of it
       const long long at = begin + (end - begin - left) - (cur.step - n);  // the item's first step
       const long long first = ((at + 1) * blocks - 1) / total, final = ((at + cur.steps) * blocks - 1) / total;
-      __threadfence();
       __syncthreads();
-      if (tid == 0) sm.last = atomicAdd(p.arrived + first, 1) == (int)(final - first);
+      if (tid == 0) {
+        __threadfence();  // the block's part before its arrival, the others' before what follows
+        sm.last = atomicAdd(p.arrived + first, 1) == (int)(final - first);
+        __threadfence();
+      }
       __syncthreads();
       if (sm.last) {
-        __threadfence();
         const int count = (int)(final - first) + 1;
-        auto part_of = [&](int i) {
-          return p.parts + (size_t)(2 * (first + i) + (i == 0 ? 1 : 0)) * kPartFloats<D, kHeads>;
-        };
-        {
-          // maxima and sums: kEach threads per head over the parts
-          constexpr int kEach = kThreads / kHeads;
-          const int h = tid / kEach, j = tid % kEach;
-          float top = -INFINITY, sum = 0.f;
-          if (h < heads)
-            for (int i = j; i < count; i += kEach) top = fmaxf(top, __ldcg(part_of(i) + kHeads * D + h));
-#pragma unroll
-          for (int w = 1; w < kEach; w <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-          const float base = top == -INFINITY ? 0.f : top;
-          if (h < heads)
-            for (int i = j; i < count; i += kEach)
-              sum += __ldcg(part_of(i) + kHeads * D + kHeads + h) * ex2(__ldcg(part_of(i) + kHeads * D + h) - base);
-#pragma unroll
-          for (int w = 1; w < kEach; w <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-          if (j == 0) {
-            sm.top[h] = top;
-            sm.sum[h] = sum;
-          }
-        }
-        __syncthreads();
+        // four dimensions of a head per thread, kBatch parts in flight: their
+        // maxima, sums and values arrive in one round of latency
+        constexpr int kBatch = 8;
         for (int u = tid; u < heads * (D / 4); u += kThreads) {
           const int h = u / (D / 4), d = u % (D / 4) * 4;
-          const float base = sm.top[h] == -INFINITY ? 0.f : sm.top[h];
+          float top = -INFINITY, sum = 0.f;
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-          for (int i = 0; i < count; ++i) {
-            const float* q = part_of(i);
-            const float f = ex2(__ldcg(q + kHeads * D + h) - base);
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(q + h * D + d));
-            v.x = fmaf(x.x, f, v.x), v.y = fmaf(x.y, f, v.y), v.z = fmaf(x.z, f, v.z), v.w = fmaf(x.w, f, v.w);
+          for (int i0 = 0; i0 < count; i0 += kBatch) {
+            float mi[kBatch], li[kBatch];
+            float4 x[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+              mi[i] = -INFINITY, li[i] = 0.f;
+              x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (i0 + i < count) {
+                const float* q = p.parts + (size_t)(2 * (first + i0 + i) + (i0 + i == 0 ? 1 : 0)) * kPartFloats<D, kHeads>;
+                mi[i] = __ldcg(q + kHeads * D + h);
+                li[i] = __ldcg(q + kHeads * D + kHeads + h);
+                x[i] = __ldcg(reinterpret_cast<const float4*>(q + h * D + d));
+              }
+            }
+            float now = top;
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) now = fmaxf(now, mi[i]);
+            const float base = now == -INFINITY ? 0.f : now;
+            const float old = ex2(top - base);
+            top = now;
+            sum *= old, v.x *= old, v.y *= old, v.z *= old, v.w *= old;
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+              const float f = ex2(mi[i] - base);
+              sum = fmaf(li[i], f, sum);
+              v.x = fmaf(x[i].x, f, v.x), v.y = fmaf(x[i].y, f, v.y), v.z = fmaf(x[i].z, f, v.z), v.w = fmaf(x[i].w, f, v.w);
+            }
           }
-          const float l1 = sm.sum[h], inv = l1 > 0.f ? v_scale / l1 : 0.f;
+          const float inv = sum > 0.f ? v_scale / sum : 0.f;
           *reinterpret_cast<uint2*>(a.out + (out0 + h) * D + d) =
               make_uint2(pack16<kB>(v.x * inv, v.y * inv), pack16<kB>(v.z * inv, v.w * inv));
+          if (a.lse && d == 0) a.lse[out0 + h] = sum > 0.f ? top * kLn2 + logf(sum) : -INFINITY;
         }
-        if (a.lse && tid < heads)
-          a.lse[out0 + tid] = sm.sum[tid] > 0.f ? sm.top[tid] * kLn2 + logf(sm.sum[tid]) : -INFINITY;
         if (tid == 0) p.arrived[first] = 0;  // left zero for the next call
       }
     }

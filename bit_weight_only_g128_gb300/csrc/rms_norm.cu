@@ -85,15 +85,16 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormArgs a, int ro
   const uint4* xr = reinterpret_cast<const uint4*>(a.x + (live ? m : 0) * a.ldx);
   const uint4* rr = a.residual ? reinterpret_cast<const uint4*>(a.residual + (live ? m : 0) * a.ldr) : nullptr;
   const uint4* wr = reinterpret_cast<const uint4*>(a.weight);
-  uint4 xv[kVecs], rv[kVecs];
+  uint4 xv[kVecs], rv[kVecs], wv[kVecs];
   float h[kVecs][8];
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
     const int c = t + i * row_threads;
-    xv[i] = rv[i] = make_uint4(0, 0, 0, 0);
+    xv[i] = rv[i] = wv[i] = make_uint4(0, 0, 0, 0);
     if (live && c < nv) {
       xv[i] = ldg_stream(xr + c);
       if (rr) rv[i] = rr[c];
+      if (kVecs <= 2) wv[i] = wr[c];  // in flight with the row (more would not fit the registers)
     }
   }
   float sum = 0.f;
@@ -126,7 +127,7 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormArgs a, int ro
         o.w = pack16<kB>(h[i][6], h[i][7]);
         reinterpret_cast<uint4*>(a.h + m * a.ldh)[c] = o;
       }
-      const uint4 w = wr[c];
+      const uint4 w = kVecs <= 2 ? wv[i] : wr[c];
       const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -227,11 +228,12 @@ cudaError_t launch_norm(const NormArgs& a, cudaStream_t stream) {
                    al(a.residual) && al(a.weight) && al(a.y) && al(a.codes) && al(a.aq) && al(a.h);
   if (!vec) return launch_pdl(rms_norm_any_kernel<kB>, dim3((unsigned)a.M), dim3(256), 0, stream, a);
   const int nv = a.K / 8;
-  // threads per row: one vector each while the rows are few (the chain of a
-  // row is what counts), up to four each once the rows fill the device
+  // Vectors per thread: one while all rows' threads fit the device at once
+  // (then a row's chain of loads, sums and stores is what counts), up to four
+  // beyond that (then the bytes in flight of the resident blocks; 8192
+  // channels x 4096 rows: 44 us with one, 42 with four).
   int vecs = nv <= 1024 ? 1 : nv <= 2048 ? 2 : nv <= 4096 ? 4 : 8;
-  if (a.M > 152 * 2)
-    while (vecs < 4 && (nv + vecs - 1) / vecs > 256) vecs *= 2;
+  while (vecs < 4 && (long long)a.M * ((nv + vecs - 1) / vecs) > (long long)device_sms() * 2048) vecs *= 2;
   int threads = ((nv + vecs - 1) / vecs + 31) / 32 * 32;
   int rows = threads >= 128 ? 1 : 128 / threads;
   if (rows > a.M) rows = a.M;

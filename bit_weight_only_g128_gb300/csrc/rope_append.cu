@@ -12,7 +12,7 @@
 // Bound: HBM bytes (the qkv rows in, q and the cache rows out); for a few
 // tokens the chain slot/position - table row - store (latency). Each thread
 // takes both halves of a rotated pair as two 16-byte vectors and keeps its
-// cosines and sines in registers over the heads of its token.
+// cosines and sines in registers over the heads that it takes.
 #include "common.cuh"
 #include "kernels.h"
 #include "layer.cuh"
@@ -51,13 +51,13 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
   }
 }
 
-// 8 consecutive values to q or the cache, at element `at`.
+// 8 consecutive values to q or the cache, at element `at` (e4m3: f * inv).
 template <bool kB, bool k8>
-__device__ __forceinline__ void store8(void* base, size_t at, const float (&f)[8], float scale) {
+__device__ __forceinline__ void store8(void* base, size_t at, const float (&f)[8], float inv) {
   if (k8) {
     float g[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) g[i] = __fdiv_rn(f[i], scale);
+    for (int i = 0; i < 8; ++i) g[i] = f[i] * inv;
     uint2 o;
     o.x = e4m3x2(g[0], g[1]) | (e4m3x2(g[2], g[3]) << 16);
     o.y = e4m3x2(g[4], g[5]) | (e4m3x2(g[6], g[7]) << 16);
@@ -67,19 +67,47 @@ __device__ __forceinline__ void store8(void* base, size_t at, const float (&f)[8
   }
 }
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;    // of the element path
+constexpr int kMostThreads = 512;  // of the vector path
+
+// A load that stays where it is written: ahead of the loads that the block
+// waits for.
+__device__ __forceinline__ uint4 ldg_now(const uint16_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
 
 // R a multiple of 16. D / 16 threads per head, each with two vectors of 8:
-// the halves of a pair below R, consecutive ones above. blockIdx.x: token,
-// blockIdx.y: share of the heads.
+// the halves of a pair below R, consecutive ones above. A thread takes two
+// heads, whose four vectors are in flight while the slot, the position and
+// the table's row arrive. blockIdx.x: token, blockIdx.y: share of the heads.
 template <bool kB, bool k8, bool kInter, int D>
-__global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeArgs a) {
-  constexpr int kLanes = D / 16;            // threads per head
-  constexpr int kHeads = kThreads / kLanes;  // heads per step of the block
+__global__ void __launch_bounds__(kMostThreads) rope_append_kernel(const RopeArgs a) {
+  constexpr int kLanes = D / 16;  // threads per head
   allow_dependent_launch();
   grid_dependency_wait();
   const int t = blockIdx.x;
   const int j = threadIdx.x % kLanes;
+  const int heads = a.heads + 2 * a.kv_heads, stride = blockDim.x / kLanes;
+  const bool turned = 16 * j < a.R;
+  const int half = a.R / 2;
+  // the two vectors' first dimensions
+  const int d0 = turned && !kInter ? 8 * j : 16 * j;
+  const int d1 = turned && !kInter ? half + 8 * j : 16 * j + 8;
+  const uint16_t* row = a.qkv + (size_t)t * a.ld;
+  const int h0 = blockIdx.y * 2 * stride + threadIdx.x / kLanes;
+  uint4 x[2][2];
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+    const int h = h0 + n * stride;
+    if (h < heads) {
+      x[n][0] = ldg_now(row + (size_t)h * D + d0);
+      x[n][1] = ldg_now(row + (size_t)h * D + d1);
+    }
+  }
   const long long slot = a.slots[t];
   int pos = a.positions[t];
   bool keep = slot >= 0;
@@ -88,41 +116,37 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeArgs a)
     if (slot >= a.capacity) keep = false;
     if (pos < 0 || pos >= a.table_len) pos = 0;
   }
-  const bool turned = 16 * j < a.R;
-  const int half = a.R / 2;
-  // the two vectors' first dimensions, and the first of their 8 angles
-  const int d0 = turned && !kInter ? 8 * j : 16 * j;
-  const int d1 = turned && !kInter ? half + 8 * j : 16 * j + 8;
   float c[8], s[8];
   if (turned) {
-    const float4* row = reinterpret_cast<const float4*>(a.table + (size_t)pos * a.R);
+    const float4* angles = reinterpret_cast<const float4*>(a.table + (size_t)pos * a.R);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float4 u = row[2 * j + i], w = row[half / 4 + 2 * j + i];
+      const float4 u = angles[2 * j + i], w = angles[half / 4 + 2 * j + i];
       c[4 * i] = u.x, c[4 * i + 1] = u.y, c[4 * i + 2] = u.z, c[4 * i + 3] = u.w;
       s[4 * i] = w.x, s[4 * i + 1] = w.y, s[4 * i + 2] = w.z, s[4 * i + 3] = w.w;
     }
   }
-  const int heads = a.heads + 2 * a.kv_heads;
-  const uint16_t* row = a.qkv + (size_t)t * a.ld;
   const int page_size = 1 << a.page_shift;
   const size_t page = keep ? (size_t)(slot >> a.page_shift) : 0;
   const int off = keep ? (int)(slot & (page_size - 1)) : 0;
-  for (int h = blockIdx.y * kHeads + threadIdx.x / kLanes; h < heads; h += gridDim.y * kHeads) {
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+    const int h = h0 + n * stride;
+    if (h >= heads) break;
     const bool is_q = h < a.heads, is_v = h >= a.heads + a.kv_heads;
     if (!is_q && !keep) continue;
     float lo[8], hi[8];
-    unpack8<kB>(ldg_stream(reinterpret_cast<const uint4*>(row + (size_t)h * D + d0)), lo);
-    unpack8<kB>(ldg_stream(reinterpret_cast<const uint4*>(row + (size_t)h * D + d1)), hi);
+    unpack8<kB>(x[n][0], lo);
+    unpack8<kB>(x[n][1], hi);
     if (turned && !is_v) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         if (kInter) {
           // 16 consecutive dimensions: pairs (0,1) .. (6,7) of lo, then of hi
-          float& x = i < 4 ? lo[2 * i] : hi[2 * i - 8];
-          float& y = i < 4 ? lo[2 * i + 1] : hi[2 * i - 7];
-          const float u = x * c[i] - y * s[i], w = y * c[i] + x * s[i];
-          x = u, y = w;
+          float& u0 = i < 4 ? lo[2 * i] : hi[2 * i - 8];
+          float& w0 = i < 4 ? lo[2 * i + 1] : hi[2 * i - 7];
+          const float u = u0 * c[i] - w0 * s[i], w = w0 * c[i] + u0 * s[i];
+          u0 = u, w0 = w;
         } else {
           const float u = lo[i] * c[i] - hi[i] * s[i], w = hi[i] * c[i] + lo[i] * s[i];
           lo[i] = u, hi[i] = w;
@@ -136,9 +160,9 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeArgs a)
     } else {
       const int hk = is_v ? h - a.heads - a.kv_heads : h - a.heads;
       const size_t at = ((page * a.kv_heads + hk) * page_size + off) * D;
-      const float scale = k8 ? (is_v ? a.v_scale : a.k_scale)[hk] : 1.f;
-      store8<kB, k8>(is_v ? a.v : a.k, at + d0, lo, scale);
-      store8<kB, k8>(is_v ? a.v : a.k, at + d1, hi, scale);
+      const float inv = k8 ? __frcp_rn((is_v ? a.v_scale : a.k_scale)[hk]) : 1.f;
+      store8<kB, k8>(is_v ? a.v : a.k, at + d0, lo, inv);
+      store8<kB, k8>(is_v ? a.v : a.k, at + d1, hi, inv);
     }
   }
 }
@@ -181,7 +205,7 @@ __global__ void __launch_bounds__(kThreads) rope_append_any_kernel(const RopeArg
     const size_t at = ((page * a.kv_heads + hk) * page_size + off) * D + d;
     void* base = is_v ? a.v : a.k;
     if (k8)
-      static_cast<uint8_t*>(base)[at] = (uint8_t)e4m3x2(__fdiv_rn(f, (is_v ? a.v_scale : a.k_scale)[hk]), 0.f);
+      static_cast<uint8_t*>(base)[at] = (uint8_t)e4m3x2(f * __frcp_rn((is_v ? a.v_scale : a.k_scale)[hk]), 0.f);
     else
       static_cast<uint16_t*>(base)[at] = bits16<kB>(f);
   }
@@ -191,20 +215,19 @@ template <bool kB, bool k8, bool kInter>
 cudaError_t launch_rope(const RopeArgs& a, int D, cudaStream_t stream) {
   const int heads = a.heads + 2 * a.kv_heads;
   auto al = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
-  // heads of a token over several blocks while the tokens are few
-  auto shares = [&](int steps) {
-    int y = (152 * 4 + a.T - 1) / a.T;
-    return (unsigned)(y < steps ? y : steps);
-  };
   if (a.R % 16 != 0 || a.ld % 8 != 0 || !al(a.qkv) || !al(a.q) || !al(a.table)) {
-    const int steps = (heads * D + kThreads - 1) / kThreads;
-    return launch_pdl(rope_append_any_kernel<kB, k8, kInter>, dim3((unsigned)a.T, shares(steps)), dim3(kThreads), 0,
-                      stream, a, D);
+    // a token over several blocks while the tokens are few
+    const int steps = (heads * D + kThreads - 1) / kThreads, share = (device_sms() * 4 + a.T - 1) / a.T;
+    return launch_pdl(rope_append_any_kernel<kB, k8, kInter>, dim3((unsigned)a.T, (unsigned)(share < steps ? share : steps)),
+                      dim3(kThreads), 0, stream, a, D);
   }
-  const int steps = (heads * (D / 16) + kThreads - 1) / kThreads;
-  const dim3 grid((unsigned)a.T, shares(steps));
-  return D == 64 ? launch_pdl(rope_append_kernel<kB, k8, kInter, 64>, grid, dim3(kThreads), 0, stream, a)
-                 : launch_pdl(rope_append_kernel<kB, k8, kInter, 128>, grid, dim3(kThreads), 0, stream, a);
+  // two heads per thread, in as few blocks per token as hold them, evenly
+  const int tasks = (heads + 1) / 2 * (D / 16);
+  const int blocks = (tasks + kMostThreads - 1) / kMostThreads;
+  const int threads = ((tasks + blocks - 1) / blocks + 31) / 32 * 32;
+  const dim3 grid((unsigned)a.T, (unsigned)blocks);
+  return D == 64 ? launch_pdl(rope_append_kernel<kB, k8, kInter, 64>, grid, dim3(threads), 0, stream, a)
+                 : launch_pdl(rope_append_kernel<kB, k8, kInter, 128>, grid, dim3(threads), 0, stream, a);
 }
 
 }  // namespace

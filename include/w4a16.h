@@ -393,7 +393,7 @@ int w4a16_rms_norm(const uint16_t* x, int64_t x_stride, const uint16_t* residual
  * `rotary` on (even, at most head_dim) pass through. q [tokens][heads]
  * [head_dim] receives the queries; keys and values go to slot
  * slots[t] = page * page_size + place of the cache, rounded to its type
- * (e4m3: x / scale, nearest even, saturating). A negative slot stores
+ * (e4m3: x times the fp32 reciprocal of the scale, nearest even, saturating). A negative slot stores
  * nothing. A slot beyond the cache stores nothing and a position outside the
  * table turns as position 0, both recorded (bit 128). Two tokens must not
  * have the same slot. */
