@@ -7,7 +7,8 @@ shared library against the shared CUDA runtime (the one PyTorch loads).
 shared-memory access of its kernels is tested against its buffer first, and
 an access outside sets a bit of the device error word instead of running.
 Load it by setting W4A16_LIBRARY to its path before the binding loads the
-library. Running ``python -m bit_weight_only_g128_gb300.build [--checked]``
+library. Both also compile csrc/binding.cpp (the Python binding's native part)
+with the host compiler against PyTorch's headers. Running ``python -m bit_weight_only_g128_gb300.build [--checked]``
 builds by hand.
 """
 from __future__ import annotations
@@ -18,6 +19,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -25,6 +27,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libw4a16.so")
 BUILD_CHECKED = os.path.join(BUILD, "checked")
 LIB_CHECKED = os.path.join(BUILD_CHECKED, "libw4a16_checked.so")
+BINDING = os.path.join(BUILD, "_binding.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -40,8 +43,34 @@ def nvcc() -> str:
 
 
 def _deps_mtime() -> float:
-    files = glob.glob(os.path.join(CSRC, "*")) + glob.glob(os.path.join(INCLUDE, "*.h"))
+    files = glob.glob(os.path.join(CSRC, "*.cu*")) + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(
+        os.path.join(INCLUDE, "*.h"))
     return max(os.path.getmtime(f) for f in files)
+
+
+def build_binding(force: bool = False) -> str:
+    """Compile csrc/binding.cpp to the CPython module _build/_binding.so
+    (against PyTorch's headers, host compiler); returns its path."""
+    src = os.path.join(CSRC, "binding.cpp")
+    deps = [src] + glob.glob(os.path.join(INCLUDE, "*.h"))
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(map(os.path.getmtime, deps)):
+        return BINDING
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    headers = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    os.makedirs(BUILD, exist_ok=True)
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           *[f for h in headers for f in ("-isystem", h)], "-I" + INCLUDE, src, "-o", tmp,
+           "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed for binding.cpp:\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 def _compile(src: str, obj: str, extra) -> str:
@@ -58,12 +87,15 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), checked: b
     out_dir, lib = (BUILD_CHECKED, LIB_CHECKED) if checked else (BUILD, LIB)
     os.makedirs(out_dir, exist_ok=True)
     if not force and os.path.exists(lib) and os.path.getmtime(lib) >= _deps_mtime():
+        build_binding()
         return lib
     sources = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     objs = [os.path.join(out_dir, os.path.basename(s)[:-3] + ".o") for s in sources]
     extra = list(extra_flags) + (["-DW4A16_CHECKED"] if checked else []) + (["-Xptxas", "-v"] if verbose else [])
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(sources))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(os.cpu_count() or 8, len(sources) + 1)) as ex:
+        binding = ex.submit(build_binding, force)
         logs = list(ex.map(lambda so: _compile(so[0], so[1], extra), zip(sources, objs)))
+        binding.result()
     if verbose:
         for src, log in zip(sources, logs):
             if log.strip():

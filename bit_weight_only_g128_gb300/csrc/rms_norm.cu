@@ -11,7 +11,7 @@
 //
 // Bound: HBM bytes, 2 K (x) + 2 K (residual) + 2 K (h) + 2 K or K (y) per
 // row; for few rows the chain load - block sum - store (latency). One pass: a
-// row's h stays in its threads' registers (at most 8 vectors of 8 channels
+// row's h stays in its threads' registers (at most 4 vectors of 8 channels
 // each) from the load to the store.
 #include "common.cuh"
 #include "kernels.h"
@@ -178,7 +178,8 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormArgs a, int ro
   }
 }
 
-// Any K, stride and 2-byte alignment: one block per row, the row read again
+// Any K (above 32768 a row does not fit the registers), stride and 2-byte
+// alignment: one block per row, the row read again
 // for each of the steps (sum, maximum, result). An output that is the
 // residual itself is written in the last step only, each element by the
 // thread that reads it.
@@ -224,7 +225,7 @@ __global__ void __launch_bounds__(256) rms_norm_any_kernel(const NormArgs a) {
 template <bool kB>
 cudaError_t launch_norm(const NormArgs& a, cudaStream_t stream) {
   auto al = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
-  const bool vec = a.K % 8 == 0 && a.ldx % 8 == 0 && a.ldr % 8 == 0 && a.ldh % 8 == 0 && al(a.x) &&
+  const bool vec = a.K % 8 == 0 && a.K <= 32768 && a.ldx % 8 == 0 && a.ldr % 8 == 0 && a.ldh % 8 == 0 && al(a.x) &&
                    al(a.residual) && al(a.weight) && al(a.y) && al(a.codes) && al(a.aq) && al(a.h);
   if (!vec) return launch_pdl(rms_norm_any_kernel<kB>, dim3((unsigned)a.M), dim3(256), 0, stream, a);
   const int nv = a.K / 8;
@@ -232,7 +233,7 @@ cudaError_t launch_norm(const NormArgs& a, cudaStream_t stream) {
   // (then a row's chain of loads, sums and stores is what counts), up to four
   // beyond that (then the bytes in flight of the resident blocks; 8192
   // channels x 4096 rows: 44 us with one, 42 with four).
-  int vecs = nv <= 1024 ? 1 : nv <= 2048 ? 2 : nv <= 4096 ? 4 : 8;
+  int vecs = nv <= 1024 ? 1 : nv <= 2048 ? 2 : 4;
   while (vecs < 4 && (long long)a.M * ((nv + vecs - 1) / vecs) > (long long)device_sms() * 2048) vecs *= 2;
   int threads = ((nv + vecs - 1) / vecs + 31) / 32 * 32;
   int rows = threads >= 128 ? 1 : 128 / threads;
@@ -241,8 +242,7 @@ cudaError_t launch_norm(const NormArgs& a, cudaStream_t stream) {
   switch (vecs) {
     case 1: return launch_pdl(rms_norm_kernel<kB, 1>, grid, block, 0, stream, a, threads);
     case 2: return launch_pdl(rms_norm_kernel<kB, 2>, grid, block, 0, stream, a, threads);
-    case 4: return launch_pdl(rms_norm_kernel<kB, 4>, grid, block, 0, stream, a, threads);
-    default: return launch_pdl(rms_norm_kernel<kB, 8>, grid, block, 0, stream, a, threads);
+    default: return launch_pdl(rms_norm_kernel<kB, 4>, grid, block, 0, stream, a, threads);
   }
 }
 
