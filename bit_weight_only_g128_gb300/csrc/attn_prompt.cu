@@ -538,6 +538,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
           loaders_sync();  // the ring's slots are within one round of `pos`
           const int r0 = u / kChunks, c = u % kChunks;
           constexpr int kStride = 128 / kChunks;
+          const int first_tile = i;
+          int pair[2] = {0, 0};  // slots of the tile's keys and values
           for (; i < 2 * most && ok; ++i) {
             const uint8_t* src = static_cast<const uint8_t*>(i & 1 ? a.cache.v : a.cache.k);
             const unsigned long long group = row_of_or_0(row_of, (i >> 1) * kTile + 16 * (lane & 7), len);
@@ -551,11 +553,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
               cp16(dst + x * kStride * 128, valid ? src + row * (2 * D) + c * 16 : src, valid);
             }
             cp_commit();
-            cp_wait<0>();
-            fence_async_shared();
-            loaders_sync();
-            if (u == 0 && ok) mbar_arrive(bar(kFull + pos.slot));
+            pair[(i - first_tile) & 1] = pos.slot;
             pos.step(1, kSlots);
+            if ((i - first_tile) & 1) {  // keys and values are on their way: announce the keys, then both
+              cp_wait<1>();
+              fence_async_shared();
+              loaders_sync();
+              if (u == 0 && ok) mbar_arrive(bar(kFull + pair[0]));
+              cp_wait<0>();
+              fence_async_shared();
+              loaders_sync();
+              if (u == 0 && ok) mbar_arrive(bar(kFull + pair[1]));
+            }
           }
         }
       } else {

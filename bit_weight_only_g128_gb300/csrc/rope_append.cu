@@ -11,8 +11,7 @@
 //
 // Bound: HBM bytes (the qkv rows in, q and the cache rows out); for a few
 // tokens the chain slot/position - table row - store (latency). Each thread
-// takes both halves of a rotated pair as two 16-byte vectors and keeps its
-// cosines and sines in registers over the heads that it takes.
+// takes both halves of a rotated pair as two 16-byte vectors, for two heads.
 #include "common.cuh"
 #include "kernels.h"
 #include "layer.cuh"
@@ -36,37 +35,6 @@ struct RopeArgs {
   int* err;
 };
 
-template <bool kB>
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack16<kB>(f[0], f[1]), pack16<kB>(f[2], f[3]), pack16<kB>(f[4], f[5]), pack16<kB>(f[6], f[7]));
-}
-template <bool kB>
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 u = unpack16<kB>(w[i]);
-    f[2 * i] = u.x;
-    f[2 * i + 1] = u.y;
-  }
-}
-
-// 8 consecutive values to q or the cache, at element `at` (e4m3: f * inv).
-template <bool kB, bool k8>
-__device__ __forceinline__ void store8(void* base, size_t at, const float (&f)[8], float inv) {
-  if (k8) {
-    float g[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) g[i] = f[i] * inv;
-    uint2 o;
-    o.x = e4m3x2(g[0], g[1]) | (e4m3x2(g[2], g[3]) << 16);
-    o.y = e4m3x2(g[4], g[5]) | (e4m3x2(g[6], g[7]) << 16);
-    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(base) + at) = o;
-  } else {
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + at) = pack8<kB>(f);
-  }
-}
-
 constexpr int kThreads = 256;    // of the element path
 constexpr int kMostThreads = 512;  // of the vector path
 
@@ -85,7 +53,7 @@ __device__ __forceinline__ uint4 ldg_now(const uint16_t* p) {
 // heads, whose four vectors are in flight while the slot, the position and
 // the table's row arrive. blockIdx.x: token, blockIdx.y: share of the heads.
 template <bool kB, bool k8, bool kInter, int D>
-__global__ void __launch_bounds__(kMostThreads) rope_append_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kMostThreads, 2) rope_append_kernel(const RopeArgs a) {
   constexpr int kLanes = D / 16;  // threads per head
   allow_dependent_launch();
   grid_dependency_wait();
@@ -99,7 +67,7 @@ __global__ void __launch_bounds__(kMostThreads) rope_append_kernel(const RopeArg
   const int d1 = turned && !kInter ? half + 8 * j : 16 * j + 8;
   const uint16_t* row = a.qkv + (size_t)t * a.ld;
   const int h0 = blockIdx.y * 2 * stride + threadIdx.x / kLanes;
-  uint4 x[2][2];
+  uint4 x[2][2] = {};
 #pragma unroll
   for (int n = 0; n < 2; ++n) {
     const int h = h0 + n * stride;
@@ -116,53 +84,78 @@ __global__ void __launch_bounds__(kMostThreads) rope_append_kernel(const RopeArg
     if (slot >= a.capacity) keep = false;
     if (pos < 0 || pos >= a.table_len) pos = 0;
   }
-  float c[8], s[8];
-  if (turned) {
-    const float4* angles = reinterpret_cast<const float4*>(a.table + (size_t)pos * a.R);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float4 u = angles[2 * j + i], w = angles[half / 4 + 2 * j + i];
-      c[4 * i] = u.x, c[4 * i + 1] = u.y, c[4 * i + 2] = u.z, c[4 * i + 3] = u.w;
-      s[4 * i] = w.x, s[4 * i + 1] = w.y, s[4 * i + 2] = w.z, s[4 * i + 3] = w.w;
-    }
-  }
   const int page_size = 1 << a.page_shift;
   const size_t page = keep ? (size_t)(slot >> a.page_shift) : 0;
   const int off = keep ? (int)(slot & (page_size - 1)) : 0;
+  const float* cosines = a.table + (size_t)pos * a.R + 8 * j;
+  const float* sines = cosines + half;
+  float inv[2];  // of the head's e4m3 scale
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+    const int h = h0 + n * stride;
+    inv[n] = 1.f;
+    if (k8 && h >= a.heads && h < heads)
+      inv[n] = __frcp_rn(h < a.heads + a.kv_heads ? a.k_scale[h - a.heads] : a.v_scale[h - a.heads - a.kv_heads]);
+  }
+  // two dimensions of each vector at a time, in place (an e4m3 pair takes the
+  // word's lower half)
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    float2 c = make_float2(1.f, 1.f), s = make_float2(0.f, 0.f);
+    if (turned) {
+      // interleaved: word w of the first vector turns by angle w, of the
+      // second by angle 4 + w; else both words by angles 2w and 2w + 1
+      c = kInter ? make_float2(cosines[w], cosines[4 + w]) : *reinterpret_cast<const float2*>(cosines + 2 * w);
+      s = kInter ? make_float2(sines[w], sines[4 + w]) : *reinterpret_cast<const float2*>(sines + 2 * w);
+    }
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const int h = h0 + n * stride;
+      const bool is_q = h < a.heads, is_v = h >= a.heads + a.kv_heads;
+      uint32_t& x0 = reinterpret_cast<uint32_t(&)[4]>(x[n][0])[w];
+      uint32_t& x1 = reinterpret_cast<uint32_t(&)[4]>(x[n][1])[w];
+      float2 lo = unpack16<kB>(x0), hi = unpack16<kB>(x1);
+      if (turned && !is_v) {
+        const float2 u = lo, v = hi;
+        if (kInter) {
+          lo = make_float2(u.x * c.x - u.y * s.x, u.y * c.x + u.x * s.x);
+          hi = make_float2(v.x * c.y - v.y * s.y, v.y * c.y + v.x * s.y);
+        } else {
+          lo = make_float2(u.x * c.x - v.x * s.x, u.y * c.y - v.y * s.y);
+          hi = make_float2(v.x * c.x + u.x * s.x, v.y * c.y + u.y * s.y);
+        }
+      }
+      if (k8 && !is_q) {
+        x0 = e4m3x2(lo.x * inv[n], lo.y * inv[n]);
+        x1 = e4m3x2(hi.x * inv[n], hi.y * inv[n]);
+      } else {
+        x0 = pack16<kB>(lo.x, lo.y);
+        x1 = pack16<kB>(hi.x, hi.y);
+      }
+    }
+  }
 #pragma unroll
   for (int n = 0; n < 2; ++n) {
     const int h = h0 + n * stride;
     if (h >= heads) break;
     const bool is_q = h < a.heads, is_v = h >= a.heads + a.kv_heads;
-    if (!is_q && !keep) continue;
-    float lo[8], hi[8];
-    unpack8<kB>(x[n][0], lo);
-    unpack8<kB>(x[n][1], hi);
-    if (turned && !is_v) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (kInter) {
-          // 16 consecutive dimensions: pairs (0,1) .. (6,7) of lo, then of hi
-          float& u0 = i < 4 ? lo[2 * i] : hi[2 * i - 8];
-          float& w0 = i < 4 ? lo[2 * i + 1] : hi[2 * i - 7];
-          const float u = u0 * c[i] - w0 * s[i], w = w0 * c[i] + u0 * s[i];
-          u0 = u, w0 = w;
-        } else {
-          const float u = lo[i] * c[i] - hi[i] * s[i], w = hi[i] * c[i] + lo[i] * s[i];
-          lo[i] = u, hi[i] = w;
-        }
-      }
-    }
     if (is_q) {
-      const size_t at = ((size_t)t * a.heads + h) * D;
-      store8<kB, false>(a.q, at + d0, lo, 1.f);
-      store8<kB, false>(a.q, at + d1, hi, 1.f);
-    } else {
+      uint16_t* q = a.q + ((size_t)t * a.heads + h) * D;
+      *reinterpret_cast<uint4*>(q + d0) = x[n][0];
+      *reinterpret_cast<uint4*>(q + d1) = x[n][1];
+    } else if (keep) {
       const int hk = is_v ? h - a.heads - a.kv_heads : h - a.heads;
       const size_t at = ((page * a.kv_heads + hk) * page_size + off) * D;
-      const float inv = k8 ? __frcp_rn((is_v ? a.v_scale : a.k_scale)[hk]) : 1.f;
-      store8<kB, k8>(is_v ? a.v : a.k, at + d0, lo, inv);
-      store8<kB, k8>(is_v ? a.v : a.k, at + d1, hi, inv);
+      void* base = is_v ? a.v : a.k;
+      if (k8) {
+        uint8_t* to = static_cast<uint8_t*>(base) + at;
+        *reinterpret_cast<uint2*>(to + d0) = make_uint2(x[n][0].x | (x[n][0].y << 16), x[n][0].z | (x[n][0].w << 16));
+        *reinterpret_cast<uint2*>(to + d1) = make_uint2(x[n][1].x | (x[n][1].y << 16), x[n][1].z | (x[n][1].w << 16));
+      } else {
+        uint16_t* to = static_cast<uint16_t*>(base) + at;
+        *reinterpret_cast<uint4*>(to + d0) = x[n][0];
+        *reinterpret_cast<uint4*>(to + d1) = x[n][1];
+      }
     }
   }
 }
