@@ -10,19 +10,24 @@
 // fp32) and O is rarely rescaled.
 //
 // Bound: the tensor cores, 4 D operations per row and key. One block per SM
-// takes 256 rows, two tiles of 128 whose softmax and products alternate: while
-// one tile's 128 threads (a row each) form P, the tensor cores work on the
-// other tile.
+// takes units of 256 rows from a queue (the most keys of a sequence first),
+// two tiles of 128 whose softmax and products alternate: while one tile's 128
+// threads (a row each) form P, the tensor cores work on the other tile. Every
+// role runs through the units by itself, so that a unit's queries and first
+// keys arrive, and its first products run, while the unit before it ends.
 //   warps 0-3, 4-7   softmax of tile 0, 1 (a thread owns a row: a lane of
 //                    tensor memory), the rare rescaling of O, the results
-//   warps 8-11       copies: queries, then the tiles K0 V0 K1 V1 .. into a
-//                    ring of five slots: tile copies (TMA) of the pages' rows;
+//   warps 8-11       keys and values: the tiles K0 V0 K1 V1 .. into a ring of
+//                    five slots: tile copies (TMA) of the pages' rows;
 //                    16 bytes at a time where a tile ends beyond the sequence
 //                    (those rows as zeros, so that what the cache holds there
 //                    meets P = 0 as 0) and for e4m3 codes, which become fp16
 //                    on the way
-//   warps 14, 15     tcgen05.mma of tile 0, 1: S from shared memory, O += P V with P read
-//                    from tensor memory, where it takes the place of S
+//   warps 12, 13     the units (warp 12) and their queries: tile copies where
+//                    the group divides 128, else 16 bytes at a time
+//   warps 14, 15     tcgen05.mma of tile 0, 1: S from shared memory, O += P V
+//                    with P read from tensor memory, where it takes the place
+//                    of S
 // Tensor memory: S0, S1 (128 columns each), O0, O1 (D each). Registers: 128 a
 // thread at launch, 192 for the softmax warps and 64 for the rest (256 x 192
 // + 256 x 64 = 512 x 128).
@@ -43,18 +48,37 @@ constexpr int kPanel = kTile * 128;  // bytes of 64 dimensions of 128 rows
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.f;  // log2 of how far a row's maximum may run ahead
 
-// barriers: full[kSlots], empty[kSlots], queries[2], scores[2], probs[2 parts][2],
-// out[2], drain[2], turn[2]
-enum { kFull = 0, kEmpty = kSlots, kQueries = 2 * kSlots, kScores = kQueries + 2, kProbs = kScores + 2,
-       kOut = kProbs + 4, kDrain = kOut + 2, kTurn = kDrain + 2,
-       kBars = kTurn + 2 };
+// barriers, [2]: of the row tiles, or of the two places of a unit's description
+enum {
+  kFull = 0,                   // [kSlots] a key or value tile is there
+  kEmpty = kFull + kSlots,     // [kSlots] both row tiles' products have read it
+  kUnit = kEmpty + kSlots,     // [2] a unit is described
+  kUnitFree = kUnit + 2,       // [2] every role has read it
+  kQueries = kUnitFree + 2,    // [2] the queries are there
+  kQueriesFree = kQueries + 2, // [2] the unit's last scores have read them
+  kScores = kQueriesFree + 2,  // [2] S is there (and the last P V done)
+  kProbs = kScores + 2,        // [2 parts][2] P is there
+  kOut = kProbs + 4,           // [2] the unit's O is there
+  kOutFree = kOut + 2,         // [2] O has been read
+  kTurn = kOutFree + 2,        // [2] the tile's products may be issued
+  kCopiers = kTurn + 2,        // the four copying warps meet
+  kDrain = kCopiers + 1,       // [2] products in flight, when giving up
+  kBars = kDrain + 2
+};
+constexpr int kReaders = 8 + 4 + 1 + 2;  // warps that read a unit's description
+
+struct Unit {
+  int b, first, fresh, len;  // sequence, its first row, rows, cached tokens
+  int row0, head;            // first of the unit's rows (tokens x heads), key/value head
+  int n[2];                  // key tiles that the two row tiles need, up to their last row's position
+  int valid;                 // 0: no unit is left
+};
 
 struct Control {
   uint64_t bars[kBars];
+  Unit unit[2];
   uint32_t tmem;
   int abort;
-  int scan[kThreads / 32];
-  int unit[5];  // sequence, unit of it, its first row, rows and length
   float power[2 * kTile];  // what a row's queries were divided by (bf16 over e4m3)
 };
 
@@ -62,13 +86,16 @@ template <int D>
 constexpr int kTileBytes = D / 64 * kPanel;
 template <int D>
 constexpr int kSmem = (2 + kSlots) * kTileBytes<D> + (int)sizeof(Control) + 1024;
+static_assert(kSmem<128> <= 227 * 1024, "one block's shared memory");
 
 struct PromptArgs {
   AttnArgs a;
   int group;
   float mult;      // |scale| log2 e
   uint32_t negate;  // scale < 0
-  int tiled;        // the maps are there
+  int tiled;        // the maps of the keys and values are there
+  int q_tiled;      // the map of the queries is there
+  int* queue;       // next unit, blocks that are through; zero between calls
 };
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
@@ -122,6 +149,11 @@ __device__ __forceinline__ void tie(uint32_t (&r)[32]) {
                  "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
                  "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
 }
+__device__ __forceinline__ void tie(uint32_t (&r)[16]) {
+  asm volatile(""
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+}
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool valid) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
 }
@@ -135,13 +167,40 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
   return (uint32_t)((c >> 3) * kPanel + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
-// Among the 128 copying threads.
-__device__ __forceinline__ void loaders_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-
 // The row of a key, or 0 for one beyond the sequence (whose page is not looked up).
 template <class F>
 __device__ __forceinline__ unsigned long long row_of_or_0(const F& row_of, int key, int len) {
   return key < len ? row_of(key) : 0ull;
+}
+
+// Bounded wait for the phase of parity `parity`, as mbar_wait's, by waits
+// that the hardware suspends for up to kNap: most of this kernel's warps wait
+// most of the time, and polling would take the issue slots of the softmax
+// warps beside them.
+constexpr uint32_t kNap = 20000;  // ns
+__device__ __forceinline__ bool nap_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int code, int* err) {
+  auto nap = [&]() {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(kNap)
+        : "memory");
+    return ok != 0;
+  };
+  if (nap()) return true;
+  const uint64_t t0 = globaltimer();
+  while (true) {
+    if (nap()) return true;
+    if (*abort_flag) return false;
+    if (globaltimer() - t0 > kWaitLimitNs) {
+      *abort_flag = 1;
+      atomicOr(err, code);
+      return false;
+    }
+  }
 }
 
 // True in one lane of the (converged) warp.
@@ -189,13 +248,16 @@ __device__ __forceinline__ uint4 widen(uint32_t lo, uint32_t hi) {
 // two per row that brings them into fp16's range.
 template <bool kB, bool k8, int D>
 __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptArgs p, const __grid_constant__ CUtensorMap map_k,
-                                                                 const __grid_constant__ CUtensorMap map_v) {
+                                                                 const __grid_constant__ CUtensorMap map_v,
+                                                                 const __grid_constant__ CUtensorMap map_q) {
   constexpr int kBytes = kTileBytes<D>;
   constexpr bool kP = kB && !k8;  // products in bf16
+  constexpr int kChunks = D / 8;  // 16-byte chunks of a row
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = (uint32_t)__cvta_generic_to_shared(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
-  Control& ctl = *reinterpret_cast<Control*>(smem_raw + (base - raw) + (2 + kSlots) * kBytes);
+  const uint32_t base = (raw + 1023u) & ~1023u;  // queries [2], ring [kSlots]
+  const uint32_t ring = base + 2 * kBytes;
+  Control& ctl = *reinterpret_cast<Control*>(smem_raw + (ring - raw) + kSlots * kBytes);
   const uint32_t bars = (uint32_t)__cvta_generic_to_shared(&ctl.bars[0]);
   auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
   const AttnArgs& a = p.a;
@@ -208,14 +270,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
       mbar_init(bar(kEmpty + i), 2);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(bar(kQueries + t), 128);
+      mbar_init(bar(kUnit + t), 1);
+      mbar_init(bar(kUnitFree + t), kReaders);
+      mbar_init(bar(kQueries + t), p.q_tiled ? 1 : 64);
+      mbar_init(bar(kQueriesFree + t), kB && k8 ? 129 : 1);
       mbar_init(bar(kScores + t), 1);
       mbar_init(bar(kProbs + t), 128);
       mbar_init(bar(kProbs + 2 + t), 128);
       mbar_init(bar(kOut + t), 1);
-      mbar_init(bar(kDrain + t), 1);
+      mbar_init(bar(kOutFree + t), 128);
       mbar_init(bar(kTurn + t), 1);
+      mbar_init(bar(kDrain + t), 1);
     }
+    mbar_init(bar(kCopiers), 128);
     ctl.abort = 0;
     fence_barrier_init();
   }
@@ -224,399 +291,469 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
     tmem_relinquish();
   }
   tc_fence_before();
-  allow_dependent_launch();
-  grid_dependency_wait();
-
-  // which unit of 256 rows: the last ones of a sequence (the most keys) first
-  const int hk = blockIdx.x % a.cache.kv_heads;
-  const int turn = (int)(blockIdx.x / a.cache.kv_heads);
-  // units of the sequence b0 + tid, and what is known of it
-  int first = 0, fresh = 0, len = 0;
-  auto units = [&](int b) {
-    fresh = 0;
-    if (b >= a.batch) return 0;
-    const int s0 = a.starts[b], s1 = a.starts[b + 1], n = a.lens[b];
-    first = checked(a, s0, a.rows);
-    fresh = checked(a, s1, a.rows) - first;
-    if (fresh < 0) {
-      atomicOr(a.err, kErrRange);
-      fresh = 0;
-    }
-    len = checked(a, n, (int)min((long long)a.max_pages << a.cache.page_shift, 0x7fffffffll));
-    return (int)(((long long)fresh * p.group + 2 * kTile - 1) / (2 * kTile));
-  };
-  auto scan = [&](int v) {  // inclusive over the block, and the total
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += u;
-    }
-    if (lane == 31) ctl.scan[warp] = v;
-    __syncthreads();
-    int before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) before += ctl.scan[w];
-      all += ctl.scan[w];
-    }
-    __syncthreads();
-    return make_int2(v + before, all);
-  };
-  int want = -1;
-  auto find = [&](int b, int v, int lo) {
-    if (lo <= want && want < lo + v) {
-      ctl.unit[0] = b;
-      ctl.unit[1] = want - lo;
-      ctl.unit[2] = first;
-      ctl.unit[3] = fresh;
-      ctl.unit[4] = len;
-    }
-  };
-  if (a.batch <= kThreads) {
-    const int v = units(tid);
-    const int2 s = scan(v);
-    want = s.y - 1 - turn;
-    find(tid, v, s.x - v);
-  } else {
-    int total = 0;
-    for (int b0 = 0; b0 < a.batch; b0 += kThreads) total += scan(units(b0 + tid)).y;
-    want = total - 1 - turn;
-    for (int b0 = 0, carry = 0; b0 < a.batch; b0 += kThreads) {
-      const int v = units(b0 + tid);
-      const int2 s = scan(v);
-      find(b0 + tid, v, carry + s.x - v);
-      carry += s.y;
-    }
-  }
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl.tmem;
-  if (want < 0) {  // fewer units than blocks
-    if (warp == 12) tmem_dealloc(tmem, 512);
-    return;
-  }
-  const int b = ctl.unit[0];
-  first = ctl.unit[2];
-  fresh = ctl.unit[3];
-  len = ctl.unit[4];
-  const int past = len - fresh;  // may be negative: rows that see nothing
-  const int rows = fresh * p.group;  // at most 2^30
-  const int row0 = ctl.unit[1] * (2 * kTile);
-  // key tiles of the two row tiles: up to the last row's position
-  int n[2];
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int lo = row0 + t * kTile, hi = min(lo + kTile, rows);
-    const int last = lo < hi ? past + (hi - 1) / p.group : -1;
-    n[t] = last < 0 ? 0 : last / kTile + 1;
-  }
-  const int most = max(n[0], n[1]);
+  allow_dependent_launch();
+  grid_dependency_wait();
+
+  // The u-th unit of this block.
+  Unit unit;
+  int most = 0;
+  auto read_unit = [&](int u) {
+    unit = ctl.unit[u & 1];
+    most = max(unit.n[0], unit.n[1]);
+    return unit.valid != 0;
+  };
+  // A wait of a whole warp: all of its lanes go on, or none.
+  auto warp_wait = [&](int i, uint32_t phase, int code) {
+    return __all_sync(0xffffffffu, nap_wait(bar(i), phase, abort_flag, code, a.err)) != 0;
+  };
+  auto next_unit = [&](int u, int code, bool release) {  // of a whole warp
+    if (!warp_wait(kUnit + (u & 1), (uint32_t)(u >> 1) & 1u, code)) return false;
+    const bool valid = read_unit(u);
+    __syncwarp();
+    if (valid && release && lane == 0) mbar_arrive(bar(kUnitFree + (u & 1)));
+    return valid;
+  };
 
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     const int t = warp >> 2;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // the warp's quarter of the lanes
     const uint32_t scores = tmem + lanes + (uint32_t)(t * kTile), out = tmem + lanes + 256u + (uint32_t)(t * D);
-    const int row = row0 + t * kTile + (tid & 127);
-    const bool live = row < rows;
-    const int token = live ? row / p.group : 0, head = hk * p.group + (live ? row % p.group : 0);
-    const int limit = live ? past + token + 1 : 0;  // keys this row sees
-    float mult = p.mult * (k8 ? a.cache.k_scale[hk] : 1.f);
-    const int nt = t ? n[1] : n[0];
-    float m = -INFINITY, l = 0.f;
+    uint32_t score_phase = 0, out_phase = 0;
     bool ok = true;
-    if (kB && k8 && nt > 0) {
-      ok = mbar_wait(bar(kQueries + t), 0u, abort_flag, kErrEpilogue, a.err);
-      mult *= ctl.power[t * kTile + (tid & 127)];
-    }
-    for (int j = 0; j < nt && ok; ++j) {
-      if (!(ok = mbar_wait(bar(kScores + t), (uint32_t)j & 1u, abort_flag, kErrEpilogue, a.err))) break;
-      tc_fence_after();
-      uint32_t s[4][32];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) tmem_ld32(scores + 32 * q, s[q]);
-      tmem_wait_ld();
-#pragma unroll
-      for (int q = 0; q < 4; ++q) tie(s[q]);
-      const int seen = limit - j * kTile;
-      if (!__all_sync(0xffffffffu, seen >= kTile)) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (32 * q + i >= seen) s[q][i] = 0xff800000u;
+    for (int u = 0; ok; ++u) {
+      if (!next_unit(u, kErrEpilogue, true)) break;
+      const int nt = t ? unit.n[1] : unit.n[0];
+      const int row = unit.row0 + t * kTile + (tid & 127);
+      const bool live = row < unit.fresh * p.group;
+      const int token = live ? row / p.group : 0, head = unit.head * p.group + (live ? row % p.group : 0);
+      const int limit = live ? unit.len - unit.fresh + token + 1 : 0;  // keys this row sees
+      const int to = live ? (unit.first + token) * a.heads + head : -1;
+      float mult = p.mult * (k8 ? a.cache.k_scale[unit.head] : 1.f);
+      const float v_scale = k8 ? a.cache.v_scale[unit.head] : 1.f;
+      if (kB && k8) {
+        if (!(ok = warp_wait(kQueries + t, (uint32_t)u & 1u, kErrEpilogue))) break;
+        mult *= ctl.power[t * kTile + (tid & 127)];
+        mbar_arrive(bar(kQueriesFree + t));
       }
-      float top4[4];
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < nt; ++j) {
+        if (!(ok = warp_wait(kScores + t, score_phase, kErrEpilogue))) break;
+        score_phase ^= 1u;
+        tc_fence_after();
+        uint32_t s[4][32];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) top4[q] = fmaxf(__uint_as_float(s[q][0]), __uint_as_float(s[q][1]));
+        for (int q = 0; q < 4; ++q) tmem_ld32(scores + 32 * q, s[q]);
+        tmem_wait_ld();
 #pragma unroll
-      for (int i = 2; i < 32; i += 2)
+        for (int q = 0; q < 4; ++q) tie(s[q]);
+        const int seen = limit - j * kTile;
+        if (!__all_sync(0xffffffffu, seen >= kTile)) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          top4[q] = fmaxf(fmaxf(top4[q], __uint_as_float(s[q][i])), __uint_as_float(s[q][i + 1]));
-      const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * mult;
-      const bool moves = top > m + kSlack;
-      if (__any_sync(0xffffffffu, moves)) {
-        const float f = moves ? ex2(m - top) : 1.f;
-        if (moves) m = top;
-        l *= f;
-        if (j > 0) {
-          // the scores' arrival says that the product with the last P is done
+          for (int q = 0; q < 4; ++q)
 #pragma unroll
-          for (int c = 0; c < D; c += 16) {
-            uint32_t o[16];
-            tmem_ld16(out + c, o);
+            for (int i = 0; i < 32; ++i)
+              if (32 * q + i >= seen) s[q][i] = 0xff800000u;
+        }
+        float top4[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) top4[q] = fmaxf(__uint_as_float(s[q][0]), __uint_as_float(s[q][1]));
+#pragma unroll
+        for (int i = 2; i < 32; i += 2)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            top4[q] = fmaxf(fmaxf(top4[q], __uint_as_float(s[q][i])), __uint_as_float(s[q][i + 1]));
+        const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * mult;
+        const bool moves = top > m + kSlack;
+        if (__any_sync(0xffffffffu, moves)) {
+          const float f = moves ? ex2(m - top) : 1.f;
+          if (moves) m = top;
+          l *= f;
+          if (j > 0) {
+            // the scores' arrival says that the product with the last P is done
+#pragma unroll
+            for (int c = 0; c < D; c += 16) {
+              uint32_t o[16];
+              tmem_ld16(out + c, o);
+              tmem_wait_ld();
+              tie(o);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st16(out + c, o);
+            }
+          }
+        }
+        const float shift = m == -INFINITY ? 0.f : -m;
+        // P in two parts, of 96 and 32 keys: the product with the first runs
+        // while the second is formed; the sums wait until both are on their way
+        const uint64_t mult2 = pack2(mult, mult), shift2 = pack2(shift, shift);
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+#pragma unroll
+          for (int q = part ? 3 : 0; q < (part ? 4 : 3); ++q) {
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float x, y;
+              unpack2(fma2(pack2(__uint_as_float(s[q][2 * i]), __uint_as_float(s[q][2 * i + 1])), mult2, shift2), x, y);
+              x = ex2(x), y = ex2(y);
+              s[q][2 * i] = __float_as_uint(x), s[q][2 * i + 1] = __float_as_uint(y);
+              w[i] = pack16<kP>(x, y);
+            }
+            tmem_st16(scores + 16 * q, w);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(bar(kProbs + 2 * part + t));
+        }
+        uint64_t l4[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < 32; i += 2)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) l4[q] = add2(l4[q], pack2(__uint_as_float(s[q][i]), __uint_as_float(s[q][i + 1])));
+        float lo, hi;
+        unpack2(add2(add2(l4[0], l4[1]), add2(l4[2], l4[3])), lo, hi);
+        l += lo + hi;
+      }
+      if (ok && nt > 0) {
+        ok = warp_wait(kOut + t, out_phase, kErrEpilogue);
+        out_phase ^= 1u;
+        tc_fence_after();
+      }
+      if (!ok) break;
+      const float inv = l > 0.f ? v_scale / l : 0.f;
+      // 64 dimensions at a time, transposed among eight lanes (a lane's eight
+      // 16-byte chunks of its row become one chunk of eight rows), so that
+      // whole lines are written: a row per lane would be 32 lines per store
+#pragma unroll
+      for (int d0 = 0; d0 < D; d0 += 64) {
+        uint32_t x[8][4];
+#pragma unroll
+        for (int c = 0; c < 64; c += 32) {
+          uint32_t o[32];
+          if (nt > 0) {
+            tmem_ld32(out + d0 + c, o);
             tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-            tmem_st16(out + c, o);
+            tie(o);
+            if (d0 + c + 32 == D) {  // O is read: the next unit may write it
+              tc_fence_before();
+              mbar_arrive(bar(kOutFree + t));
+            }
           }
-        }
-      }
-      const float shift = m == -INFINITY ? 0.f : -m;
-      // P in two parts, of 96 and 32 keys: the product with the first runs
-      // while the second is formed; the sums wait until both are on their way
-      const uint64_t mult2 = pack2(mult, mult), shift2 = pack2(shift, shift);
 #pragma unroll
-      for (int part = 0; part < 2; ++part) {
-#pragma unroll
-        for (int q = part ? 3 : 0; q < (part ? 4 : 3); ++q) {
-          uint32_t w[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float x, y;
-            unpack2(fma2(pack2(__uint_as_float(s[q][2 * i]), __uint_as_float(s[q][2 * i + 1])), mult2, shift2), x, y);
-            x = ex2(x), y = ex2(y);
-            s[q][2 * i] = __float_as_uint(x), s[q][2 * i + 1] = __float_as_uint(y);
-            w[i] = pack16<kP>(x, y);
-          }
-          tmem_st16(scores + 16 * q, w);
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(bar(kProbs + 2 * part + t));
-      }
-      uint64_t l4[4] = {0, 0, 0, 0};
-#pragma unroll
-      for (int i = 0; i < 32; i += 2)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) l4[q] = add2(l4[q], pack2(__uint_as_float(s[q][i]), __uint_as_float(s[q][i + 1])));
-      float lo, hi;
-      unpack2(add2(add2(l4[0], l4[1]), add2(l4[2], l4[3])), lo, hi);
-      l += lo + hi;
-    }
-    // (rows without a key wait for their queries only, whose place is used below)
-    if (ok) ok = mbar_wait(bar(nt > 0 ? kOut + t : kQueries + t), 0u, abort_flag, kErrEpilogue, a.err);
-    tc_fence_after();
-    if (ok) {
-      const float inv = l > 0.f ? (k8 ? a.cache.v_scale[hk] : 1.f) / l : 0.f;
-      // through the warp's rows of the queries' tile, which no product reads
-      // any more, so that whole rows are written
-#pragma unroll
-      for (int c = 0; c < D; c += 32) {
-        uint32_t o[32];
-        if (nt > 0) {
-          tmem_ld32(out + c, o);
-          tmem_wait_ld();
-          tie(o);
+          for (int i = 0; i < 16; ++i)
+            x[(c + 2 * i) / 8][i & 3] = l > 0.f ? pack16<kB>(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv) : 0;
         }
 #pragma unroll
-        for (int i = 0; i < 32; i += 8) {
-          float f[8];
+        for (int bit = 1; bit < 8; bit <<= 1)
 #pragma unroll
-          for (int k = 0; k < 8; ++k) f[k] = l > 0.f ? __uint_as_float(o[i + k]) * inv : 0.f;
-          sts128(base + t * kBytes + chunk_at(tid & 127, (c + i) / 8), pack16<kB>(f[0], f[1]), pack16<kB>(f[2], f[3]),
-                 pack16<kB>(f[4], f[5]), pack16<kB>(f[6], f[7]));
+          for (int i = 0; i < 8; ++i)
+            if (!(i & bit)) {
+              const bool upper = lane & bit;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? x[i][k] : x[i | bit][k], bit);
+                x[i][k] = upper ? got : x[i][k];
+                x[i | bit][k] = upper ? x[i | bit][k] : got;
+              }
+            }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int place = __shfl_sync(0xffffffffu, to, (lane & 24) + i);
+          if (place >= 0)
+            *reinterpret_cast<uint4*>(a.out + (size_t)place * D + d0 + (lane & 7) * 8) = make_uint4(x[i][0], x[i][1], x[i][2], x[i][3]);
         }
       }
-      __syncwarp();
-      constexpr int kChunks = D / 8, kAtOnce = 32 / kChunks;  // rows per store of the warp
-      const int c = lane % kChunks, r1 = lane / kChunks;
-#pragma unroll 4
-      for (int r = r1; r < 32; r += kAtOnce) {
-        const int to = __shfl_sync(0xffffffffu, live ? (first + token) * a.heads + head : -1, r);
-        const uint4 v = lds128(base + t * kBytes + chunk_at((tid & 96) + r, c));
-        if (to >= 0) *reinterpret_cast<uint4*>(a.out + (size_t)to * D + c * 8) = v;
-      }
-      if (live && a.lse) a.lse[(size_t)(first + token) * a.heads + head] = l > 0.f ? m * kLn2 + logf(l) : -INFINITY;
+      if (live && a.lse) a.lse[to] = l > 0.f ? m * kLn2 + logf(l) : -INFINITY;
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    if (warp >= 10 && warp < 14) {
-      // the queries: a thread copies chunk c of every kStride-th row
-      constexpr int kChunks = D / 8, kStride = 128 / kChunks;
-      const int u = tid - 320, c = u % kChunks;
-      const int step_token = kStride / p.group, step_head = kStride % p.group;
-      int row = row0 + u / kChunks;
-      int token = row / p.group, head = row % p.group;
-#pragma unroll 1
-      for (int t = 0; t < 2; ++t) {
-#pragma unroll 4
-        for (int r = u / kChunks; r < kTile; r += kStride) {
-          const bool valid = row < rows;
-          const uint16_t* src = a.q + (valid ? (size_t)(first + token) * a.ldq + (size_t)(hk * p.group + head) * D + c * 8 : 0);
-          const uint32_t dst = base + t * kBytes + chunk_at(r, c);
-          if (kB && k8) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (valid) v = *reinterpret_cast<const uint4*>(src);
-            const float2 f[4] = {unpack16<true>(v.x), unpack16<true>(v.y), unpack16<true>(v.z), unpack16<true>(v.w)};
-            float top = 0.f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) top = fmaxf(top, fmaxf(fabsf(f[k].x), fabsf(f[k].y)));
-#pragma unroll
-            for (int o = kChunks / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const int e = top > 0.f ? ilogbf(top) : 0;  // |q| 2^-e < 2
-            uint32_t w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) w[k] = pack16<false>(scalbnf(f[k].x, -e), scalbnf(f[k].y, -e));
-            sts128(dst, w[0], w[1], w[2], w[3]);
-            if (c == 0) ctl.power[t * kTile + r] = scalbnf(1.f, e);
-          } else {
-            cp16(dst, src, valid);
-          }
-          row += kStride;
-          token += step_token;
-          head += step_head;
-          if (head >= p.group) {
-            head -= p.group;
-            ++token;
-          }
-        }
-        cp_commit();
-      }
-      cp_wait<1>();
-      fence_async_shared();
-      mbar_arrive(bar(kQueries));
-      cp_wait<0>();
-      fence_async_shared();
-      mbar_arrive(bar(kQueries + 1));
-    }
     if (warp < 12) {
-      const int u = tid - 256;
-      constexpr int kChunks = D / 8;  // 16-byte chunks of a row
-      bool ok = true;
+      const int v = tid - 256;
       const int shift = a.cache.page_shift, mask = (1 << shift) - 1;
-      RingPos pos;
-      pos.init(0, kSlots);
-      int i = 0;
+      bool ok = true;
+      int count = 0;  // tiles so far
+      uint32_t met = 0;
+      auto slot_of = [&]() { return count % kSlots; };
       auto wait_slot = [&]() {
-        return i < kSlots || mbar_wait(bar(kEmpty + pos.slot), pos.phase ^ 1u, abort_flag, kErrProducer, a.err);
+        return count < kSlots || warp_wait(kEmpty + count % kSlots, (uint32_t)(count / kSlots - 1) & 1u, kErrProducer);
       };
-      // the first row, in the cache seen as rows of D values, of this head's
-      // place of key `key` of the sequence
-      auto row_of = [&](int key) {
-        return (((unsigned long long)page_of(a, b, key >> shift) * a.cache.kv_heads + hk) << shift) + (key & mask);
+      auto meet = [&]() {  // of the four copying warps, bounded
+        mbar_arrive(bar(kCopiers));
+        ok = warp_wait(kCopiers, met, kErrProducer) && ok;
+        met ^= 1u;
       };
-      if (!k8) {
-        // tiles that lie inside the sequence: tile copies of the pages' rows,
-        // a lane of the first warp for each page and panel
-        const int whole = p.tiled ? min(most, len / kTile) : 0;
-        if (warp == 8) {
-          const int box = min(1 << shift, kTile), boxes = kTile / box;
-          const int panel = lane / boxes, part = lane % boxes;
-          unsigned long long row = 0;
-          for (; i < 2 * whole && ok; ++i) {
-            const int j = i >> 1;
-            if (!(i & 1)) row = row_of(j * kTile + part * box);
-            if (!(ok = wait_slot())) break;
-            const uint32_t full = bar(kFull + pos.slot);
-            if (lane == 0) mbar_expect_tx(full, kBytes);
-            __syncwarp();
-            if (lane < D / 64 * boxes)
-              tma_load_2d(base + (2 + pos.slot) * kBytes + panel * kPanel + part * box * 128, i & 1 ? &map_v : &map_k, panel * 64,
-                          (int)row, full);
-            pos.step(1, kSlots);
-          }
-          ok = __all_sync(0xffffffffu, ok);
-        } else {
-          i = 2 * whole;
-          pos.init(i, kSlots);
-        }
-        // the ragged last tile: 16 bytes at a time, rows beyond the sequence
-        // as zeros
-        if (whole < most) {
-          loaders_sync();  // the ring's slots are within one round of `pos`
-          const int r0 = u / kChunks, c = u % kChunks;
-          constexpr int kStride = 128 / kChunks;
-          const int first_tile = i;
-          int pair[2] = {0, 0};  // slots of the tile's keys and values
-          for (; i < 2 * most && ok; ++i) {
-            const uint8_t* src = static_cast<const uint8_t*>(i & 1 ? a.cache.v : a.cache.k);
-            const unsigned long long group = row_of_or_0(row_of, (i >> 1) * kTile + 16 * (lane & 7), len);
-            ok = wait_slot();
-            const uint32_t dst = base + (2 + pos.slot) * kBytes + chunk_at(r0, c);
-#pragma unroll 4
-            for (int x = 0; x < kTile / kStride; ++x) {
-              const int r = r0 + x * kStride;
-              const unsigned long long row = __shfl_sync(0xffffffffu, group, r >> 4) + (r & 15);
-              const bool valid = ok && (i >> 1) * kTile + r < len;
-              cp16(dst + x * kStride * 128, valid ? src + row * (2 * D) + c * 16 : src, valid);
+      for (int u = 0; ok; ++u) {
+        if (!next_unit(u, kErrProducer, true)) break;
+        const int len = unit.len;
+        // the first row, in the cache seen as rows of D values, of this head's
+        // place of key `key` of the sequence
+        auto row_of = [&](int key) {
+          return (((unsigned long long)page_of(a, unit.b, key >> shift) * a.cache.kv_heads + unit.head) << shift) + (key & mask);
+        };
+        if (!k8) {
+          // tiles that lie inside the sequence: tile copies of the pages' rows,
+          // a lane for each page and panel. Small pages' copies (16 of them
+          // for 16 tokens) are shared among the four warps: a warp issues its
+          // lanes' copies one after another.
+          const int whole = p.tiled ? min(most, len / kTile) : 0;
+          const int end = count + 2 * whole;
+          const int box = min(1 << shift, kTile), boxes = kTile / box, copies = D / 64 * boxes;
+          const int sharing = copies > 4 ? 4 : 1, each = copies / sharing;
+          if (warp - 8 < sharing) {
+            const int mine = (warp - 8) * each + lane, panel = mine / boxes, part = mine % boxes;
+            // the page of the next tile is looked up while this one is waited for
+            unsigned long long row = 0, ahead = whole > 0 ? row_of(part * box) : 0;
+            for (int j = 0; count < end && ok; ++count) {
+              const bool values = (end - count) & 1;
+              if (!values) {
+                row = ahead;
+                if (++j < whole) ahead = row_of(j * kTile + part * box);
+              }
+              if (!(ok = wait_slot())) break;
+              const uint32_t full = bar(kFull + slot_of());
+              if (mine == 0) mbar_expect_tx(full, kBytes);
+              __syncwarp();
+              if (lane < each)
+                tma_load_2d(ring + slot_of() * kBytes + panel * kPanel + part * box * 128, values ? &map_v : &map_k, panel * 64,
+                            (int)row, full);
             }
-            cp_commit();
-            pair[(i - first_tile) & 1] = pos.slot;
-            pos.step(1, kSlots);
-            if ((i - first_tile) & 1) {  // keys and values are on their way: announce the keys, then both
+          }
+          count = end;
+          // the ragged last tile (every tile where there are no maps): 16
+          // bytes at a time, rows beyond the sequence as zeros
+          if (whole < most) {
+            meet();  // the first warp has come as far: a slot's phase is known
+            const int r0 = v / kChunks, c = v % kChunks;
+            constexpr int kStride = 128 / kChunks;
+            for (int j = whole; j < most && ok; ++j) {
+              const unsigned long long group = row_of_or_0(row_of, j * kTile + 16 * (lane & 7), len);
+              int slots[2];
+#pragma unroll 1
+              for (int kv = 0; kv < 2 && ok; ++kv) {
+                if (!(ok = wait_slot())) break;
+                const uint8_t* src = static_cast<const uint8_t*>(kv ? a.cache.v : a.cache.k);
+                const uint32_t dst = ring + slot_of() * kBytes + chunk_at(r0, c);
+#pragma unroll 4
+                for (int x = 0; x < kTile / kStride; ++x) {
+                  const int r = r0 + x * kStride;
+                  const unsigned long long row = __shfl_sync(0xffffffffu, group, r >> 4) + (r & 15);
+                  const bool valid = j * kTile + r < len;
+                  cp16(dst + x * kStride * 128, valid ? src + row * (2 * D) + c * 16 : src, valid);
+                }
+                cp_commit();
+                slots[kv] = slot_of();
+                ++count;
+              }
+              // the keys, then the values
               cp_wait<1>();
               fence_async_shared();
-              loaders_sync();
-              if (u == 0 && ok) mbar_arrive(bar(kFull + pair[0]));
+              meet();
+              if (v == 0 && ok) mbar_arrive(bar(kFull + slots[0]));
               cp_wait<0>();
               fence_async_shared();
-              loaders_sync();
-              if (u == 0 && ok) mbar_arrive(bar(kFull + pair[1]));
+              meet();
+              if (v == 0 && ok) mbar_arrive(bar(kFull + slots[1]));
             }
           }
-        }
-      } else {
-        // A thread copies one 16-code piece c of the rows r0 + x * kStride of
-        // a tile's eight groups of 16 rows (a group lies in one page): the
-        // group is a constant of x and of the warp.
-        constexpr int kPieces = D / 16, kStride = 128 / kPieces, kLoads = kTile / kStride;
-        const int r0 = u / kPieces, c = u % kPieces;
-        unsigned long long group = 0;
-        for (; i < 2 * most; ++i) {
-          const int j = i >> 1;
-          if (!(i & 1)) group = row_of_or_0(row_of, j * kTile + 16 * (lane & 7), len) * D;
-          const uint8_t* src = static_cast<const uint8_t*>(i & 1 ? a.cache.v : a.cache.k) + (r0 & 15) * D + c * 16;
-          const bool inside = (j + 1) * kTile <= len;
-          uint4 v[kLoads];
+        } else {
+          // A thread copies one 16-code piece c of the rows r0 + x * kStride of
+          // a tile's eight groups of 16 rows (a group lies in one page): the
+          // group is a constant of x and of the warp.
+          constexpr int kPieces = D / 16, kStride = 128 / kPieces, kLoads = kTile / kStride;
+          const int r0 = v / kPieces, c = v % kPieces;
+          unsigned long long group = 0;
+          for (int i = 0; i < 2 * most; ++i, ++count) {
+            const int j = i >> 1;
+            if (!(i & 1)) group = row_of_or_0(row_of, j * kTile + 16 * (lane & 7), len) * D;
+            const uint8_t* src = static_cast<const uint8_t*>(i & 1 ? a.cache.v : a.cache.k) + (r0 & 15) * D + c * 16;
+            const bool inside = (j + 1) * kTile <= len;
+            uint4 x4[kLoads];
 #pragma unroll
-          for (int x = 0; x < kLoads; ++x) {
-            const uint8_t* from = src + __shfl_sync(0xffffffffu, group, x * (kStride / 16) + (r0 >> 4));
-            v[x] = make_uint4(0, 0, 0, 0);
-            if (inside || j * kTile + r0 + x * kStride < len) v[x] = ldg_stream(reinterpret_cast<const uint4*>(from));
-          }
-          if (!(ok = wait_slot())) break;
-          const uint32_t dst = base + (2 + pos.slot) * kBytes;
-          const uint32_t lo_at = dst + chunk_at(r0, 2 * c), hi_at = dst + chunk_at(r0, 2 * c + 1);
+            for (int x = 0; x < kLoads; ++x) {
+              const uint8_t* from = src + __shfl_sync(0xffffffffu, group, x * (kStride / 16) + (r0 >> 4));
+              x4[x] = make_uint4(0, 0, 0, 0);
+              if (inside || j * kTile + r0 + x * kStride < len) x4[x] = ldg_stream(reinterpret_cast<const uint4*>(from));
+            }
+            if (!(ok = wait_slot())) break;
+            const uint32_t dst = ring + slot_of() * kBytes;
+            const uint32_t lo_at = dst + chunk_at(r0, 2 * c), hi_at = dst + chunk_at(r0, 2 * c + 1);
 #pragma unroll
-          for (int x = 0; x < kLoads; ++x) {  // kStride is a multiple of 8: the swizzle stays
-            const uint4 lo = widen(v[x].x, v[x].y), hi = widen(v[x].z, v[x].w);
-            sts128(lo_at + x * kStride * 128, lo.x, lo.y, lo.z, lo.w);
-            sts128(hi_at + x * kStride * 128, hi.x, hi.y, hi.z, hi.w);
+            for (int x = 0; x < kLoads; ++x) {  // kStride is a multiple of 8: the swizzle stays
+              const uint4 lo = widen(x4[x].x, x4[x].y), hi = widen(x4[x].z, x4[x].w);
+              sts128(lo_at + x * kStride * 128, lo.x, lo.y, lo.z, lo.w);
+              sts128(hi_at + x * kStride * 128, hi.x, hi.y, hi.z, hi.w);
+            }
+            fence_async_shared();
+            mbar_arrive(bar(kFull + slot_of()));
           }
-          fence_async_shared();
-          mbar_arrive(bar(kFull + pos.slot));
-          pos.step(1, kSlots);
         }
       }
       cp_wait<0>();
-    } else if (warp >= 14 && elect_one()) {
+    } else if (warp < 14) {
+      // Warp 12 takes units from the queue, numbered from the last rows of the
+      // last sequence on, a key/value head after another. It walks back over
+      // the sequences, 32 at a time: v units of this lane's sequence, `upto`
+      // of the group's up to it, `before` of the groups before.
+      int first = 0, fresh = 0, len = 0, v = 0, upto = 0, group = 0, before = 0, total = 0;
+      auto look = [&]() {
+        const int b = 32 * group + lane;
+        first = fresh = len = v = 0;
+        if (b < a.batch) {
+          const int s0 = a.starts[b], s1 = a.starts[b + 1], n0 = a.lens[b];
+          first = checked(a, s0, a.rows);
+          fresh = checked(a, s1, a.rows) - first;
+          if (fresh < 0) {
+            atomicOr(a.err, kErrRange);
+            fresh = 0;
+          }
+          len = checked(a, n0, (int)min((long long)a.max_pages << a.cache.page_shift, 0x7fffffffll));
+          v = (int)(((long long)fresh * p.group + 2 * kTile - 1) / (2 * kTile));
+        }
+        upto = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int x = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += x;
+        }
+      };
+      const int groups = (a.batch + 31) / 32;
+      if (warp == 12) {
+        for (group = 0; group < groups; ++group) {
+          before = total;
+          look();
+          total += __shfl_sync(0xffffffffu, upto, 31);
+        }
+        --group;
+      }
+      const int w = tid - 384, c = w % kChunks;
+      constexpr int kStride = 64 / kChunks;
+      const int step_head = kStride % p.group;
+      const long long step = (long long)(kStride / p.group) * a.ldq + step_head * D, wrap = a.ldq - (long long)p.group * D;
+      bool ok = true;
+      for (int u = 0; ok; ++u) {
+        if (warp == 12) {
+          if (u >= 2 && !(ok = warp_wait(kUnitFree + (u & 1), (uint32_t)(u / 2 - 1) & 1u, kErrProducer))) break;
+          int i = 0;
+          if (lane == 0) i = atomicAdd(p.queue, 1);
+          i = __shfl_sync(0xffffffffu, i, 0);
+          const int want = total - 1 - i / a.cache.kv_heads;
+          Unit& to = ctl.unit[u & 1];
+          if (want >= 0) {
+            while (want < before) {
+              --group;
+              look();
+              before -= __shfl_sync(0xffffffffu, upto, 31);
+            }
+            const int lo = before + upto - v;
+            if (lo <= want && want < lo + v) {
+              const int row0 = (want - lo) * (2 * kTile), rows = fresh * p.group;  // rows: at most 2^30
+              to = {32 * group + lane, first, fresh, len, row0, i % a.cache.kv_heads, {0, 0}, 1};
+#pragma unroll
+              for (int t = 0; t < 2; ++t) {
+                const int from = row0 + t * kTile, past = min(from + kTile, rows);
+                const int last = from < past ? len - fresh + (past - 1) / p.group : -1;
+                to.n[t] = last < 0 ? 0 : last / kTile + 1;
+              }
+            }
+          } else if (lane == 0) {
+            to.valid = 0;
+            // the last block to come here leaves the queue zero
+            __threadfence();
+            if (atomicAdd(p.queue + 1, 1) == (int)gridDim.x - 1) p.queue[0] = p.queue[1] = 0;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kUnit + (u & 1)));
+        }
+        if (!next_unit(u, kErrProducer, warp == 13)) break;
+        if (p.q_tiled) {
+          // whole tokens to a tile: a tile copy of [tokens][heads][D]; rows
+          // beyond the sequence's are of no use and do no harm
+          if (warp == 13) {
+#pragma unroll 1
+            for (int t = 0; t < 2 && ok; ++t) {
+              if (u > 0 && !(ok = warp_wait(kQueriesFree + t, (uint32_t)(u - 1) & 1u, kErrProducer))) break;
+              if (lane == 0) {
+                mbar_expect_tx(bar(kQueries + t), kBytes);
+#pragma unroll
+                for (int d = 0; d < D / 64; ++d)
+                  tma_load_3d(base + t * kBytes + d * kPanel, &map_q, d * 64, unit.head * p.group,
+                              unit.first + (unit.row0 + t * kTile) / p.group, bar(kQueries + t));
+              }
+              __syncwarp();
+            }
+          }
+          continue;
+        }
+        // else a thread copies chunk c of every kStride-th row
+        int row = unit.row0 + w / kChunks, head = row % p.group;
+        const uint16_t* src =
+            a.q + (size_t)(unit.first + row / p.group) * a.ldq + (size_t)(unit.head * p.group + head) * D + c * 8;
+#pragma unroll 1
+        for (int t = 0; t < 2 && ok; ++t) {
+          if (u > 0 && !(ok = warp_wait(kQueriesFree + t, (uint32_t)(u - 1) & 1u, kErrProducer))) break;
+#pragma unroll 4
+          for (int r = w / kChunks; r < kTile; r += kStride) {
+            const bool valid = row < unit.fresh * p.group;
+            const uint32_t dst = base + t * kBytes + chunk_at(r, c);
+            if (kB && k8) {
+              uint4 x = make_uint4(0, 0, 0, 0);
+              if (valid) x = *reinterpret_cast<const uint4*>(src);
+              const float2 f[4] = {unpack16<true>(x.x), unpack16<true>(x.y), unpack16<true>(x.z), unpack16<true>(x.w)};
+              float top = 0.f;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) top = fmaxf(top, fmaxf(fabsf(f[k].x), fabsf(f[k].y)));
+#pragma unroll
+              for (int o = kChunks / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+              const int e = top > 0.f ? ilogbf(top) : 0;  // |q| 2^-e < 2
+              uint32_t y[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) y[k] = pack16<false>(scalbnf(f[k].x, -e), scalbnf(f[k].y, -e));
+              sts128(dst, y[0], y[1], y[2], y[3]);
+              if (c == 0) ctl.power[t * kTile + r] = scalbnf(1.f, e);
+            } else {
+              cp16(dst, valid ? src : a.q, valid);
+            }
+            row += kStride;
+            src += step;
+            head += step_head;
+            if (head >= p.group) {
+              head -= p.group;
+              src += wrap;
+            }
+          }
+          cp_commit();
+          if (t == 1) {
+            cp_wait<1>();
+            fence_async_shared();
+            mbar_arrive(bar(kQueries));
+            cp_wait<0>();
+            fence_async_shared();
+            mbar_arrive(bar(kQueries + 1));
+          }
+        }
+        __syncwarp();
+      }
+      cp_wait<0>();
+    } else if (elect_one()) {
       // one warp per row tile, one thread of it
       constexpr uint32_t kDescHi = (uint32_t)(1024 >> 4) | (1u << 14) | (2u << 29);  // the upper half of both descriptors
-      const int t = warp - 14, nt = t ? n[1] : n[0];
+      const int t = warp - 14;
       const uint32_t scores = tmem + t * kTile, out = tmem + 256 + t * D;
       const uint32_t idesc_s = f16_idesc(kTile, kTile, kP) | (p.negate << 13);
       const uint32_t idesc_o = f16_idesc(kTile, D, kP) | (1u << 16);  // B with the dimensions innermost
       const uint32_t q_lo = (((base + t * kBytes) & 0x3FFFFu) >> 4) | (1u << 16);  // K-major
-      const uint32_t k_lo = (((base + 2 * kBytes) & 0x3FFFFu) >> 4) | (1u << 16);
-      const uint32_t v_lo = (((base + 2 * kBytes) & 0x3FFFFu) >> 4) | ((uint32_t)(kPanel >> 4) << 16);  // MN-major
+      const uint32_t k_lo = ((ring & 0x3FFFFu) >> 4) | (1u << 16);
+      const uint32_t v_lo = ((ring & 0x3FFFFu) >> 4) | ((uint32_t)(kPanel >> 4) << 16);  // MN-major
       bool ok = true;
       auto wait = [&](int i, uint32_t phase) {
         ok = mbar_wait(bar(i), phase, abort_flag, kErrMma, a.err);
         return ok;
       };
-      auto score = [&](int slot) {
+      auto score = [&](int slot, bool last) {
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t off = (uint32_t)((k >> 2) * kPanel + (k & 3) * 32) >> 4;
@@ -624,6 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
         }
         tc_commit(bar(kScores + t));
         tc_commit(bar(kEmpty + slot));
+        if (last) tc_commit(bar(kQueriesFree + t));
       };
       auto value = [&](int slot, int part, bool add) {  // 96 or 32 keys
 #pragma unroll
@@ -632,38 +770,49 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
       };
       RingPos pos;  // of the next tile
       pos.init(0, kSlots);
-      if (most > 0 && (nt == 0 || wait(kQueries + t, 0)) && wait(kFull, 0)) {
+      uint32_t prob_phase = 0, free_phase = 1, turns = 0;
+      for (int u = 0; ok; ++u) {
+        if (!wait(kUnit + (u & 1), (uint32_t)(u >> 1) & 1u) || !read_unit(u)) break;
+        mbar_arrive(bar(kUnitFree + (u & 1)));
+        const int nt = t ? unit.n[1] : unit.n[0];
+        if (!wait(kQueries + t, (uint32_t)u & 1u)) break;
+        if (nt == 0) mbar_arrive(bar(kQueriesFree + t));
+        if (most == 0) continue;
+        if (!wait(kFull + pos.slot, pos.phase)) break;
         tc_fence_after();
-        if (nt > 0) score(0); else mbar_arrive(bar(kEmpty));
+        if (nt > 0) score(pos.slot, nt == 1); else mbar_arrive(bar(kEmpty + pos.slot));
         pos.step(1, kSlots);
-      }
-      for (int j = 0; j < most && ok; ++j) {
-        const int sv = pos.slot;
-        const uint32_t pv = pos.phase;
-        pos.step(1, kSlots);
-        const int sk = pos.slot;
-        const uint32_t pk = pos.phase;
-        pos.step(1, kSlots);
-        const bool more = j + 1 < nt;
-        // the tiles take turns, so that one's products run while the other's
-        // softmax does: in step they would wait for the tensor cores together
-        if (!wait(kFull + sv, pv)) break;
-        if (j + 1 < most && !wait(kFull + sk, pk)) break;
-        if (j < nt && !wait(kProbs + t, (uint32_t)j & 1u)) break;
-        if ((t || j) && !wait(kTurn + t, (uint32_t)(t ? j : j - 1) & 1u)) break;
-        if (j < nt) {
-          tc_fence_after();
-          value(sv, 0, j > 0);
-          if (!wait(kProbs + 2 + t, (uint32_t)j & 1u)) break;
-          tc_fence_after();
-          value(sv, 1, true);
-          tc_commit(bar(kEmpty + sv));
-          if (more) score(sk); else tc_commit(bar(kOut + t));
-        } else {
-          mbar_arrive(bar(kEmpty + sv));  // a tile that only the other rows need
+        for (int j = 0; j < most; ++j, ++turns) {
+          const int sv = pos.slot;
+          const uint32_t pv = pos.phase;
+          pos.step(1, kSlots);
+          const int sk = pos.slot;
+          const uint32_t pk = pos.phase;
+          if (j + 1 < most) pos.step(1, kSlots);
+          const bool more = j + 1 < nt;
+          // the tiles take turns, so that one's products run while the other's
+          // softmax does: in step they would wait for the tensor cores together
+          if (!wait(kFull + sv, pv)) break;
+          if (j + 1 < most && !wait(kFull + sk, pk)) break;
+          if (j == 0 && nt > 0 && !wait(kOutFree + t, free_phase)) break;  // O of the unit before
+          if ((t || turns) && !wait(kTurn + t, (t ? turns : turns - 1) & 1u)) break;
+          if (j < nt && !wait(kProbs + t, prob_phase)) break;
+          if (j < nt) {
+            tc_fence_after();
+            value(sv, 0, j > 0);
+            if (!wait(kProbs + 2 + t, prob_phase)) break;
+            prob_phase ^= 1u;
+            tc_fence_after();
+            value(sv, 1, true);
+            tc_commit(bar(kEmpty + sv));
+            if (more) score(sk, j + 2 == nt); else tc_commit(bar(kOut + t));
+          } else {
+            mbar_arrive(bar(kEmpty + sv));  // a tile that only the other rows need
+          }
+          mbar_arrive(bar(kTurn + 1 - t));
+          if (!more && j + 1 < most) mbar_arrive(bar(kEmpty + sk));
         }
-        mbar_arrive(bar(kTurn + 1 - t));
-        if (!more && j + 1 < most) mbar_arrive(bar(kEmpty + sk));
+        if (nt > 0) free_phase ^= 1u;
       }
       if (!ok) {
         // no product may run past the release of the tensor memory
@@ -684,7 +833,7 @@ template <bool kB, bool k8, int D>
 cudaError_t launch(PromptArgs p, unsigned blocks, cudaStream_t stream) {
   // the caches as rows of D values, copied in panels of 64 dimensions by up to
   // 128 rows of a page (row numbers are 32-bit coordinates)
-  CUtensorMap map_k = {}, map_v = {};
+  CUtensorMap map_k = {}, map_v = {}, map_q = {};
   const long long rows = ((long long)p.a.cache.pages * p.a.cache.kv_heads) << p.a.cache.page_shift;
   p.tiled = !k8 && rows <= 0x7fffffff;
   if (p.tiled) {
@@ -694,15 +843,20 @@ cudaError_t launch(PromptArgs p, unsigned blocks, cudaStream_t stream) {
         !encode_tensor_map(&map_v, p.a.cache.v, dt, 2, D, (uint64_t)rows, 64, box, CU_TENSOR_MAP_SWIZZLE_128B))
       return cudaErrorInvalidValue;
   }
+  // the queries as [tokens][heads][D], where a tile of 128 rows is whole
+  // tokens of a key/value head's group
+  p.q_tiled = !(kB && k8) && kTile % p.group == 0;
+  if (p.q_tiled && !encode_query_map(&map_q, p.a.q, kB, D, p.a.heads, p.a.rows, p.a.ldq, p.group)) return cudaErrorInvalidValue;
   auto kern = attn_prompt_kernel<kB, k8, D>;
   cudaError_t e = set_max_smem_once(reinterpret_cast<const void*>(kern), kSmem<D>);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(blocks), dim3(kThreads), kSmem<D>, stream, p, map_k, map_v);
+  return launch_pdl(kern, dim3(blocks), dim3(kThreads), kSmem<D>, stream, p, map_k, map_v, map_q);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_prompt(const AttnArgs& args, int head_dim, bool bf16, bool e4m3, cudaStream_t stream) {
+cudaError_t launch_attn_prompt(const AttnArgs& args, int head_dim, bool bf16, bool e4m3, void* workspace, int sms,
+                               cudaStream_t stream) {
   if (args.rows == 0 || args.batch == 0) return cudaSuccess;
   PromptArgs p;
   p.a = args;
@@ -714,19 +868,20 @@ cudaError_t launch_attn_prompt(const AttnArgs& args, int head_dim, bool bf16, bo
   // small to tell from it
   p.mult = fmaxf(fabsf(args.scale) * kLog2e, 1e-37f);
   p.negate = args.scale < 0.f;
-  // at most: whole units of all rows, and a ragged one per sequence
-  const long long units = (long long)args.rows * p.group / (2 * kTile) + args.batch;
-  const long long blocks = units * args.cache.kv_heads;
-  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+  p.queue = static_cast<int*>(workspace);
+  // a block per SM, or as many as there can be units: whole ones of all rows,
+  // and a ragged one per sequence
+  const long long units = ((long long)args.rows * p.group / (2 * kTile) + args.batch) * args.cache.kv_heads;
+  const unsigned blocks = units < sms ? (unsigned)units : (unsigned)sms;
   switch ((bf16 ? 4 : 0) | (e4m3 ? 2 : 0) | (head_dim == 128 ? 1 : 0)) {
-    case 0: return launch<false, false, 64>(p, (unsigned)blocks, stream);
-    case 1: return launch<false, false, 128>(p, (unsigned)blocks, stream);
-    case 2: return launch<false, true, 64>(p, (unsigned)blocks, stream);
-    case 3: return launch<false, true, 128>(p, (unsigned)blocks, stream);
-    case 4: return launch<true, false, 64>(p, (unsigned)blocks, stream);
-    case 5: return launch<true, false, 128>(p, (unsigned)blocks, stream);
-    case 6: return launch<true, true, 64>(p, (unsigned)blocks, stream);
-    default: return launch<true, true, 128>(p, (unsigned)blocks, stream);
+    case 0: return launch<false, false, 64>(p, blocks, stream);
+    case 1: return launch<false, false, 128>(p, blocks, stream);
+    case 2: return launch<false, true, 64>(p, blocks, stream);
+    case 3: return launch<false, true, 128>(p, blocks, stream);
+    case 4: return launch<true, false, 64>(p, blocks, stream);
+    case 5: return launch<true, false, 128>(p, blocks, stream);
+    case 6: return launch<true, true, 64>(p, blocks, stream);
+    default: return launch<true, true, 128>(p, blocks, stream);
   }
 }
 

@@ -105,6 +105,9 @@ bool cached_tensor_map(CUtensorMap* out, const void* ptr, CUtensorMapDataType dt
 bool encode_tensor_map(CUtensorMap* out, const void* ptr, CUtensorMapDataType dt, int esize,
                        uint64_t dims0, uint64_t dims1, uint32_t box0, uint32_t box1,
                        CUtensorMapSwizzle swizzle);
+// 3-D tensor map of queries [tokens][heads][dim] (row stride ld) with box
+// [128 / group tokens][group heads][64] and the 128-byte swizzle.
+bool encode_query_map(CUtensorMap* out, const void* ptr, bool bf16, int dim, int heads, int tokens, long long ld, int group);
 // 3-D tensor map of the packed weights as [N/16 strips][K/64 atoms x 4 rows]
 // [32 words] with the 128-byte swizzle; a box is `sa` atoms of 8 strips (128
 // columns). From the same cache.
@@ -142,8 +145,10 @@ cudaError_t launch_rope_append(const uint16_t* qkv, long long ld, const float* t
                                bool interleaved, cudaStream_t stream);
 // Attention over the paged cache (AttnArgs: layer.cuh).
 struct AttnArgs;
-// Causal attention of prompts on the tensor cores.
-cudaError_t launch_attn_prompt(const AttnArgs& args, int head_dim, bool bf16, bool e4m3, cudaStream_t stream);
+// Causal attention of prompts on the tensor cores. The queue of its units is
+// the first two integers of the workspace's flag area (zero between calls).
+cudaError_t launch_attn_prompt(const AttnArgs& args, int head_dim, bool bf16, bool e4m3, void* workspace, int sms,
+                               cudaStream_t stream);
 // Decode attention, split over the cache's length: the workspace holds the
 // arrival counters (zero between calls) in its flag area, then the parts.
 size_t attn_decode_workspace_bytes(int head_dim, int sms);

@@ -192,8 +192,10 @@ int w4a16_attn_prompt(const uint16_t* q, int64_t q_stride, const void* k_cache, 
   if (!starts) return fail(W4A16_ERR_INVALID_ARG, "null pointer (starts)");
   if (!aligned(starts, 4)) return fail(W4A16_ERR_MISALIGNED, "alignment: starts needs 4 bytes");
   a.starts = starts;
-  return finish(launch_attn_prompt(a, head_dim, (flags & W4A16_BF16) != 0, (flags & W4A16_CACHE_E4M3) != 0,
-                                   (cudaStream_t)stream),
+  const int sms = device_sms();
+  if (int rc = check_workspace(workspace, workspace_bytes, attn_decode_workspace_bytes(head_dim, sms))) return rc;
+  return finish(launch_attn_prompt(a, head_dim, (flags & W4A16_BF16) != 0, (flags & W4A16_CACHE_E4M3) != 0, workspace,
+                                   sms, (cudaStream_t)stream),
                 "prompt attention launch");
 }
 

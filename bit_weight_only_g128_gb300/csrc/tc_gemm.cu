@@ -817,6 +817,18 @@ bool encode_tensor_map(CUtensorMap* out, const void* ptr, CUtensorMapDataType dt
   return encode_map(out, ptr, dt, esize, 2, {dims0, dims1, 1}, {box0, box1, 1}, swizzle);
 }
 
+bool encode_query_map(CUtensorMap* out, const void* ptr, bool bf16, int dim, int heads, int tokens, long long ld, int group) {
+  PFN_cuTensorMapEncodeTiled_v12000 encode = encode_fn();
+  if (!encode) return false;
+  const cuuint64_t gdims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)tokens};
+  const cuuint64_t strides[2] = {(cuuint64_t)dim * 2, (cuuint64_t)ld * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)(128 / group)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return encode(out, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(ptr),
+                gdims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool cached_tensor_map(CUtensorMap* out, const void* ptr, CUtensorMapDataType dt, int esize,
                        uint64_t dims0, uint64_t dims1, uint32_t box0, uint32_t box1,
                        CUtensorMapSwizzle swizzle) {
