@@ -330,7 +330,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
       const int row = unit.row0 + t * kTile + (tid & 127);
       const bool live = row < unit.fresh * p.group;
       const int token = live ? row / p.group : 0, head = unit.head * p.group + (live ? row % p.group : 0);
-      const int limit = live ? unit.len - unit.fresh + token + 1 : 0;  // keys this row sees
+      // keys this row sees (rows beyond the sequence mask nothing: what they
+      // give is not written)
+      const int limit = live ? unit.len - unit.fresh + token + 1 : 0x7fffffff;
+      const bool idle = __all_sync(0xffffffffu, !live);
       const int to = live ? (unit.first + token) * a.heads + head : -1;
       float mult = p.mult * (k8 ? a.cache.k_scale[unit.head] : 1.f);
       const float v_scale = k8 ? a.cache.v_scale[unit.head] : 1.f;
@@ -343,6 +346,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
       for (int j = 0; j < nt; ++j) {
         if (!(ok = warp_wait(kScores + t, score_phase, kErrEpilogue))) break;
         score_phase ^= 1u;
+        if (idle) {  // no row of this warp's: P is left as it is
+          mbar_arrive(bar(kProbs + t));
+          mbar_arrive(bar(kProbs + 2 + t));
+          continue;
+        }
         tc_fence_after();
         uint32_t s[4][32];
 #pragma unroll
