@@ -358,13 +358,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
         tmem_wait_ld();
 #pragma unroll
         for (int q = 0; q < 4; ++q) tie(s[q]);
+        // masked 32 keys at a time, where a row of the warp needs it
         const int seen = limit - j * kTile;
         if (!__all_sync(0xffffffffu, seen >= kTile)) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
+          for (int q = 0; q < 4; ++q) {
+            const int left = seen - 32 * q;
+            if (__all_sync(0xffffffffu, left >= 32)) continue;
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (32 * q + i >= seen) s[q][i] = 0xff800000u;
+              if (i >= left) s[q][i] = 0xff800000u;
+          }
         }
         float top4[4];
 #pragma unroll
@@ -382,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
           l *= f;
           if (j > 0) {
             // the scores' arrival says that the product with the last P is done
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D; c += 16) {
               uint32_t o[16];
               tmem_ld16(out + c, o);
@@ -433,32 +437,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
       }
       if (!ok) break;
       const float inv = l > 0.f ? v_scale / l : 0.f;
-      // 64 dimensions at a time, transposed among eight lanes (a lane's eight
-      // 16-byte chunks of its row become one chunk of eight rows), so that
-      // whole lines are written: a row per lane would be 32 lines per store
-#pragma unroll
-      for (int d0 = 0; d0 < D; d0 += 64) {
-        uint32_t x[8][4];
-#pragma unroll
-        for (int c = 0; c < 64; c += 32) {
-          uint32_t o[32];
-          if (nt > 0) {
-            tmem_ld32(out + d0 + c, o);
-            tmem_wait_ld();
-            tie(o);
-            if (d0 + c + 32 == D) {  // O is read: the next unit may write it
-              tc_fence_before();
-              mbar_arrive(bar(kOutFree + t));
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            x[(c + 2 * i) / 8][i & 3] = l > 0.f ? pack16<kB>(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv) : 0;
+      // 32 dimensions at a time, transposed among four lanes (a lane's four
+      // 16-byte chunks of its row become one chunk of four rows), so that
+      // whole sectors are written: a row per lane would be 32 lines per store.
+      // (Loops: code that runs once per unit is fetched anew every time.)
+#pragma unroll 1
+      for (int d0 = 0; d0 < D; d0 += 32) {
+        uint32_t o[32], x[4][4];
+        if (nt > 0) {
+          tmem_ld32(out + d0, o);
+          tmem_wait_ld();
+          tie(o);
         }
 #pragma unroll
-        for (int bit = 1; bit < 8; bit <<= 1)
+        for (int i = 0; i < 16; ++i)
+          x[i / 4][i & 3] = l > 0.f ? pack16<kB>(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv) : 0;
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
+        for (int bit = 1; bit < 4; bit <<= 1)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
             if (!(i & bit)) {
               const bool upper = lane & bit;
 #pragma unroll
@@ -469,11 +466,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
               }
             }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int place = __shfl_sync(0xffffffffu, to, (lane & 24) + i);
+        for (int i = 0; i < 4; ++i) {
+          const int place = __shfl_sync(0xffffffffu, to, (lane & 28) + i);
           if (place >= 0)
-            *reinterpret_cast<uint4*>(a.out + (size_t)place * D + d0 + (lane & 7) * 8) = make_uint4(x[i][0], x[i][1], x[i][2], x[i][3]);
+            *reinterpret_cast<uint4*>(a.out + (size_t)place * D + d0 + (lane & 3) * 8) = make_uint4(x[i][0], x[i][1], x[i][2], x[i][3]);
         }
+      }
+      if (nt > 0) {  // O is read: the next unit may write it
+        tc_fence_before();
+        mbar_arrive(bar(kOutFree + t));
       }
       if (live && a.lse) a.lse[to] = l > 0.f ? m * kLn2 + logf(l) : -INFINITY;
     }
