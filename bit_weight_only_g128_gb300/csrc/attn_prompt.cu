@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
       // 16-byte chunks of its row become one chunk of four rows), so that
       // whole sectors are written: a row per lane would be 32 lines per store.
       // (Loops: code that runs once per unit is fetched anew every time.)
-#pragma unroll 1
+#pragma unroll 2
       for (int d0 = 0; d0 < D; d0 += 32) {
         uint32_t o[32], x[4][4];
         if (nt > 0) {
