@@ -28,6 +28,9 @@
 //   warps 14, 15     tcgen05.mma of tile 0, 1: S from shared memory, O += P V
 //                    with P read from tensor memory, where it takes the place
 //                    of S
+// Where the units are fewer than the blocks, each is split over its keys into
+// parts of at least kLeast tiles; the parts' (m, l, O) go to the workspace as
+// fp32, and of each 32 rows the last part to arrive joins them, in their order.
 // Tensor memory: S0, S1 (128 columns each), O0, O1 (D each). Registers: 128 a
 // thread at launch, 192 for the softmax warps and 64 for the rest (256 x 192
 // + 256 x 64 = 512 x 128).
@@ -46,6 +49,7 @@ constexpr int kTile = 128;  // rows of a tile, and keys of a tile
 constexpr int kSlots = 5;
 constexpr int kPanel = kTile * 128;  // bytes of 64 dimensions of 128 rows
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kLeast = 4;    // key tiles of a part: as long as what a part costs beside them
 constexpr float kSlack = 8.f;  // log2 of how far a row's maximum may run ahead
 
 // barriers, [2]: of the row tiles, or of the two places of a unit's description
@@ -70,7 +74,9 @@ constexpr int kReaders = 8 + 4 + 1 + 2;  // warps that read a unit's description
 struct Unit {
   int b, first, fresh, len;  // sequence, its first row, rows, cached tokens
   int row0, head;            // first of the unit's rows (tokens x heads), key/value head
-  int n[2];                  // key tiles that the two row tiles need, up to their last row's position
+  int j0, n[2];              // first key tile, and key tiles that the two row tiles need from it on
+  int parts, slot, id;       // parts of the rows' keys, place of this one and number of the whole
+  int part;
   int valid;                 // 0: no unit is left
 };
 
@@ -88,6 +94,10 @@ template <int D>
 constexpr int kSmem = (2 + kSlots) * kTileBytes<D> + (int)sizeof(Control) + 1024;
 static_assert(kSmem<128> <= 227 * 1024, "one block's shared memory");
 
+// A warp's part: O as [D / 4][32 rows] of four, maxima, sums.
+template <int D>
+constexpr int kPartFloats = 32 * (D + 2);
+
 struct PromptArgs {
   AttnArgs a;
   int group;
@@ -96,6 +106,9 @@ struct PromptArgs {
   int tiled;        // the maps of the keys and values are there
   int q_tiled;      // the map of the queries is there
   int* queue;       // next unit, blocks that are through; zero between calls
+  int* arrived;     // [units split][8 warps] parts that are there; zero between calls
+  float* partial;   // [blocks][8 warps] of kPartFloats
+  int most_parts;
 };
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
@@ -334,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
       // give is not written)
       const int limit = live ? unit.len - unit.fresh + token + 1 : 0x7fffffff;
       const bool idle = __all_sync(0xffffffffu, !live);
-      const int to = live ? (unit.first + token) * a.heads + head : -1;
+      int to = live ? (unit.first + token) * a.heads + head : -1;
       float mult = p.mult * (k8 ? a.cache.k_scale[unit.head] : 1.f);
       const float v_scale = k8 ? a.cache.v_scale[unit.head] : 1.f;
       if (kB && k8) {
@@ -359,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
 #pragma unroll
         for (int q = 0; q < 4; ++q) tie(s[q]);
         // masked 32 keys at a time, where a row of the warp needs it
-        const int seen = limit - j * kTile;
+        const int seen = limit - (unit.j0 + j) * kTile;
         if (!__all_sync(0xffffffffu, seen >= kTile)) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
@@ -436,22 +449,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
         tc_fence_after();
       }
       if (!ok) break;
-      const float inv = l > 0.f ? v_scale / l : 0.f;
-      // 32 dimensions at a time, transposed among four lanes (a lane's four
+      // 32 dimensions of the rows, transposed among four lanes (a lane's four
       // 16-byte chunks of its row become one chunk of four rows), so that
-      // whole sectors are written: a row per lane would be 32 lines per store.
-      // (Loops: code that runs once per unit is fetched anew every time.)
-#pragma unroll 2
-      for (int d0 = 0; d0 < D; d0 += 32) {
-        uint32_t o[32], x[4][4];
-        if (nt > 0) {
-          tmem_ld32(out + d0, o);
-          tmem_wait_ld();
-          tie(o);
-        }
+      // whole sectors are written: a row per lane would be 32 lines per store
+      auto write = [&](int d0, const float (&v)[32]) {
+        uint32_t x[4][4];
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          x[i / 4][i & 3] = l > 0.f ? pack16<kB>(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv) : 0;
+        for (int i = 0; i < 16; ++i) x[i / 4][i & 3] = pack16<kB>(v[2 * i], v[2 * i + 1]);
 #pragma unroll
         for (int bit = 1; bit < 4; bit <<= 1)
 #pragma unroll
@@ -471,12 +475,89 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
           if (place >= 0)
             *reinterpret_cast<uint4*>(a.out + (size_t)place * D + d0 + (lane & 3) * 8) = make_uint4(x[i][0], x[i][1], x[i][2], x[i][3]);
         }
+      };
+      // (Loops: code that runs once per unit is fetched anew every time.)
+      if (unit.parts == 1) {
+        const float inv = l > 0.f ? v_scale / l : 0.f;
+#pragma unroll 2
+        for (int d0 = 0; d0 < D; d0 += 32) {
+          uint32_t o[32];
+          float v[32];
+          if (nt > 0) {
+            tmem_ld32(out + d0, o);
+            tmem_wait_ld();
+            tie(o);
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = l > 0.f ? __uint_as_float(o[i]) * inv : 0.f;
+          write(d0, v);
+        }
+      } else if (!idle) {
+        float* mine = p.partial + (size_t)(unit.slot * 8 + warp) * kPartFloats<D>;
+        if (nt > 0) {
+#pragma unroll 1
+          for (int d0 = 0; d0 < D; d0 += 32) {
+            uint32_t o[32];
+            tmem_ld32(out + d0, o);
+            tmem_wait_ld();
+            tie(o);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              reinterpret_cast<uint4*>(mine)[(d0 / 4 + i) * 32 + lane] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+        }
+        mine[32 * D + lane] = m;
+        mine[32 * D + 32 + lane] = l;
+        __syncwarp();
+        int last = 0;
+        if (lane == 0) {
+          __threadfence();  // the warp's part before its arrival, the others' before what follows
+          last = atomicAdd(p.arrived + unit.id * 8 + warp, 1) == unit.parts - 1;
+          __threadfence();
+          if (last) p.arrived[unit.id * 8 + warp] = 0;  // left zero for the next call
+        }
+        if (__shfl_sync(0xffffffffu, last, 0)) {
+          const float* part = p.partial + (size_t)((unit.slot - unit.part) * 8 + warp) * kPartFloats<D>;
+          constexpr size_t kNext = (size_t)8 * kPartFloats<D>;
+          m = -INFINITY;
+          for (int i = 0; i < unit.parts; ++i)
+            if (__ldcg(part + i * kNext + 32 * D + 32 + lane) > 0.f) m = fmaxf(m, __ldcg(part + i * kNext + 32 * D + lane));
+          l = 0.f;
+          for (int i = 0; i < unit.parts; ++i) {
+            const float li = __ldcg(part + i * kNext + 32 * D + 32 + lane);
+            if (li > 0.f) l += li * ex2(__ldcg(part + i * kNext + 32 * D + lane) - m);
+          }
+          const float inv = l > 0.f ? v_scale / l : 0.f;
+#pragma unroll 1
+          for (int d0 = 0; d0 < D; d0 += 32) {
+            float v[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0.f;
+#pragma unroll 2
+            for (int i = 0; i < unit.parts; ++i) {
+              // a part that a row sees no key of holds no O
+              const bool some = __ldcg(part + i * kNext + 32 * D + 32 + lane) > 0.f;
+              const float f = some ? ex2(__ldcg(part + i * kNext + 32 * D + lane) - m) * inv : 0.f;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const float4 x = __ldcg(reinterpret_cast<const float4*>(part + i * kNext) + (d0 / 4 + k) * 32 + lane);
+                v[4 * k] = some ? fmaf(x.x, f, v[4 * k]) : v[4 * k];
+                v[4 * k + 1] = some ? fmaf(x.y, f, v[4 * k + 1]) : v[4 * k + 1];
+                v[4 * k + 2] = some ? fmaf(x.z, f, v[4 * k + 2]) : v[4 * k + 2];
+                v[4 * k + 3] = some ? fmaf(x.w, f, v[4 * k + 3]) : v[4 * k + 3];
+              }
+            }
+            write(d0, v);
+          }
+        } else {
+          to = -1;  // another warp writes these rows
+        }
       }
       if (nt > 0) {  // O is read: the next unit may write it
         tc_fence_before();
         mbar_arrive(bar(kOutFree + t));
       }
-      if (live && a.lse) a.lse[to] = l > 0.f ? m * kLn2 + logf(l) : -INFINITY;
+      if (to >= 0 && a.lse) a.lse[to] = l > 0.f ? m * kLn2 + logf(l) : -INFINITY;
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
@@ -508,19 +589,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
           // a lane for each page and panel. Small pages' copies (16 of them
           // for 16 tokens) are shared among the four warps: a warp issues its
           // lanes' copies one after another.
-          const int whole = p.tiled ? min(most, len / kTile) : 0;
+          const int whole = p.tiled ? max(0, min(most, len / kTile - unit.j0)) : 0;
           const int end = count + 2 * whole;
           const int box = min(1 << shift, kTile), boxes = kTile / box, copies = D / 64 * boxes;
           const int sharing = copies > 4 ? 4 : 1, each = copies / sharing;
           if (warp - 8 < sharing) {
             const int mine = (warp - 8) * each + lane, panel = mine / boxes, part = mine % boxes;
             // the page of the next tile is looked up while this one is waited for
-            unsigned long long row = 0, ahead = whole > 0 ? row_of(part * box) : 0;
+            unsigned long long row = 0, ahead = whole > 0 ? row_of(unit.j0 * kTile + part * box) : 0;
             for (int j = 0; count < end && ok; ++count) {
               const bool values = (end - count) & 1;
               if (!values) {
                 row = ahead;
-                if (++j < whole) ahead = row_of(j * kTile + part * box);
+                if (++j < whole) ahead = row_of((unit.j0 + j) * kTile + part * box);
               }
               if (!(ok = wait_slot())) break;
               const uint32_t full = bar(kFull + slot_of());
@@ -539,7 +620,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
             const int r0 = v / kChunks, c = v % kChunks;
             constexpr int kStride = 128 / kChunks;
             for (int j = whole; j < most && ok; ++j) {
-              const unsigned long long group = row_of_or_0(row_of, j * kTile + 16 * (lane & 7), len);
+              const int key0 = (unit.j0 + j) * kTile;
+              const unsigned long long group = row_of_or_0(row_of, key0 + 16 * (lane & 7), len);
               int slots[2];
 #pragma unroll 1
               for (int kv = 0; kv < 2 && ok; ++kv) {
@@ -550,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
                 for (int x = 0; x < kTile / kStride; ++x) {
                   const int r = r0 + x * kStride;
                   const unsigned long long row = __shfl_sync(0xffffffffu, group, r >> 4) + (r & 15);
-                  const bool valid = j * kTile + r < len;
+                  const bool valid = key0 + r < len;
                   cp16(dst + x * kStride * 128, valid ? src + row * (2 * D) + c * 16 : src, valid);
                 }
                 cp_commit();
@@ -576,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
           const int r0 = v / kPieces, c = v % kPieces;
           unsigned long long group = 0;
           for (int i = 0; i < 2 * most; ++i, ++count) {
-            const int j = i >> 1;
+            const int j = unit.j0 + (i >> 1);
             if (!(i & 1)) group = row_of_or_0(row_of, j * kTile + 16 * (lane & 7), len) * D;
             const uint8_t* src = static_cast<const uint8_t*>(i & 1 ? a.cache.v : a.cache.k) + (r0 & 15) * D + c * 16;
             const bool inside = (j + 1) * kTile <= len;
@@ -638,6 +720,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
         }
         --group;
       }
+      // places for parts per unit, as many as there are blocks
+      const int count = total * a.cache.kv_heads;
+      const int split = count > 0 && count < (int)gridDim.x ? max(1, min((int)gridDim.x / count, p.most_parts)) : 1;
       const int w = tid - 384, c = w % kChunks;
       constexpr int kStride = 64 / kChunks;
       const int step_head = kStride % p.group;
@@ -646,33 +731,47 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
       for (int u = 0; ok; ++u) {
         if (warp == 12) {
           if (u >= 2 && !(ok = warp_wait(kUnitFree + (u & 1), (uint32_t)(u / 2 - 1) & 1u, kErrProducer))) break;
-          int i = 0;
-          if (lane == 0) i = atomicAdd(p.queue, 1);
-          i = __shfl_sync(0xffffffffu, i, 0);
-          const int want = total - 1 - i / a.cache.kv_heads;
           Unit& to = ctl.unit[u & 1];
-          if (want >= 0) {
+          for (bool found = false; !found;) {
+            int i = 0;
+            if (lane == 0) i = atomicAdd(p.queue, 1);
+            i = __shfl_sync(0xffffffffu, i, 0);
+            // (a queue that was not zero ends the call, it does not search)
+            const int id = i / split, want = i < 0 ? -1 : total - 1 - id / a.cache.kv_heads;
+            if (want < 0) {
+              if (lane == 0) {
+                to.valid = 0;
+                // the last block to come here leaves the queue zero
+                __threadfence();
+                if (atomicAdd(p.queue + 1, 1) == (int)gridDim.x - 1) p.queue[0] = p.queue[1] = 0;
+              }
+              break;
+            }
             while (want < before) {
               --group;
               look();
               before -= __shfl_sync(0xffffffffu, upto, 31);
             }
             const int lo = before + upto - v;
+            bool mine = false;
             if (lo <= want && want < lo + v) {
               const int row0 = (want - lo) * (2 * kTile), rows = fresh * p.group;  // rows: at most 2^30
-              to = {32 * group + lane, first, fresh, len, row0, i % a.cache.kv_heads, {0, 0}, 1};
+              int n[2];
 #pragma unroll
-              for (int t = 0; t < 2; ++t) {
+              for (int t = 0; t < 2; ++t) {  // up to the last row's position
                 const int from = row0 + t * kTile, past = min(from + kTile, rows);
                 const int last = from < past ? len - fresh + (past - 1) / p.group : -1;
-                to.n[t] = last < 0 ? 0 : last / kTile + 1;
+                n[t] = last < 0 ? 0 : last / kTile + 1;
+              }
+              const int all = max(n[0], n[1]), parts = max(1, min(split, all / kLeast)), part = i % split;
+              if (part < parts) {  // (a short unit has fewer parts than there are places)
+                const int j0 = (int)((long long)part * all / parts), j1 = (int)((long long)(part + 1) * all / parts);
+                to = {32 * group + lane, first, fresh, len, row0, id % a.cache.kv_heads, j0,
+                      {max(0, min(n[0], j1) - j0), max(0, min(n[1], j1) - j0)}, parts, i, id, part, 1};
+                mine = true;
               }
             }
-          } else if (lane == 0) {
-            to.valid = 0;
-            // the last block to come here leaves the queue zero
-            __threadfence();
-            if (atomicAdd(p.queue + 1, 1) == (int)gridDim.x - 1) p.queue[0] = p.queue[1] = 0;
+            found = __any_sync(0xffffffffu, mine);
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(kUnit + (u & 1)));
@@ -862,7 +961,18 @@ cudaError_t launch(PromptArgs p, unsigned blocks, cudaStream_t stream) {
   return launch_pdl(kern, dim3(blocks), dim3(kThreads), kSmem<D>, stream, p, map_k, map_v, map_q);
 }
 
+constexpr size_t kFlagBytes = 32768;
+
+// Whether the units can be fewer than the blocks.
+bool may_split(int tokens, int group, int kv_heads, int sms) {
+  return ((long long)tokens * group + 2 * kTile - 1) / (2 * kTile) * kv_heads < sms;
+}
+
 }  // namespace
+
+size_t attn_prompt_workspace_bytes(int tokens, int group, int kv_heads, int head_dim, int sms) {
+  return kFlagBytes + (may_split(tokens, group, kv_heads, sms) ? (size_t)sms * 8 * 32 * (head_dim + 2) * sizeof(float) : 0);
+}
 
 cudaError_t launch_attn_prompt(const AttnArgs& args, int head_dim, bool bf16, bool e4m3, void* workspace, int sms,
                                cudaStream_t stream) {
@@ -878,10 +988,16 @@ cudaError_t launch_attn_prompt(const AttnArgs& args, int head_dim, bool bf16, bo
   p.mult = fmaxf(fabsf(args.scale) * kLog2e, 1e-37f);
   p.negate = args.scale < 0.f;
   p.queue = static_cast<int*>(workspace);
-  // a block per SM, or as many as there can be units: whole ones of all rows,
-  // and a ragged one per sequence
+  p.arrived = p.queue + 2;
+  p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kFlagBytes);
+  // a block per SM, or as many as there can be units (whole ones of all rows,
+  // and a ragged one per sequence) where none is long enough for two parts
   const long long units = ((long long)args.rows * p.group / (2 * kTile) + args.batch) * args.cache.kv_heads;
-  const unsigned blocks = units < sms ? (unsigned)units : (unsigned)sms;
+  const long long tiles = (((long long)args.max_pages << args.cache.page_shift) + kTile - 1) / kTile;
+  p.most_parts = 1;
+  if (may_split(args.rows, p.group, args.cache.kv_heads, sms) && tiles >= 2 * kLeast)
+    p.most_parts = (int)(tiles / kLeast < sms ? tiles / kLeast : sms);
+  const unsigned blocks = units < sms && p.most_parts < 2 ? (unsigned)units : (unsigned)sms;
   switch ((bf16 ? 4 : 0) | (e4m3 ? 2 : 0) | (head_dim == 128 ? 1 : 0)) {
     case 0: return launch<false, false, 64>(p, blocks, stream);
     case 1: return launch<false, false, 128>(p, blocks, stream);

@@ -158,7 +158,12 @@ int w4a16_attn_workspace_size(int tokens, int batch, int heads, int kv_heads, in
   if (tokens < 0 || batch < 0 || heads <= 0 || kv_heads <= 0 || head_dim <= 0)
     return fail(W4A16_ERR_INVALID_ARG, "negative or zero size");
   if (!bytes) return fail(W4A16_ERR_INVALID_ARG, "null output pointer");
-  *bytes = tokens == 0 || batch == 0 ? 0 : attn_decode_workspace_bytes(head_dim, device_sms());
+  *bytes = 0;
+  if (tokens == 0 || batch == 0) return report_ok();
+  const int sms = device_sms();
+  const size_t decode = tokens == batch ? attn_decode_workspace_bytes(head_dim, sms) : 0;
+  const size_t prompt = attn_prompt_workspace_bytes(tokens, (heads + kv_heads - 1) / kv_heads, kv_heads, head_dim, sms);
+  *bytes = decode > prompt ? decode : prompt;
   return report_ok();
 }
 
@@ -193,7 +198,7 @@ int w4a16_attn_prompt(const uint16_t* q, int64_t q_stride, const void* k_cache, 
   if (!aligned(starts, 4)) return fail(W4A16_ERR_MISALIGNED, "alignment: starts needs 4 bytes");
   a.starts = starts;
   const int sms = device_sms();
-  if (int rc = check_workspace(workspace, workspace_bytes, attn_decode_workspace_bytes(head_dim, sms))) return rc;
+  if (int rc = check_workspace(workspace, workspace_bytes, attn_prompt_workspace_bytes(tokens, heads / kv_heads, kv_heads, head_dim, sms))) return rc;
   return finish(launch_attn_prompt(a, head_dim, (flags & W4A16_BF16) != 0, (flags & W4A16_CACHE_E4M3) != 0, workspace,
                                    sms, (cudaStream_t)stream),
                 "prompt attention launch");

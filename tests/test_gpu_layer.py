@@ -341,6 +341,61 @@ def test_prompt(seqs, heads, hk, D, page, dtype, cache_dtype):
     assert same(again[lead:T - trail].contiguous(), got[lead:T - trail].contiguous())
 
 
+@pytest.mark.parametrize("seqs,heads,hk,D,page", [
+    ([(16, 9000)], 16, 2, 128, 64),                  # few rows behind a long cache: split over it
+    ([(1, 5000), (3, 700), (40, 41)], 8, 1, 128, 16),  # sequences too short for every part among them
+    ([(300, 4000), (2, 0)], 2, 2, 64, 128),          # two row tiles with other last keys; rows that see none
+    ([(9, 3001)], 40, 1, 128, 32),
+])
+@pytest.mark.parametrize("dtype,cache_dtype", [(FP16, FP16), (BF16, BF16), (FP16, E4M3), (BF16, E4M3)])
+def test_prompt_split_over_a_long_cache(seqs, heads, hk, D, page, dtype, cache_dtype):
+    new, lens = [a for a, _ in seqs], [n for _, n in seqs]
+    g = gen(sum(new) + sum(lens))
+    cache, tab = scattered(g, lens, hk, page, D, cache_dtype)
+    starts = [sum(new[:b]) for b in range(len(new) + 1)]
+    q = normal(g, starts[-1], heads, D, std=2, dtype=dtype)
+    st = torch.tensor(starts, dtype=torch.int32, device="cuda")
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    ws = w4.new_workspace(w4.attn_workspace_size(starts[-1], len(lens), heads, hk, D) + 4096)
+    ws[-4096:] = 0x5A
+    for _ in range(3):  # the same bits whichever part comes last, and the flags zero for the next call
+        got, lse = w4.attn_prompt(q, cache, tab, st, n, return_lse=True, workspace=ws)
+        w4.device_status()
+        assert not ws[:32768].any() and (ws[-4096:] == 0x5A).all()
+        check_attention(q, cache, tab, starts, lens, got, lse, D ** -0.5)
+        again, l2 = w4.attn_prompt(q, cache, tab, st, n, return_lse=True, workspace=ws)
+        assert same(again, got) and same(l2, lse)
+
+
+def test_attention_workspaces():
+    """A workspace too small or misaligned is refused; one serves decode,
+    prompt and GEMM calls in turn."""
+    g = gen(23)
+    lens, heads, hk, D = [300, 70], 8, 2, 128
+    cache, tab = scattered(g, lens, hk, 16, D, FP16)
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    st = torch.tensor([0, 5, 7], dtype=torch.int32, device="cuda")
+    qd, qp = normal(g, 2, heads, D, dtype=FP16), normal(g, 7, heads, D, dtype=FP16)
+    calls = [lambda ws: w4.attn_decode(qd, cache, tab, n, workspace=ws),
+             lambda ws: w4.attn_prompt(qp, cache, tab, st, n, workspace=ws)]
+    pw = w4.quantize_pack(normal(g, 1024, 512, std=0.02), 128)
+    x = normal(g, 40, 1024, dtype=FP16)
+    calls.append(lambda ws: w4.gemm(x, pw, path="tensor", parts=4, workspace=ws))
+    calls.append(lambda ws: w4.gemm(x[:3], pw, path="decode-streamk", workspace=ws))
+    for call in calls[:2]:
+        for ws, code in ((w4.new_workspace(4096), -4), (w4.new_workspace(64 << 20)[8:], -3)):
+            with pytest.raises(w4.W4A16Error) as e:
+                call(ws)
+            assert e.value.code == code
+    ws = w4.new_workspace(64 << 20)
+    want = [call(None) for call in calls]
+    for _ in range(3):
+        for call, y in zip(calls, want):
+            assert same(call(ws), y)
+            assert not ws[:32768].any()
+    w4.device_status()
+
+
 @pytest.mark.parametrize("cache_dtype", [FP16, E4M3])
 @pytest.mark.parametrize("std,scale", [(0.0, None), (30.0, None), (1.0, -0.3), (1.0, 0.0), (200.0, 1.0)])
 def test_attention_of_extreme_scores(std, scale, cache_dtype):
