@@ -338,18 +338,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
     uint32_t score_phase = 0, out_phase = 0;
     bool ok = true;
     for (int u = 0; ok; ++u) {
-      if (!next_unit(u, kErrEpilogue, true)) break;
-      const int nt = t ? unit.n[1] : unit.n[0];
+      // (read where it is needed, and released at the end: registers are short)
+      if (!warp_wait(kUnit + (u & 1), (uint32_t)(u >> 1) & 1u, kErrEpilogue)) break;
+      const Unit& unit = ctl.unit[u & 1];
+      if (!unit.valid) break;
+      const int nt = unit.n[t];
       const int row = unit.row0 + t * kTile + (tid & 127);
       const bool live = row < unit.fresh * p.group;
-      const int token = live ? row / p.group : 0, head = unit.head * p.group + (live ? row % p.group : 0);
-      // keys this row sees (rows beyond the sequence mask nothing: what they
-      // give is not written)
-      const int limit = live ? unit.len - unit.fresh + token + 1 : 0x7fffffff;
+      const int token = live ? row / p.group : 0, head = unit.head * p.group + (live ? row - token * p.group : 0);
+      // keys of the unit's that this row sees (rows beyond the sequence mask
+      // nothing: what they give is not written)
+      const int limit = live ? unit.len - unit.fresh + token + 1 - unit.j0 * kTile : 0x7fffffff;
       const bool idle = __all_sync(0xffffffffu, !live);
       int to = live ? (unit.first + token) * a.heads + head : -1;
       float mult = p.mult * (k8 ? a.cache.k_scale[unit.head] : 1.f);
-      const float v_scale = k8 ? a.cache.v_scale[unit.head] : 1.f;
       if (kB && k8) {
         if (!(ok = warp_wait(kQueries + t, (uint32_t)u & 1u, kErrEpilogue))) break;
         mult *= ctl.power[t * kTile + (tid & 127)];
@@ -372,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
 #pragma unroll
         for (int q = 0; q < 4; ++q) tie(s[q]);
         // masked 32 keys at a time, where a row of the warp needs it
-        const int seen = limit - (unit.j0 + j) * kTile;
+        const int seen = limit - j * kTile;
         if (!__all_sync(0xffffffffu, seen >= kTile)) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
@@ -449,50 +451,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
         tc_fence_after();
       }
       if (!ok) break;
-      // 32 dimensions of the rows, transposed among four lanes (a lane's four
-      // 16-byte chunks of its row become one chunk of four rows), so that
-      // whole sectors are written: a row per lane would be 32 lines per store
-      auto write = [&](int d0, const float (&v)[32]) {
-        uint32_t x[4][4];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i / 4][i & 3] = pack16<kB>(v[2 * i], v[2 * i + 1]);
-#pragma unroll
-        for (int bit = 1; bit < 4; bit <<= 1)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (!(i & bit)) {
-              const bool upper = lane & bit;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? x[i][k] : x[i | bit][k], bit);
-                x[i][k] = upper ? got : x[i][k];
-                x[i | bit][k] = upper ? x[i | bit][k] : got;
-              }
-            }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int place = __shfl_sync(0xffffffffu, to, (lane & 28) + i);
-          if (place >= 0)
-            *reinterpret_cast<uint4*>(a.out + (size_t)place * D + d0 + (lane & 3) * 8) = make_uint4(x[i][0], x[i][1], x[i][2], x[i][3]);
-        }
-      };
       // (Loops: code that runs once per unit is fetched anew every time.)
-      if (unit.parts == 1) {
-        const float inv = l > 0.f ? v_scale / l : 0.f;
-#pragma unroll 2
-        for (int d0 = 0; d0 < D; d0 += 32) {
-          uint32_t o[32];
-          float v[32];
-          if (nt > 0) {
-            tmem_ld32(out + d0, o);
-            tmem_wait_ld();
-            tie(o);
-          }
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = l > 0.f ? __uint_as_float(o[i]) * inv : 0.f;
-          write(d0, v);
-        }
-      } else if (!idle) {
+      const float* part = nullptr;  // the unit's first, where this warp joins them
+      constexpr size_t kNext = (size_t)8 * kPartFloats<D>;
+      if (unit.parts > 1 && !idle) {
         float* mine = p.partial + (size_t)(unit.slot * 8 + warp) * kPartFloats<D>;
         if (nt > 0) {
 #pragma unroll 1
@@ -517,8 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
           if (last) p.arrived[unit.id * 8 + warp] = 0;  // left zero for the next call
         }
         if (__shfl_sync(0xffffffffu, last, 0)) {
-          const float* part = p.partial + (size_t)((unit.slot - unit.part) * 8 + warp) * kPartFloats<D>;
-          constexpr size_t kNext = (size_t)8 * kPartFloats<D>;
+          part = p.partial + (size_t)((unit.slot - unit.part) * 8 + warp) * kPartFloats<D>;
           m = -INFINITY;
           for (int i = 0; i < unit.parts; ++i)
             if (__ldcg(part + i * kNext + 32 * D + 32 + lane) > 0.f) m = fmaxf(m, __ldcg(part + i * kNext + 32 * D + lane));
@@ -527,30 +488,67 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
             const float li = __ldcg(part + i * kNext + 32 * D + 32 + lane);
             if (li > 0.f) l += li * ex2(__ldcg(part + i * kNext + 32 * D + lane) - m);
           }
-          const float inv = l > 0.f ? v_scale / l : 0.f;
-#pragma unroll 1
-          for (int d0 = 0; d0 < D; d0 += 32) {
-            float v[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = 0.f;
+        } else {
+          to = -1;  // another warp writes these rows
+        }
+      }
+      if (unit.parts == 1 || part) {
+        const float inv = l > 0.f ? (k8 ? a.cache.v_scale[unit.head] : 1.f) / l : 0.f;
 #pragma unroll 2
+        for (int d0 = 0; d0 < D; d0 += 32) {
+          float o[32];
+          if (!part) {
+            uint32_t r[32];
+            if (nt > 0) {
+              tmem_ld32(out + d0, r);
+              tmem_wait_ld();
+              tie(r);
+            }
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = l > 0.f ? __uint_as_float(r[i]) : 0.f;
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = 0.f;
+#pragma unroll 1
             for (int i = 0; i < unit.parts; ++i) {
-              // a part that a row sees no key of holds no O
+              // (a part that a row sees no key of holds no O)
               const bool some = __ldcg(part + i * kNext + 32 * D + 32 + lane) > 0.f;
-              const float f = some ? ex2(__ldcg(part + i * kNext + 32 * D + lane) - m) * inv : 0.f;
+              const float f = some ? ex2(__ldcg(part + i * kNext + 32 * D + lane) - m) : 0.f;
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
                 const float4 x = __ldcg(reinterpret_cast<const float4*>(part + i * kNext) + (d0 / 4 + k) * 32 + lane);
-                v[4 * k] = some ? fmaf(x.x, f, v[4 * k]) : v[4 * k];
-                v[4 * k + 1] = some ? fmaf(x.y, f, v[4 * k + 1]) : v[4 * k + 1];
-                v[4 * k + 2] = some ? fmaf(x.z, f, v[4 * k + 2]) : v[4 * k + 2];
-                v[4 * k + 3] = some ? fmaf(x.w, f, v[4 * k + 3]) : v[4 * k + 3];
+                o[4 * k] = some ? fmaf(x.x, f, o[4 * k]) : o[4 * k];
+                o[4 * k + 1] = some ? fmaf(x.y, f, o[4 * k + 1]) : o[4 * k + 1];
+                o[4 * k + 2] = some ? fmaf(x.z, f, o[4 * k + 2]) : o[4 * k + 2];
+                o[4 * k + 3] = some ? fmaf(x.w, f, o[4 * k + 3]) : o[4 * k + 3];
               }
             }
-            write(d0, v);
           }
-        } else {
-          to = -1;  // another warp writes these rows
+          // transposed among four lanes (a lane's four 16-byte chunks of its
+          // row become one chunk of four rows), so that whole sectors are
+          // written: a row per lane would be 32 lines per store
+          uint32_t x[4][4];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i / 4][i & 3] = pack16<kB>(o[2 * i] * inv, o[2 * i + 1] * inv);
+#pragma unroll
+          for (int bit = 1; bit < 4; bit <<= 1)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (!(i & bit)) {
+                const bool upper = lane & bit;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? x[i][k] : x[i | bit][k], bit);
+                  x[i][k] = upper ? got : x[i][k];
+                  x[i | bit][k] = upper ? x[i | bit][k] : got;
+                }
+              }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int place = __shfl_sync(0xffffffffu, to, (lane & 28) + i);
+            if (place >= 0)
+              *reinterpret_cast<uint4*>(a.out + (size_t)place * D + d0 + (lane & 3) * 8) = make_uint4(x[i][0], x[i][1], x[i][2], x[i][3]);
+          }
         }
       }
       if (nt > 0) {  // O is read: the next unit may write it
@@ -558,6 +556,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
         mbar_arrive(bar(kOutFree + t));
       }
       if (to >= 0 && a.lse) a.lse[to] = l > 0.f ? m * kLn2 + logf(l) : -INFINITY;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kUnitFree + (u & 1)));
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
@@ -765,7 +765,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
               }
               const int all = max(n[0], n[1]), parts = max(1, min(split, all / kLeast)), part = i % split;
               if (part < parts) {  // (a short unit has fewer parts than there are places)
-                const int j0 = (int)((long long)part * all / parts), j1 = (int)((long long)(part + 1) * all / parts);
+                // (products below 2^31: at most 2^23 tiles, parts up to the blocks)
+                const int j0 = parts == 1 ? 0 : part * all / parts, j1 = parts == 1 ? all : (part + 1) * all / parts;
                 to = {32 * group + lane, first, fresh, len, row0, id % a.cache.kv_heads, j0,
                       {max(0, min(n[0], j1) - j0), max(0, min(n[1], j1) - j0)}, parts, i, id, part, 1};
                 mine = true;
