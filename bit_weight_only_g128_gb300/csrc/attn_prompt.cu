@@ -30,7 +30,9 @@
 //                    of S
 // Where the units are fewer than the blocks, each is split over its keys into
 // parts of at least kLeast tiles; the parts' (m, l, O) go to the workspace as
-// fp32, and of each 32 rows the last part to arrive joins them, in their order.
+// fp32, and a second kernel joins them in their order. (Joined by the last
+// part to arrive, 19 parts of 128 rows took one block longer than the parts
+// themselves: 16 rows behind 30000 keys 55-76 us against 50.)
 // Tensor memory: S0, S1 (128 columns each), O0, O1 (D each). Registers: 128 a
 // thread at launch, 192 for the softmax warps and 64 for the rest (256 x 192
 // + 256 x 64 = 512 x 128).
@@ -75,8 +77,7 @@ struct Unit {
   int b, first, fresh, len;  // sequence, its first row, rows, cached tokens
   int row0, head;            // first of the unit's rows (tokens x heads), key/value head
   int j0, n[2];              // first key tile, and key tiles that the two row tiles need from it on
-  int parts, slot, id;       // parts of the rows' keys, place of this one and number of the whole
-  int part;
+  int parts, part, slot;     // parts of the rows' keys, which one this is, and its place
   int valid;                 // 0: no unit is left
 };
 
@@ -94,9 +95,11 @@ template <int D>
 constexpr int kSmem = (2 + kSlots) * kTileBytes<D> + (int)sizeof(Control) + 1024;
 static_assert(kSmem<128> <= 227 * 1024, "one block's shared memory");
 
-// A warp's part: O as [D / 4][32 rows] of four, maxima, sums.
+// A warp's part: O as [D / 4][32 rows] of four, maxima, sums, the rows' places
+// in the output (or -1), and the number of parts to join from this one on (0:
+// none).
 template <int D>
-constexpr int kPartFloats = 32 * (D + 2);
+constexpr int kPartFloats = 32 * (D + 4);
 
 struct PromptArgs {
   AttnArgs a;
@@ -106,8 +109,7 @@ struct PromptArgs {
   int tiled;        // the maps of the keys and values are there
   int q_tiled;      // the map of the queries is there
   int* queue;       // next unit, blocks that are through; zero between calls
-  int* arrived;     // [units split][8 warps] parts that are there; zero between calls
-  float* partial;   // [blocks][8 warps] of kPartFloats
+  float* partial;   // [blocks][8 warps] of kPartFloats, where units can be split
   int most_parts;
 };
 
@@ -452,84 +454,45 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
       }
       if (!ok) break;
       // (Loops: code that runs once per unit is fetched anew every time.)
-      const float* part = nullptr;  // the unit's first, where this warp joins them
-      constexpr size_t kNext = (size_t)8 * kPartFloats<D>;
-      if (unit.parts > 1 && !idle) {
-        float* mine = p.partial + (size_t)(unit.slot * 8 + warp) * kPartFloats<D>;
-        if (nt > 0) {
+      float* mine = p.partial + (size_t)(unit.slot * 8 + warp) * kPartFloats<D>;
+      if (p.most_parts > 1 && unit.slot < (int)gridDim.x)
+        reinterpret_cast<int*>(mine)[32 * (D + 3) + lane] = unit.part == 0 && unit.parts > 1 && !idle ? unit.parts : 0;
+      if (unit.parts > 1) {
+        if (!idle) {
+          if (nt > 0) {
 #pragma unroll 1
-          for (int d0 = 0; d0 < D; d0 += 32) {
-            uint32_t o[32];
-            tmem_ld32(out + d0, o);
-            tmem_wait_ld();
-            tie(o);
+            for (int d0 = 0; d0 < D; d0 += 32) {
+              uint32_t o[32];
+              tmem_ld32(out + d0, o);
+              tmem_wait_ld();
+              tie(o);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              reinterpret_cast<uint4*>(mine)[(d0 / 4 + i) * 32 + lane] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+              for (int i = 0; i < 8; ++i)
+                reinterpret_cast<uint4*>(mine)[(d0 / 4 + i) * 32 + lane] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            }
           }
+          mine[32 * D + lane] = m;
+          mine[32 * (D + 1) + lane] = l;
+          reinterpret_cast<int*>(mine)[32 * (D + 2) + lane] = to;
         }
-        mine[32 * D + lane] = m;
-        mine[32 * D + 32 + lane] = l;
-        __syncwarp();
-        int last = 0;
-        if (lane == 0) {
-          __threadfence();  // the warp's part before its arrival, the others' before what follows
-          last = atomicAdd(p.arrived + unit.id * 8 + warp, 1) == unit.parts - 1;
-          __threadfence();
-          if (last) p.arrived[unit.id * 8 + warp] = 0;  // left zero for the next call
-        }
-        if (__shfl_sync(0xffffffffu, last, 0)) {
-          part = p.partial + (size_t)((unit.slot - unit.part) * 8 + warp) * kPartFloats<D>;
-          m = -INFINITY;
-          for (int i = 0; i < unit.parts; ++i)
-            if (__ldcg(part + i * kNext + 32 * D + 32 + lane) > 0.f) m = fmaxf(m, __ldcg(part + i * kNext + 32 * D + lane));
-          l = 0.f;
-          for (int i = 0; i < unit.parts; ++i) {
-            const float li = __ldcg(part + i * kNext + 32 * D + 32 + lane);
-            if (li > 0.f) l += li * ex2(__ldcg(part + i * kNext + 32 * D + lane) - m);
-          }
-        } else {
-          to = -1;  // another warp writes these rows
-        }
-      }
-      if (unit.parts == 1 || part) {
+        to = -1;  // written by the joining kernel
+      } else {
         const float inv = l > 0.f ? (k8 ? a.cache.v_scale[unit.head] : 1.f) / l : 0.f;
 #pragma unroll 2
         for (int d0 = 0; d0 < D; d0 += 32) {
-          float o[32];
-          if (!part) {
-            uint32_t r[32];
-            if (nt > 0) {
-              tmem_ld32(out + d0, r);
-              tmem_wait_ld();
-              tie(r);
-            }
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = l > 0.f ? __uint_as_float(r[i]) : 0.f;
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = 0.f;
-#pragma unroll 1
-            for (int i = 0; i < unit.parts; ++i) {
-              // (a part that a row sees no key of holds no O)
-              const bool some = __ldcg(part + i * kNext + 32 * D + 32 + lane) > 0.f;
-              const float f = some ? ex2(__ldcg(part + i * kNext + 32 * D + lane) - m) : 0.f;
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const float4 x = __ldcg(reinterpret_cast<const float4*>(part + i * kNext) + (d0 / 4 + k) * 32 + lane);
-                o[4 * k] = some ? fmaf(x.x, f, o[4 * k]) : o[4 * k];
-                o[4 * k + 1] = some ? fmaf(x.y, f, o[4 * k + 1]) : o[4 * k + 1];
-                o[4 * k + 2] = some ? fmaf(x.z, f, o[4 * k + 2]) : o[4 * k + 2];
-                o[4 * k + 3] = some ? fmaf(x.w, f, o[4 * k + 3]) : o[4 * k + 3];
-              }
-            }
+          uint32_t o[32];
+          if (nt > 0) {
+            tmem_ld32(out + d0, o);
+            tmem_wait_ld();
+            tie(o);
           }
           // transposed among four lanes (a lane's four 16-byte chunks of its
           // row become one chunk of four rows), so that whole sectors are
           // written: a row per lane would be 32 lines per store
           uint32_t x[4][4];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) x[i / 4][i & 3] = pack16<kB>(o[2 * i] * inv, o[2 * i + 1] * inv);
+          for (int i = 0; i < 16; ++i)
+            x[i / 4][i & 3] = l > 0.f ? pack16<kB>(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv) : 0;
 #pragma unroll
           for (int bit = 1; bit < 4; bit <<= 1)
 #pragma unroll
@@ -723,6 +686,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
       // places for parts per unit, as many as there are blocks
       const int count = total * a.cache.kv_heads;
       const int split = count > 0 && count < (int)gridDim.x ? max(1, min((int)gridDim.x / count, p.most_parts)) : 1;
+      auto no_part = [&](int i) {  // place i holds nothing to join
+        if (p.most_parts > 1 && i >= 0 && i < (int)gridDim.x)
+#pragma unroll 1
+          for (int k = 0; k < 8; ++k)
+            reinterpret_cast<int*>(p.partial + (size_t)(i * 8 + k) * kPartFloats<D>)[32 * (D + 3) + lane] = 0;
+      };
       const int w = tid - 384, c = w % kChunks;
       constexpr int kStride = 64 / kChunks;
       const int step_head = kStride % p.group;
@@ -739,6 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
             // (a queue that was not zero ends the call, it does not search)
             const int id = i / split, want = i < 0 ? -1 : total - 1 - id / a.cache.kv_heads;
             if (want < 0) {
+              no_part(i);
               if (lane == 0) {
                 to.valid = 0;
                 // the last block to come here leaves the queue zero
@@ -768,11 +738,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
                 // (products below 2^31: at most 2^23 tiles, parts up to the blocks)
                 const int j0 = parts == 1 ? 0 : part * all / parts, j1 = parts == 1 ? all : (part + 1) * all / parts;
                 to = {32 * group + lane, first, fresh, len, row0, id % a.cache.kv_heads, j0,
-                      {max(0, min(n[0], j1) - j0), max(0, min(n[1], j1) - j0)}, parts, i, id, part, 1};
+                      {max(0, min(n[0], j1) - j0), max(0, min(n[1], j1) - j0)}, parts, part, i, 1};
                 mine = true;
               }
             }
             found = __any_sync(0xffffffffu, mine);
+            if (!found) no_part(i);
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(kUnit + (u & 1)));
@@ -938,6 +909,55 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
   }
 }
 
+// Joins the parts of split units: a warp for 32 rows (a lane each) and 32
+// dimensions, blockIdx.x the place of a first part and its warp. All places
+// are looked at; those that hold no first part end at once.
+template <bool kB, int D>
+__global__ void __launch_bounds__(D) attn_join_kernel(const PromptArgs p) {
+  allow_dependent_launch();
+  grid_dependency_wait();
+  const int lane = threadIdx.x & 31, d0 = threadIdx.x & ~31;
+  const float* first = p.partial + (size_t)blockIdx.x * kPartFloats<D>;
+  constexpr size_t kNext = (size_t)8 * kPartFloats<D>;
+  const int parts = reinterpret_cast<const int*>(first)[32 * (D + 3) + lane];
+  if (parts == 0) return;  // (the same in all lanes)
+  float m = -INFINITY, l = 0.f;
+  float o[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) o[i] = 0.f;
+#pragma unroll 2
+  for (int i = 0; i < parts; ++i) {
+    const float* from = first + i * kNext;
+    const float mi = from[32 * D + lane], li = from[32 * (D + 1) + lane];
+    float4 x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = reinterpret_cast<const float4*>(from)[(d0 / 4 + k) * 32 + lane];
+    if (li > 0.f) {  // (a part that a row sees no key of holds no O)
+      const float top = fmaxf(m, mi), old = ex2(m - top), f = ex2(mi - top);
+      m = top;
+      l = l * old + li * f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        o[4 * k] = fmaf(x[k].x, f, o[4 * k] * old);
+        o[4 * k + 1] = fmaf(x[k].y, f, o[4 * k + 1] * old);
+        o[4 * k + 2] = fmaf(x[k].z, f, o[4 * k + 2] * old);
+        o[4 * k + 3] = fmaf(x[k].w, f, o[4 * k + 3] * old);
+      }
+    }
+  }
+  const int to = reinterpret_cast<const int*>(first)[32 * (D + 2) + lane];
+  if (to < 0) return;
+  const int head = to % p.a.heads / p.group;
+  const float inv = l > 0.f ? (p.a.cache.v_scale ? p.a.cache.v_scale[head] : 1.f) / l : 0.f;
+  uint16_t* dst = p.a.out + (size_t)to * D + d0;
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+    *reinterpret_cast<uint4*>(dst + i) =
+        make_uint4(pack16<kB>(o[i] * inv, o[i + 1] * inv), pack16<kB>(o[i + 2] * inv, o[i + 3] * inv),
+                   pack16<kB>(o[i + 4] * inv, o[i + 5] * inv), pack16<kB>(o[i + 6] * inv, o[i + 7] * inv));
+  if (p.a.lse && d0 == 0) p.a.lse[to] = l > 0.f ? m * kLn2 + logf(l) : -INFINITY;
+}
+
 template <bool kB, bool k8, int D>
 cudaError_t launch(PromptArgs p, unsigned blocks, cudaStream_t stream) {
   // the caches as rows of D values, copied in panels of 64 dimensions by up to
@@ -959,7 +979,9 @@ cudaError_t launch(PromptArgs p, unsigned blocks, cudaStream_t stream) {
   auto kern = attn_prompt_kernel<kB, k8, D>;
   cudaError_t e = set_max_smem_once(reinterpret_cast<const void*>(kern), kSmem<D>);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(blocks), dim3(kThreads), kSmem<D>, stream, p, map_k, map_v, map_q);
+  e = launch_pdl(kern, dim3(blocks), dim3(kThreads), kSmem<D>, stream, p, map_k, map_v, map_q);
+  if (e != cudaSuccess || p.most_parts < 2) return e;
+  return launch_pdl(attn_join_kernel<kB, D>, dim3(blocks * 8), dim3(D), 0, stream, p);
 }
 
 constexpr size_t kFlagBytes = 32768;
@@ -972,7 +994,7 @@ bool may_split(int tokens, int group, int kv_heads, int sms) {
 }  // namespace
 
 size_t attn_prompt_workspace_bytes(int tokens, int group, int kv_heads, int head_dim, int sms) {
-  return kFlagBytes + (may_split(tokens, group, kv_heads, sms) ? (size_t)sms * 8 * 32 * (head_dim + 2) * sizeof(float) : 0);
+  return kFlagBytes + (may_split(tokens, group, kv_heads, sms) ? (size_t)sms * 8 * 32 * (head_dim + 4) * sizeof(float) : 0);
 }
 
 cudaError_t launch_attn_prompt(const AttnArgs& args, int head_dim, bool bf16, bool e4m3, void* workspace, int sms,
@@ -989,7 +1011,6 @@ cudaError_t launch_attn_prompt(const AttnArgs& args, int head_dim, bool bf16, bo
   p.mult = fmaxf(fabsf(args.scale) * kLog2e, 1e-37f);
   p.negate = args.scale < 0.f;
   p.queue = static_cast<int*>(workspace);
-  p.arrived = p.queue + 2;
   p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kFlagBytes);
   // a block per SM, or as many as there can be units (whole ones of all rows,
   // and a ragged one per sequence) where none is long enough for two parts

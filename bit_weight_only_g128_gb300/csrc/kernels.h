@@ -146,8 +146,8 @@ cudaError_t launch_rope_append(const uint16_t* qkv, long long ld, const float* t
 // Attention over the paged cache (AttnArgs: layer.cuh).
 struct AttnArgs;
 // Causal attention of prompts on the tensor cores. The workspace's flag area
-// holds the queue of its units and the arrivals of split ones (zero between
-// calls), the rest the parts of those.
+// holds the queue of its units (zero between calls), the rest the parts of
+// split ones.
 size_t attn_prompt_workspace_bytes(int tokens, int group, int kv_heads, int head_dim, int sms);
 cudaError_t launch_attn_prompt(const AttnArgs& args, int head_dim, bool bf16, bool e4m3, void* workspace, int sms,
                                cudaStream_t stream);
