@@ -21,8 +21,8 @@
 //                    five slots: tile copies (TMA) of the pages' rows;
 //                    16 bytes at a time where a tile ends beyond the sequence
 //                    (those rows as zeros, so that what the cache holds there
-//                    meets P = 0 as 0) and for e4m3 codes, which become fp16
-//                    on the way
+//                    meets P = 0 as 0). e4m3 codes are copied to two tiles
+//                    beside a ring of four slots and widened to fp16 from there
 //   warps 12, 13     the units (warp 12) and their queries: tile copies where
 //                    the group divides 128, else 16 bytes at a time
 //   warps 14, 15     tcgen05.mma of tile 0, 1: S from shared memory, O += P V
@@ -48,7 +48,7 @@ using namespace tc;
 
 constexpr int kThreads = 512;
 constexpr int kTile = 128;  // rows of a tile, and keys of a tile
-constexpr int kSlots = 5;
+constexpr int kMostSlots = 5;
 constexpr int kPanel = kTile * 128;  // bytes of 64 dimensions of 128 rows
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kLeast = 4;    // key tiles of a part: as long as what a part costs beside them
@@ -57,8 +57,8 @@ constexpr float kSlack = 8.f;  // log2 of how far a row's maximum may run ahead
 // barriers, [2]: of the row tiles, or of the two places of a unit's description
 enum {
   kFull = 0,                   // [kSlots] a key or value tile is there
-  kEmpty = kFull + kSlots,     // [kSlots] both row tiles' products have read it
-  kUnit = kEmpty + kSlots,     // [2] a unit is described
+  kEmpty = kFull + kMostSlots, // [kSlots] both row tiles' products have read it
+  kUnit = kEmpty + kMostSlots,     // [2] a unit is described
   kUnitFree = kUnit + 2,       // [2] every role has read it
   kQueries = kUnitFree + 2,    // [2] the queries are there
   kQueriesFree = kQueries + 2, // [2] the unit's last scores have read them
@@ -68,7 +68,9 @@ enum {
   kOutFree = kOut + 2,         // [2] O has been read
   kTurn = kOutFree + 2,        // [2] the tile's products may be issued
   kCopiers = kTurn + 2,        // the four copying warps meet
-  kDrain = kCopiers + 1,       // [2] products in flight, when giving up
+  kCodes = kCopiers + 1,       // [2] a tile of e4m3 codes is there
+  kCodesFree = kCodes + 2,     // [2] it has been read
+  kDrain = kCodesFree + 2,       // [2] products in flight, when giving up
   kBars = kDrain + 2
 };
 constexpr int kReaders = 8 + 4 + 1 + 2;  // warps that read a unit's description
@@ -86,13 +88,12 @@ struct Control {
   Unit unit[2];
   uint32_t tmem;
   int abort;
-  float power[2 * kTile];  // what a row's queries were divided by (bf16 over e4m3)
 };
 
 template <int D>
 constexpr int kTileBytes = D / 64 * kPanel;
 template <int D>
-constexpr int kSmem = (2 + kSlots) * kTileBytes<D> + (int)sizeof(Control) + 1024;
+constexpr int kSmem = (2 + kMostSlots) * kTileBytes<D> + (int)sizeof(Control) + 1024;
 static_assert(kSmem<128> <= 227 * 1024, "one block's shared memory");
 
 // A warp's part: O as [D / 4][32 rows] of four, maxima, sums, the rows' places
@@ -106,7 +107,6 @@ struct PromptArgs {
   int group;
   float mult;      // |scale| log2 e
   uint32_t negate;  // scale < 0
-  int tiled;        // the maps of the keys and values are there
   int q_tiled;      // the map of the queries is there
   int* queue;       // next unit, blocks that are through; zero between calls
   float* partial;   // [blocks][8 warps] of kPartFloats, where units can be split
@@ -258,21 +258,29 @@ __device__ __forceinline__ uint4 widen(uint32_t lo, uint32_t hi) {
   return v;
 }
 
-// kB: 16-bit values are bf16, else fp16; k8: e4m3 cache. Its products are in
-// fp16, which holds every code; bf16 queries are then divided by a power of
-// two per row that brings them into fp16's range.
+// And to bf16 (exact).
+__device__ __forceinline__ uint4 widen_bf16(uint32_t lo, uint32_t hi) {
+  const uint4 h = widen(lo, hi);
+  const float2 a = unpack16<false>(h.x), b = unpack16<false>(h.y), c = unpack16<false>(h.z), d = unpack16<false>(h.w);
+  return make_uint4(pack16<true>(a.x, a.y), pack16<true>(b.x, b.y), pack16<true>(c.x, c.y), pack16<true>(d.x, d.y));
+}
+
+// kB: 16-bit values are bf16, else fp16; k8: e4m3 cache. The scores' product
+// is in the queries' type, P V in the cache's or, over e4m3 codes, in fp16
+// (both types hold every code).
 template <bool kB, bool k8, int D>
 __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptArgs p, const __grid_constant__ CUtensorMap map_k,
                                                                  const __grid_constant__ CUtensorMap map_v,
                                                                  const __grid_constant__ CUtensorMap map_q) {
   constexpr int kBytes = kTileBytes<D>;
-  constexpr bool kP = kB && !k8;  // products in bf16
+  constexpr bool kP = kB && !k8;  // P V in bf16
   constexpr int kChunks = D / 8;  // 16-byte chunks of a row
+  constexpr int kSlots = k8 ? kMostSlots - 1 : kMostSlots;  // (two tiles of codes in place of one)
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = (uint32_t)__cvta_generic_to_shared(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;  // queries [2], ring [kSlots]
-  const uint32_t ring = base + 2 * kBytes;
-  Control& ctl = *reinterpret_cast<Control*>(smem_raw + (ring - raw) + kSlots * kBytes);
+  const uint32_t ring = base + 2 * kBytes, codes = ring + kSlots * kBytes;
+  Control& ctl = *reinterpret_cast<Control*>(smem_raw + (ring - raw) + kMostSlots * kBytes);
   const uint32_t bars = (uint32_t)__cvta_generic_to_shared(&ctl.bars[0]);
   auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
   const AttnArgs& a = p.a;
@@ -288,13 +296,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
       mbar_init(bar(kUnit + t), 1);
       mbar_init(bar(kUnitFree + t), kReaders);
       mbar_init(bar(kQueries + t), p.q_tiled ? 1 : 64);
-      mbar_init(bar(kQueriesFree + t), kB && k8 ? 129 : 1);
+      mbar_init(bar(kQueriesFree + t), 1);
       mbar_init(bar(kScores + t), 1);
       mbar_init(bar(kProbs + t), 128);
       mbar_init(bar(kProbs + 2 + t), 128);
       mbar_init(bar(kOut + t), 1);
       mbar_init(bar(kOutFree + t), 128);
       mbar_init(bar(kTurn + t), 1);
+      mbar_init(bar(kCodes + t), 1);
+      mbar_init(bar(kCodesFree + t), 128);
       mbar_init(bar(kDrain + t), 1);
     }
     mbar_init(bar(kCopiers), 128);
@@ -353,12 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
       const int limit = live ? unit.len - unit.fresh + token + 1 - unit.j0 * kTile : 0x7fffffff;
       const bool idle = __all_sync(0xffffffffu, !live);
       int to = live ? (unit.first + token) * a.heads + head : -1;
-      float mult = p.mult * (k8 ? a.cache.k_scale[unit.head] : 1.f);
-      if (kB && k8) {
-        if (!(ok = warp_wait(kQueries + t, (uint32_t)u & 1u, kErrEpilogue))) break;
-        mult *= ctl.power[t * kTile + (tid & 127)];
-        mbar_arrive(bar(kQueriesFree + t));
-      }
+      const float mult = p.mult * (k8 ? a.cache.k_scale[unit.head] : 1.f);
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < nt; ++j) {
         if (!(ok = warp_wait(kScores + t, score_phase, kErrEpilogue))) break;
@@ -552,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
           // a lane for each page and panel. Small pages' copies (16 of them
           // for 16 tokens) are shared among the four warps: a warp issues its
           // lanes' copies one after another.
-          const int whole = p.tiled ? max(0, min(most, len / kTile - unit.j0)) : 0;
+          const int whole = max(0, min(most, len / kTile - unit.j0));
           const int end = count + 2 * whole;
           const int box = min(1 << shift, kTile), boxes = kTile / box, copies = D / 64 * boxes;
           const int sharing = copies > 4 ? 4 : 1, each = copies / sharing;
@@ -576,8 +581,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
             }
           }
           count = end;
-          // the ragged last tile (every tile where there are no maps): 16
-          // bytes at a time, rows beyond the sequence as zeros
+          // the ragged last tile: 16 bytes at a time, rows beyond the sequence
+          // as zeros
           if (whole < most) {
             meet();  // the first warp has come as far: a slot's phase is known
             const int r0 = v / kChunks, c = v % kChunks;
@@ -614,30 +619,50 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
             }
           }
         } else {
-          // A thread copies one 16-code piece c of the rows r0 + x * kStride of
-          // a tile's eight groups of 16 rows (a group lies in one page): the
-          // group is a constant of x and of the warp.
+          // tile copies of the pages' codes, one tile ahead; then a thread
+          // widens the 16-code piece c of the rows r0 + x * kStride
           constexpr int kPieces = D / 16, kStride = 128 / kPieces, kLoads = kTile / kStride;
           const int r0 = v / kPieces, c = v % kPieces;
-          unsigned long long group = 0;
-          for (int i = 0; i < 2 * most; ++i, ++count) {
-            const int j = unit.j0 + (i >> 1);
-            if (!(i & 1)) group = row_of_or_0(row_of, j * kTile + 16 * (lane & 7), len) * D;
-            const uint8_t* src = static_cast<const uint8_t*>(i & 1 ? a.cache.v : a.cache.k) + (r0 & 15) * D + c * 16;
-            const bool inside = (j + 1) * kTile <= len;
+          const int box = min(1 << shift, kTile), boxes = kTile / box;
+          const int sharing = boxes >= 4 ? 4 : 1, each = boxes / sharing, mine = (warp - 8) * each + lane;
+          // (the page of the next tile is looked up while this one is copied)
+          auto look = [&](int j) { return row_of_or_0(row_of, (unit.j0 + j) * kTile + min(mine, boxes - 1) * box, len); };
+          unsigned long long row = 0, ahead = most > 0 ? look(0) : 0;
+          const int start = count;
+          auto copy = [&](int i) {  // tile i of the unit
+            const int n = start + i, at = n & 1;
+            if (!(i & 1)) {
+              row = ahead;
+              if (i / 2 + 1 < most) ahead = look(i / 2 + 1);
+            }
+            if (n >= 2 && !warp_wait(kCodesFree + at, (uint32_t)(n / 2 - 1) & 1u, kErrProducer)) return false;
+            if (mine == 0) mbar_expect_tx(bar(kCodes + at), kTile * D);
+            __syncwarp();
+            if (lane < each)
+              tma_load_2d(codes + at * (kTile * D) + mine * box * D, i & 1 ? &map_v : &map_k, 0, (int)row, bar(kCodes + at));
+            return true;
+          };
+          if (most > 0 && warp - 8 < sharing) ok = copy(0);
+          for (int i = 0; i < 2 * most && ok; ++i, ++count) {
+            if (i + 1 < 2 * most && warp - 8 < sharing && !(ok = copy(i + 1))) break;
+            const int key0 = (unit.j0 + (i >> 1)) * kTile, at = count & 1;
+            const bool inside = key0 + kTile <= len;
+            if (!(ok = warp_wait(kCodes + at, (uint32_t)(count / 2) & 1u, kErrProducer))) break;
             uint4 x4[kLoads];
 #pragma unroll
             for (int x = 0; x < kLoads; ++x) {
-              const uint8_t* from = src + __shfl_sync(0xffffffffu, group, x * (kStride / 16) + (r0 >> 4));
-              x4[x] = make_uint4(0, 0, 0, 0);
-              if (inside || j * kTile + r0 + x * kStride < len) x4[x] = ldg_stream(reinterpret_cast<const uint4*>(from));
+              x4[x] = lds128(codes + at * (kTile * D) + (r0 + x * kStride) * D + c * 16);
+              if (!inside && key0 + r0 + x * kStride >= len) x4[x] = make_uint4(0, 0, 0, 0);
             }
+            mbar_arrive(bar(kCodesFree + at));
             if (!(ok = wait_slot())) break;
             const uint32_t dst = ring + slot_of() * kBytes;
             const uint32_t lo_at = dst + chunk_at(r0, 2 * c), hi_at = dst + chunk_at(r0, 2 * c + 1);
 #pragma unroll
             for (int x = 0; x < kLoads; ++x) {  // kStride is a multiple of 8: the swizzle stays
-              const uint4 lo = widen(x4[x].x, x4[x].y), hi = widen(x4[x].z, x4[x].w);
+              const bool b16 = kB && !(i & 1);
+              const uint4 lo = b16 ? widen_bf16(x4[x].x, x4[x].y) : widen(x4[x].x, x4[x].y);
+              const uint4 hi = b16 ? widen_bf16(x4[x].z, x4[x].w) : widen(x4[x].z, x4[x].w);
               sts128(lo_at + x * kStride * 128, lo.x, lo.y, lo.z, lo.w);
               sts128(hi_at + x * kStride * 128, hi.x, hi.y, hi.z, hi.w);
             }
@@ -779,24 +804,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
           for (int r = w / kChunks; r < kTile; r += kStride) {
             const bool valid = row < unit.fresh * p.group;
             const uint32_t dst = base + t * kBytes + chunk_at(r, c);
-            if (kB && k8) {
-              uint4 x = make_uint4(0, 0, 0, 0);
-              if (valid) x = *reinterpret_cast<const uint4*>(src);
-              const float2 f[4] = {unpack16<true>(x.x), unpack16<true>(x.y), unpack16<true>(x.z), unpack16<true>(x.w)};
-              float top = 0.f;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) top = fmaxf(top, fmaxf(fabsf(f[k].x), fabsf(f[k].y)));
-#pragma unroll
-              for (int o = kChunks / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-              const int e = top > 0.f ? ilogbf(top) : 0;  // |q| 2^-e < 2
-              uint32_t y[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) y[k] = pack16<false>(scalbnf(f[k].x, -e), scalbnf(f[k].y, -e));
-              sts128(dst, y[0], y[1], y[2], y[3]);
-              if (c == 0) ctl.power[t * kTile + r] = scalbnf(1.f, e);
-            } else {
-              cp16(dst, valid ? src : a.q, valid);
-            }
+            cp16(dst, valid ? src : a.q, valid);
             row += kStride;
             src += step;
             head += step_head;
@@ -823,7 +831,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
       constexpr uint32_t kDescHi = (uint32_t)(1024 >> 4) | (1u << 14) | (2u << 29);  // the upper half of both descriptors
       const int t = warp - 14;
       const uint32_t scores = tmem + t * kTile, out = tmem + 256 + t * D;
-      const uint32_t idesc_s = f16_idesc(kTile, kTile, kP) | (p.negate << 13);
+      const uint32_t idesc_s = f16_idesc(kTile, kTile, kB) | (p.negate << 13);
       const uint32_t idesc_o = f16_idesc(kTile, D, kP) | (1u << 16);  // B with the dimensions innermost
       const uint32_t q_lo = (((base + t * kBytes) & 0x3FFFFu) >> 4) | (1u << 16);  // K-major
       const uint32_t k_lo = ((ring & 0x3FFFFu) >> 4) | (1u << 16);
@@ -960,21 +968,21 @@ __global__ void __launch_bounds__(D) attn_join_kernel(const PromptArgs p) {
 
 template <bool kB, bool k8, int D>
 cudaError_t launch(PromptArgs p, unsigned blocks, cudaStream_t stream) {
-  // the caches as rows of D values, copied in panels of 64 dimensions by up to
-  // 128 rows of a page (row numbers are 32-bit coordinates)
+  // the caches as rows of D values, copied by up to 128 rows of a page, in
+  // panels of 64 dimensions or whole rows of codes (row numbers are 32-bit
+  // coordinates: the cache's rows are below 2^31)
   CUtensorMap map_k = {}, map_v = {}, map_q = {};
   const long long rows = ((long long)p.a.cache.pages * p.a.cache.kv_heads) << p.a.cache.page_shift;
-  p.tiled = !k8 && rows <= 0x7fffffff;
-  if (p.tiled) {
-    const auto dt = kB ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    const uint32_t box = 1u << (p.a.cache.page_shift < 7 ? p.a.cache.page_shift : 7);
-    if (!encode_tensor_map(&map_k, p.a.cache.k, dt, 2, D, (uint64_t)rows, 64, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_tensor_map(&map_v, p.a.cache.v, dt, 2, D, (uint64_t)rows, 64, box, CU_TENSOR_MAP_SWIZZLE_128B))
-      return cudaErrorInvalidValue;
-  }
+  const auto dt = k8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                     : kB ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const auto swizzle = k8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
+  const uint32_t box = 1u << (p.a.cache.page_shift < 7 ? p.a.cache.page_shift : 7);
+  if (!encode_tensor_map(&map_k, p.a.cache.k, dt, k8 ? 1 : 2, D, (uint64_t)rows, k8 ? D : 64, box, swizzle) ||
+      !encode_tensor_map(&map_v, p.a.cache.v, dt, k8 ? 1 : 2, D, (uint64_t)rows, k8 ? D : 64, box, swizzle))
+    return cudaErrorInvalidValue;
   // the queries as [tokens][heads][D], where a tile of 128 rows is whole
   // tokens of a key/value head's group
-  p.q_tiled = !(kB && k8) && kTile % p.group == 0;
+  p.q_tiled = kTile % p.group == 0;
   if (p.q_tiled && !encode_query_map(&map_q, p.a.q, kB, D, p.a.heads, p.a.rows, p.a.ldq, p.group)) return cudaErrorInvalidValue;
   auto kern = attn_prompt_kernel<kB, k8, D>;
   cudaError_t e = set_max_smem_once(reinterpret_cast<const void*>(kern), kSmem<D>);

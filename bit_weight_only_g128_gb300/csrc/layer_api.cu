@@ -39,6 +39,8 @@ int check_cache(const void* k, const void* v, const float* k_scale, const float*
   if (head_dim != 64 && head_dim != 128) return fail(W4A16_ERR_UNSUPPORTED_SHAPE, "head_dim=%d is neither 64 nor 128", head_dim);
   if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1)))
     return fail(W4A16_ERR_UNSUPPORTED_SHAPE, "page_size=%d is not 16, 32, 64, 128 or 256", page_size);
+  if ((long long)pages * kv_heads * page_size > 0x7fffffffll)
+    return fail(W4A16_ERR_UNSUPPORTED_SHAPE, "%d pages of %d x %d rows: a cache of 2^31 rows or more", pages, kv_heads, page_size);
   if (!k || !v) return fail(W4A16_ERR_INVALID_ARG, "null cache pointer");
   if (!aligned(k, 16) || !aligned(v, 16)) return fail(W4A16_ERR_MISALIGNED, "alignment: the caches need 16 bytes");
   const bool e4m3 = (flags & W4A16_CACHE_E4M3) != 0;

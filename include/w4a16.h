@@ -377,7 +377,7 @@ int w4a16_rms_norm(const uint16_t* x, int64_t x_stride, const uint16_t* residual
  * W4A16_CACHE_E4M3 8-bit floats (e4m3) whose value is code * k_scale[head]
  * (v_scale[head]), fp32 [kv_heads], positive; not null then and null otherwise.
  * page_size 16, 32, 64, 128 or 256; head_dim 64 or 128; heads a multiple of
- * kv_heads, at most 1024; query head h reads the keys and values of head
+ * kv_heads, at most 1024; pages * kv_heads * page_size below 2^31; query head h reads the keys and values of head
  * h / (heads / kv_heads). Token i of a sequence lies at place i % page_size
  * of the page that entry i / page_size of its page table names. */
 #define W4A16_CACHE_E4M3 0x1000
