@@ -100,7 +100,7 @@ static_assert(kSmem<128> <= 227 * 1024, "one block's shared memory");
 // in the output (or -1), and the number of parts to join from this one on (0:
 // none).
 template <int D>
-constexpr int kPartFloats = 32 * (D + 4);
+constexpr int kPartFloats = 32 * (D + 4);  // (the last 32: one number)
 
 struct PromptArgs {
   AttnArgs a;
@@ -460,8 +460,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
       if (!ok) break;
       // (Loops: code that runs once per unit is fetched anew every time.)
       float* mine = p.partial + (size_t)(unit.slot * 8 + warp) * kPartFloats<D>;
-      if (p.most_parts > 1 && unit.slot < (int)gridDim.x)
-        reinterpret_cast<int*>(mine)[32 * (D + 3) + lane] = unit.part == 0 && unit.parts > 1 && !idle ? unit.parts : 0;
+      if (p.most_parts > 1 && unit.slot < (int)gridDim.x && lane == 0)
+        reinterpret_cast<int*>(mine)[32 * (D + 3)] = unit.part == 0 && unit.parts > 1 && !idle ? unit.parts : 0;
       if (unit.parts > 1) {
         if (!idle) {
           if (nt > 0) {
@@ -708,14 +708,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
         }
         --group;
       }
-      // places for parts per unit, as many as there are blocks
-      const int count = total * a.cache.kv_heads;
-      const int split = count > 0 && count < (int)gridDim.x ? max(1, min((int)gridDim.x / count, p.most_parts)) : 1;
+      // parts per unit: as many as there are blocks for. (Two rounds of more and
+      // smaller parts, where that is shorter, gained 2% at 300 rows behind 4000
+      // of 64 heads over 8: 80 units on 152 blocks.)
+      const int count = total * a.cache.kv_heads, grid = (int)gridDim.x;
+      const int split = count > 0 && count < grid ? max(1, min(grid / count, p.most_parts)) : 1;
       auto no_part = [&](int i) {  // place i holds nothing to join
-        if (p.most_parts > 1 && i >= 0 && i < (int)gridDim.x)
-#pragma unroll 1
-          for (int k = 0; k < 8; ++k)
-            reinterpret_cast<int*>(p.partial + (size_t)(i * 8 + k) * kPartFloats<D>)[32 * (D + 3) + lane] = 0;
+        if (p.most_parts > 1 && i >= 0 && i < grid && lane < 8)
+          reinterpret_cast<int*>(p.partial + (size_t)(i * 8 + lane) * kPartFloats<D>)[32 * (D + 3)] = 0;
       };
       const int w = tid - 384, c = w % kChunks;
       constexpr int kStride = 64 / kChunks;
@@ -738,7 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
                 to.valid = 0;
                 // the last block to come here leaves the queue zero
                 __threadfence();
-                if (atomicAdd(p.queue + 1, 1) == (int)gridDim.x - 1) p.queue[0] = p.queue[1] = 0;
+                if (atomicAdd(p.queue + 1, 1) == grid - 1) p.queue[0] = p.queue[1] = 0;
               }
               break;
             }
@@ -927,8 +927,8 @@ __global__ void __launch_bounds__(D) attn_join_kernel(const PromptArgs p) {
   const int lane = threadIdx.x & 31, d0 = threadIdx.x & ~31;
   const float* first = p.partial + (size_t)blockIdx.x * kPartFloats<D>;
   constexpr size_t kNext = (size_t)8 * kPartFloats<D>;
-  const int parts = reinterpret_cast<const int*>(first)[32 * (D + 3) + lane];
-  if (parts == 0) return;  // (the same in all lanes)
+  const int parts = reinterpret_cast<const int*>(first)[32 * (D + 3)];
+  if (parts == 0) return;
   float m = -INFINITY, l = 0.f;
   float o[32];
 #pragma unroll
@@ -966,6 +966,25 @@ __global__ void __launch_bounds__(D) attn_join_kernel(const PromptArgs p) {
   if (p.a.lse && d0 == 0) p.a.lse[to] = l > 0.f ? m * kLn2 + logf(l) : -INFINITY;
 }
 
+// Tensor map of a row-major array: dims and box innermost first, strides of
+// the outer dimensions in bytes. Encoded by each call: half a microsecond, and
+// nothing is kept by a buffer's address.
+bool encode_tiles(CUtensorMap* out, const void* ptr, CUtensorMapDataType type, int rank, const cuuint64_t (&dims)[3],
+                  const cuuint64_t (&strides)[2], const cuuint32_t (&box)[3], CUtensorMapSwizzle swizzle) {
+  static const PFN_cuTensorMapEncodeTiled_v12000 encode = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      return nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  }();
+  const cuuint32_t steps[3] = {1, 1, 1};
+  return encode && encode(out, type, (cuuint32_t)rank, const_cast<void*>(ptr), dims, strides, box, steps,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <bool kB, bool k8, int D>
 cudaError_t launch(PromptArgs p, unsigned blocks, cudaStream_t stream) {
   // the caches as rows of D values, copied by up to 128 rows of a page, in
@@ -973,17 +992,23 @@ cudaError_t launch(PromptArgs p, unsigned blocks, cudaStream_t stream) {
   // coordinates: the cache's rows are below 2^31)
   CUtensorMap map_k = {}, map_v = {}, map_q = {};
   const long long rows = ((long long)p.a.cache.pages * p.a.cache.kv_heads) << p.a.cache.page_shift;
-  const auto dt = k8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                     : kB ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const auto type16 = kB ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const auto type = k8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : type16;
   const auto swizzle = k8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
-  const uint32_t box = 1u << (p.a.cache.page_shift < 7 ? p.a.cache.page_shift : 7);
-  if (!encode_tensor_map(&map_k, p.a.cache.k, dt, k8 ? 1 : 2, D, (uint64_t)rows, k8 ? D : 64, box, swizzle) ||
-      !encode_tensor_map(&map_v, p.a.cache.v, dt, k8 ? 1 : 2, D, (uint64_t)rows, k8 ? D : 64, box, swizzle))
+  const cuuint64_t dims[3] = {D, (cuuint64_t)rows, 1}, strides[2] = {D * (k8 ? 1 : 2), 0};
+  const cuuint32_t box[3] = {k8 ? D : 64, 1u << (p.a.cache.page_shift < 7 ? p.a.cache.page_shift : 7), 1};
+  if (!encode_tiles(&map_k, p.a.cache.k, type, 2, dims, strides, box, swizzle) ||
+      !encode_tiles(&map_v, p.a.cache.v, type, 2, dims, strides, box, swizzle))
     return cudaErrorInvalidValue;
   // the queries as [tokens][heads][D], where a tile of 128 rows is whole
   // tokens of a key/value head's group
   p.q_tiled = kTile % p.group == 0;
-  if (p.q_tiled && !encode_query_map(&map_q, p.a.q, kB, D, p.a.heads, p.a.rows, p.a.ldq, p.group)) return cudaErrorInvalidValue;
+  if (p.q_tiled) {
+    const cuuint64_t q_dims[3] = {D, (cuuint64_t)p.a.heads, (cuuint64_t)p.a.rows};
+    const cuuint64_t q_strides[2] = {D * 2, (cuuint64_t)p.a.ldq * 2};
+    const cuuint32_t q_box[3] = {64, (cuuint32_t)p.group, (cuuint32_t)(kTile / p.group)};
+    if (!encode_tiles(&map_q, p.a.q, type16, 3, q_dims, q_strides, q_box, CU_TENSOR_MAP_SWIZZLE_128B)) return cudaErrorInvalidValue;
+  }
   auto kern = attn_prompt_kernel<kB, k8, D>;
   cudaError_t e = set_max_smem_once(reinterpret_cast<const void*>(kern), kSmem<D>);
   if (e != cudaSuccess) return e;

@@ -101,13 +101,6 @@ bool tc_pair_config(int M, int K, int group, int out[7]);
 bool cached_tensor_map(CUtensorMap* out, const void* ptr, CUtensorMapDataType dt, int esize,
                        uint64_t dims0, uint64_t dims1, uint32_t box0, uint32_t box1,
                        CUtensorMapSwizzle swizzle);
-// The same map encoded anew, without the cache.
-bool encode_tensor_map(CUtensorMap* out, const void* ptr, CUtensorMapDataType dt, int esize,
-                       uint64_t dims0, uint64_t dims1, uint32_t box0, uint32_t box1,
-                       CUtensorMapSwizzle swizzle);
-// 3-D tensor map of queries [tokens][heads][dim] (row stride ld) with box
-// [128 / group tokens][group heads][64] and the 128-byte swizzle.
-bool encode_query_map(CUtensorMap* out, const void* ptr, bool bf16, int dim, int heads, int tokens, long long ld, int group);
 // 3-D tensor map of the packed weights as [N/16 strips][K/64 atoms x 4 rows]
 // [32 words] with the 128-byte swizzle; a box is `sa` atoms of 8 strips (128
 // columns). From the same cache.

@@ -229,11 +229,12 @@ cudaError_t launch_norm(const NormArgs& a, cudaStream_t stream) {
                    al(a.residual) && al(a.weight) && al(a.y) && al(a.codes) && al(a.aq) && al(a.h);
   if (!vec) return launch_pdl(rms_norm_any_kernel<kB>, dim3((unsigned)a.M), dim3(256), 0, stream, a);
   const int nv = a.K / 8;
-  // Vectors per thread: one while all rows' threads fit the device at once
-  // (then a row's chain of loads, sums and stores is what counts), up to four
-  // beyond that (then the bytes in flight of the resident blocks; 8192
-  // channels x 4096 rows: 44 us with one, 42 with four).
-  int vecs = nv <= 1024 ? 1 : nv <= 2048 ? 2 : 4;
+  // Vectors per thread: one in short rows; two while all rows' threads fit the
+  // device at once (then a row's chain of loads, sums and stores is what
+  // counts, and fewer warps join sooner: 333 x 5120 codes 4.4 us with two, 5.2
+  // with one, 6.1 with four); four beyond that (bytes in flight of the resident
+  // blocks: 4096 x 8192 41.6 us with four, 47.7 with two, 50.9 with one).
+  int vecs = nv <= 128 ? 1 : nv <= 2048 ? 2 : 4;
   while (vecs < 4 && (long long)a.M * ((nv + vecs - 1) / vecs) > (long long)device_sms() * 2048) vecs *= 2;
   int threads = ((nv + vecs - 1) / vecs + 31) / 32 * 32;
   int rows = threads >= 128 ? 1 : 128 / threads;

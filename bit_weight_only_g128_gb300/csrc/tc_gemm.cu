@@ -776,19 +776,6 @@ CUtensorMap g_maps[kMapCache];
 int g_map_used = 0, g_map_next = 0;
 
 // A densely packed row-major array of rank 2 or 3 (dims[0] innermost).
-bool encode_map(CUtensorMap* out, const void* ptr, CUtensorMapDataType dt, int esize, int rank,
-                const uint64_t (&dims)[3], const uint32_t (&box)[3], CUtensorMapSwizzle swizzle) {
-  PFN_cuTensorMapEncodeTiled_v12000 encode = encode_fn();
-  if (!encode) return false;
-  const cuuint64_t gdims[3] = {(cuuint64_t)dims[0], (cuuint64_t)dims[1], (cuuint64_t)dims[2]};
-  const cuuint64_t strides[2] = {(cuuint64_t)dims[0] * esize, (cuuint64_t)dims[0] * dims[1] * esize};
-  const cuuint32_t gbox[3] = {box[0], box[1], box[2]};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return encode(out, dt, (cuuint32_t)rank, const_cast<void*>(ptr), gdims, strides, gbox, estr,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 bool cached_map(CUtensorMap* out, const void* ptr, CUtensorMapDataType dt, int esize, int rank,
                 const uint64_t (&dims)[3], const uint32_t (&box)[3], CUtensorMapSwizzle swizzle) {
   const MapKey key = {ptr, {dims[0], dims[1], dims[2]}, {box[0], box[1], box[2]}, (int)dt, rank,
@@ -801,7 +788,16 @@ bool cached_map(CUtensorMap* out, const void* ptr, CUtensorMapDataType dt, int e
         return true;
       }
   }
-  if (!encode_map(out, ptr, dt, esize, rank, dims, box, swizzle)) return false;
+  PFN_cuTensorMapEncodeTiled_v12000 encode = encode_fn();
+  if (!encode) return false;
+  const cuuint64_t gdims[3] = {(cuuint64_t)dims[0], (cuuint64_t)dims[1], (cuuint64_t)dims[2]};
+  const cuuint64_t strides[2] = {(cuuint64_t)dims[0] * esize, (cuuint64_t)dims[0] * dims[1] * esize};
+  const cuuint32_t gbox[3] = {box[0], box[1], box[2]};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  if (encode(out, dt, (cuuint32_t)rank, const_cast<void*>(ptr), gdims, strides, gbox, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return false;
   std::lock_guard<std::mutex> lock(g_map_mutex);
   const int slot = g_map_used < kMapCache ? g_map_used++ : (g_map_next++ % kMapCache);
   g_map_keys[slot] = key;
@@ -810,24 +806,6 @@ bool cached_map(CUtensorMap* out, const void* ptr, CUtensorMapDataType dt, int e
 }
 
 }  // namespace
-
-bool encode_tensor_map(CUtensorMap* out, const void* ptr, CUtensorMapDataType dt, int esize,
-                       uint64_t dims0, uint64_t dims1, uint32_t box0, uint32_t box1,
-                       CUtensorMapSwizzle swizzle) {
-  return encode_map(out, ptr, dt, esize, 2, {dims0, dims1, 1}, {box0, box1, 1}, swizzle);
-}
-
-bool encode_query_map(CUtensorMap* out, const void* ptr, bool bf16, int dim, int heads, int tokens, long long ld, int group) {
-  PFN_cuTensorMapEncodeTiled_v12000 encode = encode_fn();
-  if (!encode) return false;
-  const cuuint64_t gdims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)tokens};
-  const cuuint64_t strides[2] = {(cuuint64_t)dim * 2, (cuuint64_t)ld * 2};
-  const cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)(128 / group)};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return encode(out, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(ptr),
-                gdims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 
 bool cached_tensor_map(CUtensorMap* out, const void* ptr, CUtensorMapDataType dt, int esize,
                        uint64_t dims0, uint64_t dims1, uint32_t box0, uint32_t box1,
