@@ -13,7 +13,7 @@
 #include <string>
 
 #include <ATen/ATen.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -99,8 +99,13 @@ T* flat(const at::Tensor& t, const char* name, int64_t n, at::ScalarType type, c
   return static_cast<T*>(t.data_ptr());
 }
 
+// A new contiguous tensor on a CUDA device (without the dispatcher's round).
+at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const at::Device& dev) {
+  return at::detail::empty_cuda(shape, type, dev, std::nullopt);
+}
+
 at::Tensor result(PyObject* given, const char* name, at::IntArrayRef shape, at::ScalarType type, const at::Device& dev) {
-  if (given == Py_None) return at::empty(shape, at::TensorOptions().dtype(type).device(dev));
+  if (given == Py_None) return fresh(shape, type, dev);
   const at::Tensor& t = tensor(given, name);
   int64_t n = 1;
   for (int64_t s : shape) n *= s;
@@ -196,7 +201,7 @@ PyObject* rms_norm(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
       ldr = rows_of(res, "residual", K, type, dev);
       if (res.size(0) != M) refuse("residual has %lld rows, x has %lld", (long long)res.size(0), (long long)M);
       r = static_cast<uint16_t*>(res.data_ptr());
-      h = args[6] == Py_None ? at::empty({M, K}, x.options()) : tensor(args[6], "residual_out");
+      h = args[6] == Py_None ? fresh({M, K}, type, dev) : tensor(args[6], "residual_out");
       ldh = rows_of(h, "residual_out", K, type, dev);
       if (h.size(0) != M) refuse("residual_out has %lld rows, x has %lld", (long long)h.size(0), (long long)M);
       hp = static_cast<uint16_t*>(h.data_ptr());
@@ -217,7 +222,7 @@ PyObject* rms_norm(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     at::Tensor scale;
     float* sp = nullptr;
     if (int8 || codes) {
-      scale = at::empty({M}, at::TensorOptions().dtype(at::kFloat).device(dev));
+      scale = fresh({M}, at::kFloat, dev);
       sp = scale.data_ptr<float>();
     }
     void* yp = y.data_ptr();
@@ -338,7 +343,7 @@ PyObject* attend(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     const int want_lse = PyObject_IsTrue(args[7]);
     if (want_lse < 0) throw Raised();
     at::Tensor lse;
-    if (want_lse) lse = at::empty({T, heads}, at::TensorOptions().dtype(at::kFloat).device(dev));
+    if (want_lse) lse = fresh({T, heads}, at::kFloat, dev);
     float* lp = want_lse ? lse.data_ptr<float>() : nullptr;
     void* stream = stream_of(args[9], dev);
     const int t32 = int32_of(T, "tokens"), b32 = int32_of(batch, "batch"), h32 = int32_of(heads, "heads"),
