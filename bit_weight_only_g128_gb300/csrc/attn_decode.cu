@@ -21,6 +21,10 @@
 // B per clock and SM they need a twentieth of its rate; a tcgen05 tile of 128
 // rows would be filled with at most 16.
 //
+// Measured: 64 x 8190 tokens, 64 heads over 8, fp16: 306 us, 7020 GB/s; 16 x up
+// to 4096, 32 heads, bf16: 84 us, 6450 GB/s; 3 x 100003, 64 heads over 8, e4m3:
+// 94.6 us, 6490 GB/s; 1 x 777: 8.0 us.
+//
 // Work: all (sequence, head, step of four tiles) triples in one line, cut into
 // equal runs, one per block, from the lengths on the device. A run may begin
 // and end inside an item (sequence, head); such an item's parts go to the
@@ -676,7 +680,13 @@ cudaError_t launch(const DecodeArgs& p, int sms, cudaStream_t stream) {
   auto kern = attn_decode_kernel<kB, k8, D, kHeads>;
   cudaError_t e = set_max_smem_once(reinterpret_cast<const void*>(kern), (int)sizeof(Smem<D, kHeads>));
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3((unsigned)(kBlocks<kHeads> * sms)), dim3(kThreads), sizeof(Smem<D, kHeads>), stream, p);
+  // no more blocks than there can be steps (a block without one costs its
+  // launch: 1 x 777, 104 steps, 8.0 us with 104 blocks, 8.2 with all 456)
+  constexpr int kStep = kWarps * kTileBytes / (D * (k8 ? 1 : 2));
+  const long long longest = (((long long)p.a.max_pages << p.a.cache.page_shift) + kStep - 1) / kStep;
+  const long long steps = (longest > 0 ? longest : 1) * p.a.batch * p.a.cache.kv_heads * p.tiles;
+  const long long most = (long long)kBlocks<kHeads> * sms;
+  return launch_pdl(kern, dim3((unsigned)(steps < most ? steps : most)), dim3(kThreads), sizeof(Smem<D, kHeads>), stream, p);
 }
 
 template <bool kB, bool k8, int D>

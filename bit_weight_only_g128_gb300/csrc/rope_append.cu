@@ -12,6 +12,8 @@
 // Bound: HBM bytes (the qkv rows in, q and the cache rows out); for a few
 // tokens the chain slot/position - table row - store (latency). Each thread
 // takes both halves of a rotated pair as two 16-byte vectors, for two heads.
+// Measured: 4001 tokens of 64 heads over 8 into e4m3 27.0 us, 5840 GB/s; 16
+// tokens of 32 heads 1.8 us.
 #include "common.cuh"
 #include "kernels.h"
 #include "layer.cuh"

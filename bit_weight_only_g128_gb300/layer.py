@@ -5,9 +5,9 @@ product), the rotation of queries and keys with the append to a paged
 key-value cache, and the attention of single new tokens and of prompts over
 that cache. As the rest of the binding: thin calls of the C ABI
 (include/w4a16.h), no fallback, work on the current stream of the tensors'
-device unless `stream` is given. The calls' argument checks and allocations
-are native (csrc/binding.cpp): a call costs the host about as much as its
-launch. Call them through the package
+device unless `stream` is given (results and workspaces then belong to it).
+The calls' argument checks and allocations are native (csrc/binding.cpp): a
+call costs the host about as much as its launch. Call them through the package
 (``bit_weight_only_g128_gb300.rms_norm`` and so on).
 """
 from __future__ import annotations
@@ -167,7 +167,9 @@ def attn_decode(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: torc
     page numbers of each sequence, lens int32 [batch] its cached tokens (the
     new one among them; 0: zeros and -inf). scale defaults to
     head_dim^(-1/2). Returns out, or (out, lse) with lse float32 [batch,
-    heads] the logarithm of the softmax's sum. `workspace` as for gemm."""
+    heads] the logarithm of the softmax's sum. `workspace` as for gemm (a
+    captured graph keeps its address: the cached one of a stream is replaced
+    when a later call on the stream needs more)."""
     return (_native_module or _native()).attend(q, cache, table, None, lens, scale, out, return_lse, workspace, stream)
 
 

@@ -522,3 +522,12 @@ def test_other_streams():
     w4.attn_decode(src, cache, tab, n, out=out, stream=side)
     side.synchronize()
     assert same(out, want)
+    # results and workspace of a stream that has none yet, behind slow work on
+    # the current one (which their zeros must not wait for)
+    fresh = torch.cuda.Stream()
+    for _ in range(10):
+        big = big @ big * 1e-3
+    got = w4.attn_decode(src, cache, tab, n, stream=fresh)
+    norm = w4.rms_norm(src.view(2, 1024), w, stream=fresh)
+    fresh.synchronize()
+    assert same(got.clone(), want) and same(norm.clone(), want_norm)
