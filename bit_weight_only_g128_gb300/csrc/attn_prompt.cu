@@ -253,6 +253,12 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, ui
       : "memory");
 }
 
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
+}
+
 // Eight e4m3 codes to fp16 (exact).
 __device__ __forceinline__ uint4 widen(uint32_t lo, uint32_t hi) {
   uint4 v;
@@ -623,8 +629,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
           }
         } else {
           // tile copies of the pages' codes, one tile ahead; then a thread
-          // widens the 16-code piece c of the rows r0 + x * kStride
-          constexpr int kPieces = D / 16, kStride = 128 / kPieces, kLoads = kTile / kStride;
+          // widens the 8-code chunk c of the rows r0 + x * kStride (eight lanes
+          // then write the eight chunks of one row of a panel: no bank twice)
+          constexpr int kPieces = D / 8, kStride = 128 / kPieces, kLoads = kTile / kStride;
           const int r0 = v / kPieces, c = v % kPieces;
           const int box = min(1 << shift, kTile), boxes = kTile / box;
           const int sharing = boxes >= 4 ? 4 : 1, each = boxes / sharing, mine = (warp - 8) * each + lane;
@@ -651,23 +658,29 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
             const int key0 = (unit.j0 + (i >> 1)) * kTile, at = count & 1;
             const bool inside = key0 + kTile <= len;
             if (!(ok = warp_wait(kCodes + at, (uint32_t)(count / 2) & 1u, kErrProducer))) break;
-            uint4 x4[kLoads];
+            uint2 x2[kLoads];
 #pragma unroll
             for (int x = 0; x < kLoads; ++x) {
-              x4[x] = lds128(codes + at * (kTile * D) + (r0 + x * kStride) * D + c * 16);
-              if (!inside && key0 + r0 + x * kStride >= len) x4[x] = make_uint4(0, 0, 0, 0);
+              x2[x] = lds64(codes + at * (kTile * D) + (r0 + x * kStride) * D + c * 8);
+              if (!inside && key0 + r0 + x * kStride >= len) x2[x] = make_uint2(0, 0);
             }
             mbar_arrive(bar(kCodesFree + at));
             if (!(ok = wait_slot())) break;
             const uint32_t dst = ring + slot_of() * kBytes;
-            const uint32_t lo_at = dst + chunk_at(r0, 2 * c), hi_at = dst + chunk_at(r0, 2 * c + 1);
+            const uint32_t to = dst + chunk_at(r0, c);
+            // kStride is a multiple of 8: the swizzle stays
+            if (kB && !(i & 1)) {
 #pragma unroll
-            for (int x = 0; x < kLoads; ++x) {  // kStride is a multiple of 8: the swizzle stays
-              const bool b16 = kB && !(i & 1);
-              const uint4 lo = b16 ? widen_bf16(x4[x].x, x4[x].y) : widen(x4[x].x, x4[x].y);
-              const uint4 hi = b16 ? widen_bf16(x4[x].z, x4[x].w) : widen(x4[x].z, x4[x].w);
-              sts128(lo_at + x * kStride * 128, lo.x, lo.y, lo.z, lo.w);
-              sts128(hi_at + x * kStride * 128, hi.x, hi.y, hi.z, hi.w);
+              for (int x = 0; x < kLoads; ++x) {
+                const uint4 w = widen_bf16(x2[x].x, x2[x].y);
+                sts128(to + x * kStride * 128, w.x, w.y, w.z, w.w);
+              }
+            } else {
+#pragma unroll
+              for (int x = 0; x < kLoads; ++x) {
+                const uint4 w = widen(x2[x].x, x2[x].y);
+                sts128(to + x * kStride * 128, w.x, w.y, w.z, w.w);
+              }
             }
             fence_async_shared();
             mbar_arrive(bar(kFull + slot_of()));
