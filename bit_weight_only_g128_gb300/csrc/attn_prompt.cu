@@ -544,7 +544,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
       const int v = tid - 256;
       const int shift = a.cache.page_shift, mask = (1 << shift) - 1;
       bool ok = true;
-      int count = 0;  // tiles so far
+      int count = 0;   // tiles so far
+      int copied = 0;  // those before which this warp's tile copies have been issued
       uint32_t met = 0;
       auto slot_of = [&]() { return count % kSlots; };
       auto wait_slot = [&]() {
@@ -589,9 +590,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
               if (lane < each)
                 tma_load_2d(ring + slot_of() * kBytes + panel * kPanel + part * box * 128, values ? &map_v : &map_k, panel * 64,
                             (int)row, full);
+              copied = count + 1;
             }
           }
-          count = end;
+          if (ok) count = end;
           // the ragged last tile: 16 bytes at a time, rows beyond the sequence
           // as zeros
           if (whole < most) {
@@ -652,6 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
             __syncwarp();
             if (lane < each)
               tma_load_2d(codes + at * (kTile * D) + mine * box * D, i & 1 ? &map_v : &map_k, 0, (int)row, bar(kCodes + at));
+            copied = n + 1;
             return true;
           };
           if (most > 0 && warp - 8 < sharing) ok = copy(0) && copy(1);
@@ -700,6 +703,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
         }
       }
       cp_wait<0>();
+      // no copy may land after this CTA has left, whatever ended its work (a
+      // slot that has been filled again since was read before: it had landed)
+      for (int n = k8 ? count : max(0, count - kSlots); n < copied; ++n) {
+        if (k8)
+          mbar_drain(bar(kCodes + (n & 1)), (uint32_t)(n / 2) & 1u, a.err);
+        else
+          mbar_drain(bar(kFull + n % kSlots), (uint32_t)(n / kSlots) & 1u, a.err);
+      }
     } else if (warp < 14) {
       // Warp 12 takes units from the queue, numbered from the last rows of the
       // last sequence on, a key/value head after another. It walks back over
@@ -750,6 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
       const int step_head = kStride % p.group;
       const long long step = (long long)(kStride / p.group) * a.ldq + step_head * D, wrap = a.ldq - (long long)p.group * D;
       bool ok = true;
+      int asked = 0;  // tile copies of queries, alternately of tile 0 and 1
       for (int u = 0; ok; ++u) {
         if (warp == 12) {
           if (u >= 2 && !(ok = warp_wait(kUnitFree + (u & 1), (uint32_t)(u / 2 - 1) & 1u, kErrProducer))) break;
@@ -816,6 +828,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
                   tma_load_3d(base + t * kBytes + d * kPanel, &map_q, d * 64, unit.head * p.group,
                               unit.first + (unit.row0 + t * kTile) / p.group, bar(kQueries + t));
               }
+              ++asked;
               __syncwarp();
             }
           }
@@ -854,6 +867,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
         __syncwarp();
       }
       cp_wait<0>();
+      for (int n = max(0, asked - 2); n < asked; ++n) mbar_drain(bar(kQueries + (n & 1)), (uint32_t)(n / 2) & 1u, a.err);
     } else if (elect_one()) {
       // one warp per row tile, one thread of it
       constexpr uint32_t kDescHi = (uint32_t)(1024 >> 4) | (1u << 14) | (2u << 29);  // the upper half of both descriptors
