@@ -497,7 +497,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
         }
         to = -1;  // written by the joining kernel
       } else {
-        const float inv = l > 0.f ? (k8 ? a.cache.v_scale[unit.head] : 1.f) / l : 0.f;
+        // (a sum of zero: no key has weight; a NaN sum is the row's result)
+        const float inv = l == 0.f ? 0.f : (k8 ? a.cache.v_scale[unit.head] : 1.f) / l;
 #pragma unroll 2
         for (int d0 = 0; d0 < D; d0 += 32) {
           uint32_t o[32];
@@ -512,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
           uint32_t x[4][4];
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            x[i / 4][i & 3] = l > 0.f ? pack16<kB>(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv) : 0;
+            x[i / 4][i & 3] = l == 0.f ? 0 : pack16<kB>(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
 #pragma unroll
           for (int bit = 1; bit < 4; bit <<= 1)
 #pragma unroll
@@ -538,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
         tc_fence_before();
         mbar_arrive(bar(kOutFree + t));
       }
-      if (to >= 0 && a.lse) a.lse[to] = l > 0.f ? m * kLn2 + logf(l) : -INFINITY;
+      if (to >= 0 && a.lse) a.lse[to] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kUnitFree + (u & 1)));
     }
@@ -986,7 +987,7 @@ __global__ void __launch_bounds__(D) attn_join_kernel(const PromptArgs p) {
     float4 x[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) x[k] = reinterpret_cast<const float4*>(from)[(d0 / 4 + k) * 32 + lane];
-    if (li > 0.f) {  // (a part that a row sees no key of holds no O)
+    if (li != 0.f) {  // (a part that a row sees no key of holds no O; one with a NaN sum does)
       const float top = fmaxf(m, mi), old = ex2(m - top), f = ex2(mi - top);
       m = top;
       l = l * old + li * f;
@@ -1002,14 +1003,14 @@ __global__ void __launch_bounds__(D) attn_join_kernel(const PromptArgs p) {
   const int to = reinterpret_cast<const int*>(first)[32 * (D + 2) + lane];
   if (to < 0) return;
   const int head = to % p.a.heads / p.group;
-  const float inv = l > 0.f ? (p.a.cache.v_scale ? p.a.cache.v_scale[head] : 1.f) / l : 0.f;
+  const float inv = l == 0.f ? 0.f : (p.a.cache.v_scale ? p.a.cache.v_scale[head] : 1.f) / l;
   uint16_t* dst = p.a.out + (size_t)to * D + d0;
 #pragma unroll
   for (int i = 0; i < 32; i += 8)
     *reinterpret_cast<uint4*>(dst + i) =
         make_uint4(pack16<kB>(o[i] * inv, o[i + 1] * inv), pack16<kB>(o[i + 2] * inv, o[i + 3] * inv),
                    pack16<kB>(o[i + 4] * inv, o[i + 5] * inv), pack16<kB>(o[i + 6] * inv, o[i + 7] * inv));
-  if (p.a.lse && d0 == 0) p.a.lse[to] = l > 0.f ? m * kLn2 + logf(l) : -INFINITY;
+  if (p.a.lse && d0 == 0) p.a.lse[to] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
 }
 
 // Tensor map of a row-major array: dims and box innermost first, strides of
