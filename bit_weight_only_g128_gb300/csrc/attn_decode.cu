@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks<kHeads>) attn_decode_kernel(
           v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
         }
         if (whole) {
-          const float l1 = sm.sum[h], inv = l1 > 0.f ? v_scale / l1 : 0.f;
+          const float l1 = sm.sum[h], inv = l1 == 0.f ? 0.f : v_scale / l1;  // (a NaN sum is the result)
           *reinterpret_cast<uint2*>(a.out + (out0 + h) * D + d) =
               make_uint2(pack16<kB>(v.x * inv, v.y * inv), pack16<kB>(v.z * inv, v.w * inv));
         } else {
@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks<kHeads>) attn_decode_kernel(
     }
     if (tid < heads) {
       if (whole) {
-        if (a.lse) a.lse[out0 + tid] = sm.sum[tid] > 0.f ? sm.top[tid] * kLn2 + logf(sm.sum[tid]) : -INFINITY;
+        if (a.lse) a.lse[out0 + tid] = sm.sum[tid] == 0.f ? -INFINITY : sm.top[tid] * kLn2 + logf(sm.sum[tid]);
       } else {
         part[kHeads * D + tid] = sm.top[tid];
         part[kHeads * D + kHeads + tid] = sm.sum[tid];
@@ -660,10 +660,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks<kHeads>) attn_decode_kernel(
               v.x = fmaf(x[i].x, f, v.x), v.y = fmaf(x[i].y, f, v.y), v.z = fmaf(x[i].z, f, v.z), v.w = fmaf(x[i].w, f, v.w);
             }
           }
-          const float inv = sum > 0.f ? v_scale / sum : 0.f;
+          const float inv = sum == 0.f ? 0.f : v_scale / sum;
           *reinterpret_cast<uint2*>(a.out + (out0 + h) * D + d) =
               make_uint2(pack16<kB>(v.x * inv, v.y * inv), pack16<kB>(v.z * inv, v.w * inv));
-          if (a.lse && d == 0) a.lse[out0 + h] = sum > 0.f ? top * kLn2 + logf(sum) : -INFINITY;
+          if (a.lse && d == 0) a.lse[out0 + h] = sum == 0.f ? -INFINITY : top * kLn2 + logf(sum);
         }
         if (tid == 0) p.arrived[first] = 0;  // left zero for the next call
       }

@@ -112,3 +112,25 @@ def test_prompt(seqs, heads, hk, D, where, value, dtype, cache_dtype):
     w4.device_status()
     counts = check(q, cache, tab, starts, lens, got, lse, where == "value")
     assert counts["touched" if where == "value" else "nan"] > 0 and (counts["finite"] > 0 or hk == 1)
+
+
+@pytest.mark.parametrize("dtype,cache_dtype", TYPES)
+@pytest.mark.parametrize("heads,hk,D", [(8, 2, 128), (32, 2, 64), (1, 1, 128)])
+@pytest.mark.parametrize("where,value", [("query", math.nan), ("query", math.inf), ("key", math.nan),
+                                         ("value", math.nan), ("value", math.inf)])
+def test_decode(heads, hk, D, where, value, dtype, cache_dtype):
+    lens = [300, 1, 9000, 33]
+    g = gen(sum(lens) + heads)
+    cache, tab = scattered(g, lens, hk, 16, D, cache_dtype)
+    q = normal(g, len(lens), heads, D, std=2, dtype=dtype)
+    if where == "query":
+        q[0, 0, 5] = value
+        q[2, heads - 1, 0] = value
+    else:
+        put(cache, tab, 0, 299, 0, 3, where == "key", value)
+        put(cache, tab, 1, 0, hk - 1, 0, where == "key", value)
+        put(cache, tab, 2, 5000, 0, D - 1, where == "key", value)
+    got, lse = w4.attn_decode(q, cache, tab, torch.tensor(lens, dtype=torch.int32, device="cuda"), return_lse=True)
+    w4.device_status()
+    counts = check(q, cache, tab, list(range(len(lens) + 1)), lens, got, lse, where == "value")
+    assert counts["touched" if where == "value" else "nan"] > 0 and counts["finite"] > 0
