@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks<kHeads>) attn_decode_kernel(
             float f[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              f[h] = ex2(m[nb][h] - shift2[nb][h]);
+              f[h] = ex2(m[nb][h] - (shift2[nb][h] == -INFINITY ? 0.f : shift2[nb][h]));
               l[nb][h] *= f[h];
               m[nb][h] = shift2[nb][h];
             }
@@ -466,8 +466,13 @@ __global__ void __launch_bounds__(kThreads, kBlocks<kHeads>) attn_decode_kernel(
           }
         }
         // probabilities, rounded to 16 bits for the product (relative 2^-11
-        // or 2^-8 of each term), as B fragments: 16 tokens x 8 heads. (The
-        // tile has a token, so the maxima are finite.)
+        // or 2^-8 of each term), as B fragments: 16 tokens x 8 heads. (A
+        // maximum of -inf, where infinite keys leave no score, subtracts 0.)
+        float base[kNb][2];
+#pragma unroll
+        for (int nb = 0; nb < kNb; ++nb)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) base[nb][h] = m[nb][h] == -INFINITY ? 0.f : -m[nb][h];
         uint32_t pf[kTok / 16][kNb][2];
 #pragma unroll
         for (int i = 0; i < kTok / 16; ++i)
@@ -475,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks<kHeads>) attn_decode_kernel(
           for (int nb = 0; nb < kNb; ++nb) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              s[i][nb][j] = ex2(fmaf(s[i][nb][j], mult[nb][j & 1], -m[nb][j & 1]));
+              s[i][nb][j] = ex2(fmaf(s[i][nb][j], mult[nb][j & 1], base[nb][j & 1]));
               l[nb][j & 1] += s[i][nb][j];
             }
             pf[i][nb][0] = transpose8(pack16<kP>(s[i][nb][0], s[i][nb][1]));

@@ -117,7 +117,7 @@ def test_prompt(seqs, heads, hk, D, where, value, dtype, cache_dtype):
 @pytest.mark.parametrize("dtype,cache_dtype", TYPES)
 @pytest.mark.parametrize("heads,hk,D", [(8, 2, 128), (32, 2, 64), (1, 1, 128)])
 @pytest.mark.parametrize("where,value", [("query", math.nan), ("query", math.inf), ("key", math.nan),
-                                         ("value", math.nan), ("value", math.inf)])
+                                         ("key", math.inf), ("value", math.nan), ("value", math.inf)])
 def test_decode(heads, hk, D, where, value, dtype, cache_dtype):
     lens = [300, 1, 9000, 33]
     g = gen(sum(lens) + heads)
@@ -134,3 +134,34 @@ def test_decode(heads, hk, D, where, value, dtype, cache_dtype):
     w4.device_status()
     counts = check(q, cache, tab, list(range(len(lens) + 1)), lens, got, lse, where == "value")
     assert counts["touched" if where == "value" else "nan"] > 0 and counts["finite"] > 0
+
+
+@pytest.mark.parametrize("dtype", [FP16, BF16])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("decode", [True, False])
+def test_tiles_of_scores_without_weight(decode, D, dtype):
+    """The first 256 keys all score -inf, as do all keys of a short sequence:
+    the others decide, and a row of nothing else is as an empty one."""
+    lens, heads, hk = [300, 20, 2000], 8, 2
+    new = [1, 1, 1] if decode else [9, 3, 40]
+    g = gen(D)
+    cache, tab = scattered(g, lens, hk, 16, D, dtype)
+    for b, n in enumerate(lens):
+        for t in range(min(n, 256)):
+            page, at = place(cache, tab, b, t)
+            cache.k[page, :, at, 2] = math.inf
+    starts = [sum(new[:b]) for b in range(4)]
+    q = normal(g, starts[-1], heads, D, std=2, dtype=dtype)
+    q[:, :, 2] = -q[:, :, 2].abs() - 0.5
+    q[0, 0, 2] = 1.0  # and a head that those keys score +inf for
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    if decode:
+        got, lse = w4.attn_decode(q, cache, tab, n, return_lse=True)
+    else:
+        got, lse = w4.attn_prompt(q, cache, tab, torch.tensor(starts, dtype=torch.int32, device="cuda"), n,
+                                  return_lse=True)
+    w4.device_status()
+    counts = check(q, cache, tab, starts, lens, got, lse, False)
+    assert counts["nan"] == 1 and counts["finite"] == starts[-1] * heads - 1
+    rows = slice(starts[1], starts[2])
+    assert not got[rows].any() and lse[rows].isneginf().all()
