@@ -525,7 +525,8 @@ int w4a16_device_status(void* stream) {
     return fail(W4A16_ERR_DEVICE_CHECK,
                 "device error word = 0x%x (bits: 1 producer, 2 MMA, 4 dequant, 8 epilogue waits "
                 "timed out; 16 drain timed out; 32 decode fix-up wait timed out; 64 access out of "
-                "bounds, bounds-checked build; 128 slot, position, page or length outside its range)",
+                "bounds, bounds-checked build; 128 slot, position, page or length outside its range; 256 "
+                "workspace whose flag area was not zero before an attention call)",
                 flag);
   return ok();
 }

@@ -105,11 +105,15 @@ template <int D>
 constexpr int kSmem = (2 + kMostSlots) * kTileBytes<D> + (int)sizeof(Control) + 1024;
 static_assert(kSmem<128> <= 227 * 1024, "one block's shared memory");
 
-// A warp's part: O as [D / 4][32 rows] of four, maxima, sums, the rows' places
-// in the output (or -1), and the number of parts to join from this one on (0:
-// none).
+// A warp's part: O as [D / 4][32 rows] of four, maxima, sums, and the rows'
+// places in the output (or -1).
 template <int D>
-constexpr int kPartFloats = 32 * (D + 4);  // (the last 32: one number)
+constexpr int kPartFloats = 32 * (D + 3);
+// The workspace's flag area, zero between calls: the queue, then from this
+// byte on a count per place and warp of the parts to join from there on (0:
+// none; a call that gave up before it had written a part joins nothing of
+// it). 152 SMs' take 4.75 KiB.
+constexpr size_t kFlagBytes = 32768, kJoinsAt = 256;
 
 struct PromptArgs {
   AttnArgs a;
@@ -119,6 +123,7 @@ struct PromptArgs {
   int q_tiled;      // the map of the queries is there
   int* queue;       // next unit, blocks that are through; zero between calls
   float* partial;   // [blocks][8 warps] of kPartFloats, where units can be split
+  int* joins;       // [blocks][8 warps]
   int most_parts;
 };
 
@@ -475,8 +480,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
       if (!ok) break;
       // (Loops: code that runs once per unit is fetched anew every time.)
       float* mine = p.partial + (size_t)(unit.slot * 8 + warp) * kPartFloats<D>;
-      if (p.most_parts > 1 && unit.slot < (int)gridDim.x && lane == 0)
-        reinterpret_cast<int*>(mine)[32 * (D + 3)] = unit.part == 0 && unit.parts > 1 && !idle ? unit.parts : 0;
       if (unit.parts > 1) {
         if (!idle) {
           if (nt > 0) {
@@ -494,6 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
           mine[32 * D + lane] = m;
           mine[32 * (D + 1) + lane] = l;
           reinterpret_cast<int*>(mine)[32 * (D + 2) + lane] = to;
+          if (unit.part == 0 && lane == 0) p.joins[unit.slot * 8 + warp] = unit.parts;
         }
         to = -1;  // written by the joining kernel
       } else {
@@ -757,10 +761,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
       // of 64 heads over 8: 80 units on 152 blocks.)
       const int count = total * a.cache.kv_heads, grid = (int)gridDim.x;
       const int split = count > 0 && count < grid ? max(1, min(grid / count, p.most_parts)) : 1;
-      auto no_part = [&](int i) {  // place i holds nothing to join
-        if (p.most_parts > 1 && i >= 0 && i < grid && lane < 8)
-          reinterpret_cast<int*>(p.partial + (size_t)(i * 8 + lane) * kPartFloats<D>)[32 * (D + 3)] = 0;
-      };
       const int w = tid - 384, c = w % kChunks;
       constexpr int kStride = 64 / kChunks;
       const int step_head = kStride % p.group;
@@ -778,7 +778,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
             // (a queue that was not zero ends the call, it does not search)
             const int id = i / split, want = i < 0 ? -1 : total - 1 - id / a.cache.kv_heads;
             if (want < 0) {
-              no_part(i);
               if (lane == 0) {
                 to.valid = 0;
                 // the last block to come here leaves the queue zero
@@ -813,7 +812,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
               }
             }
             found = __any_sync(0xffffffffu, mine);
-            if (!found) no_part(i);
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(kUnit + (u & 1)));
@@ -966,7 +964,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
 
 // Joins the parts of split units: a warp for 32 rows (a lane each) and 32
 // dimensions, blockIdx.x the place of a first part and its warp. All places
-// are looked at; those that hold no first part end at once.
+// are looked at; those that hold no first part end at once. A count of parts
+// beyond the places and a row beyond the output (a flag area that was not
+// zero) are recorded and touch nothing.
 template <bool kB, int D>
 __global__ void __launch_bounds__(D) attn_join_kernel(const PromptArgs p) {
   allow_dependent_launch();
@@ -974,8 +974,16 @@ __global__ void __launch_bounds__(D) attn_join_kernel(const PromptArgs p) {
   const int lane = threadIdx.x & 31, d0 = threadIdx.x & ~31;
   const float* first = p.partial + (size_t)blockIdx.x * kPartFloats<D>;
   constexpr size_t kNext = (size_t)8 * kPartFloats<D>;
-  const int parts = reinterpret_cast<const int*>(first)[32 * (D + 3)];
+  const int parts = p.joins[blockIdx.x];
   if (parts == 0) return;
+  __syncthreads();  // all have read it
+  if (threadIdx.x == 0) p.joins[blockIdx.x] = 0;
+  const int places = (int)gridDim.x / 8, place = (int)blockIdx.x / 8;
+  const int to = reinterpret_cast<const int*>(first)[32 * (D + 2) + lane];
+  if (parts < 2 || parts > places - place || to >= p.a.rows * p.a.heads) {
+    atomicOr(p.a.err, kErrWorkspace);
+    return;
+  }
   float m = -INFINITY, l = 0.f;
   float o[32];
 #pragma unroll
@@ -1000,7 +1008,6 @@ __global__ void __launch_bounds__(D) attn_join_kernel(const PromptArgs p) {
       }
     }
   }
-  const int to = reinterpret_cast<const int*>(first)[32 * (D + 2) + lane];
   if (to < 0) return;
   const int head = to % p.a.heads / p.group;
   const float inv = l == 0.f ? 0.f : (p.a.cache.v_scale ? p.a.cache.v_scale[head] : 1.f) / l;
@@ -1064,8 +1071,6 @@ cudaError_t launch(PromptArgs p, unsigned blocks, cudaStream_t stream) {
   return launch_pdl(attn_join_kernel<kB, D>, dim3(blocks * 8), dim3(D), 0, stream, p);
 }
 
-constexpr size_t kFlagBytes = 32768;
-
 // Whether the units can be fewer than the blocks.
 bool may_split(int tokens, int group, int kv_heads, int sms) {
   return ((long long)tokens * group + 2 * kTile - 1) / (2 * kTile) * kv_heads < sms;
@@ -1074,7 +1079,7 @@ bool may_split(int tokens, int group, int kv_heads, int sms) {
 }  // namespace
 
 size_t attn_prompt_workspace_bytes(int tokens, int group, int kv_heads, int head_dim, int sms) {
-  return kFlagBytes + (may_split(tokens, group, kv_heads, sms) ? (size_t)sms * 8 * 32 * (head_dim + 4) * sizeof(float) : 0);
+  return kFlagBytes + (may_split(tokens, group, kv_heads, sms) ? (size_t)sms * 8 * 32 * (head_dim + 3) * sizeof(float) : 0);
 }
 
 cudaError_t launch_attn_prompt(const AttnArgs& args, int head_dim, bool bf16, bool e4m3, void* workspace, int sms,
@@ -1092,6 +1097,7 @@ cudaError_t launch_attn_prompt(const AttnArgs& args, int head_dim, bool bf16, bo
   p.negate = args.scale < 0.f;
   p.queue = static_cast<int*>(workspace);
   p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kFlagBytes);
+  p.joins = reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + kJoinsAt);
   // a block per SM, or as many as there can be units (whole ones of all rows,
   // and a ragged one per sequence) where none is long enough for two parts
   const long long units = ((long long)args.rows * p.group / (2 * kTile) + args.batch) * args.cache.kv_heads;

@@ -74,6 +74,8 @@ __device__ __forceinline__ void e4m3x4_to_half2x2(uint32_t codes, uint32_t& lo, 
 // Error bit of data read on the device that names something outside its
 // buffer: a slot, a position, a page number, a length.
 constexpr int kErrRange = 128;
+// Error bit of a workspace whose flag area was not as every call leaves it.
+constexpr int kErrWorkspace = 256;
 
 // The paged key-value cache: k and v are [pages][kv heads][page_size][head
 // dim] of 16-bit values or of e4m3 codes that a per-head scale multiplies.

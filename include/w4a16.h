@@ -406,7 +406,9 @@ int w4a16_rope_append(const uint16_t* qkv, int64_t qkv_stride, const float* cos_
 /* Scratch bytes of w4a16_attn_decode (tokens = batch) and w4a16_attn_prompt
  * on the current device; 0 when none. The buffer is of w4a16_gemm's kind: a
  * flag area that must be zero before the first use and that every call
- * leaves zero, so one buffer serves the GEMMs and these calls in turn.
+ * leaves zero, so one buffer serves the GEMMs and these calls in turn. A
+ * prompt call that finds in it what no call leaves there records it (bit 256
+ * of the error word) and touches nothing outside its buffers.
  * Host-only. */
 int w4a16_attn_workspace_size(int tokens, int batch, int heads, int kv_heads, int head_dim,
                               size_t* bytes);

@@ -1,0 +1,67 @@
+"""The attention workspace's flag area: zero between calls, and recorded,
+not trusted, where it was not zero before one."""
+import pytest
+import torch
+
+import bit_weight_only_g128_gb300 as w4
+from test_gpu_layer import BF16, E4M3, FP16, check_attention, gen, normal, same, scattered
+
+pytestmark = pytest.mark.gpu
+
+FLAGS = 32768
+
+
+def split_prompt(cache_dtype=FP16, dtype=FP16, D=128):
+    """A prompt call whose units are split, its check, and a workspace of zero
+    flags with floats of an earlier call behind them."""
+    seqs, heads, hk = [(16, 3000), (3, 1400)], 16, 2
+    new, lens = [a for a, _ in seqs], [n for _, n in seqs]
+    g = gen(31)
+    cache, tab = scattered(g, lens, hk, 64, D, cache_dtype)
+    starts = [0, 16, 19]
+    q = normal(g, 19, heads, D, std=2, dtype=dtype)
+    st = torch.tensor(starts, dtype=torch.int32, device="cuda")
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    ws = w4.new_workspace(w4.attn_workspace_size(19, 2, heads, hk, D))
+    ws[FLAGS:].view(torch.float32).fill_(1.0)
+
+    def call():
+        return w4.attn_prompt(q, cache, tab, st, n, return_lse=True, workspace=ws)
+
+    def check(got, lse):
+        check_attention(q, cache, tab, starts, lens, got, lse, D ** -0.5)
+
+    return call, check, ws
+
+
+@pytest.mark.parametrize("dtype,cache_dtype,D", [(FP16, FP16, 128), (BF16, BF16, 64), (BF16, E4M3, 128)])
+def test_what_the_parts_held_before_does_not_matter(dtype, cache_dtype, D):
+    call, check, ws = split_prompt(cache_dtype, dtype, D)
+    first = None
+    for fill in (0x3F800000, -1, 0x7FC00000, 5):
+        ws[FLAGS:].view(torch.int32).fill_(fill)
+        got, lse = call()
+        w4.device_status()
+        check(got, lse)
+        assert not ws[:FLAGS].any()
+        first = first or (got, lse)
+        assert same(got, first[0]) and same(lse, first[1])
+
+
+@pytest.mark.parametrize("parts", [1, -1, 1 << 30, 0x3F800000])
+def test_a_count_of_parts_beyond_the_places_is_refused(parts):
+    """The last place's count, as no call leaves it: recorded, not followed."""
+    call, check, ws = split_prompt()
+    want = call()
+    w4.device_status()
+    places = torch.cuda.get_device_properties(0).multi_processor_count
+    ws[:FLAGS].view(torch.int32)[64 + places * 8 - 1] = parts
+    got = call()
+    with pytest.raises(w4.W4A16Error) as e:
+        w4.device_status()
+    assert e.value.code == -6 and "0x100" in str(e.value)
+    assert not ws[:FLAGS].any()
+    assert same(got[0], want[0]) and same(got[1], want[1])
+    got, lse = call()
+    w4.device_status()
+    check(got, lse)
