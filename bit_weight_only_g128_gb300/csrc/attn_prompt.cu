@@ -121,7 +121,7 @@ struct PromptArgs {
   float mult;      // |scale| log2 e
   uint32_t negate;  // scale < 0
   int q_tiled;      // the map of the queries is there
-  int* queue;       // next unit, blocks that are through; zero between calls
+  int* queue;       // next unit; at [2], 64 bits: blocks that are through << 32 | what they drew
   float* partial;   // [blocks][8 warps] of kPartFloats, where units can be split
   int* joins;       // [blocks][8 warps]
   int most_parts;
@@ -767,6 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
       const long long step = (long long)(kStride / p.group) * a.ldq + step_head * D, wrap = a.ldq - (long long)p.group * D;
       bool ok = true;
       int asked = 0;  // tile copies of queries, alternately of tile 0 and 1
+      uint32_t drawn = 0;  // numbers that this block took from the queue
       for (int u = 0; ok; ++u) {
         if (warp == 12) {
           if (u >= 2 && !(ok = warp_wait(kUnitFree + (u & 1), (uint32_t)(u / 2 - 1) & 1u, kErrProducer))) break;
@@ -775,15 +776,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
             int i = 0;
             if (lane == 0) i = atomicAdd(p.queue, 1);
             i = __shfl_sync(0xffffffffu, i, 0);
-            // (a queue that was not zero ends the call, it does not search)
+            ++drawn;
+            // (a queue that was negative ends the block's work, it does not search)
+            if (i < 0 && lane == 0) atomicOr(a.err, kErrWorkspace);
             const int id = i / split, want = i < 0 ? -1 : total - 1 - id / a.cache.kv_heads;
             if (want < 0) {
-              if (lane == 0) {
-                to.valid = 0;
-                // the last block to come here leaves the queue zero
-                __threadfence();
-                if (atomicAdd(p.queue + 1, 1) == grid - 1) p.queue[0] = p.queue[1] = 0;
-              }
+              if (lane == 0) to.valid = 0;
               break;
             }
             while (want < before) {
@@ -868,6 +866,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
           }
         }
         __syncwarp();
+      }
+      // Every block comes here once, whatever ended its work; the last one
+      // leaves the queue zero. The blocks draw every part's number and one
+      // more each: another sum is that of a queue that was not zero before the
+      // call (or of a block that gave up), whose call has left rows out.
+      if (warp == 12 && lane == 0) {
+        const unsigned long long all =
+            atomicAdd(reinterpret_cast<unsigned long long*>(p.queue + 2), (1ull << 32) | drawn) + ((1ull << 32) | drawn);
+        if ((int)(all >> 32) == grid) {
+          if ((uint32_t)all != (uint32_t)max(count, 0) * split + grid) atomicOr(a.err, kErrWorkspace);
+          p.queue[0] = p.queue[2] = p.queue[3] = 0;
+        } else if ((uint32_t)(all >> 32) > (uint32_t)grid) {
+          atomicOr(a.err, kErrWorkspace);
+        }
       }
       cp_wait<0>();
       for (int n = max(0, asked - 2); n < asked; ++n) mbar_drain(bar(kQueries + (n & 1)), (uint32_t)(n / 2) & 1u, a.err);

@@ -65,3 +65,39 @@ def test_a_count_of_parts_beyond_the_places_is_refused(parts):
     got, lse = call()
     w4.device_status()
     check(got, lse)
+
+
+@pytest.mark.parametrize("word,value", [(0, 1), (0, 7), (0, 100000), (0, -5), (2, 3), (3, 1), (3, 1000)])
+@pytest.mark.parametrize("split", [True, False])
+def test_a_queue_that_was_not_zero_is_recorded(word, value, split):
+    """The call has left rows out: it says so, and its buffers and the next
+    call with a zero flag area are right."""
+    if split:
+        call, check, ws = split_prompt()
+    else:
+        g = gen(32)
+        seqs = [(700, 700), (90, 400)]
+        lens, starts = [n for _, n in seqs], [0, 700, 790]
+        cache, tab = scattered(g, lens, 2, 64, 128, FP16)
+        q = normal(g, 790, 8, 128, std=2, dtype=FP16)
+        st = torch.tensor(starts, dtype=torch.int32, device="cuda")
+        n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        ws = w4.new_workspace(w4.attn_workspace_size(790, 2, 8, 2, 128))
+
+        def call():
+            return w4.attn_prompt(q, cache, tab, st, n, return_lse=True, workspace=ws)
+
+        def check(got, lse):
+            check_attention(q, cache, tab, starts, lens, got, lse, 128 ** -0.5)
+
+    ws[:FLAGS].view(torch.int32)[word] = value
+    call()
+    with pytest.raises(w4.W4A16Error) as e:
+        w4.device_status()
+    assert e.value.code == -6 and "0x100" in str(e.value)
+    if word == 0:  # (the blocks that are through were counted right: cleared)
+        assert not ws[:FLAGS].any()
+    ws[:FLAGS].zero_()
+    check(*call())
+    w4.device_status()
+    assert not ws[:FLAGS].any()
