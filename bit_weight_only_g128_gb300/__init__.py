@@ -39,6 +39,8 @@ ACT_A8 = 0x800          # W4A16_ACT_A8
 CACHE_E4M3 = 0x1000        # W4A16_CACHE_E4M3
 ROPE_INTERLEAVED = 0x2000  # W4A16_ROPE_INTERLEAVED
 
+FLAG_BYTES = 32768  # a workspace's flag area: zero before and after every call
+
 ERRORS = {
     -1: "INVALID_ARG", -2: "UNSUPPORTED_SHAPE", -3: "MISALIGNED",
     -4: "WORKSPACE_TOO_SMALL", -5: "CUDA_ERROR", -6: "DEVICE_CHECK",
@@ -360,5 +362,15 @@ def selftest_wait(which: int, stream=None) -> None:
 
 
 def device_status(stream=None) -> None:
-    """Synchronize and raise if a kernel reported an error on the device."""
-    _check(lib().w4a16_device_status(_stream(stream)), "w4a16_device_status")
+    """Synchronize and raise if a kernel reported an error on the device. A
+    call that gave up may have left its workspace's flag area non-zero: the
+    cached workspaces' are zeroed, each on its stream, before the exception
+    (a workspace of the caller's own has to be zeroed by the caller)."""
+    try:
+        _check(lib().w4a16_device_status(_stream(stream)), "w4a16_device_status")
+    except W4A16Error as e:
+        if e.code == -6:
+            for (device, st), ws in list(_stream_ws.items()):
+                with torch.cuda.stream(torch.cuda.ExternalStream(st, device=device)):
+                    ws[:FLAG_BYTES].zero_()
+        raise

@@ -101,3 +101,26 @@ def test_a_queue_that_was_not_zero_is_recorded(word, value, split):
     check(*call())
     w4.device_status()
     assert not ws[:FLAGS].any()
+
+
+def test_cached_workspaces_are_zero_after_an_error():
+    """What a call that gave up may have left in the flag areas of the cached
+    workspaces does not reach the next call."""
+    call, check, _ = split_prompt()
+    seqs, heads, hk, D = [(16, 3000), (3, 1400)], 16, 2, 128
+    need = w4.attn_workspace_size(19, 2, heads, hk, D)
+    side = torch.cuda.Stream()
+    streams = [torch.cuda.current_stream(), side]
+    cached = [w4.stream_workspace(need, 0, s.cuda_stream) for s in streams]
+    torch.cuda.synchronize()
+    for ws in cached:
+        ws[:FLAGS].view(torch.int32)[:2000] = 1
+    w4.selftest_wait(0)
+    with pytest.raises(w4.W4A16Error) as e:
+        w4.device_status()
+    assert e.value.code == -6
+    torch.cuda.synchronize()
+    assert [w4.stream_workspace(need, 0, s.cuda_stream) is ws for s, ws in zip(streams, cached)] == [True, True]
+    for ws in cached:
+        assert not ws[:FLAGS].any()
+    w4.device_status()
