@@ -259,6 +259,13 @@ def stream_workspace(nbytes: int, device: int, stream: int) -> torch.Tensor:
     return ws
 
 
+def _workspace_args(ws: torch.Tensor, device: torch.device) -> Tuple[int, int]:
+    """Pointer and bytes of a given workspace, which the kernels use as it is."""
+    if not ws.is_cuda or ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous CUDA tensor on {device}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
 def plan(M: int, N: int, K: int, group: int) -> Tuple[str, int]:
     """(path, decode CTA count) the library picks for this problem."""
     p, c = ctypes.c_int(), ctypes.c_int()
@@ -311,7 +318,7 @@ def gemm(A: torch.Tensor, pw: PackedWeight, out: Optional[torch.Tensor] = None,
     if need:
         if workspace is None:
             workspace = stream_workspace(need, dev, st)
-        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        ws_ptr, ws_bytes = _workspace_args(workspace, A.device)
     rc = lib().w4a16_gemm_ex(a_ptr, pw.Wq.data_ptr(), pw.Sp.data_ptr(), pw.Zp.data_ptr(), M,
                              pw.N, pw.K, pw.group, y_ptr, ws_ptr, ws_bytes,
                              _PATHS[path] | (STATIC_WEIGHTS if static_weights else 0)

@@ -367,6 +367,8 @@ PyObject* attend(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     at::Tensor ws;
     if (args[8] != Py_None) {
       ws = tensor(args[8], "workspace");
+      if (!ws.is_cuda() || ws.device() != dev || !ws.is_contiguous())
+        refuse("workspace must be a contiguous CUDA tensor on %s", text(dev).c_str());
     } else if (need) {
       PyObject* o = PyObject_CallFunction(workspace_of, "niK", (Py_ssize_t)need, (int)dev.index(),
                                           (unsigned long long)(uintptr_t)stream.ptr);

@@ -91,7 +91,7 @@ def gemm_scaled(codes: torch.Tensor, row_scale: torch.Tensor, pw, out: Optional[
     if need:
         if workspace is None:
             workspace = w4.stream_workspace(need, dev.index, st)
-        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        ws_ptr, ws_bytes = w4._workspace_args(workspace, dev)
     rc = w4.lib().w4a16_gemm_scaled(
         a_ptr, s_ptr, pw.Wq.data_ptr(), pw.Sp.data_ptr(), pw.Zp.data_ptr(), M, pw.N, pw.K, pw.group, y_ptr,
         ws_ptr, ws_bytes, w4._PATHS[path] | (w4.STATIC_WEIGHTS if static_weights else 0)

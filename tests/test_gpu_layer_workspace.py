@@ -124,3 +124,23 @@ def test_cached_workspaces_are_zero_after_an_error():
     for ws in cached:
         assert not ws[:FLAGS].any()
     w4.device_status()
+
+
+def test_workspaces_that_the_kernels_cannot_use_are_refused():
+    """Host memory, and strided tensors: refused before any launch."""
+    g = gen(33)
+    cache, tab = scattered(g, [40, 5], 2, 16, 64, FP16)
+    q = normal(g, 2, 4, 64, dtype=FP16)
+    n = torch.tensor([40, 5], dtype=torch.int32, device="cuda")
+    st = torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
+    pw = w4.quantize_pack(normal(g, 1024, 512, std=0.02), 128)
+    x = normal(g, 40, 1024, dtype=FP16)
+    codes, s = w4.rms_norm(x, normal(g, 1024, dtype=FP16), quant="codes")
+    for ws in (torch.zeros(64 << 20, dtype=torch.uint8), w4.new_workspace(128 << 20)[::2]):
+        for call in (lambda: w4.attn_decode(q, cache, tab, n, workspace=ws),
+                     lambda: w4.attn_prompt(q, cache, tab, st, n, workspace=ws),
+                     lambda: w4.gemm(x, pw, path="tensor", parts=4, workspace=ws),
+                     lambda: w4.gemm_scaled(codes, s, pw, path="tensor", parts=4, workspace=ws)):
+            with pytest.raises(ValueError, match="workspace must be a contiguous CUDA tensor"):
+                call()
+    w4.device_status()
