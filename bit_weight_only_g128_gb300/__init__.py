@@ -130,6 +130,16 @@ def _stream(stream: Optional[torch.cuda.Stream], device: Optional[int] = None) -
     return torch._C._cuda_getCurrentRawStream(device)
 
 
+def _on_stream(stream, device: torch.device):
+    """A context in which `stream`, of the tensors' device, is the current
+    one: what is allocated and zero-filled for a call on it belongs to it."""
+    if not isinstance(stream, torch.cuda.Stream):  # another package's, by its handle
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    return torch.cuda.stream(stream)
+
+
 def _dev(t: torch.Tensor, dtype: torch.dtype, name: str) -> int:
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -290,8 +300,9 @@ def gemm(A: torch.Tensor, pw: PackedWeight, out: Optional[torch.Tensor] = None,
          path: str = "auto", parts: int = 0, workspace: Optional[torch.Tensor] = None,
          stream=None, static_weights: bool = False, silu_mul: bool = False,
          a8: bool = False) -> torch.Tensor:
-    """Y [M, N] = A [M, K] . dequant(pw), on the current stream; A and Y are
-    both fp16 or both bf16 (W4A16_BF16, chosen by A's dtype).
+    """Y [M, N] = A [M, K] . dequant(pw), on the current stream, or on
+    `stream` (to which a result and a workspace allocated here then belong); A
+    and Y are both fp16 or both bf16 (W4A16_BF16, chosen by A's dtype).
 
     `workspace` must be zero-filled before its first use (new_workspace);
     without one, the call uses the cached workspace of its stream
@@ -308,11 +319,14 @@ def gemm(A: torch.Tensor, pw: PackedWeight, out: Optional[torch.Tensor] = None,
         raise ValueError(f"A has K={K}, weight has K={pw.K}")
     dt = A.dtype if A.dtype in (torch.float16, torch.bfloat16) else torch.float16
     a_ptr = _dev(A, dt, "A")
+    if stream is not None:
+        with _on_stream(stream, A.device):
+            return gemm(A, pw, out, path, parts, workspace, None, static_weights, silu_mul, a8)
     dev = A.device.index
     if out is None:
         out = torch.empty((M, pw.N // 2 if silu_mul else pw.N), dtype=dt, device=A.device)
     y_ptr = _dev(out, dt, "out")
-    st = _stream(stream, dev)
+    st = _stream(None, dev)
     ws_ptr, ws_bytes = None, 0
     need = workspace_size(M, pw.N, pw.K, pw.group, path, parts, silu_mul, a8, dev)
     if need:

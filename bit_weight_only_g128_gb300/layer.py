@@ -82,10 +82,13 @@ def gemm_scaled(codes: torch.Tensor, row_scale: torch.Tensor, pw, out: Optional[
     dev = codes.device
     a_ptr = _flat(codes, "codes", M * K, codes.dtype, dev)
     s_ptr = _flat(row_scale, "row_scale", M, torch.float32, dev)
+    if stream is not None:
+        with w4._on_stream(stream, dev):
+            return gemm_scaled(codes, row_scale, pw, out, path, parts, workspace, None, static_weights, silu_mul)
     if out is None:
         out = torch.empty((M, pw.N // 2 if silu_mul else pw.N), dtype=codes.dtype, device=dev)
     y_ptr = _flat(out, "out", M * (pw.N // 2 if silu_mul else pw.N), codes.dtype, dev)
-    st = w4._stream(stream, dev.index)
+    st = w4._stream(None, dev.index)
     ws_ptr, ws_bytes = None, 0
     need = w4.workspace_size(M, pw.N, pw.K, pw.group, path, parts, silu_mul, False, dev.index)
     if need:

@@ -144,3 +144,27 @@ def test_workspaces_that_the_kernels_cannot_use_are_refused():
             with pytest.raises(ValueError, match="workspace must be a contiguous CUDA tensor"):
                 call()
     w4.device_status()
+
+
+def test_gemms_on_a_stream_of_their_own():
+    """Results and workspace of a stream that has none yet, behind slow work
+    on the current one, which their zeros must not wait for."""
+    g = gen(34)
+    pw = w4.quantize_pack(normal(g, 1024, 512, std=0.02), 128)
+    x = normal(g, 40, 1024, dtype=FP16)
+    codes, s = w4.rms_norm(x, normal(g, 1024, dtype=FP16), quant="codes")
+    calls = [lambda **k: w4.gemm(x, pw, path="tensor", parts=4, **k),
+             lambda **k: w4.gemm(x, pw, path="tensor", parts=4, a8=True, **k),
+             lambda **k: w4.gemm_scaled(codes, s, pw, path="tensor", parts=4, **k)]
+    want = [call() for call in calls]
+    big = torch.randn(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    for call, y in zip(calls, want):
+        own = torch.cuda.Stream()
+        for _ in range(10):
+            big = big @ big * 1e-3
+        got = call(stream=own)
+        own.synchronize()
+        with torch.cuda.stream(own):
+            assert same(got, y)
+    w4.device_status()
