@@ -323,6 +323,9 @@ def gemm(A: torch.Tensor, pw: PackedWeight, out: Optional[torch.Tensor] = None,
         with _on_stream(stream, A.device):
             return gemm(A, pw, out, path, parts, workspace, None, static_weights, silu_mul, a8)
     dev = A.device.index
+    if dev != torch._C._cuda_getDevice():  # the library works on the current device
+        with torch.cuda.device(A.device):
+            return gemm(A, pw, out, path, parts, workspace, None, static_weights, silu_mul, a8)
     if out is None:
         out = torch.empty((M, pw.N // 2 if silu_mul else pw.N), dtype=dt, device=A.device)
     y_ptr = _dev(out, dt, "out")

@@ -114,14 +114,17 @@ at::Tensor result(PyObject* given, const char* name, at::IntArrayRef shape, at::
   return t;
 }
 
-// The call's stream: the current one of the device, or the given
+// The call's stream: the current one of the tensors' device, or the given
 // torch.cuda.Stream, which is then the current one while results and workspace
-// are allocated (and the workspace's zeros written): they belong to it.
+// are allocated (and the workspace's zeros written): they belong to it. The
+// library works on the current device (its SM count, error word and launches),
+// so that is the tensors' for the call.
 struct CallStream {
   void* ptr;
+  c10::cuda::CUDAGuard device;
   c10::cuda::OptionalCUDAStreamGuard guard;
 
-  CallStream(PyObject* o, const at::Device& dev) {
+  CallStream(PyObject* o, const at::Device& dev) : device(dev) {
     if (o == Py_None) {
       ptr = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
       return;

@@ -85,6 +85,9 @@ def gemm_scaled(codes: torch.Tensor, row_scale: torch.Tensor, pw, out: Optional[
     if stream is not None:
         with w4._on_stream(stream, dev):
             return gemm_scaled(codes, row_scale, pw, out, path, parts, workspace, None, static_weights, silu_mul)
+    if dev.index != torch._C._cuda_getDevice():  # the library works on the current device
+        with torch.cuda.device(dev):
+            return gemm_scaled(codes, row_scale, pw, out, path, parts, workspace, None, static_weights, silu_mul)
     if out is None:
         out = torch.empty((M, pw.N // 2 if silu_mul else pw.N), dtype=codes.dtype, device=dev)
     y_ptr = _flat(out, "out", M * (pw.N // 2 if silu_mul else pw.N), codes.dtype, dev)

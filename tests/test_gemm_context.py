@@ -116,3 +116,12 @@ def test_a_stream_of_another_device_is_refused(seen, call):
     with pytest.raises(ValueError, match="stream is on cuda:0"):
         call(stream=Stream(torch.device("cuda", 0)))
     assert not [what for what, _, _ in log if what == "launch"]
+
+
+@pytest.mark.parametrize("call", CALLS)
+@pytest.mark.parametrize("stream", [None, Stream()])
+def test_the_tensors_device_is_the_current_one_for_the_call(seen, call, stream):
+    log, current = seen
+    call(stream=stream)
+    assert log and all(device == 1 for _, device, _ in log), log
+    assert current["device"] == 0
