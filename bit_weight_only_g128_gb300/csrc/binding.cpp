@@ -246,10 +246,12 @@ PyObject* rms_norm(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
                        int8 || codes ? nullptr : static_cast<uint16_t*>(yp), codes ? static_cast<uint16_t*>(yp) : nullptr,
                        int8 ? static_cast<int8_t*>(yp) : nullptr, sp, hp, ldh, stream.ptr),
           "w4a16_rms_norm");
+    // (not by the pointers: those of no rows are null)
+    const bool quant = int8 || codes, residual = args[2] != Py_None;
     PyObject* yo = wrap(y, args[5]);
-    if (!sp && !hp) return yo;
-    if (!sp) return tuple(yo, wrap(h, args[6]));
-    if (!hp) return tuple(yo, wrap(scale));
+    if (!quant && !residual) return yo;
+    if (!quant) return tuple(yo, wrap(h, args[6]));
+    if (!residual) return tuple(yo, wrap(scale));
     return tuple(yo, wrap(scale), wrap(h, args[6]));
   });
 }
