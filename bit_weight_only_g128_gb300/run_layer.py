@@ -61,7 +61,10 @@ def rotary_table(length: int, dim: int, base: float = 10000.0, device="cuda") ->
 
 class Stack:
     """Decoder layers over one paged cache per layer and one page table for
-    all. The sequences' pages are assigned at the start, in turn."""
+    all. The sequences' pages are assigned at the start, in turn, for
+    `longest` tokens each (rounded up to pages). Tokens beyond them are
+    refused; those of a replayed graph, which the host does not see, are not
+    stored and are recorded (device_status)."""
 
     def __init__(self, shape: Shape, layers: int, batch: int, longest: int, page: int = 16,
                  dtype: torch.dtype = torch.float16, e4m3: bool = False, a8: bool = False, seed: int = 0):
@@ -70,9 +73,14 @@ class Stack:
         gen.manual_seed(seed)
         per = -(-longest // page)
         order = torch.randperm(batch * per, generator=gen, device="cuda").to(torch.int32)
-        self.table = order.view(batch, per)
+        # a page more than a sequence has names a slot beyond the cache
+        self._pages = torch.full((batch, per + 1), batch * per, dtype=torch.int32, device="cuda")
+        self._pages[:, :per] = order.view(batch, per)
+        self.table = self._pages[:, :per]
+        self.capacity = per * page
         self.lens = torch.zeros(batch, dtype=torch.int32, device="cuda")
-        self.cos_sin = rotary_table(longest, shape.head_dim)
+        self._held = [0] * batch  # as far as the host knows
+        self.cos_sin = rotary_table(self.capacity, shape.head_dim)
         scale = torch.full((shape.kv_heads,), 0.05, device="cuda") if e4m3 else None
 
         def weight(K, N):
@@ -98,19 +106,33 @@ class Stack:
         return w4.gemm(y, pw, static_weights=True, silu_mul=silu_mul)
 
     def _forward(self, x, h, positions, slots, attend):
-        rows = x.shape[0]
         for layer in self.layers:
             qkv = self._norm_gemm(x, h, layer.norm1, layer.qkv)
             q = w4.rope_append(qkv, self.cos_sin, positions, slots, layer.cache)
-            x = w4.gemm(attend(q, layer.cache).view(rows, -1), layer.o, static_weights=True, a8=self.a8)
+            x = w4.gemm(attend(q, layer.cache).flatten(1), layer.o, static_weights=True, a8=self.a8)
             y = self._norm_gemm(x, h, layer.norm2, layer.gate_up, silu_mul=True)
             x = w4.gemm(y, layer.down, static_weights=True, a8=self.a8)
         return h.add_(x)
+
+    def clear(self) -> None:
+        """Forget the sequences' tokens."""
+        self.lens.zero_()
+        self._held = [0] * self.batch
+
+    def _take(self, counts: List[int], rows: int) -> None:
+        """Refuse new tokens that do not fit, or count them."""
+        if len(counts) != self.batch or min(counts) < 0 or sum(counts) != rows:
+            raise ValueError(f"{rows} rows and counts {counts} do not fit {self.batch} sequences")
+        held = [a + n for a, n in zip(self._held, counts)]
+        if max(held) > self.capacity:
+            raise ValueError(f"a sequence of {max(held)} tokens is longer than the {self.capacity} that the stack holds")
+        self._held = held
 
     def prompt(self, x: torch.Tensor, counts: List[int]) -> torch.Tensor:
         """The rows of counts[b] new tokens of every sequence, one after
         another ([sum(counts), hidden]); returns their hidden states. x is not
         changed."""
+        self._take(counts, len(x))
         new = torch.tensor(counts, dtype=torch.int32, device="cuda")
         starts = torch.zeros(self.batch + 1, dtype=torch.int32, device="cuda")
         starts[1:] = new.cumsum(0)
@@ -124,6 +146,7 @@ class Stack:
         """One new token of every sequence ([batch, hidden]); returns their
         hidden states. Every launch is on the current stream and none waits
         for the host: it can be captured as a CUDA graph."""
+        self._take([1] * self.batch, len(x))
         positions = self.lens.long()
         self.lens += 1
         of = torch.arange(self.batch, device="cuda")
@@ -131,7 +154,8 @@ class Stack:
                              lambda q, cache: w4.attn_decode(q, cache, self.table, self.lens))
 
     def _slots(self, of, positions):
-        return self.table[of, positions // self.page].long() * self.page + positions % self.page
+        page = (positions // self.page).clamp_(max=self._pages.shape[1] - 1)
+        return self._pages[of, page].long() * self.page + positions % self.page
 
 
 def run(model: str, layers: int, batch: int, prompt: int, steps: int, e4m3=False, a8=False, bf16=False, seed=0):
@@ -148,7 +172,7 @@ def run(model: str, layers: int, batch: int, prompt: int, steps: int, e4m3=False
     x = rows(sum(counts))
     mark = [torch.cuda.Event(enable_timing=True) for _ in range(4)]
     stack.prompt(x, counts)  # warm-up; the timed prompt starts over
-    stack.lens.zero_()
+    stack.clear()
     mark[0].record()
     hidden = stack.prompt(x, counts)
     mark[1].record()
