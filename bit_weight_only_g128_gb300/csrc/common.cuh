@@ -163,6 +163,29 @@ __device__ __forceinline__ void dequant_word_bf16(uint32_t w, const DeqConstBf16
   out[3] = bf16x2_rn(f(u, 0x4155), f(u, 0x4355));  // k 6, 7
 }
 
+// ------------------------------------------------------------------ 8-bit activations
+
+// The scale of a row whose largest magnitude is `top`: top / 127, and 1 where
+// that is zero (a row of zeros, or of subnormals too small for 1/127 of them).
+__device__ __forceinline__ float act_scale(float top) {
+  const float s = __fdiv_rn(top, 127.0f);
+  return s > 0.f ? s : 1.0f;
+}
+
+// The code of a at scale s, round(RN(a / s)), with inv = RN(1/s). t = a * inv
+// differs from the exact quotient by under 2 ulps of t (two roundings), and so
+// does RN(a / s); where the exact quotient is farther than that from a
+// midpoint k + 1/2, both round to the same integer. So t decides unless it
+// lies within 2^-14 (at least 4 ulps, |t| < 128) of a midpoint, or 1/s is
+// beyond fp32 (t is infinite, or 0 * inf); there the correctly rounded
+// quotient decides.
+__device__ __forceinline__ float act_code(float a, float s, float inv) {
+  const float t = a * inv;
+  float r = rintf(t);
+  if (!(fabsf(fabsf(t - r) - 0.5f) >= 6.103515625e-05f)) r = rintf(__fdiv_rn(a, s));
+  return fminf(fmaxf(r, -127.f), 127.f);
+}
+
 // ------------------------------------------------------------------ loads
 
 // Streaming 16-byte load of packed weights: read once, keep out of L1.

@@ -37,17 +37,6 @@ struct NormArgs {
   int* err;
 };
 
-// The code of y at scale s, inv = RN(1/s). t = y * inv differs from the exact
-// quotient by under 2 ulps, so it decides unless it lies within 2^-14 of a
-// midpoint (at least 4 ulps, |t| < 128); there the correctly rounded quotient
-// decides.
-__device__ __forceinline__ float act_code(float y, float s, float inv) {
-  const float t = y * inv;
-  float r = rintf(t);
-  if (fabsf(fabsf(t - r) - 0.5f) < 6.103515625e-05f) r = rintf(__fdiv_rn(y, s));
-  return fminf(fmaxf(r, -127.f), 127.f);
-}
-
 // Sum or maximum over the `threads` threads (a multiple of 32) of one row;
 // `part` holds one float per warp of the block. Every thread of the block
 // takes part.
@@ -151,7 +140,7 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormArgs a, int ro
   if (!a.s_a) return;
   top = row_reduce<true>(top, warps, part2);
   if (!live) return;
-  const float s = top > 0.f ? __fdiv_rn(top, 127.0f) : 1.0f;
+  const float s = act_scale(top);
   const float inv = __frcp_rn(s);
   if (t == 0) a.s_a[m] = s;
 #pragma unroll
@@ -207,7 +196,7 @@ __global__ void __launch_bounds__(256) rms_norm_any_kernel(const NormArgs a) {
     for (int k = threadIdx.x; k < a.K; k += 256)
       top = fmaxf(top, fabsf(value(k) * scale * value16<kB>(a.weight[k])));
     top = row_reduce<true>(top, 8, part2);
-    s = top > 0.f ? __fdiv_rn(top, 127.0f) : 1.0f;
+    s = act_scale(top);
     inv = __frcp_rn(s);
     if (threadIdx.x == 0) a.s_a[m] = s;
   }

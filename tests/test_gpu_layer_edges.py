@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import bit_weight_only_g128_gb300 as w4
-from test_gpu_layer import BF16, FP16
+from test_gpu_layer import BF16, FP16, gen
 
 pytestmark = pytest.mark.gpu
 
@@ -22,3 +22,43 @@ def test_norm_of_no_rows_answers_as_of_some(dtype):
             assert q.shape == (rows, 64) and q.dtype == code and s.shape == (rows,)
             q, s, h = w4.rms_norm(x, w, residual=r, quant=quant)
             assert q.shape == h.shape == (rows, 64) and s.shape == (rows,)
+
+
+def nearest_codes(v):
+    """Codes and scales of rows v (float32) by the rule, in IEEE fp32 on the
+    host: s = max / 127 (1 where that is zero), clamp(round(v / s))."""
+    v = v.cpu()
+    s = v.abs().amax(1) / 127
+    s = torch.where(s > 0, s, torch.ones_like(s))
+    return (v / s[:, None]).round().clamp(-127, 127), s
+
+
+# 1 over the scale leaves fp32 below 3.7e-37, the scale has few bits below 1e-36, bf16 ends at 9.2e-41
+TINY = [1e-30, 4e-37, 3.7e-37, 1e-37, 1e-38, 1e-39, 1e-43, 1e-45]
+
+
+@pytest.mark.parametrize("size", TINY)
+def test_codes_of_tiny_activations(size):
+    x = (torch.randn((5, 96), generator=gen(1), device="cuda").double() * size).to(BF16)
+    x[:, ::3] = 0
+    x[4] = 0
+    aq, s = w4.quantize_act(x)
+    want, scale = nearest_codes(x.float())
+    assert torch.equal(s.cpu(), scale) and torch.equal(aq.cpu().float(), want)
+
+
+@pytest.mark.parametrize("K", [96, 97, 4096])
+@pytest.mark.parametrize("size", TINY)
+def test_norm_codes_of_tiny_results(size, K):
+    """Powers of two and rows of one magnitude: y is exact, so the codes are
+    those of the rule."""
+    x = torch.zeros((3, K), dtype=BF16, device="cuda")
+    x[0, ::2], x[1, 1::2] = 1, -1
+    w = torch.full((K,), size, dtype=BF16, device="cuda")
+    y = w4.rms_norm(x, w, eps=0.5 - 0.25 * (K % 2)).float()
+    codes, s = w4.rms_norm(x, w, eps=0.5 - 0.25 * (K % 2), quant="codes")
+    aq, s2 = w4.rms_norm(x, w, eps=0.5 - 0.25 * (K % 2), quant="int8")
+    assert torch.equal(codes.float(), aq.float()) and torch.equal(s, s2)
+    assert not aq[x == 0].any() and float(s[2]) == 1.0
+    if y.abs().amax() / 127 > 2.0 ** -140:  # (the scale has bits enough to tell)
+        assert (aq[0, ::2] == 127).all() and (aq[1, 1::2] == -127).all()
