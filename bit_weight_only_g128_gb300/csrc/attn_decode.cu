@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks<kHeads>) attn_decode_kernel(
     float mult[kNb][2];
 #pragma unroll
     for (int nb = 0; nb < kNb; ++nb) {
-      const float m0 = p.mult * (k8 ? a.cache.k_scale[head] : 1.f);
+      const float m0 = positive(p.mult * (k8 ? a.cache.k_scale[head] : 1.f));
       float top = 0.f;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i)
@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks<kHeads>) attn_decode_kernel(
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         // 2^e with |q| 2^-e < 4, from the exponent's bits (e from -126 to 126)
         const int e = min(max((int)(__float_as_uint(top) >> 23), 1), 253);
-        const float down = __uint_as_float((uint32_t)(254 - e) << 23), own = m0 * __uint_as_float((uint32_t)e << 23);
+        const float down = __uint_as_float((uint32_t)(254 - e) << 23), own = positive(m0 * __uint_as_float((uint32_t)e << 23));
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
 #pragma unroll

@@ -114,6 +114,12 @@ __device__ __forceinline__ int checked(const AttnArgs& a, int v, int most) {
   return v < 0 ? 0 : most;
 }
 
+// What scores are multiplied by before the exponential, as a positive normal
+// number: with zero (tiny scales of e4m3 keys, zero queries) a masked score of
+// -inf would become NaN. Products of scores with one this small are as good
+// as zero.
+__device__ __forceinline__ float positive(float mult) { return mult < 1.17549435e-38f ? 1.17549435e-38f : mult; }
+
 // Cached tokens of sequence b, within the capacity of its table row.
 __device__ __forceinline__ int seq_length(const AttnArgs& a, int b) {
   return checked(a, a.lens[b], (int)min((long long)a.max_pages << a.cache.page_shift, 0x7fffffffll));

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import bit_weight_only_g128_gb300 as w4
-from test_gpu_layer import BF16, FP16, gen
+from test_gpu_layer import BF16, E4M3, FP16, check_attention, gen, normal, scattered
 
 pytestmark = pytest.mark.gpu
 
@@ -62,3 +62,27 @@ def test_norm_codes_of_tiny_results(size, K):
     assert not aq[x == 0].any() and float(s[2]) == 1.0
     if y.abs().amax() / 127 > 2.0 ** -140:  # (the scale has bits enough to tell)
         assert (aq[0, ::2] == 127).all() and (aq[1, 1::2] == -127).all()
+
+
+@pytest.mark.parametrize("dtype", [FP16, BF16])
+@pytest.mark.parametrize("k_scale", [0.02, 1e-20])
+@pytest.mark.parametrize("scale", [0.0, 1e-30, 1e-7, 0.125])
+def test_scores_too_small_for_their_factor(scale, k_scale, dtype):
+    """Queries of zero, or of ordinary size under tiny scales, over e4m3 keys:
+    the mean of the values, whatever the masked places held."""
+    lens, heads, hk = [300, 1, 33, 700], 8, 2
+    g = gen(35)
+    cache, tab = scattered(g, lens, hk, 16, 64, E4M3)
+    cache.k_scale.fill_(k_scale)
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    for std in (0.0, 1.0):
+        q = normal(g, 4, heads, 64, std=std, dtype=dtype)
+        q[0] = 0
+        got, lse = w4.attn_decode(q, cache, tab, n, scale=scale, return_lse=True)
+        check_attention(q, cache, tab, [0, 1, 2, 3, 4], lens, got, lse, scale)
+        starts = [0, 100, 101, 134, 150]
+        q = normal(g, 150, heads, 64, std=std, dtype=dtype)
+        got, lse = w4.attn_prompt(q, cache, tab, torch.tensor(starts, dtype=torch.int32, device="cuda"), n,
+                                  scale=scale, return_lse=True)
+        check_attention(q, cache, tab, starts, lens, got, lse, scale)
+    w4.device_status()
