@@ -71,7 +71,8 @@ int check_attn(AttnArgs* a, const uint16_t* q, int64_t q_stride, const void* k, 
     return fail(W4A16_ERR_UNSUPPORTED_SHAPE, "%d pages of %d tokens per sequence: above 2^30 tokens", max_pages, page_size);
   if (!std::isfinite(scale)) return fail(W4A16_ERR_INVALID_ARG, "scale=%g is not finite", (double)scale);
   if (q_stride < (int64_t)heads * head_dim) return fail(W4A16_ERR_INVALID_ARG, "q's row stride is below heads * head_dim");
-  if (rows > 0 && (!q || !table || !lens || !out)) return fail(W4A16_ERR_INVALID_ARG, "null pointer");
+  // (no sequence has no lengths, and sequences of no pages have no table)
+  if (rows > 0 && batch > 0 && (!q || (!table && max_pages > 0) || !lens || !out)) return fail(W4A16_ERR_INVALID_ARG, "null pointer");
   if (!aligned(q, 16) || !aligned(out, 16) || q_stride % 8)
     return fail(W4A16_ERR_MISALIGNED, "alignment: q, its rows and out need 16 bytes");
   if (!aligned(table, 4) || !aligned(lens, 4) || !aligned(lse, 4))

@@ -418,8 +418,8 @@ int w4a16_attn_workspace_size(int tokens, int batch, int heads, int kv_heads, in
  * q [batch] rows (stride in elements, heads adjacent, 16-byte aligned rows),
  * out [batch][heads][head_dim]; lse [batch][heads] fp32 (or null) receives
  * the logarithm of the softmax's sum. table [batch] rows (stride in
- * elements) of max_pages page numbers, of which the first
- * ceil(lens[b] / page_size) are read. A length of 0 gives zeros and -inf.
+ * elements) of max_pages page numbers (null where that is 0), of which the
+ * first ceil(lens[b] / page_size) are read. A length of 0 gives zeros and -inf.
  * What the cache holds beyond a sequence's length is never used. A length
  * below 0 or beyond the table's row is clamped and a page number outside the
  * cache reads page 0, both recorded (bit 128). */

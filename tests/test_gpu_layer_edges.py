@@ -86,3 +86,23 @@ def test_scores_too_small_for_their_factor(scale, k_scale, dtype):
                                   scale=scale, return_lse=True)
         check_attention(q, cache, tab, starts, lens, got, lse, scale)
     w4.device_status()
+
+
+def test_sequences_of_no_pages():
+    """Tables of no columns, as a server's first step of empty slots has them,
+    and a prompt call of no sequences."""
+    g = gen(36)
+    cache, _ = scattered(g, [20], 2, 16, 64, FP16)
+    n = torch.zeros(3, dtype=torch.int32, device="cuda")
+    tab = torch.empty((3, 0), dtype=torch.int32, device="cuda")
+    got, lse = w4.attn_decode(normal(g, 3, 8, 64, dtype=FP16), cache, tab, n, return_lse=True)
+    assert not got.any() and lse.isneginf().all()
+    st = torch.tensor([0, 2, 2, 5], dtype=torch.int32, device="cuda")
+    q = normal(g, 5, 8, 64, dtype=FP16)
+    got, lse = w4.attn_prompt(q, cache, tab, st, n, return_lse=True)
+    assert not got.any() and lse.isneginf().all()
+    out = torch.full_like(q, 3.0)
+    assert w4.attn_prompt(q, cache, tab[:0], st[:1], n[:0], out=out) is out
+    assert (out == 3).all()
+    assert w4.attn_decode(q[:0], cache, tab[:0], n[:0]).shape == (0, 8, 64)
+    w4.device_status()
