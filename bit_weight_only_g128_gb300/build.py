@@ -28,6 +28,7 @@ LIB = os.path.join(BUILD, "libw4a16.so")
 BUILD_CHECKED = os.path.join(BUILD, "checked")
 LIB_CHECKED = os.path.join(BUILD_CHECKED, "libw4a16_checked.so")
 BINDING = os.path.join(BUILD, "_binding.so")
+BINDING_FOR = BINDING + ".torch"  # the PyTorch version that it was compiled for
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -48,14 +49,24 @@ def _deps_mtime() -> float:
     return max(os.path.getmtime(f) for f in files)
 
 
+def binding_version() -> str:
+    """The PyTorch version that _binding.so was compiled for ("" without one)."""
+    if not (os.path.exists(BINDING) and os.path.exists(BINDING_FOR)):
+        return ""
+    with open(BINDING_FOR) as f:
+        return f.read()
+
+
 def build_binding(force: bool = False) -> str:
     """Compile csrc/binding.cpp to the CPython module _build/_binding.so
-    (against PyTorch's headers, host compiler); returns its path."""
+    (against PyTorch's headers, host compiler) if it is not there, older than
+    its sources or of another PyTorch; returns its path."""
+    import torch
     src = os.path.join(CSRC, "binding.cpp")
     deps = [src] + glob.glob(os.path.join(INCLUDE, "*.h"))
-    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(map(os.path.getmtime, deps)):
+    if (not force and binding_version() == torch.__version__
+            and os.path.getmtime(BINDING) >= max(map(os.path.getmtime, deps))):
         return BINDING
-    import torch
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     headers = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
@@ -70,6 +81,8 @@ def build_binding(force: bool = False) -> str:
     if res.returncode != 0:
         raise RuntimeError(f"{cmd[0]} failed for binding.cpp:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, BINDING)
+    with open(BINDING_FOR, "w") as f:
+        f.write(torch.__version__)
     return BINDING
 
 

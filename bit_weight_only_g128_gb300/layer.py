@@ -115,10 +115,13 @@ def _native():
     (raises if either has not been built)."""
     global _native_module
     if _native_module is None:
-        from .build import BINDING
+        from .build import BINDING, binding_version
         lib = w4.lib()
         if not os.path.exists(BINDING):
             raise ImportError(f"{BINDING} is missing: build it with `python -m bit_weight_only_g128_gb300.build`")
+        if binding_version() != torch.__version__:
+            raise ImportError(f"{BINDING} was compiled for another PyTorch ({binding_version() or 'unknown'}, this is "
+                              f"{torch.__version__}): build it again")
         spec = importlib.util.spec_from_file_location("_binding", BINDING)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
