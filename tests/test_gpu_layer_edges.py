@@ -5,9 +5,44 @@ import pytest
 import torch
 
 import bit_weight_only_g128_gb300 as w4
-from test_gpu_layer import BF16, E4M3, FP16, check_attention, gen, normal, scattered
+from test_gpu_layer import BF16, E4M3, FP16, check_attention, gen, normal, same, scattered
 
 pytestmark = pytest.mark.gpu
+
+TYPES = [(FP16, FP16), (BF16, BF16), (FP16, E4M3), (BF16, E4M3)]
+
+
+@pytest.mark.parametrize("batch", [129, 300])
+@pytest.mark.parametrize("dtype,cache_dtype", TYPES)
+def test_decode_of_many_sequences(batch, dtype, cache_dtype):
+    g = gen(batch)
+    lens = [(37 * b) % 211 for b in range(batch)]
+    lens[-1] = 3000
+    cache, tab = scattered(g, lens, 2, 16, 128, cache_dtype)
+    q = normal(g, batch, 4, 128, std=2, dtype=dtype)
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    got, lse = w4.attn_decode(q, cache, tab, n, return_lse=True)
+    w4.device_status()
+    check_attention(q, cache, tab, list(range(batch + 1)), lens, got, lse, 128 ** -0.5)
+    assert same(w4.attn_decode(q, cache, tab, n), got)
+
+
+@pytest.mark.parametrize("batch", [33, 70])
+@pytest.mark.parametrize("dtype,cache_dtype", TYPES)
+def test_prompts_of_many_sequences(batch, dtype, cache_dtype):
+    g = gen(batch)
+    new = [(13 * b) % 41 for b in range(batch)]
+    lens = [a + (29 * b) % 97 for b, a in enumerate(new)]
+    new[batch // 2], lens[batch // 2] = 200, 2500
+    cache, tab = scattered(g, lens, 2, 16, 64, cache_dtype)
+    starts = [sum(new[:b]) for b in range(batch + 1)]
+    q = normal(g, starts[-1], 8, 64, std=2, dtype=dtype)
+    st = torch.tensor(starts, dtype=torch.int32, device="cuda")
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    for t in (tab, tab[:, : -(-2500 // 16)].contiguous()):
+        got, lse = w4.attn_prompt(q, cache, t, st, n, return_lse=True)
+        w4.device_status()
+        check_attention(q, cache, t, starts, lens, got, lse, 64 ** -0.5)
 
 
 @pytest.mark.parametrize("dtype", [FP16, BF16])
