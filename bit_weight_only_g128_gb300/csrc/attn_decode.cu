@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks<kHeads>) attn_decode_kernel(
     float mult[kNb][2];
 #pragma unroll
     for (int nb = 0; nb < kNb; ++nb) {
-      const float m0 = positive(p.mult * (k8 ? a.cache.k_scale[head] : 1.f));
+      const float m0 = k8 ? positive(p.mult * a.cache.k_scale[head]) : p.mult;
       float top = 0.f;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i)

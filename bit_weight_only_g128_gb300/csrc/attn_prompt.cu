@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
       const int limit = live ? unit.len - unit.fresh + token + 1 - unit.j0 * kTile : 0x7fffffff;
       const bool idle = __all_sync(0xffffffffu, !live);
       int to = live ? (unit.first + token) * a.heads + head : -1;
-      const float mult = positive(p.mult * (k8 ? a.cache.k_scale[unit.head] : 1.f));
+      const float mult = k8 ? positive(p.mult * a.cache.k_scale[unit.head]) : p.mult;
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < nt; ++j) {
         if (!(ok = warp_wait(kScores + t, score_phase, kErrEpilogue))) break;
