@@ -121,10 +121,11 @@ at::Tensor result(PyObject* given, const char* name, at::IntArrayRef shape, at::
 // so that is the tensors' for the call.
 struct CallStream {
   void* ptr;
-  c10::cuda::CUDAGuard device;
+  c10::cuda::OptionalCUDAGuard device;  // (empty where it is current already: one query less)
   c10::cuda::OptionalCUDAStreamGuard guard;
 
-  CallStream(PyObject* o, const at::Device& dev) : device(dev) {
+  CallStream(PyObject* o, const at::Device& dev) {
+    if (c10::cuda::current_device() != dev.index()) device.set_device(dev);
     if (o == Py_None) {
       ptr = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
       return;
