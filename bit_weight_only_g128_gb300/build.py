@@ -3,9 +3,10 @@
 Each translation unit is compiled by nvcc in parallel, then linked into one
 shared library against the shared CUDA runtime (the one PyTorch loads).
 ``build(checked=True)`` builds the bounds-checked variant instead
-(-DW4A16_CHECKED, _build/checked/libw4a16_checked.so): every global and
-shared-memory access of its kernels is tested against its buffer first, and
-an access outside sets a bit of the device error word instead of running.
+(-DW4A16_CHECKED, _build/checked/libw4a16_checked.so): every global access of
+its kernels and every place in shared memory that a copy or a product is given
+is tested against its buffer first, and one outside sets a bit of the device
+error word instead of being used (csrc/common.cuh).
 Load it by setting W4A16_LIBRARY to its path before the binding loads the
 library. Both also compile csrc/binding.cpp (the Python binding's native part)
 with the host compiler against PyTorch's headers. Running ``python -m bit_weight_only_g128_gb300.build [--checked]``

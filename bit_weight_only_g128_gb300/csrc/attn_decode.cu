@@ -41,6 +41,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTileBytes = 4096;  // of keys, and as many of values
+constexpr size_t kFlagBytes = 32768;  // of the workspace: arrival counters, zero between calls
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // Blocks per SM and ring slots of a warp by the heads of an item: 8 heads'
@@ -75,6 +76,7 @@ struct DecodeArgs {
   AttnArgs a;
   int* arrived;  // one counter per block: parts of the split item that it begins
   float* parts;  // [blocks][2] of kPartFloats
+  size_t part_floats;  // of all of them
   int group, tiles;  // query heads per key/value head, items of kHeads of them
   float mult;        // |scale| log2 e
   uint32_t negate;   // sign bits of a pair of queries, where scale < 0
@@ -262,6 +264,12 @@ __global__ void __launch_bounds__(kThreads, kBlocks<kHeads>) attn_decode_kernel(
   for (int i = 0; i < kPeriod; ++i) place[i] = tile_at<kRowBytes>(r0 + i * kLaneRows, c0);
   const uint8_t* const k_lane = static_cast<const uint8_t*>(a.cache.k) + r0 * kRowBytes + c0 * 16;
   const uint8_t* const v_lane = static_cast<const uint8_t*>(a.cache.v) + r0 * kRowBytes + c0 * 16;
+  // a 16-byte copy from the cache into the ring
+  const uint32_t shared = (uint32_t)__cvta_generic_to_shared(smem_raw);
+  const size_t cache_bytes = cache_rows(a.cache) * kRowBytes;
+  auto fetch = [&](uint32_t to, const uint8_t* from, const void* cache, bool valid) {
+    if (in_smem(to, 16, shared, a.err)) cp16(to, ld_at(from, static_cast<const uint8_t*>(cache), cache_bytes - 15, a.err), valid);
+  };
   auto issue = [&](int slot) {  // the next step's tile of this warp into a ring slot
     if (load_left > 0) {
       --load_left;
@@ -283,12 +291,12 @@ __global__ void __launch_bounds__(kThreads, kBlocks<kHeads>) attn_decode_kernel(
               const int n = i * (16 / kLaneRows) + x;
               const uint32_t to = dst + place[n % kPeriod] + n / kPeriod * kPeriod * kLaneRows * kRowBytes;
               if (whole) {
-                cp16(to, k + x * kLaneRows * kRowBytes, true);
-                cp16(to + kTileBytes, v + x * kLaneRows * kRowBytes, true);
+                fetch(to, k + x * kLaneRows * kRowBytes, a.cache.k, true);
+                fetch(to + kTileBytes, v + x * kLaneRows * kRowBytes, a.cache.v, true);
               } else {
                 const bool valid = tok + r0 + x * kLaneRows < load.len;
-                cp16(to, valid ? k + x * kLaneRows * kRowBytes : k_lane, valid);
-                cp16(to + kTileBytes, valid ? v + x * kLaneRows * kRowBytes : v_lane, valid);
+                fetch(to, valid ? k + x * kLaneRows * kRowBytes : k_lane, a.cache.k, valid);
+                fetch(to + kTileBytes, valid ? v + x * kLaneRows * kRowBytes : v_lane, a.cache.v, valid);
               }
             }
           } else {  // rows beyond the sequence, as zeros
@@ -296,8 +304,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks<kHeads>) attn_decode_kernel(
             for (int x = 0; x < 16 / kLaneRows; ++x) {
               const int n = i * (16 / kLaneRows) + x;
               const uint32_t to = dst + place[n % kPeriod] + n / kPeriod * kPeriod * kLaneRows * kRowBytes;
-              cp16(to, k_lane, false);
-              cp16(to + kTileBytes, v_lane, false);
+              fetch(to, k_lane, a.cache.k, false);
+              fetch(to + kTileBytes, v_lane, a.cache.v, false);
             }
           }
         }
@@ -321,7 +329,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks<kHeads>) attn_decode_kernel(
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           const int d = k8 ? 16 * i + 4 * t + 2 * w : 16 * i + 2 * t + 8 * w;
-          qf[nb][i][w] = some ? *reinterpret_cast<const uint32_t*>(from + d) : 0;
+          qf[nb][i][w] = some ? *ld_at(reinterpret_cast<const uint32_t*>(from + d), reinterpret_cast<const uint32_t*>(a.q),
+                                       span(a.batch, a.ldq, a.heads * D) / 2, a.err)
+                              : 0;
         }
     }
   };
@@ -345,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks<kHeads>) attn_decode_kernel(
     float mult[kNb][2];
 #pragma unroll
     for (int nb = 0; nb < kNb; ++nb) {
-      const float m0 = k8 ? positive(p.mult * a.cache.k_scale[head]) : p.mult;
+      const float m0 = k8 ? positive(p.mult * *ld_at(a.cache.k_scale + head, a.cache.k_scale, (size_t)a.cache.kv_heads, a.err)) : p.mult;
       float top = 0.f;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i)
@@ -551,8 +561,16 @@ __global__ void __launch_bounds__(kThreads, kBlocks<kHeads>) attn_decode_kernel(
     __syncthreads();
     const bool whole = starts && ends;
     float* part = p.parts + (size_t)(2 * me + (starts ? 1 : 0)) * kPartFloats<D, kHeads>;
-    const float v_scale = k8 ? a.cache.v_scale[head] : 1.f;
+    const float v_scale = k8 ? *ld_at(a.cache.v_scale + head, a.cache.v_scale, (size_t)a.cache.kv_heads, a.err) : 1.f;
     const size_t out0 = (size_t)cur.b * a.heads + head * p.group + head0;
+    auto put_out = [&](int h, int d, uint2 v) {
+      uint16_t* to = a.out + (out0 + h) * D + d;
+      if (in_buf(to, a.out, (size_t)a.batch * a.heads * D - 3, a.err)) *reinterpret_cast<uint2*>(to) = v;
+    };
+    auto put_lse = [&](int h, float top, float sum) {
+      if (a.lse && in_buf(a.lse + out0 + h, a.lse, (size_t)a.batch * a.heads, a.err))
+        a.lse[out0 + h] = sum == 0.f ? -INFINITY : top * kLn2 + logf(sum);
+    };
 #pragma unroll
     for (int nb = 0; nb < kNb; ++nb)
 #pragma unroll
@@ -595,17 +613,16 @@ __global__ void __launch_bounds__(kThreads, kBlocks<kHeads>) attn_decode_kernel(
         }
         if (whole) {
           const float l1 = sm.sum[h], inv = l1 == 0.f ? 0.f : v_scale / l1;  // (a NaN sum is the result)
-          *reinterpret_cast<uint2*>(a.out + (out0 + h) * D + d) =
-              make_uint2(pack16<kB>(v.x * inv, v.y * inv), pack16<kB>(v.z * inv, v.w * inv));
-        } else {
+          put_out(h, d, make_uint2(pack16<kB>(v.x * inv, v.y * inv), pack16<kB>(v.z * inv, v.w * inv)));
+        } else if (in_buf(part + h * D + d, p.parts, p.part_floats - 3, a.err)) {
           *reinterpret_cast<float4*>(part + h * D + d) = v;
         }
       }
     }
     if (tid < heads) {
       if (whole) {
-        if (a.lse) a.lse[out0 + tid] = sm.sum[tid] == 0.f ? -INFINITY : sm.top[tid] * kLn2 + logf(sm.sum[tid]);
-      } else {
+        put_lse(tid, sm.top[tid], sm.sum[tid]);
+      } else if (in_buf(part + kHeads * D + kHeads + tid, p.parts, p.part_floats, a.err)) {
         part[kHeads * D + tid] = sm.top[tid];
         part[kHeads * D + kHeads + tid] = sm.sum[tid];
       }
@@ -623,8 +640,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks<kHeads>) attn_decode_kernel(
       __syncthreads();
       if (tid == 0) {
         // the block's part before its arrival, the others' before what follows
-        int before;
-        asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(p.arrived + first) : "memory");
+        int before = -1;
+        if (in_buf(p.arrived + first, p.arrived, kFlagBytes / sizeof(int), a.err))
+          asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(p.arrived + first) : "memory");
         sm.last = before == (int)(final - first);
       }
       __syncthreads();
@@ -646,6 +664,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks<kHeads>) attn_decode_kernel(
               x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
               if (i0 + i < count) {
                 const float* q = p.parts + (size_t)(2 * (first + i0 + i) + (i0 + i == 0 ? 1 : 0)) * kPartFloats<D, kHeads>;
+                q = ld_at(q, p.parts, p.part_floats - kPartFloats<D, kHeads> + 1, a.err);
                 mi[i] = __ldcg(q + kHeads * D + h);
                 li[i] = __ldcg(q + kHeads * D + kHeads + h);
                 x[i] = __ldcg(reinterpret_cast<const float4*>(q + h * D + d));
@@ -666,9 +685,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks<kHeads>) attn_decode_kernel(
             }
           }
           const float inv = sum == 0.f ? 0.f : v_scale / sum;
-          *reinterpret_cast<uint2*>(a.out + (out0 + h) * D + d) =
-              make_uint2(pack16<kB>(v.x * inv, v.y * inv), pack16<kB>(v.z * inv, v.w * inv));
-          if (a.lse && d == 0) a.lse[out0 + h] = sum == 0.f ? -INFINITY : top * kLn2 + logf(sum);
+          put_out(h, d, make_uint2(pack16<kB>(v.x * inv, v.y * inv), pack16<kB>(v.z * inv, v.w * inv)));
+          if (d == 0) put_lse(h, top, sum);
         }
         if (tid == 0) p.arrived[first] = 0;  // left zero for the next call
       }
@@ -701,8 +719,6 @@ cudaError_t launch_heads(DecodeArgs& p, int sms, cudaStream_t stream) {
   return heads == 8 ? launch<kB, k8, D, 8>(p, sms, stream) : launch<kB, k8, D, 16>(p, sms, stream);
 }
 
-constexpr size_t kFlagBytes = 32768;
-
 }  // namespace
 
 size_t attn_decode_workspace_bytes(int head_dim, int sms) {
@@ -719,6 +735,7 @@ cudaError_t launch_attn_decode(const AttnArgs& args, int head_dim, bool bf16, bo
   if (e != cudaSuccess) return e;
   p.arrived = static_cast<int*>(workspace);
   p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kFlagBytes);
+  p.part_floats = (attn_decode_workspace_bytes(head_dim, sms) - kFlagBytes) / sizeof(float);
   p.group = args.heads / args.cache.kv_heads;
   // the scores' maximum is taken before the scale, so it has to be positive:
   // a negative scale negates the queries, and a scale of zero becomes one too

@@ -124,6 +124,7 @@ struct PromptArgs {
   int* queue;       // next unit; at [2], 64 bits: blocks that are through << 32 | what they drew
   float* partial;   // [blocks][8 warps] of kPartFloats, where units can be split
   int* joins;       // [blocks][8 warps]
+  size_t partial_floats;  // of the workspace's
   int most_parts;
 };
 
@@ -383,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
       const int limit = live ? unit.len - unit.fresh + token + 1 - unit.j0 * kTile : 0x7fffffff;
       const bool idle = __all_sync(0xffffffffu, !live);
       int to = live ? (unit.first + token) * a.heads + head : -1;
-      const float mult = k8 ? positive(p.mult * a.cache.k_scale[unit.head]) : p.mult;
+      const float mult = k8 ? positive(p.mult * *ld_at(a.cache.k_scale + unit.head, a.cache.k_scale, (size_t)a.cache.kv_heads, a.err)) : p.mult;
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < nt; ++j) {
         if (!(ok = warp_wait(kScores + t, score_phase, kErrEpilogue))) break;
@@ -395,6 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
         }
         tc_fence_after();
         uint32_t s[4][32];
+        in_tmem((uint32_t)(t * kTile), kTile, 512, a.err);
 #pragma unroll
         for (int q = 0; q < 4; ++q) tmem_ld32(scores + 32 * q, s[q]);
         tmem_wait_ld();
@@ -479,9 +481,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
       }
       if (!ok) break;
       // (Loops: code that runs once per unit is fetched anew every time.)
+      in_tmem(256u + (uint32_t)(t * D), D, 512, a.err);
       float* mine = p.partial + (size_t)(unit.slot * 8 + warp) * kPartFloats<D>;
       if (unit.parts > 1) {
-        if (!idle) {
+        if (!idle && in_buf(mine + kPartFloats<D> - 1, p.partial, p.partial_floats, a.err) &&
+            in_buf(p.joins + unit.slot * 8 + warp, p.joins, (kFlagBytes - kJoinsAt) / sizeof(int), a.err)) {
           if (nt > 0) {
 #pragma unroll 1
             for (int d0 = 0; d0 < D; d0 += 32) {
@@ -502,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
         to = -1;  // written by the joining kernel
       } else {
         // (a sum of zero: no key has weight; a NaN sum is the row's result)
-        const float inv = l == 0.f ? 0.f : (k8 ? a.cache.v_scale[unit.head] : 1.f) / l;
+        const float inv = l == 0.f ? 0.f : (k8 ? *ld_at(a.cache.v_scale + unit.head, a.cache.v_scale, (size_t)a.cache.kv_heads, a.err) : 1.f) / l;
 #pragma unroll 2
         for (int d0 = 0; d0 < D; d0 += 32) {
           uint32_t o[32];
@@ -534,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int place = __shfl_sync(0xffffffffu, to, (lane & 28) + i);
-            if (place >= 0)
+            if (place >= 0 && in_buf(a.out + (size_t)place * D + d0 + (lane & 3) * 8, a.out, (size_t)a.rows * a.heads * D - 7, a.err))
               *reinterpret_cast<uint4*>(a.out + (size_t)place * D + d0 + (lane & 3) * 8) = make_uint4(x[i][0], x[i][1], x[i][2], x[i][3]);
           }
         }
@@ -543,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
         tc_fence_before();
         mbar_arrive(bar(kOutFree + t));
       }
-      if (to >= 0 && a.lse) a.lse[to] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+      if (to >= 0 && a.lse && in_buf(a.lse + to, a.lse, (size_t)a.rows * a.heads, a.err)) a.lse[to] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kUnitFree + (u & 1)));
     }
@@ -573,6 +577,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
         auto row_of = [&](int key) {
           return (((unsigned long long)page_of(a, unit.b, key >> shift) * a.cache.kv_heads + unit.head) << shift) + (key & mask);
         };
+        // a tile copy's first row and its place: as they are, or (checked
+        // build) 0 and the first slot, recorded, where it would leave them
+        auto first_row = [&](unsigned long long row, int n) {
+          if (!kCheckedBuild || row + n <= cache_rows(a.cache)) return (int)row;
+          atomicOr(a.err, kErrBounds);
+          return 0;
+        };
+        auto slot_at = [&](uint32_t at, uint32_t bytes) { return in_smem(at, bytes, raw, a.err) ? at : ring; };
         if (!k8) {
           // tiles that lie inside the sequence: tile copies of the pages' rows,
           // a lane for each page and panel. Small pages' copies (16 of them
@@ -597,8 +609,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
               if (mine == 0) mbar_expect_tx(full, kBytes);
               __syncwarp();
               if (lane < each)
-                tma_load_2d(ring + slot_of() * kBytes + panel * kPanel + part * box * 128, values ? &map_v : &map_k, panel * 64,
-                            (int)row, full);
+                tma_load_2d(slot_at(ring + slot_of() * kBytes, kBytes) + panel * kPanel + part * box * 128, values ? &map_v : &map_k,
+                            panel * 64, first_row(row, box), full);
               copied = count + 1;
             }
           }
@@ -623,7 +635,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
                   const int r = r0 + x * kStride;
                   const unsigned long long row = __shfl_sync(0xffffffffu, group, r >> 4) + (r & 15);
                   const bool valid = key0 + r < len;
-                  cp16(dst + x * kStride * 128, valid ? src + row * (2 * D) + c * 16 : src, valid);
+                  const uint8_t* from = valid ? ld_at(src + row * (2 * D) + c * 16, src, cache_rows(a.cache) * (2 * D) - 15, a.err) : src;
+                  if (in_smem(dst + x * kStride * 128, 16, raw, a.err)) cp16(dst + x * kStride * 128, from, valid);
                 }
                 cp_commit();
                 slots[kv] = slot_of();
@@ -662,7 +675,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
             if (mine == 0) mbar_expect_tx(bar(kCodes + at), kTile * D);
             __syncwarp();
             if (lane < each)
-              tma_load_2d(codes + at * (kTile * D) + mine * box * D, i & 1 ? &map_v : &map_k, 0, (int)row, bar(kCodes + at));
+              tma_load_2d(slot_at(codes + at * (kTile * D), kTile * D) + mine * box * D, i & 1 ? &map_v : &map_k, 0,
+                          first_row(row, box), bar(kCodes + at));
             copied = n + 1;
             return true;
           };
@@ -687,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
             };
             load(0);
             if (!(ok = wait_slot())) break;
-            const uint32_t to = ring + slot_of() * kBytes + chunk_at(r0, c);
+            const uint32_t to = slot_at(ring + slot_of() * kBytes, kBytes) + chunk_at(r0, c);
             auto groups = [&](auto b16) {
 #pragma unroll
               for (int g = 0; g < kLoads / kGroup; ++g) {
@@ -730,7 +744,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
         const int b = 32 * group + lane;
         first = fresh = len = v = 0;
         if (b < a.batch) {
-          const int s0 = a.starts[b], s1 = a.starts[b + 1], n0 = a.lens[b];
+          const int s0 = *ld_at(a.starts + b, a.starts, (size_t)a.batch + 1, a.err);
+          const int s1 = *ld_at(a.starts + b + 1, a.starts, (size_t)a.batch + 1, a.err);
+          const int n0 = *ld_at(a.lens + b, a.lens, (size_t)a.batch, a.err);
           first = checked(a, s0, a.rows);
           fresh = checked(a, s1, a.rows) - first;
           if (fresh < 0) {
@@ -826,7 +842,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
                 mbar_expect_tx(bar(kQueries + t), kBytes);
 #pragma unroll
                 for (int d = 0; d < D / 64; ++d)
-                  tma_load_3d(base + t * kBytes + d * kPanel, &map_q, d * 64, unit.head * p.group,
+                  tma_load_3d((in_smem(base + t * kBytes, kBytes, raw, a.err) ? base + t * kBytes : base) + d * kPanel, &map_q, d * 64, unit.head * p.group,
                               unit.first + (unit.row0 + t * kTile) / p.group, bar(kQueries + t));
               }
               ++asked;
@@ -846,7 +862,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
           for (int r = w / kChunks; r < kTile; r += kStride) {
             const bool valid = row < unit.fresh * p.group;
             const uint32_t dst = base + t * kBytes + chunk_at(r, c);
-            cp16(dst, valid ? src : a.q, valid);
+            const uint16_t* from = valid ? ld_at(src, a.q, span(a.rows, a.ldq, a.heads * D) - 7, a.err) : a.q;
+            if (in_smem(dst, 16, raw, a.err)) cp16(dst, from, valid);
             row += kStride;
             src += step;
             head += step_head;
@@ -899,6 +916,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
         return ok;
       };
       auto score = [&](int slot, bool last) {
+        if (!in_smem(ring + slot * kBytes, kBytes, raw, a.err)) slot = 0;
+        in_smem(base + t * kBytes, kBytes, raw, a.err), in_tmem((uint32_t)(t * kTile), kTile, 512, a.err);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t off = (uint32_t)((k >> 2) * kPanel + (k & 3) * 32) >> 4;
@@ -909,6 +928,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
         if (last) tc_commit(bar(kQueriesFree + t));
       };
       auto value = [&](int slot, int part, bool add) {  // 96 or 32 keys
+        if (!in_smem(ring + slot * kBytes, kBytes, raw, a.err)) slot = 0;
+        in_tmem(256u + (uint32_t)(t * D), D, 512, a.err);
 #pragma unroll
         for (int k = part ? 6 : 0; k < (part ? 8 : 6); ++k)
           mma_ts(out, scores + 8 * k, v_lo + slot * (kBytes >> 4) + k * (2048 >> 4), kDescHi, idesc_o, add || k > 0);
@@ -986,7 +1007,7 @@ __global__ void __launch_bounds__(D) attn_join_kernel(const PromptArgs p) {
   const int lane = threadIdx.x & 31, d0 = threadIdx.x & ~31;
   const float* first = p.partial + (size_t)blockIdx.x * kPartFloats<D>;
   constexpr size_t kNext = (size_t)8 * kPartFloats<D>;
-  const int parts = p.joins[blockIdx.x];
+  const int parts = *ld_at(p.joins + blockIdx.x, p.joins, (kFlagBytes - kJoinsAt) / sizeof(int), p.a.err);
   if (parts == 0) return;
   __syncthreads();  // all have read it
   if (threadIdx.x == 0) p.joins[blockIdx.x] = 0;
@@ -1002,7 +1023,7 @@ __global__ void __launch_bounds__(D) attn_join_kernel(const PromptArgs p) {
   for (int i = 0; i < 32; ++i) o[i] = 0.f;
 #pragma unroll 2
   for (int i = 0; i < parts; ++i) {
-    const float* from = first + i * kNext;
+    const float* from = ld_at(first + i * kNext, p.partial, p.partial_floats - kPartFloats<D> + 1, p.a.err);
     const float mi = from[32 * D + lane], li = from[32 * (D + 1) + lane];
     float4 x[8];
 #pragma unroll
@@ -1022,8 +1043,9 @@ __global__ void __launch_bounds__(D) attn_join_kernel(const PromptArgs p) {
   }
   if (to < 0) return;
   const int head = to % p.a.heads / p.group;
-  const float inv = l == 0.f ? 0.f : (p.a.cache.v_scale ? p.a.cache.v_scale[head] : 1.f) / l;
+  const float inv = l == 0.f ? 0.f : (p.a.cache.v_scale ? *ld_at(p.a.cache.v_scale + head, p.a.cache.v_scale, (size_t)p.a.cache.kv_heads, p.a.err) : 1.f) / l;
   uint16_t* dst = p.a.out + (size_t)to * D + d0;
+  if (!in_buf(dst + 24, p.a.out, (size_t)p.a.rows * p.a.heads * D - 7, p.a.err)) return;
 #pragma unroll
   for (int i = 0; i < 32; i += 8)
     *reinterpret_cast<uint4*>(dst + i) =
@@ -1110,6 +1132,7 @@ cudaError_t launch_attn_prompt(const AttnArgs& args, int head_dim, bool bf16, bo
   p.queue = static_cast<int*>(workspace);
   p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kFlagBytes);
   p.joins = reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + kJoinsAt);
+  p.partial_floats = (attn_prompt_workspace_bytes(args.rows, p.group, args.cache.kv_heads, head_dim, sms) - kFlagBytes) / sizeof(float);
   // a block per SM, or as many as there can be units (whole ones of all rows,
   // and a ragged one per sequence) where none is long enough for two parts
   const long long units = ((long long)args.rows * p.group / (2 * kTile) + args.batch) * args.cache.kv_heads;

@@ -23,9 +23,11 @@ constexpr int kAtomK = 64;       // k per atom
 constexpr int kAtomWords = 128;  // 32-bit words per atom (16 * 64 / 8)
 
 // ------------------------------------------------------------------ checked build
-// Compiled with -DW4A16_CHECKED (build(checked=True)), every global and
-// shared-memory access of the kernels is tested against its buffer's extent
-// first; an access outside sets kErrBounds in the library's device error
+// Compiled with -DW4A16_CHECKED (build(checked=True)), every global access of
+// the kernels, every place in dynamic shared memory or tensor memory that a
+// copy or a product is given, and the GEMMs' own shared-memory accesses are
+// tested against their buffer's extent first (not the fixed arrays that a
+// kernel names in shared memory); an access outside sets kErrBounds in the library's device error
 // word and is skipped (a load reads the buffer's first element instead), so
 // nothing faults and w4a16_device_status reports it. In the normal build the
 // tests compile away.

@@ -71,6 +71,12 @@ __device__ __forceinline__ void e4m3x4_to_half2x2(uint32_t codes, uint32_t& lo, 
       : "r"(codes));
 }
 
+// Elements from the first row's first to the last row's last (for the checked
+// build's tests of strided arrays).
+__host__ __device__ __forceinline__ size_t span(long long rows, long long stride, long long cols) {
+  return rows > 0 ? (size_t)((rows - 1) * stride + cols) : 0;
+}
+
 // Error bit of data read on the device that names something outside its
 // buffer: a slot, a position, a page number, a length.
 constexpr int kErrRange = 128;
@@ -106,6 +112,11 @@ struct AttnArgs {
   int* err;
 };
 
+// Rows of the cache: [pages][kv heads][page_size].
+__device__ __forceinline__ size_t cache_rows(const PagedCache& c) {
+  return ((size_t)c.pages * c.kv_heads) << c.page_shift;
+}
+
 // A value read on the device that has to lie in [0, most]; one that does not
 // is recorded and clamped.
 __device__ __forceinline__ int checked(const AttnArgs& a, int v, int most) {
@@ -122,13 +133,13 @@ __device__ __forceinline__ float positive(float mult) { return mult < 1.17549435
 
 // Cached tokens of sequence b, within the capacity of its table row.
 __device__ __forceinline__ int seq_length(const AttnArgs& a, int b) {
-  return checked(a, a.lens[b], (int)min((long long)a.max_pages << a.cache.page_shift, 0x7fffffffll));
+  return checked(a, *ld_at(a.lens + b, a.lens, (size_t)a.batch, a.err), (int)min((long long)a.max_pages << a.cache.page_shift, 0x7fffffffll));
 }
 
 // Page number i of sequence b; one outside the cache is recorded and page 0
 // read in its place.
 __device__ __forceinline__ int page_of(const AttnArgs& a, int b, int i) {
-  const int p = a.table[b * a.table_ld + i];
+  const int p = *ld_at(a.table + b * a.table_ld + i, a.table, span(a.batch, a.table_ld, a.max_pages), a.err);
   if ((unsigned)p < (unsigned)a.cache.pages) return p;
   atomicOr(a.err, kErrRange);
   return 0;

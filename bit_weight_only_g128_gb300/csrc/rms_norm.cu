@@ -83,9 +83,9 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormArgs a, int ro
     const int c = t + i * row_threads;
     xv[i] = rv[i] = wv[i] = make_uint4(0, 0, 0, 0);
     if (live && c < nv) {
-      xv[i] = ldg_stream(xr + c);
-      if (rr) rv[i] = rr[c];
-      if (kVecs <= 2) wv[i] = wr[c];  // in flight with the row (more would not fit the registers)
+      xv[i] = ldg_stream(ld_at(xr + c, reinterpret_cast<const uint4*>(a.x), span(a.M, a.ldx, a.K) / 8, a.err));
+      if (rr) rv[i] = *ld_at(rr + c, reinterpret_cast<const uint4*>(a.residual), span(a.M, a.ldr, a.K) / 8, a.err);
+      if (kVecs <= 2) wv[i] = *ld_at(wr + c, wr, (size_t)nv, a.err);  // in flight with the row (more would not fit the registers)
     }
   }
   float sum = 0.f;
@@ -116,9 +116,10 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormArgs a, int ro
         o.y = pack16<kB>(h[i][2], h[i][3]);
         o.z = pack16<kB>(h[i][4], h[i][5]);
         o.w = pack16<kB>(h[i][6], h[i][7]);
-        reinterpret_cast<uint4*>(a.h + m * a.ldh)[c] = o;
+        uint4* d = reinterpret_cast<uint4*>(a.h + m * a.ldh) + c;
+        if (in_buf(d, reinterpret_cast<uint4*>(a.h), span(a.M, a.ldh, a.K) / 8, a.err)) *d = o;
       }
-      const uint4 w = kVecs <= 2 ? wv[i] : wr[c];
+      const uint4 w = kVecs <= 2 ? wv[i] : *ld_at(wr + c, wr, (size_t)nv, a.err);
       const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -133,7 +134,8 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormArgs a, int ro
         o.y = pack16<kB>(h[i][2], h[i][3]);
         o.z = pack16<kB>(h[i][4], h[i][5]);
         o.w = pack16<kB>(h[i][6], h[i][7]);
-        reinterpret_cast<uint4*>(a.y + m * a.K)[c] = o;
+        uint4* d = reinterpret_cast<uint4*>(a.y + m * a.K) + c;
+        if (in_buf(d, reinterpret_cast<uint4*>(a.y), (size_t)a.M * nv, a.err)) *d = o;
       }
     }
   }
@@ -142,7 +144,7 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormArgs a, int ro
   if (!live) return;
   const float s = act_scale(top);
   const float inv = __frcp_rn(s);
-  if (t == 0) a.s_a[m] = s;
+  if (t == 0 && in_buf(a.s_a + m, a.s_a, (size_t)a.M, a.err)) a.s_a[m] = s;
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
     const int c = t + i * row_threads;
@@ -155,7 +157,8 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormArgs a, int ro
       o.y = pack16<kB>(h[i][2], h[i][3]);
       o.z = pack16<kB>(h[i][4], h[i][5]);
       o.w = pack16<kB>(h[i][6], h[i][7]);
-      reinterpret_cast<uint4*>(a.codes + m * a.K)[c] = o;
+      uint4* d = reinterpret_cast<uint4*>(a.codes + m * a.K) + c;
+      if (in_buf(d, reinterpret_cast<uint4*>(a.codes), (size_t)a.M * nv, a.err)) *d = o;
     }
     if (a.aq) {
       uint32_t lo = 0, hi = 0;
@@ -164,7 +167,8 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormArgs a, int ro
         lo |= ((uint32_t)(int)h[i][j] & 0xffu) << (8 * j);
         hi |= ((uint32_t)(int)h[i][4 + j] & 0xffu) << (8 * j);
       }
-      reinterpret_cast<uint2*>(a.aq + m * a.K)[c] = make_uint2(lo, hi);
+      uint2* d = reinterpret_cast<uint2*>(a.aq + m * a.K) + c;
+      if (in_buf(d, reinterpret_cast<uint2*>(a.aq), (size_t)a.M * nv, a.err)) *d = make_uint2(lo, hi);
     }
   }
 }
@@ -182,7 +186,15 @@ __global__ void __launch_bounds__(256) rms_norm_any_kernel(const NormArgs a) {
   const long long m = blockIdx.x;
   const uint16_t* xr = a.x + m * a.ldx;
   const uint16_t* rr = a.residual ? a.residual + m * a.ldr : nullptr;
-  auto value = [&](int k) { return value16<kB>(xr[k]) + (rr ? value16<kB>(rr[k]) : 0.f); };
+  auto value = [&](int k) {
+    return value16<kB>(*ld_at(xr + k, a.x, span(a.M, a.ldx, a.K), a.err)) +
+           (rr ? value16<kB>(*ld_at(rr + k, a.residual, span(a.M, a.ldr, a.K), a.err)) : 0.f);
+  };
+  auto weight = [&](int k) { return value16<kB>(*ld_at(a.weight + k, a.weight, (size_t)a.K, a.err)); };
+  auto store = [&](auto* base, long long ld, int k, auto v) {
+    auto* d = base + m * ld + k;
+    if (in_buf(d, base, span(a.M, ld, a.K), a.err)) *d = v;
+  };
   float sum = 0.f;
   for (int k = threadIdx.x; k < a.K; k += 256) {
     const float v = value(k);
@@ -194,21 +206,21 @@ __global__ void __launch_bounds__(256) rms_norm_any_kernel(const NormArgs a) {
   if (a.s_a) {
     float top = 0.f;
     for (int k = threadIdx.x; k < a.K; k += 256)
-      top = fmaxf(top, fabsf(value(k) * scale * value16<kB>(a.weight[k])));
+      top = fmaxf(top, fabsf(value(k) * scale * weight(k)));
     top = row_reduce<true>(top, 8, part2);
     s = act_scale(top);
     inv = __frcp_rn(s);
-    if (threadIdx.x == 0) a.s_a[m] = s;
+    if (threadIdx.x == 0) store(a.s_a, 1, 0, s);
   }
   for (int k = threadIdx.x; k < a.K; k += 256) {
     const float v = value(k);
-    const float y = v * scale * value16<kB>(a.weight[k]);
-    if (a.h) a.h[m * a.ldh + k] = bits16<kB>(v);
-    if (a.y) a.y[m * a.K + k] = bits16<kB>(y);
+    const float y = v * scale * weight(k);
+    if (a.h) store(a.h, a.ldh, k, bits16<kB>(v));
+    if (a.y) store(a.y, a.K, k, bits16<kB>(y));
     if (a.s_a) {
       const float c = act_code(y, s, inv);
-      if (a.codes) a.codes[m * a.K + k] = bits16<kB>(c);
-      if (a.aq) a.aq[m * a.K + k] = (int8_t)(int)c;
+      if (a.codes) store(a.codes, a.K, k, bits16<kB>(c));
+      if (a.aq) store(a.aq, a.K, k, (int8_t)(int)c);
     }
   }
 }

@@ -74,12 +74,13 @@ __global__ void __launch_bounds__(kMostThreads, 2) rope_append_kernel(const Rope
   for (int n = 0; n < 2; ++n) {
     const int h = h0 + n * stride;
     if (h < heads) {
-      x[n][0] = ldg_now(row + (size_t)h * D + d0);
-      x[n][1] = ldg_now(row + (size_t)h * D + d1);
+      const size_t all = span(a.T, a.ld, heads * D) - 7;
+      x[n][0] = ldg_now(ld_at(row + (size_t)h * D + d0, a.qkv, all, a.err));
+      x[n][1] = ldg_now(ld_at(row + (size_t)h * D + d1, a.qkv, all, a.err));
     }
   }
-  const long long slot = a.slots[t];
-  int pos = a.positions[t];
+  const long long slot = *ld_at(a.slots + t, a.slots, (size_t)a.T, a.err);
+  int pos = *ld_at(a.positions + t, a.positions, (size_t)a.T, a.err);
   bool keep = slot >= 0;
   if (slot >= a.capacity || pos < 0 || pos >= a.table_len) {
     if (threadIdx.x == 0) atomicOr(a.err, kErrRange);
@@ -90,6 +91,7 @@ __global__ void __launch_bounds__(kMostThreads, 2) rope_append_kernel(const Rope
   const size_t page = keep ? (size_t)(slot >> a.page_shift) : 0;
   const int off = keep ? (int)(slot & (page_size - 1)) : 0;
   const float* cosines = a.table + (size_t)pos * a.R + 8 * j;
+  if (turned) cosines = ld_at(cosines, a.table, (size_t)a.table_len * a.R - half - 7, a.err);
   const float* sines = cosines + half;
   float inv[2];  // of the head's e4m3 scale
 #pragma unroll
@@ -97,7 +99,9 @@ __global__ void __launch_bounds__(kMostThreads, 2) rope_append_kernel(const Rope
     const int h = h0 + n * stride;
     inv[n] = 1.f;
     if (k8 && h >= a.heads && h < heads)
-      inv[n] = __frcp_rn(h < a.heads + a.kv_heads ? a.k_scale[h - a.heads] : a.v_scale[h - a.heads - a.kv_heads]);
+      inv[n] = __frcp_rn(h < a.heads + a.kv_heads
+                             ? *ld_at(a.k_scale + h - a.heads, a.k_scale, (size_t)a.kv_heads, a.err)
+                             : *ld_at(a.v_scale + h - a.heads - a.kv_heads, a.v_scale, (size_t)a.kv_heads, a.err));
   }
   // two dimensions of each vector at a time, in place (an e4m3 pair takes the
   // word's lower half)
@@ -143,18 +147,23 @@ __global__ void __launch_bounds__(kMostThreads, 2) rope_append_kernel(const Rope
     const bool is_q = h < a.heads, is_v = h >= a.heads + a.kv_heads;
     if (is_q) {
       uint16_t* q = a.q + ((size_t)t * a.heads + h) * D;
+      const size_t all = (size_t)a.T * a.heads * D - 7;
+      if (!in_buf(q + d0, a.q, all, a.err) || !in_buf(q + d1, a.q, all, a.err)) continue;
       *reinterpret_cast<uint4*>(q + d0) = x[n][0];
       *reinterpret_cast<uint4*>(q + d1) = x[n][1];
     } else if (keep) {
       const int hk = is_v ? h - a.heads - a.kv_heads : h - a.heads;
       const size_t at = ((page * a.kv_heads + hk) * page_size + off) * D;
+      const size_t all = (size_t)a.capacity * a.kv_heads * D - 7;
       void* base = is_v ? a.v : a.k;
       if (k8) {
         uint8_t* to = static_cast<uint8_t*>(base) + at;
+        if (!in_buf(to + d0, static_cast<uint8_t*>(base), all, a.err) || !in_buf(to + d1, static_cast<uint8_t*>(base), all, a.err)) continue;
         *reinterpret_cast<uint2*>(to + d0) = make_uint2(x[n][0].x | (x[n][0].y << 16), x[n][0].z | (x[n][0].w << 16));
         *reinterpret_cast<uint2*>(to + d1) = make_uint2(x[n][1].x | (x[n][1].y << 16), x[n][1].z | (x[n][1].w << 16));
       } else {
         uint16_t* to = static_cast<uint16_t*>(base) + at;
+        if (!in_buf(to + d0, static_cast<uint16_t*>(base), all, a.err) || !in_buf(to + d1, static_cast<uint16_t*>(base), all, a.err)) continue;
         *reinterpret_cast<uint4*>(to + d0) = x[n][0];
         *reinterpret_cast<uint4*>(to + d1) = x[n][1];
       }
@@ -168,8 +177,8 @@ __global__ void __launch_bounds__(kThreads) rope_append_any_kernel(const RopeArg
   allow_dependent_launch();
   grid_dependency_wait();
   const int t = blockIdx.x;
-  const long long slot = a.slots[t];
-  int pos = a.positions[t];
+  const long long slot = *ld_at(a.slots + t, a.slots, (size_t)a.T, a.err);
+  int pos = *ld_at(a.positions + t, a.positions, (size_t)a.T, a.err);
   bool keep = slot >= 0;
   if (slot >= a.capacity || pos < 0 || pos >= a.table_len) {
     if (threadIdx.x == 0) atomicOr(a.err, kErrRange);
@@ -185,22 +194,26 @@ __global__ void __launch_bounds__(kThreads) rope_append_any_kernel(const RopeArg
     const bool is_q = h < a.heads, is_v = h >= a.heads + a.kv_heads;
     if (!is_q && !keep) continue;
     const uint16_t* x = a.qkv + (size_t)t * a.ld + (size_t)h * D;
-    float f = value16<kB>(x[d]);
+    auto at16 = [&](int i) { return value16<kB>(*ld_at(x + i, a.qkv, span(a.T, a.ld, heads * D), a.err)); };
+    auto angle = [&](int i) { return *ld_at(turn + i, a.table, (size_t)a.table_len * a.R, a.err); };
+    float f = at16(d);
     if (d < a.R && !is_v) {
       const bool first = kInter ? d % 2 == 0 : d < half;
       const int k = kInter ? d / 2 : (first ? d : d - half);
-      const float g = value16<kB>(x[kInter ? (first ? d + 1 : d - 1) : (first ? d + half : d - half)]);
-      f = first ? f * turn[k] - g * turn[half + k] : f * turn[k] + g * turn[half + k];
+      const float g = at16(kInter ? (first ? d + 1 : d - 1) : (first ? d + half : d - half));
+      f = first ? f * angle(k) - g * angle(half + k) : f * angle(k) + g * angle(half + k);
     }
     if (is_q) {
-      a.q[((size_t)t * a.heads + h) * D + d] = bits16<kB>(f);
+      uint16_t* q = a.q + ((size_t)t * a.heads + h) * D + d;
+      if (in_buf(q, a.q, (size_t)a.T * a.heads * D, a.err)) *q = bits16<kB>(f);
       continue;
     }
     const int hk = is_v ? h - a.heads - a.kv_heads : h - a.heads;
     const size_t at = ((page * a.kv_heads + hk) * page_size + off) * D + d;
     void* base = is_v ? a.v : a.k;
+    if (!in_buf(static_cast<uint8_t*>(base) + at, static_cast<uint8_t*>(base), (size_t)a.capacity * a.kv_heads * D, a.err)) continue;
     if (k8)
-      static_cast<uint8_t*>(base)[at] = (uint8_t)e4m3x2(f * __frcp_rn((is_v ? a.v_scale : a.k_scale)[hk]), 0.f);
+      static_cast<uint8_t*>(base)[at] = (uint8_t)e4m3x2(f * __frcp_rn(*ld_at((is_v ? a.v_scale : a.k_scale) + hk, is_v ? a.v_scale : a.k_scale, (size_t)a.kv_heads, a.err)), 0.f);
     else
       static_cast<uint16_t*>(base)[at] = bits16<kB>(f);
   }

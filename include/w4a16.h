@@ -449,8 +449,13 @@ int w4a16_attn_prompt(const uint16_t* q, int64_t q_stride, const void* k_cache, 
 /* Synchronizes `stream`, then reads and clears the library's device error
  * word (set by a kernel that gave up a bounded wait or failed a self-check;
  * in the bounds-checked build of the library, compiled with -DW4A16_CHECKED,
- * also by any global or shared-memory access outside its buffer, which the
- * kernel then skips: bit 64).
+ * also by an access outside its buffer, which the kernel then skips: bit 64).
+ * Bits: 1, 2, 4, 8 a bounded wait of the producer, MMA, dequantization or
+ * epilogue role gave up; 16 a drain did; 32 the decode fix-up's wait did; 128
+ * a slot, position, page number or length outside its range; 256 an attention
+ * workspace whose flag area was not zero. After a wait that gave up, the
+ * results of that call are incomplete and workspaces' flag areas have to be
+ * zeroed.
  * Returns W4A16_OK or W4A16_ERR_DEVICE_CHECK (message: which check, where). */
 int w4a16_device_status(void* stream);
 
