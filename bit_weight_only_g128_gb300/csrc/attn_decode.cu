@@ -21,9 +21,11 @@
 // B per clock and SM they need a twentieth of its rate; a tcgen05 tile of 128
 // rows would be filled with at most 16.
 //
-// Measured: 64 x 8190 tokens, 64 heads over 8, fp16: 306 us, 7020 GB/s; 16 x up
-// to 4096, 32 heads, bf16: 84 us, 6450 GB/s; 3 x 100003, 64 heads over 8, e4m3:
-// 94.6 us, 6490 GB/s; 1 x 777: 8.0 us.
+// Measured, back to back: 64 x 8190 tokens, 64 heads over 8, fp16: 306 to 312
+// us, 6870 to 7030 GB/s; 16 x up to 4096, 32 heads, bf16: 85 us, 6380 GB/s; 3 x
+// 100003, 64 heads over 8, e4m3: 95 us, 6440 GB/s; 1 x 777: 8.2 us on the
+// device, 8.8 a call. More than 16 heads per key/value head read the cache once
+// per 16 of them: 16 x 8192, 64 heads over 1: 41 us for 67 MB.
 //
 // Work: all (sequence, head, step of four tiles) triples in one line, cut into
 // equal runs, one per block, from the lengths on the device. A run may begin
@@ -350,7 +352,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks<kHeads>) attn_decode_kernel(
 
     // For the e4m3 cache the queries are taken in fp16, with the dimensions of
     // a k-step in the order its codes come in (4t, 4t + 1 | 4t + 2, 4t + 3),
-    // each head divided by a power of two. mult: of this lane's accumulator
+    // each head divided by a power of two (dimensions below 2^-15 of the
+    // head's largest lose bits to it). mult: of this lane's accumulator
     // columns, heads 2t and 2t + 1.
     float mult[kNb][2];
 #pragma unroll
@@ -476,8 +479,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks<kHeads>) attn_decode_kernel(
           }
         }
         // probabilities, rounded to 16 bits for the product (relative 2^-11
-        // or 2^-8 of each term), as B fragments: 16 tokens x 8 heads. (A
-        // maximum of -inf, where infinite keys leave no score, subtracts 0.)
+        // or 2^-8 of each term; fp16 has fewer bits for terms below 2^-14 of
+        // the warp's maximum and none below 2^-25, while the sum takes them
+        // whole), as B fragments: 16 tokens x 8 heads. (A maximum of -inf,
+        // where infinite keys leave no score, subtracts 0.)
         float base[kNb][2];
 #pragma unroll
         for (int nb = 0; nb < kNb; ++nb)

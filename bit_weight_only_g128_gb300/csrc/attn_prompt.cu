@@ -29,10 +29,11 @@
 //   warps 14, 15     tcgen05.mma of tile 0, 1: S from shared memory, O += P V
 //                    with P read from tensor memory, where it takes the place
 //                    of S
-// Measured: 8192 rows of 64 heads over 8, fp16: 722 us back to back (1523
-// TFLOP/s, at the power limit), 624 us with idle gaps (1763 TFLOP/s); 140 to 700
-// rows behind 300 to 1500, 40 heads, bf16: 58 us; 37 rows of 32 heads: 8.0 us.
-// 8192 rows over e4m3 codes: fp16 queries 800 us, bf16 880. Head dim 64: 530 us
+// Measured, back to back: 8192 rows of 64 heads over 8, fp16: 709 to 720 us
+// (1530 to 1550 TFLOP/s, at the power limit; 624 with idle gaps); 140 to 700 rows
+// behind 300 to 1500, 40 heads, bf16: 57 us; 37 rows of 32 heads: 8.2 us on the
+// device, 9.2 a call. 8192 rows over e4m3 codes: fp16 queries 807 us, bf16 877.
+// Head dim 64: 538 us
 // (no pipe full: issue 49%, tensor 44%, exponentials 44%; a softmax warp's own
 // 570 instructions per tile are the chain that binds).
 // Where the units are fewer than the blocks, each is split over its keys into
@@ -444,7 +445,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const PromptAr
         }
         const float shift = m == -INFINITY ? 0.f : -m;
         // P in two parts, of 96 and 32 keys: the product with the first runs
-        // while the second is formed; the sums wait until both are on their way
+        // while the second is formed; the sums wait until both are on their
+        // way. P is rounded to 16 bits (relative 2^-11, or 2^-8 with bf16
+        // values; fp16 has fewer bits for terms below 2^-14 of m and none below
+        // 2^-25, which the sums take whole: with one key 2^26 above 8192 others
+        // the result is 2^-13 low).
         const uint64_t mult2 = pack2(mult, mult), shift2 = pack2(shift, shift);
 #pragma unroll
         for (int part = 0; part < 2; ++part) {

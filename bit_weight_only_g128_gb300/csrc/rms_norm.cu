@@ -12,9 +12,9 @@
 // Bound: HBM bytes, 2 K (x) + 2 K (residual) + 2 K (h) + 2 K or K (y) per
 // row; for few rows the chain load - block sum - store (latency). One pass: a
 // row's h stays in its threads' registers (at most 4 vectors of 8 channels
-// each) from the load to the store. Measured: 4096 x 8192 bf16 with residual
-// 41.7 us, 6430 GB/s (96% of the copy rate); 1 x 4096 1.7 us; 333 x 5120 to
-// codes 4.3 us.
+// each) from the load to the store. Measured, back to back: 4096 x 8192 bf16 with
+// residual 41.6 us, 6450 GB/s (96% of the copy rate); 1 x 4096 1.7 us on the
+// device, 4.3 a call; 333 x 5120 to codes 4.2 us on the device, 6 a call.
 #include "common.cuh"
 #include "kernels.h"
 #include "layer.cuh"

@@ -420,7 +420,10 @@ int w4a16_attn_workspace_size(int tokens, int batch, int heads, int kv_heads, in
  * the logarithm of the softmax's sum. table [batch] rows (stride in
  * elements) of max_pages page numbers (null where that is 0), of which the
  * first ceil(lens[b] / page_size) are read. A length of 0 gives zeros and -inf.
- * What the cache holds beyond a sequence's length is never used. A length
+ * What the cache holds beyond a sequence's length is never used. Within it
+ * NaN and infinities go where the formula takes them: a score of NaN or +inf
+ * makes the row NaN (lse too), a key that scores -inf has no weight, a
+ * non-finite value reaches the rows that see it. A length
  * below 0 or beyond the table's row is clamped and a page number outside the
  * cache reads page 0, both recorded (bit 128). */
 int w4a16_attn_decode(const uint16_t* q, int64_t q_stride, const void* k_cache, const void* v_cache,
@@ -438,7 +441,8 @@ int w4a16_attn_decode(const uint16_t* q, int64_t q_stride, const void* k_cache, 
  * -inf. starts [batch + 1] must not decrease nor leave
  * [0, tokens] (clamped and recorded, bit 128); rows outside
  * [starts[0], starts[batch]) of out and lse are left as they are. The rest as
- * w4a16_attn_decode. */
+ * w4a16_attn_decode; a non-finite value (of V) may also make rows of up
+ * to 254 tokens before its own NaN (their weight of 0 multiplies it). */
 int w4a16_attn_prompt(const uint16_t* q, int64_t q_stride, const void* k_cache, const void* v_cache,
                       const float* k_scale, const float* v_scale, int pages, int page_size,
                       const int32_t* table, int64_t table_stride, int max_pages,
