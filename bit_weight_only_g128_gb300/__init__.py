@@ -38,6 +38,11 @@ BF16 = 0x400            # W4A16_BF16
 ACT_A8 = 0x800          # W4A16_ACT_A8
 CACHE_E4M3 = 0x1000        # W4A16_CACHE_E4M3
 ROPE_INTERLEAVED = 0x2000  # W4A16_ROPE_INTERLEAVED
+ROUTE_FP32 = 0x4000           # W4A16_ROUTE_FP32
+ROUTE_SIGMOID = 0x8000        # W4A16_ROUTE_SIGMOID
+ROUTE_RENORMALIZE = 0x10000   # W4A16_ROUTE_RENORMALIZE
+EXPERTS_PER_CHOICE = 0x20000  # W4A16_EXPERTS_PER_CHOICE
+EXPERTS_COMBINE = 0x40000     # W4A16_EXPERTS_COMBINE
 
 FLAG_BYTES = 32768  # a workspace's flag area: zero before and after every call
 
@@ -75,6 +80,13 @@ SIGNATURES = {
     "w4a16_rms_norm": (_I, [_P, _L, _P, _L, _P, _I, _I, _F, _I, _P, _P, _P, _P, _P, _L, _P]),
     "w4a16_rope_append": (_I, [_P, _L, _P, _I, _I, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _I,
                                _I, _I, _P]),
+    "w4a16_rope_append_norm": (_I, [_P, _L, _P, _I, _I, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _I,
+                                    _I, _P, _P, _F, _I, _P]),
+    "w4a16_route_workspace_size": (_I, [_I, _I, _I, _PSZ]),
+    "w4a16_route": (_I, [_P, _L, _I, _I, _I, _P, _P, _P, _P, _P, _SZ, _I, _P]),
+    "w4a16_experts_workspace_size": (_I, [_I, _I, _I, _I, _I, _I, _I, _PSZ]),
+    "w4a16_gemm_experts": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _SZ,
+                                _I, _P]),
     "w4a16_attn_workspace_size": (_I, [_I, _I, _I, _I, _I, _PSZ]),
     "w4a16_attn_decode": (_I, [_P, _L, _P, _P, _P, _P, _I, _I, _P, _L, _I, _P, _I, _I, _I, _I, _F,
                                _P, _P, _P, _SZ, _I, _P]),
@@ -375,8 +387,9 @@ def gemm_noalloc(A: torch.Tensor, pw: PackedWeight, out: Optional[torch.Tensor] 
     return out
 
 
-from .layer import (KVCache, attn_decode, attn_prompt, attn_workspace_size,  # noqa: E402,F401
-                    gemm_scaled, new_kv_cache, rms_norm, rope_append)
+from .layer import (KVCache, PackedExperts, Routing, attn_decode, attn_prompt,  # noqa: E402,F401
+                    attn_workspace_size, experts_workspace_size, gemm_experts, gemm_scaled, new_kv_cache,
+                    rms_norm, rope_append, route, stack_experts)
 
 
 def selftest_wait(which: int, stream=None) -> None:

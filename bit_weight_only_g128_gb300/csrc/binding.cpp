@@ -1,5 +1,5 @@
 // The binding's calls of the decoder layer's operators (norm, rotation and
-// append, attention), as a CPython module: argument checks, allocation of the
+// append, attention, router, products of experts), as a CPython module: argument checks, allocation of the
 // results and the call of the C ABI in one native step, for calls whose
 // kernels take a few microseconds. The entry points come from the library that
 // the package has loaded (bind), the results' memory and the current stream
@@ -24,14 +24,20 @@ namespace {
 
 struct Library {
   decltype(&w4a16_rms_norm) rms_norm;
-  decltype(&w4a16_rope_append) rope_append;
+  decltype(&w4a16_rope_append_norm) rope_append_norm;
   decltype(&w4a16_attn_workspace_size) attn_workspace_size;
   decltype(&w4a16_attn_decode) attn_decode;
   decltype(&w4a16_attn_prompt) attn_prompt;
+  decltype(&w4a16_route_workspace_size) route_workspace_size;
+  decltype(&w4a16_route) route;
+  decltype(&w4a16_experts_workspace_size) experts_workspace_size;
+  decltype(&w4a16_gemm_experts) gemm_experts;
 } lib;
 PyObject* on_error = nullptr;   // (code, entry point): raises the package's error
 PyObject* workspace_of = nullptr;  // (bytes, device, stream): the stream's workspace
 PyObject *name_k, *name_v, *name_k_scale, *name_v_scale, *name_cuda_stream;
+PyObject *name_Wq, *name_Sp, *name_Zp, *name_experts, *name_K, *name_N, *name_group;
+PyObject *name_weights, *name_rows, *name_offsets;
 
 // A Python exception that is set (or is set by the text).
 struct Raised {};
@@ -99,6 +105,21 @@ T* flat(const at::Tensor& t, const char* name, int64_t n, at::ScalarType type, c
     refuse("%s must be contiguous with %lld elements, got shape %s", name, (long long)n, text(t.sizes()).c_str());
   return static_cast<T*>(t.data_ptr());
 }
+
+// An attribute of a Python object, held while it is looked at.
+struct Held {
+  PyObject* o;
+  Held(PyObject* from, PyObject* name) : o(PyObject_GetAttr(from, name)) {
+    if (!o) throw Raised();
+  }
+  Held(const Held&) = delete;
+  ~Held() { Py_XDECREF(o); }
+  int64_t integer() const {
+    const long long v = PyLong_AsLongLong(o);
+    if (v == -1 && PyErr_Occurred()) throw Raised();
+    return v;
+  }
+};
 
 // A new contiguous tensor on a CUDA device (without the dispatcher's round).
 at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const at::Device& dev) {
@@ -289,20 +310,30 @@ struct Cache {
     k = kt.data_ptr();
     v = vt.data_ptr();
   }
-
- private:
-  struct Held {
-    PyObject* o;
-    Held(PyObject* from, PyObject* name) : o(PyObject_GetAttr(from, name)) {
-      if (!o) throw Raised();
-    }
-    ~Held() { Py_XDECREF(o); }
-  };
 };
 
-// rope_append(qkv, cos_sin, positions, slots, cache, interleaved, out, stream)
+// The workspace of a call that needs `need` bytes: the given one, checked, or
+// the stream's.
+at::Tensor workspace(PyObject* given, size_t need, const at::Device& dev, const CallStream& stream) {
+  at::Tensor ws;
+  if (given != Py_None) {
+    ws = tensor(given, "workspace");
+    if (!ws.is_cuda() || ws.device() != dev || !ws.is_contiguous())
+      refuse("workspace must be a contiguous CUDA tensor on %s", text(dev).c_str());
+  } else if (need) {
+    PyObject* o = PyObject_CallFunction(workspace_of, "niK", (Py_ssize_t)need, (int)dev.index(),
+                                        (unsigned long long)(uintptr_t)stream.ptr);
+    if (!o) throw Raised();
+    ws = THPVariable_Unpack(o);
+    Py_DECREF(o);
+  }
+  return ws;
+}
+
+// rope_append(qkv, cos_sin, positions, slots, cache, interleaved, out, stream,
+// q_norm, k_norm, eps)
 PyObject* rope_append(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
-  return guarded(nargs, 8, [&]() -> PyObject* {
+  return guarded(nargs, 11, [&]() -> PyObject* {
     const at::Tensor& qkv = tensor(args[0], "qkv");
     const int flags = flags16(qkv, "qkv");
     const at::Device dev = qkv.device();
@@ -320,12 +351,17 @@ PyObject* rope_append(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     const auto* slots = flat<int64_t>(tensor(args[3], "slots"), "slots", T, at::kLong, dev);
     const int interleaved = PyObject_IsTrue(args[5]);
     if (interleaved < 0) throw Raised();
+    const uint16_t *q_norm = nullptr, *k_norm = nullptr;
+    if (args[8] != Py_None) q_norm = flat<uint16_t>(tensor(args[8], "q_norm"), "q_norm", c.dim, type, dev);
+    if (args[9] != Py_None) k_norm = flat<uint16_t>(tensor(args[9], "k_norm"), "k_norm", c.dim, type, dev);
+    const double eps = PyFloat_AsDouble(args[10]);
+    if (eps == -1.0 && PyErr_Occurred()) throw Raised();
     const CallStream stream(args[7], dev);
     const at::Tensor q = result(args[6], "out", {T, heads, c.dim}, type, dev);
-    check(lib.rope_append(static_cast<uint16_t*>(qkv.data_ptr()), ld, table, int32_of(cs.size(0), "table_len"),
+    check(lib.rope_append_norm(static_cast<uint16_t*>(qkv.data_ptr()), ld, table, int32_of(cs.size(0), "table_len"),
                           int32_of(cs.size(1), "rotary"), pos, slots, int32_of(T, "tokens"), heads, c.heads, c.dim,
                           static_cast<uint16_t*>(q.data_ptr()), c.k, c.v, c.k_scale, c.v_scale, c.pages, c.page_size,
-                          flags | c.flags | (interleaved ? W4A16_ROPE_INTERLEAVED : 0), stream.ptr),
+                          q_norm, k_norm, (float)eps, flags | c.flags | (interleaved ? W4A16_ROPE_INTERLEAVED : 0), stream.ptr),
           "w4a16_rope_append");
     return wrap(q, args[6]);
   });
@@ -370,18 +406,7 @@ PyObject* attend(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
               m32 = int32_of(most, "max_pages");
     size_t need = 0;
     if (T > 0) check(lib.attn_workspace_size(t32, b32, h32, c.heads, c.dim, &need), "w4a16_attn_workspace_size");
-    at::Tensor ws;
-    if (args[8] != Py_None) {
-      ws = tensor(args[8], "workspace");
-      if (!ws.is_cuda() || ws.device() != dev || !ws.is_contiguous())
-        refuse("workspace must be a contiguous CUDA tensor on %s", text(dev).c_str());
-    } else if (need) {
-      PyObject* o = PyObject_CallFunction(workspace_of, "niK", (Py_ssize_t)need, (int)dev.index(),
-                                          (unsigned long long)(uintptr_t)stream.ptr);
-      if (!o) throw Raised();
-      ws = THPVariable_Unpack(o);
-      Py_DECREF(o);
-    }
+    const at::Tensor ws = workspace(args[8], need, dev, stream);
     void* wp = ws.defined() ? ws.data_ptr() : nullptr;
     const size_t wb = ws.defined() ? ws.nbytes() : 0;
     auto* qp = static_cast<uint16_t*>(q.data_ptr());
@@ -400,14 +425,115 @@ PyObject* attend(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   });
 }
 
-// bind(addresses of the five entry points, error function, workspace function)
+// route(logits, top_k, scoring, renormalize, workspace, stream) -> (experts,
+// weights, rows, offsets)
+PyObject* route(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+  return guarded(nargs, 6, [&]() -> PyObject* {
+    const at::Tensor& x = tensor(args[0], "logits");
+    const at::Device dev = x.device();
+    const at::ScalarType type = x.scalar_type();
+    int flags = 0;
+    if (type == at::kFloat) flags = W4A16_ROUTE_FP32;
+    else if (type == at::kBFloat16) flags = W4A16_BF16;
+    else if (type != at::kHalf) refuse("logits must be float16, bfloat16 or float32, got %s", text(type));
+    if (x.dim() != 2) refuse("logits must be [T, experts], got shape %s", text(x.sizes()).c_str());
+    const int64_t T = x.size(0), E = x.size(1);
+    const int64_t ld = rows_of(x, "logits", E, type, dev);
+    const int64_t top = PyLong_AsLongLong(args[1]);
+    if (top == -1 && PyErr_Occurred()) throw Raised();
+    const char* scoring = PyUnicode_Check(args[2]) ? PyUnicode_AsUTF8(args[2]) : nullptr;
+    if (scoring && std::string(scoring) == "sigmoid") {
+      flags |= W4A16_ROUTE_SIGMOID;
+    } else if (!scoring || std::string(scoring) != "softmax") {
+      PyErr_Format(PyExc_ValueError, "scoring must be 'softmax' or 'sigmoid', got %R", args[2]);
+      throw Raised();
+    }
+    const int renormalize = PyObject_IsTrue(args[3]);
+    if (renormalize < 0) throw Raised();
+    if (renormalize) flags |= W4A16_ROUTE_RENORMALIZE;
+    const int t32 = int32_of(T, "T"), e32 = int32_of(E, "experts"), k32 = int32_of(top, "top_k");
+    const CallStream stream(args[5], dev);
+    size_t need = 0;
+    check(lib.route_workspace_size(t32, e32, k32, &need), "w4a16_route_workspace_size");
+    const at::Tensor ws = workspace(args[4], need, dev, stream);
+    const at::Tensor experts = fresh({T, top}, at::kInt, dev), weights = fresh({T, top}, at::kFloat, dev);
+    const at::Tensor rows = fresh({T * top}, at::kInt, dev), offsets = fresh({E + 1}, at::kInt, dev);
+    check(lib.route(x.data_ptr(), ld, t32, e32, k32, static_cast<int32_t*>(experts.data_ptr()), weights.data_ptr<float>(),
+                    static_cast<int32_t*>(rows.data_ptr()), static_cast<int32_t*>(offsets.data_ptr()),
+                    ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.nbytes() : 0, flags, stream.ptr),
+          "w4a16_route");
+    PyObject* t = PyTuple_New(4);
+    if (!t) throw Raised();
+    const at::Tensor* all[4] = {&experts, &weights, &rows, &offsets};
+    for (int i = 0; i < 4; ++i) {
+      PyObject* o = wrap(*all[i]);
+      if (!o) {
+        Py_DECREF(t);
+        throw Raised();
+      }
+      PyTuple_SET_ITEM(t, i, o);
+    }
+    return t;
+  });
+}
+
+// gemm_experts(A, weights, routing, silu_mul, combine, out, path, workspace, stream)
+PyObject* gemm_experts(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+  return guarded(nargs, 9, [&]() -> PyObject* {
+    const at::Tensor& A = tensor(args[0], "A");
+    int flags = flags16(A, "A");
+    const at::Device dev = A.device();
+    const at::ScalarType type = A.scalar_type();
+    const Held wq(args[1], name_Wq), sp(args[1], name_Sp), zp(args[1], name_Zp);
+    const int64_t E = Held(args[1], name_experts).integer(), K = Held(args[1], name_K).integer(),
+                  N = Held(args[1], name_N).integer(), group = Held(args[1], name_group).integer();
+    const int e32 = int32_of(E, "experts"), k32 = int32_of(K, "K"), n32 = int32_of(N, "N"), g32 = int32_of(group, "group");
+    if (E <= 0 || K <= 0 || N <= 0 || group <= 0 || K % group) refuse("experts, K, N and group must be positive, and group divide K");
+    const Held ex(args[2], name_experts), wt(args[2], name_weights), ro(args[2], name_rows), of(args[2], name_offsets);
+    const at::Tensor& experts = tensor(ex.o, "routing.experts");
+    if (experts.dim() != 2) refuse("routing.experts must be [T, top_k], got shape %s", text(experts.sizes()).c_str());
+    const int64_t T = experts.size(0), top = experts.size(1);
+    const auto* ep = flat<int32_t>(experts, "routing.experts", T * top, at::kInt, dev);
+    const auto* wp = flat<float>(tensor(wt.o, "routing.weights"), "routing.weights", T * top, at::kFloat, dev);
+    const auto* rp = flat<int32_t>(tensor(ro.o, "routing.rows"), "routing.rows", T * top, at::kInt, dev);
+    const auto* op = flat<int32_t>(tensor(of.o, "routing.offsets"), "routing.offsets", E + 1, at::kInt, dev);
+    if (A.dim() == 3 && A.size(0) == T && A.size(1) == top && A.size(2) == K) flags |= W4A16_EXPERTS_PER_CHOICE;
+    else if (A.dim() != 2 || A.size(0) != T || A.size(1) != K)
+      refuse("A must be [%lld, %lld] or [%lld, %lld, %lld], got shape %s", (long long)T, (long long)K, (long long)T, (long long)top,
+             (long long)K, text(A.sizes()).c_str());
+    const auto* ap = flat<uint16_t>(A, "A", A.numel(), type, dev);
+    const auto* qp = flat<uint32_t>(tensor(wq.o, "Wq"), "Wq", E * N * K / 8, at::kInt, dev);
+    const auto* sc = flat<uint16_t>(tensor(sp.o, "Sp"), "Sp", E * N * (K / group), at::kHalf, dev);
+    const auto* zc = flat<uint32_t>(tensor(zp.o, "Zp"), "Zp", E * N * (K / group) / 8, at::kInt, dev);
+    const int silu = PyObject_IsTrue(args[3]), combine = PyObject_IsTrue(args[4]);
+    if (silu < 0 || combine < 0) throw Raised();
+    if (silu) flags |= W4A16_SILU_MUL;
+    if (combine) flags |= W4A16_EXPERTS_COMBINE;
+    const int64_t path = PyLong_AsLongLong(args[6]);
+    if (path == -1 && PyErr_Occurred()) throw Raised();
+    flags |= (int)path;
+    const CallStream stream(args[8], dev);
+    const int t32 = int32_of(T, "T"), top32 = int32_of(top, "top_k");
+    size_t need = 0;
+    check(lib.experts_workspace_size(t32, top32, e32, n32, k32, g32, flags, &need), "w4a16_experts_workspace_size");
+    const int64_t width = silu ? N / 2 : N;
+    const at::Tensor y = combine ? result(args[5], "out", {T, width}, type, dev) : result(args[5], "out", {T, top, width}, type, dev);
+    const at::Tensor ws = workspace(args[7], need, dev, stream);
+    check(lib.gemm_experts(ap, qp, sc, zc, t32, top32, e32, n32, k32, g32, ep, wp, rp, op, static_cast<uint16_t*>(y.data_ptr()),
+                           ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.nbytes() : 0, flags, stream.ptr),
+          "w4a16_gemm_experts");
+    return wrap(y, args[5]);
+  });
+}
+
+// bind(addresses of the nine entry points, error function, workspace function)
 PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
-  if (nargs != 7) {
-    PyErr_SetString(PyExc_TypeError, "7 arguments expected");
+  if (nargs != 11) {
+    PyErr_SetString(PyExc_TypeError, "11 arguments expected");
     return nullptr;
   }
-  void* p[5];
-  for (int i = 0; i < 5; ++i) {
+  void* p[9];
+  for (int i = 0; i < 9; ++i) {
     p[i] = PyLong_AsVoidPtr(args[i]);
     if (!p[i]) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "null entry point");
@@ -415,16 +541,20 @@ PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     }
   }
   lib.rms_norm = reinterpret_cast<decltype(lib.rms_norm)>(p[0]);
-  lib.rope_append = reinterpret_cast<decltype(lib.rope_append)>(p[1]);
+  lib.rope_append_norm = reinterpret_cast<decltype(lib.rope_append_norm)>(p[1]);
   lib.attn_workspace_size = reinterpret_cast<decltype(lib.attn_workspace_size)>(p[2]);
   lib.attn_decode = reinterpret_cast<decltype(lib.attn_decode)>(p[3]);
   lib.attn_prompt = reinterpret_cast<decltype(lib.attn_prompt)>(p[4]);
-  Py_INCREF(args[5]);
-  Py_INCREF(args[6]);
+  lib.route_workspace_size = reinterpret_cast<decltype(lib.route_workspace_size)>(p[5]);
+  lib.route = reinterpret_cast<decltype(lib.route)>(p[6]);
+  lib.experts_workspace_size = reinterpret_cast<decltype(lib.experts_workspace_size)>(p[7]);
+  lib.gemm_experts = reinterpret_cast<decltype(lib.gemm_experts)>(p[8]);
+  Py_INCREF(args[9]);
+  Py_INCREF(args[10]);
   Py_XDECREF(on_error);
   Py_XDECREF(workspace_of);
-  on_error = args[5];
-  workspace_of = args[6];
+  on_error = args[9];
+  workspace_of = args[10];
   Py_RETURN_NONE;
 }
 
@@ -433,6 +563,8 @@ PyMethodDef methods[] = {
     {"rms_norm", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&rms_norm)), METH_FASTCALL, nullptr},
     {"rope_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&rope_append)), METH_FASTCALL, nullptr},
     {"attend", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&attend)), METH_FASTCALL, nullptr},
+    {"route", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&route)), METH_FASTCALL, nullptr},
+    {"gemm_experts", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&gemm_experts)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
@@ -440,11 +572,13 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, n
 }  // namespace
 
 PyMODINIT_FUNC PyInit__binding(void) {
-  name_k = PyUnicode_InternFromString("k");
-  name_v = PyUnicode_InternFromString("v");
-  name_k_scale = PyUnicode_InternFromString("k_scale");
-  name_v_scale = PyUnicode_InternFromString("v_scale");
-  name_cuda_stream = PyUnicode_InternFromString("cuda_stream");
-  if (!name_k || !name_v || !name_k_scale || !name_v_scale || !name_cuda_stream) return nullptr;
+  const struct {
+    PyObject** to;
+    const char* name;
+  } names[] = {{&name_k, "k"},   {&name_v, "v"},   {&name_k_scale, "k_scale"}, {&name_v_scale, "v_scale"}, {&name_cuda_stream, "cuda_stream"},
+               {&name_Wq, "Wq"}, {&name_Sp, "Sp"}, {&name_Zp, "Zp"},           {&name_experts, "experts"}, {&name_K, "K"},
+               {&name_N, "N"},   {&name_group, "group"}, {&name_weights, "weights"}, {&name_rows, "rows"}, {&name_offsets, "offsets"}};
+  for (const auto& n : names)
+    if (!(*n.to = PyUnicode_InternFromString(n.name))) return nullptr;
   return PyModule_Create(&module);
 }

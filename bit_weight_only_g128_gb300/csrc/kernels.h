@@ -130,12 +130,14 @@ cudaError_t launch_rms_norm(const uint16_t* x, long long ldx, const uint16_t* re
                             uint16_t* codes, int8_t* aq, float* s_a, uint16_t* h, long long ldh,
                             cudaStream_t stream);
 // Rotation of the query and key heads of T qkv rows, q written out and keys
-// and values stored at their slots of the paged cache.
+// and values stored at their slots of the paged cache; q_norm and k_norm, or
+// null: the weights of a norm of every query (key) head before it.
 cudaError_t launch_rope_append(const uint16_t* qkv, long long ld, const float* table, int table_len, int R,
                                const int32_t* positions, const int64_t* slots, int T, int heads, int kv_heads,
                                int head_dim, uint16_t* q, void* k, void* v, const float* k_scale,
-                               const float* v_scale, int pages, int page_shift, bool bf16, bool e4m3,
-                               bool interleaved, cudaStream_t stream);
+                               const float* v_scale, int pages, int page_shift, const uint16_t* q_norm,
+                               const uint16_t* k_norm, float eps, bool bf16, bool e4m3, bool interleaved,
+                               cudaStream_t stream);
 // Attention over the paged cache (AttnArgs: layer.cuh).
 struct AttnArgs;
 // Causal attention of prompts on the tensor cores. The workspace's flag area
@@ -149,6 +151,19 @@ cudaError_t launch_attn_prompt(const AttnArgs& args, int head_dim, bool bf16, bo
 size_t attn_decode_workspace_bytes(int head_dim, int sms);
 cudaError_t launch_attn_decode(const AttnArgs& args, int head_dim, bool bf16, bool e4m3, void* workspace, int sms,
                                cudaStream_t stream);
+
+// The router: experts [T][k] and weights of the k largest of each token's E
+// logits (type 0 fp16, 1 bf16, 2 fp32), the choices by expert in rows [T * k],
+// offsets [E + 1]. The workspace holds the blocks' counts.
+size_t route_workspace_bytes(int T, int E);
+cudaError_t launch_route(const void* logits, long long ld, int type, int T, int E, int k, bool sigmoid,
+                         bool renormalize, int32_t* experts, float* weights, int32_t* rows, int32_t* offsets,
+                         void* workspace, cudaStream_t stream);
+// Products grouped by expert (ExpertArgs: experts.cuh), for few rows per
+// expert. Combined, the workspace holds the choices' products.
+struct ExpertArgs;
+size_t experts_decode_workspace_bytes(int choices, int N, bool combine);
+cudaError_t launch_experts_decode(ExpertArgs args, bool bf16, void* workspace, cudaStream_t stream);
 
 // Reads the device error word (bounded waits that gave up, self-checks) and
 // clears it if set.

@@ -83,6 +83,9 @@ constexpr int kErrRange = 128;
 // Error bit of a workspace whose flag area was not as every call leaves it.
 constexpr int kErrWorkspace = 256;
 
+// The flag area that every workspace starts with; scratch lies behind it.
+constexpr size_t kWorkspaceFlags = 32768;
+
 // The paged key-value cache: k and v are [pages][kv heads][page_size][head
 // dim] of 16-bit values or of e4m3 codes that a per-head scale multiplies.
 struct PagedCache {

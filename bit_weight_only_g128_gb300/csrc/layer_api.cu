@@ -5,6 +5,7 @@
 #include <cstdio>
 
 #include "common.cuh"
+#include "experts.cuh"
 #include "kernels.h"
 #include "layer.cuh"
 
@@ -97,9 +98,38 @@ int check_attn(AttnArgs* a, const uint16_t* q, int64_t q_stride, const void* k, 
 
 int check_workspace(const void* workspace, size_t bytes, size_t need) {
   if (need > 0 && (!workspace || bytes < need))
-    return fail(W4A16_ERR_WORKSPACE_TOO_SMALL, "attention needs a workspace of %zu bytes (got %zu)", need,
+    return fail(W4A16_ERR_WORKSPACE_TOO_SMALL, "the call needs a workspace of %zu bytes (got %zu)", need,
                 workspace ? bytes : (size_t)0);
   if (need > 0 && !aligned(workspace, 256)) return fail(W4A16_ERR_MISALIGNED, "workspace needs 256-byte alignment");
+  return W4A16_OK;
+}
+
+constexpr int kMaxExperts = 512, kMaxTop = 32;
+
+int check_routing(int T, int E, int top_k) {
+  if (T < 0 || E <= 0 || top_k <= 0)
+    return fail(W4A16_ERR_INVALID_ARG, "T=%d is negative, or E=%d or top_k=%d not positive", T, E, top_k);
+  if (T > kMaxRows || E > kMaxExperts || top_k > kMaxTop || top_k > E)
+    return fail(W4A16_ERR_UNSUPPORTED_SHAPE, "T=%d above %d, E=%d above %d, or top_k=%d above %d or E", T, kMaxRows, E,
+                kMaxExperts, top_k, kMaxTop);
+  return W4A16_OK;
+}
+
+// The path, the shape rules and the flags of the products grouped by expert.
+int check_experts(int T, int top_k, int E, int N, int K, int group, int flags) {
+  if (int rc = check_routing(T, E, top_k)) return rc;
+  constexpr int known = W4A16_BF16 | W4A16_SILU_MUL | W4A16_EXPERTS_PER_CHOICE | W4A16_EXPERTS_COMBINE;
+  const int path = flags & 0xff;
+  if ((flags & ~(known | 0xff)) || (path != W4A16_PATH_AUTO && path != W4A16_PATH_DECODE))
+    return fail(W4A16_ERR_INVALID_ARG, "flags=0x%x: unknown bits or path", flags);
+  if ((flags & W4A16_SILU_MUL) && (flags & W4A16_EXPERTS_COMBINE))
+    return fail(W4A16_ERR_INVALID_ARG, "W4A16_SILU_MUL does not go with W4A16_EXPERTS_COMBINE");
+  if (N <= 0 || K <= 0 || group <= 0) return fail(W4A16_ERR_INVALID_ARG, "N=%d, K=%d, group=%d must be positive", N, K, group);
+  if (N > kMaxRows || K > kMaxRows || N % 16 || K % 64 || group % 64 || K % group)
+    return fail(W4A16_ERR_UNSUPPORTED_SHAPE, "N=%d, K=%d, group=%d: N %% 16, K %% 64, group %% 64 and K %% group must be 0", N, K, group);
+  if ((flags & W4A16_SILU_MUL) && N % 32)
+    return fail(W4A16_ERR_UNSUPPORTED_SHAPE, "N=%d: gate and up need a multiple of 32", N);
+  if ((long long)E * N > 0x7fffffffll) return fail(W4A16_ERR_UNSUPPORTED_SHAPE, "E=%d experts of N=%d columns: above 2^31", E, N);
   return W4A16_OK;
 }
 
@@ -130,10 +160,11 @@ int w4a16_rms_norm(const uint16_t* x, int64_t x_stride, const uint16_t* residual
                 "norm launch");
 }
 
-int w4a16_rope_append(const uint16_t* qkv, int64_t qkv_stride, const float* cos_sin, int table_len, int rotary,
-                      const int32_t* positions, const int64_t* slots, int tokens, int heads, int kv_heads,
-                      int head_dim, uint16_t* q, void* k_cache, void* v_cache, const float* k_scale,
-                      const float* v_scale, int pages, int page_size, int flags, void* stream) {
+int w4a16_rope_append_norm(const uint16_t* qkv, int64_t qkv_stride, const float* cos_sin, int table_len, int rotary,
+                           const int32_t* positions, const int64_t* slots, int tokens, int heads, int kv_heads,
+                           int head_dim, uint16_t* q, void* k_cache, void* v_cache, const float* k_scale,
+                           const float* v_scale, int pages, int page_size, const uint16_t* q_norm,
+                           const uint16_t* k_norm, float eps, int flags, void* stream) {
   if (tokens < 0) return fail(W4A16_ERR_INVALID_ARG, "tokens=%d is negative", tokens);
   if (flags & ~(W4A16_BF16 | W4A16_CACHE_E4M3 | W4A16_ROPE_INTERLEAVED))
     return fail(W4A16_ERR_INVALID_ARG, "flags=0x%x: unknown bits", flags);
@@ -146,15 +177,26 @@ int w4a16_rope_append(const uint16_t* qkv, int64_t qkv_stride, const float* cos_
   if (table_len <= 0) return fail(W4A16_ERR_INVALID_ARG, "table_len=%d must be positive", table_len);
   if (qkv_stride < (int64_t)(heads + 2 * kv_heads) * head_dim)
     return fail(W4A16_ERR_INVALID_ARG, "qkv's row stride is below (heads + 2 kv_heads) * head_dim");
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(W4A16_ERR_INVALID_ARG, "eps=%g is negative or not finite", (double)eps);
   if (tokens == 0) return report_ok();
   if (!qkv || !cos_sin || !positions || !slots || !q) return fail(W4A16_ERR_INVALID_ARG, "null pointer");
-  if (!aligned(qkv, 2) || !aligned(q, 2) || !aligned(cos_sin, 4) || !aligned(positions, 4) || !aligned(slots, 8))
-    return fail(W4A16_ERR_MISALIGNED, "alignment: qkv, q need 2 bytes, cos_sin, positions 4, slots 8");
+  if (!aligned(qkv, 2) || !aligned(q, 2) || !aligned(cos_sin, 4) || !aligned(positions, 4) || !aligned(slots, 8) ||
+      !aligned(q_norm, 2) || !aligned(k_norm, 2))
+    return fail(W4A16_ERR_MISALIGNED, "alignment: qkv, q and the norms need 2 bytes, cos_sin, positions 4, slots 8");
   return finish(launch_rope_append(qkv, qkv_stride, cos_sin, table_len, rotary, positions, slots, tokens, heads,
-                                   kv_heads, head_dim, q, k_cache, v_cache, k_scale, v_scale, pages, shift,
-                                   (flags & W4A16_BF16) != 0, (flags & W4A16_CACHE_E4M3) != 0,
+                                   kv_heads, head_dim, q, k_cache, v_cache, k_scale, v_scale, pages, shift, q_norm, k_norm,
+                                   eps, (flags & W4A16_BF16) != 0, (flags & W4A16_CACHE_E4M3) != 0,
                                    (flags & W4A16_ROPE_INTERLEAVED) != 0, (cudaStream_t)stream),
                 "rotation and append launch");
+}
+
+int w4a16_rope_append(const uint16_t* qkv, int64_t qkv_stride, const float* cos_sin, int table_len, int rotary,
+                      const int32_t* positions, const int64_t* slots, int tokens, int heads, int kv_heads,
+                      int head_dim, uint16_t* q, void* k_cache, void* v_cache, const float* k_scale,
+                      const float* v_scale, int pages, int page_size, int flags, void* stream) {
+  return w4a16_rope_append_norm(qkv, qkv_stride, cos_sin, table_len, rotary, positions, slots, tokens, heads, kv_heads,
+                                head_dim, q, k_cache, v_cache, k_scale, v_scale, pages, page_size, nullptr, nullptr, 0.f,
+                                flags, stream);
 }
 
 int w4a16_attn_workspace_size(int tokens, int batch, int heads, int kv_heads, int head_dim, size_t* bytes) {
@@ -205,6 +247,58 @@ int w4a16_attn_prompt(const uint16_t* q, int64_t q_stride, const void* k_cache, 
   return finish(launch_attn_prompt(a, head_dim, (flags & W4A16_BF16) != 0, (flags & W4A16_CACHE_E4M3) != 0, workspace,
                                    sms, (cudaStream_t)stream),
                 "prompt attention launch");
+}
+
+int w4a16_route_workspace_size(int T, int E, int top_k, size_t* bytes) {
+  if (int rc = check_routing(T, E, top_k)) return rc;
+  if (!bytes) return fail(W4A16_ERR_INVALID_ARG, "null output pointer");
+  *bytes = route_workspace_bytes(T, E);
+  return report_ok();
+}
+
+int w4a16_route(const void* logits, int64_t logits_stride, int T, int E, int top_k, int32_t* experts, float* weights,
+                int32_t* rows, int32_t* offsets, void* workspace, size_t workspace_bytes, int flags, void* stream) {
+  if (int rc = check_routing(T, E, top_k)) return rc;
+  constexpr int known = W4A16_BF16 | W4A16_ROUTE_FP32 | W4A16_ROUTE_SIGMOID | W4A16_ROUTE_RENORMALIZE;
+  if ((flags & ~known) || ((flags & W4A16_BF16) && (flags & W4A16_ROUTE_FP32)))
+    return fail(W4A16_ERR_INVALID_ARG, "flags=0x%x: unknown bits, or two types", flags);
+  if (logits_stride < E) return fail(W4A16_ERR_INVALID_ARG, "the logits' row stride is below E=%d", E);
+  if (!offsets || (T > 0 && (!logits || !experts || !weights || !rows))) return fail(W4A16_ERR_INVALID_ARG, "null pointer");
+  const int type = (flags & W4A16_ROUTE_FP32) ? 2 : (flags & W4A16_BF16) ? 1 : 0;
+  if (!aligned(logits, type == 2 ? 4 : 2) || !aligned(experts, 4) || !aligned(weights, 4) || !aligned(rows, 4) || !aligned(offsets, 4))
+    return fail(W4A16_ERR_MISALIGNED, "alignment: logits need their type's, the results 4 bytes");
+  if (int rc = check_workspace(workspace, workspace_bytes, route_workspace_bytes(T, E))) return rc;
+  return finish(launch_route(logits, logits_stride, type, T, E, top_k, (flags & W4A16_ROUTE_SIGMOID) != 0,
+                             (flags & W4A16_ROUTE_RENORMALIZE) != 0, experts, weights, rows, offsets, workspace,
+                             (cudaStream_t)stream),
+                "router launch");
+}
+
+int w4a16_experts_workspace_size(int T, int top_k, int E, int N, int K, int group, int flags, size_t* bytes) {
+  if (int rc = check_experts(T, top_k, E, N, K, group, flags)) return rc;
+  if (!bytes) return fail(W4A16_ERR_INVALID_ARG, "null output pointer");
+  *bytes = T == 0 ? 0 : experts_decode_workspace_bytes(T * top_k, N, (flags & W4A16_EXPERTS_COMBINE) != 0);
+  return report_ok();
+}
+
+int w4a16_gemm_experts(const uint16_t* A, const uint32_t* Wq, const uint16_t* scales, const uint32_t* zeros, int T,
+                       int top_k, int E, int N, int K, int group, const int32_t* experts, const float* weights,
+                       const int32_t* rows, const int32_t* offsets, uint16_t* Y, void* workspace,
+                       size_t workspace_bytes, int flags, void* stream) {
+  if (int rc = check_experts(T, top_k, E, N, K, group, flags)) return rc;
+  if (T == 0) return report_ok();
+  const bool combine = (flags & W4A16_EXPERTS_COMBINE) != 0;
+  if (!A || !Wq || !scales || !zeros || !experts || !rows || !offsets || !Y || (combine && !weights))
+    return fail(W4A16_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(A, 16) || !aligned(Wq, 16) || !aligned(scales, 16) || !aligned(Y, 16) || !aligned(zeros, 8) ||
+      !aligned(experts, 4) || !aligned(weights, 4) || !aligned(rows, 4) || !aligned(offsets, 4))
+    return fail(W4A16_ERR_MISALIGNED, "alignment: A, Wq, scales and Y need 16 bytes, zeros 8, the routing 4");
+  const size_t need = experts_decode_workspace_bytes(T * top_k, N, combine);
+  if (int rc = check_workspace(workspace, workspace_bytes, need)) return rc;
+  const ExpertArgs a = {A, Wq, scales, zeros, experts, weights, rows, offsets, Y, T, top_k, E, N, K, group,
+                        (flags & W4A16_EXPERTS_PER_CHOICE) != 0, (flags & W4A16_SILU_MUL) != 0, combine, nullptr};
+  return finish(launch_experts_decode(a, (flags & W4A16_BF16) != 0, need ? workspace : nullptr, (cudaStream_t)stream),
+                "experts' product launch");
 }
 
 }  // extern "C"

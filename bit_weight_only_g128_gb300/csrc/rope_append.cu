@@ -9,6 +9,11 @@
 // fp32; each result is rounded once, to 16 bits, or to the cache's e4m3 codes
 // of x times the fp32 reciprocal of scale[head].
 //
+// With norms of queries and keys, x * (mean x^2 + eps)^(-1/2) * weight[dim] of
+// each query (key) head comes before the rotation: the lanes that hold a head
+// add their squares and exchange the sums, so that it costs no pass of its
+// own; all in fp32, without a rounding in between.
+//
 // Bound: HBM bytes (the qkv rows in, q and the cache rows out); for a few
 // tokens the chain slot/position - table row - store (latency). Each thread
 // takes both halves of a rotated pair as two 16-byte vectors, for two heads.
@@ -35,8 +40,16 @@ struct RopeArgs {
   long long ld;  // row stride of qkv
   long long capacity;  // pages * page_size
   int table_len, R, T, heads, kv_heads, page_shift;
+  const uint16_t* q_norm;  // [D] weights of the norms, or null
+  const uint16_t* k_norm;
+  float eps;
   int* err;
 };
+
+// The norm's weights of head h, or null.
+__device__ __forceinline__ const uint16_t* norm_of(const RopeArgs& a, int h) {
+  return h < a.heads ? a.q_norm : h < a.heads + a.kv_heads ? a.k_norm : nullptr;
+}
 
 constexpr int kThreads = 256;    // of the element path
 constexpr int kMostThreads = 512;  // of the vector path
@@ -55,7 +68,7 @@ __device__ __forceinline__ uint4 ldg_now(const uint16_t* p) {
 // the halves of a pair below R, consecutive ones above. A thread takes two
 // heads, whose four vectors are in flight while the slot, the position and
 // the table's row arrive. blockIdx.x: token, blockIdx.y: share of the heads.
-template <bool kB, bool k8, bool kInter, int D>
+template <bool kB, bool k8, bool kInter, bool kNorm, int D>
 __global__ void __launch_bounds__(kMostThreads, 2) rope_append_kernel(const RopeArgs a) {
   constexpr int kLanes = D / 16;  // threads per head
   allow_dependent_launch();
@@ -78,6 +91,19 @@ __global__ void __launch_bounds__(kMostThreads, 2) rope_append_kernel(const Rope
       const size_t all = span(a.T, a.ld, heads * D) - 7;
       x[n][0] = ldg_now(ld_at(row + (size_t)h * D + d0, a.qkv, all, a.err));
       x[n][1] = ldg_now(ld_at(row + (size_t)h * D + d1, a.qkv, all, a.err));
+    }
+  }
+  // the weights of the two heads' norms
+  uint4 g[2][2] = {};
+  if (kNorm) {
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const int h = h0 + n * stride;
+      const uint16_t* w = h < heads ? norm_of(a, h) : nullptr;
+      if (w) {
+        g[n][0] = ldg_keep(ld_at(w + d0, w, (size_t)D - 7, a.err));
+        g[n][1] = ldg_keep(ld_at(w + d1, w, (size_t)D - 7, a.err));
+      }
     }
   }
   const long long slot = *ld_at(a.slots + t, a.slots, (size_t)a.T, a.err);
@@ -104,6 +130,21 @@ __global__ void __launch_bounds__(kMostThreads, 2) rope_append_kernel(const Rope
                              ? *ld_at(a.k_scale + h - a.heads, a.k_scale, (size_t)a.kv_heads, a.err)
                              : *ld_at(a.v_scale + h - a.heads - a.kv_heads, a.v_scale, (size_t)a.kv_heads, a.err));
   }
+  float rms[2] = {1.f, 1.f};  // of the heads, inverse
+  if (kNorm) {
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      float sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        const float2 v = unpack16<kB>(reinterpret_cast<const uint32_t(&)[4]>(x[n][w / 4])[w % 4]);
+        sum = fmaf(v.x, v.x, fmaf(v.y, v.y, sum));
+      }
+#pragma unroll
+      for (int d = 1; d < kLanes; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      rms[n] = rsqrtf(sum * (1.f / D) + a.eps);
+    }
+  }
   // two dimensions of each vector at a time, in place (an e4m3 pair takes the
   // word's lower half)
 #pragma unroll
@@ -122,6 +163,12 @@ __global__ void __launch_bounds__(kMostThreads, 2) rope_append_kernel(const Rope
       uint32_t& x0 = reinterpret_cast<uint32_t(&)[4]>(x[n][0])[w];
       uint32_t& x1 = reinterpret_cast<uint32_t(&)[4]>(x[n][1])[w];
       float2 lo = unpack16<kB>(x0), hi = unpack16<kB>(x1);
+      if (kNorm && norm_of(a, h)) {
+        const float2 u = unpack16<kB>(reinterpret_cast<const uint32_t(&)[4]>(g[n][0])[w]);
+        const float2 v = unpack16<kB>(reinterpret_cast<const uint32_t(&)[4]>(g[n][1])[w]);
+        lo = make_float2(lo.x * rms[n] * u.x, lo.y * rms[n] * u.y);
+        hi = make_float2(hi.x * rms[n] * v.x, hi.y * rms[n] * v.y);
+      }
       if (turned && !is_v) {
         const float2 u = lo, v = hi;
         if (kInter) {
@@ -173,7 +220,7 @@ __global__ void __launch_bounds__(kMostThreads, 2) rope_append_kernel(const Rope
 }
 
 // Any even R, stride and 2-byte alignment of qkv: one thread per element.
-template <bool kB, bool k8, bool kInter>
+template <bool kB, bool k8, bool kInter, bool kNorm>
 __global__ void __launch_bounds__(kThreads) rope_append_any_kernel(const RopeArgs a, int D) {
   allow_dependent_launch();
   grid_dependency_wait();
@@ -195,7 +242,22 @@ __global__ void __launch_bounds__(kThreads) rope_append_any_kernel(const RopeArg
     const bool is_q = h < a.heads, is_v = h >= a.heads + a.kv_heads;
     if (!is_q && !keep) continue;
     const uint16_t* x = a.qkv + (size_t)t * a.ld + (size_t)h * D;
-    auto at16 = [&](int i) { return value16<kB>(*ld_at(x + i, a.qkv, span(a.T, a.ld, heads * D), a.err)); };
+    const uint16_t* weight = kNorm ? norm_of(a, h) : nullptr;
+    float rms = 1.f;
+    if (kNorm && weight) {  // (D is a multiple of 32: a warp's elements are of one head)
+      float sum = 0.f;
+      for (int j = threadIdx.x % 32; j < D; j += 32) {
+        const float v = value16<kB>(*ld_at(x + j, a.qkv, span(a.T, a.ld, heads * D), a.err));
+        sum = fmaf(v, v, sum);
+      }
+#pragma unroll
+      for (int j = 16; j; j >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, j);
+      rms = rsqrtf(sum / D + a.eps);
+    }
+    auto at16 = [&](int i) {
+      const float v = value16<kB>(*ld_at(x + i, a.qkv, span(a.T, a.ld, heads * D), a.err));
+      return kNorm && weight ? v * rms * value16<kB>(*ld_at(weight + i, weight, (size_t)D, a.err)) : v;
+    };
     auto angle = [&](int i) { return *ld_at(turn + i, a.table, (size_t)a.table_len * a.R, a.err); };
     float f = at16(d);
     if (d < a.R && !is_v) {
@@ -220,14 +282,14 @@ __global__ void __launch_bounds__(kThreads) rope_append_any_kernel(const RopeArg
   }
 }
 
-template <bool kB, bool k8, bool kInter>
+template <bool kB, bool k8, bool kInter, bool kNorm>
 cudaError_t launch_rope(const RopeArgs& a, int D, cudaStream_t stream) {
   const int heads = a.heads + 2 * a.kv_heads;
   auto al = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
-  if (a.R % 16 != 0 || a.ld % 8 != 0 || !al(a.qkv) || !al(a.q) || !al(a.table)) {
+  if (a.R % 16 != 0 || a.ld % 8 != 0 || !al(a.qkv) || !al(a.q) || !al(a.table) || !al(a.q_norm) || !al(a.k_norm)) {
     // a token over several blocks while the tokens are few
     const int steps = (heads * D + kThreads - 1) / kThreads, share = (device_sms() * 4 + a.T - 1) / a.T;
-    return launch_pdl(rope_append_any_kernel<kB, k8, kInter>, dim3((unsigned)a.T, (unsigned)(share < steps ? share : steps)),
+    return launch_pdl(rope_append_any_kernel<kB, k8, kInter, kNorm>, dim3((unsigned)a.T, (unsigned)(share < steps ? share : steps)),
                       dim3(kThreads), 0, stream, a, D);
   }
   // two heads per thread, in as few blocks per token as hold them, evenly
@@ -235,8 +297,22 @@ cudaError_t launch_rope(const RopeArgs& a, int D, cudaStream_t stream) {
   const int blocks = (tasks + kMostThreads - 1) / kMostThreads;
   const int threads = ((tasks + blocks - 1) / blocks + 31) / 32 * 32;
   const dim3 grid((unsigned)a.T, (unsigned)blocks);
-  return D == 64 ? launch_pdl(rope_append_kernel<kB, k8, kInter, 64>, grid, dim3(threads), 0, stream, a)
-                 : launch_pdl(rope_append_kernel<kB, k8, kInter, 128>, grid, dim3(threads), 0, stream, a);
+  return D == 64 ? launch_pdl(rope_append_kernel<kB, k8, kInter, kNorm, 64>, grid, dim3(threads), 0, stream, a)
+                 : launch_pdl(rope_append_kernel<kB, k8, kInter, kNorm, 128>, grid, dim3(threads), 0, stream, a);
+}
+
+template <bool kNorm>
+cudaError_t launch_types(const RopeArgs& a, int D, bool bf16, bool e4m3, bool interleaved, cudaStream_t stream) {
+  switch ((bf16 ? 4 : 0) | (e4m3 ? 2 : 0) | (interleaved ? 1 : 0)) {
+    case 0: return launch_rope<false, false, false, kNorm>(a, D, stream);
+    case 1: return launch_rope<false, false, true, kNorm>(a, D, stream);
+    case 2: return launch_rope<false, true, false, kNorm>(a, D, stream);
+    case 3: return launch_rope<false, true, true, kNorm>(a, D, stream);
+    case 4: return launch_rope<true, false, false, kNorm>(a, D, stream);
+    case 5: return launch_rope<true, false, true, kNorm>(a, D, stream);
+    case 6: return launch_rope<true, true, false, kNorm>(a, D, stream);
+    default: return launch_rope<true, true, true, kNorm>(a, D, stream);
+  }
 }
 
 }  // namespace
@@ -244,23 +320,16 @@ cudaError_t launch_rope(const RopeArgs& a, int D, cudaStream_t stream) {
 cudaError_t launch_rope_append(const uint16_t* qkv, long long ld, const float* table, int table_len, int R,
                                const int32_t* positions, const int64_t* slots, int T, int heads, int kv_heads,
                                int head_dim, uint16_t* q, void* k, void* v, const float* k_scale,
-                               const float* v_scale, int pages, int page_shift, bool bf16, bool e4m3,
-                               bool interleaved, cudaStream_t stream) {
+                               const float* v_scale, int pages, int page_shift, const uint16_t* q_norm,
+                               const uint16_t* k_norm, float eps, bool bf16, bool e4m3, bool interleaved,
+                               cudaStream_t stream) {
   if (T == 0) return cudaSuccess;
   RopeArgs a = {qkv, table, positions, slots, q, k, v, k_scale, v_scale, ld, (long long)pages << page_shift,
-                table_len, R, T, heads, kv_heads, page_shift, nullptr};
+                table_len, R, T, heads, kv_heads, page_shift, q_norm, k_norm, eps, nullptr};
   cudaError_t e = device_error_word(&a.err);
   if (e != cudaSuccess) return e;
-  switch ((bf16 ? 4 : 0) | (e4m3 ? 2 : 0) | (interleaved ? 1 : 0)) {
-    case 0: return launch_rope<false, false, false>(a, head_dim, stream);
-    case 1: return launch_rope<false, false, true>(a, head_dim, stream);
-    case 2: return launch_rope<false, true, false>(a, head_dim, stream);
-    case 3: return launch_rope<false, true, true>(a, head_dim, stream);
-    case 4: return launch_rope<true, false, false>(a, head_dim, stream);
-    case 5: return launch_rope<true, false, true>(a, head_dim, stream);
-    case 6: return launch_rope<true, true, false>(a, head_dim, stream);
-    default: return launch_rope<true, true, true>(a, head_dim, stream);
-  }
+  return q_norm || k_norm ? launch_types<true>(a, head_dim, bf16, e4m3, interleaved, stream)
+                          : launch_types<false>(a, head_dim, bf16, e4m3, interleaved, stream);
 }
 
 }  // namespace w4a16

@@ -16,7 +16,7 @@ import ctypes
 import dataclasses
 import importlib.util
 import os
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -126,7 +126,8 @@ def _native():
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
         module.bind(*[ctypes.cast(getattr(lib, "w4a16_" + name), ctypes.c_void_p).value for name in
-                      ("rms_norm", "rope_append", "attn_workspace_size", "attn_decode", "attn_prompt")],
+                      ("rms_norm", "rope_append_norm", "attn_workspace_size", "attn_decode", "attn_prompt",
+                       "route_workspace_size", "route", "experts_workspace_size", "gemm_experts")],
                     w4._check, w4.stream_workspace)
         _native_module = module
     return _native_module
@@ -149,14 +150,20 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Ten
 
 def rope_append(qkv: torch.Tensor, cos_sin: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor,
                 cache: KVCache, interleaved: bool = False, out: Optional[torch.Tensor] = None,
-                stream=None) -> torch.Tensor:
+                stream=None, q_norm: Optional[torch.Tensor] = None, k_norm: Optional[torch.Tensor] = None,
+                eps: float = 1e-5) -> torch.Tensor:
     """Rotate the query and key heads of qkv [T, (heads + 2 kv_heads) *
     head_dim] by `positions` (int32 [T]) and append keys and values to
     `cache` at `slots` (int64 [T], page * page_size + place; negative: not
     stored). cos_sin float32 [table_len, rotary]: the cosines of a position's
     rotary/2 angles, then the sines. Returns the queries [T, heads, head_dim].
+
+    With `q_norm` and `k_norm` (each [head_dim] of qkv's type, or None) every
+    query (key) head is x * (mean x^2 + eps)^(-1/2) * weight before its
+    rotation, in the same pass.
     """
-    return (_native_module or _native()).rope_append(qkv, cos_sin, positions, slots, cache, interleaved, out, stream)
+    return (_native_module or _native()).rope_append(qkv, cos_sin, positions, slots, cache, interleaved, out, stream,
+                                                     q_norm, k_norm, eps)
 
 
 def attn_workspace_size(tokens: int, batch: int, heads: int, kv_heads: int, head_dim: int) -> int:
@@ -190,3 +197,90 @@ def attn_prompt(q: torch.Tensor, cache: KVCache, table: torch.Tensor, starts: to
     starts[b + 1) (int32 [batch + 1]) and lens[b] cached tokens, the new ones
     last and already appended. The rest as attn_decode."""
     return (_native_module or _native()).attend(q, cache, table, starts, lens, scale, out, return_lse, workspace, stream)
+
+
+# ------------------------------------------------------------------ experts
+
+
+@dataclasses.dataclass
+class PackedExperts:
+    """The packed int4 weights of a layer's experts, all K x N: the buffers of
+    one expert (PackedWeight) after those of another."""
+    Wq: torch.Tensor       # int32 [experts * K*N/8]
+    Sp: torch.Tensor       # float16 [experts * K/group * N]
+    Zp: torch.Tensor       # int32 [experts * K/group * N / 8]
+    experts: int
+    K: int
+    N: int
+    group: int
+
+    @property
+    def nbytes(self) -> int:
+        return self.Wq.numel() * 4 + self.Sp.numel() * 2 + self.Zp.numel() * 4
+
+    def expert(self, e: int):
+        """Expert e as a PackedWeight (the same memory)."""
+        if not 0 <= e < self.experts:
+            raise IndexError(f"expert {e} of {self.experts}")
+        return w4.PackedWeight(*(t.view(self.experts, -1)[e] for t in (self.Wq, self.Sp, self.Zp)), self.K, self.N,
+                               self.group)
+
+
+def stack_experts(weights) -> PackedExperts:
+    """The PackedWeights of experts, alike in K, N and group, as one (copied)."""
+    weights = list(weights)
+    if not weights:
+        raise ValueError("no experts")
+    first = weights[0]
+    for w in weights:
+        if (w.K, w.N, w.group) != (first.K, first.N, first.group):
+            raise ValueError(f"experts differ: {w.K} x {w.N} group {w.group} beside {first.K} x {first.N} group "
+                             f"{first.group}")
+    return PackedExperts(*(torch.cat([getattr(w, n) for w in weights]) for n in ("Wq", "Sp", "Zp")), len(weights),
+                         first.K, first.N, first.group)
+
+
+class Routing(NamedTuple):
+    """What route answers and gemm_experts takes. A choice is token * top_k +
+    j, the j-th expert of a token."""
+    experts: torch.Tensor  # int32 [T, top_k], descending; -1: none
+    weights: torch.Tensor  # float32 [T, top_k]
+    rows: torch.Tensor     # int32 [T * top_k]: the choices by expert, those of none last
+    offsets: torch.Tensor  # int32 [experts + 1]: expert e's are rows[offsets[e]:offsets[e + 1]]
+
+
+def route(logits: torch.Tensor, top_k: int, scoring: str = "softmax", renormalize: bool = True,
+          workspace: Optional[torch.Tensor] = None, stream=None) -> Routing:
+    """The router: of logits [T, experts] (fp16, bf16 or fp32; rows may be
+    strided) each token's top_k largest, in descending order, equal ones by
+    the lower index, their weights (softmax over all experts, or "sigmoid" of
+    each; with `renormalize` divided by the chosen ones' sum) and the choices
+    by expert. A logit of -inf is never chosen: its place has expert -1 and
+    weight 0 (a row of -inf, for a padded token, chooses no expert).
+    `workspace` as for gemm."""
+    return Routing(*(_native_module or _native()).route(logits, top_k, scoring, renormalize, workspace, stream))
+
+
+def experts_workspace_size(T: int, top_k: int, pe: PackedExperts, silu_mul: bool = False, combine: bool = False,
+                           path: str = "auto") -> int:
+    """Scratch bytes of a gemm_experts call on the current device."""
+    b = ctypes.c_size_t()
+    flags = w4._PATHS[path] | (w4.SILU_MUL if silu_mul else 0) | (w4.EXPERTS_COMBINE if combine else 0)
+    w4._check(w4.lib().w4a16_experts_workspace_size(T, top_k, pe.experts, pe.N, pe.K, pe.group, flags, ctypes.byref(b)),
+              "w4a16_experts_workspace_size")
+    return b.value
+
+
+def gemm_experts(A: torch.Tensor, pe: PackedExperts, routing: Routing, silu_mul: bool = False, combine: bool = False,
+                 out: Optional[torch.Tensor] = None, path: str = "auto", workspace: Optional[torch.Tensor] = None,
+                 stream=None) -> torch.Tensor:
+    """Every token's rows times its experts' weights, grouped by expert.
+
+    A [T, K] gives each of a token's choices the token's row, A [T, top_k, K]
+    a row of its own (fp16 or bf16). Returns Y [T, top_k, N], choice (t, j)
+    times expert routing.experts[t, j] (zeros where that is -1); with
+    `silu_mul` (pe's columns are [gate | up]) silu(gate) * up, [T, top_k,
+    N/2]; with `combine` the sum over j weighted by routing.weights, [T, N].
+    `path`: "auto" or "decode". `workspace` as for gemm."""
+    return (_native_module or _native()).gemm_experts(A, pe, routing, silu_mul, combine, out, w4._PATHS[path], workspace,
+                                                      stream)

@@ -403,6 +403,19 @@ int w4a16_rope_append(const uint16_t* qkv, int64_t qkv_stride, const float* cos_
                       void* v_cache, const float* k_scale, const float* v_scale, int pages,
                       int page_size, int flags, void* stream);
 
+/* As w4a16_rope_append with a norm of every query head and every key head
+ * before the rotation: in fp32, x * (mean_d x^2 + eps)^(-1/2) * weight[d],
+ * with the weights q_norm of queries and k_norm of keys, [head_dim] in qkv's
+ * type, each null where its heads have no norm (2-byte aligned; 16 bytes run
+ * faster). Nothing is rounded between norm, rotation and the result. Values
+ * pass through. */
+int w4a16_rope_append_norm(const uint16_t* qkv, int64_t qkv_stride, const float* cos_sin,
+                           int table_len, int rotary, const int32_t* positions,
+                           const int64_t* slots, int tokens, int heads, int kv_heads, int head_dim,
+                           uint16_t* q, void* k_cache, void* v_cache, const float* k_scale,
+                           const float* v_scale, int pages, int page_size, const uint16_t* q_norm,
+                           const uint16_t* k_norm, float eps, int flags, void* stream);
+
 /* Scratch bytes of w4a16_attn_decode (tokens = batch) and w4a16_attn_prompt
  * on the current device; 0 when none. The buffer is of w4a16_gemm's kind: a
  * flag area that must be zero before the first use and that every call
@@ -449,6 +462,69 @@ int w4a16_attn_prompt(const uint16_t* q, int64_t q_stride, const void* k_cache, 
                       const int32_t* starts, const int32_t* lens, int tokens, int batch, int heads,
                       int kv_heads, int head_dim, float scale, uint16_t* out, float* lse,
                       void* workspace, size_t workspace_bytes, int flags, void* stream);
+
+/* ------------------------------------------------------------------------
+ * A layer of experts: the router, and the W4A16 products grouped by expert.
+ * ------------------------------------------------------------------------ */
+
+/* The router. logits [T][E] (row stride in elements): fp16, bfloat16 with
+ * W4A16_BF16 or fp32 with W4A16_ROUTE_FP32. A token's experts are its top_k
+ * largest logits in descending order, equal ones by the lower index (NaN
+ * before everything, -0 equal to +0). A logit of -inf is never chosen: where
+ * fewer than top_k are left, the rest of the token's choices have the expert
+ * -1 and the weight 0 (a row of -inf alone, for a padded token, chooses none).
+ *   experts [T][top_k]  int32
+ *   weights [T][top_k]  fp32: exp(x) / sum_e exp(x_e) of the chosen logit x
+ *                       (1 / (1 + exp(-x)) with W4A16_ROUTE_SIGMOID); with
+ *                       W4A16_ROUTE_RENORMALIZE divided by the sum of the
+ *                       token's chosen ones (0 where that is 0)
+ *   rows    [T * top_k] int32: the choices token * top_k + j by expert, those
+ *                       of one expert in ascending order, those of none last
+ *   offsets [E + 1]     int32: expert e's choices are rows[offsets[e]] ..
+ *                       rows[offsets[e + 1] - 1]
+ * NaN and +inf logits go where the formulas take them. T <= 2^20, E <= 512,
+ * top_k <= 32 and E. T = 0 writes the offsets only. The workspace (256-byte
+ * aligned; w4a16_route_workspace_size, 0 for few tokens) may be the one of
+ * the GEMMs: its flag area is not touched. */
+#define W4A16_ROUTE_FP32 0x4000
+#define W4A16_ROUTE_SIGMOID 0x8000
+#define W4A16_ROUTE_RENORMALIZE 0x10000
+int w4a16_route_workspace_size(int T, int E, int top_k, size_t* bytes);
+int w4a16_route(const void* logits, int64_t logits_stride, int T, int E, int top_k, int32_t* experts,
+                float* weights, int32_t* rows, int32_t* offsets, void* workspace,
+                size_t workspace_bytes, int flags, void* stream);
+
+/* The products of T tokens with their experts' weights. Wq, scales and zeros
+ * are the packed weight of E * N columns: expert e's packed buffers (K x N)
+ * after one another. experts, weights, rows and offsets are the router's.
+ * For every choice f = token * top_k + j of an expert e = experts[f]
+ *   y[f] = A[token] . dequant(W_e)
+ * (A [T][K]; with W4A16_EXPERTS_PER_CHOICE A is [T * top_k][K] and choice f
+ * multiplies A[f]), and
+ *   Y [T * top_k][N]    = y, with zeros for choices of no expert; or
+ *   Y [T * top_k][N/2]  = silu(y[:, :N/2]) * y[:, N/2:] with W4A16_SILU_MUL; or
+ *   Y [T][N]            = sum_j weights[f] * y[f] over a token's choices that
+ *                         have an expert, with W4A16_EXPERTS_COMBINE.
+ * The two do not go together. A and Y are fp16, or bfloat16 with W4A16_BF16;
+ * accumulation is fp32. The weights enter as (q - z) * s, unrounded on the
+ * path for few rows (W4A16_PATH_DECODE).
+ * Combined, the products wait in the workspace and are added in the order of
+ * the token's choices: the result is the same every time.
+ * Shapes as w4a16_gemm's (N % 32 == 0 with W4A16_SILU_MUL, any group that is a multiple of
+ * 64 and divides K), E * N below 2^31, T, E and top_k as the router's. `flags`
+ * carries the path in its low byte: W4A16_PATH_AUTO or _DECODE. An offset outside [0, T * top_k] is clamped
+ * and a row outside [0, T * top_k) skipped, both recorded (bit 128); choices
+ * that `rows` does not list stay as they are (in a combined result, what the
+ * workspace held counts). */
+#define W4A16_EXPERTS_PER_CHOICE 0x20000
+#define W4A16_EXPERTS_COMBINE 0x40000
+int w4a16_experts_workspace_size(int T, int top_k, int E, int N, int K, int group, int flags,
+                                 size_t* bytes);
+int w4a16_gemm_experts(const uint16_t* A, const uint32_t* Wq, const uint16_t* scales,
+                       const uint32_t* zeros, int T, int top_k, int E, int N, int K, int group,
+                       const int32_t* experts, const float* weights, const int32_t* rows,
+                       const int32_t* offsets, uint16_t* Y, void* workspace, size_t workspace_bytes,
+                       int flags, void* stream);
 
 /* Synchronizes `stream`, then reads and clears the library's device error
  * word (set by a kernel that gave up a bounded wait or failed a self-check;
