@@ -378,28 +378,55 @@ __global__ void __launch_bounds__(kThreads, 2) experts_decode_kernel(const Decod
   }
 }
 
-// Y[t] = the sum of the rows of token t's choices that have an expert, in
-// their order. One thread per four columns.
+// Eight columns of a row of products, 16-bit or fp32.
 template <bool kB>
-__global__ void __launch_bounds__(kThreads) experts_sum_kernel(const ExpertArgs a, const float* D) {
+__device__ __forceinline__ void eight(const uint16_t* p, float (&v)[8]) {
+  const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p));
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = unpack16<kB>(w[i]);
+    v[2 * i] = f.x, v[2 * i + 1] = f.y;
+  }
+}
+template <bool kB>
+__device__ __forceinline__ void eight(const float* p, float (&v)[8]) {
+  const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+
+// Y[t] = the sum of the rows of D of token t's choices that have an expert, in
+// their order, in fp32. One thread per eight columns.
+template <bool kB, class T>
+__global__ void __launch_bounds__(kThreads) experts_sum_kernel(const ExpertArgs a, const T* D) {
   allow_dependent_launch();
   grid_dependency_wait();
-  const int vecs = a.N / 4;
+  const int vecs = a.N / 8;
   const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
   if (i >= (long long)a.T * vecs) return;
-  const int t = (int)(i / vecs), n = (int)(i % vecs) * 4;
-  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int t = (int)(i / vecs), n = (int)(i % vecs) * 8;
+  float sum[8] = {};
 #pragma unroll 4
   for (int j = 0; j < a.top; ++j) {
     const size_t f = (size_t)t * a.top + j;
     if (*ld_at(a.experts + f, a.experts, (size_t)choices(a), a.err) < 0) continue;
-    const float* d = D + f * a.N + n;
-    const float4 v = __ldcs(reinterpret_cast<const float4*>(ld_at(d, D, (size_t)choices(a) * a.N - 3, a.err)));
-    sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+    float v[8];
+    eight<kB>(ld_at(D + f * a.N + n, D, (size_t)choices(a) * a.N - 7, a.err), v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum[k] += v[k];
   }
   uint16_t* y = a.Y + (size_t)t * a.N + n;
-  if (in_buf(y, a.Y, (size_t)a.T * a.N - 3, a.err))
-    *reinterpret_cast<uint2*>(y) = make_uint2(pack16<kB>(sum.x, sum.y), pack16<kB>(sum.z, sum.w));
+  if (in_buf(y, a.Y, (size_t)a.T * a.N - 7, a.err))
+    *reinterpret_cast<uint4*>(y) = make_uint4(pack16<kB>(sum[0], sum[1]), pack16<kB>(sum[2], sum[3]),
+                                              pack16<kB>(sum[4], sum[5]), pack16<kB>(sum[6], sum[7]));
+}
+
+template <class T>
+cudaError_t launch_sum(const ExpertArgs& a, const T* D, bool bf16, cudaStream_t stream) {
+  const long long threads = (long long)a.T * (a.N / 8);
+  const dim3 grid((unsigned)((threads + kThreads - 1) / kThreads));
+  return bf16 ? launch_pdl(experts_sum_kernel<true, T>, grid, dim3(kThreads), 0, stream, a, D)
+              : launch_pdl(experts_sum_kernel<false, T>, grid, dim3(kThreads), 0, stream, a, D);
 }
 
 template <bool kB, int KS>
@@ -440,11 +467,11 @@ cudaError_t launch_experts_decode(ExpertArgs a, bool bf16, void* workspace, cuda
   DecodeParams p = {a, workspace ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kWorkspaceFlags) : nullptr, 0, 0};
   const int parts = 1;
   e = bf16 ? launch_experts_decode_t<true>(p, parts, stream) : launch_experts_decode_t<false>(p, parts, stream);
-  if (e != cudaSuccess || !a.combine) return e;
-  const long long threads = (long long)a.T * (a.N / 4);
-  const dim3 grid((unsigned)((threads + kThreads - 1) / kThreads));
-  return bf16 ? launch_pdl(experts_sum_kernel<true>, grid, dim3(kThreads), 0, stream, a, p.D)
-              : launch_pdl(experts_sum_kernel<false>, grid, dim3(kThreads), 0, stream, a, p.D);
+  return e != cudaSuccess || !a.combine ? e : launch_sum(a, p.D, bf16, stream);
+}
+
+cudaError_t launch_experts_sum(const ExpertArgs& a, const uint16_t* D, bool bf16, cudaStream_t stream) {
+  return launch_sum(a, D, bf16, stream);
 }
 
 }  // namespace w4a16

@@ -105,6 +105,11 @@ bool cached_tensor_map(CUtensorMap* out, const void* ptr, CUtensorMapDataType dt
 // [32 words] with the 128-byte swizzle; a box is `sa` atoms of 8 strips (128
 // columns). From the same cache.
 bool cached_code_map(CUtensorMap* out, const uint32_t* Wq, int N, int K, int sa);
+// 4-D tensor map of E experts' packed weights, [E][N/16 strips][K/64 atoms x 4
+// rows][32 words]; a box is `sa` atoms of 8 strips of one expert. With `halves`
+// [E][2 halves][N/32 strips], and a box 4 strips of both halves. From the same
+// cache.
+bool cached_expert_map(CUtensorMap* out, const uint32_t* Wq, int N, int K, int E, int sa, bool halves);
 int tc_choose_split(int M, int N, int K, int group, int sms);
 // 64-k atoms per pipeline stage of the tensor-core GEMM (2 when K and the
 // group are multiples of 128, else 1).
@@ -164,6 +169,12 @@ cudaError_t launch_route(const void* logits, long long ld, int type, int T, int 
 struct ExpertArgs;
 size_t experts_decode_workspace_bytes(int choices, int N, bool combine);
 cudaError_t launch_experts_decode(ExpertArgs args, bool bf16, void* workspace, cudaStream_t stream);
+// The same for many rows per expert, on the tensor cores; combined, the
+// choices' products in 16 bits.
+size_t experts_tc_workspace_bytes(int choices, int N, bool combine);
+cudaError_t launch_experts_tc(ExpertArgs args, bool bf16, void* workspace, cudaStream_t stream);
+// Y[t] = the sum of D's rows of token t's choices (16 bits).
+cudaError_t launch_experts_sum(const ExpertArgs& args, const uint16_t* D, bool bf16, cudaStream_t stream);
 
 // Reads the device error word (bounded waits that gave up, self-checks) and
 // clears it if set.

@@ -120,7 +120,7 @@ int check_experts(int T, int top_k, int E, int N, int K, int group, int flags) {
   if (int rc = check_routing(T, E, top_k)) return rc;
   constexpr int known = W4A16_BF16 | W4A16_SILU_MUL | W4A16_EXPERTS_PER_CHOICE | W4A16_EXPERTS_COMBINE;
   const int path = flags & 0xff;
-  if ((flags & ~(known | 0xff)) || (path != W4A16_PATH_AUTO && path != W4A16_PATH_DECODE))
+  if ((flags & ~(known | 0xff)) || (path != W4A16_PATH_AUTO && path != W4A16_PATH_DECODE && path != W4A16_PATH_TENSOR_PAIR))
     return fail(W4A16_ERR_INVALID_ARG, "flags=0x%x: unknown bits or path", flags);
   if ((flags & W4A16_SILU_MUL) && (flags & W4A16_EXPERTS_COMBINE))
     return fail(W4A16_ERR_INVALID_ARG, "W4A16_SILU_MUL does not go with W4A16_EXPERTS_COMBINE");
@@ -131,6 +131,20 @@ int check_experts(int T, int top_k, int E, int N, int K, int group, int flags) {
     return fail(W4A16_ERR_UNSUPPORTED_SHAPE, "N=%d: gate and up need a multiple of 32", N);
   if ((long long)E * N > 0x7fffffffll) return fail(W4A16_ERR_UNSUPPORTED_SHAPE, "E=%d experts of N=%d columns: above 2^31", E, N);
   return W4A16_OK;
+}
+
+// Whether a call takes the kernel on the tensor cores.
+bool experts_on_tensor_cores(int T, int top_k, int E, int flags) {
+  const int path = flags & 0xff;
+  if (path != W4A16_PATH_AUTO) return path == W4A16_PATH_TENSOR_PAIR;
+  return (long long)T * top_k > 16ll * E;
+}
+
+size_t experts_workspace(int T, int top_k, int E, int N, int flags) {
+  const bool combine = (flags & W4A16_EXPERTS_COMBINE) != 0;
+  if (T == 0) return 0;
+  return experts_on_tensor_cores(T, top_k, E, flags) ? experts_tc_workspace_bytes(T * top_k, N, combine)
+                                                     : experts_decode_workspace_bytes(T * top_k, N, combine);
 }
 
 }  // namespace
@@ -277,7 +291,7 @@ int w4a16_route(const void* logits, int64_t logits_stride, int T, int E, int top
 int w4a16_experts_workspace_size(int T, int top_k, int E, int N, int K, int group, int flags, size_t* bytes) {
   if (int rc = check_experts(T, top_k, E, N, K, group, flags)) return rc;
   if (!bytes) return fail(W4A16_ERR_INVALID_ARG, "null output pointer");
-  *bytes = T == 0 ? 0 : experts_decode_workspace_bytes(T * top_k, N, (flags & W4A16_EXPERTS_COMBINE) != 0);
+  *bytes = experts_workspace(T, top_k, E, N, flags);
   return report_ok();
 }
 
@@ -293,12 +307,12 @@ int w4a16_gemm_experts(const uint16_t* A, const uint32_t* Wq, const uint16_t* sc
   if (!aligned(A, 16) || !aligned(Wq, 16) || !aligned(scales, 16) || !aligned(Y, 16) || !aligned(zeros, 8) ||
       !aligned(experts, 4) || !aligned(weights, 4) || !aligned(rows, 4) || !aligned(offsets, 4))
     return fail(W4A16_ERR_MISALIGNED, "alignment: A, Wq, scales and Y need 16 bytes, zeros 8, the routing 4");
-  const size_t need = experts_decode_workspace_bytes(T * top_k, N, combine);
+  const size_t need = experts_workspace(T, top_k, E, N, flags);
   if (int rc = check_workspace(workspace, workspace_bytes, need)) return rc;
   const ExpertArgs a = {A, Wq, scales, zeros, experts, weights, rows, offsets, Y, T, top_k, E, N, K, group,
                         (flags & W4A16_EXPERTS_PER_CHOICE) != 0, (flags & W4A16_SILU_MUL) != 0, combine, nullptr};
-  return finish(launch_experts_decode(a, (flags & W4A16_BF16) != 0, need ? workspace : nullptr, (cudaStream_t)stream),
-                "experts' product launch");
+  const auto launch = experts_on_tensor_cores(T, top_k, E, flags) ? launch_experts_tc : launch_experts_decode;
+  return finish(launch(a, (flags & W4A16_BF16) != 0, need ? workspace : nullptr, (cudaStream_t)stream), "experts' product launch");
 }
 
 }  // extern "C"

@@ -760,13 +760,13 @@ namespace {
 
 struct MapKey {
   const void* ptr;
-  uint64_t dims[3];
-  uint32_t box[3];
+  uint64_t dims[4];
+  uint32_t box[4];
   int dtype, rank, swizzle;
   bool operator==(const MapKey& o) const {
-    return ptr == o.ptr && dims[0] == o.dims[0] && dims[1] == o.dims[1] && dims[2] == o.dims[2] &&
-           box[0] == o.box[0] && box[1] == o.box[1] && box[2] == o.box[2] && dtype == o.dtype &&
-           rank == o.rank && swizzle == o.swizzle;
+    for (int i = 0; i < 4; ++i)
+      if (dims[i] != o.dims[i] || box[i] != o.box[i]) return false;
+    return ptr == o.ptr && dtype == o.dtype && rank == o.rank && swizzle == o.swizzle;
   }
 };
 constexpr int kMapCache = 64;
@@ -775,10 +775,11 @@ MapKey g_map_keys[kMapCache];
 CUtensorMap g_maps[kMapCache];
 int g_map_used = 0, g_map_next = 0;
 
-// A densely packed row-major array of rank 2 or 3 (dims[0] innermost).
+// A densely packed row-major array of rank 2 to 4 (dims[0] innermost; those
+// beyond the rank are 1).
 bool cached_map(CUtensorMap* out, const void* ptr, CUtensorMapDataType dt, int esize, int rank,
-                const uint64_t (&dims)[3], const uint32_t (&box)[3], CUtensorMapSwizzle swizzle) {
-  const MapKey key = {ptr, {dims[0], dims[1], dims[2]}, {box[0], box[1], box[2]}, (int)dt, rank,
+                const uint64_t (&dims)[4], const uint32_t (&box)[4], CUtensorMapSwizzle swizzle) {
+  const MapKey key = {ptr, {dims[0], dims[1], dims[2], dims[3]}, {box[0], box[1], box[2], box[3]}, (int)dt, rank,
                       (int)swizzle};
   {
     std::lock_guard<std::mutex> lock(g_map_mutex);
@@ -790,10 +791,11 @@ bool cached_map(CUtensorMap* out, const void* ptr, CUtensorMapDataType dt, int e
   }
   PFN_cuTensorMapEncodeTiled_v12000 encode = encode_fn();
   if (!encode) return false;
-  const cuuint64_t gdims[3] = {(cuuint64_t)dims[0], (cuuint64_t)dims[1], (cuuint64_t)dims[2]};
-  const cuuint64_t strides[2] = {(cuuint64_t)dims[0] * esize, (cuuint64_t)dims[0] * dims[1] * esize};
-  const cuuint32_t gbox[3] = {box[0], box[1], box[2]};
-  const cuuint32_t estr[3] = {1, 1, 1};
+  const cuuint64_t gdims[4] = {(cuuint64_t)dims[0], (cuuint64_t)dims[1], (cuuint64_t)dims[2], (cuuint64_t)dims[3]};
+  const cuuint64_t strides[3] = {(cuuint64_t)dims[0] * esize, (cuuint64_t)dims[0] * dims[1] * esize,
+                                 (cuuint64_t)dims[0] * dims[1] * dims[2] * esize};
+  const cuuint32_t gbox[4] = {box[0], box[1], box[2], box[3]};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
   if (encode(out, dt, (cuuint32_t)rank, const_cast<void*>(ptr), gdims, strides, gbox, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
@@ -810,13 +812,20 @@ bool cached_map(CUtensorMap* out, const void* ptr, CUtensorMapDataType dt, int e
 bool cached_tensor_map(CUtensorMap* out, const void* ptr, CUtensorMapDataType dt, int esize,
                        uint64_t dims0, uint64_t dims1, uint32_t box0, uint32_t box1,
                        CUtensorMapSwizzle swizzle) {
-  return cached_map(out, ptr, dt, esize, 2, {dims0, dims1, 1}, {box0, box1, 1}, swizzle);
+  return cached_map(out, ptr, dt, esize, 2, {dims0, dims1, 1, 1}, {box0, box1, 1, 1}, swizzle);
 }
 
 bool cached_code_map(CUtensorMap* out, const uint32_t* Wq, int N, int K, int sa) {
   return cached_map(out, Wq, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, 3,
-                    {32, (uint64_t)(K / kAtomK) * 4, (uint64_t)(N / kStripCols)},
-                    {32, (uint32_t)(4 * sa), (uint32_t)(kTileN / kStripCols)}, CU_TENSOR_MAP_SWIZZLE_128B);
+                    {32, (uint64_t)(K / kAtomK) * 4, (uint64_t)(N / kStripCols), 1},
+                    {32, (uint32_t)(4 * sa), (uint32_t)(kTileN / kStripCols), 1}, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+bool cached_expert_map(CUtensorMap* out, const uint32_t* Wq, int N, int K, int E, int sa, bool halves) {
+  const uint64_t h = halves ? 2 : 1;
+  return cached_map(out, Wq, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, 4,
+                    {32, (uint64_t)(K / kAtomK) * 4, (uint64_t)(N / kStripCols) / h, h * E},
+                    {32, (uint32_t)(4 * sa), (uint32_t)(kTileN / kStripCols / h), (uint32_t)h}, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 cudaError_t launch_tc_gemm(const uint16_t* A, const uint32_t* Wq, const uint16_t* Sp,

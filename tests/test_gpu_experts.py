@@ -162,7 +162,7 @@ def check_products(g, pe, routing, dtype, path, silu=True, plain=True, combine=T
     w4.device_status()
 
 
-PATHS = ["decode"]
+PATHS = ["decode", "tensor-pair"]
 SHAPES = [(1, 64, 16, 64), (8, 128, 32, 64), (5, 192, 208, 64), (4, 256, 288, 256), (3, 1024, 160, 128),
           (4, 1408, 96, 64), (2, 2048, 544, 128), (16, 384, 64, 384), (2, 4096, 48, 512), (2, 5120, 32, 1024)]
 
