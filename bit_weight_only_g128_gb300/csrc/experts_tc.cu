@@ -7,17 +7,20 @@
 // token's choices (experts.cu adds them up in fp32).
 //
 // The contraction is the one of the kernel for one weight (tc_pair.cu): a
-// cluster of two CTAs makes a tile of 256 weight columns x up to 192 rows,
-// each CTA dequantizing its 128 columns, RNE((q - z) s) in the activations'
-// type, straight into tensor memory (the MMA's A operand) and staging half of
-// the rows (the B operand). What differs:
-//   - An expert's n rows make ceil(n / 192) tiles of the same size, rounded up
-//     to 16 rows, and the MMA's N is that size: an expert of 40 rows costs
-//     MMAs of 48, not 192. Which tiles there are is known on the device only:
-//     every CTA makes the list of the experts' first tiles from the offsets
-//     when it starts, and each role walks it (a cluster's tiles ascend).
+// cluster of two CTAs makes a tile of 256 weight columns, each CTA dequantizing
+// its 128 columns, RNE((q - z) s) in the activations' type, straight into
+// tensor memory (the MMA's A operand) and staging half of the rows (the B
+// operand). What differs:
+//   - A tile has up to 384 rows in two parts of up to 192, each with its own
+//     accumulator: a dequantized atom serves both, so that conversions, whose
+//     instructions bound the kernel below that, take half as many per row.
+//     An expert's n rows make ceil(n / 384) tiles of the same size, and the
+//     MMA's N is a part's size, rounded up to 16: an expert of 40 rows costs
+//     MMAs of 48. Which tiles there are is known on the device only: every CTA
+//     makes the list of the experts' first tiles from the offsets when it
+//     starts, and each role walks it (a cluster's tiles ascend).
 //   - The rows are gathered by the converting warps: the group that will
-//     convert a stage copies the stage's rows two of its stages before
+//     convert a stage copies the stage's rows one of its stages before
 //     (cp.async, eight lanes a row of 128 bytes, to the swizzled places), and
 //     each of its warps waits for its own copies before it arrives for the
 //     stage. (tile::gather4 copies by the lanes of one warp took about 95
@@ -29,17 +32,14 @@
 //     warp's lanes 0..15 hold gate and 16..31 up of the same 16 results: one
 //     shuffle per two results brings them together in fp32, and the output is
 //     half as wide.
-//   - K is short (an expert's inner width), so that a tile's end matters: two
-//     accumulators of 192 columns take the tiles in turn, and the converting
-//     warps store a tile's results 16 rows at a time between the conversions
-//     of the next tile's stages, which keeps the MMAs fed meanwhile. The
-//     dequantized operand has the remaining 128 columns, four atoms; a stage is
-//     one atom.
+//   - K is short (an expert's inner width), so that a tile's end matters: the
+//     converting warps take a part's accumulator to registers, hand it back
+//     and only then convert and store, one part after the other. The next
+//     tile begins with the first part's MMAs of the stages that are converted
+//     already, and catches up with the second part's when its accumulator is
+//     free.
 // Rings, barriers and their invariants are those of tc_pair.cu, without a
-// barrier for the rows' arrival. Besides, a
-// group finishes a tile's results before it converts a stage of the tile two
-// after it, whose accumulator is the same: what a group waits for before a
-// stage is the work of earlier stages alone. Every wait is
+// barrier for the rows' arrival. A stage is one atom. Every wait is
 // bounded; a wait that gives up sets the library's error word, and its CTA
 // drains and leaves through the same final cluster barrier as a normal run.
 #include <cuda.h>
@@ -55,10 +55,12 @@ using namespace tc;
 using namespace pair;
 
 constexpr int kGroups = 4;                  // dequantizing groups of four warps
-constexpr int kThreads = 64 + 128 * kGroups;
-constexpr int kRows = 192;                  // most rows of a tile (MMA N)
+constexpr int kFirst = 2;                   // the first converting warp, after producer and MMA issuer
+constexpr int kThreads = 32 * kFirst + 128 * kGroups;
+constexpr int kRows = 192;                  // most rows of a part (MMA N); a tile has two
 constexpr int kMostExperts = 512;
-constexpr int kActSlot = kRows / 2 * 128;   // bytes of a CTA's rows of one atom, at most
+constexpr int kPartSlot = kRows / 2 * 128;  // bytes of a CTA's rows of one atom of a part, at most
+constexpr int kActSlot = 2 * kPartSlot;
 // the list of tiles in shared memory: offsets and first tiles [E + 1] each
 constexpr int kListBytes = ((kMostExperts + 1) * 8 + 127) / 128 * 128;
 
@@ -69,24 +71,25 @@ struct TensorParams {
 };
 
 // Tile t of the launch (which lies in expert e's): 256 columns (with silu 128
-// of gate and of up) x the rows [first, first + n) of the list; size: the
-// MMA's N.
+// of gate and of up) x the rows [first, first + n) of the list, in `parts` parts
+// of `size` (the MMA's N).
 struct Tile {
-  int e, col, first, n, size;
+  int e, col, first, n, parts, size;
 };
 
-// Ring depths per CTA (a stage is an atom): codes 16 (64 KiB), the rows as
-// deep as a group's copies two of its stages ahead need (12 slots of 12 KiB),
-// the dequantized operand in the tensor memory that the accumulators leave.
-// The invariants of tc_pair.cu: at least as many dequantized slots as groups,
-// no more than activation slots, code slots a multiple of the groups.
-constexpr int kActSlots = 12, kCodeSlots = 16, kDqSlots = (512 - 2 * kRows) / kAtomCols;
-constexpr int kSmemBytes = kActSlots * kActSlot + kCodeSlots * kCodeAtomBytes + 1024 + kBarBytes + kListBytes;
+// Ring depths per CTA (a stage is an atom): the dequantized operand in the
+// tensor memory beside the accumulators, four slots; the rows four stages
+// deeper, which is how far ahead a group copies them (8 slots of 24 KiB); codes
+// four. The invariants of tc_pair.cu: at least as many dequantized slots as
+// groups, no more than activation slots, code slots a multiple of the groups.
+constexpr int kActSlots = 8, kCodeSlots = 4, kDqSlots = (512 - 2 * kRows) / kAtomCols;
+constexpr int kMetaBytes = 128 * kGroups * 8;  // scales and zero points of a stage of every converting thread
+constexpr int kSmemBytes = kActSlots * kActSlot + kCodeSlots * kCodeAtomBytes + 1024 + kBarBytes + kListBytes + 2 * kMetaBytes;
 static_assert(kDqSlots >= kGroups && kDqSlots <= kActSlots && kCodeSlots % kGroups == 0 && kSmemBytes <= kSmemLimit &&
                   8 * (kActSlots + kDqSlots + 2 * kCodeSlots + 5) + 8 <= kBarBytes,
               "ring depths break the barriers' invariants");
 
-__device__ __forceinline__ int row_tiles(int n) { return (n + kRows - 1) / kRows; }
+__device__ __forceinline__ int row_tiles(int n) { return (n + 2 * kRows - 1) / (2 * kRows); }
 
 // 4-D tile load (x innermost).
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
@@ -101,10 +104,11 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
 __device__ __forceinline__ void copy16(uint32_t to, const void* from) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// all but this thread's N most recent groups of copies have landed
-template <int N>
-__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void copy4(uint32_t to, const void* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
+}
+// all of this thread's copies have landed
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 template <bool kB>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -125,9 +129,9 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmW, const TensorParams p)
   auto dq_full = [&](int i) { return bars + 8u * (nact + i); };
   auto code_full = [&](int i) { return bars + 8u * (nact + ndq + i); };
   auto code_empty = [&](int i) { return bars + 8u * (nact + ndq + ncode + i); };
-  // of tile i's accumulator, i & 1; phase i >> 1
-  auto accum_full = [&](int i) { return bars + 8u * (nact + ndq + 2 * ncode + (i & 1)); };
-  auto accum_empty = [&](int i) { return bars + 8u * (nact + ndq + 2 * ncode + 2 + (i & 1)); };  // in the first CTA
+  // of a part's accumulator
+  auto accum_full = [&](int part) { return bars + 8u * (nact + ndq + 2 * ncode + part); };
+  auto accum_empty = [&](int part) { return bars + 8u * (nact + ndq + 2 * ncode + 2 + part); };  // used in the first CTA
   const uint32_t drain_bar = bars + 8u * (nact + ndq + 2 * ncode + 4);  // the MMAs issued before an abort completed
   const uint32_t tmem_slot = drain_bar + 8u;
   uint8_t* gen_base = smem_raw + (base - raw);
@@ -208,8 +212,9 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmW, const TensorParams p)
     const int t = cluster + i * clusters;
     while (firsts[e + 1] <= t) ++e;
     const int n = offs[e + 1] - offs[e], rt = row_tiles(n), local = t - firsts[e];
-    const int size = ((n + rt - 1) / rt + 15) & ~15, row = local % rt * size;
-    return {e, local / rt, offs[e] + row, min(size, n - row), size};
+    const int each = (n + rt - 1) / rt, parts = each > kRows ? 2 : 1;
+    const int size = ((each + parts - 1) / parts + 15) & ~15, row = local % rt * parts * size;
+    return {e, local / rt, offs[e] + row, min(parts * size, n - row), parts, size};
   };
   // the first strip of this CTA in a tile (with silu: of its gate columns)
   auto first_strip = [&](const Tile& t) { return (2 * t.col + (int)rank) * (a.silu ? 4 : 8); };
@@ -247,40 +252,63 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmW, const TensorParams p)
   } else if (warp == 1) {
     if (lane == 0 && rank == 0 && total > 0) {
       // ---------------------------------------------------------- MMA issuer (first CTA)
-      int slot = 0, w = 0, e = 0;
-      uint32_t pw = 0;
-      bool ok = mbar_wait_poll(dq_full(0), 0, abort_flag, kErrMma, a.err);
+      // The walk over the stages: activation slot, dequantized slot and its
+      // phase. A stage's barrier is tested after the MMAs of the one before it.
+      struct Walk {
+        int slot, w;
+        uint32_t phase;
+        __device__ __forceinline__ void step() {
+          slot = slot + 1 == nact ? 0 : slot + 1;
+          w = w + 1 == ndq ? 0 : w + 1;
+          if (w == 0) phase ^= 1u;
+        }
+      };
+      Walk at{0, 0, 0u};
+      int e = 0;
+      bool ok = true;
       for (int tl = 0; tl < ntl && ok; ++tl) {
-        const uint32_t idesc = f16_idesc(2 * kCols, tile_at(tl, e).size, kB);
-        const uint32_t acc = (uint32_t)((tl & 1) * kRows);
-        if (tl > 1 && !(ok = mbar_wait_poll(accum_empty(tl), (uint32_t)((tl >> 1) - 1) & 1u, abort_flag, kErrMma, a.err)))
-          break;
-        const bool more = tl + 1 < ntl;  // another tile's stages follow this tile's last
-        for (int kb = 0; kb < nk && ok; ++kb) {
-          tc_fence_after();
-          const uint32_t bst = base + (uint32_t)slot * kActBytes;
-          const uint32_t acol = tmem_base + (uint32_t)(kDqCol0 + w * kAtomCols);
-          if (!in_smem(bst, kActBytes, raw, a.err) || !in_tmem((uint32_t)(kDqCol0 + w * kAtomCols), kAtomCols, 512, a.err)) {
-            ok = false;
-            break;
-          }
-          const bool next = kb + 1 < nk || more;
-          const int w2 = w + 1 == ndq ? 0 : w + 1;
-          const uint32_t pw2 = w2 == 0 ? pw ^ 1u : pw;
-          bool ready = true;
+        const Tile t = tile_at(tl, e);
+        const uint32_t idesc = f16_idesc(2 * kCols, t.size, kB);
+        const uint32_t phase = (uint32_t)(tl - 1) & 1u;  // of the accumulators' release by the tile before
+        auto ready = [&](const Walk& k) {
+          return mbar_wait_poll(dq_full(k.w), k.phase, abort_flag, kErrMma, a.err);
+        };
+        // the four MMAs (16 k: 8 columns of A, 32 bytes of B) of a part of a stage
+        auto mmas = [&](const Walk& k, int part, bool first) {
+          const uint32_t bst = base + (uint32_t)(k.slot * kActSlot + part * kPartSlot);
+          const uint32_t acol = (uint32_t)(kDqCol0 + k.w * kAtomCols);
+          if (!in_smem(bst, kPartSlot, raw, a.err) || !in_tmem(acol, kAtomCols, 512, a.err)) return;
           const uint64_t bdesc = sw128_kmajor_desc(bst);
 #pragma unroll
-          for (int kk = 0; kk < kStageK / 16; ++kk) {  // 16 k per MMA: 8 columns of A, 32 bytes of B
-            pair_mma_f16_ts(tmem_base + acc, acol + (uint32_t)(8 * kk), bdesc + 2u * kk, idesc, (kb | kk) != 0);
-            if (kk == 1 && next) ready = mbar_test(dq_full(w2), pw2);
-          }
-          pair_commit_both(stage_done(slot));
-          slot = slot + 1 == nact ? 0 : slot + 1;
-          w = w2;
-          pw = pw2;
-          if (next && !ready) ok = mbar_wait_poll(dq_full(w), pw, abort_flag, kErrMma, a.err);
+          for (int kk = 0; kk < kStageK / 16; ++kk)
+            pair_mma_f16_ts(tmem_base + (uint32_t)(part * kRows), tmem_base + acol + (uint32_t)(8 * kk), bdesc + 2u * kk,
+                            idesc, !first || kk != 0);
+        };
+        if (tl > 0 && !(ok = mbar_wait_poll(accum_empty(0), phase, abort_flag, kErrMma, a.err))) break;
+        // after another tile, the first part of the stages that there are slots
+        // for, then the second (no slot is freed in between)
+        const int begin = tl > 0 && t.parts == 2 ? min(nk, ndq) : 0;
+        Walk ahead = at;
+        for (int kb = 0; kb < begin && ok; ++kb, ahead.step()) {
+          if (!(ok = ready(ahead))) break;
+          tc_fence_after();
+          mmas(ahead, 0, kb == 0);
         }
-        if (ok) pair_commit_both(accum_full(tl));  // the tile's accumulator is complete
+        if (ok && begin == nk) pair_commit_both(accum_full(0));
+        if (ok && tl > 0) ok = mbar_wait_poll(accum_empty(1), phase, abort_flag, kErrMma, a.err);
+        for (int kb = 0; kb < begin && ok; ++kb, at.step()) {
+          mmas(at, 1, kb == 0);
+          pair_commit_both(stage_done(at.slot));
+        }
+        for (int kb = begin; kb < nk && ok; ++kb, at.step()) {
+          if (!(ok = ready(at))) break;
+          tc_fence_after();
+          mmas(at, 0, kb == 0);
+          if (kb + 1 == nk) pair_commit_both(accum_full(0));
+          if (t.parts == 2) mmas(at, 1, kb == 0);
+          pair_commit_both(stage_done(at.slot));
+        }
+        if (ok) pair_commit_both(accum_full(1));
       }
       if (!ok) {
         // no MMA may run past the release of tensor memory: one more commit,
@@ -295,7 +323,7 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmW, const TensorParams p)
     // sequence. Thread (lane quarter q, lane) owns tensor-memory lane 32 q +
     // lane: column c = lane % 16 of the CTA's strip 2 q + lane / 16 (with silu:
     // of gate strip q, or up strip q, the CTA's strip 4 + q).
-    const int dw = warp - 2;
+    const int dw = warp - kFirst;
     const int grp_id = dw >> 2;
     const int q = warp & 3;
     const int ls = a.silu ? q + 4 * (lane >> 4) : 2 * q + (lane >> 4);
@@ -310,53 +338,14 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmW, const TensorParams p)
     if (!a.combine)
       for (int i = offs[a.E] + (int)blockIdx.x; i < choices(a); i += gridDim.x) {
         const int f = choice_of(a, i);
-        for (int n = threadIdx.x - 64; f >= 0 && n < width; n += 128 * kGroups) {
+        for (int n = threadIdx.x - 32 * kFirst; f >= 0 && n < width; n += 128 * kGroups) {
           uint16_t* y = a.Y + (size_t)f * width + n;
           if (in_buf(y, a.Y, (size_t)choices(a) * width, a.err)) *y = 0;
         }
       }
 
-    // the strip of this lane in a tile, of all experts' strips; -1: beyond the columns
-    auto strip_of = [&](const Tile& t) {
-      const int s = first_strip(t) + (a.silu ? q : ls);
-      return s < limit ? t.e * strips + s + (a.silu && lane >= 16 ? limit : 0) : -1;
-    };
-    // scale and zero point of this column for a stage, in order, kGroups stages
-    // apart (taken apart where they are used: their loads are in flight until then)
-    int mi = grp_id, me = 0;
-    SeqPos mseq{grp_id, 0};
-    mseq.step(0, nk);
-    int mstrip = mi < total ? strip_of(tile_at(mseq.tile, me)) : -1;
-    int mgrp = mseq.kb * kStageK / a.group;
-    int mgend = (mgrp + 1) * a.group;
-    struct Meta {
-      uint16_t s;  // scale bits
-      uint8_t z;   // the zero points of columns cp and cp + 8
-    };
-    auto load_meta = [&]() -> Meta {
-      Meta v = {0, 0};
-      if (mi < total && mstrip >= 0) {
-        const size_t pg = (size_t)mstrip * G + mgrp;
-        const uint8_t* zp = reinterpret_cast<const uint8_t*>(a.Zp);
-        v.s = __ldg(ld_at(a.Sp + pg * 16 + 2 * cp + (hi ? 1 : 0), a.Sp, (size_t)G * a.N * a.E, a.err));
-        v.z = __ldg(ld_at(zp + pg * 8 + cp, zp, (size_t)G * a.N / 2 * a.E, a.err));
-      }
-      mi += kGroups;
-      const int tl = mseq.tile;
-      mseq.step(kGroups, nk);
-      if (mseq.tile != tl) {
-        if (mi < total) mstrip = strip_of(tile_at(mseq.tile, me));
-        mgrp = 0;
-        mgend = a.group;
-      }
-      while (mseq.kb * kStageK >= mgend) {
-        ++mgrp;
-        mgend += a.group;
-      }
-      return v;
-    };
-    const uint32_t dq_remote0 = cluster_addr(dq_full(0), 0);     // the first CTA's dq_full(0)
-    const uint32_t empty_remote = cluster_addr(accum_empty(0), 0);  // the first CTA's accum_empty(0)
+    const uint32_t dq_remote = cluster_addr(dq_full(grp_id), 0);       // the first CTA's dq_full of this group's slot
+    const uint32_t empty_remote = cluster_addr(accum_empty(0), 0);     // the first CTA's accum_empty(0)
     // a wait that every lane of the warp passes or every lane gives up on:
     // the tensor-memory stores and loads that follow are .sync.aligned
     auto warp_wait = [&](uint32_t bar, uint32_t parity, bool poll, int code) -> bool {
@@ -364,73 +353,84 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmW, const TensorParams p)
                            : mbar_wait(bar, parity, abort_flag, code, a.err);
       return __all_sync(0xffffffffu, ok);
     };
-    // the rows of the group's stages: this warp copies those of steps q, q + 4,
-    // ... (step i: rows 4 i .. 4 i + 3 of this CTA's half), this lane the 16
-    // bytes lane % 8 of row 4 i + lane / 8. aseq: the next stage to copy.
+
+    // The group's stages are grp_id, grp_id + 4, ...: its it-th stage has the
+    // code slot and the dequantized slot grp_id, and the activation slots
+    // grp_id and grp_id + 4 in turn. `next` is the stage whose rows and scales
+    // are fetched while the one before it is converted: its place, its tile's
+    // expert, this lane's strip of all experts' strips (-1: beyond the
+    // columns), the group of its scale and the k where the group after it
+    // starts, and the rows.
+    static_assert(ncode == kGroups && ndq == kGroups && nact == 2 * kGroups, "slots by the group's number alone");
+    SeqPos next{grp_id, 0};
+    next.step(0, nk);
+    int ne = 0, nstrip = -1, ngrp = next.kb * kStageK / a.group, ngend = (ngrp + 1) * a.group;
+    // Rows: of each part this warp copies those of steps q, q + 4, ... (step
+    // i: rows 4 i .. 4 i + 3 of this CTA's half of it), a lane the 16 bytes lane
+    // % 8 of row lane / 8 of each; lane 4 j + r holds which row of A is the
+    // r-th of the warp's j-th step, held[part].
     constexpr int kSteps = kRows / 2 / 16;
-    int rows[kSteps];  // in A
-    int ai = grp_id, ae = 0, ahalf = 0;
-    SeqPos aseq{grp_id, 0};
-    aseq.step(0, nk);
-    RingPos apos;
-    apos.init(grp_id, nact);
-    const size_t a_all = a_elements(a) - 7;
+    static_assert(4 * kSteps <= 32, "a row per lane");
+    int held[2] = {0, 0}, half = 0;  // half: of a part's rows; minus that with one part
+    auto enter_tile = [&]() {
+      const Tile t = tile_at(next.tile, ne);
+      const int st = first_strip(t) + (a.silu ? q : ls);
+      nstrip = st < limit ? t.e * strips + st + (a.silu && lane >= 16 ? limit : 0) : -1;
+      half = t.size / 2;
+      const int i = 4 * (q + lane / 4 * 4) + lane % 4;
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {
+        if (part == t.parts) break;
+        const int f = choice_of(a, t.first + min(part * t.size + (int)rank * half + min(i, half - 1), t.n - 1));
+        held[part] = f < 0 ? 0 : a.per_choice ? f : f / a.top;
+      }
+      if (t.parts == 1) half = -half;
+    };
+    // the lane's scale and zero point words of a stage, in shared memory by the
+    // stage's parity: scales of columns cp and cp + 8, and zero points of columns
+    // cp & 4 .. (cp & 4) + 3, each with its column + 8
+    const uint32_t meta0 = bars + kBarBytes + kListBytes + (uint32_t)(dw * 32 + lane) * 8u;
+    auto copy_meta = [&](int it) {
+      if (nstrip < 0) return;
+      const size_t pg = (size_t)nstrip * G + ngrp;
+      const uint32_t* sp = reinterpret_cast<const uint32_t*>(a.Sp);
+      const uint32_t to = meta0 + (uint32_t)(it & 1) * kMetaBytes;
+      copy4(to, ld_at(sp + pg * 8 + cp, sp, (size_t)G * a.N * a.E / 2, a.err));
+      copy4(to + 4, ld_at(a.Zp + pg * 2 + cp / 4, a.Zp, (size_t)G * a.N * a.E / 8, a.err));
+    };
     // chunk lane % 8 of row lane / 8 of a step, swizzled by the row's number in
     // its group of eight: 4 (i & 1) + lane / 8, and i is as odd as q
     const uint32_t place = (uint32_t)q * 512u + (uint32_t)(lane / 8) * 128u +
                            (uint32_t)((lane % 8) ^ (lane / 8 + 4 * (q & 1))) * 16u;
-    auto load_rows = [&]() {
-      const Tile t = tile_at(aseq.tile, ae);
-      ahalf = t.size / 2;
+    auto copy_rows = [&](int it) {  // of the group's it-th stage
+      const uint32_t to = base + (uint32_t)(grp_id + (it & 1) * kGroups) * kActBytes + place;
+      const char* from = reinterpret_cast<const char*>(a.A + next.kb * kStageK + lane % 8 * 8);
+      const uint32_t pitch = 2u * (uint32_t)a.K;  // bytes of a row
+      const int rows = abs(half);
 #pragma unroll
-      for (int j = 0; j < kSteps; ++j) {
-        const int i = 4 * (q + 4 * j) + lane / 8;
-        if (i < ahalf) {
-          const int f = choice_of(a, t.first + min((int)rank * ahalf + i, t.n - 1));
-          rows[j] = f < 0 ? 0 : a.per_choice ? f : f / a.top;
+      for (int part = 0; part < 2; ++part) {
+        if (part == 1 && half < 0) break;
+        uint32_t row[kSteps];
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j) row[j] = (uint32_t)__shfl_sync(0xffffffffu, held[part], 4 * j + lane / 8);
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j) {
+          const uint32_t dst = to + (uint32_t)part * kPartSlot + 2048u * j;
+          const uint16_t* src = reinterpret_cast<const uint16_t*>(from + (uint64_t)row[j] * pitch);
+          if (4 * (q + 4 * j) < rows && in_smem(dst, 16, raw, a.err))
+            copy16(dst, ld_at(src, a.A, a_elements(a) - 7, a.err));
         }
       }
     };
-    auto copy_rows = [&]() {
-      if (ai < total) {
-        const uint32_t to = base + (uint32_t)apos.slot * kActBytes + place;
-        const uint16_t* from = a.A + aseq.kb * kStageK + lane % 8 * 8;
-#pragma unroll
-        for (int j = 0; j < kSteps; ++j)
-          if (4 * (q + 4 * j) < ahalf && in_smem(to + 2048u * j, 16, raw, a.err))
-            copy16(to + 2048u * j, ld_at(from + (size_t)rows[j] * a.K, a.A, a_all, a.err));
-        ai += kGroups;
-        apos.step(kGroups, nact);
-        const int tl = aseq.tile;
-        aseq.step(kGroups, nk);
-        if (aseq.tile != tl && ai < total) load_rows();
-      }
-      copies_commit();
-    };
-    constexpr int kAhead = nact - ndq;  // stages: the slot of stage s + kAhead was that of stage s - ndq
-    static_assert(kAhead == 2 * kGroups, "two groups of copies are in flight beside a stage's own");
-    if (ai < total) load_rows();
-    copy_rows();
-    copy_rows();
-    RingPos spos_code, spos_act;
-    spos_code.init(grp_id, ncode);
-    spos_act.init(grp_id, nact);
-    int sw = grp_id % ndq;
-    SeqPos sseq{grp_id, 0};
-    sseq.step(0, nk);
-    int stile = 0;  // the tile of the stage converted last
-    auto stage = [&](int s, const Meta& meta) -> bool {
-      const int cs = spos_code.slot, w = sw;
-      const uint32_t code_par = spos_code.phase;
-      const RingPos prev = spos_act.before(ndq, nact);  // stage s - dq_slots (dq_slots <= act_slots)
-      stile = sseq.tile;
-      spos_code.step(kGroups, ncode);
-      spos_act.step(kGroups, nact);
-      sw += kGroups;
-      while (sw >= ndq) sw -= ndq;
-      sseq.step(kGroups, nk);
-      if (!warp_wait(code_full(cs), code_par, false, kErrDequant)) return false;
-      const uint32_t cb = code_base + (uint32_t)cs * kCodeBytes;
+    // converts the group's it-th stage and copies the rows of the one after it
+    auto stage = [&](int it, bool more) -> bool {
+      // this warp's rows of the stage (the MMAs read them too), and its scales
+      copies_wait();
+      fence_async_shared();  // (the copies wrote them through the generic proxy)
+      uint32_t mscale, mzero;
+      asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(mscale), "=r"(mzero) : "r"(meta0 + (uint32_t)(it & 1) * kMetaBytes) : "memory");
+      if (!warp_wait(code_full(grp_id), (uint32_t)it & 1u, false, kErrDequant)) return false;
+      const uint32_t cb = code_base + (uint32_t)grp_id * kCodeBytes;
       uint32_t wl[4], wh[4];  // k-octets l and 4 + l
       const uint32_t row = (uint32_t)(ls * 4 + (cp >> 1));  // 128-byte row of the tile
 #pragma unroll
@@ -442,9 +442,9 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmW, const TensorParams p)
         wh[l] = hi ? v.w : v.z;
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(code_empty(cs));  // the codes are in registers
-      const uint32_t z = ((uint32_t)meta.z >> (hi ? 4 : 0)) & 15u;
-      const uint16_t sc = meta.s;
+      if (lane == 0) mbar_arrive(code_empty(grp_id));  // the codes are in registers
+      const uint32_t z = (mzero >> (8 * (cp & 3) + (hi ? 4 : 0))) & 15u;
+      const uint16_t sc = (uint16_t)(mscale >> (hi ? 16 : 0));
       uint32_t r[32];  // cell j = (deq[2j], deq[2j + 1]): k-octet o fills cells 4o..4o+3
 #pragma unroll
       for (int l = 0; l < 4; ++l) {
@@ -464,115 +464,148 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmW, const TensorParams p)
           r[16 + 4 * l + j] = o1[j];
         }
       }
-      // (the slot is waited for with the cells in registers: what is between its
-      // last MMA and its next is then the store alone)
-      if (s >= ndq) {
-        if (!warp_wait(stage_done(prev.slot), prev.phase, true, kErrDequant)) return false;
+      // the slot's MMAs, of the group's stage before, are done (waited for with
+      // the cells in registers: what is between them and the slot's next MMAs is
+      // then the store alone)
+      if (it > 0) {
+        if (!warp_wait(stage_done(grp_id + ((it - 1) & 1) * kGroups), (uint32_t)((it - 1) >> 1) & 1u, true, kErrDequant))
+          return false;
         tc_fence_after();
       }
-      copy_rows();  // of stage s + kAhead, to the slot of the stage waited for
-      if (in_tmem((uint32_t)(kDqCol0 + w * kAtomCols), kAtomCols, 512, a.err))
-        tmem_st32(tmem_base + tlane + (uint32_t)(kDqCol0 + w * kAtomCols), r);
+      const uint32_t col = (uint32_t)(kDqCol0 + grp_id * kAtomCols);
+      if (in_tmem(col, kAtomCols, 512, a.err)) tmem_st32(tmem_base + tlane + col, r);
+      if (more) {  // the stage after it, to the slot of the stage waited for
+        copy_meta(it + 1);
+        copy_rows(it + 1);
+      }
       tmem_wait_st();
-      // this warp's rows of the stage have landed (the MMAs read them too)
-      copies_wait<2>();
-      fence_async_shared();  // (the copies wrote them through the generic proxy)
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_remote(dq_remote0 + 8u * w);
+      if (lane == 0) mbar_arrive_remote(dq_remote);
       return true;
     };
-    // the epilogue of this warp: tensor-memory lanes 32q..32q+31 are this CTA's
-    // columns, an accumulator's columns the tile's rows, 16 at a time by the
-    // groups in turn. done: the tiles that the warp has finished; of the next
-    // one, et and the group's next chunk of 16 rows, of which lane l (and 16 +
-    // l) holds row l's choice and weight.
-    int done = 0, ee = 0, chunk = 0, of = -1;
-    float factor = 1.f;
-    Tile et{};
-    auto load_chunk = [&]() {
-      const int r = 16 * chunk + (lane & 15);
-      of = r < et.n ? choice_of(a, et.first + r) : -1;
-      if (a.combine) factor = of >= 0 ? *ld_at(a.weights + of, a.weights, (size_t)choices(a), a.err) : 1.f;
-    };
-    auto begin_tile = [&]() {
-      if (done >= ntl) return;
-      et = tile_at(done, ee);
-      chunk = grp_id;
-      load_chunk();
-    };
-    // the tile's next chunk; the tile's accumulator is complete
+    // this warp's part of tile i's epilogue: tensor-memory lanes 32q..32q+31
+    // are this CTA's columns, an accumulator's columns the rows of a part, 16
+    // at a time by the groups in turn
+    constexpr int kChunks = kRows / 16 / kGroups;
+    int ee = 0;
     uint16_t* out = a.combine ? p.D : a.Y;
-    const size_t all = (size_t)choices(a) * width;
-    auto store_chunk = [&]() {
-      if (16 * chunk < et.n) {
-        const uint32_t col = (uint32_t)((done & 1) * kRows + 16 * chunk);
-        const int s = first_strip(et) + (a.silu ? q : ls);
-        const bool live = s < limit;
-        uint16_t* to = out + s * kStripCols + c;
-        uint32_t r[16];
+    const size_t all = (size_t)choices(a) * width - 1;
+    auto epilogue = [&](int i) -> bool {
+      const Tile t = tile_at(i, ee);
+      const int s = first_strip(t) + (a.silu ? q : ls);
+      const bool live = s < limit;
+      // two neighbouring columns at a time: even lanes finish one row, odd
+      // lanes the next, of which each gives the other its own column
+      char* to = reinterpret_cast<char*>(out + s * kStripCols + (c & ~1));
+      const bool odd = lane & 1;
+      // the choices of the warp's chunks and their weights, on their way while
+      // it waits: lane l holds row l of a part's first (0) and third (1) chunk,
+      // lane 16 + l that of the second
+      int of[2][2];
+      float factor[2][2];
+#pragma unroll
+      for (int part = 0; part < 2; ++part)
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const int k = 16 * (grp_id + (2 * m + lane / 16) * kGroups) + lane % 16;
+          of[part][m] = k < t.size && part * t.size + k < t.n && part < t.parts ? choice_of(a, t.first + part * t.size + k) : -1;
+        }
+#pragma unroll
+      for (int part = 0; part < 2; ++part)
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+          factor[part][m] =
+              a.combine && of[part][m] >= 0 ? *ld_at(a.weights + of[part][m], a.weights, (size_t)choices(a), a.err) : 1.f;
+      static_assert(kChunks <= 4, "two registers of rows");
+      for (int part = 0; part < 2; ++part) {
+        const int n = part < t.parts ? min(t.size, t.n - part * t.size) : 0;
+        if (!warp_wait(accum_full(part), (uint32_t)i & 1u, true, kErrEpilogue)) return false;
         tc_fence_after();
-        if (in_tmem(col, 16, kDqCol0, a.err)) tmem_ld16(tmem_base + tlane + col, r);
-        tmem_wait_ld();
-        if (a.silu) {
-          // lanes 0..15 finish rows 0..7 of the chunk, lanes 16..31 rows 8..15
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const uint32_t other = __shfl_xor_sync(0xffffffffu, lane < 16 ? r[k + 8] : r[k], 16);
-            const float g = __uint_as_float(lane < 16 ? r[k] : other);
-            const float u = __uint_as_float(lane < 16 ? other : r[k + 8]);
-            const int f = __shfl_sync(0xffffffffu, of, k + (lane < 16 ? 0 : 8));
-            uint16_t* y = to + (size_t)f * width;
-            if (f >= 0 && live && in_buf(y, out, all, a.err)) *y = to_out<kB>(silu_times(g, u));
+#pragma unroll 1
+        for (int j = 0; j < kChunks; ++j) {
+          const int row0 = 16 * (grp_id + j * kGroups);
+          uint32_t r[16];
+          const uint32_t col = (uint32_t)(part * kRows + row0);
+          if (row0 < n && in_tmem(col, 16, kDqCol0, a.err)) tmem_ld16(tmem_base + tlane + col, r);
+          tmem_wait_ld();
+          if (j + 1 == kChunks) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(empty_remote + 8u * part);
           }
-        } else {
+          if (row0 >= n) continue;
+          const int chosen = part ? (j > 1 ? of[1][1] : of[1][0]) : (j > 1 ? of[0][1] : of[0][0]);
+          const float weight = part ? (j > 1 ? factor[1][1] : factor[1][0]) : (j > 1 ? factor[0][1] : factor[0][0]);
+          auto store = [&](int row, float lo, float hi) {
+            const int f = __shfl_sync(0xffffffffu, chosen, row + j % 2 * 16);
+            if (a.combine) {
+              const float w = __shfl_sync(0xffffffffu, weight, row + j % 2 * 16);
+              lo *= w, hi *= w;
+            }
+            uint16_t* y = reinterpret_cast<uint16_t*>(to + (uint64_t)(uint32_t)f * (2u * (uint32_t)width));
+            if (f >= 0 && live && in_buf(y, out, all, a.err)) *reinterpret_cast<uint32_t*>(y) = to_out2<kB>(lo, hi);
+          };
+          if (a.silu) {
+            // lanes 0..15 finish rows 0..7 of the chunk, lanes 16..31 rows 8..15
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const int f = __shfl_sync(0xffffffffu, of, k);
-            const float w = a.combine ? __shfl_sync(0xffffffffu, factor, k) : 1.f;
-            uint16_t* y = to + (size_t)f * width;
-            if (f >= 0 && live && in_buf(y, out, all, a.err)) *y = to_out<kB>(__uint_as_float(r[k]) * w);
+            for (int k = 0; k < 8; k += 2) {
+              float v[2];
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t other = __shfl_xor_sync(0xffffffffu, lane < 16 ? r[k + h + 8] : r[k + h], 16);
+                const float g = __uint_as_float(lane < 16 ? r[k + h] : other);
+                const float u = __uint_as_float(lane < 16 ? other : r[k + h + 8]);
+                v[h] = silu_times(g, u);
+              }
+              const float other = __shfl_xor_sync(0xffffffffu, odd ? v[0] : v[1], 1);
+              store(k + (odd ? 1 : 0) + (lane < 16 ? 0 : 8), odd ? other : v[0], odd ? v[1] : other);
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 16; k += 2) {
+              const float v0 = __uint_as_float(r[k]), v1 = __uint_as_float(r[k + 1]);
+              const float other = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
+              store(k + (odd ? 1 : 0), odd ? other : v0, odd ? v1 : other);
+            }
           }
         }
       }
-      chunk += kGroups;
-      if (16 * chunk < et.n) {
-        load_chunk();
-      } else {  // the warp has read all it reads of this accumulator
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_remote(empty_remote + 8u * (done & 1));
-        ++done;
-        begin_tile();
-      }
+      return true;
     };
-    auto wait_tile = [&]() { return warp_wait(accum_full(done), (uint32_t)(done >> 1) & 1u, true, kErrEpilogue); };
-    // scales and zero points, loaded two of this group's stages before their own
-    Meta m0s = load_meta(), m1s = load_meta();
-    begin_tile();
     bool ok = true;
-    for (int s = grp_id; s < total && ok; s += kGroups) {
-      const Meta m2s = load_meta();  // stage s + 2 groups
-      while (ok && done + 1 < sseq.tile)
-        if ((ok = wait_tile())) store_chunk();
-      if (ok) ok = stage(s, m0s);
-      // a chunk of an earlier tile, if its accumulator is complete
-      if (ok && done < stile &&
-          __all_sync(0xffffffffu, mbar_test(accum_full(done), (uint32_t)(done >> 1) & 1u)))
-        store_chunk();
-      m0s = m1s;
-      m1s = m2s;
+    int done = 0;  // the tiles whose epilogue this warp has done: [0, done)
+    if (grp_id < total) {
+      enter_tile();
+      copy_meta(0);
+      copy_rows(0);
     }
-    while (ok && done < ntl)
-      if ((ok = wait_tile())) store_chunk();
-    copies_wait<0>();
+    for (int s = grp_id, it = 0; s < total && ok; s += kGroups, ++it) {
+      const int tile = next.tile;
+      const bool more = s + kGroups < total;
+      next.step(kGroups, nk);
+      if (more && next.tile != tile) {
+        enter_tile();
+        ngrp = 0;
+        ngend = a.group;
+      }
+      while (next.kb * kStageK >= ngend) {
+        ++ngrp;
+        ngend += a.group;
+      }
+      ok = stage(it, more);
+      // the epilogues of the tiles before the converted stage's tile
+      for (; ok && done < tile; ++done) ok = epilogue(done);
+    }
+    for (; ok && done < ntl; ++done) ok = epilogue(done);
+    copies_wait();
   }
 
   // the pair's last commit has landed here before the CTA can leave: the last
   // tile's accumulator commit in a normal run (already waited for by the
   // epilogue), the drain commit after an abort
-  if (threadIdx.x == 64 && ntl > 0) {
-    if (*abort_flag == 0) mbar_drain(accum_full(ntl - 1), (uint32_t)((ntl - 1) >> 1) & 1u, a.err);
+  if (threadIdx.x == 32 * kFirst && ntl > 0) {
+    if (*abort_flag == 0) mbar_drain(accum_full(1), (uint32_t)(ntl - 1) & 1u, a.err);
     else mbar_drain(drain_bar, 0, a.err);
   }
   __syncwarp();
@@ -611,7 +644,7 @@ cudaError_t launch(const CUtensorMap& tmW, TensorParams p, cudaStream_t stream) 
   if (e != cudaSuccess) return e;
   // persistent: no more clusters than there can be tiles
   const ExpertArgs& a = p.a;
-  const long long most = (long long)(choices(a) / kRows + (choices(a) < a.E ? choices(a) : a.E)) * p.pairs;
+  const long long most = (long long)(choices(a) / (2 * kRows) + (choices(a) < a.E ? choices(a) : a.E)) * p.pairs;
   cfg.gridDim = dim3((unsigned)(2 * (most < resident ? most : resident)), 1, 1);
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, experts_tc_kernel<kB>, tmW, p);
