@@ -107,6 +107,12 @@ __device__ __forceinline__ void copy16(uint32_t to, const void* from) {
 __device__ __forceinline__ void copy4(uint32_t to, const void* from) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
 }
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+  return ok != 0;
+}
 // all of this thread's copies have landed
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
@@ -250,35 +256,29 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmW, const TensorParams p)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0 && total > 0) {
+    if (rank == 0 && total > 0 && elect_one()) {
       // ---------------------------------------------------------- MMA issuer (first CTA)
-      // The walk over the stages: activation slot, dequantized slot and its
-      // phase. A stage's barrier is tested after the MMAs of the one before it.
-      struct Walk {
-        int slot, w;
-        uint32_t phase;
-        __device__ __forceinline__ void step() {
-          slot = slot + 1 == nact ? 0 : slot + 1;
-          w = w + 1 == ndq ? 0 : w + 1;
-          if (w == 0) phase ^= 1u;
-        }
-      };
-      Walk at{0, 0, 0u};
+      // (an elected lane of a converged warp: the operands' places then stay in
+      // uniform registers, and an MMA takes few instructions to issue)
+      // stage n of the sequence has activation slot n & 7 and dequantized slot n & 3
+      static_assert(nact == 8 && ndq == 4, "slots by the stage's number alone");
+      const uint64_t bdesc0 = sw128_kmajor_desc(base);
+      int n = 0;
       int e = 0;
       bool ok = true;
       for (int tl = 0; tl < ntl && ok; ++tl) {
         const Tile t = tile_at(tl, e);
         const uint32_t idesc = f16_idesc(2 * kCols, t.size, kB);
         const uint32_t phase = (uint32_t)(tl - 1) & 1u;  // of the accumulators' release by the tile before
-        auto ready = [&](const Walk& k) {
-          return mbar_wait_poll(dq_full(k.w), k.phase, abort_flag, kErrMma, a.err);
+        auto ready = [&](int i) {
+          return mbar_wait_poll(dq_full(i & 3), (uint32_t)(i >> 2) & 1u, abort_flag, kErrMma, a.err);
         };
         // the four MMAs (16 k: 8 columns of A, 32 bytes of B) of a part of a stage
-        auto mmas = [&](const Walk& k, int part, bool first) {
-          const uint32_t bst = base + (uint32_t)(k.slot * kActSlot + part * kPartSlot);
-          const uint32_t acol = (uint32_t)(kDqCol0 + k.w * kAtomCols);
-          if (!in_smem(bst, kPartSlot, raw, a.err) || !in_tmem(acol, kAtomCols, 512, a.err)) return;
-          const uint64_t bdesc = sw128_kmajor_desc(bst);
+        auto mmas = [&](int i, int part, bool first) {
+          const uint32_t place = (uint32_t)((i & 7) * kActSlot + part * kPartSlot);
+          const uint32_t acol = (uint32_t)(kDqCol0 + (i & 3) * kAtomCols);
+          if (!in_smem(base + place, kPartSlot, raw, a.err) || !in_tmem(acol, kAtomCols, 512, a.err)) return;
+          const uint64_t bdesc = bdesc0 + (place >> 4);
 #pragma unroll
           for (int kk = 0; kk < kStageK / 16; ++kk)
             pair_mma_f16_ts(tmem_base + (uint32_t)(part * kRows), tmem_base + acol + (uint32_t)(8 * kk), bdesc + 2u * kk,
@@ -288,25 +288,24 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmW, const TensorParams p)
         // after another tile, the first part of the stages that there are slots
         // for, then the second (no slot is freed in between)
         const int begin = tl > 0 && t.parts == 2 ? min(nk, ndq) : 0;
-        Walk ahead = at;
-        for (int kb = 0; kb < begin && ok; ++kb, ahead.step()) {
-          if (!(ok = ready(ahead))) break;
+        for (int kb = 0; kb < begin && ok; ++kb) {
+          if (!(ok = ready(n + kb))) break;
           tc_fence_after();
-          mmas(ahead, 0, kb == 0);
+          mmas(n + kb, 0, kb == 0);
         }
         if (ok && begin == nk) pair_commit_both(accum_full(0));
         if (ok && tl > 0) ok = mbar_wait_poll(accum_empty(1), phase, abort_flag, kErrMma, a.err);
-        for (int kb = 0; kb < begin && ok; ++kb, at.step()) {
-          mmas(at, 1, kb == 0);
-          pair_commit_both(stage_done(at.slot));
+        for (int kb = 0; kb < begin && ok; ++kb, ++n) {
+          mmas(n, 1, kb == 0);
+          pair_commit_both(stage_done(n & 7));
         }
-        for (int kb = begin; kb < nk && ok; ++kb, at.step()) {
-          if (!(ok = ready(at))) break;
+        for (int kb = begin; kb < nk && ok; ++kb, ++n) {
+          if (!(ok = ready(n))) break;
           tc_fence_after();
-          mmas(at, 0, kb == 0);
+          mmas(n, 0, kb == 0);
           if (kb + 1 == nk) pair_commit_both(accum_full(0));
-          if (t.parts == 2) mmas(at, 1, kb == 0);
-          pair_commit_both(stage_done(at.slot));
+          if (t.parts == 2) mmas(n, 1, kb == 0);
+          pair_commit_both(stage_done(n & 7));
         }
         if (ok) pair_commit_both(accum_full(1));
       }
@@ -474,14 +473,14 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmW, const TensorParams p)
       }
       const uint32_t col = (uint32_t)(kDqCol0 + grp_id * kAtomCols);
       if (in_tmem(col, kAtomCols, 512, a.err)) tmem_st32(tmem_base + tlane + col, r);
-      if (more) {  // the stage after it, to the slot of the stage waited for
-        copy_meta(it + 1);
-        copy_rows(it + 1);
-      }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_remote(dq_remote);
+      if (more) {  // the stage after it, to the slot of the stage waited for
+        copy_meta(it + 1);
+        copy_rows(it + 1);
+      }
       return true;
     };
     // this warp's part of tile i's epilogue: tensor-memory lanes 32q..32q+31
