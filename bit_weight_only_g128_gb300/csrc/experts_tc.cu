@@ -11,37 +11,41 @@
 // its 128 columns, RNE((q - z) s) in the activations' type, straight into
 // tensor memory (the MMA's A operand) and staging half of the rows (the B
 // operand). What differs:
-//   - A tile has up to 384 rows in two parts of up to 192, each with its own
-//     accumulator: a dequantized atom serves both, so that conversions, whose
-//     instructions bound the kernel below that, take half as many per row.
-//     An expert's n rows make ceil(n / 384) tiles of the same size, and the
-//     MMA's N is a part's size, rounded up to 16: an expert of 40 rows costs
-//     MMAs of 48. Which tiles there are is known on the device only: every CTA
-//     makes the list of the experts' first tiles from the offsets when it
-//     starts, and each role walks it (a cluster's tiles ascend).
-//   - The rows are gathered by the converting warps: the group that will
-//     convert a stage copies the stage's rows one of its stages before
-//     (cp.async, eight lanes a row of 128 bytes, to the swizzled places), and
-//     each of its warps waits for its own copies before it arrives for the
-//     stage. (tile::gather4 copies by the lanes of one warp took about 95
-//     cycles each, one warp's cp.async about 85: the MMAs waited for rows most
-//     of the time.) Places beyond a tile's rows repeat its last row; their
-//     results are not stored.
+//   - A tile has up to 256 rows in one or two parts of up to 128, each with
+//     its own accumulator. An expert's n rows make ceil(n / 256) tiles of the
+//     same size, and the MMA's N is a part's size, rounded up to 16: an expert
+//     of 40 rows costs MMAs of 48. Which tiles there are is known on the device
+//     only: every CTA makes the list of the experts' first tiles from the
+//     offsets when it starts, and each role walks it (a cluster's tiles
+//     ascend).
+//   - The rows are gathered by the converting warps: while a group converts
+//     a stage it copies the stage's rows (cp.async, eight lanes a row of 128
+//     bytes, to the swizzled places), and each of its warps waits for its own
+//     copies before it arrives for the stage. (tile::gather4 copies by the lanes
+//     of one warp took about 95 cycles each, one warp's cp.async about 85: the
+//     MMAs waited for rows most of the time.) Places beyond a tile's rows repeat
+//     its last row; their results are not stored.
 //   - With silu(gate) * up a CTA's eight strips are four of gate columns and
 //     the four of up columns beside them (one 4-D copy), placed so that a
 //     warp's lanes 0..15 hold gate and 16..31 up of the same 16 results: one
 //     shuffle per two results brings them together in fp32, and the output is
 //     half as wide.
 //   - K is short (an expert's inner width), so that a tile's end matters: the
-//     converting warps take a part's accumulator to registers, hand it back
-//     and only then convert and store, one part after the other. The next
-//     tile begins with the first part's MMAs of the stages that are converted
-//     already, and catches up with the second part's when its accumulator is
-//     free.
+//     converting warps hand the first part's accumulator back before they take
+//     the second's, and the next tile begins with the first part's MMAs of the
+//     stages that are converted already, to catch up with the second part's
+//     when its accumulator is free.
+// What bounds it is the converting warps' issue slots, so a stage is two atoms
+// (of the last one only what K has), and nothing is spilled: the first-level
+// cache beside 214 KB of shared memory is too small for it, and each spilled
+// value cost a trip to L2.
+//
 // Rings, barriers and their invariants are those of tc_pair.cu, without a
-// barrier for the rows' arrival. A stage is one atom. Every wait is
-// bounded; a wait that gives up sets the library's error word, and its CTA
-// drains and leaves through the same final cluster barrier as a normal run.
+// barrier for the rows' arrival. What a group waits for before it converts stage
+// s are the MMAs of stages s - 5 (the rows' slot) and s - 4 (the dequantized
+// slot), which need no accumulator that the group has still to hand back. Every
+// wait is bounded; a wait that gives up sets the library's error word, and its
+// CTA drains and leaves through the same final cluster barrier as a normal run.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -57,12 +61,13 @@ using namespace pair;
 constexpr int kGroups = 4;                  // dequantizing groups of four warps
 constexpr int kFirst = 2;                   // the first converting warp, after producer and MMA issuer
 constexpr int kThreads = 32 * kFirst + 128 * kGroups;
-constexpr int kRows = 192;                  // most rows of a part (MMA N); a tile has two
-constexpr int kMostExperts = 512;
+constexpr int kRows = 128;                  // most rows of a part (MMA N); a tile has two
+constexpr int kAtoms = 2;                   // 64-k atoms of a stage
 constexpr int kPartSlot = kRows / 2 * 128;  // bytes of a CTA's rows of one atom of a part, at most
-constexpr int kActSlot = 2 * kPartSlot;
-// the list of tiles in shared memory: offsets and first tiles [E + 1] each
-constexpr int kListBytes = ((kMostExperts + 1) * 8 + 127) / 128 * 128;
+constexpr int kAtomSlot = 2 * kPartSlot;
+constexpr int kActSlot = kAtoms * kAtomSlot;
+constexpr int kCodeSlot = kAtoms * kCodeAtomBytes;
+constexpr int kMostExperts = 512;
 
 struct TensorParams {
   ExpertArgs a;
@@ -77,17 +82,13 @@ struct Tile {
   int e, col, first, n, parts, size;
 };
 
-// Ring depths per CTA (a stage is an atom): the dequantized operand in the
-// tensor memory beside the accumulators, four slots; the rows four stages
-// deeper, which is how far ahead a group copies them (8 slots of 24 KiB); codes
-// four. The invariants of tc_pair.cu: at least as many dequantized slots as
-// groups, no more than activation slots, code slots a multiple of the groups.
-constexpr int kActSlots = 8, kCodeSlots = 4, kDqSlots = (512 - 2 * kRows) / kAtomCols;
-constexpr int kMetaBytes = 128 * kGroups * 8;  // scales and zero points of a stage of every converting thread
-constexpr int kSmemBytes = kActSlots * kActSlot + kCodeSlots * kCodeAtomBytes + 1024 + kBarBytes + kListBytes + 2 * kMetaBytes;
-static_assert(kDqSlots >= kGroups && kDqSlots <= kActSlots && kCodeSlots % kGroups == 0 && kSmemBytes <= kSmemLimit &&
-                  8 * (kActSlots + kDqSlots + 2 * kCodeSlots + 5) + 8 <= kBarBytes,
-              "ring depths break the barriers' invariants");
+// Ring depths per CTA: the dequantized operand in the tensor memory beside the
+// accumulators, four slots, one per group; codes four; the rows five.
+constexpr int kActSlots = 5, kCodeSlots = 4, kDqSlots = (512 - 2 * kRows) / (kAtoms * kAtomCols);
+static_assert(kDqSlots == kGroups && kCodeSlots == kGroups && kActSlots == kGroups + 1, "slots by the group's number");
+constexpr int kMetaBytes = 128 * kGroups * 8 * kAtoms;  // scales and zero points of every converting thread
+constexpr int kSmemBytes = kActSlots * kActSlot + kCodeSlots * kCodeSlot + 1024 + kBarBytes + kMetaBytes + 4 * kGroups * 1024;  // (a staged chunk per warp)
+static_assert(kSmemBytes + 8 * kMostExperts + 64 <= kSmemLimit && 8 * (kActSlots + kDqSlots + 2 * kCodeSlots + 5) + 8 <= kBarBytes, "shared memory");
 
 __device__ __forceinline__ int row_tiles(int n) { return (n + 2 * kRows - 1) / (2 * kRows); }
 
@@ -104,6 +105,12 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
 __device__ __forceinline__ void copy16(uint32_t to, const void* from) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
+// The same where `ok`, without a branch.
+__device__ __forceinline__ void copy16_if(bool ok, uint32_t to, const void* from) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p cp.async.cg.shared.global [%0], [%1], 16;\n\t}" ::"r"(to),
+               "l"(from), "r"((int)ok)
+               : "memory");
+}
 __device__ __forceinline__ void copy4(uint32_t to, const void* from) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
 }
@@ -116,6 +123,49 @@ __device__ __forceinline__ bool elect_one() {
 // all of this thread's copies have landed
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
+// 16 lanes of tensor memory x 16 columns: r[4 m + 2 v + c] is lane (thread / 4 +
+// 8 v), column 8 m + 2 (thread % 4) + c.
+__device__ __forceinline__ void tmem_ld_16x16(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+// Four 8x8 matrices of 16-bit values, stored transposed: thread 8 i + j gives
+// where matrix i's column j goes, as a row of 16 bytes.
+__device__ __forceinline__ void stmatrix_trans(uint32_t at, const uint32_t (&m)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(m[0]), "r"(m[1]), "r"(m[2]),
+               "r"(m[3])
+               : "memory");
+}
+
+// The bf16 dequantization of one column, RNE((q - z) s) as dequant_word_bf16
+// gives it, in pairs: q - z is exact in bf16, and with s = hi + lo, hi its
+// rounding to bf16 and lo the remaining (at most three) bits, (q - z) lo is
+// exact too, so that one fma of exact operands rounds the exact product once.
+// Four instructions a pair instead of five.
+struct DeqSplitBf16 {
+  __nv_bfloat162 zero, hi, lo;  // 128 + z, and the parts of the scale
+  __device__ __forceinline__ DeqSplitBf16(uint32_t z, uint16_t s_bits) {
+    const uint32_t b = 0x43004300u | z | (z << 16);
+    zero = *reinterpret_cast<const __nv_bfloat162*>(&b);
+    const float s = __half2float(__ushort_as_half(s_bits));
+    const __nv_bfloat16 h = __float2bfloat16_rn(s);
+    hi = __bfloat162bfloat162(h);
+    lo = __bfloat162bfloat162(__float2bfloat16_rn(s - __bfloat162float(h)));
+  }
+  __device__ __forceinline__ void word(uint32_t w, uint32_t* out) const {
+    const uint32_t t = w & 0x0F0F0F0Fu, u = (w >> 4) & 0x0F0F0F0Fu;
+    const uint32_t x[4] = {__byte_perm(t, 0x43434343u, 0x4240), __byte_perm(t, 0x43434343u, 0x4341),
+                           __byte_perm(u, 0x43434343u, 0x4240), __byte_perm(u, 0x43434343u, 0x4341)};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x[i]), zero);
+      const __nv_bfloat162 v = __hfma2(d, hi, __hmul2(d, lo));
+      out[i] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+  }
+};
+
 template <bool kB>
 __global__ void __launch_bounds__(kThreads, 1)
 experts_tc_kernel(const __grid_constant__ CUtensorMap tmW, const TensorParams p) {
@@ -126,7 +176,7 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmW, const TensorParams p)
   const uint32_t raw = (uint32_t)__cvta_generic_to_shared(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   constexpr int nact = kActSlots, ncode = kCodeSlots, ndq = kDqSlots;
-  constexpr uint32_t kActBytes = kActSlot, kCodeBytes = kCodeAtomBytes;
+  constexpr uint32_t kActBytes = kActSlot, kCodeBytes = kCodeSlot;
   constexpr int kDqCol0 = 2 * kRows;  // tensor memory: two accumulators, then the dequantized operand
   // [activation ring | code ring | barriers | list of tiles], 1024-aligned slots
   const uint32_t code_base = base + (uint32_t)nact * kActBytes;
@@ -141,14 +191,15 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmW, const TensorParams p)
   const uint32_t drain_bar = bars + 8u * (nact + ndq + 2 * ncode + 4);  // the MMAs issued before an abort completed
   const uint32_t tmem_slot = drain_bar + 8u;
   uint8_t* gen_base = smem_raw + (base - raw);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(gen_base + (tmem_slot + 4u - base));
-  int* offs = reinterpret_cast<int*>(gen_base + (bars + kBarBytes - base));  // [E + 1]
-  int* firsts = offs + kMostExperts + 1;                                     // [E + 1]: an expert's first tile
+  // (fixed places, which take no registers)
+  __shared__ int abort_word, offs[kMostExperts + 1];  // [E + 1]
+  __shared__ int firsts[kMostExperts + 1];            // [E + 1]: an expert's first tile
+  volatile int* abort_flag = &abort_word;
 
   const uint32_t rank = cluster_rank();  // 0: the CTA that issues the MMAs
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
-  const int nk = a.K / kStageK;  // stages of one tile
+  const int natoms = a.K / kStageK, nk = (natoms + kAtoms - 1) / kAtoms;  // stages of one tile
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < nact; ++i) mbar_init(stage_done(i), 1);
@@ -238,7 +289,7 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmW, const TensorParams p)
         const uint32_t to = code_base + (uint32_t)pos.slot * kCodeBytes;
         if (in_smem(to, kCodeBytes, raw, a.err)) {
           mbar_expect_tx(code_full(pos.slot), kCodeBytes);
-          tma_load_4d(to, &tmW, 0, seq.kb * 4, first_strip(t), a.silu ? 2 * t.e : t.e, code_full(pos.slot));
+          tma_load_4d(to, &tmW, 0, seq.kb * kAtoms * 4, first_strip(t), a.silu ? 2 * t.e : t.e, code_full(pos.slot));
         }
         pos.step(1, ncode);
         const int tl = seq.tile;
@@ -260,10 +311,10 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmW, const TensorParams p)
       // ---------------------------------------------------------- MMA issuer (first CTA)
       // (an elected lane of a converged warp: the operands' places then stay in
       // uniform registers, and an MMA takes few instructions to issue)
-      // stage n of the sequence has activation slot n & 7 and dequantized slot n & 3
-      static_assert(nact == 8 && ndq == 4, "slots by the stage's number alone");
+      // stage n of the sequence has dequantized slot n & 3, and `slot` of the rows
       const uint64_t bdesc0 = sw128_kmajor_desc(base);
-      int n = 0;
+      int n = 0, slot = 0;
+      auto after = [&](int k) { return k + 1 == nact ? 0 : k + 1; };
       int e = 0;
       bool ok = true;
       for (int tl = 0; tl < ntl && ok; ++tl) {
@@ -273,39 +324,44 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmW, const TensorParams p)
         auto ready = [&](int i) {
           return mbar_wait_poll(dq_full(i & 3), (uint32_t)(i >> 2) & 1u, abort_flag, kErrMma, a.err);
         };
-        // the four MMAs (16 k: 8 columns of A, 32 bytes of B) of a part of a stage
-        auto mmas = [&](int i, int part, bool first) {
-          const uint32_t place = (uint32_t)((i & 7) * kActSlot + part * kPartSlot);
-          const uint32_t acol = (uint32_t)(kDqCol0 + (i & 3) * kAtomCols);
-          if (!in_smem(base + place, kPartSlot, raw, a.err) || !in_tmem(acol, kAtomCols, 512, a.err)) return;
-          const uint64_t bdesc = bdesc0 + (place >> 4);
+        // the MMAs (16 k each: 8 columns of A, 32 bytes of B) of a part of
+        // stage i, whose rows are in slot k
+        auto mmas = [&](int i, int k, int part, int kb) {
 #pragma unroll
-          for (int kk = 0; kk < kStageK / 16; ++kk)
-            pair_mma_f16_ts(tmem_base + (uint32_t)(part * kRows), tmem_base + acol + (uint32_t)(8 * kk), bdesc + 2u * kk,
-                            idesc, !first || kk != 0);
+          for (int u = 0; u < kAtoms; ++u) {
+            if (kb * kAtoms + u >= natoms) break;
+            const uint32_t place = (uint32_t)(k * kActSlot + u * kAtomSlot + part * kPartSlot);
+            const uint32_t acol = (uint32_t)(kDqCol0 + ((i & 3) * kAtoms + u) * kAtomCols);
+            if (!in_smem(base + place, kPartSlot, raw, a.err) || !in_tmem(acol, kAtomCols, 512, a.err)) return;
+            const uint64_t bdesc = bdesc0 + (place >> 4);
+#pragma unroll
+            for (int kk = 0; kk < kStageK / 16; ++kk)
+              pair_mma_f16_ts(tmem_base + (uint32_t)(part * kRows), tmem_base + acol + (uint32_t)(8 * kk), bdesc + 2u * kk,
+                              idesc, (kb | u | kk) != 0);
+          }
         };
         if (tl > 0 && !(ok = mbar_wait_poll(accum_empty(0), phase, abort_flag, kErrMma, a.err))) break;
         // after another tile, the first part of the stages that there are slots
         // for, then the second (no slot is freed in between)
         const int begin = tl > 0 && t.parts == 2 ? min(nk, ndq) : 0;
-        for (int kb = 0; kb < begin && ok; ++kb) {
+        for (int kb = 0, k = slot; kb < begin && ok; ++kb, k = after(k)) {
           if (!(ok = ready(n + kb))) break;
           tc_fence_after();
-          mmas(n + kb, 0, kb == 0);
+          mmas(n + kb, k, 0, kb);
         }
         if (ok && begin == nk) pair_commit_both(accum_full(0));
         if (ok && tl > 0) ok = mbar_wait_poll(accum_empty(1), phase, abort_flag, kErrMma, a.err);
-        for (int kb = 0; kb < begin && ok; ++kb, ++n) {
-          mmas(n, 1, kb == 0);
-          pair_commit_both(stage_done(n & 7));
+        for (int kb = 0; kb < begin && ok; ++kb, ++n, slot = after(slot)) {
+          mmas(n, slot, 1, kb);
+          pair_commit_both(stage_done(slot));
         }
-        for (int kb = begin; kb < nk && ok; ++kb, ++n) {
+        for (int kb = begin; kb < nk && ok; ++kb, ++n, slot = after(slot)) {
           if (!(ok = ready(n))) break;
           tc_fence_after();
-          mmas(n, 0, kb == 0);
+          mmas(n, slot, 0, kb);
           if (kb + 1 == nk) pair_commit_both(accum_full(0));
-          if (t.parts == 2) mmas(n, 1, kb == 0);
-          pair_commit_both(stage_done(n & 7));
+          if (t.parts == 2) mmas(n, slot, 1, kb);
+          pair_commit_both(stage_done(slot));
         }
         if (ok) pair_commit_both(accum_full(1));
       }
@@ -344,7 +400,6 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmW, const TensorParams p)
       }
 
     const uint32_t dq_remote = cluster_addr(dq_full(grp_id), 0);       // the first CTA's dq_full of this group's slot
-    const uint32_t empty_remote = cluster_addr(accum_empty(0), 0);     // the first CTA's accum_empty(0)
     // a wait that every lane of the warp passes or every lane gives up on:
     // the tensor-memory stores and loads that follow are .sync.aligned
     auto warp_wait = [&](uint32_t bar, uint32_t parity, bool poll, int code) -> bool {
@@ -353,220 +408,223 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmW, const TensorParams p)
       return __all_sync(0xffffffffu, ok);
     };
 
-    // The group's stages are grp_id, grp_id + 4, ...: its it-th stage has the
-    // code slot and the dequantized slot grp_id, and the activation slots
-    // grp_id and grp_id + 4 in turn. `next` is the stage whose rows and scales
-    // are fetched while the one before it is converted: its place, its tile's
-    // expert, this lane's strip of all experts' strips (-1: beyond the
-    // columns), the group of its scale and the k where the group after it
-    // starts, and the rows.
-    static_assert(ncode == kGroups && ndq == kGroups && nact == 2 * kGroups, "slots by the group's number alone");
+    // The group's stages are s = grp_id, grp_id + 4, ...: they have the code
+    // slot and the dequantized slot grp_id, and the slot s % 5 of the rows. `next`
+    // is the next stage to fetch rows and scales for: its place, its tile's
+    // expert, this lane's strip of all experts' strips (-1: beyond the columns),
+    // the group of its first scale, and the rows.
     SeqPos next{grp_id, 0};
     next.step(0, nk);
-    int ne = 0, nstrip = -1, ngrp = next.kb * kStageK / a.group, ngend = (ngrp + 1) * a.group;
+    constexpr int kStep = kAtoms * kStageK;  // k of a stage
+    int ne = 0, nstrip = -1, ngrp = next.kb * kStep / a.group;
     // Rows: of each part this warp copies those of steps q, q + 4, ... (step
     // i: rows 4 i .. 4 i + 3 of this CTA's half of it), a lane the 16 bytes lane
-    // % 8 of row lane / 8 of each; lane 4 j + r holds which row of A is the
-    // r-th of the warp's j-th step, held[part].
+    // % 8 of row lane / 8 of each; lane 16 part + 4 j + r holds which row of A
+    // is the r-th of the warp's j-th step of the part.
     constexpr int kSteps = kRows / 2 / 16;
-    static_assert(4 * kSteps <= 32, "a row per lane");
-    int held[2] = {0, 0}, half = 0;  // half: of a part's rows; minus that with one part
+    static_assert(2 * 4 * kSteps == 32, "a row per lane");
+    int held = 0, half = 0;  // half: of a part's rows; minus that with one part
     auto enter_tile = [&]() {
       const Tile t = tile_at(next.tile, ne);
       const int st = first_strip(t) + (a.silu ? q : ls);
       nstrip = st < limit ? t.e * strips + st + (a.silu && lane >= 16 ? limit : 0) : -1;
       half = t.size / 2;
-      const int i = 4 * (q + lane / 4 * 4) + lane % 4;
-#pragma unroll
-      for (int part = 0; part < 2; ++part) {
-        if (part == t.parts) break;
-        const int f = choice_of(a, t.first + min(part * t.size + (int)rank * half + min(i, half - 1), t.n - 1));
-        held[part] = f < 0 ? 0 : a.per_choice ? f : f / a.top;
-      }
+      const int i = min(4 * (q + lane % 16 / 4 * 4) + lane % 4, half - 1);
+      const int f = choice_of(a, t.first + min(lane / 16 * t.size + (int)rank * half + i, t.n - 1));
+      held = f < 0 ? 0 : a.per_choice ? f : f / a.top;
       if (t.parts == 1) half = -half;
     };
-    // the lane's scale and zero point words of a stage, in shared memory by the
-    // stage's parity: scales of columns cp and cp + 8, and zero points of columns
-    // cp & 4 .. (cp & 4) + 3, each with its column + 8
-    const uint32_t meta0 = bars + kBarBytes + kListBytes + (uint32_t)(dw * 32 + lane) * 8u;
-    auto copy_meta = [&](int it) {
-      if (nstrip < 0) return;
-      const size_t pg = (size_t)nstrip * G + ngrp;
+    // the lane's scale and zero point words of its group's next stage, in shared
+    // memory: per atom the scales of columns cp and cp + 8, and the zero points of
+    // columns cp & 4 .. (cp & 4) + 3, each with its column + 8
+    const uint32_t meta = bars + kBarBytes + (uint32_t)(dw * 32 + lane) * 16u;
+    auto copy_meta = [&]() {
       const uint32_t* sp = reinterpret_cast<const uint32_t*>(a.Sp);
-      const uint32_t to = meta0 + (uint32_t)(it & 1) * kMetaBytes;
-      copy4(to, ld_at(sp + pg * 8 + cp, sp, (size_t)G * a.N * a.E / 2, a.err));
-      copy4(to + 4, ld_at(a.Zp + pg * 2 + cp / 4, a.Zp, (size_t)G * a.N * a.E / 8, a.err));
+      size_t pg = (size_t)nstrip * G + ngrp;
+#pragma unroll
+      for (int u = 0; u < kAtoms; ++u) {
+        if (nstrip < 0 || next.kb * kAtoms + u >= natoms) break;
+        if (u > 0 && next.kb * kStep + u * kStageK >= (ngrp + 1) * a.group) ++pg;  // a group of one atom
+        copy4(meta + 8u * u, ld_at(sp + pg * 8 + cp, sp, (size_t)G * a.N * a.E / 2, a.err));
+        copy4(meta + 8u * u + 4u, ld_at(a.Zp + pg * 2 + cp / 4, a.Zp, (size_t)G * a.N * a.E / 8, a.err));
+      }
     };
     // chunk lane % 8 of row lane / 8 of a step, swizzled by the row's number in
     // its group of eight: 4 (i & 1) + lane / 8, and i is as odd as q
     const uint32_t place = (uint32_t)q * 512u + (uint32_t)(lane / 8) * 128u +
                            (uint32_t)((lane % 8) ^ (lane / 8 + 4 * (q & 1))) * 16u;
-    auto copy_rows = [&](int it) {  // of the group's it-th stage
-      const uint32_t to = base + (uint32_t)(grp_id + (it & 1) * kGroups) * kActBytes + place;
-      const char* from = reinterpret_cast<const char*>(a.A + next.kb * kStageK + lane % 8 * 8);
-      const uint32_t pitch = 2u * (uint32_t)a.K;  // bytes of a row
-      const int rows = abs(half);
-#pragma unroll
-      for (int part = 0; part < 2; ++part) {
-        if (part == 1 && half < 0) break;
-        uint32_t row[kSteps];
-#pragma unroll
-        for (int j = 0; j < kSteps; ++j) row[j] = (uint32_t)__shfl_sync(0xffffffffu, held[part], 4 * j + lane / 8);
-#pragma unroll
-        for (int j = 0; j < kSteps; ++j) {
-          const uint32_t dst = to + (uint32_t)part * kPartSlot + 2048u * j;
-          const uint16_t* src = reinterpret_cast<const uint16_t*>(from + (uint64_t)row[j] * pitch);
-          if (4 * (q + 4 * j) < rows && in_smem(dst, 16, raw, a.err))
-            copy16(dst, ld_at(src, a.A, a_elements(a) - 7, a.err));
-        }
-      }
+    // (both atoms of) the warp's j-th step of a part, to the stage's slot
+    auto copy_step = [&](int part, int j, uint32_t to, const char* from) {
+      const uint32_t row = (uint32_t)__shfl_sync(0xffffffffu, held, 16 * part + 4 * j + lane / 8);
+      const uint32_t dst = to + (uint32_t)part * kPartSlot + 2048u * j;
+      const uint16_t* src = reinterpret_cast<const uint16_t*>(from + (uint64_t)row * (2u * (uint32_t)a.K));
+      const bool ok = 4 * (q + 4 * j) < (part == 1 ? half : abs(half)) && in_smem(dst, kAtomSlot + 16, raw, a.err);
+      const bool two = ok && (next.kb + 1) * kAtoms <= natoms;
+      copy16_if(ok, dst, ok ? ld_at(src, a.A, a_elements(a) - 7, a.err) : src);
+      copy16_if(two, dst + kAtomSlot, two ? ld_at(src + kStageK, a.A, a_elements(a) - 7, a.err) : src);
     };
-    // converts the group's it-th stage and copies the rows of the one after it
-    auto stage = [&](int it, bool more) -> bool {
-      // this warp's rows of the stage (the MMAs read them too), and its scales
-      copies_wait();
-      fence_async_shared();  // (the copies wrote them through the generic proxy)
-      uint32_t mscale, mzero;
-      asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(mscale), "=r"(mzero) : "r"(meta0 + (uint32_t)(it & 1) * kMetaBytes) : "memory");
+    // Converts the group's it-th stage, stage s of the sequence (whose place is
+    // `next`), and copies its rows meanwhile, a few copies between the words of
+    // the codes: on their own they would hold the warp up.
+    auto stage = [&](int it, int slot) -> bool {
+      const int s = grp_id + it * kGroups;
+      // the slot's rows, of stage s - 5, have been multiplied
+      if (s >= nact && !warp_wait(stage_done(slot), (uint32_t)(s / nact - 1) & 1u, true, kErrDequant)) return false;
       if (!warp_wait(code_full(grp_id), (uint32_t)it & 1u, false, kErrDequant)) return false;
+      copies_wait();  // the scales
       const uint32_t cb = code_base + (uint32_t)grp_id * kCodeBytes;
-      uint32_t wl[4], wh[4];  // k-octets l and 4 + l
-      const uint32_t row = (uint32_t)(ls * 4 + (cp >> 1));  // 128-byte row of the tile
+      const uint32_t to = base + (uint32_t)slot * kActBytes + place;
+      const char* from = reinterpret_cast<const char*>(a.A + next.kb * kStep + lane % 8 * 8);
 #pragma unroll
-      for (int l = 0; l < 4; ++l) {
-        const uint32_t chunk = ((uint32_t)(4 * (cp & 1) + l)) ^ (row & 7u);  // 128-byte swizzle
-        const uint32_t at = cb + row * 128u + (chunk << 4);
-        const uint4 v = lds128(in_smem(at, 16, raw, a.err) ? at : cb);
-        wl[l] = hi ? v.y : v.x;
-        wh[l] = hi ? v.w : v.z;
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(code_empty(grp_id));  // the codes are in registers
-      const uint32_t z = (mzero >> (8 * (cp & 3) + (hi ? 4 : 0))) & 15u;
-      const uint16_t sc = (uint16_t)(mscale >> (hi ? 16 : 0));
-      uint32_t r[32];  // cell j = (deq[2j], deq[2j + 1]): k-octet o fills cells 4o..4o+3
+      for (int u = 0; u < kAtoms; ++u) {
+        uint32_t wl[4], wh[4];  // k-octets l and 4 + l
+        const uint32_t row = (uint32_t)(ls * 4 * kAtoms + 4 * u + (cp >> 1));  // 128-byte row of the tile
 #pragma unroll
-      for (int l = 0; l < 4; ++l) {
-        uint32_t o0[4], o1[4];
+        for (int l = 0; l < 4; ++l) {
+          const uint32_t chunk = ((uint32_t)(4 * (cp & 1) + l)) ^ (row & 7u);  // 128-byte swizzle
+          const uint32_t at = cb + row * 128u + (chunk << 4);
+          const uint4 v = lds128(in_smem(at, 16, raw, a.err) ? at : cb);
+          wl[l] = hi ? v.y : v.x;
+          wh[l] = hi ? v.w : v.z;
+        }
+        uint32_t sw, zw;
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(sw), "=r"(zw) : "r"(meta + 8u * u) : "memory");
+        if (u + 1 == kAtoms) {  // the codes are in registers
+          __syncwarp();
+          if (lane == 0) mbar_arrive(code_empty(grp_id));
+        }
+        const uint32_t z = (zw >> (8 * (cp & 3) + (hi ? 4 : 0))) & 15u;
+        const uint16_t sc = (uint16_t)(sw >> (hi ? 16 : 0));
+        uint32_t r[32];  // cell j = (deq[2j], deq[2j + 1]): k-octet o fills cells 4o..4o+3
         if (kB) {
-          const DeqConstBf16 dc = make_deq_const_bf16(z, sc);
-          dequant_word_bf16(wl[l], dc, o0);
-          dequant_word_bf16(wh[l], dc, o1);
+          const DeqSplitBf16 dc(z, sc);
+#pragma unroll
+          for (int l = 0; l < 4; ++l) {
+            dc.word(wl[l], r + 4 * l);
+            dc.word(wh[l], r + 16 + 4 * l);
+            copy_step(u, l, to, from);
+          }
         } else {
           const DeqConst dc = make_deq_const(z, sc);
-          dequant_word(wl[l], dc, o0);
-          dequant_word(wh[l], dc, o1);
-        }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          r[4 * l + j] = o0[j];
-          r[16 + 4 * l + j] = o1[j];
+          for (int l = 0; l < 4; ++l) {
+            uint32_t o[4];
+            dequant_word(wl[l], dc, o);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) r[4 * l + j] = o[j];
+            dequant_word(wh[l], dc, o);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) r[16 + 4 * l + j] = o[j];
+            copy_step(u, l, to, from);
+          }
         }
+        // the slot's MMAs, of the group's stage before, are done (waited for with
+        // the first cells in registers)
+        if (u == 0 && it > 0) {
+          // (its rows' slot: (s - 4) % 5)
+          if (!warp_wait(stage_done(slot + 1 == nact ? 0 : slot + 1), (uint32_t)(s - kGroups) / nact & 1u, true, kErrDequant))
+            return false;
+          tc_fence_after();
+        }
+        const uint32_t col = (uint32_t)(kDqCol0 + (grp_id * kAtoms + u) * kAtomCols);
+        if (in_tmem(col, kAtomCols, 512, a.err)) tmem_st32(tmem_base + tlane + col, r);
       }
-      // the slot's MMAs, of the group's stage before, are done (waited for with
-      // the cells in registers: what is between them and the slot's next MMAs is
-      // then the store alone)
-      if (it > 0) {
-        if (!warp_wait(stage_done(grp_id + ((it - 1) & 1) * kGroups), (uint32_t)((it - 1) >> 1) & 1u, true, kErrDequant))
-          return false;
-        tc_fence_after();
-      }
-      const uint32_t col = (uint32_t)(kDqCol0 + grp_id * kAtomCols);
-      if (in_tmem(col, kAtomCols, 512, a.err)) tmem_st32(tmem_base + tlane + col, r);
+      copies_wait();      // this warp's rows of the stage (the MMAs read them too)
       tmem_wait_st();
+      fence_async_shared();  // (the copies wrote them through the generic proxy)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_remote(dq_remote);
-      if (more) {  // the stage after it, to the slot of the stage waited for
-        copy_meta(it + 1);
-        copy_rows(it + 1);
-      }
       return true;
     };
     // this warp's part of tile i's epilogue: tensor-memory lanes 32q..32q+31
     // are this CTA's columns, an accumulator's columns the rows of a part, 16
-    // at a time by the groups in turn
+    // at a time by the groups in turn. A chunk of 16 rows is read as 16 lanes x 8
+    // columns per register quad, the layout of an mma.sync result: with silu a
+    // thread then has gate and up of the same results. Rounded, it goes through
+    // this warp's kilobyte of shared memory, transposed (stmatrix), so that a
+    // lane stores 16 bytes of a row.
     constexpr int kChunks = kRows / 16 / kGroups;
     int ee = 0;
-    uint16_t* out = a.combine ? p.D : a.Y;
-    const size_t all = (size_t)choices(a) * width - 1;
     auto epilogue = [&](int i) -> bool {
+      uint16_t* out = a.combine ? p.D : a.Y;
+      const size_t all = (size_t)choices(a) * width - 7;
+      const uint32_t pitch = 2u * (uint32_t)width;  // bytes of a result's row
+      const uint32_t stage0 = bars + kBarBytes + kMetaBytes + (uint32_t)dw * 1024u;
       const Tile t = tile_at(i, ee);
-      const int s = first_strip(t) + (a.silu ? q : ls);
-      const bool live = s < limit;
-      // two neighbouring columns at a time: even lanes finish one row, odd
-      // lanes the next, of which each gives the other its own column
-      char* to = reinterpret_cast<char*>(out + s * kStripCols + (c & ~1));
-      const bool odd = lane & 1;
-      // the choices of the warp's chunks and their weights, on their way while
-      // it waits: lane l holds row l of a part's first (0) and third (1) chunk,
-      // lane 16 + l that of the second
-      int of[2][2];
-      float factor[2][2];
-#pragma unroll
-      for (int part = 0; part < 2; ++part)
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          const int k = 16 * (grp_id + (2 * m + lane / 16) * kGroups) + lane % 16;
-          of[part][m] = k < t.size && part * t.size + k < t.n && part < t.parts ? choice_of(a, t.first + part * t.size + k) : -1;
-        }
-#pragma unroll
-      for (int part = 0; part < 2; ++part)
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-          factor[part][m] =
-              a.combine && of[part][m] >= 0 ? *ld_at(a.weights + of[part][m], a.weights, (size_t)choices(a), a.err) : 1.f;
-      static_assert(kChunks <= 4, "two registers of rows");
+      const int s0 = first_strip(t) + (a.silu ? q : 2 * q);  // the warp's first strip of results
+#pragma unroll 1
       for (int part = 0; part < 2; ++part) {
         const int n = part < t.parts ? min(t.size, t.n - part * t.size) : 0;
+        // the choices of the warp's chunks and their weights, on their way while
+        // it waits: lane l holds row l of the first chunk, lane 16 + l that of the
+        // second
+        static_assert(kChunks == 2, "a row per lane");
+        const int k = 16 * (grp_id + lane / 16 * kGroups) + lane % 16;
+        const int chosen = k < n ? choice_of(a, t.first + part * t.size + k) : -1;
+        const float weight = a.combine && chosen >= 0 ? *ld_at(a.weights + chosen, a.weights, (size_t)choices(a), a.err) : 1.f;
         if (!warp_wait(accum_full(part), (uint32_t)i & 1u, true, kErrEpilogue)) return false;
         tc_fence_after();
 #pragma unroll 1
         for (int j = 0; j < kChunks; ++j) {
           const int row0 = 16 * (grp_id + j * kGroups);
-          uint32_t r[16];
           const uint32_t col = (uint32_t)(part * kRows + row0);
-          if (row0 < n && in_tmem(col, 16, kDqCol0, a.err)) tmem_ld16(tmem_base + tlane + col, r);
+          uint32_t r[2][8];  // lanes 0..15, 16..31 of the quarter
+          if (row0 < n && in_tmem(col, 16, kDqCol0, a.err)) {
+            tmem_ld_16x16(tmem_base + tlane + col, r[0]);
+            tmem_ld_16x16(tmem_base + tlane + (16u << 16) + col, r[1]);
+          }
           tmem_wait_ld();
-          if (j + 1 == kChunks) {
+          if (j + 1 == kChunks) {  // the warp has read all it reads of this accumulator
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_remote(empty_remote + 8u * part);
+            if (lane == 0) mbar_arrive_remote(cluster_addr(accum_empty(part), 0));  // the first CTA's
           }
           if (row0 >= n) continue;
-          const int chosen = part ? (j > 1 ? of[1][1] : of[1][0]) : (j > 1 ? of[0][1] : of[0][0]);
-          const float weight = part ? (j > 1 ? factor[1][1] : factor[1][0]) : (j > 1 ? factor[0][1] : factor[0][0]);
-          auto store = [&](int row, float lo, float hi) {
-            const int f = __shfl_sync(0xffffffffu, chosen, row + j % 2 * 16);
-            if (a.combine) {
-              const float w = __shfl_sync(0xffffffffu, weight, row + j % 2 * 16);
-              lo *= w, hi *= w;
-            }
-            uint16_t* y = reinterpret_cast<uint16_t*>(to + (uint64_t)(uint32_t)f * (2u * (uint32_t)width));
-            if (f >= 0 && live && in_buf(y, out, all, a.err)) *reinterpret_cast<uint32_t*>(y) = to_out2<kB>(lo, hi);
-          };
+          // r[h][4 m + 2 v + c]: lane (column of the strip) lane / 4 + 8 v, row 8 m + 2 (lane % 4) + c
+          uint32_t o[2][4];  // rounded: pairs of rows, [strip][2 m + v]
           if (a.silu) {
-            // lanes 0..15 finish rows 0..7 of the chunk, lanes 16..31 rows 8..15
 #pragma unroll
-            for (int k = 0; k < 8; k += 2) {
-              float v[2];
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint32_t other = __shfl_xor_sync(0xffffffffu, lane < 16 ? r[k + h + 8] : r[k + h], 16);
-                const float g = __uint_as_float(lane < 16 ? r[k + h] : other);
-                const float u = __uint_as_float(lane < 16 ? other : r[k + h + 8]);
-                v[h] = silu_times(g, u);
-              }
-              const float other = __shfl_xor_sync(0xffffffffu, odd ? v[0] : v[1], 1);
-              store(k + (odd ? 1 : 0) + (lane < 16 ? 0 : 8), odd ? other : v[0], odd ? v[1] : other);
-            }
+            for (int x = 0; x < 4; ++x)
+              o[0][x] = to_out2<kB>(silu_times(__uint_as_float(r[0][2 * x]), __uint_as_float(r[1][2 * x])),
+                                    silu_times(__uint_as_float(r[0][2 * x + 1]), __uint_as_float(r[1][2 * x + 1])));
           } else {
+            float w[4] = {1.f, 1.f, 1.f, 1.f};
+            if (a.combine)
 #pragma unroll
-            for (int k = 0; k < 16; k += 2) {
-              const float v0 = __uint_as_float(r[k]), v1 = __uint_as_float(r[k + 1]);
-              const float other = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
-              store(k + (odd ? 1 : 0), odd ? other : v0, odd ? v1 : other);
-            }
+              for (int x = 0; x < 4; ++x)
+                w[x] = __shfl_sync(0xffffffffu, weight, 16 * j + 8 * (x / 2) + 2 * (lane % 4) + x % 2);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                o[h][x] = to_out2<kB>(__uint_as_float(r[h][2 * x]) * w[x / 2 * 2], __uint_as_float(r[h][2 * x + 1]) * w[x / 2 * 2 + 1]);
+          }
+          // matrix 2 m + v of a strip: rows 8 m .., columns 8 v ..; a row of the
+          // staged chunk has 2 (silu) or 4 pieces of 16 bytes, swizzled by the row
+          const int strips_out = a.silu ? 1 : 2;
+          const int trow = 8 * (lane / 16) + lane % 8, v = lane / 8 % 2;
+          __syncwarp();  // (the chunk before has been read)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (h == strips_out) break;
+            const uint32_t piece = a.silu ? (uint32_t)(v ^ (trow >> 2 & 1)) : (uint32_t)((2 * h + v) ^ (trow >> 1 & 3));
+            stmatrix_trans(stage0 + (uint32_t)trow * 32u * strips_out + piece * 16u, o[h]);
+          }
+          __syncwarp();
+          // a lane's pieces: silu: row lane / 2, piece lane % 2; else rows lane / 4
+          // and 8 + lane / 4, piece lane % 4
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (h == strips_out) break;
+            const int row = a.silu ? lane / 2 : 8 * h + lane / 4, pc = a.silu ? lane % 2 : lane % 4;
+            const uint32_t sw = a.silu ? (uint32_t)(pc ^ (row >> 2 & 1)) : (uint32_t)(pc ^ (row >> 1 & 3));
+            const uint4 d = lds128(stage0 + (uint32_t)row * 32u * strips_out + sw * 16u);
+            const int f = __shfl_sync(0xffffffffu, chosen, 16 * j + row);
+            const int strip = s0 + pc / 2;
+            uint16_t* y = reinterpret_cast<uint16_t*>(reinterpret_cast<char*>(out + strip * kStripCols + pc % 2 * 8) +
+                                                      (uint64_t)(uint32_t)f * pitch);
+            if (f >= 0 && strip < limit && in_buf(y, out, all, a.err)) *reinterpret_cast<uint4*>(y) = d;
           }
         }
       }
@@ -574,25 +632,24 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmW, const TensorParams p)
     };
     bool ok = true;
     int done = 0;  // the tiles whose epilogue this warp has done: [0, done)
+    int slot = grp_id;  // the stage's rows' slot
     if (grp_id < total) {
       enter_tile();
-      copy_meta(0);
-      copy_rows(0);
+      copy_meta();
     }
-    for (int s = grp_id, it = 0; s < total && ok; s += kGroups, ++it) {
+    for (int it = 0; grp_id + it * kGroups < total && ok; ++it) {
+      if (!(ok = stage(it, slot))) break;
+      slot = slot == 0 ? nact - 1 : slot - 1;  // (s + 4) % 5 = (s - 1) % 5
       const int tile = next.tile;
-      const bool more = s + kGroups < total;
-      next.step(kGroups, nk);
-      if (more && next.tile != tile) {
-        enter_tile();
-        ngrp = 0;
-        ngend = a.group;
+      if (grp_id + (it + 1) * kGroups < total) {
+        next.step(kGroups, nk);
+        if (next.tile != tile) {
+          enter_tile();
+          ngrp = 0;
+        }
+        while (next.kb * kStep >= (ngrp + 1) * a.group) ++ngrp;
+        copy_meta();
       }
-      while (next.kb * kStageK >= ngend) {
-        ++ngrp;
-        ngend += a.group;
-      }
-      ok = stage(it, more);
       // the epilogues of the tiles before the converted stage's tile
       for (; ok && done < tile; ++done) ok = epilogue(done);
     }
@@ -622,7 +679,7 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmW, const TensorParams p)
 template <bool kB>
 cudaError_t launch(const CUtensorMap& tmW, TensorParams p, cudaStream_t stream) {
   const void* kern = reinterpret_cast<const void*>(experts_tc_kernel<kB>);
-  cudaError_t e = set_max_smem_once(kern, kSmemLimit);
+  cudaError_t e = set_max_smem_once(kern, kSmemBytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kThreads);
@@ -659,7 +716,7 @@ cudaError_t launch_experts_tc(ExpertArgs a, bool bf16, void* workspace, cudaStre
   cudaError_t e = device_error_word(&a.err);
   if (e != cudaSuccess) return e;
   CUtensorMap tmW;
-  if (!cached_expert_map(&tmW, a.Wq, a.N, a.K, a.E, 1, a.silu)) return cudaErrorInvalidValue;
+  if (!cached_expert_map(&tmW, a.Wq, a.N, a.K, a.E, kAtoms, a.silu)) return cudaErrorInvalidValue;
   const int wide = a.silu ? a.N / 2 : a.N, per = a.silu ? kCols : 2 * kCols;
   TensorParams p = {a, workspace ? reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + kWorkspaceFlags) : nullptr,
                     (wide + per - 1) / per};
