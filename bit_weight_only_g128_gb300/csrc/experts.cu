@@ -19,9 +19,9 @@
 // group's fp32 sum is multiplied by its scale. So the weights are (q - z) s
 // unrounded, the sums fp32, and the result is rounded once.
 //
-// Combined, each choice's product goes to the workspace in fp32, already
-// multiplied by its weight, and a second kernel adds a token's rows in the
-// order of its choices: no atomics, the same result every time.
+// Combined, each choice's product goes to the workspace in fp32, and a second
+// kernel adds a token's rows, multiplied by their weights, in the order of its
+// choices: no atomics, the same result every time.
 #include <cuda_bf16.h>
 
 #include "experts.cuh"
@@ -297,7 +297,6 @@ __global__ void __launch_bounds__(kThreads, 2) experts_decode_kernel(const Decod
   extern __shared__ __align__(16) uint8_t dynamic[];
   __shared__ float red[KS][kRows][kRed];
   __shared__ int src[kRows], of[kRows];
-  __shared__ float factor[kRows];
   __shared__ RowTile tile;
   const ExpertArgs& a = p.a;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -311,7 +310,6 @@ __global__ void __launch_bounds__(kThreads, 2) experts_decode_kernel(const Decod
       const int f = lane < t.n ? choice_of(a, t.first + lane) : -1;
       of[lane] = f;
       src[lane] = f < 0 ? 0 : a.per_choice ? f : f / a.top;
-      factor[lane] = a.combine && f >= 0 ? *ld_at(a.weights + f, a.weights, (size_t)choices(a), a.err) : 1.f;
     }
   }
   __syncthreads();
@@ -369,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 2) experts_decode_kernel(const Decod
     const size_t at = (size_t)of[r] * width + n, all = (size_t)choices(a) * width - 1;
     if (a.combine) {
       float* d = p.D + at;
-      if (in_buf(d, p.D, all, a.err)) *reinterpret_cast<float2*>(d) = make_float2(v[0] * factor[r], v[1] * factor[r]);
+      if (in_buf(d, p.D, all, a.err)) *reinterpret_cast<float2*>(d) = make_float2(v[0], v[1]);
     } else {
       if (a.silu) v[0] = silu_times(v[0], u[0]), v[1] = silu_times(v[1], u[1]);
       uint16_t* y = a.Y + at;
@@ -395,8 +393,8 @@ __device__ __forceinline__ void eight(const float* p, float (&v)[8]) {
   v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
 
-// Y[t] = the sum of the rows of D of token t's choices that have an expert, in
-// their order, in fp32. One thread per eight columns.
+// Y[t] = the weighted sum of the rows of D of token t's choices that have an
+// expert, in their order, in fp32. One thread per eight columns.
 template <bool kB, class T>
 __global__ void __launch_bounds__(kThreads) experts_sum_kernel(const ExpertArgs a, const T* D) {
   allow_dependent_launch();
@@ -410,10 +408,11 @@ __global__ void __launch_bounds__(kThreads) experts_sum_kernel(const ExpertArgs 
   for (int j = 0; j < a.top; ++j) {
     const size_t f = (size_t)t * a.top + j;
     if (*ld_at(a.experts + f, a.experts, (size_t)choices(a), a.err) < 0) continue;
+    const float w = *ld_at(a.weights + f, a.weights, (size_t)choices(a), a.err);
     float v[8];
     eight<kB>(ld_at(D + f * a.N + n, D, (size_t)choices(a) * a.N - 7, a.err), v);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) sum[k] += v[k];
+    for (int k = 0; k < 8; ++k) sum[k] = fmaf(w, v[k], sum[k]);
   }
   uint16_t* y = a.Y + (size_t)t * a.N + n;
   if (in_buf(y, a.Y, (size_t)a.T * a.N - 7, a.err))

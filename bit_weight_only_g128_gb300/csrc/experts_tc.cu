@@ -3,8 +3,8 @@
 //
 // Choice f of expert e: Y[f][n] = sum_k A[f or f / top][k] W_e[k][n], with the
 // gate/up epilogue silu(gate) * up of columns [gate | up], or the products
-// multiplied by their weights and rounded to 16 bits for the sum over a
-// token's choices (experts.cu adds them up in fp32).
+// rounded to 16 bits for the weighted sum over a token's choices
+// (experts.cu forms it in fp32).
 //
 // The contraction is the one of the kernel for one weight (tc_pair.cu): a
 // cluster of two CTAs makes a tile of 256 weight columns, each CTA dequantizing
@@ -71,7 +71,7 @@ constexpr int kMostExperts = 512;
 
 struct TensorParams {
   ExpertArgs a;
-  uint16_t* D;     // combined: [choices][N], the weighted products
+  uint16_t* D;     // combined: [choices][N], the products
   int pairs;       // tiles along the columns
 };
 
@@ -556,15 +556,18 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmW, const TensorParams p)
 #pragma unroll 1
       for (int part = 0; part < 2; ++part) {
         const int n = part < t.parts ? min(t.size, t.n - part * t.size) : 0;
-        // the choices of the warp's chunks and their weights, on their way while
-        // it waits: lane l holds row l of the first chunk, lane 16 + l that of the
-        // second
+        // the choices of the warp's chunks, on their way while it waits: lane l
+        // holds row l of the first chunk, lane 16 + l that of the second
         static_assert(kChunks == 2, "a row per lane");
         const int k = 16 * (grp_id + lane / 16 * kGroups) + lane % 16;
-        const int chosen = k < n ? choice_of(a, t.first + part * t.size + k) : -1;
-        const float weight = a.combine && chosen >= 0 ? *ld_at(a.weights + chosen, a.weights, (size_t)choices(a), a.err) : 1.f;
+        int chosen = -1;
+        if (k < n) chosen = *ld_at(a.rows + t.first + part * t.size + k, a.rows, (size_t)choices(a), a.err);
         if (!warp_wait(accum_full(part), (uint32_t)i & 1u, true, kErrEpilogue)) return false;
         tc_fence_after();
+        if (k < n && (unsigned)chosen >= (unsigned)choices(a)) {  // (as choice_of)
+          atomicOr(a.err, kErrRange);
+          chosen = -1;
+        }
 #pragma unroll 1
         for (int j = 0; j < kChunks; ++j) {
           const int row0 = 16 * (grp_id + j * kGroups);
@@ -581,24 +584,17 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmW, const TensorParams p)
             if (lane == 0) mbar_arrive_remote(cluster_addr(accum_empty(part), 0));  // the first CTA's
           }
           if (row0 >= n) continue;
-          // r[h][4 m + 2 v + c]: lane (column of the strip) lane / 4 + 8 v, row 8 m + 2 (lane % 4) + c
+          // r[j][h][4 m + 2 v + c]: column lane / 4 + 8 v of the strip, row 8 m + 2 (lane % 4) + c
           uint32_t o[2][4];  // rounded: pairs of rows, [strip][2 m + v]
-          if (a.silu) {
+          auto f = [&](int h, int x) { return __uint_as_float(r[h][x]); };
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-              o[0][x] = to_out2<kB>(silu_times(__uint_as_float(r[0][2 * x]), __uint_as_float(r[1][2 * x])),
-                                    silu_times(__uint_as_float(r[0][2 * x + 1]), __uint_as_float(r[1][2 * x + 1])));
-          } else {
-            float w[4] = {1.f, 1.f, 1.f, 1.f};
-            if (a.combine)
-#pragma unroll
-              for (int x = 0; x < 4; ++x)
-                w[x] = __shfl_sync(0xffffffffu, weight, 16 * j + 8 * (x / 2) + 2 * (lane % 4) + x % 2);
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-              for (int x = 0; x < 4; ++x)
-                o[h][x] = to_out2<kB>(__uint_as_float(r[h][2 * x]) * w[x / 2 * 2], __uint_as_float(r[h][2 * x + 1]) * w[x / 2 * 2 + 1]);
+          for (int x = 0; x < 4; ++x) {
+            if (a.silu) {
+              o[0][x] = to_out2<kB>(silu_times(f(0, 2 * x), f(1, 2 * x)), silu_times(f(0, 2 * x + 1), f(1, 2 * x + 1)));
+            } else {
+              o[0][x] = to_out2<kB>(f(0, 2 * x), f(0, 2 * x + 1));
+              o[1][x] = to_out2<kB>(f(1, 2 * x), f(1, 2 * x + 1));
+            }
           }
           // matrix 2 m + v of a strip: rows 8 m .., columns 8 v ..; a row of the
           // staged chunk has 2 (silu) or 4 pieces of 16 bytes, swizzled by the row
@@ -640,7 +636,9 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmW, const TensorParams p)
     for (int it = 0; grp_id + it * kGroups < total && ok; ++it) {
       if (!(ok = stage(it, slot))) break;
       slot = slot == 0 ? nact - 1 : slot - 1;  // (s + 4) % 5 = (s - 1) % 5
+      // the epilogues of the tiles before the converted stage's tile
       const int tile = next.tile;
+      for (; ok && done < tile; ++done) ok = epilogue(done);
       if (grp_id + (it + 1) * kGroups < total) {
         next.step(kGroups, nk);
         if (next.tile != tile) {
@@ -650,8 +648,6 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmW, const TensorParams p)
         while (next.kb * kStep >= (ngrp + 1) * a.group) ++ngrp;
         copy_meta();
       }
-      // the epilogues of the tiles before the converted stage's tile
-      for (; ok && done < tile; ++done) ok = epilogue(done);
     }
     for (; ok && done < ntl; ++done) ok = epilogue(done);
     copies_wait();

@@ -173,7 +173,7 @@ cudaError_t launch_experts_decode(ExpertArgs args, bool bf16, void* workspace, c
 // choices' products in 16 bits.
 size_t experts_tc_workspace_bytes(int choices, int N, bool combine);
 cudaError_t launch_experts_tc(ExpertArgs args, bool bf16, void* workspace, cudaStream_t stream);
-// Y[t] = the sum of D's rows of token t's choices (16 bits).
+// Y[t] = the weighted sum of D's rows of token t's choices (16 bits).
 cudaError_t launch_experts_sum(const ExpertArgs& args, const uint16_t* D, bool bf16, cudaStream_t stream);
 
 // Reads the device error word (bounded waits that gave up, self-checks) and
