@@ -7,15 +7,18 @@
 //
 // Every expert that has rows streams its packed weights once per 16 rows, so
 // the bound is HBM bytes, and for a token or two the chain offsets - rows -
-// activations and weights - sums. A block takes up to 16 rows of one expert
-// and 128 / KS columns; its 8 warps take a strip of 16 columns each and one of
-// KS parts of K, so that few rows still spread over all SMs. A lane loads its
-// four words of an atom with 16 bytes, eight atoms ahead; the activations come
-// to shared memory by asynchronous copies, gathered by row. The codes enter
+// activations and weights - sums. An item of work is up to 16 rows of one expert
+// times 128 / KS columns; a block's 8 warps take a strip of 16 columns each and
+// one of KS parts of K, so that few rows still spread over all SMs. The blocks
+// are persistent, two per SM, and take the items in turn; weights (three units
+// of four atoms ahead, each warp its own), scales and activations (two units
+// ahead, gathered by row) stream into shared memory by asynchronous copies that
+// run on across the items. The codes enter
 // mma.sync m16n8k16 as exact 16-bit numbers without a multiplication: fp16
 // takes q masked in place as the subnormal q 2^-24 (the odd pairs one nibble
 // higher, summed apart and divided by 16), bf16 takes 128 + q put together by
-// byte permutes; the zero point, in the same form, is subtracted exactly. Each
+// byte permutes; the zero point, in the same form, is subtracted exactly, or
+// (up to eight rows) multiplied and subtracted in the sums. Each
 // group's fp32 sum is multiplied by its scale. So the weights are (q - z) s
 // unrounded, the sums fp32, and the result is rounded once.
 //
@@ -24,6 +27,9 @@
 // choices: no atomics, the same result every time.
 #include <cuda_bf16.h>
 
+#include <cmath>
+#include <type_traits>
+
 #include "experts.cuh"
 
 namespace w4a16 {
@@ -31,22 +37,30 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = 8;
-constexpr int kRows = 16;      // rows of a block
-constexpr int kUnit = 8;       // atoms loaded ahead
-constexpr int kRowPad = 64;    // bytes: neighbouring rows in opposite halves of the banks
+constexpr int kRows = 16;      // rows of an item
+constexpr int kUnit = 4;       // atoms of a step
+constexpr int kWeightSlots = 4, kRowSlots = 3;  // units in shared memory: weights, activations
+constexpr int kUnitBytes = kUnit * kAtomWords * 4;         // a warp's codes of a unit
+constexpr int kSlotBytes = kUnitBytes + 2 * 32 * 4;        // with its scales and zero points
+constexpr int kRowBytes = kUnit * 128 + 64;  // of a unit's activations: neighbouring rows in opposite halves of the banks
+constexpr int kItems = 8;      // items known at a time
+constexpr int kMostExperts = 512;
 constexpr uint32_t kFull = 0xffffffffu;
 
 struct DecodeParams {
   ExpertArgs a;
   float* D;      // combined: [choices][N]
-  int chunk;     // atoms of a part in one piece of the activations
-  int pieces;    // pieces of a part
+  int blocks;    // column blocks
+  int rows;      // rows of a part's activations in shared memory: 8 or 16
 };
 
 __device__ __forceinline__ void copy16(uint32_t to, const void* from) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copy4(uint32_t to, const void* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
+}
 template <int N>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
@@ -80,144 +94,360 @@ struct Zero {
   }
 };
 
+template <bool kB>
+__device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+  if (kB)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // The four pairs of a word minus the zero point: (k 0, 1), (2, 3), (4, 5),
 // (6, 7); exact. fp16: (q - z) 2^-24 in the first two, 16 times that in the
 // others; bf16: q - z.
 template <bool kB>
-__device__ __forceinline__ void codes(uint32_t w, const Zero<kB>& z, uint32_t (&c)[4]) {
+__device__ __forceinline__ void plain_codes(uint32_t w, uint32_t (&c)[4]) {  // (not minus the zero point)
   if (kB) {
     const uint32_t t = w & 0x0F0F0F0Fu, u = (w >> 4) & 0x0F0F0F0Fu;
     c[0] = __byte_perm(t, 0x43434343u, 0x4240);
     c[1] = __byte_perm(t, 0x43434343u, 0x4341);
     c[2] = __byte_perm(u, 0x43434343u, 0x4240);
     c[3] = __byte_perm(u, 0x43434343u, 0x4341);
+  } else {
+    const uint32_t w8 = w >> 8;
+    c[0] = w & 0x000F000Fu;
+    c[1] = w8 & 0x000F000Fu;
+    c[2] = w & 0x00F000F0u;
+    c[3] = w8 & 0x00F000F0u;
+  }
+}
+template <bool kB>
+__device__ __forceinline__ void codes(uint32_t w, const Zero<kB>& z, uint32_t (&c)[4]) {
+  plain_codes<kB>(w, c);
+  if (kB) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&c[i]), *reinterpret_cast<const __nv_bfloat162*>(&z.lo));
       c[i] = *reinterpret_cast<const uint32_t*>(&d);
     }
   } else {
-    const uint32_t w8 = w >> 8;
-    c[0] = hsub2_rn(w & 0x000F000Fu, z.lo);
-    c[1] = hsub2_rn(w8 & 0x000F000Fu, z.lo);
-    c[2] = hsub2_rn(w & 0x00F000F0u, z.hi);
-    c[3] = hsub2_rn(w8 & 0x00F000F0u, z.hi);
+    c[0] = hsub2_rn(c[0], z.lo);
+    c[1] = hsub2_rn(c[1], z.lo);
+    c[2] = hsub2_rn(c[2], z.hi);
+    c[3] = hsub2_rn(c[3], z.hi);
   }
 }
 
-// The row tile `y` of the launch: expert, first row and rows (0: none). The
-// experts' tiles of kRows rows follow one another, those of no expert (e = E)
-// last. By a whole warp.
-struct RowTile {
-  int e, first, n;
-};
-__device__ __forceinline__ RowTile find_tile(const ExpertArgs& a, int y, int lane) {
-  int sum = 0;
-  for (int e0 = 0; e0 <= a.E; e0 += 32) {
-    const int e = e0 + lane;
-    int begin = 0, end = 0;
-    if (e <= a.E) {
-      begin = offset_of(a, e);
-      end = e < a.E ? offset_of(a, e + 1) : choices(a);
-    }
-    const int tiles = end > begin ? (end - begin + kRows - 1) / kRows : 0;
-    int s = tiles;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int u = __shfl_up_sync(kFull, s, d);
-      if (lane >= d) s += u;
-    }
-    s += sum;
-    const uint32_t past = __ballot_sync(kFull, s > y);
-    if (past) {
-      const int l = __ffs(past) - 1;
-      const int at = y - __shfl_sync(kFull, s - tiles, l);
-      const int first = __shfl_sync(kFull, begin, l) + at * kRows, last = __shfl_sync(kFull, end, l);
-      return {e0 + l, first, min(kRows, last - first)};
-    }
-    sum = __shfl_sync(kFull, s, 31);
-  }
-  return {0, 0, 0};
-}
-
-// One unit of a warp's strip: words, and the groups' scales and zero points:
-// lane 8 i + c holds those of columns c and c + 8 of groups i and i + 4 from
-// the unit's first group on.
-struct Unit {
-  uint4 w[kUnit];
-  uint32_t s[2], z[2];
+// An item: rows of expert e (E: of none, whose results are zeros) times a
+// block of columns.
+struct Item {
+  int e, n, col;
+  int of[kRows], src[kRows];  // choice and row of A
 };
 
-template <bool kB, int KS>
-struct Strip {
-  const DecodeParams& p;
-  int strip;      // of all experts' columns; -1: none
-  int end;        // one past the part's last atom
-  int natoms, apg, G, lane;
+// KS: parts of K. kPairs: groups of 128 k, two atoms, of which a unit has two
+// and a part a whole number; else any.
+template <bool kB, int KS, bool kPairs>
+__global__ void __launch_bounds__(kThreads, 2) experts_decode_kernel(const DecodeParams p) {
+  constexpr int S = kWarps / KS;        // strips of an item
+  constexpr int kCols = S * kStripCols;
+  constexpr int kRed = kCols + 4;       // floats of a row of partial sums
+  extern __shared__ __align__(128) uint8_t dynamic[];
+  __shared__ float red[KS][kRows][kRed];
+  __shared__ Item items[kItems];
+  __shared__ int offs[kMostExperts + 2], firsts[kMostExperts + 2];  // experts' offsets and first row tiles
+  const ExpertArgs& a = p.a;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t dyn = (uint32_t)__cvta_generic_to_shared(dynamic);
+  const uint32_t weights = dyn + (uint32_t)warp * kWeightSlots * kSlotBytes;  // this warp's units
+  const uint32_t rows = dyn + kWarps * kWeightSlots * kSlotBytes;             // the block's activations
+  const uint32_t row_slot = (uint32_t)(KS * p.rows) * kRowBytes;
+  const int part = warp / S, w = warp % S;  // this warp's part of K, and its strip of an item
+  const int natoms = a.K / kAtomK, G = a.K / a.group, apg = a.group / kAtomK;
+  // first atom of a part of K
+  auto part_begin = [&](int k) { return kPairs ? natoms / 2 * k / KS * 2 : natoms * k / KS; };
+  const int begin = part_begin(part), end = part_begin(part + 1);  // this warp's atoms
+  const int longest = kPairs ? (natoms / 2 + KS - 1) / KS * 2 : (natoms + KS - 1) / KS;
+  const int units = (longest + kUnit - 1) / kUnit;                       // steps of an item
+  const int half = a.N / 2, width = a.silu ? half : a.N;                 // of a result's row
+  const int cols = a.silu ? kCols / 2 : kCols;                           // of an item's results
+  allow_dependent_launch();
+  grid_dependency_wait();
 
-  __device__ __forceinline__ void load(Unit& u, int a0, int n) const {
-    const ExpertArgs& a = p.a;
-    const uint4* base = reinterpret_cast<const uint4*>(a.Wq);
-    const uint4* w = base + ((size_t)strip * natoms + a0) * 32 + lane;
-    const size_t all = (size_t)a.E * a.N * a.K / 32;
+  // the row tiles: of one token a choice each, else from the offsets
+  int tiles = a.top;
+  if (a.T > 1) {
+    if (warp == 0) {
+      // offsets that never decrease (recorded where they do), the last that of
+      // the choices' end; the prefix sums of the tiles
+      int top = 0, sum = 0;
+      for (int e0 = 0; e0 <= a.E + 1; e0 += 32) {
+        const int e = e0 + lane;
+        const int v = e <= a.E ? offset_of(a, e) : choices(a);
+        int m = max(v, top);
 #pragma unroll
-    for (int j = 0; j < kUnit; ++j)
-      if (j < n) u.w[j] = ldg_stream(ld_at(w + 32 * j, base, all, a.err));
-    const int g0 = a0 / apg, g1 = (a0 + n - 1) / apg;
-    const uint32_t* sp = reinterpret_cast<const uint32_t*>(a.Sp);
-    const uint8_t* zp = reinterpret_cast<const uint8_t*>(a.Zp);
+        for (int d = 1; d < 32; d <<= 1) {
+          const int u = __shfl_up_sync(kFull, m, d);
+          if (lane >= d) m = max(m, u);
+        }
+        if (e <= a.E && m != v) atomicOr(a.err, kErrRange);
+        // the tiles of expert e - 1, which ends here
+        int before = __shfl_up_sync(kFull, m, 1);
+        if (lane == 0) before = top;
+        int s = e > 0 && e <= a.E + 1 ? (m - before + kRows - 1) / kRows : 0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int g = g0 + lane / 8 + 4 * i;
-      if (g > g1) continue;
-      const size_t at = ((size_t)strip * G + g) * 8 + lane % 8, n2 = (size_t)a.E * a.N * G / 2;
-      u.s[i] = __ldg(ld_at(sp + at, sp, n2, a.err));
-      u.z[i] = __ldg(ld_at(zp + at, zp, n2, a.err));
+        for (int d = 1; d < 32; d <<= 1) {
+          const int u = __shfl_up_sync(kFull, s, d);
+          if (lane >= d) s += u;
+        }
+        if (e <= a.E + 1) {
+          offs[e] = m;
+          firsts[e] = sum + s;
+        }
+        sum += __shfl_sync(kFull, s, 31);
+        top = __shfl_sync(kFull, m, 31);
+      }
     }
+    __syncthreads();
+    tiles = firsts[a.E + 1];
   }
+  const long long all = (long long)tiles * p.blocks;
+  // this block's items: blockIdx.x, blockIdx.x + gridDim.x, ...
+  const int count = blockIdx.x < all ? (int)((all - 1 - blockIdx.x) / gridDim.x) + 1 : 0;
+  // item i of the block, written down by a warp
+  auto describe = [&](int i) {
+    if (i >= count) return;
+    const long long at = blockIdx.x + (long long)i * gridDim.x;
+    const int tile = (int)(at % tiles);  // (row tiles first: those of one expert read the same weights)
+    int e, first, n = 1;
+    if (a.T == 1) {
+      first = tile;
+      e = *ld_at(a.experts + tile, a.experts, (size_t)choices(a), a.err);
+      if (e >= a.E) {
+        if (lane == 0) atomicOr(a.err, kErrRange);
+        e = -1;
+      }
+      if (e < 0) e = a.E;
+    } else {
+      int lo = 0, hi = a.E + 1;  // the last expert whose first tile is not behind
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (firsts[mid] <= tile) lo = mid;
+        else hi = mid;
+      }
+      e = lo;
+      first = offs[e] + (tile - firsts[e]) * kRows;
+      n = min(kRows, offs[e + 1] - first);
+    }
+    Item& it = items[i % kItems];
+    if (lane == 0) it.e = e, it.n = n, it.col = (int)(at / tiles);
+    if (lane < kRows) {
+      int f = -1;
+      if (lane < n) f = a.T == 1 ? first : choice_of(a, first + lane);
+      it.of[lane] = f;
+      it.src[lane] = f < 0 ? 0 : a.per_choice ? f : f / a.top;
+    }
+  };
+  if (warp < kWeightSlots) describe(warp);
+  __syncthreads();
 
-  // out += the unit's products with the rows in shared memory (`act`: the
-  // lane's place in its first row at the unit's first atom).
-  template <int MT>
-  __device__ __forceinline__ void multiply(float (&out)[MT][4], const Unit& u, uint32_t act, uint32_t row_bytes, int a0,
-                                           int n) const {
-    const int g0 = a0 / apg;
+  // The stream of weights of this warp: the next unit to copy, this lane's first
+  // word of it (null: no strip), and with kPairs its word of scales or zero points.
+  // (with silu an item's first strips are gate columns, the rest the up columns
+  // of the same results)
+  int wi = 0, wu = 0, wslot = 0, strip = 0;
+  const uint4* codes_from = nullptr;
+  const uint32_t* meta_from = nullptr;
+  const uint4* const wq = reinterpret_cast<const uint4*>(a.Wq);
+  const uint32_t* const sp = reinterpret_cast<const uint32_t*>(a.Sp);
+  const size_t all_codes = (size_t)a.E * a.N * a.K / 32, all_scales = (size_t)a.E * a.N * G / 2;
+  auto enter = [&]() {
+    codes_from = nullptr;
+    if (wi >= count) return;
+    const Item& it = items[wi % kItems];
+    if (it.e >= a.E) return;
+    int s = it.col * S + w;
+    bool live = s < a.N / kStripCols;
+    if (a.silu) {
+      s = it.col * (S / 2) + w % (S / 2);
+      live = s < half / kStripCols;
+      if (w >= S / 2) s += half / kStripCols;
+    }
+    if (!live) return;
+    strip = it.e * (a.N / kStripCols) + s;
+    codes_from = wq + ((size_t)strip * natoms + begin) * 32 + lane;
+    const size_t at = (size_t)strip * G + begin / 2;
+    if (kPairs) meta_from = lane < 16 ? sp + at * 8 + lane : a.Zp + at * 2 + lane - 16;
+  };
+  auto copy_weights = [&]() {
+    const int n = min(kUnit, end - begin - wu * kUnit);
+    if (codes_from && n > 0) {
+      const uint32_t to = weights + (uint32_t)wslot * kSlotBytes;
+#pragma unroll
+      for (int j = 0; j < kUnit; ++j)
+        if (j < n && in_smem(to + 512u * j + 16u * lane, 16, dyn, a.err))
+          copy16(to + 512u * j + 16u * lane, ld_at(codes_from + 32 * j, wq, all_codes, a.err));
+      codes_from += 32 * kUnit;
+      if (kPairs) {
+        // lane 8 i + c: the scales of columns c and c + 8 of the unit's group i;
+        // lane 16 + 2 i + h: the zero points of columns 4 h .. 4 h + 3, each with
+        // its column + 8
+        if (lane < 16 ? lane < 4 * n : lane < 16 + n)
+          copy4(to + kUnitBytes + 4u * lane,
+                lane < 16 ? ld_at(meta_from, sp, all_scales, a.err) : ld_at(meta_from, a.Zp, all_scales / 4, a.err));
+        meta_from += lane < 16 ? 16 : 4;
+      } else {
+        // lane 8 i + c: the scales of columns c and c + 8 of the unit's i-th
+        // group, and the word of zero points that c's is in
+        const int a0 = begin + wu * kUnit, g = a0 / apg + lane / 8;
+        if (g <= (a0 + n - 1) / apg) {
+          const size_t at = (size_t)strip * G + g;
+          copy4(to + kUnitBytes + 4u * lane, ld_at(sp + at * 8 + lane % 8, sp, all_scales, a.err));
+          copy4(to + kUnitBytes + 128u + 4u * lane, ld_at(a.Zp + at * 2 + lane % 8 / 4, a.Zp, all_scales / 4, a.err));
+        }
+      }
+    }
+    wslot = wslot + 1 == kWeightSlots ? 0 : wslot + 1;
+    if (++wu == units && wi < count) {
+      wu = 0;
+      ++wi;
+      // the item three on is written down now, by one warp
+      if (wi % kWarps == warp) describe(wi + kWeightSlots - 1);
+      enter();
+    }
+  };
+  // the block's stream of activations: a unit of every part, rows of 64 vectors
+  int ri = 0, ru = 0, rslot = 0;
+  auto copy_rows = [&]() {
+    if (ri < count) {
+      const Item& it = items[ri % kItems];
+      const int n = it.e < a.E ? it.n : 0;
+      const uint32_t to = rows + (uint32_t)rslot * row_slot;
+      const int v = threadIdx.x % (8 * kUnit);  // 16 bytes of a row
+      for (int i = threadIdx.x / (8 * kUnit); i < n * KS; i += kThreads / (8 * kUnit)) {
+        const int r = KS == 1 ? i : i / KS, k = KS == 1 ? 0 : i % KS;
+        const int a0 = part_begin(k) + ru * kUnit;
+        const uint32_t at = to + (uint32_t)(k * p.rows + r) * kRowBytes + 16u * v;
+        if (a0 + v / 8 < part_begin(k + 1) && in_smem(at, 16, dyn, a.err))
+          copy16(at, ld_at(a.A + (size_t)it.src[r] * a.K + a0 * kAtomK + v * 8, a.A, a_elements(a) - 7, a.err));
+      }
+    }
+    rslot = rslot + 1 == kRowSlots ? 0 : rslot + 1;
+    if (++ru == units) ru = 0, ++ri;
+  };
+
+  float out[2][4] = {};
+  const float scale = kB ? 1.f : 16777216.f;  // of the codes' form
+  auto scales = [&](uint32_t sw, float& s0, float& s1) {
+    s0 = value16<false>(sw & 0xffffu) * scale, s1 = value16<false>(sw >> 16) * scale;
+  };
+  // out += a unit's products: MT octets of rows
+  auto multiply_pairs = [&](auto octets, uint32_t wt, uint32_t act, int n) {
+    constexpr int MT = decltype(octets)::value;
+    // One octet: the zero points go in by MMAs of their own, with the constant
+    // row -z, four a pair of atoms and octet against 32 subtractions that serve
+    // all octets: for two octets the subtractions are cheaper.
+    constexpr bool kZeroMma = MT == 1;
+#pragma unroll
+    for (int i = 0; i < kUnit / 2; ++i) {
+      if (2 * i >= n) break;
+      uint32_t sw, zw;
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(sw) : "r"(wt + kUnitBytes + (uint32_t)(8 * i + lane / 4) * 4u) : "memory");
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(zw) : "r"(wt + kUnitBytes + 64u + (uint32_t)(2 * i + lane / 16) * 4u) : "memory");
+      const uint32_t zz = zw >> (lane / 4 % 4 * 8);
+      const Zero<kB> z0(zz & 15u), z1((zz >> 4) & 15u);
+      constexpr uint32_t kMinus = 0x80008000u;
+      float lo[MT][4], hi[MT][4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint4 v = tc::lds128(wt + 512u * (2 * i + j) + 16u * lane);
+        const uint32_t wd[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          uint32_t c0[4], c1[4];
+          if (kZeroMma) {
+            plain_codes<kB>(wd[2 * s], c0);
+            plain_codes<kB>(wd[2 * s + 1], c1);
+          } else {
+            codes<kB>(wd[2 * s], z0, c0);
+            codes<kB>(wd[2 * s + 1], z1, c1);
+          }
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            const uint4 b = tc::lds128(act + m * 8 * kRowBytes + (2 * i + j) * 128 + s * 64);
+            float(&second)[4] = kB ? lo[m] : hi[m];
+            if (j == 0 && s == 0) {
+              mma_first<kB>(lo[m], c0[0], c1[0], c0[1], c1[1], b.x, b.y);
+              if (kB)
+                mma<kB>(second, c0[2], c1[2], c0[3], c1[3], b.z, b.w);
+              else
+                mma_first<kB>(second, c0[2], c1[2], c0[3], c1[3], b.z, b.w);
+            } else {
+              mma<kB>(lo[m], c0[0], c1[0], c0[1], c1[1], b.x, b.y);
+              mma<kB>(second, c0[2], c1[2], c0[3], c1[3], b.z, b.w);
+            }
+            if (kZeroMma) {
+              mma<kB>(lo[m], z0.lo ^ kMinus, z1.lo ^ kMinus, z0.lo ^ kMinus, z1.lo ^ kMinus, b.x, b.y);
+              mma<kB>(second, z0.hi ^ kMinus, z1.hi ^ kMinus, z0.hi ^ kMinus, z1.hi ^ kMinus, b.z, b.w);
+            }
+          }
+        }
+      }
+      float s0, s1;
+      scales(sw, s0, s1);
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          out[m][k] = fmaf(kB ? lo[m][k] : fmaf(hi[m][k], 0.0625f, lo[m][k]), k < 2 ? s0 : s1, out[m][k]);
+    }
+  };
+  auto multiply_any = [&](auto octets, uint32_t wt, uint32_t act, int a0, int n) {
+    constexpr int MT = decltype(octets)::value;
     float lo[MT][4] = {}, hi[MT][4] = {};
-    uint32_t zs = 0, zz = 0;
-    int left = 0, g = 0;  // atoms left of the group, group of the unit
-    left = apg - (a0 - g0 * apg);
+    int left = apg - a0 % apg, g = 0;  // atoms left of the group, group of the unit
+    float s0 = 0.f, s1 = 0.f;
+    uint32_t zz = 0;
     auto group = [&]() {
-      const uint32_t s0 = g < 4 ? u.s[0] : u.s[1], z0 = g < 4 ? u.z[0] : u.z[1];
-      zs = __shfl_sync(kFull, s0, (g & 3) * 8 + lane / 4);
-      zz = __shfl_sync(kFull, z0, (g & 3) * 8 + lane / 4);
+      const uint32_t at = wt + kUnitBytes + (uint32_t)(8 * g + lane / 4) * 4u;
+      uint32_t sw, zw;
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(sw) : "r"(at) : "memory");
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(zw) : "r"(at + 128u) : "memory");
+      zz = zw >> (lane / 4 % 4 * 8);
+      scales(sw, s0, s1);
     };
     group();
 #pragma unroll
     for (int j = 0; j < kUnit; ++j) {
       if (j >= n) break;
+      const uint4 v = tc::lds128(wt + 512u * j + 16u * lane);
       const Zero<kB> z0(zz & 15u), z1((zz >> 4) & 15u);
-      const uint32_t w[4] = {u.w[j].x, u.w[j].y, u.w[j].z, u.w[j].w};
+      const uint32_t wd[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         uint32_t c0[4], c1[4];
-        codes<kB>(w[2 * s], z0, c0);
-        codes<kB>(w[2 * s + 1], z1, c1);
+        codes<kB>(wd[2 * s], z0, c0);
+        codes<kB>(wd[2 * s + 1], z1, c1);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-          const uint4 b = tc::lds128(act + m * 8 * row_bytes + j * 128 + s * 64);
+          const uint4 b = tc::lds128(act + m * 8 * kRowBytes + j * 128 + s * 64);
           mma<kB>(lo[m], c0[0], c1[0], c0[1], c1[1], b.x, b.y);
           mma<kB>(kB ? lo[m] : hi[m], c0[2], c1[2], c0[3], c1[3], b.z, b.w);
         }
       }
       if (--left == 0 || j + 1 == n) {
-        const float scale = kB ? 1.f : 16777216.f;
-        const float s0 = value16<false>(zs & 0xffffu) * scale, s1 = value16<false>(zs >> 16) * scale;
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float v = kB ? lo[m][i] : fmaf(hi[m][i], 0.0625f, lo[m][i]);
-            out[m][i] = fmaf(v, i < 2 ? s0 : s1, out[m][i]);
+            out[m][i] = fmaf(kB ? lo[m][i] : fmaf(hi[m][i], 0.0625f, lo[m][i]), i < 2 ? s0 : s1, out[m][i]);
             lo[m][i] = hi[m][i] = 0.f;
           }
         if (left == 0 && j + 1 < n) {
@@ -227,153 +457,77 @@ struct Strip {
         }
       }
     }
-  }
-};
+  };
+  auto multiply = [&](auto octets, uint32_t wt, uint32_t act, int a0, int n) {
+    if constexpr (kPairs) multiply_pairs(octets, wt, act, n);
+    else multiply_any(octets, wt, act, a0, n);
+  };
 
-// The piece `c` of every part's activations: rows of `chunk` atoms, parts
-// after one another. All threads of the block.
-template <int KS>
-__device__ __forceinline__ void copy_piece(const DecodeParams& p, const int* src, int n, uint32_t to, int c, int natoms,
-                                           int row_bytes, uint32_t dyn) {
-  const int vecs = p.chunk * 8;  // of a row of a part
-  for (int i = threadIdx.x; i < n * KS * vecs; i += kThreads) {
-    const int v = i % vecs, r = i / vecs % n, part = i / vecs / n;
-    const int begin = natoms * part / KS + c * p.chunk, end = natoms * (part + 1) / KS;
-    if (begin + v / 8 >= end) continue;
-    const uint16_t* from = p.a.A + (size_t)src[r] * p.a.K + begin * kAtomK + v * 8;
-    const uint32_t at = to + (uint32_t)((part * kRows + r) * row_bytes + v * 16);
-    if (in_smem(at, 16, dyn, p.a.err)) copy16(at, ld_at(from, p.a.A, a_elements(p.a) - 7, p.a.err));
-  }
-}
-
-template <bool kB, int KS, int MT>
-__device__ __forceinline__ void run_strip(const DecodeParams& p, const Strip<kB, KS>& st, const int* src, int n, int part,
-                                          uint32_t buffers, int row_bytes, uint32_t dyn, float (&out)[2][4]) {
-  const int lane = threadIdx.x % 32;
-  const int begin = st.natoms * part / KS;
-  const uint32_t piece_bytes = (uint32_t)(KS * kRows * row_bytes);
-  const bool live = st.strip >= 0;
-  Unit cur, next;
-  float acc[MT][4] = {};
-  // (weights first: they are what the block waits for)
-  if (live && begin < st.end) st.load(cur, begin, min(kUnit, min(p.chunk, st.end - begin)));
-  copy_piece<KS>(p, src, n, buffers, 0, st.natoms, row_bytes, dyn);
-  copies_commit();
-  for (int c = 0; c < p.pieces; ++c) {
-    if (c + 1 < p.pieces) {
-      copy_piece<KS>(p, src, n, buffers + ((c + 1) & 1) * piece_bytes, c + 1, st.natoms, row_bytes, dyn);
-      copies_commit();
-      copies_wait<1>();
-    } else {
-      copies_wait<0>();
-    }
+  // every step commits one group of copies: weights of unit s + 3, activations
+  // of unit s + 2
+  enter();
+  for (int u = 0; u < kWeightSlots - 1; ++u) {
+    copy_weights();
+    if (u > 0) copy_rows();
+    copies_commit();
+    // (items that the stream has entered are written down for the next one)
     __syncthreads();
-    const uint32_t act = buffers + (c & 1) * piece_bytes + (uint32_t)((part * kRows + lane / 4) * row_bytes + (lane % 4) * 16);
-    const int a1 = begin + c * p.chunk, a2 = min(a1 + p.chunk, st.end);
-    if (live)
-      for (int a0 = a1; a0 < a2; a0 += kUnit) {
-        const int len = min(kUnit, a2 - a0), after = a0 + len;
-        // the next unit, in this piece or the next
-        if (after < st.end)
-          st.load(next, after, after < a2 ? min(kUnit, a2 - after) : min(kUnit, min(p.chunk, st.end - after)));
-        const uint32_t at = act + (uint32_t)(a0 - a1) * 128;
-        if (in_smem(at, (uint32_t)((MT - 1) * 8 * row_bytes + (len - 1) * 128 + 80), dyn, p.a.err))
-          st.template multiply<MT>(acc, cur, at, (uint32_t)row_bytes, a0, len);
-        cur = next;
-      }
-    __syncthreads();  // the buffer is free for the piece after the next
   }
+  int cslot = 0, aslot = 0;
+  for (int i = 0; i < count; ++i) {
+    const Item& it = items[i % kItems];
+    for (int u = 0; u < units; ++u) {
+      copies_wait<kWeightSlots - 3>();  // this step's weights and activations
+      __syncthreads();
+      copy_weights();
+      copy_rows();
+      copies_commit();
+      const int a0 = begin + u * kUnit, n = min(kUnit, end - a0);
+      if (n > 0 && it.e < a.E) {
+        const uint32_t wt = weights + (uint32_t)cslot * kSlotBytes;
+        const uint32_t act = rows + (uint32_t)aslot * row_slot + (uint32_t)(part * p.rows + lane / 4) * kRowBytes + lane % 4 * 16u;
+        if (it.n <= 8)
+          multiply(std::integral_constant<int, 1>(), wt, act, a0, n);
+        else
+          multiply(std::integral_constant<int, 2>(), wt, act, a0, n);
+      }
+      cslot = cslot + 1 == kWeightSlots ? 0 : cslot + 1;
+      aslot = aslot + 1 == kRowSlots ? 0 : aslot + 1;
+    }
+    // sums by row: lane (g, t) holds columns g, g + 8 of rows 2t, 2t + 1
 #pragma unroll
-  for (int m = 0; m < 2; ++m)
+    for (int m = 0; m < 2; ++m)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) out[m][i] = m < MT ? acc[m < MT ? m : 0][i] : 0.f;
-}
-
-template <bool kB, int KS>
-__global__ void __launch_bounds__(kThreads, 2) experts_decode_kernel(const DecodeParams p) {
-  constexpr int S = kWarps / KS;        // strips of a block
-  constexpr int kCols = S * kStripCols;
-  constexpr int kRed = kCols + 4;       // floats of a row of partial sums
-  extern __shared__ __align__(16) uint8_t dynamic[];
-  __shared__ float red[KS][kRows][kRed];
-  __shared__ int src[kRows], of[kRows];
-  __shared__ RowTile tile;
-  const ExpertArgs& a = p.a;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const uint32_t dyn = (uint32_t)__cvta_generic_to_shared(dynamic);
-  allow_dependent_launch();
-  grid_dependency_wait();
-  if (warp == 0) {
-    const RowTile t = find_tile(a, blockIdx.x, lane);
-    if (lane == 0) tile = t;
-    if (lane < kRows) {
-      const int f = lane < t.n ? choice_of(a, t.first + lane) : -1;
-      of[lane] = f;
-      src[lane] = f < 0 ? 0 : a.per_choice ? f : f / a.top;
+      for (int j = 0; j < 4; ++j) {
+        red[part][m * 8 + (lane % 4) * 2 + (j & 1)][w * kStripCols + lane / 4 + (j & 2) * 4] = out[m][j];
+        out[m][j] = 0.f;
+      }
+    __syncthreads();
+    const int n0 = it.col * cols;
+    for (int k = threadIdx.x; k < it.n * (cols / 2); k += kThreads) {
+      const int r = k / (cols / 2), c = k % (cols / 2) * 2, n = n0 + c;
+      if (it.of[r] < 0 || n >= width || (a.combine && it.e >= a.E)) continue;
+      float v[2] = {0.f, 0.f}, g[2] = {0.f, 0.f};
+#pragma unroll
+      for (int q = 0; q < KS; ++q)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          v[j] += red[q][r][c + j];
+          if (a.silu) g[j] += red[q][r][kCols / 2 + c + j];
+        }
+      if (it.e >= a.E) v[0] = v[1] = g[0] = g[1] = 0.f;
+      const size_t at = (size_t)it.of[r] * width + n, everything = (size_t)choices(a) * width - 1;
+      if (a.combine) {
+        float* d = p.D + at;
+        if (in_buf(d, p.D, everything, a.err)) *reinterpret_cast<float2*>(d) = make_float2(v[0], v[1]);
+      } else {
+        if (a.silu) v[0] = silu_times(v[0], g[0]), v[1] = silu_times(v[1], g[1]);
+        uint16_t* y = a.Y + at;
+        if (in_buf(y, a.Y, everything, a.err)) *reinterpret_cast<uint32_t*>(y) = pack16<kB>(v[0], v[1]);
+      }
     }
   }
-  __syncthreads();
-  const RowTile t = tile;
-  if (t.n <= 0) return;
-  const int half = a.N / 2, width = a.silu ? half : a.N;       // of a result's row
-  const int cols = a.silu ? kCols / 2 : kCols;                 // of this block
-  const int n0 = blockIdx.y * cols;
-  if (t.e == a.E) {  // choices of no expert
-    if (!a.combine)
-      for (int i = threadIdx.x; i < t.n * cols; i += kThreads) {
-        const int r = i / cols, n = n0 + i % cols;
-        uint16_t* y = a.Y + (size_t)of[r] * width + n;
-        if (of[r] >= 0 && n < width && in_buf(y, a.Y, (size_t)choices(a) * width, a.err)) *y = 0;
-      }
-    return;
-  }
-  // this warp's strip: with silu the block's first half are gate columns, the
-  // second the up columns of the same results
-  const int part = warp / S, w = warp % S;
-  int strip = blockIdx.y * S + w;
-  bool live = strip < a.N / kStripCols;
-  if (a.silu) {
-    const int i = blockIdx.y * (S / 2) + w % (S / 2);
-    live = i < half / kStripCols;
-    strip = i + (w < S / 2 ? 0 : half / kStripCols);
-  }
-  const int natoms = a.K / kAtomK;
-  const Strip<kB, KS> st = {p, live ? t.e * (a.N / kStripCols) + strip : -1, natoms * (part + 1) / KS, natoms,
-                            a.group / kAtomK, a.K / a.group, lane};
-  const int row_bytes = p.chunk * 128 + kRowPad;
-  float out[2][4];
-  if (t.n <= 8)
-    run_strip<kB, KS, 1>(p, st, src, t.n, part, dyn, row_bytes, dyn, out);
-  else
-    run_strip<kB, KS, 2>(p, st, src, t.n, part, dyn, row_bytes, dyn, out);
-  // sums by token: lane (g, t) holds columns g, g + 8 of tokens 2t, 2t + 1
-#pragma unroll
-  for (int m = 0; m < 2; ++m)
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      red[part][m * 8 + (lane % 4) * 2 + (i & 1)][w * kStripCols + lane / 4 + (i & 2) * 4] = out[m][i];
-  __syncthreads();
-  for (int i = threadIdx.x; i < t.n * (cols / 2); i += kThreads) {
-    const int r = i / (cols / 2), c = i % (cols / 2) * 2, n = n0 + c;
-    if (of[r] < 0 || n >= width) continue;
-    float v[2] = {0.f, 0.f}, u[2] = {0.f, 0.f};
-#pragma unroll
-    for (int k = 0; k < KS; ++k)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        v[j] += red[k][r][c + j];
-        if (a.silu) u[j] += red[k][r][kCols / 2 + c + j];
-      }
-    const size_t at = (size_t)of[r] * width + n, all = (size_t)choices(a) * width - 1;
-    if (a.combine) {
-      float* d = p.D + at;
-      if (in_buf(d, p.D, all, a.err)) *reinterpret_cast<float2*>(d) = make_float2(v[0], v[1]);
-    } else {
-      if (a.silu) v[0] = silu_times(v[0], u[0]), v[1] = silu_times(v[1], u[1]);
-      uint16_t* y = a.Y + at;
-      if (in_buf(y, a.Y, all, a.err)) *reinterpret_cast<uint32_t*>(y) = pack16<kB>(v[0], v[1]);
-    }
-  }
+  copies_wait<0>();
 }
 
 // Eight columns of a row of products, 16-bit or fp32.
@@ -428,30 +582,62 @@ cudaError_t launch_sum(const ExpertArgs& a, const T* D, bool bf16, cudaStream_t 
               : launch_pdl(experts_sum_kernel<false, T>, grid, dim3(kThreads), 0, stream, a, D);
 }
 
-template <bool kB, int KS>
-cudaError_t launch_decode_ks(DecodeParams p, cudaStream_t stream) {
-  constexpr int S = kWarps / KS;
+// Blocks of an SM: two where its 228 KB hold 74 KB of weights, 1.7 KB for each
+// part's row of activations, and 15 KB of the rest twice.
+int blocks_per_sm(int parts, int T) { return parts * (T <= 8 ? 8 : kRows) <= 16 ? 2 : 1; }
+
+template <bool kB, int KS, bool kPairs>
+cudaError_t launch_decode_kernel(DecodeParams p, int sms, cudaStream_t stream) {
   const ExpertArgs& a = p.a;
-  const int natoms = a.K / kAtomK, longest = (natoms + KS - 1) / KS;
-  // the activations of all of K at once where they fit, else in pieces
-  const auto bytes = [](int atoms) { return KS * kRows * (atoms * 128 + kRowPad); };
-  p.chunk = bytes(longest) <= 72 * 1024 ? longest : KS == 1 ? 16 : 8;
-  p.pieces = (longest + p.chunk - 1) / p.chunk;
-  const int smem = bytes(p.chunk) * (p.pieces > 1 ? 2 : 1);
-  cudaError_t e = set_max_smem_once(reinterpret_cast<const void*>(experts_decode_kernel<kB, KS>), 160 * 1024);
+  const auto kernel = experts_decode_kernel<kB, KS, kPairs>;
+  constexpr int weights = kWarps * kWeightSlots * kSlotBytes, row = kRowSlots * KS * kRowBytes;
+  cudaError_t e = set_max_smem_once(reinterpret_cast<const void*>(kernel), weights + row * kRows);
   if (e != cudaSuccess) return e;
-  const int strips = a.N / kStripCols, per = a.silu ? S / 2 : S, n = a.silu ? strips / 2 : strips;
-  const int tiles = choices(a) / kRows + (choices(a) < a.E + 1 ? choices(a) : a.E + 1);
-  // (row tiles first: those of one expert read the same weights)
-  const dim3 grid((unsigned)tiles, (unsigned)((n + per - 1) / per));
-  return launch_pdl(experts_decode_kernel<kB, KS>, grid, dim3(kThreads), (size_t)smem, stream, p);
+  // no more blocks than there can be items
+  const long long most = (long long)(choices(a) / kRows + (choices(a) < a.E + 1 ? choices(a) : a.E + 1)) * p.blocks;
+  const long long resident = (long long)blocks_per_sm(KS, a.T) * sms;
+  const dim3 grid((unsigned)(most < resident ? most : resident));
+  return launch_pdl(kernel, grid, dim3(kThreads), (size_t)(weights + row * p.rows), stream, p);
+}
+
+template <bool kB, int KS>
+cudaError_t launch_decode_ks(DecodeParams p, int column_blocks, int sms, cudaStream_t stream) {
+  p.blocks = column_blocks;
+  p.rows = p.a.T <= 8 ? 8 : kRows;  // (a token has an expert once)
+  return p.a.group == 2 * kAtomK ? launch_decode_kernel<kB, KS, true>(p, sms, stream)
+                                 : launch_decode_kernel<kB, KS, false>(p, sms, stream);
+}
+
+// Parts of K: the items that a call is likely to have (each expert's rows, if
+// every choice were as likely) are to fill the blocks, and their rounds to be
+// short: of 1, 2 and 4 parts the fewest rounds times the work of an item, the
+// fewer parts where two are alike.
+int choose_parts(const ExpertArgs& a, int sms) {
+  const double experts = a.E * (1.0 - std::pow(1.0 - 1.0 / a.E, (double)choices(a)));
+  const double tiles = experts + (double)choices(a) / kRows / 2;
+  int best = 1;
+  double least = 0;
+  for (int parts = 1; parts <= 4; parts *= 2) {
+    const int per = kWarps / parts * kStripCols / (a.silu ? 2 : 1);  // results of an item
+    const int blocks = ((a.silu ? a.N / 2 : a.N) + per - 1) / per;
+    const int resident = sms * blocks_per_sm(parts, a.T);
+    const double cost = std::ceil(tiles * blocks / resident) / parts;
+    if (parts == 1 || cost < 0.95 * least) {
+      least = cost;
+      best = parts;
+    }
+  }
+  return best;
 }
 
 template <bool kB>
-cudaError_t launch_experts_decode_t(const DecodeParams& p, int parts, cudaStream_t stream) {
-  return parts == 4   ? launch_decode_ks<kB, 4>(p, stream)
-         : parts == 2 ? launch_decode_ks<kB, 2>(p, stream)
-                      : launch_decode_ks<kB, 1>(p, stream);
+cudaError_t launch_experts_decode_t(const DecodeParams& p, int sms, cudaStream_t stream) {
+  const int parts = choose_parts(p.a, sms);
+  const int per = kWarps / parts * kStripCols / (p.a.silu ? 2 : 1);
+  const int blocks = ((p.a.silu ? p.a.N / 2 : p.a.N) + per - 1) / per;
+  return parts == 4   ? launch_decode_ks<kB, 4>(p, blocks, sms, stream)
+         : parts == 2 ? launch_decode_ks<kB, 2>(p, blocks, sms, stream)
+                      : launch_decode_ks<kB, 1>(p, blocks, sms, stream);
 }
 
 }  // namespace
@@ -464,8 +650,8 @@ cudaError_t launch_experts_decode(ExpertArgs a, bool bf16, void* workspace, cuda
   cudaError_t e = device_error_word(&a.err);
   if (e != cudaSuccess) return e;
   DecodeParams p = {a, workspace ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kWorkspaceFlags) : nullptr, 0, 0};
-  const int parts = 1;
-  e = bf16 ? launch_experts_decode_t<true>(p, parts, stream) : launch_experts_decode_t<false>(p, parts, stream);
+  const int sms = device_sms();
+  e = bf16 ? launch_experts_decode_t<true>(p, sms, stream) : launch_experts_decode_t<false>(p, sms, stream);
   return e != cudaSuccess || !a.combine ? e : launch_sum(a, p.D, bf16, stream);
 }
 

@@ -47,20 +47,38 @@ def weights_of(pe):
     return torch.stack(out)
 
 
-def products(A, W, experts, weight_error=0.0):
+def terms_of(pe, dtype):
+    """[experts, K, N]: what the path for few rows adds up for a weight, in
+    magnitude. Where an expert has up to 8 rows it does not subtract the zero
+    point from the code but its product from the code's: (c + q) s and (c + z) s
+    with c = 0, in bf16 128 (the form that the codes have there)."""
+    c = 128 if dtype == torch.bfloat16 else 0
+    out = []
+    for e in range(pe.experts):
+        q, s, z = w4.unpack(pe.expert(e))
+        rep = lambda t: t.double().repeat_interleave(pe.group, 0)  # noqa: E731
+        out.append((2 * c + q.double() + rep(z)) * rep(s))
+    return torch.stack(out)
+
+
+def products(A, W, experts, weight_error=0.0, terms=None):
     """y [T, top, N] in 64 bits with zeros for choices of no expert, and the
-    bound of its error before the result's rounding: K additions in fp32, and
-    `weight_error` relative in each weight."""
+    bound of its error before the result's rounding: K additions in fp32 of
+    `terms` (default: the weights, in magnitude), and `weight_error` relative in
+    each weight."""
     T, top = experts.shape
     E, K, N = W.shape
     a = (A if A.dim() == 3 else A[:, None].expand(T, top, K)).double()
     y = torch.zeros((T, top, N), dtype=torch.float64, device=A.device)
-    mag = torch.zeros_like(y)
+    tol = torch.zeros_like(y)
     for e in range(E):
         t, j = torch.nonzero(experts == e, as_tuple=True)
         if len(t):
-            y[t, j], mag[t, j] = a[t, j] @ W[e], a[t, j].abs() @ W[e].abs()
-    return y, ((K + 8) * E32 + weight_error) * mag
+            y[t, j] = a[t, j] @ W[e]
+            mag = a[t, j].abs() @ W[e].abs()
+            added = mag if terms is None else a[t, j].abs() @ terms[e]
+            tol[t, j] = (K + 8) * E32 * added + weight_error * mag
+    return y, tol
 
 
 def silu_mul(y, tol):

@@ -140,8 +140,9 @@ def check_products(g, pe, routing, dtype, path, silu=True, plain=True, combine=T
     W = ref.weights_of(pe)
     tokens, each = normal(g, T, pe.K, dtype=dtype), normal(g, T, top, pe.K, dtype=dtype)
     u = rounding(path, dtype)
+    terms = ref.terms_of(pe, dtype) if path == "decode" else None
     for A in (tokens, each):
-        y, tol = ref.products(A, W, routing.experts, u)
+        y, tol = ref.products(A, W, routing.experts, u, terms)
         if plain:
             full, out = guarded(T, top, pe.N, dtype=dtype)
             assert w4.gemm_experts(A, pe, routing, path=path, out=out) is out
@@ -163,7 +164,7 @@ def check_products(g, pe, routing, dtype, path, silu=True, plain=True, combine=T
 
 
 PATHS = ["decode", "tensor-pair"]
-SHAPES = [(1, 64, 16, 64), (8, 128, 32, 64), (5, 192, 208, 64), (4, 256, 288, 256), (3, 1024, 160, 128),
+SHAPES = [(1, 64, 16, 64), (7, 128, 48, 128), (4, 640, 96, 128), (8, 128, 32, 64), (5, 192, 208, 64), (4, 256, 288, 256), (3, 1024, 160, 128),
           (4, 1408, 96, 64), (2, 2048, 544, 128), (16, 384, 64, 384), (2, 4096, 48, 512), (2, 5120, 32, 1024)]
 
 
@@ -300,10 +301,10 @@ def test_a_layer_of_experts():
     got = w4.gemm_experts(h, down, routing, combine=True)
     e, w, _, _, _ = ref.route(logits, top, "softmax", True)
     u = ref.WEIGHT_ERROR[FP16]
-    y, tol = ref.products(x, ref.weights_of(gate_up), e, u)
+    y, tol = ref.products(x, ref.weights_of(gate_up), e, u, ref.terms_of(gate_up, FP16))
     act, tol = ref.silu_mul(y, tol)
     W = ref.weights_of(down)
-    y, t2 = ref.products(act, W, e, u)
+    y, t2 = ref.products(act, W, e, u, ref.terms_of(down, FP16))
     # h's own error and rounding go through down
     _, mag = ref.products(tol + u * (act.abs() + tol), W.abs(), e)
     within(got, *ref.combine(y, t2 + mag / ((inner + 8) * ref.E32), w, e, u))
