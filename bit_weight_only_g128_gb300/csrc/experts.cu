@@ -323,24 +323,41 @@ __global__ void __launch_bounds__(kThreads, 2) experts_decode_kernel(const Decod
       enter();
     }
   };
-  // the block's stream of activations: a unit of every part, rows of 64 vectors
-  int ri = 0, ru = 0, rslot = 0;
+  // The block's stream of activations: a unit of every part. This warp copies
+  // the rows (warp + 8 m) / KS of part warp % KS, a lane 16 bytes of each; src:
+  // which rows of A those are for the item that the stream is in.
+  constexpr int kPasses = kRows * KS / kWarps;
+  int ri = 0, ru = 0, rslot = 0, rn = 0;  // rn: the item's rows
+  int src[kPasses];
+  const int rbegin = part_begin(warp % KS), rend = part_begin(warp % KS + 1);
+  auto enter_rows = [&]() {
+    rn = 0;
+    if (ri >= count) return;
+    const Item& it = items[ri % kItems];
+    if (it.e < a.E) rn = it.n;
+#pragma unroll
+    for (int m = 0; m < kPasses; ++m) src[m] = it.src[(warp + kWarps * m) / KS];
+  };
   auto copy_rows = [&]() {
-    if (ri < count) {
-      const Item& it = items[ri % kItems];
-      const int n = it.e < a.E ? it.n : 0;
-      const uint32_t to = rows + (uint32_t)rslot * row_slot;
-      const int v = threadIdx.x % (8 * kUnit);  // 16 bytes of a row
-      for (int i = threadIdx.x / (8 * kUnit); i < n * KS; i += kThreads / (8 * kUnit)) {
-        const int r = KS == 1 ? i : i / KS, k = KS == 1 ? 0 : i % KS;
-        const int a0 = part_begin(k) + ru * kUnit;
-        const uint32_t at = to + (uint32_t)(k * p.rows + r) * kRowBytes + 16u * v;
-        if (a0 + v / 8 < part_begin(k + 1) && in_smem(at, 16, dyn, a.err))
-          copy16(at, ld_at(a.A + (size_t)it.src[r] * a.K + a0 * kAtomK + v * 8, a.A, a_elements(a) - 7, a.err));
+    const int k0 = rbegin + ru * kUnit + lane / 8;  // the lane's atom
+    if (k0 < rend) {
+      const uint32_t to = rows + (uint32_t)rslot * row_slot +
+                          (uint32_t)(warp % KS * p.rows + warp / KS) * kRowBytes + 16u * lane;
+      const uint16_t* from = a.A + k0 * kAtomK + lane % 8 * 8;
+#pragma unroll
+      for (int m = 0; m < kPasses; ++m) {
+        if ((warp + kWarps * m) / KS >= rn) break;
+        const uint32_t at = to + (uint32_t)(m * (kWarps / KS)) * kRowBytes;
+        if (in_smem(at, 16, dyn, a.err))
+          copy16(at, ld_at(from + (uint64_t)(uint32_t)src[m] * (uint32_t)a.K, a.A, a_elements(a) - 7, a.err));
       }
     }
     rslot = rslot + 1 == kRowSlots ? 0 : rslot + 1;
-    if (++ru == units) ru = 0, ++ri;
+    if (++ru == units) {
+      ru = 0;
+      ++ri;
+      enter_rows();
+    }
   };
 
   float out[2][4] = {};
@@ -349,15 +366,14 @@ __global__ void __launch_bounds__(kThreads, 2) experts_decode_kernel(const Decod
     s0 = value16<false>(sw & 0xffffu) * scale, s1 = value16<false>(sw >> 16) * scale;
   };
   // out += a unit's products: MT octets of rows
-  auto multiply_pairs = [&](auto octets, uint32_t wt, uint32_t act, int n) {
+  auto multiply_pairs = [&](auto octets, uint32_t wt, uint32_t act, int i0, int i1) {  // the pairs i0 .. i1
     constexpr int MT = decltype(octets)::value;
     // One octet: the zero points go in by MMAs of their own, with the constant
     // row -z, four a pair of atoms and octet against 32 subtractions that serve
     // all octets: for two octets the subtractions are cheaper.
     constexpr bool kZeroMma = MT == 1;
 #pragma unroll
-    for (int i = 0; i < kUnit / 2; ++i) {
-      if (2 * i >= n) break;
+    for (int i = i0; i < i1; ++i) {
       uint32_t sw, zw;
       asm volatile("ld.shared.u32 %0, [%1];" : "=r"(sw) : "r"(wt + kUnitBytes + (uint32_t)(8 * i + lane / 4) * 4u) : "memory");
       asm volatile("ld.shared.u32 %0, [%1];" : "=r"(zw) : "r"(wt + kUnitBytes + 64u + (uint32_t)(2 * i + lane / 16) * 4u) : "memory");
@@ -459,13 +475,17 @@ __global__ void __launch_bounds__(kThreads, 2) experts_decode_kernel(const Decod
     }
   };
   auto multiply = [&](auto octets, uint32_t wt, uint32_t act, int a0, int n) {
-    if constexpr (kPairs) multiply_pairs(octets, wt, act, n);
+    if constexpr (kPairs) {
+      if (n == kUnit) multiply_pairs(octets, wt, act, 0, kUnit / 2);  // (a constant number, without branches)
+      else multiply_pairs(octets, wt, act, 0, 1);
+    }
     else multiply_any(octets, wt, act, a0, n);
   };
 
   // every step commits one group of copies: weights of unit s + 3, activations
   // of unit s + 2
   enter();
+  enter_rows();
   for (int u = 0; u < kWeightSlots - 1; ++u) {
     copy_weights();
     if (u > 0) copy_rows();
