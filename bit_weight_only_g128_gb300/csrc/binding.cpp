@@ -126,6 +126,16 @@ at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const at::Device& d
   return at::detail::empty_cuda(shape, type, dev, std::nullopt);
 }
 
+// A contiguous tensor of 4-byte elements in the memory of `whole` (int32),
+// from its element `at` on (without the dispatcher's round).
+at::Tensor part_of(const at::Tensor& whole, int64_t at, at::IntArrayRef shape, at::ScalarType type) {
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(),
+                                                          c10::scalarTypeToTypeMeta(type));
+  t.unsafeGetTensorImpl()->set_storage_offset(at);
+  t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+  return t;
+}
+
 at::Tensor result(PyObject* given, const char* name, at::IntArrayRef shape, at::ScalarType type, const at::Device& dev) {
   if (given == Py_None) return fresh(shape, type, dev);
   const at::Tensor& t = tensor(given, name);
@@ -331,9 +341,9 @@ at::Tensor workspace(PyObject* given, size_t need, const at::Device& dev, const 
 }
 
 // rope_append(qkv, cos_sin, positions, slots, cache, interleaved, out, stream,
-// q_norm, k_norm, eps)
+// q_norm, k_norm, eps), or without the norms' three
 PyObject* rope_append(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
-  return guarded(nargs, 11, [&]() -> PyObject* {
+  return guarded(nargs, nargs == 8 ? 8 : 11, [&]() -> PyObject* {
     const at::Tensor& qkv = tensor(args[0], "qkv");
     const int flags = flags16(qkv, "qkv");
     const at::Device dev = qkv.device();
@@ -352,10 +362,13 @@ PyObject* rope_append(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     const int interleaved = PyObject_IsTrue(args[5]);
     if (interleaved < 0) throw Raised();
     const uint16_t *q_norm = nullptr, *k_norm = nullptr;
-    if (args[8] != Py_None) q_norm = flat<uint16_t>(tensor(args[8], "q_norm"), "q_norm", c.dim, type, dev);
-    if (args[9] != Py_None) k_norm = flat<uint16_t>(tensor(args[9], "k_norm"), "k_norm", c.dim, type, dev);
-    const double eps = PyFloat_AsDouble(args[10]);
-    if (eps == -1.0 && PyErr_Occurred()) throw Raised();
+    double eps = 0;
+    if (nargs > 8) {
+      if (args[8] != Py_None) q_norm = flat<uint16_t>(tensor(args[8], "q_norm"), "q_norm", c.dim, type, dev);
+      if (args[9] != Py_None) k_norm = flat<uint16_t>(tensor(args[9], "k_norm"), "k_norm", c.dim, type, dev);
+      eps = PyFloat_AsDouble(args[10]);
+      if (eps == -1.0 && PyErr_Occurred()) throw Raised();
+    }
     const CallStream stream(args[7], dev);
     const at::Tensor q = result(args[6], "out", {T, heads, c.dim}, type, dev);
     check(lib.rope_append_norm(static_cast<uint16_t*>(qkv.data_ptr()), ld, table, int32_of(cs.size(0), "table_len"),
@@ -456,17 +469,19 @@ PyObject* route(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     size_t need = 0;
     check(lib.route_workspace_size(t32, e32, k32, &need), "w4a16_route_workspace_size");
     const at::Tensor ws = workspace(args[4], need, dev, stream);
-    const at::Tensor experts = fresh({T, top}, at::kInt, dev), weights = fresh({T, top}, at::kFloat, dev);
-    const at::Tensor rows = fresh({T * top}, at::kInt, dev), offsets = fresh({E + 1}, at::kInt, dev);
+    // the four results in one allocation
+    const at::Tensor all = fresh({3 * T * top + E + 1}, at::kInt, dev);
+    const at::Tensor experts = part_of(all, 0, {T, top}, at::kInt), weights = part_of(all, T * top, {T, top}, at::kFloat);
+    const at::Tensor rows = part_of(all, 2 * T * top, {T * top}, at::kInt), offsets = part_of(all, 3 * T * top, {E + 1}, at::kInt);
     check(lib.route(x.data_ptr(), ld, t32, e32, k32, static_cast<int32_t*>(experts.data_ptr()), weights.data_ptr<float>(),
                     static_cast<int32_t*>(rows.data_ptr()), static_cast<int32_t*>(offsets.data_ptr()),
                     ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.nbytes() : 0, flags, stream.ptr),
           "w4a16_route");
     PyObject* t = PyTuple_New(4);
     if (!t) throw Raised();
-    const at::Tensor* all[4] = {&experts, &weights, &rows, &offsets};
+    const at::Tensor* parts[4] = {&experts, &weights, &rows, &offsets};
     for (int i = 0; i < 4; ++i) {
-      PyObject* o = wrap(*all[i]);
+      PyObject* o = wrap(*parts[i]);
       if (!o) {
         Py_DECREF(t);
         throw Raised();

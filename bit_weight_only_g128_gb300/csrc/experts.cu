@@ -37,7 +37,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = 8;
-constexpr int kRows = 16;      // rows of an item
+constexpr int kRows = 16;      // most rows of an item
 constexpr int kUnit = 4;       // atoms of a step
 constexpr int kWeightSlots = 4, kRowSlots = 3;  // units in shared memory: weights, activations
 constexpr int kUnitBytes = kUnit * kAtomWords * 4;         // a warp's codes of a unit
@@ -51,7 +51,8 @@ struct DecodeParams {
   ExpertArgs a;
   float* D;      // combined: [choices][N]
   int blocks;    // column blocks
-  int rows;      // rows of a part's activations in shared memory: 8 or 16
+  int tile;      // rows of an item at most: 8 or 16
+  int rows;      // of them, those that shared memory has room for: no more than T
 };
 
 __device__ __forceinline__ void copy16(uint32_t to, const void* from) {
@@ -201,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 2) experts_decode_kernel(const Decod
         // the tiles of expert e - 1, which ends here
         int before = __shfl_up_sync(kFull, m, 1);
         if (lane == 0) before = top;
-        int s = e > 0 && e <= a.E + 1 ? (m - before + kRows - 1) / kRows : 0;
+        int s = e > 0 && e <= a.E + 1 ? (m - before + p.tile - 1) / p.tile : 0;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
           const int u = __shfl_up_sync(kFull, s, d);
@@ -243,8 +244,12 @@ __global__ void __launch_bounds__(kThreads, 2) experts_decode_kernel(const Decod
         else hi = mid;
       }
       e = lo;
-      first = offs[e] + (tile - firsts[e]) * kRows;
-      n = min(kRows, offs[e + 1] - first);
+      first = offs[e] + (tile - firsts[e]) * p.tile;
+      n = min(p.tile, offs[e + 1] - first);
+      if (e < a.E && n > p.rows) {  // an expert with more choices than there are tokens
+        if (lane == 0) atomicOr(a.err, kErrRange);
+        n = p.rows;
+      }
     }
     Item& it = items[i % kItems];
     if (lane == 0) it.e = e, it.n = n, it.col = (int)(at / tiles);
@@ -602,62 +607,77 @@ cudaError_t launch_sum(const ExpertArgs& a, const T* D, bool bf16, cudaStream_t 
               : launch_pdl(experts_sum_kernel<false, T>, grid, dim3(kThreads), 0, stream, a, D);
 }
 
-// Blocks of an SM: two where its 228 KB hold 74 KB of weights, 1.7 KB for each
-// part's row of activations, and 15 KB of the rest twice.
-int blocks_per_sm(int parts, int T) { return parts * (T <= 8 ? 8 : kRows) <= 16 ? 2 : 1; }
+// How a call is laid out.
+struct Layout {
+  int tile, parts, blocks;  // rows of an item, parts of K, column blocks
+  int rows, smem, per_sm;   // rows of a part in shared memory, its bytes, blocks of an SM
+};
 
-template <bool kB, int KS, bool kPairs>
-cudaError_t launch_decode_kernel(DecodeParams p, int sms, cudaStream_t stream) {
-  const ExpertArgs& a = p.a;
-  const auto kernel = experts_decode_kernel<kB, KS, kPairs>;
-  constexpr int weights = kWarps * kWeightSlots * kSlotBytes, row = kRowSlots * KS * kRowBytes;
-  cudaError_t e = set_max_smem_once(reinterpret_cast<const void*>(kernel), weights + row * kRows);
-  if (e != cudaSuccess) return e;
-  // no more blocks than there can be items
-  const long long most = (long long)(choices(a) / kRows + (choices(a) < a.E + 1 ? choices(a) : a.E + 1)) * p.blocks;
-  const long long resident = (long long)blocks_per_sm(KS, a.T) * sms;
-  const dim3 grid((unsigned)(most < resident ? most : resident));
-  return launch_pdl(kernel, grid, dim3(kThreads), (size_t)(weights + row * p.rows), stream, p);
+// Dynamic shared memory: the warps' units of weights, the parts' rows (an octet
+// is read whole, whatever of it there is).
+int smem_bytes(int parts, int rows) {
+  return kWarps * kWeightSlots * kSlotBytes + (kRowSlots * parts * rows + (rows + 7) / 8 * 8 - rows) * kRowBytes;
 }
 
-template <bool kB, int KS>
-cudaError_t launch_decode_ks(DecodeParams p, int column_blocks, int sms, cudaStream_t stream) {
-  p.blocks = column_blocks;
-  p.rows = p.a.T <= 8 ? 8 : kRows;  // (a token has an expert once)
-  return p.a.group == 2 * kAtomK ? launch_decode_kernel<kB, KS, true>(p, sms, stream)
-                                 : launch_decode_kernel<kB, KS, false>(p, sms, stream);
-}
-
-// Parts of K: the items that a call is likely to have (each expert's rows, if
-// every choice were as likely) are to fill the blocks, and their rounds to be
-// short: of 1, 2 and 4 parts the fewest rounds times the work of an item, the
-// fewer parts where two are alike.
-int choose_parts(const ExpertArgs& a, int sms) {
+// Parts of K: of 1, 2 and 4 those with the fewest rounds of items (as many as
+// are likely, were every choice as likely) times the work of an item, the
+// fewer where two are alike: one token's gate and up over eight of 64 experts
+// take 8.4 us in two parts, 9.3 in one. Items have 16 rows where there can be more than
+// 8: gate and up of 16 tokens over 64 experts, top 8, bf16, take 36.5 us in
+// one part; items of 8 rows, which leave room for two blocks on an SM with two
+// parts, take 38.0.
+Layout choose_layout(const ExpertArgs& a, int sms) {
   const double experts = a.E * (1.0 - std::pow(1.0 - 1.0 / a.E, (double)choices(a)));
-  const double tiles = experts + (double)choices(a) / kRows / 2;
-  int best = 1;
+  Layout best = {};
   double least = 0;
   for (int parts = 1; parts <= 4; parts *= 2) {
+    Layout l;
+    l.tile = a.T <= 8 ? 8 : 16;
+    l.parts = parts;
     const int per = kWarps / parts * kStripCols / (a.silu ? 2 : 1);  // results of an item
-    const int blocks = ((a.silu ? a.N / 2 : a.N) + per - 1) / per;
-    const int resident = sms * blocks_per_sm(parts, a.T);
-    const double cost = std::ceil(tiles * blocks / resident) / parts;
+    l.blocks = ((a.silu ? a.N / 2 : a.N) + per - 1) / per;
+    l.rows = a.T < l.tile ? a.T : l.tile;
+    l.smem = smem_bytes(parts, l.rows);
+    l.per_sm = 2 * (l.smem + 15 * 1024) <= 228 * 1024 ? 2 : 1;  // (beside it 14 KB of the kernel's own and 1 KB)
+    const double tiles = experts + (double)choices(a) / l.tile / 2;
+    const double cost = std::ceil(tiles * l.blocks / (sms * l.per_sm)) / parts;
     if (parts == 1 || cost < 0.95 * least) {
       least = cost;
-      best = parts;
+      best = l;
     }
   }
   return best;
 }
 
+template <bool kB, int KS, bool kPairs>
+cudaError_t launch_decode_kernel(DecodeParams p, const Layout& l, int sms, cudaStream_t stream) {
+  const ExpertArgs& a = p.a;
+  const auto kernel = experts_decode_kernel<kB, KS, kPairs>;
+  cudaError_t e = set_max_smem_once(reinterpret_cast<const void*>(kernel),
+                                    kWarps * kWeightSlots * kSlotBytes + kRowSlots * KS * kRows * kRowBytes);
+  if (e != cudaSuccess) return e;
+  p.blocks = l.blocks;
+  p.tile = l.tile;
+  p.rows = l.rows;
+  // no more blocks than there can be items
+  const long long most = (long long)(choices(a) / l.tile + (choices(a) < a.E + 1 ? choices(a) : a.E + 1)) * l.blocks;
+  const long long resident = (long long)l.per_sm * sms;
+  const dim3 grid((unsigned)(most < resident ? most : resident));
+  return launch_pdl(kernel, grid, dim3(kThreads), (size_t)l.smem, stream, p);
+}
+
+template <bool kB, int KS>
+cudaError_t launch_decode_ks(const DecodeParams& p, const Layout& l, int sms, cudaStream_t stream) {
+  return p.a.group == 2 * kAtomK ? launch_decode_kernel<kB, KS, true>(p, l, sms, stream)
+                                 : launch_decode_kernel<kB, KS, false>(p, l, sms, stream);
+}
+
 template <bool kB>
 cudaError_t launch_experts_decode_t(const DecodeParams& p, int sms, cudaStream_t stream) {
-  const int parts = choose_parts(p.a, sms);
-  const int per = kWarps / parts * kStripCols / (p.a.silu ? 2 : 1);
-  const int blocks = ((p.a.silu ? p.a.N / 2 : p.a.N) + per - 1) / per;
-  return parts == 4   ? launch_decode_ks<kB, 4>(p, blocks, sms, stream)
-         : parts == 2 ? launch_decode_ks<kB, 2>(p, blocks, sms, stream)
-                      : launch_decode_ks<kB, 1>(p, blocks, sms, stream);
+  const Layout l = choose_layout(p.a, sms);
+  return l.parts == 4   ? launch_decode_ks<kB, 4>(p, l, sms, stream)
+         : l.parts == 2 ? launch_decode_ks<kB, 2>(p, l, sms, stream)
+                        : launch_decode_ks<kB, 1>(p, l, sms, stream);
 }
 
 }  // namespace
@@ -669,7 +689,7 @@ size_t experts_decode_workspace_bytes(int choices, int N, bool combine) {
 cudaError_t launch_experts_decode(ExpertArgs a, bool bf16, void* workspace, cudaStream_t stream) {
   cudaError_t e = device_error_word(&a.err);
   if (e != cudaSuccess) return e;
-  DecodeParams p = {a, workspace ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kWorkspaceFlags) : nullptr, 0, 0};
+  DecodeParams p = {a, workspace ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kWorkspaceFlags) : nullptr, 0, 0, 0};
   const int sms = device_sms();
   e = bf16 ? launch_experts_decode_t<true>(p, sms, stream) : launch_experts_decode_t<false>(p, sms, stream);
   return e != cudaSuccess || !a.combine ? e : launch_sum(a, p.D, bf16, stream);

@@ -29,7 +29,7 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kOneBlock = 64;  // tokens
-constexpr int kBlocks = 152;   // most blocks of the two-kernel form
+constexpr int kBlocks = 76;    // most blocks of the two-kernel form
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr uint32_t kLowest = 0x007fffffu;  // the ordered pattern of -inf
 
@@ -208,9 +208,12 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const RouteArgs a) {
   __syncthreads();
   grid_dependency_wait();
   const int t0 = blockIdx.x * a.per, t1 = min(t0 + a.per, a.T);
-  float x[V];
+  float x[V], ahead[V];
+  if (t0 + warp < t1) load_logits(a, t0 + warp, lane, ahead);
   for (int t = t0 + warp; t < t1; t += kWarps) {
-    load_logits(a, t, lane, x);
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = ahead[i];
+    if (t + kWarps < t1) load_logits(a, t + kWarps, lane, ahead);
     const int e = choose(a, t, lane, x);
     if (lane < a.k) atomicAdd(shared + (e < 0 ? a.E : e), 1);
   }
@@ -241,11 +244,19 @@ __global__ void __launch_bounds__(kThreads) place_kernel(const RouteArgs a) {
   const int parts = max(1, kThreads / bins), part = threadIdx.x / bins;
   for (int e = threadIdx.x % bins; part < parts && e < bins; e += kThreads) {
     int all = 0, own = 0;
-#pragma unroll 4
-    for (int b = part; b < a.blocks; b += parts) {
-      const int n = __ldcg(ld_at(a.hist + (size_t)b * bins + e, a.hist, (size_t)a.blocks * bins, a.err));
-      all += n;
-      own += b < (int)blockIdx.x ? n : 0;
+    constexpr int kFlight = 12;  // counts in flight
+    for (int b0 = part; b0 < a.blocks; b0 += parts * kFlight) {
+      int n[kFlight];
+#pragma unroll
+      for (int i = 0; i < kFlight; ++i) {
+        const int b = b0 + i * parts;
+        n[i] = b < a.blocks ? __ldcg(ld_at(a.hist + (size_t)b * bins + e, a.hist, (size_t)a.blocks * bins, a.err)) : 0;
+      }
+#pragma unroll
+      for (int i = 0; i < kFlight; ++i) {
+        all += n[i];
+        own += b0 + i * parts < (int)blockIdx.x ? n[i] : 0;
+      }
     }
     atomicAdd(first + e, all);
     atomicAdd(before + e, own);

@@ -162,8 +162,10 @@ def rope_append(qkv: torch.Tensor, cos_sin: torch.Tensor, positions: torch.Tenso
     query (key) head is x * (mean x^2 + eps)^(-1/2) * weight before its
     rotation, in the same pass.
     """
-    return (_native_module or _native()).rope_append(qkv, cos_sin, positions, slots, cache, interleaved, out, stream,
-                                                     q_norm, k_norm, eps)
+    native = _native_module or _native()
+    if q_norm is None and k_norm is None:
+        return native.rope_append(qkv, cos_sin, positions, slots, cache, interleaved, out, stream)
+    return native.rope_append(qkv, cos_sin, positions, slots, cache, interleaved, out, stream, q_norm, k_norm, eps)
 
 
 def attn_workspace_size(tokens: int, batch: int, heads: int, kv_heads: int, head_dim: int) -> int:

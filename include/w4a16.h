@@ -406,7 +406,7 @@ int w4a16_rope_append(const uint16_t* qkv, int64_t qkv_stride, const float* cos_
 /* As w4a16_rope_append with a norm of every query head and every key head
  * before the rotation: in fp32, x * (mean_d x^2 + eps)^(-1/2) * weight[d],
  * with the weights q_norm of queries and k_norm of keys, [head_dim] in qkv's
- * type, each null where its heads have no norm (2-byte aligned; 16 bytes run
+ * type, each null where its heads have no norm (2-byte aligned; 4 bytes run
  * faster). Nothing is rounded between norm, rotation and the result. Values
  * pass through. */
 int w4a16_rope_append_norm(const uint16_t* qkv, int64_t qkv_stride, const float* cos_sin,

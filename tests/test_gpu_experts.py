@@ -170,7 +170,7 @@ SHAPES = [(1, 64, 16, 64), (7, 128, 48, 128), (4, 640, 96, 128), (8, 128, 32, 64
 
 @pytest.mark.parametrize("path", PATHS)
 @pytest.mark.parametrize("E,K,N,group", SHAPES)
-@pytest.mark.parametrize("T", [1, 2, 9, 40])
+@pytest.mark.parametrize("T", [1, 2, 9, 15, 40])
 @pytest.mark.parametrize("dtype", [FP16, BF16])
 def test_products(E, K, N, group, T, dtype, path):
     g = gen(E + K + N + T)
@@ -255,6 +255,25 @@ def test_bad_routing_is_recorded_and_touches_nothing_else(path):
         if lost is not None:  # every other choice as before, the one that is not listed left alone
             keep = [f for f in range(18) if f != lost]
             assert torch.equal(out.view(18, 64)[keep], want.view(18, 64)[keep]) and (out.view(18, 64)[lost] == 7).all()
+    w4.device_status()
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("T", [1, 3, 10, 20])
+def test_offsets_that_give_an_expert_everything_or_too_much(T, path):
+    """All choices with one expert, which no router answers: recorded or
+    computed, and nothing outside the result is written."""
+    g = gen(T)
+    pe = experts(g, 4, 256, 64, 128)
+    good = w4.route(normal(g, T, 4), 3)
+    bad = w4.Routing(good.experts, good.weights, good.rows, torch.tensor([0, 0, 3 * T, 3 * T, 3 * T], dtype=torch.int32, device="cuda"))
+    full, out = guarded(T, 3, 64, dtype=FP16)
+    w4.gemm_experts(normal(g, T, 256, dtype=FP16), pe, bad, path=path, out=out)
+    assert (full[:64] == 7).all() and (full[-64:] == 7).all()
+    try:
+        w4.device_status()
+    except w4.W4A16Error as e:
+        assert "0x80" in str(e)
     w4.device_status()
 
 
