@@ -8,6 +8,9 @@ Layers of the model's shape with seeded random weights take the prompts of
 GEMM, rotation with the cache's append, prompt attention, o_proj, norm, fused
 gate/up and down GEMMs, and then `steps` single tokens per sequence through
 the same with decode attention, the step captured once as a CUDA graph.
+A shape with experts has a router, products grouped by expert and their
+weighted sum in place of gate/up and down (in 16 bits, with --a8 too); one
+with qk_norm norms every query and key head in the pass that rotates them.
 Prints one JSON line: the prompts' and a step's time per layer. ``Stack`` is
 the same for use from Python.
 """
@@ -16,7 +19,7 @@ from __future__ import annotations
 import argparse
 import dataclasses
 import json
-from typing import List
+from typing import List, Optional, Union
 
 import torch
 
@@ -31,12 +34,17 @@ class Shape:
     intermediate: int
     head_dim: int = 128
     group: int = 128
+    experts: int = 0    # 0: one gate/up and down for all tokens
+    top_k: int = 0
+    qk_norm: bool = False
 
 
 SHAPES = {
     "llama2-7b": Shape(4096, 32, 32, 11008),
     "llama2-13b": Shape(5120, 40, 40, 13824),
     "llama2-70b": Shape(8192, 64, 8, 28672),
+    "experts-8x2": Shape(4096, 32, 8, 11008, experts=8, top_k=2),
+    "experts-64x8": Shape(2048, 16, 4, 1024, experts=64, top_k=8, qk_norm=True),
 }
 
 
@@ -44,11 +52,14 @@ SHAPES = {
 class Layer:
     qkv: w4.PackedWeight
     o: w4.PackedWeight
-    gate_up: w4.PackedWeight
-    down: w4.PackedWeight
+    gate_up: Union[w4.PackedWeight, w4.PackedExperts]
+    down: Union[w4.PackedWeight, w4.PackedExperts]
     norm1: torch.Tensor
     norm2: torch.Tensor
     cache: w4.KVCache
+    router: Optional[torch.Tensor] = None  # float32 [hidden, experts]
+    q_norm: Optional[torch.Tensor] = None
+    k_norm: Optional[torch.Tensor] = None
 
 
 def rotary_table(length: int, dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
@@ -86,15 +97,22 @@ class Stack:
         def weight(K, N):
             return w4.quantize_pack(torch.randn((K, N), generator=gen, device="cuda") * 0.02, shape.group)
 
-        def ones():
-            return (1 + 0.1 * torch.randn(shape.hidden, generator=gen, device="cuda")).to(dtype)
+        def ones(n=shape.hidden):
+            return (1 + 0.1 * torch.randn(n, generator=gen, device="cuda")).to(dtype)
+
+        def mlp(K, N):
+            if not shape.experts:
+                return weight(K, N)
+            return w4.stack_experts([weight(K, N) for _ in range(shape.experts)])
 
         h, d = shape.hidden, shape.head_dim
         self.layers: List[Layer] = [
             Layer(weight(h, (shape.heads + 2 * shape.kv_heads) * d), weight(shape.heads * d, h),
-                  weight(h, 2 * shape.intermediate), weight(shape.intermediate, h), ones(), ones(),
+                  mlp(h, 2 * shape.intermediate), mlp(shape.intermediate, h), ones(), ones(),
                   w4.new_kv_cache(batch * per, shape.kv_heads, page, d, torch.float8_e4m3fn if e4m3 else dtype,
-                                  scale, scale))
+                                  scale, scale),
+                  torch.randn((h, shape.experts), generator=gen, device="cuda") * h ** -0.5 if shape.experts else None,
+                  *((ones(d), ones(d)) if shape.qk_norm else (None, None)))
             for _ in range(layers)]
 
     def _norm_gemm(self, x, h, norm, pw, silu_mul=False):
@@ -108,11 +126,22 @@ class Stack:
     def _forward(self, x, h, positions, slots, attend):
         for layer in self.layers:
             qkv = self._norm_gemm(x, h, layer.norm1, layer.qkv)
-            q = w4.rope_append(qkv, self.cos_sin, positions, slots, layer.cache)
+            norms = dict(q_norm=layer.q_norm, k_norm=layer.k_norm) if self.shape.qk_norm else {}
+            q = w4.rope_append(qkv, self.cos_sin, positions, slots, layer.cache, **norms)
             x = w4.gemm(attend(q, layer.cache).flatten(1), layer.o, static_weights=True, a8=self.a8)
+            if self.shape.experts:
+                x = self._experts(x, h, layer)
+                continue
             y = self._norm_gemm(x, h, layer.norm2, layer.gate_up, silu_mul=True)
             x = w4.gemm(y, layer.down, static_weights=True, a8=self.a8)
         return h.add_(x)
+
+    def _experts(self, x, h, layer):
+        """The norm of x + h (h updated) through the tokens' experts."""
+        y, _ = w4.rms_norm(x, layer.norm2, residual=h, residual_out=h)
+        routing = w4.route(y.float() @ layer.router, self.shape.top_k)
+        y = w4.gemm_experts(y, layer.gate_up, routing, silu_mul=True)
+        return w4.gemm_experts(y, layer.down, routing, combine=True)
 
     def clear(self) -> None:
         """Forget the sequences' tokens."""
