@@ -73,6 +73,7 @@ struct TensorParams {
   ExpertArgs a;
   uint16_t* D;     // combined: [choices][N], the products
   int pairs;       // tiles along the columns
+  float inv_group;  // 1 / group
 };
 
 // Tile t of the launch (which lies in expert e's): 256 columns (with silu 128
@@ -88,7 +89,7 @@ constexpr int kActSlots = 5, kCodeSlots = 4, kDqSlots = (512 - 2 * kRows) / (kAt
 static_assert(kDqSlots == kGroups && kCodeSlots == kGroups && kActSlots == kGroups + 1, "slots by the group's number");
 constexpr int kMetaBytes = 128 * kGroups * 8 * kAtoms;  // scales and zero points of every converting thread
 constexpr int kSmemBytes = kActSlots * kActSlot + kCodeSlots * kCodeSlot + 1024 + kBarBytes + kMetaBytes + 4 * kGroups * 1024;  // (a staged chunk per warp)
-static_assert(kSmemBytes + 8 * kMostExperts + 64 <= kSmemLimit && 8 * (kActSlots + kDqSlots + 2 * kCodeSlots + 5) + 8 <= kBarBytes, "shared memory");
+static_assert(kSmemBytes + 14 * kMostExperts + 64 <= kSmemLimit && 8 * (kActSlots + kDqSlots + 2 * kCodeSlots + 5) + 8 <= kBarBytes, "shared memory");
 
 __device__ __forceinline__ int row_tiles(int n) { return (n + 2 * kRows - 1) / (2 * kRows); }
 
@@ -194,6 +195,8 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmW, const TensorParams p)
   // (fixed places, which take no registers)
   __shared__ int abort_word, offs[kMostExperts + 1];  // [E + 1]
   __shared__ int firsts[kMostExperts + 1];            // [E + 1]: an expert's first tile
+  __shared__ float inverse[kMostExperts];             // of an expert's row tiles
+  __shared__ short sizes[kMostExperts];               // of its parts; negative: a tile has one
   volatile int* abort_flag = &abort_word;
 
   const uint32_t rank = cluster_rank();  // 0: the CTA that issues the MMAs
@@ -244,6 +247,11 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmW, const TensorParams p)
       int before = __shfl_up_sync(0xffffffffu, m, 1);
       if (lane == 0) before = top;
       int s = e > 0 && e <= a.E ? row_tiles(m - before) * p.pairs : 0;
+      if (s > 0) {
+        const int rt = row_tiles(m - before), each = (m - before + rt - 1) / rt;
+        inverse[e - 1] = 1.f / (float)rt;
+        sizes[e - 1] = (short)(each > kRows ? ((each + 1) / 2 + 15) & ~15 : -((each + 15) & ~15));
+      }
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const int u = __shfl_up_sync(0xffffffffu, s, d);
@@ -268,10 +276,14 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmW, const TensorParams p)
   auto tile_at = [&](int i, int& e) -> Tile {
     const int t = cluster + i * clusters;
     while (firsts[e + 1] <= t) ++e;
+    // (row tiles fastest; the quotient by their number as a product with its
+    // inverse, which is exact below 2^21: the next integer is at least half an
+    // inverse away, the product's error less)
     const int n = offs[e + 1] - offs[e], rt = row_tiles(n), local = t - firsts[e];
-    const int each = (n + rt - 1) / rt, parts = each > kRows ? 2 : 1;
-    const int size = ((each + parts - 1) / parts + 15) & ~15, row = local % rt * parts * size;
-    return {e, local / rt, offs[e] + row, min(parts * size, n - row), parts, size};
+    const int col = local < 1 << 21 ? (int)(((float)local + 0.5f) * inverse[e]) : local / rt;
+    const int signed_size = sizes[e], size = abs(signed_size), parts = signed_size > 0 ? 2 : 1;
+    const int row = (local - col * rt) * parts * size;
+    return {e, col, offs[e] + row, min(parts * size, n - row), parts, size};
   };
   // the first strip of this CTA in a tile (with silu: of its gate columns)
   auto first_strip = [&](const Tile& t) { return (2 * t.col + (int)rank) * (a.silu ? 4 : 8); };
@@ -416,7 +428,10 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmW, const TensorParams p)
     SeqPos next{grp_id, 0};
     next.step(0, nk);
     constexpr int kStep = kAtoms * kStageK;  // k of a stage
-    int ne = 0, nstrip = -1, ngrp = next.kb * kStep / a.group;
+    int ne = 0, nstrip = -1, ngrp = 0;
+    // (k / group, exact below 2^21 as above)
+    auto group_of = [&](int kb) { return (int)(((float)(kb * kStep) + 0.5f) * p.inv_group); };
+    const bool one_group = a.group % kStep == 0;  // of both atoms of a stage
     // Rows: of each part this warp copies those of steps q, q + 4, ... (step
     // i: rows 4 i .. 4 i + 3 of this CTA's half of it), a lane the 16 bytes lane
     // % 8 of row lane / 8 of each; lane 16 part + 4 j + r holds which row of A
@@ -439,14 +454,16 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmW, const TensorParams p)
     // columns cp & 4 .. (cp & 4) + 3, each with its column + 8
     const uint32_t meta = bars + kBarBytes + (uint32_t)(dw * 32 + lane) * 16u;
     auto copy_meta = [&]() {
+      if (nstrip < 0) return;
       const uint32_t* sp = reinterpret_cast<const uint32_t*>(a.Sp);
-      size_t pg = (size_t)nstrip * G + ngrp;
+      // (strips times groups are below 2^32: 16 * 64 weights each, in 280 GB)
+      uint32_t pg = (uint32_t)nstrip * (uint32_t)G + (uint32_t)ngrp;
 #pragma unroll
       for (int u = 0; u < kAtoms; ++u) {
-        if (nstrip < 0 || next.kb * kAtoms + u >= natoms) break;
-        if (u > 0 && next.kb * kStep + u * kStageK >= (ngrp + 1) * a.group) ++pg;  // a group of one atom
-        copy4(meta + 8u * u, ld_at(sp + pg * 8 + cp, sp, (size_t)G * a.N * a.E / 2, a.err));
-        copy4(meta + 8u * u + 4u, ld_at(a.Zp + pg * 2 + cp / 4, a.Zp, (size_t)G * a.N * a.E / 8, a.err));
+        if (u > 0 && (one_group || next.kb * kAtoms + u >= natoms)) break;
+        if (u > 0 && next.kb * kStep + u * kStageK >= (ngrp + 1) * a.group) ++pg;
+        copy4(meta + 8u * u, ld_at(sp + (uint64_t)pg * 8u + cp, sp, (size_t)G * a.N * a.E / 2, a.err));
+        copy4(meta + 8u * u + 4u, ld_at(a.Zp + (uint64_t)pg * 2u + cp / 4, a.Zp, (size_t)G * a.N * a.E / 8, a.err));
       }
     };
     // chunk lane % 8 of row lane / 8 of a step, swizzled by the row's number in
@@ -488,7 +505,7 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmW, const TensorParams p)
           wh[l] = hi ? v.w : v.z;
         }
         uint32_t sw, zw;
-        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(sw), "=r"(zw) : "r"(meta + 8u * u) : "memory");
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(sw), "=r"(zw) : "r"(one_group ? meta : meta + 8u * u) : "memory");
         if (u + 1 == kAtoms) {  // the codes are in registers
           __syncwarp();
           if (lane == 0) mbar_arrive(code_empty(grp_id));
@@ -631,6 +648,7 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmW, const TensorParams p)
     int slot = grp_id;  // the stage's rows' slot
     if (grp_id < total) {
       enter_tile();
+      ngrp = group_of(next.kb);
       copy_meta();
     }
     for (int it = 0; grp_id + it * kGroups < total && ok; ++it) {
@@ -641,11 +659,8 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmW, const TensorParams p)
       for (; ok && done < tile; ++done) ok = epilogue(done);
       if (grp_id + (it + 1) * kGroups < total) {
         next.step(kGroups, nk);
-        if (next.tile != tile) {
-          enter_tile();
-          ngrp = 0;
-        }
-        while (next.kb * kStep >= (ngrp + 1) * a.group) ++ngrp;
+        if (next.tile != tile) enter_tile();
+        ngrp = group_of(next.kb);
         copy_meta();
       }
     }
@@ -715,7 +730,7 @@ cudaError_t launch_experts_tc(ExpertArgs a, bool bf16, void* workspace, cudaStre
   if (!cached_expert_map(&tmW, a.Wq, a.N, a.K, a.E, kAtoms, a.silu)) return cudaErrorInvalidValue;
   const int wide = a.silu ? a.N / 2 : a.N, per = a.silu ? kCols : 2 * kCols;
   TensorParams p = {a, workspace ? reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + kWorkspaceFlags) : nullptr,
-                    (wide + per - 1) / per};
+                    (wide + per - 1) / per, 1.f / (float)a.group};
   e = bf16 ? launch<true>(tmW, p, stream) : launch<false>(tmW, p, stream);
   return e != cudaSuccess || !a.combine ? e : launch_experts_sum(a, p.D, bf16, stream);
 }

@@ -283,6 +283,8 @@ def gemm_experts(A: torch.Tensor, pe: PackedExperts, routing: Routing, silu_mul:
     times expert routing.experts[t, j] (zeros where that is -1); with
     `silu_mul` (pe's columns are [gate | up]) silu(gate) * up, [T, top_k,
     N/2]; with `combine` the sum over j weighted by routing.weights, [T, N].
-    `path`: "auto" or "decode". `workspace` as for gemm."""
+    `path`: "auto", "decode" (few rows per expert: weights unrounded) or
+    "tensor-pair" (many: weights rounded once to A's type). `workspace` as for
+    gemm."""
     return (_native_module or _native()).gemm_experts(A, pe, routing, silu_mul, combine, out, w4._PATHS[path], workspace,
                                                       stream)

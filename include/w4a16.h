@@ -506,16 +506,23 @@ int w4a16_route(const void* logits, int64_t logits_stride, int T, int E, int top
  *   Y [T][N]            = sum_j weights[f] * y[f] over a token's choices that
  *                         have an expert, with W4A16_EXPERTS_COMBINE.
  * The two do not go together. A and Y are fp16, or bfloat16 with W4A16_BF16;
- * accumulation is fp32. The weights enter as (q - z) * s, unrounded on the
- * path for few rows (W4A16_PATH_DECODE).
- * Combined, the products wait in the workspace and are added in the order of
+ * accumulation is fp32. The weights enter as (q - z) * s: unrounded on the
+ * path for few rows per expert (W4A16_PATH_DECODE), rounded once to the
+ * activations' type on the tensor cores' (W4A16_PATH_TENSOR_PAIR), which
+ * W4A16_PATH_AUTO takes above 24 rows per expert on average (T * top_k > 24 E).
+ * Combined, the products wait in the workspace (fp32 on the path for few rows,
+ * in 16 bits on the tensor cores') and are added in fp32, in the order of
  * the token's choices: the result is the same every time.
- * Shapes as w4a16_gemm's (N % 32 == 0 with W4A16_SILU_MUL, any group that is a multiple of
- * 64 and divides K), E * N below 2^31, T, E and top_k as the router's. `flags`
- * carries the path in its low byte: W4A16_PATH_AUTO or _DECODE. An offset outside [0, T * top_k] is clamped
- * and a row outside [0, T * top_k) skipped, both recorded (bit 128); choices
- * that `rows` does not list stay as they are (in a combined result, what the
- * workspace held counts). */
+ * Shapes as w4a16_gemm's (N % 32 == 0 with W4A16_SILU_MUL, any group that is
+ * a multiple of 64 and divides K), E * N below 2^31, T, E and top_k as the
+ * router's. Alignment: A, Wq, scales and Y 16 bytes, zeros 8. `flags`
+ * carries the path in its low byte: W4A16_PATH_AUTO, _DECODE or _TENSOR_PAIR.
+ * The routing is read on the device. An offset outside [0, T * top_k] or below
+ * the one before it is clamped, a row outside [0, T * top_k) skipped and an
+ * expert that has more rows than there are tokens cut short, each recorded (bit
+ * 128); choices that `rows` does not list stay as they are (in a combined
+ * result, what the workspace held counts). With T = 1 the path for few rows
+ * reads `experts` alone (an expert of E or above counts as none, recorded). */
 #define W4A16_EXPERTS_PER_CHOICE 0x20000
 #define W4A16_EXPERTS_COMBINE 0x40000
 int w4a16_experts_workspace_size(int T, int top_k, int E, int N, int K, int group, int flags,
