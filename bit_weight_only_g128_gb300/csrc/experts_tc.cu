@@ -26,19 +26,26 @@
 //     MMAs waited for rows most of the time.) Places beyond a tile's rows repeat
 //     its last row; their results are not stored.
 //   - With silu(gate) * up a CTA's eight strips are four of gate columns and
-//     the four of up columns beside them (one 4-D copy), placed so that a
-//     warp's lanes 0..15 hold gate and 16..31 up of the same 16 results: one
-//     shuffle per two results brings them together in fp32, and the output is
-//     half as wide.
+//     the four of up columns beside them (one 4-D copy), placed so that of a
+//     warp's tensor-memory lanes 0..15 hold gate and 16..31 up of the same 16
+//     results: read 16 lanes at a time, a thread gets both of a result in fp32,
+//     and the output is half as wide.
 //   - K is short (an expert's inner width), so that a tile's end matters: the
 //     converting warps hand the first part's accumulator back before they take
 //     the second's, and the next tile begins with the first part's MMAs of the
 //     stages that are converted already, to catch up with the second part's
 //     when its accumulator is free.
-// What bounds it is the converting warps' issue slots, so a stage is two atoms
-// (of the last one only what K has), and nothing is spilled: the first-level
-// cache beside 214 KB of shared memory is too small for it, and each spilled
-// value cost a trip to L2.
+// What bounds it is the converting warps: a stage takes one of them (four run
+// on a scheduler) about 600 instructions, so that a stage is two atoms (of the
+// last one only what K has), tiles are found without divisions, and hardly a
+// register is spilled: the first-level cache beside 223 KB of shared memory is
+// too small for that, and each spilled value cost a trip to L2 (519 -> 336 us at
+// the first case below).
+// Measured (us a call, TFLOP/s): 4099 tokens, 64 experts, top 8, gate and up of
+// 2048 x 2048, bf16 235, 1170; down of 1024 x 2048 with the sum 164, 840; 2047
+// tokens, 8 experts, top 2, down of 11008 x 4096 with the sum 286-300, 1230-1290 (of
+// it 24% an SM's wait for the last round of tiles: 3.4 tiles to a cluster make
+// four rounds).
 //
 // Rings, barriers and their invariants are those of tc_pair.cu, without a
 // barrier for the rows' arrival. What a group waits for before it converts stage
@@ -179,7 +186,7 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmW, const TensorParams p)
   constexpr int nact = kActSlots, ncode = kCodeSlots, ndq = kDqSlots;
   constexpr uint32_t kActBytes = kActSlot, kCodeBytes = kCodeSlot;
   constexpr int kDqCol0 = 2 * kRows;  // tensor memory: two accumulators, then the dequantized operand
-  // [activation ring | code ring | barriers | list of tiles], 1024-aligned slots
+  // [activation ring | code ring | barriers | scales | staged results], 1024-aligned slots
   const uint32_t code_base = base + (uint32_t)nact * kActBytes;
   const uint32_t bars = code_base + (uint32_t)ncode * kCodeBytes;
   auto stage_done = [&](int i) { return bars + 8u * i; };

@@ -515,7 +515,8 @@ int w4a16_route(const void* logits, int64_t logits_stride, int T, int E, int top
  * the token's choices: the result is the same every time.
  * Shapes as w4a16_gemm's (N % 32 == 0 with W4A16_SILU_MUL, any group that is
  * a multiple of 64 and divides K), E * N below 2^31, T, E and top_k as the
- * router's. Alignment: A, Wq, scales and Y 16 bytes, zeros 8. `flags`
+ * router's. Y must not overlap the inputs. Alignment: A, Wq, scales and Y 16
+ * bytes, zeros 8. `flags`
  * carries the path in its low byte: W4A16_PATH_AUTO, _DECODE or _TENSOR_PAIR.
  * The routing is read on the device. An offset outside [0, T * top_k] or below
  * the one before it is clamped, a row outside [0, T * top_k) skipped and an

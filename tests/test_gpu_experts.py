@@ -179,11 +179,27 @@ def test_products(E, K, N, group, T, dtype, path):
 
 
 @pytest.mark.parametrize("path", PATHS)
-@pytest.mark.parametrize("T,E,top", [(1, 64, 8), (7, 200, 32), (33, 40, 40 - 8), (130, 8, 1), (520, 3, 2)])
+@pytest.mark.parametrize("T,E,top", [(1, 64, 8), (7, 200, 32), (33, 40, 40 - 8), (130, 8, 1), (520, 3, 2), (40, 512, 4)])
 def test_products_of_many_experts_and_rows(T, E, top, path):
     g = gen(T + E)
     routing = w4.route(normal(g, T, E), top, scoring="sigmoid", renormalize=False)
     check_products(g, experts(g, E, 128, 64, 128), routing, BF16, path)
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("K,group", [(64, 64), (128, 128), (192, 64), (320, 64), (512, 128), (576, 192)])
+@pytest.mark.parametrize("dtype", [FP16, BF16])
+def test_many_tiles_of_little_work(K, group, dtype, path):
+    """Several tiles (items) for every block, each with as little as one stage
+    of K: the streams run on across them. Experts of few rows, of one or two
+    parts, and of several tiles."""
+    g = gen(K)
+    E, N, T = 24, 1056, 1500
+    x = normal(g, T, E) + torch.linspace(-4, 3, E, device="cuda")
+    routing = w4.route(x, 4)
+    counts = routing.offsets.diff()
+    assert int(counts.min()) < 40 and int(counts.max()) > 600
+    check_products(g, experts(g, E, K, N, group), routing, dtype, path)
 
 
 @pytest.mark.parametrize("path", PATHS)
