@@ -226,14 +226,18 @@ __global__ void __launch_bounds__(kThreads, 2) experts_decode_kernel(const Decod
     __syncthreads();
     tiles = firsts[a.E + 1];
   }
-  const long long all = (long long)tiles * p.blocks;
+  // (below 2^30: a full item has 256 results or more, of which 280 GB hold 2^37, and
+  // of others each expert has one per 32 columns, E * N / 32 below 2^26; divisions in 64
+  // bits cost one token 0.2 us)
+  const uint32_t all = (uint32_t)tiles * (uint32_t)p.blocks;
   // this block's items: blockIdx.x, blockIdx.x + gridDim.x, ...
   const int count = blockIdx.x < all ? (int)((all - 1 - blockIdx.x) / gridDim.x) + 1 : 0;
   // item i of the block, written down by a warp
   auto describe = [&](int i) {
     if (i >= count) return;
-    const long long at = blockIdx.x + (long long)i * gridDim.x;
-    const int tile = (int)(at % tiles);  // (row tiles first: those of one expert read the same weights)
+    const uint32_t at = blockIdx.x + (uint32_t)i * gridDim.x;
+    // (row tiles first: those of one expert read the same weights)
+    const int col = (int)(at / (uint32_t)tiles), tile = (int)(at % (uint32_t)tiles);
     int e, first, n = 1;
     if (a.T == 1) {
       first = tile;
@@ -259,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 2) experts_decode_kernel(const Decod
       }
     }
     Item& it = items[i % kItems];
-    if (lane == 0) it.e = e, it.n = n, it.col = (int)(at / tiles);
+    if (lane == 0) it.e = e, it.n = n, it.col = col;
     if (lane < kRows) {
       int f = -1;
       if (lane < n) f = a.T == 1 ? first : choice_of(a, first + lane);
