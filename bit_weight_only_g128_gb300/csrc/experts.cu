@@ -27,11 +27,11 @@
 // choices: no atomics, the same result every time.
 //
 // Measured (us a call, bytes of weights and rows a second): gate and up of 2048 x
-// 2048 over 64 experts, top 8, 1 token 8.4 (2.1 TB/s), 16 tokens, bf16, 36.5 (3.4);
+// 2048 over 64 experts, top 8, 1 token 8.3 (2.1 TB/s), 16 tokens, bf16, 37.5 (3.3);
 // of 4096 x 22016 over 8, top 2, 32 tokens 112 (3.4, half of the copy rate, 0.55
 // instructions a cycle and scheduler: sixteen warps on an SM, which the registers of
 // the sums and codes allow, cannot hide all the latency of shared memory and MMAs);
-// down of 1024 x 2048 over 64, 1 token 8.3, 100 tokens 43 (0.49 a cycle).
+// down of 1024 x 2048 over 64, 1 token 8.0, 100 tokens 41 (0.49 a cycle).
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -602,9 +602,11 @@ __global__ void __launch_bounds__(kThreads) experts_sum_kernel(const ExpertArgs 
   allow_dependent_launch();
   grid_dependency_wait();
   const int vecs = a.N / 8;
-  const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
-  if (i >= (long long)a.T * vecs) return;
-  const int t = (int)(i / vecs), n = (int)(i % vecs) * 8;
+  // vector kThreads * block + thread of them all, in 32 bits: vecs blocks are
+  // kThreads rows
+  const uint32_t in = blockIdx.x % (uint32_t)vecs * kThreads + threadIdx.x;
+  const int t = (int)(blockIdx.x / (uint32_t)vecs * kThreads + in / (uint32_t)vecs), n = (int)(in % (uint32_t)vecs) * 8;
+  if (t >= a.T) return;
   const size_t f0 = (size_t)t * a.top;
   float sum[8] = {};
   for (int j0 = 0; j0 < a.top; j0 += kFlight) {
