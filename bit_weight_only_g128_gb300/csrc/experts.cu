@@ -16,11 +16,16 @@
 // run on across the items. The codes enter
 // mma.sync m16n8k16 as exact 16-bit numbers without a multiplication: fp16
 // takes q masked in place as the subnormal q 2^-24 (the odd pairs one nibble
-// higher, summed apart and divided by 16), bf16 takes 128 + q put together by
-// byte permutes; the zero point, in the same form, is subtracted exactly, or
-// (up to eight rows) multiplied and subtracted in the sums. Each
-// group's fp32 sum is multiplied by its scale. So the weights are (q - z) s
-// unrounded, the sums fp32, and the result is rounded once.
+// higher, summed apart and divided by 16), bf16 takes (128 + q) 2^-12 put
+// together by byte permutes; the zero point, in the same form, is subtracted
+// exactly. Each group's fp32 sum is multiplied by its scale (and 2^24 or 2^12). So
+// the weights are (q - z) s unrounded, the sums fp32, and the result is rounded
+// once. (Zero points multiplied and subtracted in the sums would make NaN of an
+// infinite activation, and of a bf16 one from 2^121 on, where q - z times it is
+// not: inf - inf; the four MMAs that took a pair of atoms' place of 32
+// subtractions were no faster: gate and up of 1 token 8.2 us against 7.6, of 16
+// 37.3 against 36.0. The 2^-12 keeps a group's sum of up to 273 products of any
+// finite bf16 activations finite, below 2^128 15 273 2^-12, before its scale.)
 //
 // Combined, each choice's product goes to the workspace in fp32, and a second
 // kernel adds a token's rows, multiplied by their weights, in the order of its
@@ -87,6 +92,10 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The bf16 2^-5 = 128 * 2^-12, whose low 4 of 7 fraction bits count 2^-12: the
+// byte above a code's (the byte 0x0q), and two with codes of zero.
+constexpr uint32_t kBf16Code = 0x3d3d3d3du, kBf16Zero = 0x3d003d00u;
+
 // A zero point in the codes' form: lo for pairs 0 and 1, hi for 2 and 3 (bf16:
 // one form for all).
 template <bool kB>
@@ -94,7 +103,7 @@ struct Zero {
   uint32_t lo, hi;
   __device__ __forceinline__ explicit Zero(uint32_t z) {
     if (kB) {
-      lo = hi = 0x43004300u | z | (z << 16);
+      lo = hi = kBf16Zero | z | (z << 16);
     } else {
       lo = z | (z << 16);
       hi = lo << 4;
@@ -119,37 +128,26 @@ __device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a
 
 // The four pairs of a word minus the zero point: (k 0, 1), (2, 3), (4, 5),
 // (6, 7); exact. fp16: (q - z) 2^-24 in the first two, 16 times that in the
-// others; bf16: q - z.
-template <bool kB>
-__device__ __forceinline__ void plain_codes(uint32_t w, uint32_t (&c)[4]) {  // (not minus the zero point)
-  if (kB) {
-    const uint32_t t = w & 0x0F0F0F0Fu, u = (w >> 4) & 0x0F0F0F0Fu;
-    c[0] = __byte_perm(t, 0x43434343u, 0x4240);
-    c[1] = __byte_perm(t, 0x43434343u, 0x4341);
-    c[2] = __byte_perm(u, 0x43434343u, 0x4240);
-    c[3] = __byte_perm(u, 0x43434343u, 0x4341);
-  } else {
-    const uint32_t w8 = w >> 8;
-    c[0] = w & 0x000F000Fu;
-    c[1] = w8 & 0x000F000Fu;
-    c[2] = w & 0x00F000F0u;
-    c[3] = w8 & 0x00F000F0u;
-  }
-}
+// others; bf16: (q - z) 2^-12.
 template <bool kB>
 __device__ __forceinline__ void codes(uint32_t w, const Zero<kB>& z, uint32_t (&c)[4]) {
-  plain_codes<kB>(w, c);
   if (kB) {
+    const uint32_t t = w & 0x0F0F0F0Fu, u = (w >> 4) & 0x0F0F0F0Fu;
+    c[0] = __byte_perm(t, kBf16Code, 0x4240);
+    c[1] = __byte_perm(t, kBf16Code, 0x4341);
+    c[2] = __byte_perm(u, kBf16Code, 0x4240);
+    c[3] = __byte_perm(u, kBf16Code, 0x4341);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&c[i]), *reinterpret_cast<const __nv_bfloat162*>(&z.lo));
       c[i] = *reinterpret_cast<const uint32_t*>(&d);
     }
   } else {
-    c[0] = hsub2_rn(c[0], z.lo);
-    c[1] = hsub2_rn(c[1], z.lo);
-    c[2] = hsub2_rn(c[2], z.hi);
-    c[3] = hsub2_rn(c[3], z.hi);
+    const uint32_t w8 = w >> 8;
+    c[0] = hsub2_rn(w & 0x000F000Fu, z.lo);
+    c[1] = hsub2_rn(w8 & 0x000F000Fu, z.lo);
+    c[2] = hsub2_rn(w & 0x00F000F0u, z.hi);
+    c[3] = hsub2_rn(w8 & 0x00F000F0u, z.hi);
   }
 }
 
@@ -377,17 +375,13 @@ __global__ void __launch_bounds__(kThreads, 2) experts_decode_kernel(const Decod
   };
 
   float out[2][4] = {};
-  const float scale = kB ? 1.f : 16777216.f;  // of the codes' form
+  const float scale = kB ? 4096.f : 16777216.f;  // of the codes' form
   auto scales = [&](uint32_t sw, float& s0, float& s1) {
     s0 = value16<false>(sw & 0xffffu) * scale, s1 = value16<false>(sw >> 16) * scale;
   };
   // out += a unit's products: MT octets of rows
   auto multiply_pairs = [&](auto octets, uint32_t wt, uint32_t act, int i0, int i1) {  // the pairs i0 .. i1
     constexpr int MT = decltype(octets)::value;
-    // One octet: the zero points go in by MMAs of their own, with the constant
-    // row -z, four a pair of atoms and octet against 32 subtractions that serve
-    // all octets: for two octets the subtractions are cheaper.
-    constexpr bool kZeroMma = MT == 1;
 #pragma unroll
     for (int i = i0; i < i1; ++i) {
       uint32_t sw, zw;
@@ -395,7 +389,6 @@ __global__ void __launch_bounds__(kThreads, 2) experts_decode_kernel(const Decod
       asm volatile("ld.shared.u32 %0, [%1];" : "=r"(zw) : "r"(wt + kUnitBytes + 64u + (uint32_t)(2 * i + lane / 16) * 4u) : "memory");
       const uint32_t zz = zw >> (lane / 4 % 4 * 8);
       const Zero<kB> z0(zz & 15u), z1((zz >> 4) & 15u);
-      constexpr uint32_t kMinus = 0x80008000u;
       float lo[MT][4], hi[MT][4];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -404,13 +397,8 @@ __global__ void __launch_bounds__(kThreads, 2) experts_decode_kernel(const Decod
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           uint32_t c0[4], c1[4];
-          if (kZeroMma) {
-            plain_codes<kB>(wd[2 * s], c0);
-            plain_codes<kB>(wd[2 * s + 1], c1);
-          } else {
-            codes<kB>(wd[2 * s], z0, c0);
-            codes<kB>(wd[2 * s + 1], z1, c1);
-          }
+          codes<kB>(wd[2 * s], z0, c0);
+          codes<kB>(wd[2 * s + 1], z1, c1);
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
             const uint4 b = tc::lds128(act + m * 8 * kRowBytes + (2 * i + j) * 128 + s * 64);
@@ -424,10 +412,6 @@ __global__ void __launch_bounds__(kThreads, 2) experts_decode_kernel(const Decod
             } else {
               mma<kB>(lo[m], c0[0], c1[0], c0[1], c1[1], b.x, b.y);
               mma<kB>(second, c0[2], c1[2], c0[3], c1[3], b.z, b.w);
-            }
-            if (kZeroMma) {
-              mma<kB>(lo[m], z0.lo ^ kMinus, z1.lo ^ kMinus, z0.lo ^ kMinus, z1.lo ^ kMinus, b.x, b.y);
-              mma<kB>(second, z0.hi ^ kMinus, z1.hi ^ kMinus, z0.hi ^ kMinus, z1.hi ^ kMinus, b.z, b.w);
             }
           }
         }

@@ -513,6 +513,12 @@ int w4a16_route(const void* logits, int64_t logits_stride, int T, int E, int top
  * Combined, the products wait in the workspace (fp32 on the path for few rows,
  * in 16 bits on the tensor cores') and are added in fp32, in the order of
  * the token's choices: the result is the same every time.
+ * NaN and infinities go where the formulas take them, into the results of
+ * their own rows (a code equal to its zero point times an infinity is NaN). On
+ * the path for few rows a group's products A (q - z) are added before the scale
+ * multiplies the sum: a bf16 sum beyond 2^140 is infinite whatever the scale,
+ * and of bf16 activations below 2^-114 bits are lost. On the tensor cores' path
+ * a weight (q - z) * s beyond its type's range is infinite.
  * Shapes as w4a16_gemm's (N % 32 == 0 with W4A16_SILU_MUL, any group that is
  * a multiple of 64 and divides K), E * N below 2^31, T, E and top_k as the
  * router's. Y must not overlap the inputs. Alignment: A, Wq, scales and Y 16
