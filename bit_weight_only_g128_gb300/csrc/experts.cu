@@ -602,7 +602,9 @@ __global__ void __launch_bounds__(kThreads) experts_sum_kernel(const ExpertArgs 
       live[j] = j0 + j < a.top;
       if (live[j]) {
         w[j] = *ld_at(a.weights + f0 + j0 + j, a.weights, (size_t)choices(a), a.err);
-        live[j] = *ld_at(a.experts + f0 + j0 + j, a.experts, (size_t)choices(a), a.err) >= 0;
+        const int e = *ld_at(a.experts + f0 + j0 + j, a.experts, (size_t)choices(a), a.err);
+        live[j] = (unsigned)e < (unsigned)a.E;
+        if (e >= a.E) atomicOr(a.err, kErrRange);  // (none: the products may have left its row unwritten)
       }
     }
 #pragma unroll

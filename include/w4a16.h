@@ -529,7 +529,8 @@ int w4a16_route(const void* logits, int64_t logits_stride, int T, int E, int top
  * expert that has more rows than there are tokens cut short, each recorded (bit
  * 128); choices that `rows` does not list stay as they are (in a combined
  * result, what the workspace held counts). With T = 1 the path for few rows
- * reads `experts` alone (an expert of E or above counts as none, recorded). */
+ * reads `experts` alone. There, and in every weighted sum, an expert of E or above
+ * counts as none, recorded. */
 #define W4A16_EXPERTS_PER_CHOICE 0x20000
 #define W4A16_EXPERTS_COMBINE 0x40000
 int w4a16_experts_workspace_size(int T, int top_k, int E, int N, int K, int group, int flags,
