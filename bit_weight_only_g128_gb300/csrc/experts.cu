@@ -553,6 +553,12 @@ __global__ void __launch_bounds__(kThreads, 2) experts_decode_kernel(const Decod
 // Eight columns of a row of products, 16-bit or fp32, as loaded and as values.
 struct Eight16 {
   uint4 u;
+  // Any fp16 of them is infinite or NaN (a half of 0x7c00 or more).
+  __device__ __forceinline__ bool beyond() const {
+    constexpr uint32_t kValue = 0x7fff7fffu, kStep = 0x04000400u;
+    return ((((u.x & kValue) + kStep) | ((u.y & kValue) + kStep) | ((u.z & kValue) + kStep) | ((u.w & kValue) + kStep)) &
+            0x80008000u) != 0;
+  }
   __device__ __forceinline__ void load(const uint16_t* p) { u = __ldcs(reinterpret_cast<const uint4*>(p)); }
   template <bool kB>
   __device__ __forceinline__ void values(float (&v)[8]) const {
@@ -579,9 +585,10 @@ struct Eight32 {
 // expert, in their order, in fp32. One thread per eight columns; eight choices
 // in flight, of 16-bit products four (eight would take the registers of every
 // third block: 172 against 164 us with the products of 4099 tokens, top 8, 2048
-// columns). Bound: HBM bytes, for a token or two the chain experts - products.
+// columns). Products that are infinite in fp16 are read from `wide`, [choices][N]
+// in fp32. Bound: HBM bytes, for a token or two the chain experts - products.
 template <bool kB, class T, class Loaded>
-__global__ void __launch_bounds__(kThreads) experts_sum_kernel(const ExpertArgs a, const T* D) {
+__global__ void __launch_bounds__(kThreads) experts_sum_kernel(const ExpertArgs a, const T* D, const float* wide) {
   constexpr int kFlight = sizeof(T) == 2 ? 4 : 8;
   allow_dependent_launch();
   grid_dependency_wait();
@@ -615,6 +622,12 @@ __global__ void __launch_bounds__(kThreads) experts_sum_kernel(const ExpertArgs 
       if (!live[j]) continue;
       float v[8];
       d[j].template values<kB>(v);
+      if constexpr (!kB && sizeof(T) == 2) {
+        if (d[j].beyond())
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (isinf(v[k])) v[k] = *ld_at(wide + (f0 + j0 + j) * a.N + n + k, wide, (size_t)choices(a) * a.N, a.err);
+      }
 #pragma unroll
       for (int k = 0; k < 8; ++k) sum[k] = fmaf(w[j], v[k], sum[k]);
     }
@@ -626,12 +639,12 @@ __global__ void __launch_bounds__(kThreads) experts_sum_kernel(const ExpertArgs 
 }
 
 template <class T>
-cudaError_t launch_sum(const ExpertArgs& a, const T* D, bool bf16, cudaStream_t stream) {
+cudaError_t launch_sum(const ExpertArgs& a, const T* D, const float* wide, bool bf16, cudaStream_t stream) {
   const long long threads = (long long)a.T * (a.N / 8);
   const dim3 grid((unsigned)((threads + kThreads - 1) / kThreads));
   using Loaded = std::conditional_t<sizeof(T) == 2, Eight16, Eight32>;
-  return bf16 ? launch_pdl(experts_sum_kernel<true, T, Loaded>, grid, dim3(kThreads), 0, stream, a, D)
-              : launch_pdl(experts_sum_kernel<false, T, Loaded>, grid, dim3(kThreads), 0, stream, a, D);
+  return bf16 ? launch_pdl(experts_sum_kernel<true, T, Loaded>, grid, dim3(kThreads), 0, stream, a, D, wide)
+              : launch_pdl(experts_sum_kernel<false, T, Loaded>, grid, dim3(kThreads), 0, stream, a, D, wide);
 }
 
 // How a call is laid out.
@@ -719,11 +732,11 @@ cudaError_t launch_experts_decode(ExpertArgs a, bool bf16, void* workspace, cuda
   DecodeParams p = {a, workspace ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kWorkspaceFlags) : nullptr, 0, 0, 0};
   const int sms = device_sms();
   e = bf16 ? launch_experts_decode_t<true>(p, sms, stream) : launch_experts_decode_t<false>(p, sms, stream);
-  return e != cudaSuccess || !a.combine ? e : launch_sum(a, p.D, bf16, stream);
+  return e != cudaSuccess || !a.combine ? e : launch_sum(a, p.D, nullptr, bf16, stream);
 }
 
-cudaError_t launch_experts_sum(const ExpertArgs& a, const uint16_t* D, bool bf16, cudaStream_t stream) {
-  return launch_sum(a, D, bf16, stream);
+cudaError_t launch_experts_sum(const ExpertArgs& a, const uint16_t* D, const float* wide, bool bf16, cudaStream_t stream) {
+  return launch_sum(a, D, wide, bf16, stream);
 }
 
 }  // namespace w4a16

@@ -75,10 +75,12 @@ constexpr int kAtomSlot = 2 * kPartSlot;
 constexpr int kActSlot = kAtoms * kAtomSlot;
 constexpr int kCodeSlot = kAtoms * kCodeAtomBytes;
 constexpr int kMostExperts = 512;
+constexpr float kHalfInfinite = 65520.f;  // the least that rounds to fp16's infinity
 
 struct TensorParams {
   ExpertArgs a;
   uint16_t* D;     // combined: [choices][N], the products
+  float* wide;     // the same in fp32, written where fp16 products are infinite
   int pairs;       // tiles along the columns
   float inv_group;  // 1 / group
 };
@@ -620,6 +622,28 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmW, const TensorParams p)
               o[1][x] = to_out2<kB>(f(1, 2 * x), f(1, 2 * x + 1));
             }
           }
+          // Products beyond fp16's range also go to the workspace in fp32, where
+          // the weighted sum finds them: it may be within the range. (Hardly ever:
+          // one comparison per thread and chunk, against twice the bytes of all.)
+          if (!kB && a.combine) {
+            float most = 0.f;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int x = 0; x < 8; ++x) most = fmaxf(most, fabsf(f(h, x)));
+            if (__any_sync(0xffffffffu, most >= kHalfInfinite)) {
+#pragma unroll
+              for (int x = 0; x < 8; ++x) {
+                const int choice = __shfl_sync(0xffffffffu, chosen, 16 * j + 8 * (x >> 2) + 2 * (lane % 4) + (x & 1));
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  float* to = p.wide + (size_t)(uint32_t)choice * (uint32_t)width + (s0 + h) * kStripCols + lane / 4 + 8 * (x >> 1 & 1);
+                  if (choice >= 0 && s0 + h < limit && fabsf(f(h, x)) >= kHalfInfinite && in_buf(to, p.wide, all + 7, a.err))
+                    *to = f(h, x);
+                }
+              }
+            }
+          }
           // matrix 2 m + v of a strip: rows 8 m .., columns 8 v ..; a row of the
           // staged chunk has 2 (silu) or 4 pieces of 16 bytes, swizzled by the row
           const int strips_out = a.silu ? 1 : 2;
@@ -726,8 +750,10 @@ cudaError_t launch(const CUtensorMap& tmW, TensorParams p, cudaStream_t stream) 
 
 }  // namespace
 
+// The products in 16 bits, and in fp32 those that fp16 cannot hold (of both
+// types alike: a workspace's size does not depend on the type).
 size_t experts_tc_workspace_bytes(int choices, int N, bool combine) {
-  return combine ? kWorkspaceFlags + (size_t)choices * N * sizeof(uint16_t) : 0;
+  return combine ? kWorkspaceFlags + (size_t)choices * N * (sizeof(uint16_t) + sizeof(float)) : 0;
 }
 
 cudaError_t launch_experts_tc(ExpertArgs a, bool bf16, void* workspace, cudaStream_t stream) {
@@ -736,10 +762,13 @@ cudaError_t launch_experts_tc(ExpertArgs a, bool bf16, void* workspace, cudaStre
   CUtensorMap tmW;
   if (!cached_expert_map(&tmW, a.Wq, a.N, a.K, a.E, kAtoms, a.silu)) return cudaErrorInvalidValue;
   const int wide = a.silu ? a.N / 2 : a.N, per = a.silu ? kCols : 2 * kCols;
-  TensorParams p = {a, workspace ? reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + kWorkspaceFlags) : nullptr,
-                    (wide + per - 1) / per, 1.f / (float)a.group};
+  TensorParams p = {a, nullptr, nullptr, (wide + per - 1) / per, 1.f / (float)a.group};
+  if (a.combine) {
+    p.D = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + kWorkspaceFlags);
+    p.wide = reinterpret_cast<float*>(p.D + (size_t)choices(a) * a.N);  // (N is a multiple of 16)
+  }
   e = bf16 ? launch<true>(tmW, p, stream) : launch<false>(tmW, p, stream);
-  return e != cudaSuccess || !a.combine ? e : launch_experts_sum(a, p.D, bf16, stream);
+  return e != cudaSuccess || !a.combine ? e : launch_experts_sum(a, p.D, p.wide, bf16, stream);
 }
 
 }  // namespace w4a16

@@ -170,11 +170,13 @@ struct ExpertArgs;
 size_t experts_decode_workspace_bytes(int choices, int N, bool combine);
 cudaError_t launch_experts_decode(ExpertArgs args, bool bf16, void* workspace, cudaStream_t stream);
 // The same for many rows per expert, on the tensor cores; combined, the
-// choices' products in 16 bits.
+// choices' products in 16 bits, and in fp32 those that fp16 cannot hold.
 size_t experts_tc_workspace_bytes(int choices, int N, bool combine);
 cudaError_t launch_experts_tc(ExpertArgs args, bool bf16, void* workspace, cudaStream_t stream);
-// Y[t] = the weighted sum of D's rows of token t's choices (16 bits).
-cudaError_t launch_experts_sum(const ExpertArgs& args, const uint16_t* D, bool bf16, cudaStream_t stream);
+// Y[t] = the weighted sum of D's rows of token t's choices (16 bits; `wide` in
+// their place where an fp16 one is infinite).
+cudaError_t launch_experts_sum(const ExpertArgs& args, const uint16_t* D, const float* wide, bool bf16,
+                               cudaStream_t stream);
 
 // Reads the device error word (bounded waits that gave up, self-checks) and
 // clears it if set.

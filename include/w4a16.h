@@ -511,8 +511,9 @@ int w4a16_route(const void* logits, int64_t logits_stride, int T, int E, int top
  * activations' type on the tensor cores' (W4A16_PATH_TENSOR_PAIR), which
  * W4A16_PATH_AUTO takes above 24 rows per expert on average (T * top_k > 24 E).
  * Combined, the products wait in the workspace (fp32 on the path for few rows,
- * in 16 bits on the tensor cores') and are added in fp32, in the order of
- * the token's choices: the result is the same every time.
+ * in 16 bits on the tensor cores', those beyond fp16's range in fp32 too) and are
+ * added in fp32, in the order of the token's choices: the result is the same
+ * every time, and finite wherever the sum is within the type's range.
  * NaN and infinities go where the formulas take them, into the results of
  * their own rows (a code equal to its zero point times an infinity is NaN). On
  * the path for few rows a group's products A (q - z) are added before the scale

@@ -63,3 +63,29 @@ def test_large_bf16_activations(T, group, path):
         within(w4.gemm_experts(A, pe, routing, combine=True, path=path),
                *ref.combine(y, tol, routing.weights, routing.experts, ref.U[BF16]))
     w4.device_status()
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("per_choice", [False, True])
+@pytest.mark.parametrize("T", [1, 5, 40, 300])
+@pytest.mark.parametrize("N,K,group", [(96, 256, 128), (272, 192, 64)])
+def test_products_beyond_fp16_whose_sum_is_not(N, K, group, T, per_choice, path):
+    """Single products beyond 65504, some by far, beside ordinary ones in the
+    same rows: their weighted sum is finite, on both paths."""
+    g = gen(T + N)
+    pe = w4.stack_experts([w4.quantize_pack(normal(g, K, N, std=std), group) for std in (0.5, 0.5, 0.02, 0.5)])
+    routing = w4.route(normal(g, T, 4), 3)
+    routing.weights.mul_(0.01)
+    routing.weights[::2, 1] *= -1
+    A = (normal(g, T, 3, K) if per_choice else normal(g, T, K)).mul_(15000).clamp_(-60000, 60000).to(FP16)
+    A[-1] = normal(g, *A[-1].shape, dtype=FP16)  # a token with none
+    y, tol = ref.products(A, ref.weights_of(pe), routing.experts, rounding(path, FP16))
+    want, tol = ref.combine(y, tol, routing.weights, routing.experts, ref.U[FP16])
+    assert want.abs().max() < 60000 and (T == 1 or 0.1 < (y.abs() > 65520).double().mean() < 0.9)
+    ws = w4.new_workspace(w4.experts_workspace_size(T, 3, pe, combine=True, path=path))
+    for fill in (0xFF, 0):  # whatever it held
+        ws[w4.FLAG_BYTES:] = fill
+        within(w4.gemm_experts(A, pe, routing, combine=True, path=path, workspace=ws), want, tol)
+    routing.weights.mul_(1e5)  # sums beyond the range are infinite
+    assert not w4.gemm_experts(A, pe, routing, combine=True, path=path).isnan().any()
+    w4.device_status()
