@@ -268,16 +268,25 @@ def new_workspace(nbytes: int, device=None) -> torch.Tensor:
 # demand. Calls on one stream run one after another, so they can share one;
 # calls on different streams get different ones.
 _stream_ws = {}
+_captured_ws = []         # ((device, stream), workspace) whose address a captured graph has: never freed
+_zeroed_in_graph = set()  # keys of cached workspaces whose zero-fill is part of a captured graph
 
 
 def stream_workspace(nbytes: int, device: int, stream: int) -> torch.Tensor:
-    """The cached workspace of the stream `stream` (a cudaStream_t) on device
-    index `device`, at least `nbytes` long (a larger zero-filled one replaces
-    it when it is too small)."""
+    """The cached workspace of the stream `stream` (a cudaStream_t, the current
+    one) on device index `device`, at least `nbytes` long (a larger zero-filled
+    one replaces it when it is too small). One that a graph was captured with
+    is kept for good: replays write to it after it has been replaced. One that
+    was allocated during a capture is zero once that graph has run: calls
+    outside a capture get another."""
     key = (device, stream)
+    capturing = torch.cuda.is_current_stream_capturing()
     ws = _stream_ws.get(key)
-    if ws is None or ws.numel() < nbytes:
+    if ws is None or ws.numel() < nbytes or (key in _zeroed_in_graph and not capturing):
         ws = _stream_ws[key] = new_workspace(nbytes, torch.device("cuda", device))
+        (_zeroed_in_graph.add if capturing else _zeroed_in_graph.discard)(key)
+    if capturing and all(held is not ws for _, held in _captured_ws):
+        _captured_ws.append((key, ws))
     return ws
 
 
@@ -319,7 +328,10 @@ def gemm(A: torch.Tensor, pw: PackedWeight, out: Optional[torch.Tensor] = None,
     `workspace` must be zero-filled before its first use (new_workspace);
     without one, the call uses the cached workspace of its stream
     (stream_workspace), allocated on the first call that needs it and grown
-    when a call needs more.
+    when a call needs more. A captured graph keeps using the workspace that it
+    was captured with (allocate it before, by a call on the capturing stream):
+    what runs at the same time as its replays, on that stream or in another
+    graph captured on it, needs a `workspace` of its own.
     `static_weights` (W4A16_STATIC_WEIGHTS): the kernel may read pw while the
     work queued before it on the stream drains; pw must not be written by
     that work. `silu_mul` (W4A16_SILU_MUL): pw's columns are [gate | up] and
@@ -407,7 +419,7 @@ def device_status(stream=None) -> None:
         _check(lib().w4a16_device_status(_stream(stream)), "w4a16_device_status")
     except W4A16Error as e:
         if e.code == -6:
-            for (device, st), ws in list(_stream_ws.items()):
+            for (device, st), ws in [*_stream_ws.items(), *_captured_ws]:
                 with torch.cuda.stream(torch.cuda.ExternalStream(st, device=device)):
                     ws[:FLAG_BYTES].zero_()
         raise

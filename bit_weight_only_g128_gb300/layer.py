@@ -185,9 +185,7 @@ def attn_decode(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: torc
     page numbers of each sequence, lens int32 [batch] its cached tokens (the
     new one among them; 0: zeros and -inf). scale defaults to
     head_dim^(-1/2). Returns out, or (out, lse) with lse float32 [batch,
-    heads] the logarithm of the softmax's sum. `workspace` as for gemm (a
-    captured graph keeps its address: the cached one of a stream is replaced
-    when a later call on the stream needs more)."""
+    heads] the logarithm of the softmax's sum. `workspace` as for gemm."""
     return (_native_module or _native()).attend(q, cache, table, None, lens, scale, out, return_lse, workspace, stream)
 
 
