@@ -63,8 +63,7 @@ struct DecodeParams {
   ExpertArgs a;
   float* D;      // combined: [choices][N]
   int blocks;    // column blocks
-  int tile;      // rows of an item at most: 8 or 16
-  int rows;      // of them, those that shared memory has room for: no more than T
+  int tile;      // rows of an item at most: 8 or 16, and no more than T
 };
 
 __device__ __forceinline__ void copy16(uint32_t to, const void* from) {
@@ -174,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, 2) experts_decode_kernel(const Decod
   const uint32_t dyn = (uint32_t)__cvta_generic_to_shared(dynamic);
   const uint32_t weights = dyn + (uint32_t)warp * kWeightSlots * kSlotBytes;  // this warp's units
   const uint32_t rows = dyn + kWarps * kWeightSlots * kSlotBytes;             // the block's activations
-  const uint32_t row_slot = (uint32_t)(KS * p.rows) * kRowBytes;
+  const uint32_t row_slot = (uint32_t)(KS * p.tile) * kRowBytes;
   const int part = warp / S, w = warp % S;  // this warp's part of K, and its strip of an item
   const int natoms = a.K / kAtomK, G = a.K / a.group, apg = a.group / kAtomK;
   // first atom of a part of K
@@ -255,10 +254,6 @@ __global__ void __launch_bounds__(kThreads, 2) experts_decode_kernel(const Decod
       e = lo;
       first = offs[e] + (tile - firsts[e]) * p.tile;
       n = min(p.tile, offs[e + 1] - first);
-      if (e < a.E && n > p.rows) {  // an expert with more choices than there are tokens
-        if (lane == 0) atomicOr(a.err, kErrRange);
-        n = p.rows;
-      }
     }
     Item& it = items[i % kItems];
     if (lane == 0) it.e = e, it.n = n, it.col = col;
@@ -356,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 2) experts_decode_kernel(const Decod
     const int k0 = rbegin + ru * kUnit + lane / 8;  // the lane's atom
     if (k0 < rend) {
       const uint32_t to = rows + (uint32_t)rslot * row_slot +
-                          (uint32_t)(warp % KS * p.rows + warp / KS) * kRowBytes + 16u * lane;
+                          (uint32_t)(warp % KS * p.tile + warp / KS) * kRowBytes + 16u * lane;
       const uint16_t* from = a.A + k0 * kAtomK + lane % 8 * 8;
 #pragma unroll
       for (int m = 0; m < kPasses; ++m) {
@@ -505,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 2) experts_decode_kernel(const Decod
       const int a0 = begin + u * kUnit, n = min(kUnit, end - a0);
       if (n > 0 && it.e < a.E) {
         const uint32_t wt = weights + (uint32_t)cslot * kSlotBytes;
-        const uint32_t act = rows + (uint32_t)aslot * row_slot + (uint32_t)(part * p.rows + lane / 4) * kRowBytes + lane % 4 * 16u;
+        const uint32_t act = rows + (uint32_t)aslot * row_slot + (uint32_t)(part * p.tile + lane / 4) * kRowBytes + lane % 4 * 16u;
         if (it.n <= 8)
           multiply(std::integral_constant<int, 1>(), wt, act, a0, n);
         else
@@ -650,7 +645,7 @@ cudaError_t launch_sum(const ExpertArgs& a, const T* D, const float* wide, bool 
 // How a call is laid out.
 struct Layout {
   int tile, parts, blocks;  // rows of an item, parts of K, column blocks
-  int rows, smem, per_sm;   // rows of a part in shared memory, its bytes, blocks of an SM
+  int smem, per_sm;         // bytes of shared memory, blocks of an SM
 };
 
 // Dynamic shared memory: the warps' units of weights, the parts' rows (an octet
@@ -665,21 +660,22 @@ int smem_bytes(int parts, int rows) {
 // take 8.4 us in two parts, 9.3 in one. Items have 16 rows where there can be more than
 // 8: gate and up of 16 tokens over 64 experts, top 8, bf16, take 36.5 us in
 // one part; items of 8 rows, which leave room for two blocks on an SM with two
-// parts, take 38.0.
+// parts, take 38.0. Nor has an item more rows than there are tokens, as many as an
+// expert can have of the router: for a few tokens shared memory is small.
 Layout choose_layout(const ExpertArgs& a, int sms) {
   const double experts = a.E * (1.0 - std::pow(1.0 - 1.0 / a.E, (double)choices(a)));
   Layout best = {};
   double least = 0;
   for (int parts = 1; parts <= 4; parts *= 2) {
     Layout l;
-    l.tile = a.T <= 8 ? 8 : 16;
+    const int rows = a.T <= 8 ? 8 : 16;
+    l.tile = a.T < rows ? a.T : rows;
     l.parts = parts;
     const int per = kWarps / parts * kStripCols / (a.silu ? 2 : 1);  // results of an item
     l.blocks = ((a.silu ? a.N / 2 : a.N) + per - 1) / per;
-    l.rows = a.T < l.tile ? a.T : l.tile;
-    l.smem = smem_bytes(parts, l.rows);
+    l.smem = smem_bytes(parts, l.tile);
     l.per_sm = 2 * (l.smem + 15 * 1024) <= 228 * 1024 ? 2 : 1;  // (beside it 14 KB of the kernel's own and 1 KB)
-    const double tiles = experts + (double)choices(a) / l.tile / 2;
+    const double tiles = experts + (double)choices(a) / rows / 2;
     const double cost = std::ceil(tiles * l.blocks / (sms * l.per_sm)) / parts;
     if (parts == 1 || cost < 0.95 * least) {
       least = cost;
@@ -698,9 +694,8 @@ cudaError_t launch_decode_kernel(DecodeParams p, const Layout& l, int sms, cudaS
   if (e != cudaSuccess) return e;
   p.blocks = l.blocks;
   p.tile = l.tile;
-  p.rows = l.rows;
-  // no more blocks than there can be items
-  const long long most = (long long)(choices(a) / l.tile + (choices(a) < a.E + 1 ? choices(a) : a.E + 1)) * l.blocks;
+  // no more blocks than there are items of the router's choices
+  const long long most = (long long)(choices(a) / (l.tile < 8 ? 8 : l.tile) + (choices(a) < a.E + 1 ? choices(a) : a.E + 1)) * l.blocks;
   const long long resident = (long long)l.per_sm * sms;
   const dim3 grid((unsigned)(most < resident ? most : resident));
   return launch_pdl(kernel, grid, dim3(kThreads), (size_t)l.smem, stream, p);
@@ -729,7 +724,7 @@ size_t experts_decode_workspace_bytes(int choices, int N, bool combine) {
 cudaError_t launch_experts_decode(ExpertArgs a, bool bf16, void* workspace, cudaStream_t stream) {
   cudaError_t e = device_error_word(&a.err);
   if (e != cudaSuccess) return e;
-  DecodeParams p = {a, workspace ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kWorkspaceFlags) : nullptr, 0, 0, 0};
+  DecodeParams p = {a, workspace ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kWorkspaceFlags) : nullptr, 0, 0};
   const int sms = device_sms();
   e = bf16 ? launch_experts_decode_t<true>(p, sms, stream) : launch_experts_decode_t<false>(p, sms, stream);
   return e != cudaSuccess || !a.combine ? e : launch_sum(a, p.D, nullptr, bf16, stream);

@@ -526,11 +526,11 @@ int w4a16_route(const void* logits, int64_t logits_stride, int T, int E, int top
  * bytes, zeros 8. `flags`
  * carries the path in its low byte: W4A16_PATH_AUTO, _DECODE or _TENSOR_PAIR.
  * The routing is read on the device. An offset outside [0, T * top_k] or below
- * the one before it is clamped, a row outside [0, T * top_k) skipped and an
- * expert that has more rows than there are tokens cut short, each recorded (bit
- * 128); choices that `rows` does not list stay as they are (in a combined
- * result, what the workspace held counts). With T = 1 the path for few rows
- * reads `experts` alone. There, and in every weighted sum, an expert of E or above
+ * the one before it is clamped and a row outside [0, T * top_k) skipped, each
+ * recorded (bit 128); choices that `rows` does not list stay as they are (in a
+ * combined result, what the workspace held counts). An expert may have any number
+ * of rows, several of one token too. With T = 1 the path for few rows reads
+ * `experts` alone. There, and in every weighted sum, an expert of E or above
  * counts as none, recorded. */
 #define W4A16_EXPERTS_PER_CHOICE 0x20000
 #define W4A16_EXPERTS_COMBINE 0x40000
