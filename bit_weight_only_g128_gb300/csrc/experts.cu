@@ -66,30 +66,9 @@ struct DecodeParams {
   int tile;      // rows of an item at most: 8 or 16, and no more than T
 };
 
-__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-}
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void copy4(uint32_t to, const void* from) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
-}
 template <int N>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
-template <bool kB>
-__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                    uint32_t b1) {
-  if (kB)
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  else
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 
 // The bf16 2^-5 = 128 * 2^-12, whose low 4 of 7 fraction bits count 2^-12: the
 // byte above a code's (the byte 0x0q), and two with codes of zero.
@@ -109,21 +88,6 @@ struct Zero {
     }
   }
 };
-
-template <bool kB>
-__device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                          uint32_t b1) {
-  if (kB)
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%10, %10, %10, %10};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
-  else
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%10, %10, %10, %10};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
-}
 
 // The four pairs of a word minus the zero point: (k 0, 1), (2, 3), (4, 5),
 // (6, 7); exact. fp16: (q - z) 2^-24 in the first two, 16 times that in the
@@ -401,12 +365,12 @@ __global__ void __launch_bounds__(kThreads, 2) experts_decode_kernel(const Decod
             if (j == 0 && s == 0) {
               mma_first<kB>(lo[m], c0[0], c1[0], c0[1], c1[1], b.x, b.y);
               if (kB)
-                mma<kB>(second, c0[2], c1[2], c0[3], c1[3], b.z, b.w);
+                mma_acc<kB>(second, c0[2], c1[2], c0[3], c1[3], b.z, b.w);
               else
                 mma_first<kB>(second, c0[2], c1[2], c0[3], c1[3], b.z, b.w);
             } else {
-              mma<kB>(lo[m], c0[0], c1[0], c0[1], c1[1], b.x, b.y);
-              mma<kB>(second, c0[2], c1[2], c0[3], c1[3], b.z, b.w);
+              mma_acc<kB>(lo[m], c0[0], c1[0], c0[1], c1[1], b.x, b.y);
+              mma_acc<kB>(second, c0[2], c1[2], c0[3], c1[3], b.z, b.w);
             }
           }
         }
@@ -449,8 +413,8 @@ __global__ void __launch_bounds__(kThreads, 2) experts_decode_kernel(const Decod
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
           const uint4 b = tc::lds128(act + m * 8 * kRowBytes + j * 128 + s * 64);
-          mma<kB>(lo[m], c0[0], c1[0], c0[1], c1[1], b.x, b.y);
-          mma<kB>(kB ? lo[m] : hi[m], c0[2], c1[2], c0[3], c1[3], b.z, b.w);
+          mma_acc<kB>(lo[m], c0[0], c1[0], c0[1], c1[1], b.x, b.y);
+          mma_acc<kB>(kB ? lo[m] : hi[m], c0[2], c1[2], c0[3], c1[3], b.z, b.w);
         }
       }
       if (--left == 0 || j + 1 == n) {

@@ -54,6 +54,14 @@ __device__ __forceinline__ size_t a_elements(const ExpertArgs& a) {
   return (size_t)(a.per_choice ? choices(a) : a.T) * a.K;
 }
 
+// Asynchronous copies of 16 and 4 bytes to shared memory.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t to, const void* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
+}
+
 // silu(g) * u in fp32.
 __device__ __forceinline__ float silu_times(float g, float u) { return __fdividef(g, 1.f + __expf(-g)) * u; }
 

@@ -112,17 +112,11 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-}
-// The same where `ok`, without a branch.
+// copy16 where `ok`, without a branch.
 __device__ __forceinline__ void copy16_if(bool ok, uint32_t to, const void* from) {
   asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p cp.async.cg.shared.global [%0], [%1], 16;\n\t}" ::"r"(to),
                "l"(from), "r"((int)ok)
                : "memory");
-}
-__device__ __forceinline__ void copy4(uint32_t to, const void* from) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
 }
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
