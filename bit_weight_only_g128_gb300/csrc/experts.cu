@@ -512,12 +512,6 @@ __global__ void __launch_bounds__(kThreads, 2) experts_decode_kernel(const Decod
 // Eight columns of a row of products, 16-bit or fp32, as loaded and as values.
 struct Eight16 {
   uint4 u;
-  // Any fp16 of them is infinite or NaN (a half of 0x7c00 or more).
-  __device__ __forceinline__ bool beyond() const {
-    constexpr uint32_t kValue = 0x7fff7fffu, kStep = 0x04000400u;
-    return ((((u.x & kValue) + kStep) | ((u.y & kValue) + kStep) | ((u.z & kValue) + kStep) | ((u.w & kValue) + kStep)) &
-            0x80008000u) != 0;
-  }
   __device__ __forceinline__ void load(const uint16_t* p) { u = __ldcs(reinterpret_cast<const uint4*>(p)); }
   template <bool kB>
   __device__ __forceinline__ void values(float (&v)[8]) const {
@@ -581,14 +575,33 @@ __global__ void __launch_bounds__(kThreads) experts_sum_kernel(const ExpertArgs 
       if (!live[j]) continue;
       float v[8];
       d[j].template values<kB>(v);
-      if constexpr (!kB && sizeof(T) == 2) {
-        if (d[j].beyond())
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (isinf(v[k])) v[k] = *ld_at(wide + (f0 + j0 + j) * a.N + n + k, wide, (size_t)choices(a) * a.N, a.err);
-      }
 #pragma unroll
       for (int k = 0; k < 8; ++k) sum[k] = fmaf(w[j], v[k], sum[k]);
+    }
+  }
+  if constexpr (!kB && sizeof(T) == 2) {
+    // an infinite product leaves its sum infinite or NaN: once more, with `wide`
+    // (asked of the sums at the end: of every product it cost 1.5 us of 27 at the
+    // case above)
+    float any = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) any = fmaf(sum[k], 0.f, any);
+    if (any != 0.f) {
+#pragma unroll 1
+      for (int k = 0; k < 8; ++k) {
+        float s = 0.f;
+#pragma unroll 1
+        for (size_t f = f0; f < f0 + a.top; ++f) {
+          if ((unsigned)*ld_at(a.experts + f, a.experts, (size_t)choices(a), a.err) >= (unsigned)a.E) continue;
+          const size_t at = f * a.N + n + k, all = (size_t)choices(a) * a.N;
+          float v = value16<kB>(*ld_at(D + at, D, all, a.err));
+          if (isinf(v)) v = *ld_at(wide + at, wide, all, a.err);
+          s = fmaf(*ld_at(a.weights + f, a.weights, (size_t)choices(a), a.err), v, s);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i == k) sum[i] = s;
+      }
     }
   }
   uint16_t* y = a.Y + (size_t)t * a.N + n;

@@ -76,6 +76,7 @@ constexpr int kActSlot = kAtoms * kAtomSlot;
 constexpr int kCodeSlot = kAtoms * kCodeAtomBytes;
 constexpr int kMostExperts = 512;
 constexpr float kHalfInfinite = 65520.f;  // the least that rounds to fp16's infinity
+constexpr uint32_t kHalfInf = 0x7c00u;    // which is
 
 struct TensorParams {
   ExpertArgs a;
@@ -133,6 +134,12 @@ __device__ __forceinline__ void tmem_ld_16x16(uint32_t taddr, uint32_t (&r)[8]) 
   asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                : "r"(taddr));
+}
+// Of each pair of fp16 the larger in magnitude (a number beside NaN), of either sign.
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
 }
 // Four 8x8 matrices of 16-bit values, stored transposed: thread 8 i + j gives
 // where matrix i's column j goes, as a row of 16 bytes.
@@ -618,14 +625,14 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmW, const TensorParams p)
           }
           // Products beyond fp16's range also go to the workspace in fp32, where
           // the weighted sum finds them: it may be within the range. (Hardly ever:
-          // one comparison per thread and chunk, against twice the bytes of all.)
+          // eight instructions per thread and chunk, against twice the bytes of all.)
           if (!kB && a.combine) {
-            float most = 0.f;
+            uint32_t most = 0u;  // the largest magnitudes, in pairs
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
-              for (int x = 0; x < 8; ++x) most = fmaxf(most, fabsf(f(h, x)));
-            if (__any_sync(0xffffffffu, most >= kHalfInfinite)) {
+              for (int x = 0; x < 4; ++x) most = max_abs2(most, o[h][x]);
+            if (__any_sync(0xffffffffu, (most & 0x7fffu) == kHalfInf || (most >> 16 & 0x7fffu) == kHalfInf)) {
 #pragma unroll
               for (int x = 0; x < 8; ++x) {
                 const int choice = __shfl_sync(0xffffffffu, chosen, 16 * j + 8 * (x >> 2) + 2 * (lane % 4) + (x & 1));
