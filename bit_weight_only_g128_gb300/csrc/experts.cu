@@ -32,11 +32,11 @@
 // choices: no atomics, the same result every time.
 //
 // Measured (us a call, bytes of weights and rows a second): gate and up of 2048 x
-// 2048 over 64 experts, top 8, 1 token 8.3 (2.1 TB/s), 16 tokens, bf16, 37.5 (3.3);
-// of 4096 x 22016 over 8, top 2, 32 tokens 112 (3.4, half of the copy rate, 0.55
+// 2048 over 64 experts, top 8, 1 token 7.6 (2.3 TB/s), 16 tokens, bf16, 36 (3.4);
+// of 4096 x 22016 over 8, top 2, 32 tokens 108-114 (3.4, half of the copy rate, 0.61
 // instructions a cycle and scheduler: sixteen warps on an SM, which the registers of
 // the sums and codes allow, cannot hide all the latency of shared memory and MMAs);
-// down of 1024 x 2048 over 64, 1 token 8.0, 100 tokens 41 (0.49 a cycle).
+// down of 1024 x 2048 over 64, 1 token 8.0-8.6, 100 tokens 41 (0.53 a cycle).
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -634,10 +634,10 @@ int smem_bytes(int parts, int rows) {
 // Parts of K: of 1, 2 and 4 those with the fewest rounds of items (as many as
 // are likely, were every choice as likely) times the work of an item, the
 // fewer where two are alike: one token's gate and up over eight of 64 experts
-// take 8.4 us in two parts, 9.3 in one. Items have 16 rows where there can be more than
-// 8: gate and up of 16 tokens over 64 experts, top 8, bf16, take 36.5 us in
-// one part; items of 8 rows, which leave room for two blocks on an SM with two
-// parts, take 38.0. Nor has an item more rows than there are tokens, as many as an
+// take 7.7 us in two parts, 11.1 in one. Items have 16 rows where there can be more
+// than 8: with items of 8 gate and up of 32 tokens over 8 experts, top 2, take
+// 115-120 us against 100-111, down of 100 over 64, top 8, 48 against 41, gate and up
+// of 16 tokens over 64 the same 35-37. Nor has an item more rows than there are tokens, as many as an
 // expert can have of the router: for a few tokens shared memory is small.
 Layout choose_layout(const ExpertArgs& a, int sms) {
   const double experts = a.E * (1.0 - std::pow(1.0 - 1.0 / a.E, (double)choices(a)));

@@ -42,8 +42,8 @@
 // too small for that, and each spilled value cost a trip to L2 (519 -> 336 us at
 // the first case below).
 // Measured (us a call, TFLOP/s): 4099 tokens, 64 experts, top 8, gate and up of
-// 2048 x 2048, bf16 235, 1170; down of 1024 x 2048 with the sum 164, 840; 2047
-// tokens, 8 experts, top 2, down of 11008 x 4096 with the sum 286-300, 1230-1290 (of
+// 2048 x 2048, bf16 235, 1170; down of 1024 x 2048 with the sum 169, 815; 2047
+// tokens, 8 experts, top 2, down of 11008 x 4096 with the sum 286-293, 1260-1290 (of
 // it 24% an SM's wait for the last round of tiles: 3.4 tiles to a cluster make
 // four rounds).
 //

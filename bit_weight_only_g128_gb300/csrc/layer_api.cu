@@ -135,10 +135,10 @@ int check_experts(int T, int top_k, int E, int N, int K, int group, int flags) {
 
 // Whether a call takes the kernel on the tensor cores: above 24 rows per expert
 // on average. Measured (us, few rows against tensor cores): 64 experts of 2048 x
-// 2048, top 8, 16 rows each 65 against 90, 24 89 against 90, 32 110 against 91; 8
-// of 4096 x 22016, top 2, 24 200 against 214, 32 265 against 216; 8 of 11008 x
-// 4096, 24 124 against 114; 128 of 4096 x 3584, top 8, 16 399 against 513, 24 537
-// against 494.
+// 2048, top 8, 16 rows each 64 against 84, 24 86 against 85, 32 107 against 85; 8
+// of 4096 x 22016, top 2, 24 193 against 199, 32 256 against 199; 8 of 11008 x
+// 4096, 24 123 against 108; 128 of 4096 x 3584, top 8, 16 384 against 477, 24 516
+// against 460.
 bool experts_on_tensor_cores(int T, int top_k, int E, int flags) {
   const int path = flags & 0xff;
   if (path != W4A16_PATH_AUTO) return path == W4A16_PATH_TENSOR_PAIR;

@@ -19,8 +19,9 @@
 // the chain of k dependent reductions per token and the launches. Up to
 // kOneBlock tokens one block does everything in one launch; above it a second
 // kernel places the choices once every block's counts are known.
-// Measured (top 8 of 64, a call; in a graph): 1 token 5.0 us, 3.0; 4099 tokens
-// 12.8 us, 9.8 (1.4 MB moved: 0.15 TB/s).
+// Measured (top 8 of 64, a call; in a graph): 1 token 4.7-5.3 us, 3.0; 4099 tokens
+// 10-20 us from process to process (the same binary; 19-20 where the inputs
+// change from call to call), 9.8 (1.4 MB moved: 0.15 TB/s).
 #include "common.cuh"
 #include "kernels.h"
 #include "layer.cuh"

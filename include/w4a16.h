@@ -408,7 +408,9 @@ int w4a16_rope_append(const uint16_t* qkv, int64_t qkv_stride, const float* cos_
  * with the weights q_norm of queries and k_norm of keys, [head_dim] in qkv's
  * type, each null where its heads have no norm (2-byte aligned; 4 bytes run
  * faster). Nothing is rounded between norm, rotation and the result. Values
- * pass through. */
+ * pass through. (The squares are added in fp32: from values of about 2^60 on, in
+ * bf16, their sum is infinite and the head 0; with eps = 0 a head of values of
+ * 2^-75 and below is infinite.) */
 int w4a16_rope_append_norm(const uint16_t* qkv, int64_t qkv_stride, const float* cos_sin,
                            int table_len, int rotary, const int32_t* positions,
                            const int64_t* slots, int tokens, int heads, int kv_heads, int head_dim,
