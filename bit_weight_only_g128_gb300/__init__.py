@@ -278,13 +278,15 @@ def stream_workspace(nbytes: int, device: int, stream: int) -> torch.Tensor:
     one replaces it when it is too small). One that a graph was captured with
     is kept for good: replays write to it after it has been replaced. One that
     was allocated during a capture is zero once that graph has run: calls
-    outside a capture get another."""
+    outside a capture get another, and captures zero its flag area again."""
     key = (device, stream)
     capturing = torch.cuda.is_current_stream_capturing()
     ws = _stream_ws.get(key)
     if ws is None or ws.numel() < nbytes or (key in _zeroed_in_graph and not capturing):
         ws = _stream_ws[key] = new_workspace(nbytes, torch.device("cuda", device))
         (_zeroed_in_graph.add if capturing else _zeroed_in_graph.discard)(key)
+    elif key in _zeroed_in_graph:  # (perhaps by a graph that is not the one being captured)
+        ws[:FLAG_BYTES].zero_()
     if capturing and all(held is not ws for _, held in _captured_ws):
         _captured_ws.append((key, ws))
     return ws
@@ -329,8 +331,8 @@ def gemm(A: torch.Tensor, pw: PackedWeight, out: Optional[torch.Tensor] = None,
     without one, the call uses the cached workspace of its stream
     (stream_workspace), allocated on the first call that needs it and grown
     when a call needs more. A captured graph keeps using the workspace that it
-    was captured with (allocate it before, by a call on the capturing stream):
-    what runs at the same time as its replays, on that stream or in another
+    was captured with (allocated before, by a call on the capturing stream, its
+    zero-fill is no part of the graph): what runs at the same time as its replays, on that stream or in another
     graph captured on it, needs a `workspace` of its own.
     `static_weights` (W4A16_STATIC_WEIGHTS): the kernel may read pw while the
     work queued before it on the stream drains; pw must not be written by

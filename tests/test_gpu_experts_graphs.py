@@ -45,3 +45,32 @@ def test_replays_after_the_streams_workspace_has_grown():
         assert torch.equal(w4.gemm_experts(A, pe, routing, combine=True), sums)
     torch.cuda.synchronize()
     w4.device_status()
+
+
+def test_a_graph_whose_workspace_was_made_in_another_capture():
+    """Neither stream has had a call before: the second graph runs without the
+    first's zero-fill."""
+    g = gen(5)
+    pw = w4.quantize_pack(normal(g, 1024, 512, std=0.02), 128)
+    x = normal(g, 40, 1024, dtype=FP16)
+    want = w4.gemm(x, pw, path="tensor", parts=4)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    outs = []
+    for graph in graphs:
+        with torch.cuda.graph(graph, stream=side):
+            outs.append(w4.gemm(x, pw, path="tensor", parts=4))
+            inside = w4.stream_workspace(1, 0, side.cuda_stream)
+    inside[:w4.FLAG_BYTES] = 0xFF  # as memory may be before the first graph has run
+    torch.cuda.synchronize()
+    for i in (1, 0, 1):
+        outs[i].zero_()
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[i], want)
+    with torch.cuda.stream(side):
+        assert w4.stream_workspace(1, 0, side.cuda_stream) is not inside
+        assert torch.equal(w4.gemm(x, pw, path="tensor", parts=4), want)
+    torch.cuda.synchronize()
+    w4.device_status()

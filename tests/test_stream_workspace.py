@@ -54,3 +54,16 @@ def test_a_workspace_made_in_a_capture_serves_captures_only(stream):
     outside = w4.stream_workspace(50, 0, 7)
     assert outside is not inside and w4.stream_workspace(50, 0, 7) is outside
     assert w4.stream_workspace(50, 0, 8) is not outside and stream["made"] == 3
+
+
+def test_a_second_graph_does_not_count_on_the_firsts_zeros(stream):
+    stream["capturing"] = True
+    ws = w4.stream_workspace(w4.FLAG_BYTES + 100, 0, 7)  # its zero-fill: a node of the first graph
+    ws[:] = 1
+    assert w4.stream_workspace(100, 0, 7) is ws
+    assert not ws[:w4.FLAG_BYTES].any() and ws[w4.FLAG_BYTES:].all()
+    stream["capturing"] = False
+    warm = w4.stream_workspace(w4.FLAG_BYTES + 100, 0, 8)
+    warm[:] = 1
+    stream["capturing"] = True
+    assert w4.stream_workspace(100, 0, 8) is warm and warm.all()  # zeroed before: no node of its own
